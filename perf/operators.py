@@ -334,12 +334,12 @@ def _exact_round(x, block):
     X = torch.floor(torch.log2(torch.where(top > 0, top, torch.ones_like(top)))) - 2
     X = torch.where(top > 0, X, torch.full_like(X, -127.0)).clamp(min=-127.0)
     unit = torch.exp2(X)[:, None]
-    gap = ((b.abs() / unit)[..., None] - torch.tensor(_LEVELS, dtype=torch.float64, device=x.device)).abs()
-    code = gap.argmin(-1)
-    tied = gap.gather(-1, (code + 1).clamp_max(7)[..., None]) == gap.gather(-1, code[..., None])
-    code = code + (tied[..., 0] & (code % 2 == 1) & (code < 7))
-    best = torch.tensor(_LEVELS, dtype=torch.float64, device=x.device)[code]
-    return (torch.sign(b) * best * unit).reshape(shape)
+    level = torch.tensor(_LEVELS, dtype=torch.float64, device=x.device)
+    half = (level[1:] + level[:-1]) / 2
+    a = (b.abs() / unit)[..., None]
+    upper_even = torch.arange(1, 8, device=x.device) % 2 == 0
+    code = ((a > half) | ((a == half) & upper_even)).sum(-1)
+    return (torch.sign(b) * level[code] * unit).reshape(shape)
 
 
 def exact(case, seed):
