@@ -116,13 +116,18 @@ def _axis_of_pair(case):
 
 
 # ------------------------------------------------------------------ inputs
+def _pow2(e):
+    """2^e in float32 for integer tensors -126 <= e <= 127, from its bits."""
+    return ((e.int() + 127) << 23).view(torch.float32)
+
+
 def _quantise(x, block):
     """bf16 [..., D] -> (codes [..., D / 2], scale bytes [..., D / block])."""
     b = x.float().unflatten(-1, (-1, block))
     amax = b.abs().amax(-1)
     e = torch.frexp(amax).exponent - 3
     X = torch.where(amax > 0, e, torch.full_like(e, -127)).clamp_min(-127)
-    y = torch.ldexp(b, -X.unsqueeze(-1))
+    y = b * _pow2(-X).unsqueeze(-1)
     a = y.abs()
     step = torch.where(a < 2, 0.5, torch.where(a < 4, 1.0, 2.0))
     r = (torch.round(a / step) * step).clamp_max(6.0)
@@ -137,7 +142,9 @@ def _values(codes, scales, block, dtype):
     lut = torch.tensor(_LEVELS + tuple(-v for v in _LEVELS), dtype=dtype, device=codes.device)
     pair = torch.stack([codes & 15, codes >> 4], dim=-1).flatten(-2)
     v = lut[pair.int()].unflatten(-1, (-1, block))
-    return torch.ldexp(v, (scales.int() - 127).unsqueeze(-1)).flatten(-2)
+    e = scales.int() - 127
+    p = torch.where(e > -127, _pow2(e.clamp_min(-126)), torch.full_like(e, 2.0 ** -127, dtype=torch.float32))
+    return (v * p.to(dtype).unsqueeze(-1)).flatten(-2)
 
 
 def prepare(case, seed):
@@ -321,8 +328,8 @@ def _exact_decode(codes, scales, block):
     c = c - 8 * neg
     e = torch.floor(c / 2)
     f = c - 2 * e
-    mag = torch.where(e == 0, f / 2, (1 + f / 2) * torch.exp2(e - 1))
-    x = torch.exp2(scales.to(torch.float64) - 127).repeat_interleave(block, dim=-1)
+    mag = torch.where(e == 0, f / 2, (1 + f / 2) * 2.0 ** (e - 1))
+    x = ((scales.long() - 127 + 1023) << 52).view(torch.float64).repeat_interleave(block, dim=-1)
     return mag * (1 - 2 * neg) * x
 
 
@@ -331,9 +338,9 @@ def _exact_round(x, block):
     shape = x.shape
     b = x.double().reshape(-1, block)
     top = b.abs().max(dim=1).values
-    X = torch.floor(torch.log2(torch.where(top > 0, top, torch.ones_like(top)))) - 2
-    X = torch.where(top > 0, X, torch.full_like(X, -127.0)).clamp(min=-127.0)
-    unit = torch.exp2(X)[:, None]
+    X = torch.frexp(top).exponent - 3
+    X = torch.where(top > 0, X, torch.full_like(X, -127)).clamp(min=-127)
+    unit = ((X.long() + 1023) << 52).view(torch.float64)[:, None]
     level = torch.tensor(_LEVELS, dtype=torch.float64, device=x.device)
     half = (level[1:] + level[:-1]) / 2
     a = (b.abs() / unit)[..., None]
