@@ -101,7 +101,8 @@ enum {
   RNL_OP_QKV_ROPE = 4,
   RNL_OP_QMRS = 5,
   RNL_OP_MXFP8 = 6,
-  RNL_OP_W8A8_PREPARED = 7
+  RNL_OP_W8A8_PREPARED = 7,
+  RNL_OP_KV4_ATTENTION = 8
 };
 
 /* Library version (major * 10000 + minor * 100 + patch). */
@@ -130,6 +131,7 @@ const char *rnl_status_string(rnl_status s);
  *   RNL_OP_QMRS:    T = M, K, N, N2 = B (the batch)
  *   RNL_OP_MXFP8:   T, K, N; N2 ignored (rmsnorm_linear_mxfp8 and mxfp8_scaled_mm)
  *   RNL_OP_W8A8_PREPARED: T, K, N; N2 ignored (rmsnorm_linear_w8a8_prepared)
+ *   RNL_OP_KV4_ATTENTION: T = rows, K = head_dim, N = n_q_heads, N2 = n_kv_heads
  * Returns (size_t)-1 for invalid sizes.  Host-only; needs no GPU.
  */
 size_t rnl_workspace_size(int op, int64_t T, int64_t K, int64_t N, int64_t N2);
@@ -210,6 +212,120 @@ rnl_status rnl_qkv_rope(const void *y, int64_t T, int64_t n_q_heads, int64_t n_k
                         int64_t head_dim, const void *q_gamma, const void *k_gamma, float eps,
                         const int32_t *positions, const float *cos_sin, int64_t max_pos,
                         void *q_out, void *k_out, void *v_out, rnl_stream_t stream);
+
+/*
+ * rnl_qkv_rope with positions of several axes (time, height and width of a
+ * video, row and column of an image; no counterpart on the pages, which have
+ * one position a token).  Pair i (elements i and i + D/2) turns by the angle
+ * in column i of the row of its own axis' position:
+ *   n_axes        1 .. RNL_ROPE_MAX_AXES (else RNL_ERR_ARG)
+ *   positions     int32 [n_axes, T]: row a holds every token's position on axis
+ *                 a.  A token with one of its positions outside [0, max_pos)
+ *                 keeps its q / k rows unwritten and makes the next
+ *                 rnl_check_device_error() return RNL_ERR_ARG.  Positions of
+ *                 an axis that no pair uses are not read.
+ *   axis_of_pair  HOST pointer, head_dim / 2 values below n_axes (else
+ *                 RNL_ERR_ARG): contiguous sections, interleaved, or any other
+ *                 assignment.  Read during the call only.
+ *   q_gamma, k_gamma  as rnl_qkv_rope, or NULL: those heads are not normalised
+ *                 (z is the bf16 head itself)
+ * Everything else as rnl_qkv_rope; with one axis and both gammas the results
+ * are the same bits.
+ */
+#define RNL_ROPE_MAX_AXES 4
+rnl_status rnl_qkv_rope_axes(const void *y, int64_t T, int64_t n_q_heads, int64_t n_kv_heads,
+                             int64_t head_dim, const void *q_gamma, const void *k_gamma, float eps,
+                             const int32_t *positions, int64_t n_axes, const uint8_t *axis_of_pair,
+                             const float *cos_sin, int64_t max_pos, void *q_out, void *k_out,
+                             void *v_out, rnl_stream_t stream);
+
+/*
+ * The 4-bit paged KV cache: where k and v of the qkv stage go, and what
+ * attention reads (no counterpart on the pages).  MX format with E2M1
+ * elements, the 4-bit sibling of the MXFP8 mode's E4M3:
+ *   codes   uint8 [n_pages, n_kv_heads, page_size, head_dim / 2]: element 2j of
+ *           a head row in the low nibble of byte j, element 2j + 1 in the high
+ *   scales  uint8 [n_pages, n_kv_heads, page_size, head_dim / block]: E8M0, the
+ *           elements of that block are E2M1 value * 2^(byte - 127)
+ * for keys and values each.  head_dim 64, 128 or 256; page_size a power of two
+ * in [16, 1024] (else RNL_ERR_UNSUPPORTED); block 32 or 64 (else RNL_ERR_ARG).
+ * Device pointers, 16-byte aligned.
+ */
+typedef struct rnl_kv4_cache {
+  void *k_codes, *k_scales, *v_codes, *v_scales;
+  int64_t n_pages, n_kv_heads, page_size, head_dim, block;
+} rnl_kv4_cache;
+
+/*
+ * The sequences of a call.  Sequence b has seq_lens[b] tokens in the cache,
+ * token j in page block_table[b, j / page_size] at offset j % page_size, and
+ * the call's rows cu_rows[b] .. cu_rows[b + 1] - 1 are its LAST tokens: row i
+ * of r rows stands at position seq_lens[b] - r + i.  cu_rows = NULL: one row a
+ * sequence (n_rows == n_seqs).  Rows from cu_rows[n_seqs] on belong to no
+ * sequence: their outputs are left as they were (padded batches).
+ *   block_table int32 [n_seqs, max_pages];  seq_lens int32 [n_seqs];
+ *   cu_rows int32 [n_seqs + 1], not decreasing, from 0, or NULL
+ * These are device arrays and are checked on the device: a sequence whose
+ * rows or length are out of range (length above max_pages * page_size, rows
+ * beyond n_rows, cu_rows decreasing) and a page id outside [0, n_pages) make
+ * the next rnl_check_device_error() return RNL_ERR_ARG; the rows concerned are
+ * left unwritten or, for a bad page that attention would read, unspecified.
+ * Two sequences may share pages that the call only reads.
+ */
+typedef struct rnl_kv4_seqs {
+  const int32_t *block_table, *seq_lens, *cu_rows;
+  int64_t n_seqs, max_pages, n_rows;
+} rnl_kv4_seqs;
+
+/*
+ * Quantises the rows of k and v into the cache at their positions.
+ *   k, v  bf16 [n_rows, n_kv_heads, head_dim], rows k_stride / v_stride elements
+ *         apart (multiples of 8, at least n_kv_heads * head_dim): k and v of
+ *         rnl_qkv_rope, or column ranges of a wider projection output
+ * Per block: X = floor(log2 max|x|) - 2 (at least -127; an all-zero block gets
+ * -127), scale byte X + 127, codes E2M1(x * 2^-X) rounded to nearest even and
+ * saturated to +-6: exact functions of x.  A block with an infinity or NaN
+ * gets scale byte 255, and what reads it is not finite.  A row with no
+ * position (more rows than the length counts) is reported as RNL_ERR_ARG.
+ * Other tokens of the cache are not touched.  Two rows of a call must not name
+ * the same place (a page twice in the tables' written parts): its contents
+ * would be a mixture of both.
+ */
+rnl_status rnl_kv4_append(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                          const rnl_kv4_cache *cache, const rnl_kv4_seqs *seqs, rnl_stream_t stream);
+
+/*
+ * The rows' tokens read back as bf16 (exact): k_out, v_out [n_rows,
+ * n_kv_heads, head_dim].  A cached prefix is fetched by giving every sequence
+ * as many rows as tokens wanted.
+ */
+rnl_status rnl_kv4_gather(const rnl_kv4_cache *cache, const rnl_kv4_seqs *seqs, void *k_out, void *v_out,
+                          rnl_stream_t stream);
+
+/*
+ * Attention of the rows' queries over their sequences' cached tokens:
+ *   out[t, h] = sum_j softmax_j(scale * q[t, h] . k[j, h / G]) v[j, h / G],
+ *   G = n_q_heads / n_kv_heads (n_q_heads a multiple, else RNL_ERR_SHAPE)
+ *   q       bf16 [n_rows, n_q_heads, head_dim], rows q_stride elements apart
+ *           (a multiple of 8, at least n_q_heads * head_dim)
+ *   causal  1: the row at position p reads tokens 0 .. p (the rows' own tokens
+ *           are appended first), with window > 0 only the last `window` of
+ *           them; 0: every row reads all seq_lens[b] tokens (cross attention;
+ *           window must be 0, else RNL_ERR_ARG)
+ *   out     bf16 [n_rows, n_q_heads, head_dim], rounded once
+ *   lse_out fp32 [n_rows, n_q_heads] or NULL: log sum_j exp(scale * q . k[j])
+ * A row that reads no token (length 0, or a position below 0) gets zeros and
+ * lse -infinity.  What stands in the cache behind a sequence's length has no
+ * effect.  Softmax statistics and sums in FP32; products of binary16 operands
+ * that hold the cache's values and q (scaled by powers of two) exactly down to
+ * 2^-37 of the largest; the softmax weights are rounded to binary16 (11 bits).
+ * Workspace: rnl_workspace_size(RNL_OP_KV4_ATTENTION, n_rows, head_dim,
+ * n_q_heads, n_kv_heads) bytes; results do not depend on its contents.
+ */
+rnl_status rnl_kv4_attention(const void *q, int64_t q_stride, int64_t n_q_heads,
+                             const rnl_kv4_cache *cache, const rnl_kv4_seqs *seqs, float scale, int causal,
+                             int64_t window, void *out, float *lse_out, void *workspace,
+                             size_t workspace_bytes, rnl_stream_t stream);
 
 /*
  * rmsnorm_linear_bf16 (AT-10, bf16 out, N = (n_q_heads + 2 * n_kv_heads) *

@@ -20,6 +20,11 @@ arguments; the computation runs in the library's CUDA kernels.
     mxfp8_scaled_mm       scaled_mm on MXFP8 operands
     rnl_qkv_rope / rmsnorm_linear_qkv_rope
                           QKV split + per-head RMSNorm + RoPE after the qkv projection
+    rnl_qkv_rope_axes     the same stage with positions of several axes
+    Kv4Cache, rnl_kv4_append / rnl_kv4_gather
+                          the 4-bit paged KV cache: quantise k and v into it, read them back
+    rnl_kv4_attention     attention over that cache: single tokens, drafts, prompts,
+                          cross attention
     rnl_pipeline_*        host-buffer pipeline: calls fed from and answering into
                           pinned host memory, copies overlapped with the kernels
     debug_library()       route calls through librnl_debug.so, the build whose
@@ -31,6 +36,7 @@ from ._native import (  # noqa: F401
     NORM_SQRT_DIV,
     OP_BF16,
     OP_GEMM_S8,
+    OP_KV4_ATTENTION,
     OP_MLA,
     OP_MXFP8,
     OP_QKV_ROPE,
@@ -39,6 +45,7 @@ from ._native import (  # noqa: F401
     OP_W8A8_PREPARED,
     OUT_BF16,
     OUT_FP32,
+    Kv4Cache,
     PipelineHandle,
     RnlError,
     debug_library,
@@ -58,6 +65,9 @@ from ._native import (  # noqa: F401
     rnl_debug_build,
     rnl_gemm_s8s8s32,
     rnl_head_rmsnorm,
+    rnl_kv4_append,
+    rnl_kv4_attention,
+    rnl_kv4_gather,
     rnl_pipeline_create,
     rnl_pipeline_destroy,
     rnl_pipeline_submit_bf16,
@@ -65,6 +75,7 @@ from ._native import (  # noqa: F401
     rnl_pipeline_submit_w8a8,
     rnl_pipeline_wait,
     rnl_qkv_rope,
+    rnl_qkv_rope_axes,
     rnl_selftest_bounds_check,
     rnl_selftest_wait_timeout,
     rnl_trace_enable,

@@ -22,7 +22,7 @@ DEBUG_LIB_PATH = os.path.join(PKG, "librnl_debug.so")
 
 NORM_RSQRT, NORM_SQRT_DIV = 0, 1
 OUT_BF16, OUT_FP32 = 0, 1
-OP_BF16, OP_W8A8, OP_MLA, OP_GEMM_S8, OP_QKV_ROPE, OP_QMRS, OP_MXFP8, OP_W8A8_PREPARED = range(8)
+OP_BF16, OP_W8A8, OP_MLA, OP_GEMM_S8, OP_QKV_ROPE, OP_QMRS, OP_MXFP8, OP_W8A8_PREPARED, OP_KV4_ATTENTION = range(9)
 
 STATUS = {
     0: "RNL_OK", 1: "RNL_ERR_NULL", 2: "RNL_ERR_SHAPE", 3: "RNL_ERR_ALIGN", 4: "RNL_ERR_ARG",
@@ -38,13 +38,24 @@ EXPORTS = ("rnl_version", "rnl_debug_build", "rnl_selftest_bounds_check", "rnl_s
            "rnl_pipeline_destroy", "rmsnorm_linear_bf16_ex", "rnl_qkv_rope",
            "rmsnorm_linear_qkv_rope", "quant_matmul_reduce_sum", "rmsnorm_linear_mxfp8",
            "mxfp8_scaled_mm", "rnl_head_rmsnorm", "mla_q_chain_head_norm", "rnl_w8a8_prepare_weight",
-           "rmsnorm_linear_w8a8_prepared")
+           "rmsnorm_linear_w8a8_prepared", "rnl_qkv_rope_axes", "rnl_kv4_append", "rnl_kv4_gather",
+           "rnl_kv4_attention")
 
 
 class RnlError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {STATUS.get(status, status)}")
         self.status = status
+
+
+class _Kv4CacheC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "k_scales", "v_codes", "v_scales")] + \
+        [(n, ctypes.c_int64) for n in ("n_pages", "n_kv_heads", "page_size", "head_dim", "block")]
+
+
+class _Kv4SeqsC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("block_table", "seq_lens", "cu_rows")] + \
+        [(n, ctypes.c_int64) for n in ("n_seqs", "max_pages", "n_rows")]
 
 
 _lock = threading.Lock()
@@ -86,6 +97,13 @@ def _declare(lib):
         "rmsnorm_linear_qkv_rope": (I, [P, P, P, I64, I64, I64, I64, I64, F, I, P, P, F, P, P, I64,
                                         P, P, P, P, SZ, P]),
     }
+    CP, SP = ctypes.POINTER(_Kv4CacheC), ctypes.POINTER(_Kv4SeqsC)
+    sig.update({
+        "rnl_qkv_rope_axes": (I, [P, I64, I64, I64, I64, P, P, F, P, I64, P, P, I64, P, P, P, P]),
+        "rnl_kv4_append": (I, [P, I64, P, I64, CP, SP, P]),
+        "rnl_kv4_gather": (I, [CP, SP, P, P, P]),
+        "rnl_kv4_attention": (I, [P, I64, I64, CP, SP, F, I, I64, P, P, P, SZ, P]),
+    })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -258,6 +276,137 @@ def rnl_qkv_rope(y, n_q_heads, n_kv_heads, head_dim, q_gamma, k_gamma, positions
                                _ptr(positions), _ptr(cos_sin), P, _ptr(q_out), _ptr(k_out),
                                _ptr(v_out), _stream(dev, stream)), "rnl_qkv_rope")
     return q_out, k_out, v_out
+
+
+def rnl_qkv_rope_axes(y, n_q_heads, n_kv_heads, head_dim, q_gamma, k_gamma, positions, axis_of_pair, cos_sin,
+                      eps=1e-6, q_out=None, k_out=None, v_out=None, stream=None):
+    """rnl_qkv_rope with positions of several axes: positions int32 [n_axes, T],
+    axis_of_pair a host sequence of head_dim / 2 axis numbers; a None gamma
+    leaves its heads without the norm.  Returns (q, k, v)."""
+    T = y.shape[0]
+    Hq, Hkv, D = n_q_heads, n_kv_heads, head_dim
+    dev = y.device
+    _need(y, "y", torch.bfloat16, (T, (Hq + 2 * Hkv) * D), dev)
+    if q_gamma is not None:
+        _need(q_gamma, "q_gamma", torch.bfloat16, (D,), dev)
+    if k_gamma is not None:
+        _need(k_gamma, "k_gamma", torch.bfloat16, (D,), dev)
+    A = positions.shape[0]
+    _need(positions, "positions", torch.int32, (A, T), dev)
+    axes = bytes(axis_of_pair)
+    if len(axes) != D // 2:
+        raise ValueError(f"axis_of_pair must hold {D // 2} values, got {len(axes)}")
+    P = cos_sin.shape[0]
+    _need(cos_sin, "cos_sin", torch.float32, (P, D), dev)
+    q_out, k_out, v_out = _qkv_outputs(T, Hq, Hkv, D, dev, q_out, k_out, v_out)
+    _check(load().rnl_qkv_rope_axes(_ptr(y), T, Hq, Hkv, D, _ptr(q_gamma), _ptr(k_gamma), float(eps),
+                                    _ptr(positions), A, axes, _ptr(cos_sin), P, _ptr(q_out), _ptr(k_out),
+                                    _ptr(v_out), _stream(dev, stream)), "rnl_qkv_rope_axes")
+    return q_out, k_out, v_out
+
+
+class Kv4Cache:
+    """The tensors of a 4-bit paged KV cache (include/rnl.h, rnl_kv4_cache): codes
+    uint8 [n_pages, n_kv_heads, page_size, head_dim / 2] and E8M0 scale bytes
+    [n_pages, n_kv_heads, page_size, head_dim / block] of keys and of values."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales):
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        if k_codes.dim() != 4 or k_scales.dim() != 4 or 0 in k_scales.shape:
+            raise ValueError("codes and scales must be [n_pages, n_kv_heads, page_size, ...]")
+        P, H, S, half = k_codes.shape
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = P, H, S, 2 * half
+        self.block = self.head_dim // k_scales.shape[3]
+        self.device = k_codes.device
+        for t, name, w in ((k_codes, "k_codes", half), (k_scales, "k_scales", k_scales.shape[3]),
+                           (v_codes, "v_codes", half), (v_scales, "v_scales", k_scales.shape[3])):
+            _need(t, name, torch.uint8, (P, H, S, w), self.device)
+
+    @classmethod
+    def empty(cls, n_pages, n_kv_heads, page_size, head_dim, block=32, device="cuda"):
+        """An uninitialised cache (what no sequence's length covers is never read)."""
+        def t(width):
+            return torch.empty((n_pages, n_kv_heads, page_size, width), dtype=torch.uint8, device=device)
+        return cls(t(head_dim // 2), t(head_dim // block), t(head_dim // 2), t(head_dim // block))
+
+    def _c(self):
+        return _Kv4CacheC(self.k_codes.data_ptr(), self.k_scales.data_ptr(), self.v_codes.data_ptr(),
+                          self.v_scales.data_ptr(), self.n_pages, self.n_kv_heads, self.page_size,
+                          self.head_dim, self.block)
+
+
+def _kv4_seqs(cache, block_table, seq_lens, cu_rows, n_rows):
+    dev = cache.device
+    B = seq_lens.shape[0]
+    _need(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    _need(block_table, "block_table", torch.int32, (B, block_table.shape[-1]), dev)
+    if cu_rows is not None:
+        _need(cu_rows, "cu_rows", torch.int32, (B + 1,), dev)
+    return _Kv4SeqsC(block_table.data_ptr(), seq_lens.data_ptr(), None if cu_rows is None else cu_rows.data_ptr(),
+                     B, block_table.shape[-1], n_rows)
+
+
+def _need_rows(t, name, shape, device):
+    """A bf16 [rows, heads, head_dim] tensor whose rows may be apart; the row stride."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    T, H, D = shape
+    if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D)):
+        raise ValueError(f"{name} must have contiguous rows of heads")
+    return t.stride(0) if T > 1 else H * D
+
+
+def rnl_kv4_append(k, v, cache, block_table, seq_lens, cu_rows=None, stream=None):
+    """Quantise the rows of k and v [T, Hkv, D] (bf16, rows may be strided) into the
+    last positions of their sequences; seq_lens counts them already."""
+    T = k.shape[0]
+    dev = cache.device
+    ks = _need_rows(k, "k", (T, cache.n_kv_heads, cache.head_dim), dev)
+    vs = _need_rows(v, "v", (T, cache.n_kv_heads, cache.head_dim), dev)
+    seqs = _kv4_seqs(cache, block_table, seq_lens, cu_rows, T)
+    _check(load().rnl_kv4_append(_ptr(k), ks, _ptr(v), vs, cache._c(), seqs, _stream(dev, stream)),
+           "rnl_kv4_append")
+
+
+def rnl_kv4_gather(cache, block_table, seq_lens, n_rows, cu_rows=None, k_out=None, v_out=None, stream=None):
+    """The last tokens of every sequence (as many as it has rows) back as bf16:
+    returns (k, v) [n_rows, Hkv, D]."""
+    dev = cache.device
+    shape = (n_rows, cache.n_kv_heads, cache.head_dim)
+    k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k_out is None else k_out
+    v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v_out is None else v_out
+    _need(k_out, "k_out", torch.bfloat16, shape, dev)
+    _need(v_out, "v_out", torch.bfloat16, shape, dev)
+    seqs = _kv4_seqs(cache, block_table, seq_lens, cu_rows, n_rows)
+    _check(load().rnl_kv4_gather(cache._c(), seqs, _ptr(k_out), _ptr(v_out), _stream(dev, stream)),
+           "rnl_kv4_gather")
+    return k_out, v_out
+
+
+def rnl_kv4_attention(q, cache, block_table, seq_lens, cu_rows=None, scale=None, causal=True, window=0,
+                      out=None, lse_out=None, workspace=None, stream=None):
+    """Attention of q [T, Hq, D] (bf16, rows may be strided) over the cached tokens
+    of the rows' sequences; scale defaults to 1 / sqrt(D).  Returns out."""
+    T, Hq = q.shape[0], q.shape[1]
+    D = cache.head_dim
+    dev = cache.device
+    qs = _need_rows(q, "q", (T, Hq, D), dev)
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    _need(out, "out", torch.bfloat16, (T, Hq, D), dev)
+    if lse_out is not None:
+        _need(lse_out, "lse_out", torch.float32, (T, Hq), dev)
+    seqs = _kv4_seqs(cache, block_table, seq_lens, cu_rows, T)
+    ws = _workspace(workspace_size(OP_KV4_ATTENTION, T, D, Hq, cache.n_kv_heads), dev, workspace)
+    _check(load().rnl_kv4_attention(_ptr(q), qs, Hq, cache._c(), seqs,
+                                    float(D ** -0.5 if scale is None else scale), int(bool(causal)), int(window),
+                                    _ptr(out), _ptr(lse_out), _ptr(ws), ws.numel() * ws.element_size(),
+                                    _stream(dev, stream)), "rnl_kv4_attention")
+    return out
 
 
 def rmsnorm_linear_qkv_rope(x, gamma, W, n_q_heads, n_kv_heads, head_dim, q_gamma, k_gamma,

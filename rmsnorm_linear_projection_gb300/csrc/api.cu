@@ -246,6 +246,31 @@ S8Layout s8_layout(void* ws, int64_t M, int64_t K, int64_t N) {
   return l;
 }
 
+// The cache and sequences that the kv4 calls share.  Rows, heads and pages
+// stay inside 32-bit kernel indices; byte offsets into the cache are 64-bit.
+rnl_status check_kv4(const rnl_kv4_cache* c, const rnl_kv4_seqs* q) {
+  if (!c || !q) return RNL_ERR_NULL;
+  if (bad_dim(c->n_pages) || c->n_pages == 0 || bad_dim(c->n_kv_heads) || c->n_kv_heads == 0 ||
+      c->n_kv_heads > 65535 || bad_dim(q->n_seqs) || bad_dim(q->max_pages) || bad_dim(q->n_rows))
+    return RNL_ERR_SHAPE;
+  if (!qkv_rope_head_dim_ok(c->head_dim)) return RNL_ERR_UNSUPPORTED;
+  if (!mx_block_ok(c->block)) return RNL_ERR_ARG;
+  if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) != 0)
+    return RNL_ERR_UNSUPPORTED;
+  if (bad_dim(q->max_pages * c->page_size) || bad_dim(q->n_rows * (c->n_kv_heads * c->head_dim / 64)))
+    return RNL_ERR_SHAPE;
+  if (!q->cu_rows && q->n_rows != q->n_seqs) return RNL_ERR_SHAPE;
+  if (q->n_rows == 0 || q->n_seqs == 0) return RNL_OK;
+  if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales || !q->seq_lens ||
+      (!q->block_table && q->max_pages > 0))
+    return RNL_ERR_NULL;
+  if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) ||
+      !aligned16(c->v_scales) || (reinterpret_cast<uintptr_t>(q->seq_lens) & 3u) ||
+      (reinterpret_cast<uintptr_t>(q->block_table) & 3u) || (reinterpret_cast<uintptr_t>(q->cu_rows) & 3u))
+    return RNL_ERR_ALIGN;
+  return RNL_OK;
+}
+
 inline cudaStream_t cs(rnl_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 // The W8A8 front end's quantising part: the streamed form (each row read
@@ -440,12 +465,13 @@ void trace_after(cudaStream_t s, const char* name) {
 }
 
 rnl_status read_device_errors(int* site) {
-  unsigned int words[10] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+  unsigned int words[12] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
   if (read_clear_error_rowwise(&words[0]) != RNL_OK || read_clear_error_gemm(&words[1]) != RNL_OK ||
       read_clear_error_skinny(&words[2]) != RNL_OK || read_clear_error_pair(&words[3]) != RNL_OK ||
       read_clear_error_norm(&words[4]) != RNL_OK || read_clear_error_selftest(&words[5]) != RNL_OK ||
       read_clear_error_rope(&words[6]) != RNL_OK || read_clear_error_mx(&words[7]) != RNL_OK ||
-      read_clear_error_quant(&words[8]) != RNL_OK || read_clear_error_decmma(&words[9]) != RNL_OK)
+      read_clear_error_quant(&words[8]) != RNL_OK || read_clear_error_decmma(&words[9]) != RNL_OK ||
+      read_clear_error_kv4cache(&words[10]) != RNL_OK || read_clear_error_kv4attn(&words[11]) != RNL_OK)
     return RNL_ERR_LAUNCH;
   for (unsigned int w : words) {
     if (w != 0) {
@@ -507,6 +533,9 @@ size_t rnl_workspace_size(int op, int64_t T, int64_t K, int64_t N, int64_t N2) {
       if (N2 <= 0) return static_cast<size_t>(-1);
       return qmrs_layout(nullptr, N2, T, K, N).bytes;
     case RNL_OP_MXFP8: return mx_layout(nullptr, T, K, N).bytes;
+    case RNL_OP_KV4_ATTENTION:
+      if (!qkv_rope_head_dim_ok(K) || N == 0 || N2 == 0 || N % N2 != 0) return static_cast<size_t>(-1);
+      return round_up(kv4_attn_workspace_bytes(T, K, N, N2));
     case RNL_OP_QKV_ROPE:
       return bf16_layout(nullptr, T, K, N, RNL_OUT_BF16).bytes + round_up(static_cast<size_t>(T) * N * 2);
   }
@@ -663,6 +692,97 @@ rnl_status rnl_qkv_rope(const void* y, int64_t T, int64_t n_q_heads, int64_t n_k
   if (st != RNL_OK) return st;
   return launch_qkv_rope(y, T, n_q_heads, n_kv_heads, head_dim, q_gamma, k_gamma, eps, positions,
                          cos_sin, max_pos, q_out, k_out, v_out, cs(stream));
+}
+
+rnl_status rnl_qkv_rope_axes(const void* y, int64_t T, int64_t n_q_heads, int64_t n_kv_heads,
+                             int64_t head_dim, const void* q_gamma, const void* k_gamma, float eps,
+                             const int32_t* positions, int64_t n_axes, const uint8_t* axis_of_pair,
+                             const float* cos_sin, int64_t max_pos, void* q_out, void* k_out,
+                             void* v_out, rnl_stream_t stream) {
+  if (bad_dim(T) || bad_dim(n_q_heads) || bad_dim(n_kv_heads) || bad_dim(max_pos) ||
+      n_q_heads + 2 * n_kv_heads == 0 || max_pos == 0 ||
+      n_q_heads + 2 * n_kv_heads > kMaxDim / 256 || bad_dim(T * (n_q_heads + 2 * n_kv_heads)))
+    return RNL_ERR_SHAPE;
+  if (!qkv_rope_head_dim_ok(head_dim)) return RNL_ERR_UNSUPPORTED;
+  if (bad_eps(eps) || n_axes < 1 || n_axes > RNL_ROPE_MAX_AXES) return RNL_ERR_ARG;
+  if (!axis_of_pair) return RNL_ERR_NULL;
+  for (int64_t i = 0; i < head_dim / 2; ++i)
+    if (axis_of_pair[i] >= n_axes) return RNL_ERR_ARG;
+  if (T == 0) return RNL_OK;
+  if (!y || !positions || !cos_sin || (n_q_heads && !q_out) || (n_kv_heads && (!k_out || !v_out)))
+    return RNL_ERR_NULL;
+  if (!aligned16(y) || !aligned16(cos_sin) || (q_gamma && !aligned16(q_gamma)) ||
+      (k_gamma && !aligned16(k_gamma)) || (q_out && !aligned16(q_out)) ||
+      (k_out && !aligned16(k_out)) || (v_out && !aligned16(v_out)) ||
+      (reinterpret_cast<uintptr_t>(positions) & 3u))
+    return RNL_ERR_ALIGN;
+  DeviceInfo dev;
+  const rnl_status st = current_device(&dev);
+  if (st != RNL_OK) return st;
+  return launch_qkv_rope_axes(y, T, n_q_heads, n_kv_heads, head_dim, q_gamma, k_gamma, eps, positions,
+                              axis_of_pair, cos_sin, max_pos, q_out, k_out, v_out, cs(stream));
+}
+
+rnl_status rnl_kv4_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                          const rnl_kv4_cache* cache, const rnl_kv4_seqs* seqs, rnl_stream_t stream) {
+  rnl_status st = check_kv4(cache, seqs);
+  if (st != RNL_OK || seqs->n_rows == 0 || seqs->n_seqs == 0) return st;
+  const int64_t row = cache->n_kv_heads * cache->head_dim;
+  if (k_stride < row || v_stride < row || bad_dim(k_stride) || bad_dim(v_stride)) return RNL_ERR_SHAPE;
+  if (!k || !v) return RNL_ERR_NULL;
+  if (!aligned16(k) || !aligned16(v) || k_stride % 8 != 0 || v_stride % 8 != 0) return RNL_ERR_ALIGN;
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != RNL_OK) return st;
+  return launch_kv4_append(k, k_stride, v, v_stride, *cache, *seqs, cs(stream));
+}
+
+rnl_status rnl_kv4_gather(const rnl_kv4_cache* cache, const rnl_kv4_seqs* seqs, void* k_out, void* v_out,
+                          rnl_stream_t stream) {
+  rnl_status st = check_kv4(cache, seqs);
+  if (st != RNL_OK || seqs->n_rows == 0 || seqs->n_seqs == 0) return st;
+  if (!k_out || !v_out) return RNL_ERR_NULL;
+  if (!aligned16(k_out) || !aligned16(v_out)) return RNL_ERR_ALIGN;
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != RNL_OK) return st;
+  return launch_kv4_gather(*cache, *seqs, k_out, v_out, cs(stream));
+}
+
+rnl_status rnl_kv4_attention(const void* q, int64_t q_stride, int64_t n_q_heads,
+                             const rnl_kv4_cache* cache, const rnl_kv4_seqs* seqs, float scale, int causal,
+                             int64_t window, void* out, float* lse_out, void* workspace,
+                             size_t workspace_bytes, rnl_stream_t stream) {
+  rnl_status st = check_kv4(cache, seqs);
+  if (st != RNL_OK) return st;
+  if (bad_dim(n_q_heads) || n_q_heads == 0 || n_q_heads % cache->n_kv_heads != 0 ||
+      n_q_heads > kMaxDim / 256 || bad_dim(window) || bad_dim(seqs->n_rows * n_q_heads))
+    return RNL_ERR_SHAPE;
+  if (!std::isfinite(scale) || (causal != 0 && causal != 1) || (window > 0 && !causal)) return RNL_ERR_ARG;
+  if (seqs->n_rows == 0 || seqs->n_seqs == 0) return RNL_OK;
+  if (q_stride < n_q_heads * cache->head_dim || bad_dim(q_stride)) return RNL_ERR_SHAPE;
+  if (!q || !out) return RNL_ERR_NULL;
+  if (!aligned16(q) || !aligned16(out) || q_stride % 8 != 0 ||
+      (reinterpret_cast<uintptr_t>(lse_out) & 3u) || (workspace && !aligned16(workspace)))
+    return RNL_ERR_ALIGN;
+  const size_t need =
+      rnl_workspace_size(RNL_OP_KV4_ATTENTION, seqs->n_rows, cache->head_dim, n_q_heads, cache->n_kv_heads);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return RNL_ERR_WORKSPACE;
+  DeviceInfo dev;
+  st = current_device(&dev);
+  if (st != RNL_OK) return st;
+  Kv4AttnArgs a;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.Hq = n_q_heads;
+  a.scale = scale;
+  a.causal = causal != 0;
+  a.window = window;
+  a.out = out;
+  a.lse = lse_out;
+  a.ws = workspace;
+  a.ws_bytes = workspace_bytes;
+  return launch_kv4_attention(a, *cache, *seqs, cs(stream));
 }
 
 rnl_status rmsnorm_linear_qkv_rope(const void* x, const void* gamma, const void* W, int64_t T,

@@ -180,6 +180,38 @@ rnl_status launch_qkv_rope(const void* y, int64_t T, int64_t Hq, int64_t Hkv, in
                            const int32_t* positions, const float* cos_sin, int64_t max_pos,
                            void* q, void* k, void* v, cudaStream_t s);
 
+// The same with one position per axis (positions [axes, T]) and the host map
+// axis_of_pair [D / 2]; null gammas: no head norm.
+rnl_status launch_qkv_rope_axes(const void* y, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                                const void* q_gamma, const void* k_gamma, float eps,
+                                const int32_t* positions, const uint8_t* axis_of_pair,
+                                const float* cos_sin, int64_t max_pos, void* q, void* k, void* v,
+                                cudaStream_t s);
+
+// ---- 4-bit KV cache (kv4cache.cu) and attention over it (kv4attn.cu) ----
+// Quantises rows of k and v [n_rows, Hkv, D] (row strides in elements) into
+// the last positions of their sequences' pages.
+rnl_status launch_kv4_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             const rnl_kv4_cache& c, const rnl_kv4_seqs& q, cudaStream_t s);
+// The inverse: the same positions as bf16 [n_rows, Hkv, D].
+rnl_status launch_kv4_gather(const rnl_kv4_cache& c, const rnl_kv4_seqs& q, void* k_out, void* v_out,
+                             cudaStream_t s);
+struct Kv4AttnArgs {
+  const void* q = nullptr;  // bf16 rows of Hq * D, q_stride elements apart
+  int64_t q_stride = 0;
+  int64_t Hq = 0;
+  float scale = 0.f;
+  bool causal = true;
+  int64_t window = 0;
+  void* out = nullptr;   // bf16 [n_rows, Hq, D]
+  float* lse = nullptr;  // [n_rows, Hq] or null
+  void* ws = nullptr;
+  size_t ws_bytes = 0;
+};
+size_t kv4_attn_workspace_bytes(int64_t T, int64_t D, int64_t Hq, int64_t Hkv);
+rnl_status launch_kv4_attention(const Kv4AttnArgs& a, const rnl_kv4_cache& c, const rnl_kv4_seqs& q,
+                                cudaStream_t s);
+
 // ---- tcgen05 GEMM (gemm_tc.cu) ----
 enum class Epi : int {
   kBf16 = 0,         // out bf16 = acc
@@ -300,6 +332,8 @@ rnl_status read_clear_error_rope(unsigned int* word);
 rnl_status read_clear_error_mx(unsigned int* word);
 rnl_status read_clear_error_quant(unsigned int* word);
 rnl_status read_clear_error_decmma(unsigned int* word);
+rnl_status read_clear_error_kv4cache(unsigned int* word);
+rnl_status read_clear_error_kv4attn(unsigned int* word);
 // Reads and clears all of them without synchronising (api.cu): RNL_OK, or
 // RNL_ERR_TIMEOUT / RNL_ERR_ARG with the first recorded site in *site
 // (optional).

@@ -1,0 +1,147 @@
+// kv4.cuh -- device-side pieces of the 4-bit paged KV cache that its writer,
+// its reader and the attention kernels share: the element format and the walk
+// from a row of the call to its sequence and page.
+//
+// Format (MX with E2M1 elements): a block of 32 or 64 elements of one token's
+// head row shares the power of two 2^X; element = E2M1 value (0, 0.5, 1, 1.5,
+// 2, 3, 4, 6 and their negatives) * 2^X.  Two significant bits: the product is
+// exact in bf16 and in binary32, and the E2M1 value alone is exact in binary16.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace rnl {
+namespace kv4 {
+
+// One side (keys or values) of the cache: codes [pages, Hkv, page, D / 2],
+// scale bytes [pages, Hkv, page, D / block].
+struct Side {
+  uint8_t* codes;
+  uint8_t* scales;
+};
+
+// The cache and the sequences of a call, as the kernels take them.
+struct Args {
+  Side k, v;
+  int n_pages, Hkv, page, page_shift;  // page = tokens a page, a power of two
+  int D, block_shift;                  // log2 of the elements a scale covers
+  const int* table;                    // [n_seqs, max_pages]
+  const int* lens;                     // [n_seqs]
+  const int* cu;                       // [n_seqs + 1] or null: one row a sequence
+  int n_seqs, max_pages;
+  int n_rows;
+};
+
+inline Args make_args(const rnl_kv4_cache& c, const rnl_kv4_seqs& q) {
+  Args a;
+  a.k = {static_cast<uint8_t*>(c.k_codes), static_cast<uint8_t*>(c.k_scales)};
+  a.v = {static_cast<uint8_t*>(c.v_codes), static_cast<uint8_t*>(c.v_scales)};
+  a.n_pages = static_cast<int>(c.n_pages);
+  a.Hkv = static_cast<int>(c.n_kv_heads);
+  a.page = static_cast<int>(c.page_size);
+  a.page_shift = 0;
+  while ((1 << a.page_shift) < a.page) ++a.page_shift;
+  a.D = static_cast<int>(c.head_dim);
+  a.block_shift = c.block == 64 ? 6 : 5;
+  a.table = q.block_table;
+  a.lens = q.seq_lens;
+  a.cu = q.cu_rows;
+  a.n_seqs = static_cast<int>(q.n_seqs);
+  a.max_pages = static_cast<int>(q.max_pages);
+  a.n_rows = static_cast<int>(q.n_rows);
+  return a;
+}
+
+// First row, row count and cached length of sequence b; false (and the error
+// word set) where the device-side data is out of range: the caller leaves
+// that sequence alone.
+struct Seq {
+  int row0, rows, len;
+};
+__device__ __forceinline__ bool load_seq(const Args& a, int b, Seq& s, unsigned int* err, uint32_t site) {
+  s.row0 = a.cu != nullptr ? __ldg(a.cu + b) : b;
+  const int end = a.cu != nullptr ? __ldg(a.cu + b + 1) : b + 1;
+  s.rows = end - s.row0;
+  s.len = __ldg(a.lens + b);
+  const bool ok = s.row0 >= 0 && end >= s.row0 && end <= a.n_rows && s.len >= 0 &&
+                  s.len <= static_cast<int64_t>(a.max_pages) * a.page;
+  if (!ok) {
+    atomicCAS(err, 0u, kErrArg | (site << 8));
+    s.rows = 0;
+    s.len = 0;
+  }
+  return ok;
+}
+
+// The sequence that row t belongs to: the last b with cu[b] <= t, found by
+// the whole warp (32 probes a step).  -1 where no sequence covers the row.
+__device__ __forceinline__ int seq_of_row(const Args& a, int t) {
+  if (a.cu == nullptr) return t < a.n_seqs ? t : -1;
+  int lo = 0, n = a.n_seqs;  // the answer + 1 lies in [lo, lo + n]
+  const int lane = threadIdx.x & 31;
+  while (n > 0) {
+    const int step = (n + 31) / 32;
+    const int i = lo + (lane + 1) * step - 1;  // last index of this lane's part
+    const bool le = i < lo + n ? __ldg(a.cu + i) <= t : false;
+    const int full = __popc(__ballot_sync(0xffffffffu, le));
+    const int left = n - full * step;
+    lo += full * step;
+    n = left < step - 1 ? left : step - 1;
+    if (n < 0) n = 0;
+  }
+  const int b = lo - 1;
+  if (b < 0 || t >= __ldg(a.cu + b + 1)) return -1;
+  return b;
+}
+
+// The cache row (page * Hkv + head) * page + offset of token position pos, or
+// -1 for a page id outside the cache (error word set).
+__device__ __forceinline__ int64_t token_row(const Args& a, int b, int pos, int head, unsigned int* err,
+                                             uint32_t site) {
+  const int p = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + (pos >> a.page_shift));
+  if (p < 0 || p >= a.n_pages) {
+    atomicCAS(err, 0u, kErrArg | (site << 8));
+    return -1;
+  }
+  return ((static_cast<int64_t>(p) * a.Hkv + head) << a.page_shift) + (pos & (a.page - 1));
+}
+
+// 8 codes -> 4 half2 of consecutive elements (exact).
+__device__ __forceinline__ void e2m1x8_to_half(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+// 8 values -> 8 codes (element 0 in the lowest nibble), round to nearest
+// even, saturating at 6.
+__device__ __forceinline__ uint32_t e2m1x8_code(const float (&f)[8]) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w)
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+  return w;
+}
+
+// 2^(byte - 127) in binary32 (byte 0 is the subnormal 2^-127; byte 255, the
+// E8M0 NaN, gives an infinity, so that what it scales is not finite).
+__device__ __forceinline__ float e8m0_value(uint32_t byte) {
+  return __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
+}
+
+}  // namespace kv4
+}  // namespace rnl
