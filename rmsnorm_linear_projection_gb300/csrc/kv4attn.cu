@@ -79,17 +79,17 @@ __global__ void __launch_bounds__(kSimpleWarps * 32)
   for (int w = 0; w < kSimpleWarps; ++w) mm = fmaxf(mm, sm[w]);
   float f[kSimpleWarps];
   for (int w = 0; w < kSimpleWarps; ++w) {
-    f[w] = sl[w] > 0.f ? exp2f(sm[w] - mm) : 0.f;
+    f[w] = sl[w] != 0.f ? exp2f(sm[w] - mm) : 0.f;
     ll += sl[w] * f[w];
   }
   const int64_t o = (static_cast<int64_t>(t) * Hq + h) * D;
   for (int d = threadIdx.x; d < D; d += kSimpleWarps * 32) {
     float x = 0.f;
     for (int w = 0; w < kSimpleWarps; ++w) x = fmaf(so[w][d], f[w], x);
-    out[o + d] = __float2bfloat16_rn(ll > 0.f ? x / ll : 0.f);
+    out[o + d] = __float2bfloat16_rn(ll != 0.f ? x / ll : 0.f);
   }
   if (lse != nullptr && threadIdx.x == 0)
-    lse[static_cast<int64_t>(t) * Hq + h] = ll > 0.f ? mm * 0.6931471805599453f + logf(ll) : -INFINITY;
+    lse[static_cast<int64_t>(t) * Hq + h] = ll != 0.f ? mm * 0.6931471805599453f + logf(ll) : -INFINITY;
 }
 
 }  // namespace
