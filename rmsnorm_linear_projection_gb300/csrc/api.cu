@@ -257,7 +257,7 @@ rnl_status check_kv4(const rnl_kv4_cache* c, const rnl_kv4_seqs* q) {
   if (!mx_block_ok(c->block)) return RNL_ERR_ARG;
   if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) != 0)
     return RNL_ERR_UNSUPPORTED;
-  if (bad_dim(q->max_pages * c->page_size) || bad_dim(q->n_rows * (c->n_kv_heads * c->head_dim / 64)))
+  if (q->max_pages * c->page_size > (int64_t{1} << 30) || bad_dim(q->n_rows * (c->n_kv_heads * c->head_dim / 64)))
     return RNL_ERR_SHAPE;
   if (!q->cu_rows && q->n_rows != q->n_seqs) return RNL_ERR_SHAPE;
   if (q->n_rows == 0 || q->n_seqs == 0) return RNL_OK;
@@ -535,7 +535,7 @@ size_t rnl_workspace_size(int op, int64_t T, int64_t K, int64_t N, int64_t N2) {
     case RNL_OP_MXFP8: return mx_layout(nullptr, T, K, N).bytes;
     case RNL_OP_KV4_ATTENTION:
       if (!qkv_rope_head_dim_ok(K) || N == 0 || N2 == 0 || N % N2 != 0) return static_cast<size_t>(-1);
-      return round_up(kv4_attn_workspace_bytes(T, K, N, N2));
+      return round_up(kv4_attn_workspace_bytes(K));
     case RNL_OP_QKV_ROPE:
       return bf16_layout(nullptr, T, K, N, RNL_OUT_BF16).bytes + round_up(static_cast<size_t>(T) * N * 2);
   }

@@ -208,7 +208,7 @@ struct Kv4AttnArgs {
   void* ws = nullptr;
   size_t ws_bytes = 0;
 };
-size_t kv4_attn_workspace_bytes(int64_t T, int64_t D, int64_t Hq, int64_t Hkv);
+size_t kv4_attn_workspace_bytes(int64_t D);
 rnl_status launch_kv4_attention(const Kv4AttnArgs& a, const rnl_kv4_cache& c, const rnl_kv4_seqs& q,
                                 cudaStream_t s);
 

@@ -2,7 +2,41 @@
 //
 //   out[t, h] = sum_j p_j v[j] / sum_j p_j,   p_j = exp(scale q[t, h] . k[j] - max)
 //
-// over the tokens j of the row's sequence that the mask leaves it.
+// over the tokens j of the row's sequence that the mask leaves it, for calls
+// of few rows a sequence (single tokens, drafts): the cache is read once and
+// its bytes at HBM rate are the floor, so what counts is how few instructions
+// a byte of codes costs.
+//
+// Rows and items.  The G = Hq / Hkv query heads of one key head and the rows of
+// one sequence form one list of rows (row r: token r / G, head r % G); an item
+// is (sequence, key head, 8 NT of these rows).  Every item's tokens are cut
+// into tiles of TT; all items' tiles, one after the other, are dealt to the
+// CTAs in equal contiguous ranges, whatever the lengths are, so that no SM
+// waits for a long sequence.  An item that lies in one range is written by its
+// CTA; one that is cut leaves partial sums (FP32, with their maxima) in the
+// workspace, and a second, dependent kernel joins them in CTA order.
+//
+// A warp owns a tile at a time: four bulk copies a page (codes and scales of
+// keys and values) bring it into the warp's two-stage ring in shared memory.
+//
+// The products run on mma.sync m16n8k16 with binary16 operands, transposed, so
+// that the query rows are the narrow side (8) and tokens and dims the wide one:
+//   S^T = K Q^T   A = 16 tokens of keys, B = 8 query rows
+//   O^T = V^T P^T A = 16 dims of values over 16 tokens, B = the weights
+// A's registers come straight from the codes: E2M1 pairs convert to half2 in
+// one instruction, one half2 multiplication applies the block's scale, and the
+// order of dims (in S) and of tokens (in O) is free, so every lane reads whole
+// 4- to 16-byte runs of codes.  tcgen05 would need both operands written to
+// shared memory as binary16 first, 8 times the bytes the codes have.
+//
+// Scales.  2^X of a block does not fit binary16's range, 2^(X - R) does, where
+// R is the largest X of the tile (keys) or of the tiles so far (values): an
+// operand is E2M1 * 2^(X - R + 13), exact unless it lies 2^37 below the
+// largest, and 2^(R - 13) goes into the FP32 factors of the scores and of the
+// sums.  Query rows are scaled by a power of two of their own, weights by 2^15
+// (p <= 1, so that weights down to 2^-29 keep all 11 bits).
+#include <algorithm>
+
 #include "kv4.cuh"
 
 namespace rnl {
@@ -12,108 +46,726 @@ using namespace kv4;
 
 __device__ unsigned int g_err_kv4attn;
 
-constexpr int kSimpleWarps = 4;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kCodeBytes = 2048;                           // codes of a tile, keys or values
+constexpr int kScaleBytes = 128;                           // scales of a tile, room for blocks of 32
+constexpr int kSideBytes = kCodeBytes + kScaleBytes;
+constexpr int kStageBytes = 2 * kSideBytes;
+constexpr int kStages = 2;
+constexpr int kMaxCtas = 640;                              // partial-sum slots in the workspace
+constexpr float kLn2 = 0.6931471805599453f;
 
-// One CTA per (row, query head); its warps take every fourth token, the
-// running maximum, sum and weighted values in binary32 registers.
-template <int D>
-__global__ void __launch_bounds__(kSimpleWarps * 32)
-    kv4_attn_simple_kernel(const __nv_bfloat16* __restrict__ q, int64_t q_stride, int Hq, float scale_log2,
-                           bool causal, int window, const Args a, __nv_bfloat16* __restrict__ out,
-                           float* __restrict__ lse) {
-  constexpr int R = D / 32;  // dims per lane
-  const int t = blockIdx.x / Hq, h = blockIdx.x - t * Hq;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = seq_of_row(a, t);
-  if (b < 0) return;
+struct AttnParams {
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  __nv_bfloat16* out;
+  float* lse;
+  float* part;   // partial sums: 2 slots a CTA
+  int4* rec;     // [CTAs]: the cut item a CTA begins (item, sequence, last CTA), .x = -1: none
+  float scale_log2;
+  int Hq, G;
+  int causal, window;
+};
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr int TT = 4096 / D;      // tokens a tile (64, 32, 16)
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kPitch = D + 4;     // floats between rows of the merge buffer
+  static constexpr int kSlot = kRows * (D + 2);  // floats of a partial: sums, maxima, weights
+  static constexpr size_t kSmem = kWarps * kStages * kStageBytes + kWarps * kRows * kPitch * 4;
+  static constexpr int kJoin = D * NT > 256 ? 2 : 4;  // thread groups that join pieces (static shared memory)
+  // registers: 4 CTAs an SM where the sums and queries leave 128 a thread
+  static constexpr int kMinCtas = D * NT <= 128 ? 4 : D * NT <= 256 ? 3 : 2;
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 2^(byte - ref + 13) for byte <= ref, 0 far below (as a binary32).
+__device__ __forceinline__ float scale_of(int byte, int ref) {
+  return __uint_as_float(static_cast<uint32_t>(max(byte - ref + 140, 0)) << 23);
+}
+
+// 2^e; the clamp is reached only where what it scales vanishes anyway.
+__device__ __forceinline__ float pow2i(int e) {
+  return __uint_as_float(static_cast<uint32_t>(min(max(e, -126), 127) + 127) << 23);
+}
+// 2^e for |e| up to 250, subnormal or infinite outside binary32's range.
+__device__ __forceinline__ float pow2w(int e) { return pow2i(e / 2) * pow2i(e - e / 2); }
+
+// What of a sequence the call's rows read, in tiles.
+struct Span {
   Seq s;
-  if (!load_seq(a, b, s, &g_err_kv4attn, 45)) return;
-  if (t < s.row0) return;
-  const int kvh = h / (Hq / a.Hkv);
-  int lo = 0, hi = s.len;
-  if (causal) {
-    const int pos = s.len - s.rows + (t - s.row0);
-    hi = pos + 1;
-    if (window > 0 && pos + 1 > window) lo = pos + 1 - window;
+  int items;      // Hkv * row groups
+  int groups;     // row groups of kRows
+  int lo, hi;     // tokens that any row reads
+  int t0, tiles;  // first tile, number of tiles (at least 1: an item without tokens still writes zeros)
+};
+template <int D, int NT>
+__device__ __forceinline__ bool load_span(const Args& a, const AttnParams& p, int b, Span& w) {
+  constexpr int TT = Cfg<D, NT>::TT;
+  if (!load_seq(a, b, w.s, &g_err_kv4attn, 45) || w.s.rows == 0) return false;
+  w.groups = (w.s.rows * p.G + Cfg<D, NT>::kRows - 1) / Cfg<D, NT>::kRows;
+  w.items = w.groups * a.Hkv;
+  w.lo = 0;
+  w.hi = w.s.len;
+  if (p.causal && p.window > 0) w.lo = max(0, w.s.len - w.s.rows + 1 - p.window);
+  w.t0 = w.lo / TT;
+  w.tiles = max(1, (w.hi + TT - 1) / TT - w.t0);
+  return true;
+}
+
+// A place in the sequence of all tiles.
+struct Cursor {
+  int b, item, tile;
+  Span w;
+};
+template <int D, int NT>
+__device__ __forceinline__ void skip(const Args& a, const AttnParams& p, Cursor& c, int n) {
+  c.tile += n;
+  while (c.tile >= c.w.tiles) {
+    c.tile -= c.w.tiles;
+    if (++c.item == c.w.items) {
+      c.item = 0;
+      do {
+        if (++c.b >= a.n_seqs) {
+          c.w.tiles = 0x7fffffff;  // behind the last tile: never reached by a range
+          return;
+        }
+      } while (!load_span<D, NT>(a, p, c.b, c.w));
+    }
   }
-  float qf[R], acc[R];
+}
+
+// Eight dims of row r of key head kvh: sums v over weights ll with maximum mm.
+template <int D>
+__device__ __forceinline__ void store_row(const AttnParams& p, const Seq& s, int kvh, int r, int d,
+                                          const float (&v)[8], float mm, float ll) {
+  const int tok = r / p.G;
+  const int64_t row = static_cast<int64_t>(s.row0 + tok) * p.Hq + kvh * p.G + (r - tok * p.G);
+  const float inv = ll != 0.f ? 1.f / ll : 0.f;
+  uint32_t w[4];
 #pragma unroll
-  for (int e = 0; e < R; ++e) {
-    qf[e] = __bfloat162float(q[t * q_stride + static_cast<int64_t>(h) * D + lane * R + e]) * scale_log2;
-    acc[e] = 0.f;
+  for (int y = 0; y < 4; ++y) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * y] * inv, v[2 * y + 1] * inv);
+    w[y] = *reinterpret_cast<const uint32_t*>(&b);
   }
-  float m = -INFINITY, l = 0.f;
-  const int sd = D >> a.block_shift, sj = (lane * R) >> a.block_shift;
-  for (int j = lo + warp; j < hi; j += kSimpleWarps) {
-    const int64_t row = token_row(a, b, j, kvh, &g_err_kv4attn, 46);
-    if (row < 0) continue;
-    auto value = [&](const Side& side, int e, float sc) {
-      const int d = lane * R + e;
-      const uint32_t byte = side.codes[(row * D + d) / 2];
-      const uint32_t c = (d & 1) ? byte >> 4 : byte & 15;
-      const float mag = (c & 7) < 2 ? 0.5f * (c & 7) : (1.f + 0.5f * (c & 1)) * static_cast<float>(1 << (((c & 7) >> 1) - 1));
-      return ((c & 8) ? -mag : mag) * sc;
-    };
-    const float ks = e8m0_value(a.k.scales[row * sd + sj]), vs = e8m0_value(a.v.scales[row * sd + sj]);
-    float dot = 0.f;
-#pragma unroll
-    for (int e = 0; e < R; ++e) dot = fmaf(qf[e], value(a.k, e, ks), dot);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    const float mn = fmaxf(m, dot);
-    const float f = exp2f(m - mn), p = exp2f(dot - mn);
-    l = l * f + p;
-#pragma unroll
-    for (int e = 0; e < R; ++e) acc[e] = fmaf(p, value(a.v, e, vs), acc[e] * f);
-    m = mn;
+  *reinterpret_cast<uint4*>(p.out + row * D + d) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (d == 0 && p.lse != nullptr) p.lse[row] = ll != 0.f ? mm * kLn2 + logf(ll) : -INFINITY;
+}
+
+__device__ __forceinline__ int64_t range_start(int64_t units, int c, int n) { return units * c / n; }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
+    kv4_attn_kernel(const Args a, const AttnParams p) {
+  using C = Cfg<D, NT>;
+  constexpr int TT = C::TT, kRows = C::kRows, kPitch = C::kPitch;
+  constexpr int KS = D / 16;        // k-steps of the scores, and groups of 16 dims of the sums
+  constexpr int MS = TT / 16;       // groups of 16 tokens a tile
+  constexpr int kKB = D / 8;        // code bytes a lane takes of a key (8, 16, 32)
+  constexpr int kVB = D / 16;       // of a value (4, 8, 16)
+  constexpr int kKW = kKB / 4, kVW = kVB / 4;
+  constexpr int kScalesPerLane = D == 256 ? 2 : 1;  // 32-element parts of a lane's key dims
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t full[kWarps * kStages];
+  __shared__ float sh_ml[2][kWarps][2][kRows];
+  __shared__ long long sh_sum[kWarps];
+  __shared__ int sh_b, sh_abort;
+  __shared__ long long sh_off;
+  float* merge = reinterpret_cast<float*>(smem + kWarps * kStages * kStageBytes);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = lane >> 2, j = lane & 3;
+
+  if (tid == 0) {
+    for (int i = 0; i < kWarps * kStages; ++i) mbar_init(smem_u32(&full[i]), 1);
+    sh_abort = 0;
+    sh_b = -1;
+    fence_mbar_init();
   }
-  __shared__ float sm[kSimpleWarps], sl[kSimpleWarps], so[kSimpleWarps][D];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
+  // ---- this CTA's range of tiles
+  auto units_of = [&](int b) -> long long {
+    Span w;
+    if (b >= a.n_seqs || !load_span<D, NT>(a, p, b, w)) return 0;
+    return static_cast<long long>(w.tiles) * w.items;
+  };
+  long long sum = 0;
+  for (int b = tid; b < a.n_seqs; b += kThreads) sum += units_of(b);
 #pragma unroll
-  for (int e = 0; e < R; ++e) so[warp][lane * R + e] = acc[e];
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) sh_sum[warp] = sum;
   __syncthreads();
-  float mm = -INFINITY, ll = 0.f;
-  for (int w = 0; w < kSimpleWarps; ++w) mm = fmaxf(mm, sm[w]);
-  float f[kSimpleWarps];
-  for (int w = 0; w < kSimpleWarps; ++w) {
-    f[w] = sl[w] != 0.f ? exp2f(sm[w] - mm) : 0.f;
-    ll += sl[w] * f[w];
+  long long units = 0;
+  for (int i = 0; i < kWarps; ++i) units += sh_sum[i];
+  // at least a tile a warp for every CTA that works
+  const int cta = blockIdx.x;
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (units + kWarps - 1) / kWarps));
+  grid_launch_dependents();
+  if (tid == 0) p.rec[cta] = make_int4(-1, 0, 0, 0);
+  if (cta >= ctas) return;  // the whole CTA
+  const int64_t u0 = range_start(units, cta, ctas), u1 = range_start(units, cta + 1, ctas);
+  long long before = 0;
+  for (int base = 0; base < a.n_seqs; base += kThreads) {
+    const long long u = units_of(base + tid);
+    long long inc = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    __syncthreads();
+    if (lane == 31) sh_sum[warp] = inc;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) inc += sh_sum[i];
+    long long all = 0;
+    for (int i = 0; i < kWarps; ++i) all += sh_sum[i];
+    inc += before;
+    if (u0 >= inc - u && u0 < inc) {
+      sh_b = base + tid;
+      sh_off = u0 - (inc - u);
+    }
+    __syncthreads();
+    if (sh_b >= 0) break;
+    before += all;
   }
-  const int64_t o = (static_cast<int64_t>(t) * Hq + h) * D;
-  for (int d = threadIdx.x; d < D; d += kSimpleWarps * 32) {
-    float x = 0.f;
-    for (int w = 0; w < kSimpleWarps; ++w) x = fmaf(so[w][d], f[w], x);
-    out[o + d] = __float2bfloat16_rn(ll != 0.f ? x / ll : 0.f);
+  if (sh_b < 0) return;  // lengths changed under the call
+  Cursor cur;  // the CTA's place
+  cur.b = sh_b;
+  load_span<D, NT>(a, p, cur.b, cur.w);
+  cur.item = static_cast<int>(sh_off / cur.w.tiles);
+  cur.tile = static_cast<int>(sh_off % cur.w.tiles);
+  const int n_units = static_cast<int>(u1 - u0);
+
+  // ---- the warp's ring
+  const uint32_t ring = smem_u32(smem) + warp * kStages * kStageBytes;
+  const uint8_t* ring_p = smem + warp * kStages * kStageBytes;
+  Cursor ahead = cur;  // the next tile to fetch
+  skip<D, NT>(a, p, ahead, warp);
+  int fetched = warp;  // its index in the range
+  uint32_t phase = 0;  // one bit a stage
+  const int sb_shift = a.block_shift;           // D >> sb_shift scale bytes a token
+  const int scale_bytes = TT * D >> sb_shift;   // of a tile
+  auto fetch = [&](int stage) {
+    if (fetched >= n_units) return;
+    // copies: pages of the tile x (k codes, k scales, v codes, v scales), one a lane
+    const int chunk_tokens = min(TT, a.page);
+    const int chunk = lane >> 2, what = lane & 3;
+    const int tok = (ahead.w.t0 + ahead.tile) * TT + chunk * chunk_tokens;
+    const bool codes = (what & 1) == 0;
+    const uint32_t bytes = static_cast<uint32_t>(codes ? chunk_tokens * (D / 2) : chunk_tokens * D >> sb_shift);
+    bool want = chunk * chunk_tokens < TT && tok < ahead.w.hi;
+    int64_t row = 0;
+    if (want) {
+      row = token_row(a, ahead.b, tok, ahead.item / ahead.w.groups, &g_err_kv4attn, 46);
+      want = row >= 0;
+    }
+    const uint32_t total = __reduce_add_sync(0xffffffffu, want ? bytes : 0u);
+    const uint32_t bar = smem_u32(&full[warp * kStages + stage]);
+    if (lane == 0) mbar_arrive_expect_tx(bar, total);
+    __syncwarp();
+    if (want) {
+      const Side& side = what < 2 ? a.k : a.v;
+      const uint8_t* src = codes ? side.codes + row * (D / 2) : side.scales + row * (D >> sb_shift);
+      const uint32_t dst = ring + stage * kStageBytes + (what < 2 ? 0 : kSideBytes) + (codes ? 0 : kCodeBytes) +
+                           chunk * bytes;
+      bulk_copy_g2s(dst, src, bytes, bar);
+    }
+    skip<D, NT>(a, p, ahead, kWarps);
+    fetched += kWarps;
+  };
+  __syncthreads();  // barriers initialised
+  for (int s = 0; s < kStages; ++s) fetch(s);
+
+  int done = 0;      // tiles of the range before the current segment
+  int stage = 0;
+  int seg = 0;
+  while (done < n_units) {
+    // ---- a segment: the range's tiles of one item
+    const int seg_tiles = min(cur.w.tiles - cur.tile, n_units - done);
+    const int kvh = cur.item / cur.w.groups, group = cur.item - kvh * cur.w.groups;
+    const int all_rows = cur.w.s.rows * p.G;
+    const int r0 = group * kRows;
+    // queries: lane (n, j) holds dims [j D/4, (j + 1) D/4) of row n of each tile of 8
+    uint32_t qf[NT][KS][2];
+    float f_row[NT][2];  // score factors of rows 2j and 2j + 1
+    int pos[NT][2];      // last token they read
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int r = min(r0 + t * 8 + n, all_rows - 1);
+      const int tok = r / p.G;
+      const __nv_bfloat16* src = p.q + (cur.w.s.row0 + tok) * p.q_stride +
+                                 static_cast<int64_t>(kvh * p.G + (r - tok * p.G)) * D + j * (D / 4);
+      uint32_t w[D / 8];
+      uint32_t am = 0;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(src) + i);
+        w[4 * i] = x.x;
+        w[4 * i + 1] = x.y;
+        w[4 * i + 2] = x.z;
+        w[4 * i + 3] = x.w;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) am = max(am, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+      const int eb = static_cast<int>(am >> 23);
+      // exponent field 127 + 14 for the largest: times 2^(141 - eb), in two steps
+      const int e = 141 - max(eb, 1);
+      const float s1 = pow2i(e / 2), s2 = pow2i(e - e / 2);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        qf[t][i >> 1][i & 1] = pack_half2(__uint_as_float(w[i] << 16) * s1 * s2,
+                                          __uint_as_float(w[i] & 0xFFFF0000u) * s1 * s2);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int er = __shfl_sync(0xffffffffu, e, (2 * j + h) * 4);
+        f_row[t][h] = p.scale_log2 * pow2w(-er);
+        const int rr = min(r0 + t * 8 + 2 * j + h, all_rows - 1);
+        pos[t][h] = p.causal ? cur.w.s.len - cur.w.s.rows + rr / p.G : cur.w.s.len - 1;
+      }
+    }
+    const int r_last = min(r0 + kRows, all_rows) - 1;
+    const int pos_min = p.causal ? cur.w.s.len - cur.w.s.rows + r0 / p.G : cur.w.s.len - 1;
+    const int pos_max = p.causal ? cur.w.s.len - cur.w.s.rows + r_last / p.G : cur.w.s.len - 1;
+    const int win = p.window > 0 ? p.window : 0x40000000;
+
+    float o[NT][KS][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int i = 0; i < KS; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
+    }
+    int ref_v = 0;
+
+    for (int i = (warp - done % kWarps + kWarps) % kWarps; i < seg_tiles; i += kWarps) {
+      mbar_wait(smem_u32(&full[warp * kStages + stage]), (phase >> stage) & 1, &sh_abort, &g_err_kv4attn, 47);
+      phase ^= 1u << stage;
+      const uint8_t* ks = ring_p + stage * kStageBytes;
+      const uint8_t* vs = ks + kSideBytes;
+      const int tok0 = (cur.w.t0 + cur.tile + i) * TT;
+      // a tile that no row of this group reads (causal, earlier rows): nothing
+      const bool any = tok0 <= pos_max && tok0 + TT > pos_min - win + 1 && cur.w.hi > 0;
+      if (any) {
+        // largest scales; scale bytes of tokens that no row reads become 0, so
+        // that whatever stands there gives zero operands
+        uint32_t* ksc = reinterpret_cast<uint32_t*>(const_cast<uint8_t*>(ks + kCodeBytes)) + lane;
+        uint32_t* vsc = reinterpret_cast<uint32_t*>(const_cast<uint8_t*>(vs + kCodeBytes)) + lane;
+        const bool has = lane * 4 < scale_bytes;
+        uint32_t kw = has ? *ksc : 0u, vw = has ? *vsc : 0u;
+        if (tok0 < cur.w.lo || tok0 + TT > cur.w.hi) {
+          uint32_t keep = 0;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int tok = tok0 + ((lane * 4 + x) << sb_shift) / D;
+            if (tok >= cur.w.lo && tok < cur.w.hi) keep |= 0xFFu << (8 * x);
+          }
+          kw &= keep;
+          vw &= keep;
+          if (has) {
+            *ksc = kw;
+            *vsc = vw;
+          }
+          fence_proxy_async_shared();  // the ring's next copy comes after these writes
+          __syncwarp();
+        }
+        auto top = [](uint32_t w) {
+          w = __vmaxu4(w, w >> 16);
+          return max(w & 0xFFu, (w >> 8) & 0xFFu);
+        };
+        const int ref_k = static_cast<int>(__reduce_max_sync(0xffffffffu, top(kw)));
+        const int tile_v = static_cast<int>(__reduce_max_sync(0xffffffffu, top(vw)));
+
+        // ---- scores, transposed: 16 tokens x 8 rows
+        float s[NT][MS][4];
+#pragma unroll
+        for (int ms = 0; ms < MS; ++ms) {
+          // tokens of the group: matrix row x is token x/2 (x even) or 4 + (x/2 ^ 1)
+          // (x odd), plus 8 for x >= 8: conflict-free reads of keys and values
+          const int tk = ms * 16 + ((n & 1) ? 4 + ((n >> 1) ^ 1) : (n >> 1));
+          uint32_t w0[kKW], w1[kKW];
+          const uint8_t* c0 = ks + tk * (D / 2) + j * kKB;
+          const uint8_t* c1 = c0 + 8 * (D / 2);
+          if constexpr (kKW == 2) {
+            const uint2 x = *reinterpret_cast<const uint2*>(c0), y = *reinterpret_cast<const uint2*>(c1);
+            w0[0] = x.x, w0[1] = x.y, w1[0] = y.x, w1[1] = y.y;
+          } else {
+#pragma unroll
+            for (int x = 0; x < kKW / 4; ++x) {
+              const uint4 u = reinterpret_cast<const uint4*>(c0)[x], y = reinterpret_cast<const uint4*>(c1)[x];
+              w0[4 * x] = u.x, w0[4 * x + 1] = u.y, w0[4 * x + 2] = u.z, w0[4 * x + 3] = u.w;
+              w1[4 * x] = y.x, w1[4 * x + 1] = y.y, w1[4 * x + 2] = y.z, w1[4 * x + 3] = y.w;
+            }
+          }
+          uint32_t m0[kScalesPerLane], m1[kScalesPerLane];
+#pragma unroll
+          for (int x = 0; x < kScalesPerLane; ++x) {
+            const int blk = (j * (D / 4) + x * 32) >> sb_shift;
+            const uint8_t* sc = ks + kCodeBytes + ((tk * D) >> sb_shift) + blk;
+            const float a0 = scale_of(sc[0], ref_k), a1 = scale_of(sc[(8 * D) >> sb_shift], ref_k);
+            m0[x] = pack_half2(a0, a0);
+            m1[x] = pack_half2(a1, a1);
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t) s[t][ms][0] = s[t][ms][1] = s[t][ms][2] = s[t][ms][3] = 0.f;
+#pragma unroll
+          for (int w = 0; w < kKW; ++w) {  // a word: 8 dims, two k-steps
+            uint32_t h0[4], h1[4];
+            e2m1x8_to_half(w0[w], h0);
+            e2m1x8_to_half(w1[w], h1);
+            const int x = w / (kKW / kScalesPerLane);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t af[4] = {hmul2(h0[2 * k], m0[x]), hmul2(h1[2 * k], m1[x]), hmul2(h0[2 * k + 1], m0[x]),
+                                      hmul2(h1[2 * k + 1], m1[x])};
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma_f16(s[t][ms], af, qf[t][2 * w + k][0], qf[t][2 * w + k][1]);
+            }
+          }
+        }
+        // ---- softmax over the tile
+        const float f_tile = ref_k == 255 ? NAN : pow2w(ref_k - 140);
+        const bool whole = tok0 + TT - 1 <= pos_min && tok0 > pos_max - win;
+        const int new_v = max(ref_v, tile_v);
+        const float fv = ref_v == new_v ? 1.f : pow2i(ref_v - new_v);
+        ref_v = new_v;
+        uint32_t pb[NT][MS][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float mx[2] = {-INFINITY, -INFINITY};
+          const float f[2] = {f_row[t][0] * f_tile, f_row[t][1] * f_tile};
+#pragma unroll
+          for (int ms = 0; ms < MS; ++ms)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              float v = s[t][ms][x] * f[x & 1];
+              if (!whole) {
+                const int tok = tok0 + ms * 16 + ((n & 1) ? 4 + ((n >> 1) ^ 1) : (n >> 1)) + (x >> 1) * 8;
+                if (tok > pos[t][x & 1] || tok <= pos[t][x & 1] - win) v = -INFINITY;
+              }
+              s[t][ms][x] = v;
+              mx[x & 1] = fmaxf(mx[x & 1], v);
+            }
+          float base[2], al[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 4));
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 8));
+            mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 16));
+            const float mn = fmaxf(m[t][h], mx[h]);
+            const float mu = mn == -INFINITY ? 0.f : mn;
+            al[h] = ex2(m[t][h] - mu);
+            base[h] = 15.f - mu;
+            m[t][h] = mn;
+            l[t][h] *= al[h];
+            al[h] *= fv;
+          }
+          if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
+#pragma unroll
+            for (int i2 = 0; i2 < KS; ++i2) {
+              o[t][i2][0] *= al[0];
+              o[t][i2][1] *= al[1];
+              o[t][i2][2] *= al[0];
+              o[t][i2][3] *= al[1];
+            }
+          }
+#pragma unroll
+          for (int ms = 0; ms < MS; ++ms) {
+            float e[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              e[x] = ex2(s[t][ms][x] + base[x & 1]);
+              l[t][x & 1] += e[x];
+            }
+            pb[t][ms][0] = movmatrix_trans(pack_half2(e[0], e[1]));
+            pb[t][ms][1] = movmatrix_trans(pack_half2(e[2], e[3]));
+          }
+        }
+        // ---- weighted values, transposed: 16 dims x 8 rows over 16 tokens
+#pragma unroll
+        for (int ms = 0; ms < MS; ++ms) {
+          uint32_t w[4][kVW];
+          float sc[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {  // tokens of k = 2j, 2j + 1, 2j + 8, 2j + 9
+            const int tk = ms * 16 + ((x & 1) ? 4 + (j ^ 1) : j) + (x >> 1) * 8;
+            const uint8_t* c = vs + tk * (D / 2) + n * kVB;
+            if constexpr (kVW == 1) {
+              w[x][0] = *reinterpret_cast<const uint32_t*>(c);
+            } else if constexpr (kVW == 2) {
+              const uint2 u = *reinterpret_cast<const uint2*>(c);
+              w[x][0] = u.x, w[x][1] = u.y;
+            } else {
+              const uint4 u = *reinterpret_cast<const uint4*>(c);
+              w[x][0] = u.x, w[x][1] = u.y, w[x][2] = u.z, w[x][3] = u.w;
+            }
+            sc[x] = scale_of(vs[kCodeBytes + ((tk * D) >> sb_shift) + ((n * (D / 8)) >> sb_shift)], ref_v);
+          }
+          const uint32_t m01 = pack_half2(sc[0], sc[1]), m23 = pack_half2(sc[2], sc[3]);
+#pragma unroll
+          for (int x = 0; x < kVW; ++x) {
+            uint32_t h[4][4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) e2m1x8_to_half(w[y][x], h[y]);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t af[4] = {hmul2(__byte_perm(h[0][y], h[1][y], 0x5410), m01),
+                                      hmul2(__byte_perm(h[0][y], h[1][y], 0x7632), m01),
+                                      hmul2(__byte_perm(h[2][y], h[3][y], 0x5410), m23),
+                                      hmul2(__byte_perm(h[2][y], h[3][y], 0x7632), m23)};
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma_f16(o[t][4 * x + y], af, pb[t][ms][0], pb[t][ms][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      fetch(stage);
+      stage ^= 1;
+    }
+
+    // ---- join the warps
+    float(*ml)[2][kRows] = sh_ml[seg & 1];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x = l[t][h];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        if (n == 0) {
+          ml[warp][0][t * 8 + 2 * j + h] = m[t][h];
+          ml[warp][1][t * 8 + 2 * j + h] = x;
+        }
+        l[t][h] = x;
+      }
+    __syncthreads();
+    const float f_v = ref_v == 255 ? NAN : 1.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = t * 8 + 2 * j + h;
+        float mm = ml[0][0][r];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, ml[w][0][r]);
+        // sums stand for value * 2^(ref_v - 127 - 13) * p 2^15
+        const float f = l[t][h] == 0.f ? 0.f : ex2(m[t][h] - mm) * f_v;
+        const float fa = pow2i((ref_v - 155) / 2), fb = pow2i(ref_v - 155 - (ref_v - 155) / 2);
+        float* dst = merge + (warp * kRows + r) * kPitch + n * (D / 8);
+#pragma unroll
+        for (int i = 0; i < KS; i += 2)
+          *reinterpret_cast<float4*>(dst + 2 * i) =
+              make_float4(o[t][i][h] * f * fa * fb, o[t][i][2 + h] * f * fa * fb, o[t][i + 1][h] * f * fa * fb,
+                          o[t][i + 1][2 + h] * f * fa * fb);
+      }
+    __syncthreads();
+    const bool complete = seg_tiles == cur.w.tiles;
+    float* slot = p.part + static_cast<int64_t>(2 * cta + (seg > 0)) * C::kSlot;
+    constexpr int kTpr = D / 8;  // threads a row, 8 dims each
+    for (int x = tid; x < kRows * kTpr; x += kThreads) {
+      const int r = x / kTpr, d = (x - r * kTpr) * 8;
+      if (r0 + r >= all_rows) continue;
+      float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[w][0][r]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        if (ml[w][1][r] != 0.f) ll += ml[w][1][r] * ex2(ml[w][0][r] - mm);
+      ll *= 1.f / 32768.f;
+      float v[8] = {};
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 y = *reinterpret_cast<const float4*>(merge + (w * kRows + r) * kPitch + d);
+        const float4 z = *reinterpret_cast<const float4*>(merge + (w * kRows + r) * kPitch + d + 4);
+        v[0] += y.x, v[1] += y.y, v[2] += y.z, v[3] += y.w;
+        v[4] += z.x, v[5] += z.y, v[6] += z.z, v[7] += z.w;
+      }
+      if (complete) {
+        store_row<D>(p, cur.w.s, kvh, r0 + r, d, v, mm, ll);
+      } else {
+        float4* dst = reinterpret_cast<float4*>(slot + r * D + d);
+        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+        if (d == 0) {
+          slot[kRows * D + r] = mm;
+          slot[kRows * D + kRows + r] = ll;
+        }
+      }
+    }
+    // the item begins here and goes on in later CTAs: this CTA's record (unit x
+    // is in the last range c with units c / ctas < x + 1)
+    if (tid == 0 && cur.tile == 0 && !complete) {
+      const int64_t end = u0 + done + cur.w.tiles;  // the item's last tile + 1
+      const int last = static_cast<int>((end * ctas - 1) / units);
+      p.rec[cta] = make_int4(cur.item, cur.b, last, seg > 0);
+    }
+    done += seg_tiles;
+    ++seg;
+    if (done < n_units) skip<D, NT>(a, p, cur, seg_tiles);
   }
-  if (lse != nullptr && threadIdx.x == 0)
-    lse[static_cast<int64_t>(t) * Hq + h] = ll != 0.f ? mm * 0.6931471805599453f + logf(ll) : -INFINITY;
+}
+
+// Joins the partial sums of the items that were cut: CTA c the one that CTA c
+// of the first kernel began.  kJoin groups of threads take every kJoin-th piece,
+// each with the pieces' maxima first and then their sums; the groups are added
+// in order.
+template <int D, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::kJoin * 128)
+    kv4_attn_join_kernel(const Args a, const AttnParams p) {
+  using C = Cfg<D, NT>;
+  constexpr int kRows = C::kRows, kTpr = D / 8, kJoin = C::kJoin;
+  __shared__ float sh_m[kRows], sh_l[kJoin][kRows];
+  __shared__ __align__(16) float sh_v[kJoin][kRows][D];
+  grid_dependency_wait();
+  const int first = blockIdx.x;
+  const int4 rec = p.rec[first];
+  if (rec.x < 0) return;
+  Span w;
+  load_span<D, NT>(a, p, rec.y, w);
+  const int kvh = rec.x / w.groups, group = rec.x - kvh * w.groups;
+  const int all_rows = w.s.rows * p.G, r0 = group * kRows;
+  const int tid = threadIdx.x, g = tid >> 7;
+  const float* base = p.part + static_cast<int64_t>(2) * first * C::kSlot;
+  auto slot = [&](int c) { return base + static_cast<int64_t>(2 * (c - first) + (c == first ? rec.w : 0)) * C::kSlot; };
+  // maxima: a warp a row
+  for (int r = tid >> 5; r < kRows; r += kJoin * 4) {
+    float mm = -INFINITY;
+    for (int c = first + (tid & 31); c <= rec.z; c += 32) mm = fmaxf(mm, slot(c)[kRows * D + r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    if ((tid & 31) == 0) sh_m[r] = mm;
+  }
+  __syncthreads();
+  for (int x = tid & 127; x < kRows * kTpr; x += 128) {
+    const int r = x / kTpr, d = (x - r * kTpr) * 8;
+    const float mm = sh_m[r];
+    float ll = 0.f, v[8] = {};
+#pragma unroll 4
+    for (int c = first + g; c <= rec.z; c += kJoin) {
+      const float* s = slot(c);
+      const float pm = s[kRows * D + r], pl = s[kRows * D + kRows + r];
+      const float4 y = *reinterpret_cast<const float4*>(s + r * D + d);
+      const float4 z = *reinterpret_cast<const float4*>(s + r * D + d + 4);
+      const float f = pl != 0.f ? ex2(pm - mm) : 0.f;
+      ll += pl * f;
+      v[0] += y.x * f, v[1] += y.y * f, v[2] += y.z * f, v[3] += y.w * f;
+      v[4] += z.x * f, v[5] += z.y * f, v[6] += z.z * f, v[7] += z.w * f;
+    }
+    *reinterpret_cast<float4*>(&sh_v[g][r][d]) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(&sh_v[g][r][d + 4]) = make_float4(v[4], v[5], v[6], v[7]);
+    if (d == 0) sh_l[g][r] = ll;
+  }
+  __syncthreads();
+  for (int x = tid; x < kRows * kTpr; x += kJoin * 128) {
+    const int r = x / kTpr, d = (x - r * kTpr) * 8;
+    if (r0 + r >= all_rows) continue;
+    float ll = 0.f, v[8] = {};
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i) {
+      ll += sh_l[i][r];
+#pragma unroll
+      for (int y = 0; y < 8; ++y) v[y] += sh_v[i][r][d + y];
+    }
+    store_row<D>(p, w.s, kvh, r0 + r, d, v, sh_m[r], ll);
+  }
+}
+
+template <int D, int NT>
+rnl_status launch_split(const AttnParams& p, const Args& a, const DeviceInfo& dev, cudaStream_t s) {
+  using C = Cfg<D, NT>;
+  const rnl_status st = ensure_smem_attr(reinterpret_cast<const void*>(kv4_attn_kernel<D, NT>), dev.device, C::kSmem);
+  if (st != RNL_OK) return st;
+  const int ctas = std::min(dev.sm_count * C::kMinCtas, kMaxCtas);
+  trace_before(s);
+  kv4_attn_kernel<D, NT><<<ctas, kThreads, C::kSmem, s>>>(a, p);
+  cudaError_t e = cudaGetLastError();
+  trace_after(s, "kv4_attn");
+  if (e != cudaSuccess) return RNL_ERR_LAUNCH;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(C::kJoin * 128);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  trace_before(s);
+  e = cudaLaunchKernelEx(&cfg, kv4_attn_join_kernel<D, NT>, a, p);
+  trace_after(s, "kv4_attn_join");
+  return e == cudaSuccess ? RNL_OK : RNL_ERR_LAUNCH;
 }
 
 }  // namespace
 
-size_t kv4_attn_workspace_bytes(int64_t T, int64_t D, int64_t Hq, int64_t Hkv) { return 0; }
+size_t kv4_attn_workspace_bytes(int64_t D) {
+  const size_t slot = static_cast<size_t>(16) * (static_cast<size_t>(D) + 2) * 4;  // NT = 2
+  return kMaxCtas * (sizeof(int4) + 2 * slot);
+}
 
 rnl_status launch_kv4_attention(const Kv4AttnArgs& x, const rnl_kv4_cache& c, const rnl_kv4_seqs& q,
                                 cudaStream_t s) {
-  const unsigned blocks = static_cast<unsigned>(q.n_rows * x.Hq);
-  const float sl = x.scale * 1.4426950408889634f;
+  DeviceInfo dev;
+  const rnl_status st = current_device(&dev);
+  if (st != RNL_OK) return st;
   const Args a = make_args(c, q);
-  const auto* qp = static_cast<const __nv_bfloat16*>(x.q);
-  auto* op = static_cast<__nv_bfloat16*>(x.out);
-  const int hq = static_cast<int>(x.Hq), w = static_cast<int>(x.window);
-  trace_before(s);
-  if (a.D == 64)
-    kv4_attn_simple_kernel<64><<<blocks, kSimpleWarps * 32, 0, s>>>(qp, x.q_stride, hq, sl, x.causal, w, a, op, x.lse);
-  else if (a.D == 128)
-    kv4_attn_simple_kernel<128><<<blocks, kSimpleWarps * 32, 0, s>>>(qp, x.q_stride, hq, sl, x.causal, w, a, op, x.lse);
-  else
-    kv4_attn_simple_kernel<256><<<blocks, kSimpleWarps * 32, 0, s>>>(qp, x.q_stride, hq, sl, x.causal, w, a, op, x.lse);
-  const rnl_status st = cudaGetLastError() == cudaSuccess ? RNL_OK : RNL_ERR_LAUNCH;
-  trace_after(s, "kv4_attn");
-  return st;
+  AttnParams p;
+  p.q = static_cast<const __nv_bfloat16*>(x.q);
+  p.q_stride = x.q_stride;
+  p.out = static_cast<__nv_bfloat16*>(x.out);
+  p.lse = x.lse;
+  p.rec = static_cast<int4*>(x.ws);
+  p.part = reinterpret_cast<float*>(p.rec + kMaxCtas);
+  p.scale_log2 = x.scale * 1.4426950408889634f;
+  p.Hq = static_cast<int>(x.Hq);
+  p.G = p.Hq / a.Hkv;
+  p.causal = x.causal;
+  p.window = static_cast<int>(x.window);
+  // 8 rows an item where the rows that a sequence has on average fit, else 16
+  const int64_t rows = (q.n_rows + q.n_seqs - 1) / q.n_seqs * p.G;
+  const bool wide = rows > 8;
+  switch (a.D) {
+    case 64: return wide ? launch_split<64, 2>(p, a, dev, s) : launch_split<64, 1>(p, a, dev, s);
+    case 128: return wide ? launch_split<128, 2>(p, a, dev, s) : launch_split<128, 1>(p, a, dev, s);
+    default: return wide ? launch_split<256, 2>(p, a, dev, s) : launch_split<256, 1>(p, a, dev, s);
+  }
 }
 
 rnl_status read_clear_error_kv4attn(unsigned int* word) {
