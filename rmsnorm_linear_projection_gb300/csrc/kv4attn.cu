@@ -16,15 +16,16 @@
 // CTA; one that is cut leaves partial sums (FP32, with their maxima) in the
 // workspace, and a second, dependent kernel joins them in CTA order.
 //
-// A warp owns a tile at a time: four bulk copies a page (codes and scales of
-// keys and values) bring it into the warp's two-stage ring in shared memory.
+// A warp owns a tile at a time: bulk copies (codes and scales, a page each)
+// bring its keys and its values into the warp's two buffers; the next tile's
+// keys are requested when these have been read, then its values.
 //
 // The products run on mma.sync m16n8k16 with binary16 operands, transposed, so
 // that the query rows are the narrow side (8) and tokens and dims the wide one:
 //   S^T = K Q^T   A = 16 tokens of keys, B = 8 query rows
 //   O^T = V^T P^T A = 16 dims of values over 16 tokens, B = the weights
 // A's registers come straight from the codes: E2M1 pairs convert to half2 in
-// one instruction, one half2 multiplication applies the block's scale, and the
+// one instruction, a half2 multiplication applies the block's scale, and the
 // order of dims (in S) and of tokens (in O) is free, so every lane reads whole
 // 4- to 16-byte runs of codes.  tcgen05 would need both operands written to
 // shared memory as binary16 first, 8 times the bytes the codes have.
@@ -36,6 +37,7 @@
 // sums.  Query rows are scaled by a power of two of their own, weights by 2^15
 // (p <= 1, so that weights down to 2^-29 keep all 11 bits).
 #include <algorithm>
+#include <type_traits>
 
 #include "kv4.cuh"
 
@@ -48,11 +50,6 @@ __device__ unsigned int g_err_kv4attn;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCodeBytes = 2048;                           // codes of a tile, keys or values
-constexpr int kScaleBytes = 128;                           // scales of a tile, room for blocks of 32
-constexpr int kSideBytes = kCodeBytes + kScaleBytes;
-constexpr int kStageBytes = 2 * kSideBytes;
-constexpr int kStages = 2;
 constexpr int kMaxCtas = 640;                              // partial-sum slots in the workspace
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -68,13 +65,19 @@ struct AttnParams {
   int causal, window;
 };
 
+// What an item costs a CTA beside its tiles (queries, joining the warps), in
+// tiles: counted when the tiles are dealt out.
+constexpr int kItemCost = 2;
+
 template <int D, int NT>
 struct Cfg {
-  static constexpr int TT = 4096 / D;      // tokens a tile (64, 32, 16)
+  static constexpr int TT = D == 256 ? 32 : 64;  // tokens a tile
   static constexpr int kRows = 8 * NT;
+  static constexpr int kCodeBytes = TT * D / 2;                 // codes of a tile, keys or values
+  static constexpr int kSideBytes = kCodeBytes + TT * D / 32;   // and scales, room for blocks of 32
   static constexpr int kPitch = D + 4;     // floats between rows of the merge buffer
   static constexpr int kSlot = kRows * (D + 2);  // floats of a partial: sums, maxima, weights
-  static constexpr size_t kSmem = kWarps * kStages * kStageBytes + kWarps * kRows * kPitch * 4;
+  static constexpr size_t kSmem = kWarps * 2 * kSideBytes + kWarps * kRows * kPitch * 4;
   static constexpr int kJoin = D * NT > 256 ? 2 : 4;  // thread groups that join pieces (static shared memory)
   // registers: 4 CTAs an SM where the sums and queries leave 128 a thread
   static constexpr int kMinCtas = D * NT <= 128 ? 4 : D * NT <= 256 ? 3 : 2;
@@ -100,11 +103,8 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return d;
 }
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
+__device__ __forceinline__ __half2 h2(uint32_t a) { return *reinterpret_cast<const __half2*>(&a); }
+__device__ __forceinline__ uint32_t u32(__half2 a) { return *reinterpret_cast<const uint32_t*>(&a); }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -112,10 +112,8 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// 2^(byte - ref + 13) for byte <= ref, 0 far below (as a binary32).
-__device__ __forceinline__ float scale_of(int byte, int ref) {
-  return __uint_as_float(static_cast<uint32_t>(max(byte - ref + 140, 0)) << 23);
-}
+// 2^(byte - 127) with 0 for byte 0 (and an infinity for 255, E8M0's NaN).
+__device__ __forceinline__ float byte_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 
 // 2^e; the clamp is reached only where what it scales vanishes anyway.
 __device__ __forceinline__ float pow2i(int e) {
@@ -146,21 +144,30 @@ __device__ __forceinline__ bool load_span(const Args& a, const AttnParams& p, in
   return true;
 }
 
-// A place in the sequence of all tiles.
+// A place among all tiles, and what is left of the CTA's range from there on
+// (in tiles, items counted as kItemCost more): at an end where left <= 0.
 struct Cursor {
-  int b, item, tile;
+  int b, item, tile, left;
   Span w;
 };
+// n tiles of the range further.
 template <int D, int NT>
 __device__ __forceinline__ void skip(const Args& a, const AttnParams& p, Cursor& c, int n) {
-  c.tile += n;
-  while (c.tile >= c.w.tiles) {
-    c.tile -= c.w.tiles;
-    if (++c.item == c.w.items) {
+  while (c.left > 0) {
+    const int here = c.w.tiles - c.tile;
+    if (n < here) {
+      c.tile += n;
+      c.left -= n;
+      return;
+    }
+    n -= here;
+    c.left -= here + kItemCost;
+    c.tile = 0;
+    if (++c.item == c.w.items && c.left > 0) {
       c.item = 0;
       do {
         if (++c.b >= a.n_seqs) {
-          c.w.tiles = 0x7fffffff;  // behind the last tile: never reached by a range
+          c.left = 0;
           return;
         }
       } while (!load_span<D, NT>(a, p, c.b, c.w));
@@ -187,30 +194,33 @@ __device__ __forceinline__ void store_row(const AttnParams& p, const Seq& s, int
 
 __device__ __forceinline__ int64_t range_start(int64_t units, int c, int n) { return units * c / n; }
 
-template <int D, int NT>
+template <int D, int NT, int BS>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     kv4_attn_kernel(const Args a, const AttnParams p) {
   using C = Cfg<D, NT>;
   constexpr int TT = C::TT, kRows = C::kRows, kPitch = C::kPitch;
+  constexpr int kCodeBytes = C::kCodeBytes, kSideBytes = C::kSideBytes;
   constexpr int KS = D / 16;        // k-steps of the scores, and groups of 16 dims of the sums
   constexpr int MS = TT / 16;       // groups of 16 tokens a tile
   constexpr int kKB = D / 8;        // code bytes a lane takes of a key (8, 16, 32)
   constexpr int kVB = D / 16;       // of a value (4, 8, 16)
   constexpr int kKW = kKB / 4, kVW = kVB / 4;
   constexpr int kScalesPerLane = D == 256 ? 2 : 1;  // 32-element parts of a lane's key dims
+  constexpr int kSB = D / BS;                       // scale bytes a token
+  constexpr int kSW = (TT * kSB + 127) / 128;       // words of scales a lane looks over (1 or 2)
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t full[kWarps * kStages];
+  __shared__ __align__(8) uint64_t full[kWarps * 2];
   __shared__ float sh_ml[2][kWarps][2][kRows];
   __shared__ long long sh_sum[kWarps];
   __shared__ int sh_b, sh_abort;
   __shared__ long long sh_off;
-  float* merge = reinterpret_cast<float*>(smem + kWarps * kStages * kStageBytes);
+  float* merge = reinterpret_cast<float*>(smem + kWarps * 2 * kSideBytes);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = lane >> 2, j = lane & 3;
 
   if (tid == 0) {
-    for (int i = 0; i < kWarps * kStages; ++i) mbar_init(smem_u32(&full[i]), 1);
+    for (int i = 0; i < kWarps * 2; ++i) mbar_init(smem_u32(&full[i]), 1);
     sh_abort = 0;
     sh_b = -1;
     fence_mbar_init();
@@ -219,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
   auto units_of = [&](int b) -> long long {
     Span w;
     if (b >= a.n_seqs || !load_span<D, NT>(a, p, b, w)) return 0;
-    return static_cast<long long>(w.tiles) * w.items;
+    return static_cast<long long>(w.tiles + kItemCost) * w.items;
   };
   long long sum = 0;
   for (int b = tid; b < a.n_seqs; b += kThreads) sum += units_of(b);
@@ -231,7 +241,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
   for (int i = 0; i < kWarps; ++i) units += sh_sum[i];
   // at least a tile a warp for every CTA that works
   const int cta = blockIdx.x;
-  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), (units + kWarps - 1) / kWarps));
+  const int ctas = static_cast<int>(
+      min(static_cast<long long>(gridDim.x), (units + kWarps + kItemCost - 1) / (kWarps + kItemCost)));
   grid_launch_dependents();
   if (tid == 0) p.rec[cta] = make_int4(-1, 0, 0, 0);
   if (cta >= ctas) return;  // the whole CTA
@@ -264,56 +275,80 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
   Cursor cur;  // the CTA's place
   cur.b = sh_b;
   load_span<D, NT>(a, p, cur.b, cur.w);
-  cur.item = static_cast<int>(sh_off / cur.w.tiles);
-  cur.tile = static_cast<int>(sh_off % cur.w.tiles);
-  const int n_units = static_cast<int>(u1 - u0);
+  cur.item = static_cast<int>(sh_off / (cur.w.tiles + kItemCost));
+  cur.tile = static_cast<int>(sh_off % (cur.w.tiles + kItemCost)) - kItemCost;
+  cur.left = static_cast<int>(u1 - u0);
+  int64_t at = u0;  // where the range's first tile stands
+  if (cur.tile < 0) {
+    at -= cur.tile;
+    cur.left += cur.tile;
+    cur.tile = 0;
+  }
 
-  // ---- the warp's ring
-  const uint32_t ring = smem_u32(smem) + warp * kStages * kStageBytes;
-  const uint8_t* ring_p = smem + warp * kStages * kStageBytes;
-  Cursor ahead = cur;  // the next tile to fetch
-  skip<D, NT>(a, p, ahead, warp);
-  int fetched = warp;  // its index in the range
-  uint32_t phase = 0;  // one bit a stage
-  const int sb_shift = a.block_shift;           // D >> sb_shift scale bytes a token
-  const int scale_bytes = TT * D >> sb_shift;   // of a tile
-  auto fetch = [&](int stage) {
-    if (fetched >= n_units) return;
-    // copies: pages of the tile x (k codes, k scales, v codes, v scales), one a lane
-    const int chunk_tokens = min(TT, a.page);
-    const int chunk = lane >> 2, what = lane & 3;
-    const int tok = (ahead.w.t0 + ahead.tile) * TT + chunk * chunk_tokens;
-    const bool codes = (what & 1) == 0;
-    const uint32_t bytes = static_cast<uint32_t>(codes ? chunk_tokens * (D / 2) : chunk_tokens * D >> sb_shift);
-    bool want = chunk * chunk_tokens < TT && tok < ahead.w.hi;
-    int64_t row = 0;
-    if (want) {
-      row = token_row(a, ahead.b, tok, ahead.item / ahead.w.groups, &g_err_kv4attn, 46);
-      want = row >= 0;
-    }
-    const uint32_t total = __reduce_add_sync(0xffffffffu, want ? bytes : 0u);
-    const uint32_t bar = smem_u32(&full[warp * kStages + stage]);
-    if (lane == 0) mbar_arrive_expect_tx(bar, total);
-    __syncwarp();
-    if (want) {
-      const Side& side = what < 2 ? a.k : a.v;
-      const uint8_t* src = codes ? side.codes + row * (D / 2) : side.scales + row * (D >> sb_shift);
-      const uint32_t dst = ring + stage * kStageBytes + (what < 2 ? 0 : kSideBytes) + (codes ? 0 : kCodeBytes) +
-                           chunk * bytes;
-      bulk_copy_g2s(dst, src, bytes, bar);
-    }
-    skip<D, NT>(a, p, ahead, kWarps);
-    fetched += kWarps;
+  // ---- the warp's buffers: a tile of keys and a tile of values, each fetched
+  // again as soon as it has been read
+  const uint32_t buf = smem_u32(smem) + warp * 2 * kSideBytes;
+  uint8_t* const ks = smem + warp * 2 * kSideBytes;
+  uint8_t* const vs = ks + kSideBytes;
+  const uint32_t bar_k = smem_u32(&full[warp * 2]), bar_v = bar_k + 8;
+  uint32_t phase = 0;  // of both
+  // copies of a tile: a page's codes and scales on two lanes
+  const int chunk_tokens = min(TT, a.page);
+  const bool is_code = (lane & 1) == 0;
+  const int chunk_at = (lane >> 1) * chunk_tokens;
+  const int row_bytes = is_code ? D / 2 : kSB;
+  const uint32_t copy_bytes = static_cast<uint32_t>(chunk_tokens * row_bytes);
+  const uint32_t copy_dst = buf + (is_code ? 0 : kCodeBytes) + (lane >> 1) * copy_bytes;
+  const uint8_t* const src_k = is_code ? a.k.codes : a.k.scales;
+  const uint8_t* const src_v = is_code ? a.v.codes : a.v.scales;
+  Cursor ahead = cur;      // the next tile to fetch
+  int page = -1;           // this lane's page of it, -1: none
+  int page_off = 0;        // tokens into the page, and its key head
+  int page_head = 0;
+  auto locate = [&]() {    // the table's entry is looked up a tile early
+    page = -1;
+    if (ahead.left <= 0) return;
+    const int tok = (ahead.w.t0 + ahead.tile) * TT + chunk_at;
+    page_off = tok & (a.page - 1);
+    page_head = ahead.item / ahead.w.groups;
+    if (chunk_at < TT && tok < ahead.w.hi)
+      page = __ldg(a.table + static_cast<int64_t>(ahead.b) * a.max_pages + (tok >> a.page_shift));
+    else
+      page = -2;
   };
+  int64_t fetch_at = 0;      // byte offset of this lane's copy
+  uint32_t fetch_lanes = 0;  // the lanes that have one
+  auto fetch_keys = [&]() {  // and settle the place that the values' copies use too
+    const bool ok = page >= 0 && page < a.n_pages;
+    if (!ok && page != -2) atomicCAS(&g_err_kv4attn, 0u, kErrArg | (46u << 8));  // a page id outside the cache
+    fetch_lanes = __ballot_sync(0xffffffffu, ok);
+    fetch_at = (((static_cast<int64_t>(page) * a.Hkv + page_head) << a.page_shift) + page_off) * row_bytes;
+    if (lane == 0)
+      mbar_arrive_expect_tx(bar_k, __popc(fetch_lanes) / 2 * (chunk_tokens * (D / 2 + kSB)));
+    __syncwarp();
+    if (ok) bulk_copy_g2s(copy_dst, src_k + fetch_at, copy_bytes, bar_k);
+  };
+  auto fetch_values = [&]() {
+    if (lane == 0)
+      mbar_arrive_expect_tx(bar_v, __popc(fetch_lanes) / 2 * (chunk_tokens * (D / 2 + kSB)));
+    __syncwarp();
+    if (fetch_lanes >> lane & 1) bulk_copy_g2s(copy_dst + kSideBytes, src_v + fetch_at, copy_bytes, bar_v);
+  };
+  skip<D, NT>(a, p, ahead, warp);
+  locate();
   __syncthreads();  // barriers initialised
-  for (int s = 0; s < kStages; ++s) fetch(s);
+  if (ahead.left > 0) {
+    fetch_keys();
+    fetch_values();
+    skip<D, NT>(a, p, ahead, kWarps);
+    locate();
+  }
 
   int done = 0;      // tiles of the range before the current segment
-  int stage = 0;
   int seg = 0;
-  while (done < n_units) {
+  while (cur.left > 0) {
     // ---- a segment: the range's tiles of one item
-    const int seg_tiles = min(cur.w.tiles - cur.tile, n_units - done);
+    const int seg_tiles = min(cur.w.tiles - cur.tile, cur.left);
     const int kvh = cur.item / cur.w.groups, group = cur.item - kvh * cur.w.groups;
     const int all_rows = cur.w.s.rows * p.G;
     const int r0 = group * kRows;
@@ -371,75 +406,79 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
       m[t][0] = m[t][1] = -INFINITY;
       l[t][0] = l[t][1] = 0.f;
     }
-    int ref_v = 0;
+    int ref_v = 13;  // below 13 the factor 2^(140 - ref) would leave binary32
 
     for (int i = (warp - done % kWarps + kWarps) % kWarps; i < seg_tiles; i += kWarps) {
-      mbar_wait(smem_u32(&full[warp * kStages + stage]), (phase >> stage) & 1, &sh_abort, &g_err_kv4attn, 47);
-      phase ^= 1u << stage;
-      const uint8_t* ks = ring_p + stage * kStageBytes;
-      const uint8_t* vs = ks + kSideBytes;
       const int tok0 = (cur.w.t0 + cur.tile + i) * TT;
       // a tile that no row of this group reads (causal, earlier rows): nothing
       const bool any = tok0 <= pos_max && tok0 + TT > pos_min - win + 1 && cur.w.hi > 0;
-      if (any) {
-        // largest scales; scale bytes of tokens that no row reads become 0, so
-        // that whatever stands there gives zero operands
-        uint32_t* ksc = reinterpret_cast<uint32_t*>(const_cast<uint8_t*>(ks + kCodeBytes)) + lane;
-        uint32_t* vsc = reinterpret_cast<uint32_t*>(const_cast<uint8_t*>(vs + kCodeBytes)) + lane;
-        const bool has = lane * 4 < scale_bytes;
-        uint32_t kw = has ? *ksc : 0u, vw = has ? *vsc : 0u;
-        if (tok0 < cur.w.lo || tok0 + TT > cur.w.hi) {
-          uint32_t keep = 0;
+      const bool edge = tok0 < cur.w.lo || tok0 + TT > cur.w.hi;
+      // largest scale byte of a side; at an edge of what the rows read, the
+      // scale bytes of tokens that no row reads become 0 first, so that
+      // whatever stands there gives zero operands
+      auto top_scale = [&](uint8_t* scales) {
+        uint32_t* sc = reinterpret_cast<uint32_t*>(scales) + lane;
+        uint32_t w[kSW];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int tok = tok0 + ((lane * 4 + x) << sb_shift) / D;
-            if (tok >= cur.w.lo && tok < cur.w.hi) keep |= 0xFFu << (8 * x);
+        for (int y = 0; y < kSW; ++y) {
+          const bool has = (y * 32 + lane) * 4 < TT * kSB;
+          w[y] = has ? sc[y * 32] : 0u;
+          if (edge) {
+            uint32_t keep = 0;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int tok = tok0 + ((y * 32 + lane) * 4 + x) / kSB;
+              if (tok >= cur.w.lo && tok < cur.w.hi) keep |= 0xFFu << (8 * x);
+            }
+            w[y] &= keep;
+            if (has) sc[y * 32] = w[y];
           }
-          kw &= keep;
-          vw &= keep;
-          if (has) {
-            *ksc = kw;
-            *vsc = vw;
-          }
-          fence_proxy_async_shared();  // the ring's next copy comes after these writes
+        }
+        if (edge) {
+          fence_proxy_async_shared();  // the next copy into this buffer comes after these writes
           __syncwarp();
         }
-        auto top = [](uint32_t w) {
-          w = __vmaxu4(w, w >> 16);
-          return max(w & 0xFFu, (w >> 8) & 0xFFu);
-        };
-        const int ref_k = static_cast<int>(__reduce_max_sync(0xffffffffu, top(kw)));
-        const int tile_v = static_cast<int>(__reduce_max_sync(0xffffffffu, top(vw)));
-
+        uint32_t t = w[0];
+        if constexpr (kSW == 2) t = __vmaxu4(t, w[1]);
+        t = __vmaxu4(t, t >> 16);
+        return static_cast<int>(__reduce_max_sync(0xffffffffu, max(t & 0xFFu, (t >> 8) & 0xFFu)));
+      };
+      mbar_wait(bar_k, phase & 1, &sh_abort, &g_err_kv4attn, 47);
+      float s[NT][MS][4];
+      float f_tile = 0.f;
+      if (any) {
+        const int top_k = top_scale(ks + kCodeBytes);
+        const int ref_k = max(top_k, 13);
+        const float fk = pow2i(140 - ref_k);
+        f_tile = top_k == 255 ? NAN : pow2w(ref_k - 140);
         // ---- scores, transposed: 16 tokens x 8 rows
-        float s[NT][MS][4];
+        // tokens of a group of 16: matrix row x is token x/2 (x even) or 4 + (x/2 ^ 1)
+        // (x odd), plus 8 for x >= 8: reads of keys free of bank conflicts
+        const int tk = (n & 1) ? 4 + ((n >> 1) ^ 1) : (n >> 1);
+        const uint8_t* c0 = ks + tk * (D / 2) + j * kKB;
+        const uint8_t* sc0 = ks + kCodeBytes + tk * kSB + j * (D / 4) / BS;
 #pragma unroll
         for (int ms = 0; ms < MS; ++ms) {
-          // tokens of the group: matrix row x is token x/2 (x even) or 4 + (x/2 ^ 1)
-          // (x odd), plus 8 for x >= 8: conflict-free reads of keys and values
-          const int tk = ms * 16 + ((n & 1) ? 4 + ((n >> 1) ^ 1) : (n >> 1));
           uint32_t w0[kKW], w1[kKW];
-          const uint8_t* c0 = ks + tk * (D / 2) + j * kKB;
-          const uint8_t* c1 = c0 + 8 * (D / 2);
+          const uint8_t* c = c0 + ms * 8 * D;
           if constexpr (kKW == 2) {
-            const uint2 x = *reinterpret_cast<const uint2*>(c0), y = *reinterpret_cast<const uint2*>(c1);
+            const uint2 x = *reinterpret_cast<const uint2*>(c), y = *reinterpret_cast<const uint2*>(c + 4 * D);
             w0[0] = x.x, w0[1] = x.y, w1[0] = y.x, w1[1] = y.y;
           } else {
 #pragma unroll
             for (int x = 0; x < kKW / 4; ++x) {
-              const uint4 u = reinterpret_cast<const uint4*>(c0)[x], y = reinterpret_cast<const uint4*>(c1)[x];
+              const uint4 u = reinterpret_cast<const uint4*>(c)[x], y = reinterpret_cast<const uint4*>(c + 4 * D)[x];
               w0[4 * x] = u.x, w0[4 * x + 1] = u.y, w0[4 * x + 2] = u.z, w0[4 * x + 3] = u.w;
               w1[4 * x] = y.x, w1[4 * x + 1] = y.y, w1[4 * x + 2] = y.z, w1[4 * x + 3] = y.w;
             }
           }
-          uint32_t m0[kScalesPerLane], m1[kScalesPerLane];
+          __half2 m0[kScalesPerLane], m1[kScalesPerLane];
 #pragma unroll
           for (int x = 0; x < kScalesPerLane; ++x) {
-            const int blk = (j * (D / 4) + x * 32) >> sb_shift;
-            const uint8_t* sc = ks + kCodeBytes + ((tk * D) >> sb_shift) + blk;
-            const float a0 = scale_of(sc[0], ref_k), a1 = scale_of(sc[(8 * D) >> sb_shift], ref_k);
-            m0[x] = pack_half2(a0, a0);
-            m1[x] = pack_half2(a1, a1);
+            const float a0 = byte_scale(sc0[ms * 16 * kSB + x * 32 / BS]) * fk;
+            const float a1 = byte_scale(sc0[ms * 16 * kSB + 8 * kSB + x * 32 / BS]) * fk;
+            m0[x] = h2(pack_half2(a0, a0));
+            m1[x] = h2(pack_half2(a1, a1));
           }
 #pragma unroll
           for (int t = 0; t < NT; ++t) s[t][ms][0] = s[t][ms][1] = s[t][ms][2] = s[t][ms][3] = 0.f;
@@ -451,17 +490,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
             const int x = w / (kKW / kScalesPerLane);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const uint32_t af[4] = {hmul2(h0[2 * k], m0[x]), hmul2(h1[2 * k], m1[x]), hmul2(h0[2 * k + 1], m0[x]),
-                                      hmul2(h1[2 * k + 1], m1[x])};
+              const uint32_t af[4] = {u32(__hmul2(h2(h0[2 * k]), m0[x])), u32(__hmul2(h2(h1[2 * k]), m1[x])),
+                                      u32(__hmul2(h2(h0[2 * k + 1]), m0[x])), u32(__hmul2(h2(h1[2 * k + 1]), m1[x]))};
 #pragma unroll
               for (int t = 0; t < NT; ++t) mma_f16(s[t][ms], af, qf[t][2 * w + k][0], qf[t][2 * w + k][1]);
             }
           }
         }
+      }
+      __syncwarp();  // every lane has read the keys
+      const bool more = ahead.left > 0;
+      if (more) fetch_keys();
+      mbar_wait(bar_v, phase & 1, &sh_abort, &g_err_kv4attn, 47);
+      phase ^= 1u;
+      if (any) {
         // ---- softmax over the tile
-        const float f_tile = ref_k == 255 ? NAN : pow2w(ref_k - 140);
         const bool whole = tok0 + TT - 1 <= pos_min && tok0 > pos_max - win;
-        const int new_v = max(ref_v, tile_v);
+        const int top_v = top_scale(vs + kCodeBytes);
+        const int new_v = max(ref_v, top_v);
         const float fv = ref_v == new_v ? 1.f : pow2i(ref_v - new_v);
         ref_v = new_v;
         uint32_t pb[NT][MS][2];
@@ -473,13 +519,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
           for (int ms = 0; ms < MS; ++ms)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              float v = s[t][ms][x] * f[x & 1];
+              s[t][ms][x] *= f[x & 1];
               if (!whole) {
                 const int tok = tok0 + ms * 16 + ((n & 1) ? 4 + ((n >> 1) ^ 1) : (n >> 1)) + (x >> 1) * 8;
-                if (tok > pos[t][x & 1] || tok <= pos[t][x & 1] - win) v = -INFINITY;
+                if (tok > pos[t][x & 1] || tok <= pos[t][x & 1] - win) s[t][ms][x] = -INFINITY;
               }
-              s[t][ms][x] = v;
-              mx[x & 1] = fmaxf(mx[x & 1], v);
+              mx[x & 1] = fmaxf(mx[x & 1], s[t][ms][x]);
             }
           float base[2], al[2];
 #pragma unroll
@@ -516,47 +561,70 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
             pb[t][ms][1] = movmatrix_trans(pack_half2(e[2], e[3]));
           }
         }
-        // ---- weighted values, transposed: 16 dims x 8 rows over 16 tokens
+        // ---- weighted values, transposed.  A register of A is a pair of dims
+        // of one token, so the matrix' k runs over (token, parity), 8 tokens a
+        // step, and two products with the weights at the even or at the odd
+        // places give the even and the odd dims: twice the products, which the
+        // tensor cores have room for, and no permutation of pairs
+        const float fr = pow2i(140 - ref_v);
+        // tokens of k = 2j and 2j + 1 of the scores' group of 8
+        const uint8_t* v0 = vs + j * (D / 2) + n * kVB;
+        const uint8_t* v1 = vs + (4 + (j ^ 1)) * (D / 2) + n * kVB;
+        const uint8_t* z0 = vs + kCodeBytes + j * kSB + n * (D / 8) / BS;
+        const uint8_t* z1 = vs + kCodeBytes + (4 + (j ^ 1)) * kSB + n * (D / 8) / BS;
 #pragma unroll
-        for (int ms = 0; ms < MS; ++ms) {
-          uint32_t w[4][kVW];
-          float sc[4];
+        for (int ms = 0; ms < MS; ++ms)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {  // tokens of k = 2j, 2j + 1, 2j + 8, 2j + 9
-            const int tk = ms * 16 + ((x & 1) ? 4 + (j ^ 1) : j) + (x >> 1) * 8;
-            const uint8_t* c = vs + tk * (D / 2) + n * kVB;
-            if constexpr (kVW == 1) {
-              w[x][0] = *reinterpret_cast<const uint32_t*>(c);
-            } else if constexpr (kVW == 2) {
-              const uint2 u = *reinterpret_cast<const uint2*>(c);
-              w[x][0] = u.x, w[x][1] = u.y;
-            } else {
-              const uint4 u = *reinterpret_cast<const uint4*>(c);
-              w[x][0] = u.x, w[x][1] = u.y, w[x][2] = u.z, w[x][3] = u.w;
+          for (int e8 = 0; e8 < 2; ++e8) {  // 8 tokens
+            uint32_t w[2][kVW];
+            __half2 sc[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint8_t* c = (x ? v1 : v0) + (ms * 2 + e8) * 4 * D;
+              if constexpr (kVW == 1) {
+                w[x][0] = *reinterpret_cast<const uint32_t*>(c);
+              } else if constexpr (kVW == 2) {
+                const uint2 u = *reinterpret_cast<const uint2*>(c);
+                w[x][0] = u.x, w[x][1] = u.y;
+              } else {
+                const uint4 u = *reinterpret_cast<const uint4*>(c);
+                w[x][0] = u.x, w[x][1] = u.y, w[x][2] = u.z, w[x][3] = u.w;
+              }
+              const float z = byte_scale((x ? z1 : z0)[(ms * 2 + e8) * 8 * kSB]) * fr;
+              sc[x] = h2(pack_half2(z, z));
             }
-            sc[x] = scale_of(vs[kCodeBytes + ((tk * D) >> sb_shift) + ((n * (D / 8)) >> sb_shift)], ref_v);
-          }
-          const uint32_t m01 = pack_half2(sc[0], sc[1]), m23 = pack_half2(sc[2], sc[3]);
+            uint32_t be[NT][2], bo[NT][2];
 #pragma unroll
-          for (int x = 0; x < kVW; ++x) {
-            uint32_t h[4][4];
+            for (int t = 0; t < NT; ++t) {
+              be[t][0] = pb[t][ms][e8] & 0xFFFFu;
+              bo[t][0] = pb[t][ms][e8] << 16;
+              be[t][1] = pb[t][ms][e8] >> 16;
+              bo[t][1] = pb[t][ms][e8] & 0xFFFF0000u;
+            }
 #pragma unroll
-            for (int y = 0; y < 4; ++y) e2m1x8_to_half(w[y][x], h[y]);
+            for (int x = 0; x < kVW; ++x) {
+              uint32_t ha[4], hb[4];
+              e2m1x8_to_half(w[0][x], ha);
+              e2m1x8_to_half(w[1][x], hb);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const uint32_t af[4] = {hmul2(__byte_perm(h[0][y], h[1][y], 0x5410), m01),
-                                      hmul2(__byte_perm(h[0][y], h[1][y], 0x7632), m01),
-                                      hmul2(__byte_perm(h[2][y], h[3][y], 0x5410), m23),
-                                      hmul2(__byte_perm(h[2][y], h[3][y], 0x7632), m23)};
+              for (int y = 0; y < 2; ++y) {  // dims 8x + 4y .. + 3 of the lane's
+                const uint32_t af[4] = {u32(__hmul2(h2(ha[2 * y]), sc[0])), u32(__hmul2(h2(ha[2 * y + 1]), sc[0])),
+                                        u32(__hmul2(h2(hb[2 * y]), sc[1])), u32(__hmul2(h2(hb[2 * y + 1]), sc[1]))};
 #pragma unroll
-              for (int t = 0; t < NT; ++t) mma_f16(o[t][4 * x + y], af, pb[t][ms][0], pb[t][ms][1]);
+                for (int t = 0; t < NT; ++t) {
+                  mma_f16(o[t][2 * (2 * x + y)], af, be[t][0], be[t][1]);
+                  mma_f16(o[t][2 * (2 * x + y) + 1], af, bo[t][0], bo[t][1]);
+                }
+              }
             }
           }
-        }
       }
-      __syncwarp();  // every lane has read the stage
-      fetch(stage);
-      stage ^= 1;
+      __syncwarp();  // every lane has read the values
+      if (more) {
+        fetch_values();
+        skip<D, NT>(a, p, ahead, kWarps);
+        locate();
+      }
     }
 
     // ---- join the warps
@@ -591,8 +659,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
         float* dst = merge + (warp * kRows + r) * kPitch + n * (D / 8);
 #pragma unroll
         for (int i = 0; i < KS; i += 2)
-          *reinterpret_cast<float4*>(dst + 2 * i) =
-              make_float4(o[t][i][h] * f * fa * fb, o[t][i][2 + h] * f * fa * fb, o[t][i + 1][h] * f * fa * fb,
+          *reinterpret_cast<float4*>(dst + 2 * i) =  // o[i]: even dims, o[i + 1]: odd dims
+              make_float4(o[t][i][h] * f * fa * fb, o[t][i + 1][h] * f * fa * fb, o[t][i][2 + h] * f * fa * fb,
                           o[t][i + 1][2 + h] * f * fa * fb);
       }
     __syncthreads();
@@ -632,13 +700,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     // the item begins here and goes on in later CTAs: this CTA's record (unit x
     // is in the last range c with units c / ctas < x + 1)
     if (tid == 0 && cur.tile == 0 && !complete) {
-      const int64_t end = u0 + done + cur.w.tiles;  // the item's last tile + 1
+      const int64_t end = at + cur.w.tiles;  // the item's last tile + 1
       const int last = static_cast<int>((end * ctas - 1) / units);
       p.rec[cta] = make_int4(cur.item, cur.b, last, seg > 0);
     }
     done += seg_tiles;
     ++seg;
-    if (done < n_units) skip<D, NT>(a, p, cur, seg_tiles);
+    at += seg_tiles + kItemCost;
+    skip<D, NT>(a, p, cur, seg_tiles);
   }
 }
 
@@ -707,14 +776,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kJoin * 128)
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, int BS>
 rnl_status launch_split(const AttnParams& p, const Args& a, const DeviceInfo& dev, cudaStream_t s) {
   using C = Cfg<D, NT>;
-  const rnl_status st = ensure_smem_attr(reinterpret_cast<const void*>(kv4_attn_kernel<D, NT>), dev.device, C::kSmem);
+  const rnl_status st = ensure_smem_attr(reinterpret_cast<const void*>(kv4_attn_kernel<D, NT, BS>), dev.device, C::kSmem);
   if (st != RNL_OK) return st;
   const int ctas = std::min(dev.sm_count * C::kMinCtas, kMaxCtas);
   trace_before(s);
-  kv4_attn_kernel<D, NT><<<ctas, kThreads, C::kSmem, s>>>(a, p);
+  kv4_attn_kernel<D, NT, BS><<<ctas, kThreads, C::kSmem, s>>>(a, p);
   cudaError_t e = cudaGetLastError();
   trace_after(s, "kv4_attn");
   if (e != cudaSuccess) return RNL_ERR_LAUNCH;
@@ -761,11 +830,14 @@ rnl_status launch_kv4_attention(const Kv4AttnArgs& x, const rnl_kv4_cache& c, co
   // 8 rows an item where the rows that a sequence has on average fit, else 16
   const int64_t rows = (q.n_rows + q.n_seqs - 1) / q.n_seqs * p.G;
   const bool wide = rows > 8;
-  switch (a.D) {
-    case 64: return wide ? launch_split<64, 2>(p, a, dev, s) : launch_split<64, 1>(p, a, dev, s);
-    case 128: return wide ? launch_split<128, 2>(p, a, dev, s) : launch_split<128, 1>(p, a, dev, s);
-    default: return wide ? launch_split<256, 2>(p, a, dev, s) : launch_split<256, 1>(p, a, dev, s);
-  }
+  auto go = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    if (c.block == 64) return wide ? launch_split<D, 2, 64>(p, a, dev, s) : launch_split<D, 1, 64>(p, a, dev, s);
+    return wide ? launch_split<D, 2, 32>(p, a, dev, s) : launch_split<D, 1, 32>(p, a, dev, s);
+  };
+  if (a.D == 64) return go(std::integral_constant<int, 64>{});
+  if (a.D == 128) return go(std::integral_constant<int, 128>{});
+  return go(std::integral_constant<int, 256>{});
 }
 
 rnl_status read_clear_error_kv4attn(unsigned int* word) {
