@@ -9,7 +9,7 @@
 //
 // Rows and items.  The G = Hq / Hkv query heads of one key head and the rows of
 // one sequence form one list of rows (row r: token r / G, head r % G); an item
-// is (sequence, key head, 8 NT of these rows).  Every item's tokens are cut
+// is (sequence, key head, 4, 8 or 16 of these rows).  Every item's tokens are cut
 // into tiles of TT; all items' tiles, one after the other, are dealt to the
 // CTAs in equal contiguous ranges, whatever the lengths are, so that no SM
 // waits for a long sequence.  An item that lies in one range is written by its
@@ -72,15 +72,18 @@ constexpr int kItemCost = 2;
 template <int D, int NT>
 struct Cfg {
   static constexpr int TT = D == 256 ? 32 : 64;  // tokens a tile
-  static constexpr int kRows = 8 * NT;
+  // NT = 0: 4 rows, twice in the 8 columns of a product; the second copy takes
+  // the odd dims of the sums, so that they need one product instead of two
+  static constexpr int kRows = NT == 0 ? 4 : 8 * NT;
+  static constexpr int kTiles = NT == 0 ? 1 : NT;   // column tiles of 8
   static constexpr int kCodeBytes = TT * D / 2;                 // codes of a tile, keys or values
   static constexpr int kSideBytes = kCodeBytes + TT * D / 32;   // and scales, room for blocks of 32
   static constexpr int kPitch = D + 4;     // floats between rows of the merge buffer
   static constexpr int kSlot = kRows * (D + 2);  // floats of a partial: sums, maxima, weights
   static constexpr size_t kSmem = kWarps * 2 * kSideBytes + kWarps * kRows * kPitch * 4;
-  static constexpr int kJoin = D * NT > 256 ? 2 : 4;  // thread groups that join pieces (static shared memory)
+  static constexpr int kJoin = D * kTiles > 256 ? 2 : 4;  // thread groups that join pieces (static shared memory)
   // registers: 4 CTAs an SM where the sums and queries leave 128 a thread
-  static constexpr int kMinCtas = D * NT <= 128 ? 4 : D * NT <= 256 ? 3 : 2;
+  static constexpr int kMinCtas = D * kTiles <= 128 ? 4 : D * kTiles <= 256 ? 3 : 2;
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -106,9 +109,10 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 __device__ __forceinline__ __half2 h2(uint32_t a) { return *reinterpret_cast<const __half2*>(&a); }
 __device__ __forceinline__ uint32_t u32(__half2 a) { return *reinterpret_cast<const uint32_t*>(&a); }
 
+// 2^x; results below binary32's normal range become 0.
 __device__ __forceinline__ float ex2(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -125,7 +129,6 @@ __device__ __forceinline__ float pow2w(int e) { return pow2i(e / 2) * pow2i(e - 
 // What of a sequence the call's rows read, in tiles.
 struct Span {
   Seq s;
-  int items;      // Hkv * row groups
   int groups;     // row groups of kRows
   int lo, hi;     // tokens that any row reads
   int t0, tiles;  // first tile, number of tiles (at least 1: an item without tokens still writes zeros)
@@ -135,7 +138,6 @@ __device__ __forceinline__ bool load_span(const Args& a, const AttnParams& p, in
   constexpr int TT = Cfg<D, NT>::TT;
   if (!load_seq(a, b, w.s, &g_err_kv4attn, 45) || w.s.rows == 0) return false;
   w.groups = (w.s.rows * p.G + Cfg<D, NT>::kRows - 1) / Cfg<D, NT>::kRows;
-  w.items = w.groups * a.Hkv;
   w.lo = 0;
   w.hi = w.s.len;
   if (p.causal && p.window > 0) w.lo = max(0, w.s.len - w.s.rows + 1 - p.window);
@@ -147,7 +149,7 @@ __device__ __forceinline__ bool load_span(const Args& a, const AttnParams& p, in
 // A place among all tiles, and what is left of the CTA's range from there on
 // (in tiles, items counted as kItemCost more): at an end where left <= 0.
 struct Cursor {
-  int b, item, tile, left;
+  int b, head, group, tile, left;
   Span w;
 };
 // n tiles of the range further.
@@ -163,8 +165,10 @@ __device__ __forceinline__ void skip(const Args& a, const AttnParams& p, Cursor&
     n -= here;
     c.left -= here + kItemCost;
     c.tile = 0;
-    if (++c.item == c.w.items && c.left > 0) {
-      c.item = 0;
+    if (++c.group < c.w.groups) continue;
+    c.group = 0;
+    if (++c.head == a.Hkv && c.left > 0) {
+      c.head = 0;
       do {
         if (++c.b >= a.n_seqs) {
           c.left = 0;
@@ -198,7 +202,8 @@ template <int D, int NT, int BS>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     kv4_attn_kernel(const Args a, const AttnParams p) {
   using C = Cfg<D, NT>;
-  constexpr int TT = C::TT, kRows = C::kRows, kPitch = C::kPitch;
+  constexpr int TT = C::TT, kRows = C::kRows, kPitch = C::kPitch, T8 = C::kTiles;
+  constexpr bool kTwin = NT == 0;   // both parities in one product
   constexpr int kCodeBytes = C::kCodeBytes, kSideBytes = C::kSideBytes;
   constexpr int KS = D / 16;        // k-steps of the scores, and groups of 16 dims of the sums
   constexpr int MS = TT / 16;       // groups of 16 tokens a tile
@@ -229,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
   auto units_of = [&](int b) -> long long {
     Span w;
     if (b >= a.n_seqs || !load_span<D, NT>(a, p, b, w)) return 0;
-    return static_cast<long long>(w.tiles + kItemCost) * w.items;
+    return static_cast<long long>(w.tiles + kItemCost) * w.groups * a.Hkv;
   };
   long long sum = 0;
   for (int b = tid; b < a.n_seqs; b += kThreads) sum += units_of(b);
@@ -275,7 +280,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
   Cursor cur;  // the CTA's place
   cur.b = sh_b;
   load_span<D, NT>(a, p, cur.b, cur.w);
-  cur.item = static_cast<int>(sh_off / (cur.w.tiles + kItemCost));
+  const int item = static_cast<int>(sh_off / (cur.w.tiles + kItemCost));
+  cur.head = item / cur.w.groups;
+  cur.group = item - cur.head * cur.w.groups;
   cur.tile = static_cast<int>(sh_off % (cur.w.tiles + kItemCost)) - kItemCost;
   cur.left = static_cast<int>(u1 - u0);
   int64_t at = u0;  // where the range's first tile stands
@@ -310,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     if (ahead.left <= 0) return;
     const int tok = (ahead.w.t0 + ahead.tile) * TT + chunk_at;
     page_off = tok & (a.page - 1);
-    page_head = ahead.item / ahead.w.groups;
+    page_head = ahead.head;
     if (chunk_at < TT && tok < ahead.w.hi)
       page = __ldg(a.table + static_cast<int64_t>(ahead.b) * a.max_pages + (tok >> a.page_shift));
     else
@@ -349,16 +356,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
   while (cur.left > 0) {
     // ---- a segment: the range's tiles of one item
     const int seg_tiles = min(cur.w.tiles - cur.tile, cur.left);
-    const int kvh = cur.item / cur.w.groups, group = cur.item - kvh * cur.w.groups;
+    const int kvh = cur.head;
     const int all_rows = cur.w.s.rows * p.G;
-    const int r0 = group * kRows;
+    const int r0 = cur.group * kRows;
     // queries: lane (n, j) holds dims [j D/4, (j + 1) D/4) of row n of each tile of 8
-    uint32_t qf[NT][KS][2];
-    float f_row[NT][2];  // score factors of rows 2j and 2j + 1
-    int pos[NT][2];      // last token they read
+    uint32_t qf[T8][KS][2];
+    float f_row[T8][2];  // score factors of rows 2j and 2j + 1
+    int pos[T8][2];      // last token they read
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int r = min(r0 + t * 8 + n, all_rows - 1);
+    for (int t = 0; t < T8; ++t) {
+      const int r = min(r0 + t * 8 + (kTwin ? n & 3 : n), all_rows - 1);
       const int tok = r / p.G;
       const __nv_bfloat16* src = p.q + (cur.w.s.row0 + tok) * p.q_stride +
                                  static_cast<int64_t>(kvh * p.G + (r - tok * p.G)) * D + j * (D / 4);
@@ -379,7 +386,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
       const int eb = static_cast<int>(am >> 23);
       // exponent field 127 + 14 for the largest: times 2^(141 - eb), in two steps
       const int e = 141 - max(eb, 1);
-      const float s1 = pow2i(e / 2), s2 = pow2i(e - e / 2);
+      // the scale's sign goes with the query: score factors are then positive
+      const float s1 = p.scale_log2 < 0.f ? -pow2i(e / 2) : pow2i(e / 2), s2 = pow2i(e - e / 2);
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
         qf[t][i >> 1][i & 1] = pack_half2(__uint_as_float(w[i] << 16) * s1 * s2,
@@ -387,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int er = __shfl_sync(0xffffffffu, e, (2 * j + h) * 4);
-        f_row[t][h] = p.scale_log2 * pow2w(-er);
-        const int rr = min(r0 + t * 8 + 2 * j + h, all_rows - 1);
+        f_row[t][h] = fabsf(p.scale_log2) * pow2w(-er);
+        const int rr = min(r0 + t * 8 + (kTwin ? 2 * (j & 1) : 2 * j) + h, all_rows - 1);
         pos[t][h] = p.causal ? cur.w.s.len - cur.w.s.rows + rr / p.G : cur.w.s.len - 1;
       }
     }
@@ -397,12 +405,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     const int pos_max = p.causal ? cur.w.s.len - cur.w.s.rows + r_last / p.G : cur.w.s.len - 1;
     const int win = p.window > 0 ? p.window : 0x40000000;
 
-    float o[NT][KS][4];
-    float m[NT][2], l[NT][2];
+    constexpr int KO = kTwin ? KS / 2 : KS;  // accumulators of 4
+    float o[T8][KO][4];
+    float m[T8][2], l[T8][2];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < T8; ++t) {
 #pragma unroll
-      for (int i = 0; i < KS; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
+      for (int i = 0; i < KO; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
       m[t][0] = m[t][1] = -INFINITY;
       l[t][0] = l[t][1] = 0.f;
     }
@@ -444,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
         return static_cast<int>(__reduce_max_sync(0xffffffffu, max(t & 0xFFu, (t >> 8) & 0xFFu)));
       };
       mbar_wait(bar_k, phase & 1, &sh_abort, &g_err_kv4attn, 47);
-      float s[NT][MS][4];
+      float s[T8][MS][4];
       float f_tile = 0.f;
       if (any) {
         const int top_k = top_scale(ks + kCodeBytes);
@@ -481,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
             m1[x] = h2(pack_half2(a1, a1));
           }
 #pragma unroll
-          for (int t = 0; t < NT; ++t) s[t][ms][0] = s[t][ms][1] = s[t][ms][2] = s[t][ms][3] = 0.f;
+          for (int t = 0; t < T8; ++t) s[t][ms][0] = s[t][ms][1] = s[t][ms][2] = s[t][ms][3] = 0.f;
 #pragma unroll
           for (int w = 0; w < kKW; ++w) {  // a word: 8 dims, two k-steps
             uint32_t h0[4], h1[4];
@@ -493,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
               const uint32_t af[4] = {u32(__hmul2(h2(h0[2 * k]), m0[x])), u32(__hmul2(h2(h1[2 * k]), m1[x])),
                                       u32(__hmul2(h2(h0[2 * k + 1]), m0[x])), u32(__hmul2(h2(h1[2 * k + 1]), m1[x]))};
 #pragma unroll
-              for (int t = 0; t < NT; ++t) mma_f16(s[t][ms], af, qf[t][2 * w + k][0], qf[t][2 * w + k][1]);
+              for (int t = 0; t < T8; ++t) mma_f16(s[t][ms], af, qf[t][2 * w + k][0], qf[t][2 * w + k][1]);
             }
           }
         }
@@ -510,16 +519,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
         const int new_v = max(ref_v, top_v);
         const float fv = ref_v == new_v ? 1.f : pow2i(ref_v - new_v);
         ref_v = new_v;
-        uint32_t pb[NT][MS][2];
+        uint32_t pb[T8][MS][2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
+        for (int t = 0; t < T8; ++t) {
           float mx[2] = {-INFINITY, -INFINITY};
-          const float f[2] = {f_row[t][0] * f_tile, f_row[t][1] * f_tile};
+          float f[2] = {f_row[t][0] * f_tile, f_row[t][1] * f_tile};
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (f[h] < 1e-37f) f[h] = 1e-37f;  // not 0, for masked scores (-infinity) times it
 #pragma unroll
           for (int ms = 0; ms < MS; ++ms)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              s[t][ms][x] *= f[x & 1];
               if (!whole) {
                 const int tok = tok0 + ms * 16 + ((n & 1) ? 4 + ((n >> 1) ^ 1) : (n >> 1)) + (x >> 1) * 8;
                 if (tok > pos[t][x & 1] || tok <= pos[t][x & 1] - win) s[t][ms][x] = -INFINITY;
@@ -532,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 4));
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 8));
             mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 16));
-            const float mn = fmaxf(m[t][h], mx[h]);
+            const float mn = fmaxf(m[t][h], mx[h] * f[h]);
             const float mu = mn == -INFINITY ? 0.f : mn;
             al[h] = ex2(m[t][h] - mu);
             base[h] = 15.f - mu;
@@ -542,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
           }
           if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
 #pragma unroll
-            for (int i2 = 0; i2 < KS; ++i2) {
+            for (int i2 = 0; i2 < KO; ++i2) {
               o[t][i2][0] *= al[0];
               o[t][i2][1] *= al[1];
               o[t][i2][2] *= al[0];
@@ -554,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
             float e[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              e[x] = ex2(s[t][ms][x] + base[x & 1]);
+              e[x] = ex2(fmaf(s[t][ms][x], f[x & 1], base[x & 1]));
               l[t][x & 1] += e[x];
             }
             pb[t][ms][0] = movmatrix_trans(pack_half2(e[0], e[1]));
@@ -593,13 +604,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
               const float z = byte_scale((x ? z1 : z0)[(ms * 2 + e8) * 8 * kSB]) * fr;
               sc[x] = h2(pack_half2(z, z));
             }
-            uint32_t be[NT][2], bo[NT][2];
+            uint32_t be[T8][2], bo[T8][2];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              be[t][0] = pb[t][ms][e8] & 0xFFFFu;
-              bo[t][0] = pb[t][ms][e8] << 16;
-              be[t][1] = pb[t][ms][e8] >> 16;
-              bo[t][1] = pb[t][ms][e8] & 0xFFFF0000u;
+            for (int t = 0; t < T8; ++t) {
+              if constexpr (kTwin) {  // rows 0 .. 3 at the even places, their copies at the odd ones
+                be[t][0] = __byte_perm(pb[t][ms][e8], 0u, n < 4 ? 0x4410u : 0x1044u);
+                be[t][1] = __byte_perm(pb[t][ms][e8], 0u, n < 4 ? 0x4432u : 0x3244u);
+              } else {
+                be[t][0] = pb[t][ms][e8] & 0xFFFFu;
+                bo[t][0] = pb[t][ms][e8] << 16;
+                be[t][1] = pb[t][ms][e8] >> 16;
+                bo[t][1] = pb[t][ms][e8] & 0xFFFF0000u;
+              }
             }
 #pragma unroll
             for (int x = 0; x < kVW; ++x) {
@@ -611,9 +627,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
                 const uint32_t af[4] = {u32(__hmul2(h2(ha[2 * y]), sc[0])), u32(__hmul2(h2(ha[2 * y + 1]), sc[0])),
                                         u32(__hmul2(h2(hb[2 * y]), sc[1])), u32(__hmul2(h2(hb[2 * y + 1]), sc[1]))};
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                  mma_f16(o[t][2 * (2 * x + y)], af, be[t][0], be[t][1]);
-                  mma_f16(o[t][2 * (2 * x + y) + 1], af, bo[t][0], bo[t][1]);
+                for (int t = 0; t < T8; ++t) {
+                  if constexpr (kTwin) {
+                    mma_f16(o[t][2 * x + y], af, be[t][0], be[t][1]);
+                  } else {
+                    mma_f16(o[t][2 * (2 * x + y)], af, be[t][0], be[t][1]);
+                    mma_f16(o[t][2 * (2 * x + y) + 1], af, bo[t][0], bo[t][1]);
+                  }
                 }
               }
             }
@@ -630,14 +650,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     // ---- join the warps
     float(*ml)[2][kRows] = sh_ml[seg & 1];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < T8; ++t)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float x = l[t][h];
         x += __shfl_xor_sync(0xffffffffu, x, 4);
         x += __shfl_xor_sync(0xffffffffu, x, 8);
         x += __shfl_xor_sync(0xffffffffu, x, 16);
-        if (n == 0) {
+        if (n == 0 && t * 8 + 2 * j + h < kRows) {
           ml[warp][0][t * 8 + 2 * j + h] = m[t][h];
           ml[warp][1][t * 8 + 2 * j + h] = x;
         }
@@ -646,10 +666,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     __syncthreads();
     const float f_v = ref_v == 255 ? NAN : 1.f;
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < T8; ++t)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int r = t * 8 + 2 * j + h;
+        const int r = t * 8 + (kTwin ? 2 * (j & 1) : 2 * j) + h;
         float mm = ml[0][0][r];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, ml[w][0][r]);
@@ -657,11 +677,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
         const float f = l[t][h] == 0.f ? 0.f : ex2(m[t][h] - mm) * f_v;
         const float fa = pow2i((ref_v - 155) / 2), fb = pow2i(ref_v - 155 - (ref_v - 155) / 2);
         float* dst = merge + (warp * kRows + r) * kPitch + n * (D / 8);
+        if constexpr (kTwin) {
 #pragma unroll
-        for (int i = 0; i < KS; i += 2)
-          *reinterpret_cast<float4*>(dst + 2 * i) =  // o[i]: even dims, o[i + 1]: odd dims
-              make_float4(o[t][i][h] * f * fa * fb, o[t][i + 1][h] * f * fa * fb, o[t][i][2 + h] * f * fa * fb,
-                          o[t][i + 1][2 + h] * f * fa * fb);
+          for (int i = 0; i < KO; ++i) {  // even dims in columns 0 .. 3, odd dims in 4 .. 7
+            dst[4 * i + (j >> 1)] = o[t][i][h] * f * fa * fb;
+            dst[4 * i + 2 + (j >> 1)] = o[t][i][2 + h] * f * fa * fb;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < KO; i += 2)
+            *reinterpret_cast<float4*>(dst + 2 * i) =  // o[i]: even dims, o[i + 1]: odd dims
+                make_float4(o[t][i][h] * f * fa * fb, o[t][i + 1][h] * f * fa * fb, o[t][i][2 + h] * f * fa * fb,
+                            o[t][i + 1][2 + h] * f * fa * fb);
+        }
       }
     __syncthreads();
     const bool complete = seg_tiles == cur.w.tiles;
@@ -702,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     if (tid == 0 && cur.tile == 0 && !complete) {
       const int64_t end = at + cur.w.tiles;  // the item's last tile + 1
       const int last = static_cast<int>((end * ctas - 1) / units);
-      p.rec[cta] = make_int4(cur.item, cur.b, last, seg > 0);
+      p.rec[cta] = make_int4(cur.head * cur.w.groups + cur.group, cur.b, last, seg > 0);
     }
     done += seg_tiles;
     ++seg;
@@ -827,13 +855,17 @@ rnl_status launch_kv4_attention(const Kv4AttnArgs& x, const rnl_kv4_cache& c, co
   p.G = p.Hq / a.Hkv;
   p.causal = x.causal;
   p.window = static_cast<int>(x.window);
-  // 8 rows an item where the rows that a sequence has on average fit, else 16
+  // 4, 8 or 16 rows an item: the fewest that hold the rows a sequence has on average
   const int64_t rows = (q.n_rows + q.n_seqs - 1) / q.n_seqs * p.G;
-  const bool wide = rows > 8;
   auto go = [&](auto d) {
     constexpr int D = decltype(d)::value;
-    if (c.block == 64) return wide ? launch_split<D, 2, 64>(p, a, dev, s) : launch_split<D, 1, 64>(p, a, dev, s);
-    return wide ? launch_split<D, 2, 32>(p, a, dev, s) : launch_split<D, 1, 32>(p, a, dev, s);
+    if (c.block == 64)
+      return rows <= 4   ? launch_split<D, 0, 64>(p, a, dev, s)
+             : rows <= 8 ? launch_split<D, 1, 64>(p, a, dev, s)
+                         : launch_split<D, 2, 64>(p, a, dev, s);
+    return rows <= 4   ? launch_split<D, 0, 32>(p, a, dev, s)
+           : rows <= 8 ? launch_split<D, 1, 32>(p, a, dev, s)
+                       : launch_split<D, 2, 32>(p, a, dev, s);
   };
   if (a.D == 64) return go(std::integral_constant<int, 64>{});
   if (a.D == 128) return go(std::integral_constant<int, 128>{});
