@@ -465,13 +465,14 @@ void trace_after(cudaStream_t s, const char* name) {
 }
 
 rnl_status read_device_errors(int* site) {
-  unsigned int words[12] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+  unsigned int words[13] = {};
   if (read_clear_error_rowwise(&words[0]) != RNL_OK || read_clear_error_gemm(&words[1]) != RNL_OK ||
       read_clear_error_skinny(&words[2]) != RNL_OK || read_clear_error_pair(&words[3]) != RNL_OK ||
       read_clear_error_norm(&words[4]) != RNL_OK || read_clear_error_selftest(&words[5]) != RNL_OK ||
       read_clear_error_rope(&words[6]) != RNL_OK || read_clear_error_mx(&words[7]) != RNL_OK ||
       read_clear_error_quant(&words[8]) != RNL_OK || read_clear_error_decmma(&words[9]) != RNL_OK ||
-      read_clear_error_kv4cache(&words[10]) != RNL_OK || read_clear_error_kv4attn(&words[11]) != RNL_OK)
+      read_clear_error_kv4cache(&words[10]) != RNL_OK || read_clear_error_kv4attn(&words[11]) != RNL_OK ||
+      read_clear_error_kv4prompt(&words[12]) != RNL_OK)
     return RNL_ERR_LAUNCH;
   for (unsigned int w : words) {
     if (w != 0) {
@@ -535,7 +536,7 @@ size_t rnl_workspace_size(int op, int64_t T, int64_t K, int64_t N, int64_t N2) {
     case RNL_OP_MXFP8: return mx_layout(nullptr, T, K, N).bytes;
     case RNL_OP_KV4_ATTENTION:
       if (!qkv_rope_head_dim_ok(K) || N == 0 || N2 == 0 || N % N2 != 0) return static_cast<size_t>(-1);
-      return round_up(kv4_attn_workspace_bytes(K));
+      return round_up(kv4_attn_workspace_bytes(T, K, N / N2));
     case RNL_OP_QKV_ROPE:
       return bf16_layout(nullptr, T, K, N, RNL_OUT_BF16).bytes + round_up(static_cast<size_t>(T) * N * 2);
   }

@@ -208,7 +208,7 @@ struct Kv4AttnArgs {
   void* ws = nullptr;
   size_t ws_bytes = 0;
 };
-size_t kv4_attn_workspace_bytes(int64_t D);
+size_t kv4_attn_workspace_bytes(int64_t T, int64_t D, int64_t G);
 rnl_status launch_kv4_attention(const Kv4AttnArgs& a, const rnl_kv4_cache& c, const rnl_kv4_seqs& q,
                                 cudaStream_t s);
 
@@ -334,6 +334,7 @@ rnl_status read_clear_error_quant(unsigned int* word);
 rnl_status read_clear_error_decmma(unsigned int* word);
 rnl_status read_clear_error_kv4cache(unsigned int* word);
 rnl_status read_clear_error_kv4attn(unsigned int* word);
+rnl_status read_clear_error_kv4prompt(unsigned int* word);
 // Reads and clears all of them without synchronising (api.cu): RNL_OK, or
 // RNL_ERR_TIMEOUT / RNL_ERR_ARG with the first recorded site in *site
 // (optional).

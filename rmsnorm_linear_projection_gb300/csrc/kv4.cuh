@@ -143,5 +143,73 @@ __device__ __forceinline__ float e8m0_value(uint32_t byte) {
   return __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
 }
 
+// ---- attention (kv4attn.cu, kv4prompt.cu)
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct AttnParams {
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  __nv_bfloat16* out;
+  float* lse;
+  float* part;   // partial sums: 2 slots a CTA
+  int4* rec;     // [CTAs]: the cut item a CTA begins (item, sequence, last CTA), .x = -1: none
+  float scale_log2;
+  int Hq, G;
+  int causal, window;
+  int few;  // sequences of up to this many rows (times G) are the few-row kernel's, the others the prompt kernel's
+};
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+__device__ __forceinline__ __half2 h2(uint32_t a) { return *reinterpret_cast<const __half2*>(&a); }
+__device__ __forceinline__ uint32_t u32(__half2 a) { return *reinterpret_cast<const uint32_t*>(&a); }
+
+// 2^x; results below binary32's normal range become 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 2^(byte - 127) with 0 for byte 0 (and an infinity for 255, E8M0's NaN).
+__device__ __forceinline__ float byte_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// 2^e; the clamp is reached only where what it scales vanishes anyway.
+__device__ __forceinline__ float pow2i(int e) {
+  return __uint_as_float(static_cast<uint32_t>(min(max(e, -126), 127) + 127) << 23);
+}
+// 2^e for |e| up to 250, subnormal or infinite outside binary32's range.
+__device__ __forceinline__ float pow2w(int e) { return pow2i(e / 2) * pow2i(e - e / 2); }
+
+// Eight dims of row r of key head kvh: sums v over weights ll with maximum mm.
+template <int D>
+__device__ __forceinline__ void store_row(const AttnParams& p, const Seq& s, int kvh, int r, int d,
+                                          const float (&v)[8], float mm, float ll) {
+  const int tok = r / p.G;
+  const int64_t row = static_cast<int64_t>(s.row0 + tok) * p.Hq + kvh * p.G + (r - tok * p.G);
+  const float inv = ll != 0.f ? 1.f / ll : 0.f;
+  uint32_t w[4];
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * y] * inv, v[2 * y + 1] * inv);
+    w[y] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(p.out + row * D + d) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (d == 0 && p.lse != nullptr) p.lse[row] = ll != 0.f ? mm * kLn2 + logf(ll) : -INFINITY;
+}
+
+__device__ __forceinline__ int64_t range_start(int64_t units, int c, int n) { return units * c / n; }
+
 }  // namespace kv4
+
+// Sequences of more than p.few rows (kv4prompt.cu), head_dim 64 or 128.
+bool kv4_prompt_fits(int64_t D);
+size_t kv4_prompt_workspace_bytes(int64_t D);
+rnl_status launch_kv4_prompt(const kv4::AttnParams& p, const kv4::Args& a, int block, void* ws,
+                             const DeviceInfo& dev, cudaStream_t s);
+
 }  // namespace rnl

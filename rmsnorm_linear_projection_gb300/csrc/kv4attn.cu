@@ -51,19 +51,6 @@ __device__ unsigned int g_err_kv4attn;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCtas = 640;                              // partial-sum slots in the workspace
-constexpr float kLn2 = 0.6931471805599453f;
-
-struct AttnParams {
-  const __nv_bfloat16* q;
-  int64_t q_stride;
-  __nv_bfloat16* out;
-  float* lse;
-  float* part;   // partial sums: 2 slots a CTA
-  int4* rec;     // [CTAs]: the cut item a CTA begins (item, sequence, last CTA), .x = -1: none
-  float scale_log2;
-  int Hq, G;
-  int causal, window;
-};
 
 // What an item costs a CTA beside its tiles (queries, joining the warps), in
 // tiles: counted when the tiles are dealt out.
@@ -100,32 +87,6 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   return d;
 }
 
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-
-__device__ __forceinline__ __half2 h2(uint32_t a) { return *reinterpret_cast<const __half2*>(&a); }
-__device__ __forceinline__ uint32_t u32(__half2 a) { return *reinterpret_cast<const uint32_t*>(&a); }
-
-// 2^x; results below binary32's normal range become 0.
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// 2^(byte - 127) with 0 for byte 0 (and an infinity for 255, E8M0's NaN).
-__device__ __forceinline__ float byte_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
-
-// 2^e; the clamp is reached only where what it scales vanishes anyway.
-__device__ __forceinline__ float pow2i(int e) {
-  return __uint_as_float(static_cast<uint32_t>(min(max(e, -126), 127) + 127) << 23);
-}
-// 2^e for |e| up to 250, subnormal or infinite outside binary32's range.
-__device__ __forceinline__ float pow2w(int e) { return pow2i(e / 2) * pow2i(e - e / 2); }
-
 // What of a sequence the call's rows read, in tiles.
 struct Span {
   Seq s;
@@ -136,7 +97,7 @@ struct Span {
 template <int D, int NT>
 __device__ __forceinline__ bool load_span(const Args& a, const AttnParams& p, int b, Span& w) {
   constexpr int TT = Cfg<D, NT>::TT;
-  if (!load_seq(a, b, w.s, &g_err_kv4attn, 45) || w.s.rows == 0) return false;
+  if (!load_seq(a, b, w.s, &g_err_kv4attn, 45) || w.s.rows == 0 || w.s.rows * p.G > p.few) return false;
   w.groups = (w.s.rows * p.G + Cfg<D, NT>::kRows - 1) / Cfg<D, NT>::kRows;
   w.lo = 0;
   w.hi = w.s.len;
@@ -178,25 +139,6 @@ __device__ __forceinline__ void skip(const Args& a, const AttnParams& p, Cursor&
     }
   }
 }
-
-// Eight dims of row r of key head kvh: sums v over weights ll with maximum mm.
-template <int D>
-__device__ __forceinline__ void store_row(const AttnParams& p, const Seq& s, int kvh, int r, int d,
-                                          const float (&v)[8], float mm, float ll) {
-  const int tok = r / p.G;
-  const int64_t row = static_cast<int64_t>(s.row0 + tok) * p.Hq + kvh * p.G + (r - tok * p.G);
-  const float inv = ll != 0.f ? 1.f / ll : 0.f;
-  uint32_t w[4];
-#pragma unroll
-  for (int y = 0; y < 4; ++y) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * y] * inv, v[2 * y + 1] * inv);
-    w[y] = *reinterpret_cast<const uint32_t*>(&b);
-  }
-  *reinterpret_cast<uint4*>(p.out + row * D + d) = make_uint4(w[0], w[1], w[2], w[3]);
-  if (d == 0 && p.lse != nullptr) p.lse[row] = ll != 0.f ? mm * kLn2 + logf(ll) : -INFINITY;
-}
-
-__device__ __forceinline__ int64_t range_start(int64_t units, int c, int n) { return units * c / n; }
 
 template <int D, int NT, int BS>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
@@ -832,9 +774,18 @@ rnl_status launch_split(const AttnParams& p, const Args& a, const DeviceInfo& de
 
 }  // namespace
 
-size_t kv4_attn_workspace_bytes(int64_t D) {
+namespace {
+constexpr int kFewRows = 32;  // rows of a sequence (times G) up to which this file's kernel takes it
+size_t few_workspace_bytes(int64_t D) {
   const size_t slot = static_cast<size_t>(16) * (static_cast<size_t>(D) + 2) * 4;  // NT = 2
-  return kMaxCtas * (sizeof(int4) + 2 * slot);
+  return (kMaxCtas * (sizeof(int4) + 2 * slot) + 255) / 256 * 256;
+}
+// Whether some sequence may have more than kFewRows rows.
+bool may_prompt(int64_t T, int64_t G, int64_t D) { return T * G > kFewRows && kv4_prompt_fits(D); }
+}  // namespace
+
+size_t kv4_attn_workspace_bytes(int64_t T, int64_t D, int64_t G) {
+  return few_workspace_bytes(D) + (may_prompt(T, G, D) ? kv4_prompt_workspace_bytes(D) : 0);
 }
 
 rnl_status launch_kv4_attention(const Kv4AttnArgs& x, const rnl_kv4_cache& c, const rnl_kv4_seqs& q,
@@ -855,6 +806,13 @@ rnl_status launch_kv4_attention(const Kv4AttnArgs& x, const rnl_kv4_cache& c, co
   p.G = p.Hq / a.Hkv;
   p.causal = x.causal;
   p.window = static_cast<int>(x.window);
+  p.few = 0x7fffffff;
+  if (q.cu_rows != nullptr && may_prompt(q.n_rows, p.G, a.D)) {
+    p.few = kFewRows;
+    const rnl_status pst = launch_kv4_prompt(p, a, static_cast<int>(c.block),
+                                             static_cast<char*>(x.ws) + few_workspace_bytes(a.D), dev, s);
+    if (pst != RNL_OK) return pst;
+  }
   // 4, 8 or 16 rows an item: the fewest that hold the rows a sequence has on average
   const int64_t rows = (q.n_rows + q.n_seqs - 1) / q.n_seqs * p.G;
   auto go = [&](auto d) {

@@ -1,0 +1,810 @@
+// kv4prompt.cu -- attention over the 4-bit paged KV cache for sequences with
+// many rows in the call (prompts, chunks of prompts, cross attention), on the
+// fifth-generation tensor cores.  The formulas, operands and scales are those
+// of kv4attn.cu: E2M1 values times 2^(X - R + 13) in binary16, where R is the
+// tile's largest scale (keys) or the largest so far (values), exact down to
+// 2^-37 of it; queries scaled by a power of two per row.
+//
+// A CTA works on 256 rows (token x query head of one key head), two tiles of
+// 128, against 128 tokens at a time:
+//   warps 0-3, 4-7   softmax of the two row tiles, a thread a row: scores from
+//                    TMEM, running maximum and sum, weights back to TMEM as
+//                    binary16 (the A operand of the second product), the sums
+//                    rescaled there when the maximum grew by more than 2^8
+//   warps 8-11       a thread a token: codes of the next tile from global
+//                    memory to registers, converted and scaled into shared
+//                    memory (128-byte swizzle; keys K-major, values MN-major,
+//                    the same bytes in the same order)
+//   warp 12          TMEM allocation and, on one thread, every tcgen05.mma:
+//                    S_i = Q_i K^T (both from shared memory), O_i += P_i V
+//                    (P_i from TMEM), i = 0, 1 in turn, so that one row tile's
+//                    softmax runs while the other one's products do
+// TMEM: S_0, S_1 (128 columns each; P_i takes the first 64 of S_i), O_0, O_1.
+//
+// The weights are 2^(x - m + 7) with m at most 2^8 behind the true maximum:
+// binary16 holds them with 11 bits down to 2^-21 of the largest.
+//
+// Rows later in a causal prompt read more tokens.  An item is a pair of row
+// groups, one from either end, so that all items of a sequence have about the
+// same number of tiles; the tiles of all items are dealt to the CTAs in equal
+// contiguous ranges.  A group that is cut leaves FP32 partial sums, joined by
+// a dependent kernel.
+#include <algorithm>
+#include <type_traits>
+
+#include "kv4.cuh"
+
+namespace rnl {
+namespace {
+
+using namespace kv4;
+
+__device__ unsigned int g_err_kv4prompt;
+
+constexpr int kT = 128;            // tokens a tile
+constexpr int kGroup = 256;        // rows a CTA holds
+constexpr int kSoftWarps = 8;
+constexpr int kFillWarps = 4;
+constexpr int kMmaWarp = kSoftWarps + kFillWarps;
+constexpr int kPThreads = (kMmaWarp + 1) * 32;
+constexpr int kPWarps = kMmaWarp + 1;
+// what a group costs beside its tiles (queries, output), in tiles
+constexpr int kGroupCost = 3;
+constexpr int kMaxPromptCtas = 160;
+constexpr float kLag = 8.f;        // log2 of how far the maximum may run ahead of the one in use
+constexpr float kTop = 7.f;        // weights are scaled by 2^7: at most 2^15 with the lag
+
+template <int D>
+struct PCfg {
+  static constexpr uint32_t kTileBytes = 128u * D * 2;    // Q_i, K or V in shared memory
+  static constexpr uint32_t kHalf = 128u * 128;           // bytes between blocks of 64 dims
+  static constexpr size_t kSmem = 1024 + 6 * static_cast<size_t>(kTileBytes);
+  static constexpr int kSlot = kGroup * (D + 2);          // floats of a partial: sums, maxima, weights
+};
+
+struct __align__(8) PCtrl {
+  uint64_t q_full[2], s_full[2], p_full[2];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  float k_info[4];   // score factor of tile x at x % 4
+  int v_info[4];     // the values' reference scale byte
+  int top[2][kFillWarps];
+  long long sum[kPWarps];
+  long long off;
+  uint32_t tmem;
+  int b, abort;
+};
+
+// A group's tokens in tiles.
+struct Span {
+  Seq s;
+  int groups;
+};
+__device__ __forceinline__ bool load_span(const Args& a, const AttnParams& p, int b, Span& w) {
+  if (!load_seq(a, b, w.s, &g_err_kv4prompt, 48) || w.s.rows * p.G <= p.few) return false;
+  w.groups = (w.s.rows * p.G + kGroup - 1) / kGroup;
+  return true;
+}
+__device__ __forceinline__ void group_tokens(const AttnParams& p, const Seq& s, int g, int& lo, int& hi) {
+  lo = 0;
+  hi = s.len;
+  if (p.causal) {
+    const int last = min((g + 1) * kGroup, s.rows * p.G) - 1;
+    hi = max(0, s.len - s.rows + last / p.G + 1);
+    if (p.window > 0) lo = max(0, s.len - s.rows + g * kGroup / p.G + 1 - p.window);
+  }
+}
+__device__ __forceinline__ int tiles_between(int lo, int hi) {
+  return hi > lo ? (hi + kT - 1) / kT - lo / kT : 1;  // at least one: rows without a token still get zeros
+}
+__device__ __forceinline__ int group_tiles(const AttnParams& p, const Seq& s, int g) {
+  int lo, hi;
+  group_tokens(p, s, g, lo, hi);
+  return tiles_between(lo, hi);
+}
+// Units of a pair of groups: at least both groups' tiles and costs.  Causal
+// rows: the first group and the last, were it full; with a window also at most
+// twice the tiles that a window and a group's tokens can touch.
+__device__ __forceinline__ int pair_units(const AttnParams& p, const Span& w) {
+  int t;
+  if (p.causal) {
+    const int hi = max(0, w.s.len - w.s.rows + (w.groups * kGroup - 1) / p.G + 1);
+    const int last = min((w.groups > 1 ? 1 : w.groups) * kGroup, w.s.rows * p.G) - 1;
+    const int first = max(0, w.s.len - w.s.rows + last / p.G + 1);
+    t = tiles_between(0, first) + tiles_between(0, hi) + 3;
+    if (p.window > 0) t = min(t, 2 * ((p.window + (kGroup - 1) / p.G + 1 + 2 * kT - 2) / kT) + 1);
+  } else {
+    t = 2 * tiles_between(0, w.s.len);
+  }
+  return t + 2 * kGroupCost;
+}
+
+// Walks a CTA's range: next() gives its next run of one group's tiles.
+struct Walk {
+  int b, head, pair, off;  // place: units into the pair's item
+  int64_t at, left;        // of the range's units: where, and how many are left
+  Span w;
+  // the run
+  int group, lo, hi;       // tokens of the group
+  int tile, n, all;        // first tile in the group, tiles, tiles of the group
+  int64_t unit;            // where the run's first tile stands
+  int seq, kvh;
+};
+__device__ __forceinline__ bool next_run(const Args& a, const AttnParams& p, Walk& c) {
+  while (c.left > 0) {
+    const int g0 = c.w.groups - 1 - c.pair, g1 = c.pair;
+    const int n0 = group_tiles(p, c.w.s, g0), n1 = g1 < g0 ? group_tiles(p, c.w.s, g1) : 0;
+    const int z0 = kGroupCost + n0, z1 = g1 < g0 ? kGroupCost + n1 : 0;
+    if (c.off < z0 + z1) {
+      const bool second = c.off >= z0;
+      int o = second ? c.off - z0 : c.off;
+      if (o < kGroupCost) {
+        const int d = kGroupCost - o;
+        c.left -= d;
+        c.at += d;
+        c.off += d;
+        o = kGroupCost;
+        if (c.left <= 0) return false;
+      }
+      c.group = second ? g1 : g0;
+      c.all = second ? n1 : n0;
+      c.tile = o - kGroupCost;
+      c.n = static_cast<int>(min(static_cast<int64_t>(c.all - c.tile), c.left));
+      if (c.n <= 0) return false;
+      group_tokens(p, c.w.s, c.group, c.lo, c.hi);
+      c.unit = c.at;
+      c.seq = c.b;
+      c.kvh = c.head;
+      c.left -= c.n;
+      c.at += c.n;
+      c.off += c.n;
+      return true;
+    }
+    const int rest = max(pair_units(p, c.w) - c.off, 0);
+    c.left -= rest;
+    c.at += rest;
+    c.off = 0;
+    if (++c.pair == (c.w.groups + 1) / 2) {
+      c.pair = 0;
+      if (++c.head == a.Hkv) {
+        c.head = 0;
+        if (c.left <= 0) return false;
+        do {
+          if (++c.b >= a.n_seqs) {
+            c.left = 0;
+            return false;
+          }
+        } while (!load_span(a, p, c.b, c.w));
+      }
+    }
+  }
+  return false;
+}
+
+// Shared-memory descriptor of an MN-major operand with 128-byte swizzle: rows
+// (of k) of 64 elements, 8-row groups 1024 bytes apart, blocks of 64 elements
+// `lbo` bytes apart.
+__device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(lbo >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+// kind::f16, binary16 A and B, fp32 accumulator of M x N; B MN-major if asked.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+// A from TMEM (binary16 pairs, lane = row), B from shared memory.
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_32cols(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// Where 16-byte chunk c (8 dims) of row r of a 128-row operand lies: blocks of
+// 64 dims, rows of 128 bytes, chunks permuted by row % 8.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  return static_cast<uint32_t>(c >> 3) * PCfg<D>::kHalf + static_cast<uint32_t>(r) * 128u +
+         static_cast<uint32_t>(((c & 7) ^ (r & 7)) << 4);
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
+// A token's scale bytes (D / BS of them) in one word.
+template <int N>
+__device__ __forceinline__ uint32_t load_scales(const uint8_t* p) {
+  if constexpr (N == 4) return __ldg(reinterpret_cast<const uint32_t*>(p));
+  else if constexpr (N == 2) return __ldg(reinterpret_cast<const uint16_t*>(p));
+  else return __ldg(p);
+}
+
+template <int D, int BS>
+__global__ void __launch_bounds__(kPThreads, 1)
+    kv4_prompt_kernel(const Args a, const AttnParams p) {
+  using C = PCfg<D>;
+  constexpr int kSB = D / BS;
+  constexpr uint32_t kTileBytes = C::kTileBytes;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ PCtrl ctrl;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sq = base, sk = base + 2 * kTileBytes, sv = base + 4 * kTileBytes;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  volatile int* abort = &ctrl.abort;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ctrl.q_full[i]), 4);
+      mbar_init(smem_u32(&ctrl.s_full[i]), 1);
+      mbar_init(smem_u32(&ctrl.p_full[i]), 4);
+      mbar_init(smem_u32(&ctrl.k_full[i]), kFillWarps);
+      mbar_init(smem_u32(&ctrl.k_empty[i]), 1);
+      mbar_init(smem_u32(&ctrl.v_full[i]), kFillWarps);
+      mbar_init(smem_u32(&ctrl.v_empty[i]), 1);
+    }
+    ctrl.abort = 0;
+    ctrl.b = -1;
+    fence_mbar_init();
+  }
+  // ---- this CTA's range (as kv4attn.cu, units of this kernel)
+  auto units_of = [&](int b) -> long long {
+    Span w;
+    if (b >= a.n_seqs || !load_span(a, p, b, w)) return 0;
+    return static_cast<long long>(pair_units(p, w)) * ((w.groups + 1) / 2) * a.Hkv;
+  };
+  long long sum = 0;
+  for (int b = tid; b < a.n_seqs; b += kPThreads) sum += units_of(b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) ctrl.sum[warp] = sum;
+  __syncthreads();
+  long long units = 0;
+  for (int i = 0; i < kPWarps; ++i) units += ctrl.sum[i];
+  const int cta = blockIdx.x;
+  const int ctas =
+      static_cast<int>(min(static_cast<long long>(gridDim.x), (units + kGroupCost) / (1 + kGroupCost)));
+  grid_launch_dependents();
+  if (tid == 0) p.rec[cta] = make_int4(-1, 0, 0, 0);
+  if (cta >= ctas) return;  // the whole CTA
+  const int64_t u0 = range_start(units, cta, ctas), u1 = range_start(units, cta + 1, ctas);
+  long long before = 0;
+  for (int start = 0; start < a.n_seqs; start += kPThreads) {
+    const long long u = units_of(start + tid);
+    long long inc = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    __syncthreads();
+    if (lane == 31) ctrl.sum[warp] = inc;
+    __syncthreads();
+    for (int i = 0; i < warp; ++i) inc += ctrl.sum[i];
+    long long all = 0;
+    for (int i = 0; i < kPWarps; ++i) all += ctrl.sum[i];
+    inc += before;
+    if (u0 >= inc - u && u0 < inc) {
+      ctrl.b = start + tid;
+      ctrl.off = u0 - (inc - u);
+    }
+    __syncthreads();
+    if (ctrl.b >= 0) break;
+    before += all;
+  }
+  if (ctrl.b < 0) return;  // lengths changed under the call
+  Walk walk;
+  walk.b = ctrl.b;
+  load_span(a, p, walk.b, walk.w);
+  {
+    const int len = pair_units(p, walk.w), pairs = (walk.w.groups + 1) / 2;
+    const int item = static_cast<int>(ctrl.off / len);
+    walk.off = static_cast<int>(ctrl.off - static_cast<long long>(item) * len);
+    walk.head = item / pairs;
+    walk.pair = item - walk.head * pairs;
+    walk.at = u0;
+    walk.left = u1 - u0;
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&ctrl.tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctrl.tmem;
+
+  if (warp < kSoftWarps) {
+    // ------------------------------------------------------------- softmax
+    const int i = warp >> 2;                    // row tile
+    const int rw = (warp & 3) * 32 + lane;      // row in it
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + i * 128, to = tmem + lanes + 256 + i * D;
+    const uint32_t q_full = smem_u32(&ctrl.q_full[i]), s_full = smem_u32(&ctrl.s_full[i]),
+                   p_full = smem_u32(&ctrl.p_full[i]);
+    uint32_t s_phase = 0;
+    int count = 0;  // tiles so far
+    // a wait that gives up (a bug) ends every later wait at once: the loops run
+    // on to their ends, so that the warp-wide instructions stay together
+    for (int run = 0; next_run(a, p, walk); ++run) {
+      const int all_rows = walk.w.s.rows * p.G, r0 = walk.group * kGroup;
+      if (r0 + i * 128 >= all_rows) {  // no row of this tile
+        count += walk.n;
+        continue;
+      }
+      const int r = r0 + i * 128 + rw;
+      const int rc = min(r, all_rows - 1), tok_q = rc / p.G;
+      const int pos = p.causal ? walk.w.s.len - walk.w.s.rows + tok_q : walk.w.s.len - 1;
+      const int first = p.window > 0 ? pos - p.window + 1 : 0;  // first token the row reads
+      float f_row;
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (walk.w.s.row0 + tok_q) * p.q_stride +
+                                                          static_cast<int64_t>(walk.kvh * p.G + (rc - tok_q * p.G)) * D);
+        uint4 w[D / 8];
+        uint32_t am = 0;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) w[c] = __ldg(src + c);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) am = max(am, max((x[y] << 16) & 0x7FFFFFFFu, x[y] & 0x7FFF0000u));
+        }
+        const int e = 141 - max(static_cast<int>(am >> 23), 1);
+        const float s1 = p.scale_log2 < 0.f ? -pow2i(e / 2) : pow2i(e / 2), s2 = pow2i(e - e / 2);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+          uint32_t h[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            h[y] = pack_half2(__uint_as_float(x[y] << 16) * s1 * s2, __uint_as_float(x[y] & 0xFFFF0000u) * s1 * s2);
+          st_shared16(sq + i * kTileBytes + chunk_at<D>(rw, c), h[0], h[1], h[2], h[3]);
+        }
+        f_row = fabsf(p.scale_log2) * pow2w(-e);
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+
+      float m = -INFINITY, l = 0.f;
+      int ref_v = 13;
+      for (int k = 0; k < walk.n; ++k, ++count) {
+        mbar_wait(s_full, s_phase, abort, &g_err_kv4prompt, 49);
+        __syncwarp();
+        s_phase ^= 1u;
+        tc_fence_after();
+        float f = f_row * ctrl.k_info[count & 3];
+        if (f < 1e-37f) f = 1e-37f;  // not 0, for masked scores (-infinity) times it
+        const int new_v = ctrl.v_info[count & 3];
+        const int tok0 = (walk.lo / kT + walk.tile + k) * kT;
+        const bool whole = __all_sync(0xffffffffu, tok0 + kT - 1 <= pos && tok0 >= first);
+        // maximum of the row's scores
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        uint32_t s[2][32];
+        tmem_ld_32cols(ts, s[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld_wait();
+          if (c < 3) tmem_ld_32cols(ts + 32 * (c + 1), s[(c + 1) & 1]);
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            float v = __uint_as_float(s[c & 1][x]);
+            if (!whole) {
+              const int tok = tok0 + 32 * c + x;
+              if (tok > pos || tok < first) v = -INFINITY;
+            }
+            mx[x & 3] = fmaxf(mx[x & 3], v);
+          }
+        }
+        tmem_ld_32cols(ts, s[0]);  // for the second pass
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
+        float alpha = 1.f;
+        if (top > m + kLag || (m == -INFINITY && top > m)) {
+          alpha = ex2(m - top);
+          m = top;
+          l *= alpha;
+        }
+        if (new_v != ref_v) {
+          alpha *= pow2i(ref_v - new_v);
+          ref_v = new_v;
+        }
+        const float bias = kTop - (m == -INFINITY ? 0.f : m);
+        // weights, 32 tokens at a time, into the columns whose scores are read
+        float la = 0.f, lb = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld_wait();
+          if (c < 3) tmem_ld_32cols(ts + 32 * (c + 1), s[(c + 1) & 1]);
+          uint32_t h[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            float e0 = ex2(fmaf(__uint_as_float(s[c & 1][2 * x]), f, bias));
+            float e1 = ex2(fmaf(__uint_as_float(s[c & 1][2 * x + 1]), f, bias));
+            if (!whole) {
+              const int tok = tok0 + 32 * c + 2 * x;
+              if (tok > pos || tok < first) e0 = 0.f;
+              if (tok + 1 > pos || tok + 1 < first) e1 = 0.f;
+            }
+            la += e0;
+            lb += e1;
+            h[x] = pack_half2(e0, e1);
+          }
+          tmem_st_16cols(ts + 16 * c, h);
+        }
+        l += la + lb;
+        // the sums so far, rescaled (the products before are done: this
+        // tile's scores came after them)
+        if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            tmem_ld_32cols(to + 32 * c, s[0]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) s[0][x] = __float_as_uint(__uint_as_float(s[0][x]) * alpha);
+            tmem_st_32cols(to + 32 * c, s[0]);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+      }
+      mbar_wait(s_full, s_phase, abort, &g_err_kv4prompt, 50);
+      __syncwarp();
+      s_phase ^= 1u;
+      tc_fence_after();
+      // sums stand for value * 2^(ref_v - 127 - 13), weights and sums both times 2^7
+      const bool complete = walk.n == walk.all;
+      const float inv = complete ? (l != 0.f ? 1.f / l : 0.f) : 1.f / 128.f;
+      const float fa = pow2i((ref_v - 140) / 2), fb = pow2i(ref_v - 140 - (ref_v - 140) / 2) * (ref_v == 255 ? NAN : 1.f);
+      const int64_t orow = static_cast<int64_t>(walk.w.s.row0 + tok_q) * p.Hq + walk.kvh * p.G + (rc - tok_q * p.G);
+      float* slot = p.part + static_cast<int64_t>(2 * cta + (run > 0)) * C::kSlot;
+      const int rg = i * 128 + rw;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t s[32];
+        tmem_ld_32cols(to + 32 * c, s);
+        tmem_ld_wait();
+        float v[32];
+#pragma unroll
+        for (int x = 0; x < 32; ++x) v[x] = __uint_as_float(s[x]) * inv * fa * fb;
+        if (r < all_rows) {
+          if (complete) {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + 32 * c);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              uint32_t w[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[8 * y + 2 * x], v[8 * y + 2 * x + 1]);
+                w[x] = *reinterpret_cast<const uint32_t*>(&b2);
+              }
+              dst[y] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+            float4* dst = reinterpret_cast<float4*>(slot + rg * D + 32 * c);
+#pragma unroll
+            for (int y = 0; y < 8; ++y) dst[y] = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
+          }
+        }
+      }
+      tc_fence_before();  // the next run's products overwrite these sums
+      if (r < all_rows) {
+        const float lt = l * (1.f / 128.f);
+        if (complete) {
+          if (p.lse != nullptr) p.lse[orow] = lt != 0.f ? m * kLn2 + logf(lt) : -INFINITY;
+        } else {
+          slot[kGroup * D + rg] = m;
+          slot[kGroup * D + kGroup + rg] = lt;
+        }
+      }
+      // a group that begins here and goes on in later CTAs
+      if (i == 0 && rw == 0 && walk.tile == 0 && !complete) {
+        const int64_t end = walk.unit + walk.all;
+        p.rec[cta] = make_int4(walk.kvh * walk.w.groups + walk.group, walk.seq,
+                               static_cast<int>((end * ctas - 1) / units), run > 0);
+      }
+    }
+  } else if (warp < kMmaWarp) {
+    // ---------------------------------------------- codes to binary16 tiles
+    const int tk = tid - kSoftWarps * 32;  // token in the tile
+    const int fw = warp - kSoftWarps;
+    struct Raw {
+      uint4 k[D / 32], v[D / 32];
+      uint32_t ks, vs;
+    };
+    Walk it = walk;
+    int k_it = -1;
+    bool more = next_run(a, p, it);
+    // the place of the token of the iterator's next tile
+    int page = -2, off = 0, head = 0;
+    bool have = false;
+    bool first_tile = false;
+    auto step = [&]() {  // looks the token's page up
+      have = false;
+      if (!more) return;
+      if (++k_it >= it.n) {
+        k_it = 0;
+        more = next_run(a, p, it);
+        if (!more) return;
+      }
+      have = true;
+      first_tile = k_it == 0;
+      const int tok = (it.lo / kT + it.tile + k_it) * kT + tk;
+      page = -2;
+      if (tok >= it.lo && tok < it.hi && tok < it.w.s.len) {
+        page = __ldg(a.table + static_cast<int64_t>(it.seq) * a.max_pages + (tok >> a.page_shift));
+        off = tok & (a.page - 1);
+        head = it.kvh;
+      }
+    };
+    auto load = [&](Raw& raw) {
+      raw.ks = raw.vs = 0;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) raw.k[c] = raw.v[c] = make_uint4(0, 0, 0, 0);
+      if (page >= 0 && page < a.n_pages) {
+        const int64_t row = ((static_cast<int64_t>(page) * a.Hkv + head) << a.page_shift) + off;
+        const uint4* pk = reinterpret_cast<const uint4*>(a.k.codes + row * (D / 2));
+        const uint4* pv = reinterpret_cast<const uint4*>(a.v.codes + row * (D / 2));
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          raw.k[c] = __ldg(pk + c);
+          raw.v[c] = __ldg(pv + c);
+        }
+        raw.ks = load_scales<kSB>(a.k.scales + row * kSB);
+        raw.vs = load_scales<kSB>(a.v.scales + row * kSB);
+      } else if (page != -2) {
+        atomicCAS(&g_err_kv4prompt, 0u, kErrArg | (51u << 8));
+      }
+    };
+    // a token's row into a tile: word by word 8 codes, one 16-byte chunk
+    auto put = [&](uint32_t tile, const uint4 (&x)[D / 32], uint32_t scales, float fr) {
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+        const float z = byte_scale((scales >> (8 * (c * 32 / BS))) & 0xFFu) * fr;
+        const __half2 m2 = h2(pack_half2(z, z));
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          uint32_t h[4];
+          e2m1x8_to_half(w[y], h);
+          st_shared16(tile + chunk_at<D>(tk, 4 * c + y), u32(__hmul2(h2(h[0]), m2)), u32(__hmul2(h2(h[1]), m2)),
+                      u32(__hmul2(h2(h[2]), m2)), u32(__hmul2(h2(h[3]), m2)));
+        }
+      }
+    };
+    auto top_of = [](uint32_t w) {
+      uint32_t t = 0;
+#pragma unroll
+      for (int x = 0; x < kSB; ++x) t = max(t, (w >> (8 * x)) & 0xFFu);
+      return t;
+    };
+    Raw raw;
+    step();
+    bool now = have, now_first = first_tile;
+    load(raw);
+    step();
+    int ref_v = 13;
+    for (int count = 0; now; ++count) {
+      const int stage = count & 1;
+      const uint32_t parity = ((count >> 1) & 1) ^ 1u;
+      // the tile's largest scales, over the four warps
+      const uint32_t tk_ = __reduce_max_sync(0xffffffffu, top_of(raw.ks));
+      const uint32_t tv_ = __reduce_max_sync(0xffffffffu, top_of(raw.vs));
+      if (lane == 0) ctrl.top[stage][fw] = static_cast<int>(tk_ | (tv_ << 8));
+      asm volatile("bar.sync 1, %0;" ::"n"(kFillWarps * 32) : "memory");
+      int top_k = 0, top_v = 0;
+#pragma unroll
+      for (int x = 0; x < kFillWarps; ++x) {
+        top_k = max(top_k, ctrl.top[stage][x] & 0xFF);
+        top_v = max(top_v, ctrl.top[stage][x] >> 8);
+      }
+      const int ref_k = max(top_k, 13);
+      ref_v = max(now_first ? 13 : ref_v, top_v);
+      if (tk == 0) {
+        ctrl.k_info[count & 3] = top_k == 255 ? NAN : pow2w(ref_k - 140);
+        ctrl.v_info[count & 3] = ref_v;
+      }
+      mbar_wait(smem_u32(&ctrl.k_empty[stage]), parity, abort, &g_err_kv4prompt, 52);
+      put(sk + stage * kTileBytes, raw.k, raw.ks, pow2i(140 - ref_k));
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctrl.k_full[stage]));
+      mbar_wait(smem_u32(&ctrl.v_empty[stage]), parity, abort, &g_err_kv4prompt, 53);
+      put(sv + stage * kTileBytes, raw.v, raw.vs, pow2i(140 - ref_v));
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctrl.v_full[stage]));
+      now = have;
+      now_first = first_tile;
+      if (now) {
+        load(raw);
+        step();
+      }
+    }
+  } else if (lane == 0) {
+    // ------------------------------------------------------------ products
+    constexpr uint32_t kDescQK = idesc_f16(128, kT, false), kDescPV = idesc_f16(128, D, true);
+    int count = 0;                       // tiles so far
+    uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+      ok = ok && mbar_wait(smem_u32(bar), parity, abort, &g_err_kv4prompt, site);
+      return ok;
+    };
+    auto scores = [&](int i, int stage) {
+      const uint64_t qd = desc_kmajor_sw128(sq + i * kTileBytes), kd = desc_kmajor_sw128(sk + stage * kTileBytes);
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        const uint64_t step = (static_cast<uint64_t>(x >> 2) * C::kHalf + (x & 3) * 32) >> 4;
+        umma_bf16(tmem + i * 128, qd + step, kd + step, kDescQK, x > 0);
+      }
+    };
+    auto sums = [&](int i, int stage, bool fresh) {
+      const uint64_t vd = desc_mnmajor_sw128(sv + stage * kTileBytes, C::kHalf);
+#pragma unroll
+      for (int x = 0; x < kT / 16; ++x)
+        umma_ts(tmem + 256 + i * D, tmem + i * 128 + 8 * x, vd + ((x * 2048u) >> 4), kDescPV, !fresh || x > 0);
+    };
+    while (ok && next_run(a, p, walk)) {
+      const int ni = walk.w.s.rows * p.G - walk.group * kGroup > 128 ? 2 : 1;
+      for (int i = 0; i < ni && ok; ++i) {
+        if (!wait(&ctrl.q_full[i], q_phase[i], 54)) break;
+        q_phase[i] ^= 1u;
+        if (i == 0 && !wait(&ctrl.k_full[count & 1], (count >> 1) & 1, 55)) break;
+        tc_fence_after();
+        scores(i, count & 1);
+        umma_commit(smem_u32(&ctrl.s_full[i]));
+      }
+      if (!ok) break;
+      umma_commit(smem_u32(&ctrl.k_empty[count & 1]));
+      for (int k = 0; k < walk.n && ok; ++k, ++count) {
+        const bool last = k + 1 == walk.n;
+        for (int i = 0; i < ni; ++i) {
+          if (!wait(&ctrl.p_full[i], p_phase[i], 56)) break;
+          p_phase[i] ^= 1u;
+          if (i == 0 && !wait(&ctrl.v_full[count & 1], (count >> 1) & 1, 57)) break;
+          tc_fence_after();
+          sums(i, count & 1, k == 0);
+          if (!last) {
+            if (i == 0 && !wait(&ctrl.k_full[(count + 1) & 1], ((count + 1) >> 1) & 1, 58)) break;
+            tc_fence_after();
+            scores(i, (count + 1) & 1);
+          }
+          umma_commit(smem_u32(&ctrl.s_full[i]));
+        }
+        if (!ok) break;
+        umma_commit(smem_u32(&ctrl.v_empty[count & 1]));
+        if (!last) umma_commit(smem_u32(&ctrl.k_empty[(count + 1) & 1]));
+      }
+    }
+    // the last arrival on this CTA's barriers
+    if (count > 0) wait(&ctrl.v_empty[(count - 1) & 1], ((count - 1) >> 1) & 1, 59);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the groups that were cut, pieces in CTA order.
+template <int D>
+__global__ void __launch_bounds__(512)
+    kv4_prompt_join_kernel(const Args a, const AttnParams p) {
+  using C = PCfg<D>;
+  grid_dependency_wait();
+  const int first = blockIdx.x >> 2, part = blockIdx.x & 3;  // 4 CTAs a group, 64 rows each
+  const int4 rec = p.rec[first];
+  if (rec.x < 0) return;
+  Span w;
+  load_span(a, p, rec.y, w);
+  const int kvh = rec.x / w.groups, group = rec.x - kvh * w.groups;
+  const int all_rows = w.s.rows * p.G, r0 = group * kGroup;
+  constexpr int kTpr = D / 8;
+  for (int x = threadIdx.x; x < 64 * kTpr; x += 512) {
+    const int r = part * 64 + x / kTpr, d = (x % kTpr) * 8;
+    if (r0 + r >= all_rows) continue;
+    float mm = -INFINITY, ll = 0.f, v[8] = {};
+    for (int c = first; c <= rec.z; ++c) {
+      const float* s = p.part + static_cast<int64_t>(2 * c + (c == first ? rec.w : 0)) * C::kSlot;
+      const float pm = s[kGroup * D + r], pl = s[kGroup * D + kGroup + r];
+      const float4 y = *reinterpret_cast<const float4*>(s + r * D + d);
+      const float4 z = *reinterpret_cast<const float4*>(s + r * D + d + 4);
+      if (pl == 0.f) continue;  // nothing read there
+      const float mn = fmaxf(mm, pm);
+      const float f0 = mm == -INFINITY ? 0.f : ex2(mm - mn), f1 = ex2(pm - mn);
+      mm = mn;
+      ll = ll * f0 + pl * f1;
+      v[0] = v[0] * f0 + y.x * f1, v[1] = v[1] * f0 + y.y * f1, v[2] = v[2] * f0 + y.z * f1, v[3] = v[3] * f0 + y.w * f1;
+      v[4] = v[4] * f0 + z.x * f1, v[5] = v[5] * f0 + z.y * f1, v[6] = v[6] * f0 + z.z * f1, v[7] = v[7] * f0 + z.w * f1;
+    }
+    store_row<D>(p, w.s, kvh, r0 + r, d, v, mm, ll);
+  }
+}
+
+template <int D, int BS>
+rnl_status launch(const AttnParams& p, const Args& a, const DeviceInfo& dev, cudaStream_t s) {
+  const rnl_status st =
+      ensure_smem_attr(reinterpret_cast<const void*>(kv4_prompt_kernel<D, BS>), dev.device, PCfg<D>::kSmem);
+  if (st != RNL_OK) return st;
+  const int ctas = std::min(dev.sm_count, kMaxPromptCtas);
+  trace_before(s);
+  kv4_prompt_kernel<D, BS><<<ctas, kPThreads, PCfg<D>::kSmem, s>>>(a, p);
+  cudaError_t e = cudaGetLastError();
+  trace_after(s, "kv4_prompt");
+  if (e != cudaSuccess) return RNL_ERR_LAUNCH;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(4 * ctas);
+  cfg.blockDim = dim3(512);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  trace_before(s);
+  e = cudaLaunchKernelEx(&cfg, kv4_prompt_join_kernel<D>, a, p);
+  trace_after(s, "kv4_prompt_join");
+  return e == cudaSuccess ? RNL_OK : RNL_ERR_LAUNCH;
+}
+
+}  // namespace
+
+bool kv4_prompt_fits(int64_t D) { return D == 64 || D == 128; }
+
+size_t kv4_prompt_workspace_bytes(int64_t D) {
+  const size_t slot = static_cast<size_t>(kGroup) * (static_cast<size_t>(D) + 2) * 4;
+  return kMaxPromptCtas * (sizeof(int4) + 2 * slot);
+}
+
+rnl_status launch_kv4_prompt(const AttnParams& p0, const Args& a, int block, void* ws, const DeviceInfo& dev,
+                             cudaStream_t s) {
+  AttnParams p = p0;
+  p.rec = static_cast<int4*>(ws);
+  p.part = reinterpret_cast<float*>(p.rec + kMaxPromptCtas);
+  if (a.D == 64) return block == 64 ? launch<64, 64>(p, a, dev, s) : launch<64, 32>(p, a, dev, s);
+  return block == 64 ? launch<128, 64>(p, a, dev, s) : launch<128, 32>(p, a, dev, s);
+}
+
+rnl_status read_clear_error_kv4prompt(unsigned int* word) {
+  unsigned int v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_err_kv4prompt, sizeof v) != cudaSuccess) return RNL_ERR_LAUNCH;
+  if (v != 0 && cudaMemcpyToSymbol(g_err_kv4prompt, &zero, sizeof zero) != cudaSuccess)
+    return RNL_ERR_LAUNCH;
+  *word = v;
+  return RNL_OK;
+}
+
+}  // namespace rnl
