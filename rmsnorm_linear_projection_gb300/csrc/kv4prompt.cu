@@ -227,6 +227,28 @@ __device__ __forceinline__ void tmem_st_32cols(uint32_t taddr, const uint32_t (&
       : "memory");
 }
 
+// Two binary32 in one 64-bit register: one instruction for both.
+__device__ __forceinline__ uint64_t pack_u32x2(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  return pack_u32x2(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ float lo_f32(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a)); }
+__device__ __forceinline__ float hi_f32(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a >> 32)); }
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // Where 16-byte chunk c (8 dims) of row r of a 128-row operand lies: blocks of
 // 64 dims, rows of 128 bytes, chunks permuted by row % 8.
 template <int D>
@@ -407,70 +429,80 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int new_v = ctrl.v_info[count & 3];
         const int tok0 = (walk.lo / kT + walk.tile + k) * kT;
         const bool whole = __all_sync(0xffffffffu, tok0 + kT - 1 <= pos && tok0 >= first);
-        // maximum of the row's scores
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        uint32_t s[2][32];
-        tmem_ld_32cols(ts, s[0]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld_wait();
-          if (c < 3) tmem_ld_32cols(ts + 32 * (c + 1), s[(c + 1) & 1]);
-#pragma unroll
-          for (int x = 0; x < 32; ++x) {
-            float v = __uint_as_float(s[c & 1][x]);
-            if (!whole) {
-              const int tok = tok0 + 32 * c + x;
-              if (tok > pos || tok < first) v = -INFINITY;
-            }
-            mx[x & 3] = fmaxf(mx[x & 3], v);
-          }
-        }
-        tmem_ld_32cols(ts, s[0]);  // for the second pass
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
         float alpha = 1.f;
-        if (top > m + kLag || (m == -INFINITY && top > m)) {
-          alpha = ex2(m - top);
-          m = top;
-          l *= alpha;
-        }
+        auto tile = [&](auto masked) {  // kept apart: the mask's tests stay out of whole tiles
+          constexpr bool kMasked = decltype(masked)::value;
+          // maximum of the row's scores
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          uint32_t s[2][32];
+          tmem_ld_32cols(ts, s[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld_wait();
+            if (c < 3) tmem_ld_32cols(ts + 32 * (c + 1), s[(c + 1) & 1]);
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+              float v0 = __uint_as_float(s[c & 1][x]), v1 = __uint_as_float(s[c & 1][x + 1]);
+              if constexpr (kMasked) {
+                const int tok = tok0 + 32 * c + x;
+                if (tok > pos || tok < first) v0 = -INFINITY;
+                if (tok + 1 > pos || tok + 1 < first) v1 = -INFINITY;
+              }
+              mx[(x >> 1) & 3] = fmaxf(mx[(x >> 1) & 3], fmaxf(v0, v1));
+            }
+          }
+          tmem_ld_32cols(ts, s[0]);  // for the second pass
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
+          if (top > m + kLag || (m == -INFINITY && top > m)) {
+            alpha = ex2(m - top);
+            m = top;
+            l *= alpha;
+          }
+          const float bias = kTop - (m == -INFINITY ? 0.f : m);
+          const uint64_t f2 = pack_f32x2(f, f), bias2 = pack_f32x2(bias, bias);
+          // weights, 32 tokens at a time, into the columns whose scores are read
+          uint64_t sum[2] = {0, 0};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld_wait();
+            if (c < 3) tmem_ld_32cols(ts + 32 * (c + 1), s[(c + 1) & 1]);
+            uint32_t h[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const uint64_t y = fma_f32x2(pack_u32x2(s[c & 1][2 * x], s[c & 1][2 * x + 1]), f2, bias2);
+              float e0 = ex2(lo_f32(y)), e1 = ex2(hi_f32(y));
+              if constexpr (kMasked) {
+                const int tok = tok0 + 32 * c + 2 * x;
+                if (tok > pos || tok < first) e0 = 0.f;
+                if (tok + 1 > pos || tok + 1 < first) e1 = 0.f;
+              }
+              sum[x & 1] = add_f32x2(sum[x & 1], pack_f32x2(e0, e1));
+              h[x] = pack_half2(e0, e1);
+            }
+            tmem_st_16cols(ts + 16 * c, h);
+          }
+          sum[0] = add_f32x2(sum[0], sum[1]);
+          l += lo_f32(sum[0]) + hi_f32(sum[0]);
+        };
+        if (whole)
+          tile(std::false_type{});
+        else
+          tile(std::true_type{});
         if (new_v != ref_v) {
           alpha *= pow2i(ref_v - new_v);
           ref_v = new_v;
         }
-        const float bias = kTop - (m == -INFINITY ? 0.f : m);
-        // weights, 32 tokens at a time, into the columns whose scores are read
-        float la = 0.f, lb = 0.f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld_wait();
-          if (c < 3) tmem_ld_32cols(ts + 32 * (c + 1), s[(c + 1) & 1]);
-          uint32_t h[16];
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            float e0 = ex2(fmaf(__uint_as_float(s[c & 1][2 * x]), f, bias));
-            float e1 = ex2(fmaf(__uint_as_float(s[c & 1][2 * x + 1]), f, bias));
-            if (!whole) {
-              const int tok = tok0 + 32 * c + 2 * x;
-              if (tok > pos || tok < first) e0 = 0.f;
-              if (tok + 1 > pos || tok + 1 < first) e1 = 0.f;
-            }
-            la += e0;
-            lb += e1;
-            h[x] = pack_half2(e0, e1);
-          }
-          tmem_st_16cols(ts + 16 * c, h);
-        }
-        l += la + lb;
         // the sums so far, rescaled (the products before are done: this
         // tile's scores came after them)
         if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
-            tmem_ld_32cols(to + 32 * c, s[0]);
+            uint32_t s[32];
+            tmem_ld_32cols(to + 32 * c, s);
             tmem_ld_wait();
 #pragma unroll
-            for (int x = 0; x < 32; ++x) s[0][x] = __float_as_uint(__uint_as_float(s[0][x]) * alpha);
-            tmem_st_32cols(to + 32 * c, s[0]);
+            for (int x = 0; x < 32; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * alpha);
+            tmem_st_32cols(to + 32 * c, s);
           }
         }
         tmem_st_wait();
