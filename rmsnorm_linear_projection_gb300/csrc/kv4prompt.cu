@@ -15,7 +15,7 @@
 //                    memory to registers, converted and scaled into shared
 //                    memory (128-byte swizzle; keys K-major, values MN-major,
 //                    the same bytes in the same order)
-//   warp 12          TMEM allocation and, on one thread, every tcgen05.mma:
+//   warp 12          (of a fourth warpgroup) TMEM allocation and, on one thread, every tcgen05.mma:
 //                    S_i = Q_i K^T (both from shared memory), O_i += P_i V
 //                    (P_i from TMEM), i = 0, 1 in turn, so that one row tile's
 //                    softmax runs while the other one's products do
@@ -46,8 +46,11 @@ constexpr int kGroup = 256;        // rows a CTA holds
 constexpr int kSoftWarps = 8;
 constexpr int kFillWarps = 4;
 constexpr int kMmaWarp = kSoftWarps + kFillWarps;
-constexpr int kPThreads = (kMmaWarp + 1) * 32;
-constexpr int kPWarps = kMmaWarp + 1;
+constexpr int kPWarps = 16;        // four warpgroups; warps 13-15 idle
+constexpr int kPThreads = kPWarps * 32;
+// registers a thread after the roles part (launched with 128): 8 * 152 + 4 * 120 + 4 * 80 <= 16 * 128
+constexpr int kLaunchRegs = 128, kSoftRegs = 152, kFillRegs = 120, kMmaRegs = 80;
+static_assert(8 * kSoftRegs + 4 * kFillRegs + 4 * kMmaRegs <= 16 * kLaunchRegs, "register file");
 // what a group costs beside its tiles (queries, output), in tiles
 constexpr int kGroupCost = 3;
 constexpr int kMaxPromptCtas = 160;
@@ -61,6 +64,15 @@ struct PCfg {
   static constexpr size_t kSmem = 1024 + 6 * static_cast<size_t>(kTileBytes);
   static constexpr int kSlot = kGroup * (D + 2);          // floats of a partial: sums, maxima, weights
 };
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 struct __align__(8) PCtrl {
   uint64_t q_full[2], s_full[2], p_full[2];
@@ -180,39 +192,51 @@ __device__ __forceinline__ bool next_run(const Args& a, const AttnParams& p, Wal
   return false;
 }
 
-// Shared-memory descriptor of an MN-major operand with 128-byte swizzle: rows
-// (of k) of 64 elements, 8-row groups 1024 bytes apart, blocks of 64 elements
-// `lbo` bytes apart.
-__device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr, uint32_t lbo) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(lbo >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
+// Low word of a shared-memory descriptor: start address and leading offset
+// (between blocks of 64 elements of an MN-major operand; 16 bytes, unused, for
+// a K-major one).
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16);
 }
 // kind::f16, binary16 A and B, fp32 accumulator of M x N; B MN-major if asked.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
-// A from TMEM (binary16 pairs, lane = row), B from shared memory.
-__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                        uint32_t accumulate) {
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+// The products of one 16-wide step; descriptors as their low words (address
+// and leading offset) with constant high words, so that a step costs a 32-bit
+// addition each.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups, version, 128-byte swizzle
+template <uint32_t IDESC>
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "mov.b64 da, {%1, %4};\n\t"
+      "mov.b64 db, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(accumulate), "n"(kDescHi), "r"(IDESC)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&r)[16]) {
+// A from TMEM (binary16 pairs, lane = row), B from shared memory.
+template <uint32_t IDESC>
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t accumulate) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "mov.b64 db, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(accumulate), "n"(kDescHi), "r"(IDESC)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_32cols(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -366,6 +390,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
   if (warp < kSoftWarps) {
     // ------------------------------------------------------------- softmax
+    regs_inc<kSoftRegs>();
     const int i = warp >> 2;                    // row tile
     const int rw = (warp & 3) * 32 + lane;      // row in it
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -430,64 +455,76 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int tok0 = (walk.lo / kT + walk.tile + k) * kT;
         const bool whole = __all_sync(0xffffffffu, tok0 + kT - 1 <= pos && tok0 >= first);
         float alpha = 1.f;
+        uint32_t h[64];  // the row's weights, binary16 pairs
         auto tile = [&](auto masked) {  // kept apart: the mask's tests stay out of whole tiles
           constexpr bool kMasked = decltype(masked)::value;
-          // maximum of the row's scores
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          uint32_t s[2][32];
-          tmem_ld_32cols(ts, s[0]);
+          auto seen = [&](int tok, float v, float other) { return !kMasked || (tok <= pos && tok >= first) ? v : other; };
+          // The maximum in use serves while the row's scores stay within 2^8 of
+          // it, which one pass over the scores finds while it computes the
+          // weights; where it does not (a run's first tile, or a row of the warp
+          // far above what it saw) the maximum is taken first.
+          bool exact = __any_sync(0xffffffffu, m == -INFINITY);
+          for (;;) {
+            uint32_t s[2][32];
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if (exact) {
+              tmem_ld_32cols(ts, s[0]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld_wait();
-            if (c < 3) tmem_ld_32cols(ts + 32 * (c + 1), s[(c + 1) & 1]);
+              for (int c = 0; c < 4; ++c) {
+                tmem_ld_wait();
+                if (c < 3) tmem_ld_32cols(ts + 32 * (c + 1), s[(c + 1) & 1]);
 #pragma unroll
-            for (int x = 0; x < 32; x += 2) {
-              float v0 = __uint_as_float(s[c & 1][x]), v1 = __uint_as_float(s[c & 1][x + 1]);
-              if constexpr (kMasked) {
-                const int tok = tok0 + 32 * c + x;
-                if (tok > pos || tok < first) v0 = -INFINITY;
-                if (tok + 1 > pos || tok + 1 < first) v1 = -INFINITY;
+                for (int x = 0; x < 32; x += 2) {
+                  const int tok = tok0 + 32 * c + x;
+                  mx[(x >> 1) & 3] = fmaxf(mx[(x >> 1) & 3],
+                                           fmaxf(seen(tok, __uint_as_float(s[c & 1][x]), -INFINITY),
+                                                 seen(tok + 1, __uint_as_float(s[c & 1][x + 1]), -INFINITY)));
+                }
               }
-              mx[(x >> 1) & 3] = fmaxf(mx[(x >> 1) & 3], fmaxf(v0, v1));
+              const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
+              if (top > m + kLag || (m == -INFINITY && top > m)) {
+                alpha = ex2(m - top);
+                m = top;
+                l *= alpha;
+              }
             }
-          }
-          tmem_ld_32cols(ts, s[0]);  // for the second pass
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
-          if (top > m + kLag || (m == -INFINITY && top > m)) {
-            alpha = ex2(m - top);
-            m = top;
-            l *= alpha;
-          }
-          const float bias = kTop - (m == -INFINITY ? 0.f : m);
-          const uint64_t f2 = pack_f32x2(f, f), bias2 = pack_f32x2(bias, bias);
-          // weights, 32 tokens at a time, into the columns whose scores are read
-          uint64_t sum[2] = {0, 0};
+            const float bias = kTop - (m == -INFINITY ? 0.f : m);
+            const uint64_t f2 = pack_f32x2(f, f), bias2 = pack_f32x2(bias, bias);
+            uint64_t sum[2] = {0, 0};
+            tmem_ld_32cols(ts, s[0]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld_wait();
-            if (c < 3) tmem_ld_32cols(ts + 32 * (c + 1), s[(c + 1) & 1]);
-            uint32_t h[16];
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld_wait();
+              if (c < 3) tmem_ld_32cols(ts + 32 * (c + 1), s[(c + 1) & 1]);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const uint64_t y = fma_f32x2(pack_u32x2(s[c & 1][2 * x], s[c & 1][2 * x + 1]), f2, bias2);
-              float e0 = ex2(lo_f32(y)), e1 = ex2(hi_f32(y));
-              if constexpr (kMasked) {
+              for (int x = 0; x < 16; ++x) {
+                const uint32_t s0 = s[c & 1][2 * x], s1 = s[c & 1][2 * x + 1];
                 const int tok = tok0 + 32 * c + 2 * x;
-                if (tok > pos || tok < first) e0 = 0.f;
-                if (tok + 1 > pos || tok + 1 < first) e1 = 0.f;
+                const uint64_t y = fma_f32x2(pack_u32x2(s0, s1), f2, bias2);
+                const float e0 = seen(tok, ex2(lo_f32(y)), 0.f), e1 = seen(tok + 1, ex2(hi_f32(y)), 0.f);
+                mx[x & 3] = fmaxf(mx[x & 3], fmaxf(seen(tok, __uint_as_float(s0), -INFINITY),
+                                                   seen(tok + 1, __uint_as_float(s1), -INFINITY)));
+                sum[x & 1] = add_f32x2(sum[x & 1], pack_f32x2(e0, e1));
+                h[16 * c + x] = pack_half2(e0, e1);
               }
-              sum[x & 1] = add_f32x2(sum[x & 1], pack_f32x2(e0, e1));
-              h[x] = pack_half2(e0, e1);
             }
-            tmem_st_16cols(ts + 16 * c, h);
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
+            if (!exact && __any_sync(0xffffffffu, top > m + kLag)) {
+              exact = true;
+              continue;
+            }
+            sum[0] = add_f32x2(sum[0], sum[1]);
+            l += lo_f32(sum[0]) + hi_f32(sum[0]);
+            break;
           }
-          sum[0] = add_f32x2(sum[0], sum[1]);
-          l += lo_f32(sum[0]) + hi_f32(sum[0]);
         };
         if (whole)
           tile(std::false_type{});
         else
           tile(std::true_type{});
+        // into the columns whose scores have been read
+        tmem_st_32cols(ts, *reinterpret_cast<uint32_t(*)[32]>(&h[0]));
+        tmem_st_32cols(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(&h[32]));
         if (new_v != ref_v) {
           alpha *= pow2i(ref_v - new_v);
           ref_v = new_v;
@@ -568,6 +605,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
   } else if (warp < kMmaWarp) {
     // ---------------------------------------------- codes to binary16 tiles
+    regs_dec<kFillRegs>();
     const int tk = tid - kSoftWarps * 32;  // token in the tile
     const int fw = warp - kSoftWarps;
     struct Raw {
@@ -640,18 +678,25 @@ __global__ void __launch_bounds__(kPThreads, 1)
       for (int x = 0; x < kSB; ++x) t = max(t, (w >> (8 * x)) & 0xFFu);
       return t;
     };
-    Raw raw;
+    // one tile ahead: the next one's codes are on their way while this one's
+    // are converted, and the page after that is being looked up
+    Raw raw[2];
     step();
     bool now = have, now_first = first_tile;
-    load(raw);
+    load(raw[0]);
     step();
     int ref_v = 13;
-    for (int count = 0; now; ++count) {
+    auto fill = [&](int count, const Raw& cur, Raw& next) {
       const int stage = count & 1;
       const uint32_t parity = ((count >> 1) & 1) ^ 1u;
+      const bool more_now = have, more_first = first_tile;
       // the tile's largest scales, over the four warps
-      const uint32_t tk_ = __reduce_max_sync(0xffffffffu, top_of(raw.ks));
-      const uint32_t tv_ = __reduce_max_sync(0xffffffffu, top_of(raw.vs));
+      const uint32_t tk_ = __reduce_max_sync(0xffffffffu, top_of(cur.ks));
+      const uint32_t tv_ = __reduce_max_sync(0xffffffffu, top_of(cur.vs));
+      if (more_now) {
+        load(next);
+        step();
+      }
       if (lane == 0) ctrl.top[stage][fw] = static_cast<int>(tk_ | (tv_ << 8));
       asm volatile("bar.sync 1, %0;" ::"n"(kFillWarps * 32) : "memory");
       int top_k = 0, top_v = 0;
@@ -667,80 +712,89 @@ __global__ void __launch_bounds__(kPThreads, 1)
         ctrl.v_info[count & 3] = ref_v;
       }
       mbar_wait(smem_u32(&ctrl.k_empty[stage]), parity, abort, &g_err_kv4prompt, 52);
-      put(sk + stage * kTileBytes, raw.k, raw.ks, pow2i(140 - ref_k));
+      put(sk + stage * kTileBytes, cur.k, cur.ks, pow2i(140 - ref_k));
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctrl.k_full[stage]));
       mbar_wait(smem_u32(&ctrl.v_empty[stage]), parity, abort, &g_err_kv4prompt, 53);
-      put(sv + stage * kTileBytes, raw.v, raw.vs, pow2i(140 - ref_v));
+      put(sv + stage * kTileBytes, cur.v, cur.vs, pow2i(140 - ref_v));
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctrl.v_full[stage]));
-      now = have;
-      now_first = first_tile;
-      if (now) {
-        load(raw);
-        step();
-      }
+      now = more_now;
+      now_first = more_first;
+    };
+    for (int count = 0; now; count += 2) {
+      fill(count, raw[0], raw[1]);
+      if (now) fill(count + 1, raw[1], raw[0]);
     }
-  } else if (lane == 0) {
+  } else {
     // ------------------------------------------------------------ products
-    constexpr uint32_t kDescQK = idesc_f16(128, kT, false), kDescPV = idesc_f16(128, D, true);
-    int count = 0;                       // tiles so far
-    uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
-      ok = ok && mbar_wait(smem_u32(bar), parity, abort, &g_err_kv4prompt, site);
-      return ok;
-    };
-    auto scores = [&](int i, int stage) {
-      const uint64_t qd = desc_kmajor_sw128(sq + i * kTileBytes), kd = desc_kmajor_sw128(sk + stage * kTileBytes);
+    regs_dec<kMmaRegs>();
+    if (warp == kMmaWarp) {
+      // the whole warp walks and waits; one lane issues
+      constexpr uint32_t kDescQK = idesc_f16(128, kT, false), kDescPV = idesc_f16(128, D, true);
+      int count = 0;                       // tiles so far
+      uint32_t q_phase = 0, p_phase = 0;   // a bit a row tile
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+        ok = ok && mbar_wait(smem_u32(bar), parity, abort, &g_err_kv4prompt, site);
+        ok = __all_sync(0xffffffffu, ok);
+        return ok;
+      };
+      const uint32_t q_lo = desc_lo(sq, 16), k_lo = desc_lo(sk, 16), v_lo = desc_lo(sv, C::kHalf);
+      auto scores = [&](int i, int stage) {
+        const uint32_t qd = q_lo + i * (kTileBytes >> 4), kd = k_lo + stage * (kTileBytes >> 4);
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) {
-        const uint64_t step = (static_cast<uint64_t>(x >> 2) * C::kHalf + (x & 3) * 32) >> 4;
-        umma_bf16(tmem + i * 128, qd + step, kd + step, kDescQK, x > 0);
-      }
-    };
-    auto sums = [&](int i, int stage, bool fresh) {
-      const uint64_t vd = desc_mnmajor_sw128(sv + stage * kTileBytes, C::kHalf);
-#pragma unroll
-      for (int x = 0; x < kT / 16; ++x)
-        umma_ts(tmem + 256 + i * D, tmem + i * 128 + 8 * x, vd + ((x * 2048u) >> 4), kDescPV, !fresh || x > 0);
-    };
-    while (ok && next_run(a, p, walk)) {
-      const int ni = walk.w.s.rows * p.G - walk.group * kGroup > 128 ? 2 : 1;
-      for (int i = 0; i < ni && ok; ++i) {
-        if (!wait(&ctrl.q_full[i], q_phase[i], 54)) break;
-        q_phase[i] ^= 1u;
-        if (i == 0 && !wait(&ctrl.k_full[count & 1], (count >> 1) & 1, 55)) break;
-        tc_fence_after();
-        scores(i, count & 1);
-        umma_commit(smem_u32(&ctrl.s_full[i]));
-      }
-      if (!ok) break;
-      umma_commit(smem_u32(&ctrl.k_empty[count & 1]));
-      for (int k = 0; k < walk.n && ok; ++k, ++count) {
-        const bool last = k + 1 == walk.n;
-        for (int i = 0; i < ni; ++i) {
-          if (!wait(&ctrl.p_full[i], p_phase[i], 56)) break;
-          p_phase[i] ^= 1u;
-          if (i == 0 && !wait(&ctrl.v_full[count & 1], (count >> 1) & 1, 57)) break;
-          tc_fence_after();
-          sums(i, count & 1, k == 0);
-          if (!last) {
-            if (i == 0 && !wait(&ctrl.k_full[(count + 1) & 1], ((count + 1) >> 1) & 1, 58)) break;
-            tc_fence_after();
-            scores(i, (count + 1) & 1);
-          }
-          umma_commit(smem_u32(&ctrl.s_full[i]));
+        for (int x = 0; x < D / 16; ++x) {
+          const uint32_t step = ((x >> 2) * C::kHalf + (x & 3) * 32) >> 4;
+          umma_ss<kDescQK>(tmem + i * 128, qd + step, kd + step, x > 0);
         }
-        if (!ok) break;
-        umma_commit(smem_u32(&ctrl.v_empty[count & 1]));
-        if (!last) umma_commit(smem_u32(&ctrl.k_empty[(count + 1) & 1]));
+      };
+      auto sums = [&](int i, int stage, bool fresh) {
+        const uint32_t vd = v_lo + stage * (kTileBytes >> 4);
+#pragma unroll
+        for (int x = 0; x < kT / 16; ++x)
+          umma_ts<kDescPV>(tmem + 256 + i * D, tmem + i * 128 + 8 * x, vd + ((x * 2048u) >> 4), !fresh || x > 0);
+      };
+      while (ok && next_run(a, p, walk)) {
+        const int ni = walk.w.s.rows * p.G - walk.group * kGroup > 128 ? 2 : 1;
+        for (int i = 0; i < ni && ok; ++i) {
+          if (!wait(&ctrl.q_full[i], (q_phase >> i) & 1, 54)) break;
+          q_phase ^= 1u << i;
+          if (i == 0 && !wait(&ctrl.k_full[count & 1], (count >> 1) & 1, 55)) break;
+          tc_fence_after();
+          if (elect_one()) {
+            scores(i, count & 1);
+            umma_commit(smem_u32(&ctrl.s_full[i]));
+            if (i == ni - 1) umma_commit(smem_u32(&ctrl.k_empty[count & 1]));
+          }
+          __syncwarp();
+        }
+        for (int k = 0; k < walk.n && ok; ++k, ++count) {
+          const bool last = k + 1 == walk.n;
+          for (int i = 0; i < ni; ++i) {
+            if (i == 0 && !wait(&ctrl.v_full[count & 1], (count >> 1) & 1, 57)) break;
+            if (i == 0 && !last && !wait(&ctrl.k_full[(count + 1) & 1], ((count + 1) >> 1) & 1, 58)) break;
+            if (!wait(&ctrl.p_full[i], (p_phase >> i) & 1, 56)) break;
+            p_phase ^= 1u << i;
+            tc_fence_after();
+            if (elect_one()) {
+              sums(i, count & 1, k == 0);
+              if (!last) scores(i, (count + 1) & 1);
+              umma_commit(smem_u32(&ctrl.s_full[i]));
+              if (i == ni - 1) {
+                umma_commit(smem_u32(&ctrl.v_empty[count & 1]));
+                if (!last) umma_commit(smem_u32(&ctrl.k_empty[(count + 1) & 1]));
+              }
+            }
+            __syncwarp();
+          }
+        }
       }
+      // the last arrival on this CTA's barriers
+      if (count > 0) wait(&ctrl.v_empty[(count - 1) & 1], ((count - 1) >> 1) & 1, 59);
     }
-    // the last arrival on this CTA's barriers
-    if (count > 0) wait(&ctrl.v_empty[(count - 1) & 1], ((count - 1) >> 1) & 1, 59);
   }
   __syncwarp();
   tc_fence_before();
@@ -786,11 +840,23 @@ __global__ void __launch_bounds__(512)
   }
 }
 
+// The roles' register shares add up to what the block is launched with only if
+// the kernel was built with kLaunchRegs: checked once, before a first launch.
+template <int D, int BS>
+bool built_as_planned() {
+  static const bool ok = [] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, kv4_prompt_kernel<D, BS>) == cudaSuccess && at.numRegs == kLaunchRegs;
+  }();
+  return ok;
+}
+
 template <int D, int BS>
 rnl_status launch(const AttnParams& p, const Args& a, const DeviceInfo& dev, cudaStream_t s) {
   const rnl_status st =
       ensure_smem_attr(reinterpret_cast<const void*>(kv4_prompt_kernel<D, BS>), dev.device, PCfg<D>::kSmem);
   if (st != RNL_OK) return st;
+  if (!built_as_planned<D, BS>()) return RNL_ERR_LAUNCH;
   const int ctas = std::min(dev.sm_count, kMaxPromptCtas);
   trace_before(s);
   kv4_prompt_kernel<D, BS><<<ctas, kPThreads, PCfg<D>::kSmem, s>>>(a, p);
