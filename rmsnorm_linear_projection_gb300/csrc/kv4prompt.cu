@@ -130,6 +130,13 @@ __device__ __forceinline__ int pair_units(const AttnParams& p, const Span& w) {
   return t + 2 * kGroupCost;
 }
 
+// Units of a head's items: the pairs, and the middle group alone where the
+// number of groups is odd.
+__device__ __forceinline__ int64_t head_units(const AttnParams& p, const Span& w) {
+  return static_cast<int64_t>(pair_units(p, w)) * (w.groups / 2) +
+         ((w.groups & 1) ? kGroupCost + group_tiles(p, w.s, w.groups / 2) : 0);
+}
+
 // Walks a CTA's range: next() gives its next run of one group's tiles.
 struct Walk {
   int b, head, pair, off;  // place: units into the pair's item
@@ -171,7 +178,7 @@ __device__ __forceinline__ bool next_run(const Args& a, const AttnParams& p, Wal
       c.off += c.n;
       return true;
     }
-    const int rest = max(pair_units(p, c.w) - c.off, 0);
+    const int rest = g1 < g0 ? max(pair_units(p, c.w) - c.off, 0) : 0;
     c.left -= rest;
     c.at += rest;
     c.off = 0;
@@ -325,7 +332,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   auto units_of = [&](int b) -> long long {
     Span w;
     if (b >= a.n_seqs || !load_span(a, p, b, w)) return 0;
-    return static_cast<long long>(pair_units(p, w)) * ((w.groups + 1) / 2) * a.Hkv;
+    return head_units(p, w) * a.Hkv;
   };
   long long sum = 0;
   for (int b = tid; b < a.n_seqs; b += kPThreads) sum += units_of(b);
@@ -371,11 +378,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
   walk.b = ctrl.b;
   load_span(a, p, walk.b, walk.w);
   {
-    const int len = pair_units(p, walk.w), pairs = (walk.w.groups + 1) / 2;
-    const int item = static_cast<int>(ctrl.off / len);
-    walk.off = static_cast<int>(ctrl.off - static_cast<long long>(item) * len);
-    walk.head = item / pairs;
-    walk.pair = item - walk.head * pairs;
+    const int64_t per_head = head_units(p, walk.w);
+    const int len = pair_units(p, walk.w);
+    walk.head = static_cast<int>(ctrl.off / per_head);
+    const int64_t in_head = ctrl.off - walk.head * per_head;
+    walk.pair = static_cast<int>(min(in_head / len, static_cast<int64_t>(walk.w.groups / 2)));
+    walk.off = static_cast<int>(in_head - static_cast<int64_t>(walk.pair) * len);
     walk.at = u0;
     walk.left = u1 - u0;
   }
@@ -738,8 +746,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
       uint32_t q_phase = 0, p_phase = 0;   // a bit a row tile
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
-        ok = ok && mbar_wait(smem_u32(bar), parity, abort, &g_err_kv4prompt, site);
-        ok = __all_sync(0xffffffffu, ok);
+        int done = 1;
+        if (lane == 0) done = mbar_wait(smem_u32(bar), parity, abort, &g_err_kv4prompt, site);
+        ok = ok && __shfl_sync(0xffffffffu, done, 0) != 0;
         return ok;
       };
       const uint32_t q_lo = desc_lo(sq, 16), k_lo = desc_lo(sk, 16), v_lo = desc_lo(sv, C::kHalf);
