@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
         t = __vmaxu4(t, t >> 16);
         return static_cast<int>(__reduce_max_sync(0xffffffffu, max(t & 0xFFu, (t >> 8) & 0xFFu)));
       };
-      mbar_wait(bar_k, phase & 1, &sh_abort, &g_err_kv4attn, 47);
+      quick_wait(bar_k, phase & 1, &sh_abort, &g_err_kv4attn, 47);
       float s[T8][MS][4];
       float f_tile = 0.f;
       if (any) {
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
       __syncwarp();  // every lane has read the keys
       const bool more = ahead.left > 0;
       if (more) fetch_keys();
-      mbar_wait(bar_v, phase & 1, &sh_abort, &g_err_kv4attn, 47);
+      quick_wait(bar_v, phase & 1, &sh_abort, &g_err_kv4attn, 47);
       phase ^= 1u;
       if (any) {
         // ---- softmax over the tile

@@ -11,14 +11,15 @@
 //                    TMEM, running maximum and sum, weights back to TMEM as
 //                    binary16 (the A operand of the second product), the sums
 //                    rescaled there when the maximum grew by more than 2^8
-//   warps 8-11       a thread a token: codes of the next tile from global
-//                    memory to registers, converted and scaled into shared
-//                    memory (128-byte swizzle; keys K-major, values MN-major,
-//                    the same bytes in the same order)
-//   warp 12          (of a fourth warpgroup) TMEM allocation and, on one thread, every tcgen05.mma:
+//   warps 8-11,      keys and values, a thread a token: codes and scales from a
+//     12-15          ring in shared memory, converted and scaled into the
+//                    operands there (128-byte swizzle; keys K-major, values
+//                    MN-major, the same bytes in the same order)
+//   warp 16          TMEM allocation and, on one thread, every tcgen05.mma:
 //                    S_i = Q_i K^T (both from shared memory), O_i += P_i V
 //                    (P_i from TMEM), i = 0, 1 in turn, so that one row tile's
 //                    softmax runs while the other one's products do
+//   warp 17          bulk copies of the next tiles' codes and scales into the ring
 // TMEM: S_0, S_1 (128 columns each; P_i takes the first 64 of S_i), O_0, O_1.
 //
 // The weights are 2^(x - m + 7) with m at most 2^8 behind the true maximum:
@@ -44,13 +45,16 @@ __device__ unsigned int g_err_kv4prompt;
 constexpr int kT = 128;            // tokens a tile
 constexpr int kGroup = 256;        // rows a CTA holds
 constexpr int kSoftWarps = 8;
-constexpr int kFillWarps = 4;
-constexpr int kMmaWarp = kSoftWarps + kFillWarps;
-constexpr int kPWarps = 16;        // four warpgroups; warps 13-15 idle
+constexpr int kFillWarps = 4;      // for the keys, and as many for the values
+constexpr int kValueWarp = kSoftWarps + kFillWarps;
+constexpr int kMmaWarp = kValueWarp + kFillWarps;
+constexpr int kLoadWarp = kMmaWarp + 1;
+constexpr int kMaxRing = 3;
+constexpr int kPWarps = 20;        // whole warpgroups; warps 18 and 19 idle
 constexpr int kPThreads = kPWarps * 32;
-// registers a thread after the roles part (launched with 128): 8 * 152 + 4 * 120 + 4 * 80 <= 16 * 128
-constexpr int kLaunchRegs = 128, kSoftRegs = 152, kFillRegs = 120, kMmaRegs = 80;
-static_assert(8 * kSoftRegs + 4 * kFillRegs + 4 * kMmaRegs <= 16 * kLaunchRegs, "register file");
+// registers a thread after the roles part, within what the block is launched with
+constexpr int kLaunchRegs = 96, kSoftRegs = 152, kFillRegs = 56, kMmaRegs = 64;
+static_assert(8 * kSoftRegs + 8 * kFillRegs + 4 * kMmaRegs <= kPWarps * kLaunchRegs, "register file");
 // what a group costs beside its tiles (queries, output), in tiles
 constexpr int kGroupCost = 3;
 constexpr int kMaxPromptCtas = 160;
@@ -61,7 +65,12 @@ template <int D>
 struct PCfg {
   static constexpr uint32_t kTileBytes = 128u * D * 2;    // Q_i, K or V in shared memory
   static constexpr uint32_t kHalf = 128u * 128;           // bytes between blocks of 64 dims
-  static constexpr size_t kSmem = 1024 + 6 * static_cast<size_t>(kTileBytes);
+  // a tile's codes and scales (room for blocks of 32) of keys, then of values
+  static constexpr uint32_t kRawSide = 128u * D / 2 + 128u * D / 32;
+  // tiles of codes under way, beside the one that the fill warps hold in
+  // registers: what shared memory has room for
+  static constexpr int kRing = D == 128 ? 1 : kMaxRing;
+  static constexpr size_t kSmem = 1024 + 6 * static_cast<size_t>(kTileBytes) + kRing * 2 * kRawSide;
   static constexpr int kSlot = kGroup * (D + 2);          // floats of a partial: sums, maxima, weights
 };
 
@@ -73,18 +82,6 @@ template <int N>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-
-struct __align__(8) PCtrl {
-  uint64_t q_full[2], s_full[2], p_full[2];
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  float k_info[4];   // score factor of tile x at x % 4
-  int v_info[4];     // the values' reference scale byte
-  int top[2][kFillWarps];
-  long long sum[kPWarps];
-  long long off;
-  uint32_t tmem;
-  int b, abort;
-};
 
 // A group's tokens in tiles.
 struct Span {
@@ -199,6 +196,22 @@ __device__ __forceinline__ bool next_run(const Args& a, const AttnParams& p, Wal
   return false;
 }
 
+struct __align__(16) PCtrl {
+  uint64_t q_full[2], s_full[2], p_full[2];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t raw_full[kMaxRing], raw_empty[kMaxRing];
+  uint64_t top_full[2][2];   // the fill warps' largest scales are in `top`
+  Walk walk[kLoadWarp + 1];  // a place for each warp that walks
+  int4 raw_info[kMaxRing];      // first token, the group's tokens, 1: a run's first tile, 2: no more tiles
+  float k_info[4];   // score factor of tile x at x % 4
+  int v_info[4];     // the values' reference scale byte
+  int top[2][2][kFillWarps];
+  long long sum[kPWarps];
+  long long off;
+  uint32_t tmem;
+  int b, abort, more[kLoadWarp + 1];
+};
+
 // Low word of a shared-memory descriptor: start address and leading offset
 // (between blocks of 64 elements of an MN-major operand; 16 bytes, unused, for
 // a K-major one).
@@ -258,6 +271,11 @@ __device__ __forceinline__ void tmem_st_32cols(uint32_t taddr, const uint32_t (&
       : "memory");
 }
 
+__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t site) {
+  quick_wait(bar, parity, abort, &g_err_kv4prompt, site);
+  __syncwarp();
+}
+
 // Two binary32 in one 64-bit register: one instruction for both.
 __device__ __forceinline__ uint64_t pack_u32x2(uint32_t lo, uint32_t hi) {
   uint64_t d;
@@ -293,24 +311,18 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t x, uint32_t 
                : "memory");
 }
 
-// A token's scale bytes (D / BS of them) in one word.
-template <int N>
-__device__ __forceinline__ uint32_t load_scales(const uint8_t* p) {
-  if constexpr (N == 4) return __ldg(reinterpret_cast<const uint32_t*>(p));
-  else if constexpr (N == 2) return __ldg(reinterpret_cast<const uint16_t*>(p));
-  else return __ldg(p);
-}
-
 template <int D, int BS>
 __global__ void __launch_bounds__(kPThreads, 1)
     kv4_prompt_kernel(const Args a, const AttnParams p) {
   using C = PCfg<D>;
   constexpr int kSB = D / BS;
   constexpr uint32_t kTileBytes = C::kTileBytes;
+  constexpr int kRing = C::kRing;
   extern __shared__ uint8_t smem_raw[];
   __shared__ PCtrl ctrl;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sq = base, sk = base + 2 * kTileBytes, sv = base + 4 * kTileBytes;
+  const uint8_t* const raws = smem_raw + (base - smem_u32(smem_raw)) + 6 * kTileBytes;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   volatile int* abort = &ctrl.abort;
 
@@ -323,6 +335,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
       mbar_init(smem_u32(&ctrl.k_empty[i]), 1);
       mbar_init(smem_u32(&ctrl.v_full[i]), kFillWarps);
       mbar_init(smem_u32(&ctrl.v_empty[i]), 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&ctrl.top_full[i >> 1][i & 1]), kFillWarps);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(smem_u32(&ctrl.raw_full[i]), 1);
+      mbar_init(smem_u32(&ctrl.raw_empty[i]), 2 * kFillWarps);
     }
     ctrl.abort = 0;
     ctrl.b = -1;
@@ -374,10 +391,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
     before += all;
   }
   if (ctrl.b < 0) return;  // lengths changed under the call
-  Walk walk;
-  walk.b = ctrl.b;
-  load_span(a, p, walk.b, walk.w);
-  {
+  // Every warp walks the range on its own; its place lies in shared memory, one
+  // lane moves it, and the warp reads the run from there.
+  Walk& walk = ctrl.walk[min(warp, kLoadWarp)];
+  if (lane == 0 && warp <= kLoadWarp) {
+    walk.b = ctrl.b;
+    load_span(a, p, walk.b, walk.w);
     const int64_t per_head = head_units(p, walk.w);
     const int len = pair_units(p, walk.w);
     walk.head = static_cast<int>(ctrl.off / per_head);
@@ -387,6 +406,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
     walk.at = u0;
     walk.left = u1 - u0;
   }
+  auto advance = [&]() {
+    __syncwarp();
+    if (lane == 0) ctrl.more[warp] = next_run(a, p, walk);
+    __syncwarp();
+    return ctrl.more[warp] != 0;
+  };
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&ctrl.tmem), 512);
     tmem_relinquish();
@@ -409,10 +434,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
     int count = 0;  // tiles so far
     // a wait that gives up (a bug) ends every later wait at once: the loops run
     // on to their ends, so that the warp-wide instructions stay together
-    for (int run = 0; next_run(a, p, walk); ++run) {
+    for (int run = 0; advance(); ++run) {
+      const int n_tiles = walk.n;
       const int all_rows = walk.w.s.rows * p.G, r0 = walk.group * kGroup;
       if (r0 + i * 128 >= all_rows) {  // no row of this tile
-        count += walk.n;
+        count += n_tiles;
         continue;
       }
       const int r = r0 + i * 128 + rw;
@@ -452,15 +478,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
       float m = -INFINITY, l = 0.f;
       int ref_v = 13;
-      for (int k = 0; k < walk.n; ++k, ++count) {
-        mbar_wait(s_full, s_phase, abort, &g_err_kv4prompt, 49);
-        __syncwarp();
+      const int tile0 = (walk.lo / kT + walk.tile) * kT;
+      for (int k = 0; k < n_tiles; ++k, ++count) {
+        warp_wait(s_full, s_phase, abort, 49);
         s_phase ^= 1u;
         tc_fence_after();
         float f = f_row * ctrl.k_info[count & 3];
         if (f < 1e-37f) f = 1e-37f;  // not 0, for masked scores (-infinity) times it
         const int new_v = ctrl.v_info[count & 3];
-        const int tok0 = (walk.lo / kT + walk.tile + k) * kT;
+        const int tok0 = tile0 + k * kT;
         const bool whole = __all_sync(0xffffffffu, tok0 + kT - 1 <= pos && tok0 >= first);
         float alpha = 1.f;
         uint32_t h[64];  // the row's weights, binary16 pairs
@@ -473,17 +499,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
           // far above what it saw) the maximum is taken first.
           bool exact = __any_sync(0xffffffffu, m == -INFINITY);
           for (;;) {
-            uint32_t s[2][32];
+            uint32_t s[2][16];
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             if (exact) {
-              tmem_ld_32cols(ts, s[0]);
+              tmem_ld_16cols(ts, s[0]);
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
+              for (int c = 0; c < 8; ++c) {
                 tmem_ld_wait();
-                if (c < 3) tmem_ld_32cols(ts + 32 * (c + 1), s[(c + 1) & 1]);
+                if (c < 7) tmem_ld_16cols(ts + 16 * (c + 1), s[(c + 1) & 1]);
 #pragma unroll
-                for (int x = 0; x < 32; x += 2) {
-                  const int tok = tok0 + 32 * c + x;
+                for (int x = 0; x < 16; x += 2) {
+                  const int tok = tok0 + 16 * c + x;
                   mx[(x >> 1) & 3] = fmaxf(mx[(x >> 1) & 3],
                                            fmaxf(seen(tok, __uint_as_float(s[c & 1][x]), -INFINITY),
                                                  seen(tok + 1, __uint_as_float(s[c & 1][x + 1]), -INFINITY)));
@@ -499,21 +525,21 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const float bias = kTop - (m == -INFINITY ? 0.f : m);
             const uint64_t f2 = pack_f32x2(f, f), bias2 = pack_f32x2(bias, bias);
             uint64_t sum[2] = {0, 0};
-            tmem_ld_32cols(ts, s[0]);
+            tmem_ld_16cols(ts, s[0]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 8; ++c) {
               tmem_ld_wait();
-              if (c < 3) tmem_ld_32cols(ts + 32 * (c + 1), s[(c + 1) & 1]);
+              if (c < 7) tmem_ld_16cols(ts + 16 * (c + 1), s[(c + 1) & 1]);
 #pragma unroll
-              for (int x = 0; x < 16; ++x) {
+              for (int x = 0; x < 8; ++x) {
                 const uint32_t s0 = s[c & 1][2 * x], s1 = s[c & 1][2 * x + 1];
-                const int tok = tok0 + 32 * c + 2 * x;
+                const int tok = tok0 + 16 * c + 2 * x;
                 const uint64_t y = fma_f32x2(pack_u32x2(s0, s1), f2, bias2);
                 const float e0 = seen(tok, ex2(lo_f32(y)), 0.f), e1 = seen(tok + 1, ex2(hi_f32(y)), 0.f);
                 mx[x & 3] = fmaxf(mx[x & 3], fmaxf(seen(tok, __uint_as_float(s0), -INFINITY),
                                                    seen(tok + 1, __uint_as_float(s1), -INFINITY)));
                 sum[x & 1] = add_f32x2(sum[x & 1], pack_f32x2(e0, e1));
-                h[16 * c + x] = pack_half2(e0, e1);
+                h[8 * c + x] = pack_half2(e0, e1);
               }
             }
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
@@ -555,8 +581,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full);
       }
-      mbar_wait(s_full, s_phase, abort, &g_err_kv4prompt, 50);
-      __syncwarp();
+      warp_wait(s_full, s_phase, abort, 50);
       s_phase ^= 1u;
       tc_fence_after();
       // sums stand for value * 2^(ref_v - 127 - 13), weights and sums both times 2^7
@@ -614,127 +639,94 @@ __global__ void __launch_bounds__(kPThreads, 1)
   } else if (warp < kMmaWarp) {
     // ---------------------------------------------- codes to binary16 tiles
     regs_dec<kFillRegs>();
-    const int tk = tid - kSoftWarps * 32;  // token in the tile
-    const int fw = warp - kSoftWarps;
-    struct Raw {
-      uint4 k[D / 32], v[D / 32];
-      uint32_t ks, vs;
-    };
-    Walk it = walk;
-    int k_it = -1;
-    bool more = next_run(a, p, it);
-    // the place of the token of the iterator's next tile
-    int page = -2, off = 0, head = 0;
-    bool have = false;
-    bool first_tile = false;
-    auto step = [&]() {  // looks the token's page up
-      have = false;
-      if (!more) return;
-      if (++k_it >= it.n) {
-        k_it = 0;
-        more = next_run(a, p, it);
-        if (!more) return;
-      }
-      have = true;
-      first_tile = k_it == 0;
-      const int tok = (it.lo / kT + it.tile + k_it) * kT + tk;
-      page = -2;
-      if (tok >= it.lo && tok < it.hi && tok < it.w.s.len) {
-        page = __ldg(a.table + static_cast<int64_t>(it.seq) * a.max_pages + (tok >> a.page_shift));
-        off = tok & (a.page - 1);
-        head = it.kvh;
-      }
-    };
-    auto load = [&](Raw& raw) {
-      raw.ks = raw.vs = 0;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) raw.k[c] = raw.v[c] = make_uint4(0, 0, 0, 0);
-      if (page >= 0 && page < a.n_pages) {
-        const int64_t row = ((static_cast<int64_t>(page) * a.Hkv + head) << a.page_shift) + off;
-        const uint4* pk = reinterpret_cast<const uint4*>(a.k.codes + row * (D / 2));
-        const uint4* pv = reinterpret_cast<const uint4*>(a.v.codes + row * (D / 2));
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          raw.k[c] = __ldg(pk + c);
-          raw.v[c] = __ldg(pv + c);
-        }
-        raw.ks = load_scales<kSB>(a.k.scales + row * kSB);
-        raw.vs = load_scales<kSB>(a.v.scales + row * kSB);
-      } else if (page != -2) {
-        atomicCAS(&g_err_kv4prompt, 0u, kErrArg | (51u << 8));
-      }
-    };
-    // a token's row into a tile: word by word 8 codes, one 16-byte chunk
-    auto put = [&](uint32_t tile, const uint4 (&x)[D / 32], uint32_t scales, float fr) {
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-        const float z = byte_scale((scales >> (8 * (c * 32 / BS))) & 0xFFu) * fr;
-        const __half2 m2 = h2(pack_half2(z, z));
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          uint32_t h[4];
-          e2m1x8_to_half(w[y], h);
-          st_shared16(tile + chunk_at<D>(tk, 4 * c + y), u32(__hmul2(h2(h[0]), m2)), u32(__hmul2(h2(h[1]), m2)),
-                      u32(__hmul2(h2(h[2]), m2)), u32(__hmul2(h2(h[3]), m2)));
-        }
-      }
-    };
+    const bool values = warp >= kValueWarp;
+    const int tk = tid - (values ? kValueWarp : kSoftWarps) * 32;  // token in the tile
+    const int fw = warp - (values ? kValueWarp : kSoftWarps);
+    const uint32_t tiles = values ? sv : sk;
+    uint64_t* const full = values ? ctrl.v_full : ctrl.k_full;
+    uint64_t* const empty = values ? ctrl.v_empty : ctrl.k_empty;
     auto top_of = [](uint32_t w) {
       uint32_t t = 0;
 #pragma unroll
       for (int x = 0; x < kSB; ++x) t = max(t, (w >> (8 * x)) & 0xFFu);
       return t;
     };
-    // one tile ahead: the next one's codes are on their way while this one's
-    // are converted, and the page after that is being looked up
-    Raw raw[2];
-    step();
-    bool now = have, now_first = first_tile;
-    load(raw[0]);
-    step();
+    // Of the token's 16-byte runs of codes a warp's lanes take different ones at
+    // a time (run c + tk/2), and their 8-dim chunks are permuted by the token's
+    // number: reads and writes free of bank conflicts.
+    const uint32_t row_at = tiles + static_cast<uint32_t>(tk) * 128u;
+    const uint32_t swz = static_cast<uint32_t>(tk & 7) << 4;
     int ref_v = 13;
-    auto fill = [&](int count, const Raw& cur, Raw& next) {
+    for (int count = 0, rs = 0, rp = 0;; ++count) {
       const int stage = count & 1;
-      const uint32_t parity = ((count >> 1) & 1) ^ 1u;
-      const bool more_now = have, more_first = first_tile;
-      // the tile's largest scales, over the four warps
-      const uint32_t tk_ = __reduce_max_sync(0xffffffffu, top_of(cur.ks));
-      const uint32_t tv_ = __reduce_max_sync(0xffffffffu, top_of(cur.vs));
-      if (more_now) {
-        load(next);
-        step();
+      warp_wait(smem_u32(&ctrl.raw_full[rs]), rp, abort, 60);
+      const int4 info = ctrl.raw_info[rs];
+      if ((info.w & 2) || *abort) break;
+      const uint8_t* raw = raws + rs * 2 * C::kRawSide;
+      const bool live = info.x + tk >= info.y && info.x + tk < info.z;
+      auto scale_word = [&](const uint8_t* side) -> uint32_t {
+        const uint8_t* sc = side + 128 * D / 2 + tk * kSB;
+        if (!live) return 0u;  // whatever stands there gives zero operands
+        if constexpr (kSB == 4) return *reinterpret_cast<const uint32_t*>(sc);
+        else if constexpr (kSB == 2) return *reinterpret_cast<const uint16_t*>(sc);
+        else return *sc;
+      };
+      const uint8_t* side = raw + (values ? C::kRawSide : 0);
+      const uint32_t word = scale_word(side);
+      // the tile's largest scales, over the four warps; the keys' warps look at
+      // the values' too, for the softmax
+      const uint32_t own = __reduce_max_sync(0xffffffffu, top_of(word));
+      const uint32_t other = values ? 0u : __reduce_max_sync(0xffffffffu, top_of(scale_word(raw + C::kRawSide)));
+      uint4 c[D / 32];
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x)
+        c[x] = *reinterpret_cast<const uint4*>(side + tk * (D / 2) + (((x + (tk >> 1)) & (D / 32 - 1)) << 4));
+      __syncwarp();  // the warp has read the stage
+      if (lane == 0) {
+        ctrl.top[values][stage][fw] = static_cast<int>(own | (other << 8));
+        mbar_arrive(smem_u32(&ctrl.top_full[values][stage]));
+        mbar_arrive(smem_u32(&ctrl.raw_empty[rs]));
       }
-      if (lane == 0) ctrl.top[stage][fw] = static_cast<int>(tk_ | (tv_ << 8));
-      asm volatile("bar.sync 1, %0;" ::"n"(kFillWarps * 32) : "memory");
-      int top_k = 0, top_v = 0;
+      warp_wait(smem_u32(&ctrl.top_full[values][stage]), (count >> 1) & 1, abort, 62);
+      int top = 0, top_v = 0;
 #pragma unroll
       for (int x = 0; x < kFillWarps; ++x) {
-        top_k = max(top_k, ctrl.top[stage][x] & 0xFF);
-        top_v = max(top_v, ctrl.top[stage][x] >> 8);
+        const int t = ctrl.top[values][stage][x];
+        top = max(top, t & 0xFF);
+        top_v = max(top_v, values ? t & 0xFF : t >> 8);
       }
-      const int ref_k = max(top_k, 13);
-      ref_v = max(now_first ? 13 : ref_v, top_v);
-      if (tk == 0) {
-        ctrl.k_info[count & 3] = top_k == 255 ? NAN : pow2w(ref_k - 140);
+      ref_v = max((info.w & 1) ? 13 : ref_v, top_v);
+      const int ref = values ? ref_v : max(top, 13);
+      if (tk == 0 && !values) {
+        ctrl.k_info[count & 3] = top == 255 ? NAN : pow2w(ref - 140);
         ctrl.v_info[count & 3] = ref_v;
       }
-      mbar_wait(smem_u32(&ctrl.k_empty[stage]), parity, abort, &g_err_kv4prompt, 52);
-      put(sk + stage * kTileBytes, cur.k, cur.ks, pow2i(140 - ref_k));
+      const float fr = pow2i(140 - ref);
+      warp_wait(smem_u32(&empty[stage]), ((count >> 1) & 1) ^ 1u, abort, 52);
+      const uint32_t at = row_at + stage * kTileBytes;
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) {
+        const int r = (x + (tk >> 1)) & (D / 32 - 1);
+        const uint32_t w[4] = {c[x].x, c[x].y, c[x].z, c[x].w};
+        const float z = byte_scale((word >> (8 * (r * 32 / BS))) & 0xFFu) * fr;
+        const __half2 m2 = h2(pack_half2(z, z));
+        const uint32_t dst = at + (r >> 1) * C::kHalf;
+        const uint32_t first = (static_cast<uint32_t>(r & 1) << 6) ^ swz;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          uint32_t h[4];
+          e2m1x8_to_half(w[y], h);
+          st_shared16(dst + (first ^ (y << 4)), u32(__hmul2(h2(h[0]), m2)), u32(__hmul2(h2(h[1]), m2)),
+                      u32(__hmul2(h2(h[2]), m2)), u32(__hmul2(h2(h[3]), m2)));
+        }
+      }
       fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ctrl.k_full[stage]));
-      mbar_wait(smem_u32(&ctrl.v_empty[stage]), parity, abort, &g_err_kv4prompt, 53);
-      put(sv + stage * kTileBytes, cur.v, cur.vs, pow2i(140 - ref_v));
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ctrl.v_full[stage]));
-      now = more_now;
-      now_first = more_first;
-    };
-    for (int count = 0; now; count += 2) {
-      fill(count, raw[0], raw[1]);
-      if (now) fill(count + 1, raw[1], raw[0]);
+      if (lane == 0) mbar_arrive(smem_u32(&full[stage]));
+      if (++rs == kRing) {
+        rs = 0;
+        rp ^= 1;
+      }
     }
   } else {
     // ------------------------------------------------------------ products
@@ -747,7 +739,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
         int done = 1;
-        if (lane == 0) done = mbar_wait(smem_u32(bar), parity, abort, &g_err_kv4prompt, site);
+        if (lane == 0) done = quick_wait(smem_u32(bar), parity, abort, &g_err_kv4prompt, site);
         ok = ok && __shfl_sync(0xffffffffu, done, 0) != 0;
         return ok;
       };
@@ -766,7 +758,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         for (int x = 0; x < kT / 16; ++x)
           umma_ts<kDescPV>(tmem + 256 + i * D, tmem + i * 128 + 8 * x, vd + ((x * 2048u) >> 4), !fresh || x > 0);
       };
-      while (ok && next_run(a, p, walk)) {
+      while (ok && advance()) {
+        const int n_tiles = walk.n;
         const int ni = walk.w.s.rows * p.G - walk.group * kGroup > 128 ? 2 : 1;
         for (int i = 0; i < ni && ok; ++i) {
           if (!wait(&ctrl.q_full[i], (q_phase >> i) & 1, 54)) break;
@@ -780,8 +773,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
           __syncwarp();
         }
-        for (int k = 0; k < walk.n && ok; ++k, ++count) {
-          const bool last = k + 1 == walk.n;
+        for (int k = 0; k < n_tiles && ok; ++k, ++count) {
+          const bool last = k + 1 == n_tiles;
           for (int i = 0; i < ni; ++i) {
             if (i == 0 && !wait(&ctrl.v_full[count & 1], (count >> 1) & 1, 57)) break;
             if (i == 0 && !last && !wait(&ctrl.k_full[(count + 1) & 1], ((count + 1) >> 1) & 1, 58)) break;
@@ -803,6 +796,61 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       // the last arrival on this CTA's barriers
       if (count > 0) wait(&ctrl.v_empty[(count - 1) & 1], ((count - 1) >> 1) & 1, 59);
+    } else if (warp == kLoadWarp) {
+      // ------------------------------------------------ codes from the pages
+      // A page's codes and scales of keys and values: a bulk copy a lane.
+      const int chunk_tokens = min(kT, a.page);
+      const int what = lane & 3, chunk_at = (lane >> 2) * chunk_tokens;
+      const bool codes = (what & 1) == 0;
+      const int row_bytes = codes ? D / 2 : kSB;
+      const uint32_t bytes = static_cast<uint32_t>(chunk_tokens * row_bytes);
+      const Side side = what < 2 ? a.k : a.v;
+      const uint8_t* const src = codes ? side.codes : side.scales;
+      const uint32_t dst0 = smem_u32(raws) + (what < 2 ? 0 : C::kRawSide) + (codes ? 0 : 128 * D / 2) +
+                            (lane >> 2) * bytes;
+      int rs = 0;
+      uint32_t rp = 1;
+      auto stage_up = [&]() {
+        if (++rs == kRing) {
+          rs = 0;
+          rp ^= 1u;
+        }
+      };
+      while (advance()) {
+        const int n_tiles = walk.n, lo = walk.lo, hi = walk.hi, kvh = walk.kvh;
+        const int* table = a.table + static_cast<int64_t>(walk.seq) * a.max_pages;
+        int tok0 = (lo / kT + walk.tile) * kT;
+        auto page_of = [&](int t0) {
+          const int tok = t0 + chunk_at;
+          return chunk_at < kT && tok < hi && tok + chunk_tokens > lo ? __ldg(table + (tok >> a.page_shift)) : -2;
+        };
+        int page = page_of(tok0);
+        for (int k = 0; k < n_tiles; ++k, tok0 += kT) {
+          const int next = k + 1 < n_tiles ? page_of(tok0 + kT) : -2;  // a tile early
+          const bool ok = page >= 0 && page < a.n_pages;
+          if (!ok && page != -2) atomicCAS(&g_err_kv4prompt, 0u, kErrArg | (51u << 8));
+          const uint32_t total = __reduce_add_sync(0xffffffffu, ok ? bytes : 0u);
+          warp_wait(smem_u32(&ctrl.raw_empty[rs]), rp, abort, 61);
+          const uint32_t bar = smem_u32(&ctrl.raw_full[rs]);
+          if (lane == 0) {
+            ctrl.raw_info[rs] = make_int4(tok0, lo, hi, k == 0);
+            mbar_arrive_expect_tx(bar, total);
+          }
+          __syncwarp();
+          if (ok) {
+            const int64_t row = ((static_cast<int64_t>(page) * a.Hkv + kvh) << a.page_shift) +
+                                ((tok0 + chunk_at) & (a.page - 1));
+            bulk_copy_g2s(dst0 + rs * 2 * C::kRawSide, src + row * row_bytes, bytes, bar);
+          }
+          stage_up();
+          page = next;
+        }
+      }
+      warp_wait(smem_u32(&ctrl.raw_empty[rs]), rp, abort, 61);
+      if (lane == 0) {
+        ctrl.raw_info[rs] = make_int4(0, 0, 0, 2);
+        mbar_arrive(smem_u32(&ctrl.raw_full[rs]));
+      }
     }
   }
   __syncwarp();
