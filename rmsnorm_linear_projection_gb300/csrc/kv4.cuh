@@ -159,25 +159,26 @@ struct AttnParams {
   int few;  // sequences of up to this many rows (times G) are the few-row kernel's, the others the prompt kernel's
 };
 
-// mbar_wait (ptx.cuh) for waits that are short and many: the hardware suspends
-// the warp for up to 20 us at a time instead of polling in the issue slots that
-// the other warps need.
-__device__ __forceinline__ bool try_wait_long(uint32_t bar, uint32_t parity) {
+// mbar_wait (ptx.cuh) for waits that are short and many: a tight loop first, in
+// which a poll costs few issue slots, the timer only after it.
+__device__ __forceinline__ bool quick_wait(uint32_t bar, uint32_t parity, volatile int* abort, unsigned int* err,
+                                           uint32_t site) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 n;\n\t"
+      "mov.b32 n, 0;\n\t"
+      "POLL:\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "@p bra DONE;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.lt.u32 q, n, 256;\n\t"
+      "@q bra POLL;\n\t"
+      "DONE:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(bar), "r"(parity), "r"(20000)
       : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool quick_wait(uint32_t bar, uint32_t parity, volatile int* abort, unsigned int* err,
-                                           uint32_t site) {
-  for (int n = 0; n < 4; ++n)
-    if (try_wait_long(bar, parity)) return true;
-  return mbar_wait(bar, parity, abort, err, site);
+  return ok != 0 || mbar_wait(bar, parity, abort, err, site);
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {

@@ -7,23 +7,24 @@
 //
 // A CTA works on 256 rows (token x query head of one key head), two tiles of
 // 128, against 128 tokens at a time:
-//   warps 0-3, 4-7   softmax of the two row tiles, a thread a row: scores from
-//                    TMEM, running maximum and sum, weights back to TMEM as
+//   warps 0-7, 8-15  softmax of the two row tiles, two threads a row, half of the
+//                    columns each: scores from TMEM, running maximum and sum, weights back to TMEM as
 //                    binary16 (the A operand of the second product), the sums
-//                    rescaled there when the maximum grew by more than 2^8
-//   warps 8-11,      keys and values, a thread a token: codes and scales from a
-//     12-15          ring in shared memory, converted and scaled into the
+//                    rescaled there when the maximum grew by about 2^9
+//   warps 16-19,     keys and values, a thread a token: codes and scales from a
+//     20-23          ring in shared memory, converted and scaled into the
 //                    operands there (128-byte swizzle; keys K-major, values
 //                    MN-major, the same bytes in the same order)
-//   warp 16          TMEM allocation and, on one thread, every tcgen05.mma:
+//   warp 24          TMEM allocation and, on one thread, every tcgen05.mma:
 //                    S_i = Q_i K^T (both from shared memory), O_i += P_i V
 //                    (P_i from TMEM), i = 0, 1 in turn, so that one row tile's
 //                    softmax runs while the other one's products do
-//   warp 17          bulk copies of the next tiles' codes and scales into the ring
+//   warp 25          bulk copies of the next tiles' codes and scales into the ring
+//   warp 26          walks the CTA's range and tells the others its runs
 // TMEM: S_0, S_1 (128 columns each; P_i takes the first 64 of S_i), O_0, O_1.
 //
-// The weights are 2^(x - m + 7) with m at most 2^8 behind the true maximum:
-// binary16 holds them with 11 bits down to 2^-21 of the largest.
+// The weights are 2^(x - m + 7) with m at most 9 behind the true maximum:
+// binary16 holds them with 11 bits down to 2^-21 of the largest, or less.
 //
 // Rows later in a causal prompt read more tokens.  An item is a pair of row
 // groups, one from either end, so that all items of a sequence have about the
@@ -44,33 +45,33 @@ __device__ unsigned int g_err_kv4prompt;
 
 constexpr int kT = 128;            // tokens a tile
 constexpr int kGroup = 256;        // rows a CTA holds
-constexpr int kSoftWarps = 8;
+constexpr int kSoftWarps = 16;
 constexpr int kFillWarps = 4;      // for the keys, and as many for the values
 constexpr int kValueWarp = kSoftWarps + kFillWarps;
 constexpr int kMmaWarp = kValueWarp + kFillWarps;
 constexpr int kLoadWarp = kMmaWarp + 1;
-constexpr int kMaxRing = 3;
-constexpr int kPWarps = 20;        // whole warpgroups; warps 18 and 19 idle
+constexpr int kWalkWarp = kLoadWarp + 1;
+constexpr int kMaxRing = 6;
+constexpr int kPWarps = 28;        // whole warpgroups; warp 27 idle
 constexpr int kPThreads = kPWarps * 32;
 // registers a thread after the roles part, within what the block is launched with
-constexpr int kLaunchRegs = 96, kSoftRegs = 152, kFillRegs = 56, kMmaRegs = 64;
-static_assert(8 * kSoftRegs + 8 * kFillRegs + 4 * kMmaRegs <= kPWarps * kLaunchRegs, "register file");
+constexpr int kLaunchRegs = 72, kSoftRegs = 88, kFillRegs = 48, kMmaRegs = 56;
+static_assert(16 * kSoftRegs + 8 * kFillRegs + 4 * kMmaRegs <= kPWarps * kLaunchRegs, "register file");
 // what a group costs beside its tiles (queries, output), in tiles
 constexpr int kGroupCost = 3;
 constexpr int kMaxPromptCtas = 160;
-constexpr float kLag = 8.f;        // log2 of how far the maximum may run ahead of the one in use
-constexpr float kTop = 7.f;        // weights are scaled by 2^7: at most 2^15 with the lag
+constexpr float kTop = 7.f;        // weights are scaled by 2^7: room for 2^9 above the maximum in use
 
 template <int D>
 struct PCfg {
   static constexpr uint32_t kTileBytes = 128u * D * 2;    // Q_i, K or V in shared memory
   static constexpr uint32_t kHalf = 128u * 128;           // bytes between blocks of 64 dims
-  // a tile's codes and scales (room for blocks of 32) of keys, then of values
-  static constexpr uint32_t kRawSide = 128u * D / 2 + 128u * D / 32;
-  // tiles of codes under way, beside the one that the fill warps hold in
-  // registers: what shared memory has room for
-  static constexpr int kRing = D == 128 ? 1 : kMaxRing;
-  static constexpr size_t kSmem = 1024 + 6 * static_cast<size_t>(kTileBytes) + kRing * 2 * kRawSide;
+  // The ring's places hold a tile's keys (codes, scales, and the values' scales)
+  // or its values (codes, scales), by turns; as many as there is room for.
+  static constexpr uint32_t kRawCodes = 128u * D / 2, kRawScales = 128u * D / 32;
+  static constexpr uint32_t kRaw = kRawCodes + 2 * kRawScales;
+  static constexpr int kRing = D == 128 ? 3 : kMaxRing;
+  static constexpr size_t kSmem = 1024 + 6 * static_cast<size_t>(kTileBytes) + kRing * kRaw;
   static constexpr int kSlot = kGroup * (D + 2);          // floats of a partial: sums, maxima, weights
 };
 
@@ -196,20 +197,31 @@ __device__ __forceinline__ bool next_run(const Args& a, const AttnParams& p, Wal
   return false;
 }
 
+// A run as the roles read it.
+struct Run {
+  int row0, rows, len;         // the sequence
+  int groups, group, seq, kvh;
+  int lo, tile, n, all;        // tokens from lo on, in tiles: first, number, number of the whole group
+  int hi, stop;
+  int64_t unit;
+};
+constexpr int kRuns = 4;
+
 struct __align__(16) PCtrl {
   uint64_t q_full[2], s_full[2], p_full[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t raw_full[kMaxRing], raw_empty[kMaxRing];
-  uint64_t top_full[2][2];   // the fill warps' largest scales are in `top`
-  Walk walk[kLoadWarp + 1];  // a place for each warp that walks
+  uint64_t run_full[kRuns], run_empty[kRuns];
+  Run run[kRuns];
   int4 raw_info[kMaxRing];      // first token, the group's tokens, 1: a run's first tile, 2: no more tiles
+  float half[2][2][128];   // what a row's two halves tell each other
   float k_info[4];   // score factor of tile x at x % 4
   int v_info[4];     // the values' reference scale byte
-  int top[2][2][kFillWarps];
+  int top[2][2][kFillWarps], stop[2], done[2][2];
   long long sum[kPWarps];
   long long off;
   uint32_t tmem;
-  int b, abort, more[kLoadWarp + 1];
+  int b, abort;
 };
 
 // Low word of a shared-memory descriptor: start address and leading offset
@@ -276,26 +288,37 @@ __device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, volatil
   __syncwarp();
 }
 
-// Two binary32 in one 64-bit register: one instruction for both.
-__device__ __forceinline__ uint64_t pack_u32x2(uint32_t lo, uint32_t hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
-  return d;
+// The same for waits with slack: the warp sleeps between polls.
+__device__ __forceinline__ void idle_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t site) {
+  for (int n = 0; n < 64; ++n) {
+    if (mbar_try_wait(bar, parity)) break;
+    __nanosleep(64);
+  }
+  warp_wait(bar, parity, abort, site);
 }
-__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
-  return pack_u32x2(__float_as_uint(lo), __float_as_uint(hi));
+
+// Named barriers.  A warp that polls takes issue slots from those that work:
+// of the warps that wait for the same thing one polls, the others stand at a
+// named barrier, which costs nothing.
+//   1-8 the two warps that share rows, 9-10 a row tile's warps, 11-12 the warps
+//   that fill keys, values
+template <int WARPS>
+__device__ __forceinline__ void meet(int bar) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(bar), "n"(WARPS * 32) : "memory");
 }
-__device__ __forceinline__ float lo_f32(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a)); }
-__device__ __forceinline__ float hi_f32(uint64_t a) { return __uint_as_float(static_cast<uint32_t>(a >> 32)); }
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
+__device__ __forceinline__ void pair_sync(int bar) { meet<2>(bar); }
+// The two warps that share rows meet with the logical or of a flag.
+__device__ __forceinline__ bool pair_or(int bar, bool flag) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(bar), "r"(static_cast<uint32_t>(flag))
+      : "memory");
+  return r != 0;
 }
 
 // Where 16-byte chunk c (8 dims) of row r of a 128-row operand lies: blocks of
@@ -306,6 +329,29 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
          static_cast<uint32_t>(((c & 7) ^ (r & 7)) << 4);
 }
 
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+// N bytes (1, 2 or 4) in one word.
+template <int N>
+__device__ __forceinline__ uint32_t ld_shared(uint32_t addr) {
+  uint32_t v;
+  if constexpr (N == 4) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  } else if constexpr (N == 2) {
+    uint16_t h;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(addr) : "memory");
+    v = h;
+  } else {
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  }
+  return v;
+}
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
@@ -328,18 +374,21 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&ctrl.q_full[i]), 4);
+      mbar_init(smem_u32(&ctrl.q_full[i]), 8);
       mbar_init(smem_u32(&ctrl.s_full[i]), 1);
-      mbar_init(smem_u32(&ctrl.p_full[i]), 4);
+      mbar_init(smem_u32(&ctrl.p_full[i]), 8);
       mbar_init(smem_u32(&ctrl.k_full[i]), kFillWarps);
       mbar_init(smem_u32(&ctrl.k_empty[i]), 1);
       mbar_init(smem_u32(&ctrl.v_full[i]), kFillWarps);
       mbar_init(smem_u32(&ctrl.v_empty[i]), 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&ctrl.top_full[i >> 1][i & 1]), kFillWarps);
+    for (int i = 0; i < kRuns; ++i) {
+      mbar_init(smem_u32(&ctrl.run_full[i]), 1);
+      mbar_init(smem_u32(&ctrl.run_empty[i]), kSoftWarps + 2);  // softmax, products, loads
+    }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(smem_u32(&ctrl.raw_full[i]), 1);
-      mbar_init(smem_u32(&ctrl.raw_empty[i]), 2 * kFillWarps);
+      mbar_init(smem_u32(&ctrl.raw_empty[i]), kFillWarps);
     }
     ctrl.abort = 0;
     ctrl.b = -1;
@@ -391,27 +440,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
     before += all;
   }
   if (ctrl.b < 0) return;  // lengths changed under the call
-  // Every warp walks the range on its own; its place lies in shared memory, one
-  // lane moves it, and the warp reads the run from there.
-  Walk& walk = ctrl.walk[min(warp, kLoadWarp)];
-  if (lane == 0 && warp <= kLoadWarp) {
-    walk.b = ctrl.b;
-    load_span(a, p, walk.b, walk.w);
-    const int64_t per_head = head_units(p, walk.w);
-    const int len = pair_units(p, walk.w);
-    walk.head = static_cast<int>(ctrl.off / per_head);
-    const int64_t in_head = ctrl.off - walk.head * per_head;
-    walk.pair = static_cast<int>(min(in_head / len, static_cast<int64_t>(walk.w.groups / 2)));
-    walk.off = static_cast<int>(in_head - static_cast<int64_t>(walk.pair) * len);
-    walk.at = u0;
-    walk.left = u1 - u0;
-  }
-  auto advance = [&]() {
-    __syncwarp();
-    if (lane == 0) ctrl.more[warp] = next_run(a, p, walk);
-    __syncwarp();
-    return ctrl.more[warp] != 0;
-  };
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&ctrl.tmem), 512);
     tmem_relinquish();
@@ -424,51 +452,67 @@ __global__ void __launch_bounds__(kPThreads, 1)
   if (warp < kSoftWarps) {
     // ------------------------------------------------------------- softmax
     regs_inc<kSoftRegs>();
-    const int i = warp >> 2;                    // row tile
+    const int i = warp >> 3;                    // row tile
+    const int half = (warp >> 2) & 1;           // of its columns: tokens, dims
+    const int pair_bar = 1 + i * 4 + (warp & 3);  // the two warps that share rows
     const int rw = (warp & 3) * 32 + lane;      // row in it
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + i * 128, to = tmem + lanes + 256 + i * D;
+    const uint32_t ts = tmem + lanes + i * 128 + half * 64, tp = tmem + lanes + i * 128 + half * 32,
+                   to = tmem + lanes + 256 + i * D + half * (D / 2);
     const uint32_t q_full = smem_u32(&ctrl.q_full[i]), s_full = smem_u32(&ctrl.s_full[i]),
                    p_full = smem_u32(&ctrl.p_full[i]);
     uint32_t s_phase = 0;
     int count = 0;  // tiles so far
     // a wait that gives up (a bug) ends every later wait at once: the loops run
     // on to their ends, so that the warp-wide instructions stay together
-    for (int run = 0; advance(); ++run) {
-      const int n_tiles = walk.n;
-      const int all_rows = walk.w.s.rows * p.G, r0 = walk.group * kGroup;
+    for (int nth = 0;; ++nth) {
+      const Run& run = ctrl.run[nth % kRuns];
+      if ((warp & 7) == 1 + i) {
+        warp_wait(smem_u32(&ctrl.run_full[nth % kRuns]), (nth / kRuns) & 1, abort, 63);
+        if (lane == 0) ctrl.done[i][nth & 1] = run.stop || *abort;
+      }
+      meet<8>(9 + i);
+      if (ctrl.done[i][nth & 1]) break;  // all eight warps alike
+      const int n_tiles = run.n;
+      const int all_rows = run.rows * p.G, r0 = run.group * kGroup;
       if (r0 + i * 128 >= all_rows) {  // no row of this tile
         count += n_tiles;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctrl.run_empty[nth % kRuns]));
         continue;
       }
       const int r = r0 + i * 128 + rw;
       const int rc = min(r, all_rows - 1), tok_q = rc / p.G;
-      const int pos = p.causal ? walk.w.s.len - walk.w.s.rows + tok_q : walk.w.s.len - 1;
+      const int head = run.kvh * p.G + (rc - tok_q * p.G);
+      const int pos = p.causal ? run.len - run.rows + tok_q : run.len - 1;
       const int first = p.window > 0 ? pos - p.window + 1 : 0;  // first token the row reads
       float f_row;
       {
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (walk.w.s.row0 + tok_q) * p.q_stride +
-                                                          static_cast<int64_t>(walk.kvh * p.G + (rc - tok_q * p.G)) * D);
-        uint4 w[D / 8];
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (run.row0 + tok_q) * p.q_stride +
+                                                          static_cast<int64_t>(head) * D + half * (D / 2));
+        uint4 w[D / 16];
         uint32_t am = 0;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) w[c] = __ldg(src + c);
+        for (int c = 0; c < D / 16; ++c) w[c] = __ldg(src + c);
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
+        for (int c = 0; c < D / 16; ++c) {
           const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
           for (int y = 0; y < 4; ++y) am = max(am, max((x[y] << 16) & 0x7FFFFFFFu, x[y] & 0x7FFF0000u));
         }
+        ctrl.half[i][half][rw] = __uint_as_float(am);
+        pair_sync(pair_bar);
+        am = max(am, __float_as_uint(ctrl.half[i][half ^ 1][rw]));
         const int e = 141 - max(static_cast<int>(am >> 23), 1);
         const float s1 = p.scale_log2 < 0.f ? -pow2i(e / 2) : pow2i(e / 2), s2 = pow2i(e - e / 2);
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
+        for (int c = 0; c < D / 16; ++c) {
           const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
           uint32_t h[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y)
             h[y] = pack_half2(__uint_as_float(x[y] << 16) * s1 * s2, __uint_as_float(x[y] & 0xFFFF0000u) * s1 * s2);
-          st_shared16(sq + i * kTileBytes + chunk_at<D>(rw, c), h[0], h[1], h[2], h[3]);
+          st_shared16(sq + i * kTileBytes + chunk_at<D>(rw, half * (D / 16) + c), h[0], h[1], h[2], h[3]);
         }
         f_row = fabsf(p.scale_log2) * pow2w(-e);
       }
@@ -478,77 +522,78 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
       float m = -INFINITY, l = 0.f;
       int ref_v = 13;
-      const int tile0 = (walk.lo / kT + walk.tile) * kT;
+      const int tile0 = (run.lo / kT + run.tile) * kT;
       for (int k = 0; k < n_tiles; ++k, ++count) {
-        warp_wait(s_full, s_phase, abort, 49);
+        if ((warp & 7) == 1 + i) warp_wait(s_full, s_phase, abort, 49);
+        meet<8>(9 + i);
         s_phase ^= 1u;
         tc_fence_after();
         float f = f_row * ctrl.k_info[count & 3];
         if (f < 1e-37f) f = 1e-37f;  // not 0, for masked scores (-infinity) times it
         const int new_v = ctrl.v_info[count & 3];
-        const int tok0 = tile0 + k * kT;
-        const bool whole = __all_sync(0xffffffffu, tok0 + kT - 1 <= pos && tok0 >= first);
+        const int tok0 = tile0 + k * kT + half * 64;
+        const bool whole = __all_sync(0xffffffffu, tok0 + 63 <= pos && tok0 >= first);
         float alpha = 1.f;
-        uint32_t h[64];  // the row's weights, binary16 pairs
+        uint32_t h[32];  // the half row's weights, binary16 pairs
         auto tile = [&](auto masked) {  // kept apart: the mask's tests stay out of whole tiles
           constexpr bool kMasked = decltype(masked)::value;
           auto seen = [&](int tok, float v, float other) { return !kMasked || (tok <= pos && tok >= first) ? v : other; };
-          // The maximum in use serves while the row's scores stay within 2^8 of
-          // it, which one pass over the scores finds while it computes the
-          // weights; where it does not (a run's first tile, or a row of the warp
-          // far above what it saw) the maximum is taken first.
+          // The maximum in use serves while the row's weights stay within
+          // binary16, about 2^9 above it, which one pass over the scores finds
+          // while it computes them; where it does not (a run's first tile, or a
+          // row of the warp far above what it saw) the maximum is taken first.
           bool exact = __any_sync(0xffffffffu, m == -INFINITY);
           for (;;) {
-            uint32_t s[2][16];
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            uint32_t s[32];
             if (exact) {
-              tmem_ld_16cols(ts, s[0]);
+              float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int c = 0; c < 8; ++c) {
+              for (int c = 0; c < 2; ++c) {
+                tmem_ld_32cols(ts + 32 * c, s);
                 tmem_ld_wait();
-                if (c < 7) tmem_ld_16cols(ts + 16 * (c + 1), s[(c + 1) & 1]);
 #pragma unroll
-                for (int x = 0; x < 16; x += 2) {
-                  const int tok = tok0 + 16 * c + x;
-                  mx[(x >> 1) & 3] = fmaxf(mx[(x >> 1) & 3],
-                                           fmaxf(seen(tok, __uint_as_float(s[c & 1][x]), -INFINITY),
-                                                 seen(tok + 1, __uint_as_float(s[c & 1][x + 1]), -INFINITY)));
+                for (int x = 0; x < 32; x += 2) {
+                  const int tok = tok0 + 32 * c + x;
+                  mx[(x >> 1) & 3] = fmaxf(mx[(x >> 1) & 3], fmaxf(seen(tok, __uint_as_float(s[x]), -INFINITY),
+                                                                   seen(tok + 1, __uint_as_float(s[x + 1]), -INFINITY)));
                 }
               }
-              const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
-              if (top > m + kLag || (m == -INFINITY && top > m)) {
+              float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
+              ctrl.half[i][half][rw] = top;
+              pair_sync(pair_bar);
+              top = fmaxf(top, ctrl.half[i][half ^ 1][rw]);
+              if (top > m) {
                 alpha = ex2(m - top);
                 m = top;
                 l *= alpha;
               }
             }
             const float bias = kTop - (m == -INFINITY ? 0.f : m);
-            const uint64_t f2 = pack_f32x2(f, f), bias2 = pack_f32x2(bias, bias);
-            uint64_t sum[2] = {0, 0};
-            tmem_ld_16cols(ts, s[0]);
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < 2; ++c) {
+              tmem_ld_32cols(ts + 32 * c, s);
               tmem_ld_wait();
-              if (c < 7) tmem_ld_16cols(ts + 16 * (c + 1), s[(c + 1) & 1]);
 #pragma unroll
-              for (int x = 0; x < 8; ++x) {
-                const uint32_t s0 = s[c & 1][2 * x], s1 = s[c & 1][2 * x + 1];
-                const int tok = tok0 + 16 * c + 2 * x;
-                const uint64_t y = fma_f32x2(pack_u32x2(s0, s1), f2, bias2);
-                const float e0 = seen(tok, ex2(lo_f32(y)), 0.f), e1 = seen(tok + 1, ex2(hi_f32(y)), 0.f);
-                mx[x & 3] = fmaxf(mx[x & 3], fmaxf(seen(tok, __uint_as_float(s0), -INFINITY),
-                                                   seen(tok + 1, __uint_as_float(s1), -INFINITY)));
-                sum[x & 1] = add_f32x2(sum[x & 1], pack_f32x2(e0, e1));
-                h[8 * c + x] = pack_half2(e0, e1);
+              for (int x = 0; x < 16; ++x) {
+                const int tok = tok0 + 32 * c + 2 * x;
+                const float e0 = seen(tok, ex2(fmaf(__uint_as_float(s[2 * x]), f, bias)), 0.f);
+                const float e1 = seen(tok + 1, ex2(fmaf(__uint_as_float(s[2 * x + 1]), f, bias)), 0.f);
+                sum[2 * (x & 1)] += e0;
+                sum[2 * (x & 1) + 1] += e1;
+                h[16 * c + x] = pack_half2(e0, e1);
               }
             }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
-            if (!exact && __any_sync(0xffffffffu, top > m + kLag)) {
+            // The weights are positive: none is beyond binary16 (65504) if their
+            // sum is not, so that the sum says whether the maximum in use still
+            // serves.  Both warps of the rows have read their scores here, and
+            // take the same way.
+            const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            if (pair_or(pair_bar, !exact && !(all < 65504.f))) {
               exact = true;
               continue;
             }
-            sum[0] = add_f32x2(sum[0], sum[1]);
-            l += lo_f32(sum[0]) + hi_f32(sum[0]);
+            l += all;
             break;
           }
         };
@@ -557,8 +602,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         else
           tile(std::true_type{});
         // into the columns whose scores have been read
-        tmem_st_32cols(ts, *reinterpret_cast<uint32_t(*)[32]>(&h[0]));
-        tmem_st_32cols(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(&h[32]));
+        tmem_st_32cols(tp, h);
         if (new_v != ref_v) {
           alpha *= pow2i(ref_v - new_v);
           ref_v = new_v;
@@ -567,7 +611,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         // tile's scores came after them)
         if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 0; c < D / 64; ++c) {
             uint32_t s[32];
             tmem_ld_32cols(to + 32 * c, s);
             tmem_ld_wait();
@@ -581,18 +625,22 @@ __global__ void __launch_bounds__(kPThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full);
       }
-      warp_wait(s_full, s_phase, abort, 50);
+      if ((warp & 7) == 1 + i) warp_wait(s_full, s_phase, abort, 50);
+      meet<8>(9 + i);
       s_phase ^= 1u;
       tc_fence_after();
       // sums stand for value * 2^(ref_v - 127 - 13), weights and sums both times 2^7
-      const bool complete = walk.n == walk.all;
+      const bool complete = run.n == run.all;
+      ctrl.half[i][half][rw] = l;
+      pair_sync(pair_bar);
+      l += ctrl.half[i][half ^ 1][rw];
       const float inv = complete ? (l != 0.f ? 1.f / l : 0.f) : 1.f / 128.f;
       const float fa = pow2i((ref_v - 140) / 2), fb = pow2i(ref_v - 140 - (ref_v - 140) / 2) * (ref_v == 255 ? NAN : 1.f);
-      const int64_t orow = static_cast<int64_t>(walk.w.s.row0 + tok_q) * p.Hq + walk.kvh * p.G + (rc - tok_q * p.G);
-      float* slot = p.part + static_cast<int64_t>(2 * cta + (run > 0)) * C::kSlot;
+      const int64_t orow = static_cast<int64_t>(run.row0 + tok_q) * p.Hq + head;
+      float* slot = p.part + static_cast<int64_t>(2 * cta + (nth > 0)) * C::kSlot;
       const int rg = i * 128 + rw;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < D / 64; ++c) {
         uint32_t s[32];
         tmem_ld_32cols(to + 32 * c, s);
         tmem_ld_wait();
@@ -601,7 +649,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         for (int x = 0; x < 32; ++x) v[x] = __uint_as_float(s[x]) * inv * fa * fb;
         if (r < all_rows) {
           if (complete) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + 32 * c);
+            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + half * (D / 2) + 32 * c);
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               uint32_t w[4];
@@ -613,14 +661,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
               dst[y] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else {
-            float4* dst = reinterpret_cast<float4*>(slot + rg * D + 32 * c);
+            float4* dst = reinterpret_cast<float4*>(slot + rg * D + half * (D / 2) + 32 * c);
 #pragma unroll
             for (int y = 0; y < 8; ++y) dst[y] = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
           }
         }
       }
       tc_fence_before();  // the next run's products overwrite these sums
-      if (r < all_rows) {
+      if (r < all_rows && half == 0) {
         const float lt = l * (1.f / 128.f);
         if (complete) {
           if (p.lse != nullptr) p.lse[orow] = lt != 0.f ? m * kLn2 + logf(lt) : -INFINITY;
@@ -630,11 +678,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
       }
       // a group that begins here and goes on in later CTAs
-      if (i == 0 && rw == 0 && walk.tile == 0 && !complete) {
-        const int64_t end = walk.unit + walk.all;
-        p.rec[cta] = make_int4(walk.kvh * walk.w.groups + walk.group, walk.seq,
-                               static_cast<int>((end * ctas - 1) / units), run > 0);
+      if (i == 0 && half == 0 && rw == 0 && run.tile == 0 && !complete) {
+        const int64_t end = run.unit + run.all;
+        p.rec[cta] = make_int4(run.kvh * run.groups + run.group, run.seq,
+                               static_cast<int>((end * ctas - 1) / units), nth > 0);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctrl.run_empty[nth % kRuns]));
     }
   } else if (warp < kMmaWarp) {
     // ---------------------------------------------- codes to binary16 tiles
@@ -643,8 +693,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int tk = tid - (values ? kValueWarp : kSoftWarps) * 32;  // token in the tile
     const int fw = warp - (values ? kValueWarp : kSoftWarps);
     const uint32_t tiles = values ? sv : sk;
-    uint64_t* const full = values ? ctrl.v_full : ctrl.k_full;
-    uint64_t* const empty = values ? ctrl.v_empty : ctrl.k_empty;
+    const uint32_t full = smem_u32(values ? ctrl.v_full : ctrl.k_full);
+    const uint32_t empty = smem_u32(values ? ctrl.v_empty : ctrl.k_empty);
     auto top_of = [](uint32_t w) {
       uint32_t t = 0;
 #pragma unroll
@@ -657,37 +707,37 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const uint32_t row_at = tiles + static_cast<uint32_t>(tk) * 128u;
     const uint32_t swz = static_cast<uint32_t>(tk & 7) << 4;
     int ref_v = 13;
-    for (int count = 0, rs = 0, rp = 0;; ++count) {
+    for (int count = 0, rs = values ? 1 : 0, rp = 0;; ++count) {
       const int stage = count & 1;
-      warp_wait(smem_u32(&ctrl.raw_full[rs]), rp, abort, 60);
+      if (fw == 3) {  // polling warps on different schedulers
+        idle_wait(smem_u32(&ctrl.raw_full[rs]), rp, abort, 60);
+        if (lane == 0) ctrl.stop[values] = (ctrl.raw_info[rs].w & 2) || *abort;
+      }
+      meet<kFillWarps>(11 + values);
+      if (ctrl.stop[values]) break;  // all four warps alike
       const int4 info = ctrl.raw_info[rs];
-      if ((info.w & 2) || *abort) break;
-      const uint8_t* raw = raws + rs * 2 * C::kRawSide;
+      const uint32_t raw = smem_u32(raws) + rs * C::kRaw;
       const bool live = info.x + tk >= info.y && info.x + tk < info.z;
-      auto scale_word = [&](const uint8_t* side) -> uint32_t {
-        const uint8_t* sc = side + 128 * D / 2 + tk * kSB;
-        if (!live) return 0u;  // whatever stands there gives zero operands
-        if constexpr (kSB == 4) return *reinterpret_cast<const uint32_t*>(sc);
-        else if constexpr (kSB == 2) return *reinterpret_cast<const uint16_t*>(sc);
-        else return *sc;
+      auto scale_word = [&](uint32_t of) -> uint32_t {
+        return live ? ld_shared<kSB>(of + tk * kSB) : 0u;  // else: whatever stands there gives zero operands
       };
-      const uint8_t* side = raw + (values ? C::kRawSide : 0);
-      const uint32_t word = scale_word(side);
+      const uint32_t word = scale_word(raw + C::kRawCodes);
       // the tile's largest scales, over the four warps; the keys' warps look at
       // the values' too, for the softmax
       const uint32_t own = __reduce_max_sync(0xffffffffu, top_of(word));
-      const uint32_t other = values ? 0u : __reduce_max_sync(0xffffffffu, top_of(scale_word(raw + C::kRawSide)));
+      const uint32_t other =
+          values ? 0u : __reduce_max_sync(0xffffffffu, top_of(scale_word(raw + C::kRawCodes + C::kRawScales)));
       uint4 c[D / 32];
 #pragma unroll
       for (int x = 0; x < D / 32; ++x)
-        c[x] = *reinterpret_cast<const uint4*>(side + tk * (D / 2) + (((x + (tk >> 1)) & (D / 32 - 1)) << 4));
+        c[x] = ld_shared16(raw + tk * (D / 2) + (((x + (tk >> 1)) & (D / 32 - 1)) << 4));
       __syncwarp();  // the warp has read the stage
       if (lane == 0) {
         ctrl.top[values][stage][fw] = static_cast<int>(own | (other << 8));
-        mbar_arrive(smem_u32(&ctrl.top_full[values][stage]));
         mbar_arrive(smem_u32(&ctrl.raw_empty[rs]));
       }
-      warp_wait(smem_u32(&ctrl.top_full[values][stage]), (count >> 1) & 1, abort, 62);
+      if (fw == 3) idle_wait(empty + 8 * stage, ((count >> 1) & 1) ^ 1u, abort, 52);
+      meet<kFillWarps>(11 + values);
       int top = 0, top_v = 0;
 #pragma unroll
       for (int x = 0; x < kFillWarps; ++x) {
@@ -702,7 +752,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
         ctrl.v_info[count & 3] = ref_v;
       }
       const float fr = pow2i(140 - ref);
-      warp_wait(smem_u32(&empty[stage]), ((count >> 1) & 1) ^ 1u, abort, 52);
       const uint32_t at = row_at + stage * kTileBytes;
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) {
@@ -722,9 +771,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&full[stage]));
-      if (++rs == kRing) {
-        rs = 0;
+      if (lane == 0) mbar_arrive(full + 8 * stage);
+      rs += 2;  // keys and values by turns
+      if (rs >= kRing) {
+        rs -= kRing;
         rp ^= 1;
       }
     }
@@ -758,9 +808,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
         for (int x = 0; x < kT / 16; ++x)
           umma_ts<kDescPV>(tmem + 256 + i * D, tmem + i * 128 + 8 * x, vd + ((x * 2048u) >> 4), !fresh || x > 0);
       };
-      while (ok && advance()) {
-        const int n_tiles = walk.n;
-        const int ni = walk.w.s.rows * p.G - walk.group * kGroup > 128 ? 2 : 1;
+      for (int nth = 0; ok; ++nth) {
+        if (!wait(&ctrl.run_full[nth % kRuns], (nth / kRuns) & 1, 64)) break;
+        const Run& run = ctrl.run[nth % kRuns];
+        if (run.stop) break;
+        const int n_tiles = run.n;
+        const int ni = run.rows * p.G - run.group * kGroup > 128 ? 2 : 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctrl.run_empty[nth % kRuns]));
         for (int i = 0; i < ni && ok; ++i) {
           if (!wait(&ctrl.q_full[i], (q_phase >> i) & 1, 54)) break;
           q_phase ^= 1u << i;
@@ -798,15 +853,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (count > 0) wait(&ctrl.v_empty[(count - 1) & 1], ((count - 1) >> 1) & 1, 59);
     } else if (warp == kLoadWarp) {
       // ------------------------------------------------ codes from the pages
-      // A page's codes and scales of keys and values: a bulk copy a lane.
+      // A bulk copy a lane: of a page's codes, scales or (with the keys) the
+      // values' scales.
       const int chunk_tokens = min(kT, a.page);
       const int what = lane & 3, chunk_at = (lane >> 2) * chunk_tokens;
-      const bool codes = (what & 1) == 0;
-      const int row_bytes = codes ? D / 2 : kSB;
+      const int row_bytes = what == 0 ? D / 2 : kSB;
       const uint32_t bytes = static_cast<uint32_t>(chunk_tokens * row_bytes);
-      const Side side = what < 2 ? a.k : a.v;
-      const uint8_t* const src = codes ? side.codes : side.scales;
-      const uint32_t dst0 = smem_u32(raws) + (what < 2 ? 0 : C::kRawSide) + (codes ? 0 : 128 * D / 2) +
+      const uint32_t dst0 = smem_u32(raws) + (what == 0 ? 0 : C::kRawCodes + (what - 1) * C::kRawScales) +
                             (lane >> 2) * bytes;
       int rs = 0;
       uint32_t rp = 1;
@@ -816,10 +869,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
           rp ^= 1u;
         }
       };
-      while (advance()) {
-        const int n_tiles = walk.n, lo = walk.lo, hi = walk.hi, kvh = walk.kvh;
-        const int* table = a.table + static_cast<int64_t>(walk.seq) * a.max_pages;
-        int tok0 = (lo / kT + walk.tile) * kT;
+      for (int nth = 0;; ++nth) {
+        idle_wait(smem_u32(&ctrl.run_full[nth % kRuns]), (nth / kRuns) & 1, abort, 65);
+        const Run& run = ctrl.run[nth % kRuns];
+        if (__any_sync(0xffffffffu, run.stop || *abort)) break;
+        const int n_tiles = run.n, lo = run.lo, hi = run.hi, kvh = run.kvh;
+        const int* table = a.table + static_cast<int64_t>(run.seq) * a.max_pages;
+        int tok0 = (lo / kT + run.tile) * kT;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctrl.run_empty[nth % kRuns]));
         auto page_of = [&](int t0) {
           const int tok = t0 + chunk_at;
           return chunk_at < kT && tok < hi && tok + chunk_tokens > lo ? __ldg(table + (tok >> a.page_shift)) : -2;
@@ -829,27 +887,60 @@ __global__ void __launch_bounds__(kPThreads, 1)
           const int next = k + 1 < n_tiles ? page_of(tok0 + kT) : -2;  // a tile early
           const bool ok = page >= 0 && page < a.n_pages;
           if (!ok && page != -2) atomicCAS(&g_err_kv4prompt, 0u, kErrArg | (51u << 8));
-          const uint32_t total = __reduce_add_sync(0xffffffffu, ok ? bytes : 0u);
-          warp_wait(smem_u32(&ctrl.raw_empty[rs]), rp, abort, 61);
-          const uint32_t bar = smem_u32(&ctrl.raw_full[rs]);
-          if (lane == 0) {
-            ctrl.raw_info[rs] = make_int4(tok0, lo, hi, k == 0);
-            mbar_arrive_expect_tx(bar, total);
-          }
-          __syncwarp();
-          if (ok) {
-            const int64_t row = ((static_cast<int64_t>(page) * a.Hkv + kvh) << a.page_shift) +
-                                ((tok0 + chunk_at) & (a.page - 1));
-            bulk_copy_g2s(dst0 + rs * 2 * C::kRawSide, src + row * row_bytes, bytes, bar);
+          const int64_t row = ((static_cast<int64_t>(page) * a.Hkv + kvh) << a.page_shift) +
+                              ((tok0 + chunk_at) & (a.page - 1));
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {  // keys, values
+            const bool mine = ok && what < (v ? 2 : 3);
+            const uint8_t* src = what == 0 ? (v ? a.v.codes : a.k.codes) : (v || what == 2 ? a.v.scales : a.k.scales);
+            const uint32_t total = __reduce_add_sync(0xffffffffu, mine ? bytes : 0u);
+            idle_wait(smem_u32(&ctrl.raw_empty[rs]), rp, abort, 61);
+            const uint32_t bar = smem_u32(&ctrl.raw_full[rs]);
+            if (lane == 0) {
+              ctrl.raw_info[rs] = make_int4(tok0, lo, hi, k == 0);
+              mbar_arrive_expect_tx(bar, total);
+            }
+            __syncwarp();
+            if (mine) bulk_copy_g2s(dst0 + rs * C::kRaw, src + row * row_bytes, bytes, bar);
+            if (v == 0) stage_up();
           }
           stage_up();
           page = next;
         }
       }
-      warp_wait(smem_u32(&ctrl.raw_empty[rs]), rp, abort, 61);
-      if (lane == 0) {
-        ctrl.raw_info[rs] = make_int4(0, 0, 0, 2);
-        mbar_arrive(smem_u32(&ctrl.raw_full[rs]));
+      for (int v = 0; v < 2; ++v) {
+        idle_wait(smem_u32(&ctrl.raw_empty[rs]), rp, abort, 61);
+        if (lane == 0) {
+          ctrl.raw_info[rs] = make_int4(0, 0, 0, 2);
+          mbar_arrive(smem_u32(&ctrl.raw_full[rs]));
+        }
+        stage_up();
+      }
+    } else if (warp == kWalkWarp && lane == 0) {
+      // ------------------------------------------------ the range's runs
+      Walk walk;
+      walk.b = ctrl.b;
+      load_span(a, p, walk.b, walk.w);
+      const int64_t per_head = head_units(p, walk.w);
+      const int len = pair_units(p, walk.w);
+      walk.head = static_cast<int>(ctrl.off / per_head);
+      const int64_t in_head = ctrl.off - walk.head * per_head;
+      walk.pair = static_cast<int>(min(in_head / len, static_cast<int64_t>(walk.w.groups / 2)));
+      walk.off = static_cast<int>(in_head - static_cast<int64_t>(walk.pair) * len);
+      walk.at = u0;
+      walk.left = u1 - u0;
+      for (int nth = 0, more = 1; more; ++nth) {
+        more = next_run(a, p, walk);
+        mbar_wait(smem_u32(&ctrl.run_empty[nth % kRuns]), ((nth / kRuns) & 1) ^ 1, abort, &g_err_kv4prompt, 66);
+        Run& run = ctrl.run[nth % kRuns];
+        run.stop = !more;
+        if (more) {
+          run.row0 = walk.w.s.row0, run.rows = walk.w.s.rows, run.len = walk.w.s.len;
+          run.groups = walk.w.groups, run.group = walk.group, run.seq = walk.seq, run.kvh = walk.kvh;
+          run.lo = walk.lo, run.hi = walk.hi, run.tile = walk.tile, run.n = walk.n, run.all = walk.all;
+          run.unit = walk.unit;
+        }
+        mbar_arrive(smem_u32(&ctrl.run_full[nth % kRuns]));
       }
     }
   }
