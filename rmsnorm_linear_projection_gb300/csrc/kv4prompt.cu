@@ -6,22 +6,23 @@
 // 2^-37 of it; queries scaled by a power of two per row.
 //
 // A CTA works on 256 rows (token x query head of one key head), two tiles of
-// 128, against 128 tokens at a time:
-//   warps 0-7, 8-15  softmax of the two row tiles, two threads a row, half of the
-//                    columns each: scores from TMEM, running maximum and sum, weights back to TMEM as
-//                    binary16 (the A operand of the second product), the sums
-//                    rescaled there when the maximum grew by about 2^9
-//   warps 16-19,     keys and values, a thread a token: codes and scales from a
-//     20-23          ring in shared memory, converted and scaled into the
+// 128, against tiles of 128 tokens in steps of 64:
+//   warps 0-3, 4-7   softmax of the two row tiles, a thread a row: a step's
+//                    scores from TMEM, weights back to TMEM as binary16 (the A
+//                    operand of the second product), the sums rescaled there
+//                    when the maximum grew by about 2^9
+//   warps 8-11,      keys and values, a thread a token: codes and scales from a
+//     12-15          ring in shared memory, converted and scaled into the
 //                    operands there (128-byte swizzle; keys K-major, values
 //                    MN-major, the same bytes in the same order)
-//   warp 24          TMEM allocation and, on one thread, every tcgen05.mma:
-//                    S_i = Q_i K^T (both from shared memory), O_i += P_i V
-//                    (P_i from TMEM), i = 0, 1 in turn, so that one row tile's
-//                    softmax runs while the other one's products do
-//   warp 25          bulk copies of the next tiles' codes and scales into the ring
-//   warp 26          walks the CTA's range and tells the others its runs
-// TMEM: S_0, S_1 (128 columns each; P_i takes the first 64 of S_i), O_0, O_1.
+//   warps 16, 17     (TMEM allocation and) a row tile's tcgen05.mma each:
+//                    S = Q K^T (both from shared memory), O += P V (P from TMEM)
+//   warp 18          bulk copies of the next tiles' codes and scales into the ring
+//   warp 19          walks the CTA's range and tells the others its runs
+// TMEM, per row tile: two buffers of 64 columns of scores (a step's weights
+// take the first 32 of its buffer), and D columns of sums.  The scores of a
+// step are computed while the softmax works on the step before, so that it
+// does not wait for the tensor core and its barriers.
 //
 // The weights are 2^(x - m + 7) with m at most 9 behind the true maximum:
 // binary16 holds them with 11 bits down to 2^-21 of the largest, or less.
@@ -43,20 +44,21 @@ using namespace kv4;
 
 __device__ unsigned int g_err_kv4prompt;
 
-constexpr int kT = 128;            // tokens a tile
+constexpr int kT = 128;            // tokens a tile of operands
+constexpr int kU = 64;             // tokens a step of products and softmax
 constexpr int kGroup = 256;        // rows a CTA holds
-constexpr int kSoftWarps = 16;
+constexpr int kSoftWarps = 8;
 constexpr int kFillWarps = 4;      // for the keys, and as many for the values
 constexpr int kValueWarp = kSoftWarps + kFillWarps;
 constexpr int kMmaWarp = kValueWarp + kFillWarps;
-constexpr int kLoadWarp = kMmaWarp + 1;
+constexpr int kLoadWarp = kMmaWarp + 2;
 constexpr int kWalkWarp = kLoadWarp + 1;
 constexpr int kMaxRing = 6;
-constexpr int kPWarps = 28;        // whole warpgroups; warp 27 idle
+constexpr int kPWarps = 20;        // five warpgroups
 constexpr int kPThreads = kPWarps * 32;
 // registers a thread after the roles part, within what the block is launched with
-constexpr int kLaunchRegs = 72, kSoftRegs = 88, kFillRegs = 48, kMmaRegs = 56;
-static_assert(16 * kSoftRegs + 8 * kFillRegs + 4 * kMmaRegs <= kPWarps * kLaunchRegs, "register file");
+constexpr int kLaunchRegs = 96, kSoftRegs = 136, kFillRegs = 64, kMmaRegs = 72;
+static_assert(8 * kSoftRegs + 8 * kFillRegs + 4 * kMmaRegs <= kPWarps * kLaunchRegs, "register file");
 // what a group costs beside its tiles (queries, output), in tiles
 constexpr int kGroupCost = 3;
 constexpr int kMaxPromptCtas = 160;
@@ -208,13 +210,12 @@ struct Run {
 constexpr int kRuns = 4;
 
 struct __align__(16) PCtrl {
-  uint64_t q_full[2], s_full[2], p_full[2];
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t raw_full[kMaxRing], raw_empty[kMaxRing];
   uint64_t run_full[kRuns], run_empty[kRuns];
   Run run[kRuns];
   int4 raw_info[kMaxRing];      // first token, the group's tokens, 1: a run's first tile, 2: no more tiles
-  float half[2][2][128];   // what a row's two halves tell each other
   float k_info[4];   // score factor of tile x at x % 4
   int v_info[4];     // the values' reference scale byte
   int top[2][2][kFillWarps], stop[2], done[2][2];
@@ -271,6 +272,17 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32
       "r"(a_tmem), "r"(b_lo), "r"(accumulate), "n"(kDescHi), "r"(IDESC)
       : "memory");
 }
+// tcgen05.wait::ld that the loaded registers depend on: nothing reads them earlier.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st_32cols(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -299,26 +311,11 @@ __device__ __forceinline__ void idle_wait(uint32_t bar, uint32_t parity, volatil
 
 // Named barriers.  A warp that polls takes issue slots from those that work:
 // of the warps that wait for the same thing one polls, the others stand at a
-// named barrier, which costs nothing.
-//   1-8 the two warps that share rows, 9-10 a row tile's warps, 11-12 the warps
-//   that fill keys, values
+// named barrier, which costs nothing.  1-2: a row tile's warps, 3-4: the warps
+// that fill keys, values.
 template <int WARPS>
 __device__ __forceinline__ void meet(int bar) {
   asm volatile("barrier.cta.sync %0, %1;" ::"r"(bar), "n"(WARPS * 32) : "memory");
-}
-__device__ __forceinline__ void pair_sync(int bar) { meet<2>(bar); }
-// The two warps that share rows meet with the logical or of a flag.
-__device__ __forceinline__ bool pair_or(int bar, bool flag) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %2, 0;\n\t"
-      "barrier.cta.red.or.pred q, %1, 64, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(bar), "r"(static_cast<uint32_t>(flag))
-      : "memory");
-  return r != 0;
 }
 
 // Where 16-byte chunk c (8 dims) of row r of a 128-row operand lies: blocks of
@@ -374,17 +371,21 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&ctrl.q_full[i]), 8);
-      mbar_init(smem_u32(&ctrl.s_full[i]), 1);
-      mbar_init(smem_u32(&ctrl.p_full[i]), 8);
+      mbar_init(smem_u32(&ctrl.q_full[i]), 4);
+      mbar_init(smem_u32(&ctrl.s_full[i][0]), 1);
+      mbar_init(smem_u32(&ctrl.s_full[i][1]), 1);
+      mbar_init(smem_u32(&ctrl.o_done[i][0]), 1);
+      mbar_init(smem_u32(&ctrl.o_done[i][1]), 1);
+      mbar_init(smem_u32(&ctrl.p_full[i][0]), 4);
+      mbar_init(smem_u32(&ctrl.p_full[i][1]), 4);
       mbar_init(smem_u32(&ctrl.k_full[i]), kFillWarps);
-      mbar_init(smem_u32(&ctrl.k_empty[i]), 1);
+      mbar_init(smem_u32(&ctrl.k_empty[i]), 2);
       mbar_init(smem_u32(&ctrl.v_full[i]), kFillWarps);
-      mbar_init(smem_u32(&ctrl.v_empty[i]), 1);
+      mbar_init(smem_u32(&ctrl.v_empty[i]), 2);
     }
     for (int i = 0; i < kRuns; ++i) {
       mbar_init(smem_u32(&ctrl.run_full[i]), 1);
-      mbar_init(smem_u32(&ctrl.run_empty[i]), kSoftWarps + 2);  // softmax, products, loads
+      mbar_init(smem_u32(&ctrl.run_empty[i]), kSoftWarps + 3);  // softmax, products, loads
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(smem_u32(&ctrl.raw_full[i]), 1);
@@ -452,27 +453,25 @@ __global__ void __launch_bounds__(kPThreads, 1)
   if (warp < kSoftWarps) {
     // ------------------------------------------------------------- softmax
     regs_inc<kSoftRegs>();
-    const int i = warp >> 3;                    // row tile
-    const int half = (warp >> 2) & 1;           // of its columns: tokens, dims
-    const int pair_bar = 1 + i * 4 + (warp & 3);  // the two warps that share rows
+    const int i = warp >> 2;                    // row tile
     const int rw = (warp & 3) * 32 + lane;      // row in it
+    const bool polls = (warp & 3) == 1 + i;     // for the tile's four warps
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + i * 128 + half * 64, tp = tmem + lanes + i * 128 + half * 32,
-                   to = tmem + lanes + 256 + i * D + half * (D / 2);
-    const uint32_t q_full = smem_u32(&ctrl.q_full[i]), s_full = smem_u32(&ctrl.s_full[i]),
-                   p_full = smem_u32(&ctrl.p_full[i]);
+    const uint32_t ts = tmem + lanes + i * 128, to = tmem + lanes + 256 + i * D;
+    // a bit a buffer: the phase of its next scores; the phase of its last sums is
+    // the other one (a barrier a buffer each: a parity tells two phases apart)
     uint32_t s_phase = 0;
-    int count = 0;  // tiles so far
+    int count = 0;         // tiles so far
     // a wait that gives up (a bug) ends every later wait at once: the loops run
     // on to their ends, so that the warp-wide instructions stay together
     for (int nth = 0;; ++nth) {
       const Run& run = ctrl.run[nth % kRuns];
-      if ((warp & 7) == 1 + i) {
+      if (polls) {
         warp_wait(smem_u32(&ctrl.run_full[nth % kRuns]), (nth / kRuns) & 1, abort, 63);
         if (lane == 0) ctrl.done[i][nth & 1] = run.stop || *abort;
       }
-      meet<8>(9 + i);
-      if (ctrl.done[i][nth & 1]) break;  // all eight warps alike
+      meet<4>(1 + i);
+      if (ctrl.done[i][nth & 1]) break;  // all four warps alike
       const int n_tiles = run.n;
       const int all_rows = run.rows * p.G, r0 = run.group * kGroup;
       if (r0 + i * 128 >= all_rows) {  // no row of this tile
@@ -489,68 +488,66 @@ __global__ void __launch_bounds__(kPThreads, 1)
       float f_row;
       {
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (run.row0 + tok_q) * p.q_stride +
-                                                          static_cast<int64_t>(head) * D + half * (D / 2));
-        uint4 w[D / 16];
+                                                          static_cast<int64_t>(head) * D);
+        uint4 w[D / 8];
         uint32_t am = 0;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) w[c] = __ldg(src + c);
+        for (int c = 0; c < D / 8; ++c) w[c] = __ldg(src + c);
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
+        for (int c = 0; c < D / 8; ++c) {
           const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
           for (int y = 0; y < 4; ++y) am = max(am, max((x[y] << 16) & 0x7FFFFFFFu, x[y] & 0x7FFF0000u));
         }
-        ctrl.half[i][half][rw] = __uint_as_float(am);
-        pair_sync(pair_bar);
-        am = max(am, __float_as_uint(ctrl.half[i][half ^ 1][rw]));
         const int e = 141 - max(static_cast<int>(am >> 23), 1);
         const float s1 = p.scale_log2 < 0.f ? -pow2i(e / 2) : pow2i(e / 2), s2 = pow2i(e - e / 2);
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
+        for (int c = 0; c < D / 8; ++c) {
           const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
           uint32_t h[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y)
             h[y] = pack_half2(__uint_as_float(x[y] << 16) * s1 * s2, __uint_as_float(x[y] & 0xFFFF0000u) * s1 * s2);
-          st_shared16(sq + i * kTileBytes + chunk_at<D>(rw, half * (D / 16) + c), h[0], h[1], h[2], h[3]);
+          st_shared16(sq + i * kTileBytes + chunk_at<D>(rw, c), h[0], h[1], h[2], h[3]);
         }
         f_row = fabsf(p.scale_log2) * pow2w(-e);
       }
       fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
+      if (lane == 0) mbar_arrive(smem_u32(&ctrl.q_full[i]));
 
       float m = -INFINITY, l = 0.f;
       int ref_v = 13;
-      const int tile0 = (run.lo / kT + run.tile) * kT;
-      for (int k = 0; k < n_tiles; ++k, ++count) {
-        if ((warp & 7) == 1 + i) warp_wait(s_full, s_phase, abort, 49);
-        meet<8>(9 + i);
-        s_phase ^= 1u;
+      int tok0 = (run.lo / kT + run.tile) * kT;
+      for (int u = 0; u < 2 * n_tiles; ++u, tok0 += kU) {
+        const int buf = u & 1;
+        if (polls) warp_wait(smem_u32(&ctrl.s_full[i][buf]), (s_phase >> buf) & 1, abort, 49);
+        meet<4>(1 + i);
+        s_phase ^= 1u << buf;
         tc_fence_after();
-        float f = f_row * ctrl.k_info[count & 3];
+        const int info = (count + (u >> 1)) & 3;
+        float f = f_row * ctrl.k_info[info];
         if (f < 1e-37f) f = 1e-37f;  // not 0, for masked scores (-infinity) times it
-        const int new_v = ctrl.v_info[count & 3];
-        const int tok0 = tile0 + k * kT + half * 64;
-        const bool whole = __all_sync(0xffffffffu, tok0 + 63 <= pos && tok0 >= first);
+        const int new_v = ctrl.v_info[info];
+        const uint32_t tsu = ts + buf * kU;
         float alpha = 1.f;
-        uint32_t h[32];  // the half row's weights, binary16 pairs
-        auto tile = [&](auto masked) {  // kept apart: the mask's tests stay out of whole tiles
+        auto step = [&](auto masked) {  // kept apart: the mask's tests stay out of whole steps
           constexpr bool kMasked = decltype(masked)::value;
           auto seen = [&](int tok, float v, float other) { return !kMasked || (tok <= pos && tok >= first) ? v : other; };
           // The maximum in use serves while the row's weights stay within
           // binary16, about 2^9 above it, which one pass over the scores finds
-          // while it computes them; where it does not (a run's first tile, or a
+          // while it computes them; where it does not (a run's first step, or a
           // row of the warp far above what it saw) the maximum is taken first.
           bool exact = __any_sync(0xffffffffu, m == -INFINITY);
+          uint32_t h[32];  // the row's weights, binary16 pairs
           for (;;) {
             uint32_t s[32];
             if (exact) {
               float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                tmem_ld_32cols(ts + 32 * c, s);
-                tmem_ld_wait();
+                tmem_ld_32cols(tsu + 32 * c, s);
+                tmem_ld_wait(s);
 #pragma unroll
                 for (int x = 0; x < 32; x += 2) {
                   const int tok = tok0 + 32 * c + x;
@@ -558,10 +555,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                                                                    seen(tok + 1, __uint_as_float(s[x + 1]), -INFINITY)));
                 }
               }
-              float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
-              ctrl.half[i][half][rw] = top;
-              pair_sync(pair_bar);
-              top = fmaxf(top, ctrl.half[i][half ^ 1][rw]);
+              const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
               if (top > m) {
                 alpha = ex2(m - top);
                 m = top;
@@ -570,15 +564,19 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
             const float bias = kTop - (m == -INFINITY ? 0.f : m);
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t s1[32];
+            tmem_ld_32cols(tsu, s);
+            tmem_ld_wait(s);
+            tmem_ld_32cols(tsu + 32, s1);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              tmem_ld_32cols(ts + 32 * c, s);
-              tmem_ld_wait();
+              if (c == 1) tmem_ld_wait(s1);
 #pragma unroll
               for (int x = 0; x < 16; ++x) {
                 const int tok = tok0 + 32 * c + 2 * x;
-                const float e0 = seen(tok, ex2(fmaf(__uint_as_float(s[2 * x]), f, bias)), 0.f);
-                const float e1 = seen(tok + 1, ex2(fmaf(__uint_as_float(s[2 * x + 1]), f, bias)), 0.f);
+                const uint32_t a0 = c ? s1[2 * x] : s[2 * x], a1 = c ? s1[2 * x + 1] : s[2 * x + 1];
+                const float e0 = seen(tok, ex2(fmaf(__uint_as_float(a0), f, bias)), 0.f);
+                const float e1 = seen(tok + 1, ex2(fmaf(__uint_as_float(a1), f, bias)), 0.f);
                 sum[2 * (x & 1)] += e0;
                 sum[2 * (x & 1) + 1] += e1;
                 h[16 * c + x] = pack_half2(e0, e1);
@@ -586,35 +584,35 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
             // The weights are positive: none is beyond binary16 (65504) if their
             // sum is not, so that the sum says whether the maximum in use still
-            // serves.  Both warps of the rows have read their scores here, and
-            // take the same way.
+            // serves.
             const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            if (pair_or(pair_bar, !exact && !(all < 65504.f))) {
+            if (!exact && __any_sync(0xffffffffu, !(all < 65504.f))) {
               exact = true;
               continue;
             }
             l += all;
             break;
           }
+          tmem_st_32cols(tsu, h);  // into columns whose scores have been read
         };
-        if (whole)
-          tile(std::false_type{});
+        if (__all_sync(0xffffffffu, tok0 + kU - 1 <= pos && tok0 >= first))
+          step(std::false_type{});
         else
-          tile(std::true_type{});
-        // into the columns whose scores have been read
-        tmem_st_32cols(tp, h);
+          step(std::true_type{});
         if (new_v != ref_v) {
           alpha *= pow2i(ref_v - new_v);
           ref_v = new_v;
         }
-        // the sums so far, rescaled (the products before are done: this
-        // tile's scores came after them)
-        if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        // the sums so far, rescaled: after the step before (the earlier ones are
+        // done: this step's scores came after them)
+        if (u > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          warp_wait(smem_u32(&ctrl.o_done[i][buf ^ 1]), ((s_phase >> (buf ^ 1)) & 1) ^ 1u, abort, 67);
+          tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
+          for (int c = 0; c < D / 32; ++c) {
             uint32_t s[32];
             tmem_ld_32cols(to + 32 * c, s);
-            tmem_ld_wait();
+            tmem_ld_wait(s);
 #pragma unroll
             for (int x = 0; x < 32; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * alpha);
             tmem_st_32cols(to + 32 * c, s);
@@ -623,33 +621,31 @@ __global__ void __launch_bounds__(kPThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
+        if (lane == 0) mbar_arrive(smem_u32(&ctrl.p_full[i][buf]));
       }
-      if ((warp & 7) == 1 + i) warp_wait(s_full, s_phase, abort, 50);
-      meet<8>(9 + i);
-      s_phase ^= 1u;
+      count += n_tiles;
+#pragma unroll
+      for (int buf = 0; buf < 2; ++buf)
+        warp_wait(smem_u32(&ctrl.o_done[i][buf]), ((s_phase >> buf) & 1) ^ 1u, abort, 50);
       tc_fence_after();
       // sums stand for value * 2^(ref_v - 127 - 13), weights and sums both times 2^7
       const bool complete = run.n == run.all;
-      ctrl.half[i][half][rw] = l;
-      pair_sync(pair_bar);
-      l += ctrl.half[i][half ^ 1][rw];
       const float inv = complete ? (l != 0.f ? 1.f / l : 0.f) : 1.f / 128.f;
       const float fa = pow2i((ref_v - 140) / 2), fb = pow2i(ref_v - 140 - (ref_v - 140) / 2) * (ref_v == 255 ? NAN : 1.f);
       const int64_t orow = static_cast<int64_t>(run.row0 + tok_q) * p.Hq + head;
       float* slot = p.part + static_cast<int64_t>(2 * cta + (nth > 0)) * C::kSlot;
       const int rg = i * 128 + rw;
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
+      for (int c = 0; c < D / 32; ++c) {
         uint32_t s[32];
         tmem_ld_32cols(to + 32 * c, s);
-        tmem_ld_wait();
+        tmem_ld_wait(s);
         float v[32];
 #pragma unroll
         for (int x = 0; x < 32; ++x) v[x] = __uint_as_float(s[x]) * inv * fa * fb;
         if (r < all_rows) {
           if (complete) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + half * (D / 2) + 32 * c);
+            uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + 32 * c);
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               uint32_t w[4];
@@ -661,14 +657,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
               dst[y] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else {
-            float4* dst = reinterpret_cast<float4*>(slot + rg * D + half * (D / 2) + 32 * c);
+            float4* dst = reinterpret_cast<float4*>(slot + rg * D + 32 * c);
 #pragma unroll
             for (int y = 0; y < 8; ++y) dst[y] = make_float4(v[4 * y], v[4 * y + 1], v[4 * y + 2], v[4 * y + 3]);
           }
         }
       }
       tc_fence_before();  // the next run's products overwrite these sums
-      if (r < all_rows && half == 0) {
+      if (r < all_rows) {
         const float lt = l * (1.f / 128.f);
         if (complete) {
           if (p.lse != nullptr) p.lse[orow] = lt != 0.f ? m * kLn2 + logf(lt) : -INFINITY;
@@ -678,7 +674,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
       }
       // a group that begins here and goes on in later CTAs
-      if (i == 0 && half == 0 && rw == 0 && run.tile == 0 && !complete) {
+      if (i == 0 && rw == 0 && run.tile == 0 && !complete) {
         const int64_t end = run.unit + run.all;
         p.rec[cta] = make_int4(run.kvh * run.groups + run.group, run.seq,
                                static_cast<int>((end * ctas - 1) / units), nth > 0);
@@ -713,7 +709,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         idle_wait(smem_u32(&ctrl.raw_full[rs]), rp, abort, 60);
         if (lane == 0) ctrl.stop[values] = (ctrl.raw_info[rs].w & 2) || *abort;
       }
-      meet<kFillWarps>(11 + values);
+      meet<kFillWarps>(3 + values);
       if (ctrl.stop[values]) break;  // all four warps alike
       const int4 info = ctrl.raw_info[rs];
       const uint32_t raw = smem_u32(raws) + rs * C::kRaw;
@@ -737,7 +733,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         mbar_arrive(smem_u32(&ctrl.raw_empty[rs]));
       }
       if (fw == 3) idle_wait(empty + 8 * stage, ((count >> 1) & 1) ^ 1u, abort, 52);
-      meet<kFillWarps>(11 + values);
+      meet<kFillWarps>(3 + values);
       int top = 0, top_v = 0;
 #pragma unroll
       for (int x = 0; x < kFillWarps; ++x) {
@@ -781,73 +777,89 @@ __global__ void __launch_bounds__(kPThreads, 1)
   } else {
     // ------------------------------------------------------------ products
     regs_dec<kMmaRegs>();
-    if (warp == kMmaWarp) {
-      // the whole warp walks and waits; one lane issues
-      constexpr uint32_t kDescQK = idesc_f16(128, kT, false), kDescPV = idesc_f16(128, D, true);
-      int count = 0;                       // tiles so far
-      uint32_t q_phase = 0, p_phase = 0;   // a bit a row tile
+    if (warp < kLoadWarp) {
+      // A warp for each row tile: while the products of one tile run (issuing
+      // them blocks), the other's warp waits for its tile's weights.
+      const int i = warp - kMmaWarp;
+      constexpr uint32_t kDescQK = idesc_f16(128, kU, false), kDescPV = idesc_f16(128, D, true);
+      int count = 0;             // tiles so far
+      uint32_t q_phase = 0, p_phase = 0;
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
-        int done = 1;
-        if (lane == 0) done = quick_wait(smem_u32(bar), parity, abort, &g_err_kv4prompt, site);
-        ok = ok && __shfl_sync(0xffffffffu, done, 0) != 0;
+        ok = __all_sync(0xffffffffu, quick_wait(smem_u32(bar), parity, abort, &g_err_kv4prompt, site)) && ok;
         return ok;
       };
-      const uint32_t q_lo = desc_lo(sq, 16), k_lo = desc_lo(sk, 16), v_lo = desc_lo(sv, C::kHalf);
-      auto scores = [&](int i, int stage) {
-        const uint32_t qd = q_lo + i * (kTileBytes >> 4), kd = k_lo + stage * (kTileBytes >> 4);
+      const uint32_t q_lo = desc_lo(sq, 16) + i * (kTileBytes >> 4), k_lo = desc_lo(sk, 16),
+                     v_lo = desc_lo(sv, C::kHalf);
+      const uint32_t ts = tmem + i * 128, to = tmem + 256 + i * D;
+      constexpr uint32_t kStep = kU * 128 >> 4;  // a step's rows of an operand
+      auto scores = [&](int stage, int half) {
+        const uint32_t kd = k_lo + stage * (kTileBytes >> 4) + half * kStep;
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
-          const uint32_t step = ((x >> 2) * C::kHalf + (x & 3) * 32) >> 4;
-          umma_ss<kDescQK>(tmem + i * 128, qd + step, kd + step, x > 0);
+          const uint32_t at = ((x >> 2) * C::kHalf + (x & 3) * 32) >> 4;
+          umma_ss<kDescQK>(ts + half * kU, q_lo + at, kd + at, x > 0);
         }
+        umma_commit(smem_u32(&ctrl.s_full[i][half]));
       };
-      auto sums = [&](int i, int stage, bool fresh) {
-        const uint32_t vd = v_lo + stage * (kTileBytes >> 4);
+      auto sums = [&](int stage, int half, bool fresh) {
+        const uint32_t vd = v_lo + stage * (kTileBytes >> 4) + half * kStep;
 #pragma unroll
-        for (int x = 0; x < kT / 16; ++x)
-          umma_ts<kDescPV>(tmem + 256 + i * D, tmem + i * 128 + 8 * x, vd + ((x * 2048u) >> 4), !fresh || x > 0);
+        for (int x = 0; x < kU / 16; ++x)
+          umma_ts<kDescPV>(to, ts + half * kU + 8 * x, vd + ((x * 2048u) >> 4), !fresh || x > 0);
+        umma_commit(smem_u32(&ctrl.o_done[i][half]));
       };
       for (int nth = 0; ok; ++nth) {
         if (!wait(&ctrl.run_full[nth % kRuns], (nth / kRuns) & 1, 64)) break;
         const Run& run = ctrl.run[nth % kRuns];
         if (run.stop) break;
         const int n_tiles = run.n;
-        const int ni = run.rows * p.G - run.group * kGroup > 128 ? 2 : 1;
+        const bool rows = run.rows * p.G - run.group * kGroup > i * 128;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctrl.run_empty[nth % kRuns]));
-        for (int i = 0; i < ni && ok; ++i) {
-          if (!wait(&ctrl.q_full[i], (q_phase >> i) & 1, 54)) break;
-          q_phase ^= 1u << i;
-          if (i == 0 && !wait(&ctrl.k_full[count & 1], (count >> 1) & 1, 55)) break;
+        if (!rows) {  // nothing to do for this row tile: hand the operands back
+          for (int k = 0; k < n_tiles && ok; ++k, ++count) {
+            if (!wait(&ctrl.k_full[count & 1], (count >> 1) & 1, 55) || !wait(&ctrl.v_full[count & 1], (count >> 1) & 1, 57))
+              break;
+            if (lane == 0) {
+              mbar_arrive(smem_u32(&ctrl.k_empty[count & 1]));
+              mbar_arrive(smem_u32(&ctrl.v_empty[count & 1]));
+            }
+          }
+          continue;
+        }
+        if (!wait(&ctrl.q_full[i], q_phase, 54) || !wait(&ctrl.k_full[count & 1], (count >> 1) & 1, 55)) break;
+        q_phase ^= 1u;
+        tc_fence_after();
+        if (elect_one()) {
+          scores(count & 1, 0);
+          scores(count & 1, 1);
+          umma_commit(smem_u32(&ctrl.k_empty[count & 1]));
+        }
+        __syncwarp();
+        // a step's sums, then the scores two steps on, into the same columns
+        for (int u = 0; u < 2 * n_tiles; ++u) {
+          const int half = u & 1, t = count + (u >> 1);
+          const bool more = u + 2 < 2 * n_tiles;
+          if (half == 0) {
+            if (!wait(&ctrl.v_full[t & 1], (t >> 1) & 1, 57)) break;
+            if (more && !wait(&ctrl.k_full[(t + 1) & 1], ((t + 1) >> 1) & 1, 58)) break;
+          }
+          // a barrier a buffer: the softmax may be a step ahead
+          if (!wait(&ctrl.p_full[i][half], (p_phase >> half) & 1, 56)) break;
+          p_phase ^= 1u << half;
           tc_fence_after();
           if (elect_one()) {
-            scores(i, count & 1);
-            umma_commit(smem_u32(&ctrl.s_full[i]));
-            if (i == ni - 1) umma_commit(smem_u32(&ctrl.k_empty[count & 1]));
+            sums(t & 1, half, u == 0);
+            if (more) scores((t + 1) & 1, half);
+            if (half == 1) {
+              umma_commit(smem_u32(&ctrl.v_empty[t & 1]));
+              if (more) umma_commit(smem_u32(&ctrl.k_empty[(t + 1) & 1]));
+            }
           }
           __syncwarp();
         }
-        for (int k = 0; k < n_tiles && ok; ++k, ++count) {
-          const bool last = k + 1 == n_tiles;
-          for (int i = 0; i < ni; ++i) {
-            if (i == 0 && !wait(&ctrl.v_full[count & 1], (count >> 1) & 1, 57)) break;
-            if (i == 0 && !last && !wait(&ctrl.k_full[(count + 1) & 1], ((count + 1) >> 1) & 1, 58)) break;
-            if (!wait(&ctrl.p_full[i], (p_phase >> i) & 1, 56)) break;
-            p_phase ^= 1u << i;
-            tc_fence_after();
-            if (elect_one()) {
-              sums(i, count & 1, k == 0);
-              if (!last) scores(i, (count + 1) & 1);
-              umma_commit(smem_u32(&ctrl.s_full[i]));
-              if (i == ni - 1) {
-                umma_commit(smem_u32(&ctrl.v_empty[count & 1]));
-                if (!last) umma_commit(smem_u32(&ctrl.k_empty[(count + 1) & 1]));
-              }
-            }
-            __syncwarp();
-          }
-        }
+        count += n_tiles;
       }
       // the last arrival on this CTA's barriers
       if (count > 0) wait(&ctrl.v_empty[(count - 1) & 1], ((count - 1) >> 1) & 1, 59);
