@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
   __shared__ long long sh_sum[kWarps];
   __shared__ int sh_b, sh_abort;
   __shared__ long long sh_off;
+  __shared__ Span sh_w;
   float* merge = reinterpret_cast<float*>(smem + kWarps * 2 * kSideBytes);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -173,13 +174,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     fence_mbar_init();
   }
   // ---- this CTA's range of tiles
-  auto units_of = [&](int b) -> long long {
-    Span w;
+  auto units_of = [&](int b, Span& w) -> long long {
     if (b >= a.n_seqs || !load_span<D, NT>(a, p, b, w)) return 0;
     return static_cast<long long>(w.tiles + kItemCost) * w.groups * a.Hkv;
   };
-  long long sum = 0;
-  for (int b = tid; b < a.n_seqs; b += kThreads) sum += units_of(b);
+  Span mine;
+  const long long mine_units = units_of(tid, mine);
+  long long sum = mine_units;
+  for (int b = tid + kThreads; b < a.n_seqs; b += kThreads) {
+    Span w;
+    sum += units_of(b, w);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) sh_sum[warp] = sum;
@@ -192,11 +197,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
       min(static_cast<long long>(gridDim.x), (units + kWarps + kItemCost - 1) / (kWarps + kItemCost)));
   grid_launch_dependents();
   if (tid == 0) p.rec[cta] = make_int4(-1, 0, 0, 0);
-  if (cta >= ctas) return;  // the whole CTA
+  // (launched early, beside the prompt kernel's join: both are done before this
+  // grid is, so that what follows in the stream comes after them)
+  if (cta >= ctas) {
+    grid_dependency_wait();
+    return;  // the whole CTA
+  }
   const int64_t u0 = range_start(units, cta, ctas), u1 = range_start(units, cta + 1, ctas);
   long long before = 0;
   for (int base = 0; base < a.n_seqs; base += kThreads) {
-    const long long u = units_of(base + tid);
+    Span w = mine;
+    const long long u = base == 0 ? mine_units : units_of(base + tid, w);
     long long inc = u;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -213,19 +224,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     if (u0 >= inc - u && u0 < inc) {
       sh_b = base + tid;
       sh_off = u0 - (inc - u);
+      sh_w = w;
     }
     __syncthreads();
     if (sh_b >= 0) break;
     before += all;
   }
-  if (sh_b < 0) return;  // lengths changed under the call
+  if (sh_b < 0) {  // lengths changed under the call
+    grid_dependency_wait();
+    return;
+  }
   Cursor cur;  // the CTA's place
   cur.b = sh_b;
-  load_span<D, NT>(a, p, cur.b, cur.w);
-  const int item = static_cast<int>(sh_off / (cur.w.tiles + kItemCost));
+  cur.w = sh_w;
+  // (a 64-bit division is slow)
+  const int item = sh_off >> 32 ? static_cast<int>(sh_off / (cur.w.tiles + kItemCost))
+                                : static_cast<int>(static_cast<uint32_t>(sh_off) / (cur.w.tiles + kItemCost));
   cur.head = item / cur.w.groups;
   cur.group = item - cur.head * cur.w.groups;
-  cur.tile = static_cast<int>(sh_off % (cur.w.tiles + kItemCost)) - kItemCost;
+  cur.tile = static_cast<int>(sh_off - static_cast<long long>(item) * (cur.w.tiles + kItemCost)) - kItemCost;
   cur.left = static_cast<int>(u1 - u0);
   int64_t at = u0;  // where the range's first tile stands
   if (cur.tile < 0) {
@@ -679,6 +696,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     at += seg_tiles + kItemCost;
     skip<D, NT>(a, p, cur, seg_tiles);
   }
+  grid_dependency_wait();
 }
 
 // Joins the partial sums of the items that were cut: CTA c the one that CTA c
@@ -747,24 +765,29 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kJoin * 128)
 }
 
 template <int D, int NT, int BS>
-rnl_status launch_split(const AttnParams& p, const Args& a, const DeviceInfo& dev, cudaStream_t s) {
+rnl_status launch_split(const AttnParams& p, const Args& a, const DeviceInfo& dev, bool after_prompt, cudaStream_t s) {
   using C = Cfg<D, NT>;
   const rnl_status st = ensure_smem_attr(reinterpret_cast<const void*>(kv4_attn_kernel<D, NT, BS>), dev.device, C::kSmem);
   if (st != RNL_OK) return st;
   const int ctas = std::min(dev.sm_count * C::kMinCtas, kMaxCtas);
-  trace_before(s);
-  kv4_attn_kernel<D, NT, BS><<<ctas, kThreads, C::kSmem, s>>>(a, p);
-  cudaError_t e = cudaGetLastError();
-  trace_after(s, "kv4_attn");
-  if (e != cudaSuccess) return RNL_ERR_LAUNCH;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(C::kJoin * 128);
-  cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
   cfg.attrs = at;
+  // early only behind this call's own prompt kernels: what stands before the
+  // call in the stream may write what this kernel reads
+  cfg.numAttrs = after_prompt ? 1 : 0;
+  trace_before(s);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_attn_kernel<D, NT, BS>, a, p);
+  trace_after(s, "kv4_attn");
+  if (e != cudaSuccess) return RNL_ERR_LAUNCH;
+  cfg.blockDim = dim3(C::kJoin * 128);
+  cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
   trace_before(s);
   e = cudaLaunchKernelEx(&cfg, kv4_attn_join_kernel<D, NT>, a, p);
@@ -807,23 +830,25 @@ rnl_status launch_kv4_attention(const Kv4AttnArgs& x, const rnl_kv4_cache& c, co
   p.causal = x.causal;
   p.window = static_cast<int>(x.window);
   p.few = 0x7fffffff;
+  bool after = false;
   if (q.cu_rows != nullptr && may_prompt(q.n_rows, p.G, a.D)) {
     p.few = kFewRows;
     const rnl_status pst = launch_kv4_prompt(p, a, static_cast<int>(c.block),
                                              static_cast<char*>(x.ws) + few_workspace_bytes(a.D), dev, s);
     if (pst != RNL_OK) return pst;
+    after = true;
   }
   // 4, 8 or 16 rows an item: the fewest that hold the rows a sequence has on average
   const int64_t rows = (q.n_rows + q.n_seqs - 1) / q.n_seqs * p.G;
   auto go = [&](auto d) {
     constexpr int D = decltype(d)::value;
     if (c.block == 64)
-      return rows <= 4   ? launch_split<D, 0, 64>(p, a, dev, s)
-             : rows <= 8 ? launch_split<D, 1, 64>(p, a, dev, s)
-                         : launch_split<D, 2, 64>(p, a, dev, s);
-    return rows <= 4   ? launch_split<D, 0, 32>(p, a, dev, s)
-           : rows <= 8 ? launch_split<D, 1, 32>(p, a, dev, s)
-                       : launch_split<D, 2, 32>(p, a, dev, s);
+      return rows <= 4   ? launch_split<D, 0, 64>(p, a, dev, after, s)
+             : rows <= 8 ? launch_split<D, 1, 64>(p, a, dev, after, s)
+                         : launch_split<D, 2, 64>(p, a, dev, after, s);
+    return rows <= 4   ? launch_split<D, 0, 32>(p, a, dev, after, s)
+           : rows <= 8 ? launch_split<D, 1, 32>(p, a, dev, after, s)
+                       : launch_split<D, 2, 32>(p, a, dev, after, s);
   };
   if (a.D == 64) return go(std::integral_constant<int, 64>{});
   if (a.D == 128) return go(std::integral_constant<int, 128>{});

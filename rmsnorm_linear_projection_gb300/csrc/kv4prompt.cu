@@ -222,6 +222,7 @@ struct __align__(16) PCtrl {
   long long sum[kPWarps];
   long long off;
   uint32_t tmem;
+  Span w;
   int b, abort;
 };
 
@@ -396,18 +397,23 @@ __global__ void __launch_bounds__(kPThreads, 1)
     fence_mbar_init();
   }
   // ---- this CTA's range (as kv4attn.cu, units of this kernel)
-  auto units_of = [&](int b) -> long long {
-    Span w;
+  auto units_of = [&](int b, Span& w) -> long long {
     if (b >= a.n_seqs || !load_span(a, p, b, w)) return 0;
     return head_units(p, w) * a.Hkv;
   };
-  long long sum = 0;
-  for (int b = tid; b < a.n_seqs; b += kPThreads) sum += units_of(b);
+  Span mine;
+  const long long mine_units = units_of(tid, mine);
+  long long sum = mine_units;
+  for (int b = tid + kPThreads; b < a.n_seqs; b += kPThreads) {
+    Span w;
+    sum += units_of(b, w);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) ctrl.sum[warp] = sum;
   __syncthreads();
   long long units = 0;
+#pragma unroll 1
   for (int i = 0; i < kPWarps; ++i) units += ctrl.sum[i];
   const int cta = blockIdx.x;
   const int ctas =
@@ -417,8 +423,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
   if (cta >= ctas) return;  // the whole CTA
   const int64_t u0 = range_start(units, cta, ctas), u1 = range_start(units, cta + 1, ctas);
   long long before = 0;
+#pragma unroll 1
   for (int start = 0; start < a.n_seqs; start += kPThreads) {
-    const long long u = units_of(start + tid);
+    Span w = mine;
+    const long long u = start == 0 ? mine_units : units_of(start + tid, w);
     long long inc = u;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -428,13 +436,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
     __syncthreads();
     if (lane == 31) ctrl.sum[warp] = inc;
     __syncthreads();
-    for (int i = 0; i < warp; ++i) inc += ctrl.sum[i];
     long long all = 0;
-    for (int i = 0; i < kPWarps; ++i) all += ctrl.sum[i];
+#pragma unroll 1
+    for (int i = 0; i < kPWarps; ++i) {
+      if (i < warp) inc += ctrl.sum[i];
+      all += ctrl.sum[i];
+    }
     inc += before;
     if (u0 >= inc - u && u0 < inc) {
       ctrl.b = start + tid;
       ctrl.off = u0 - (inc - u);
+      ctrl.w = w;
     }
     __syncthreads();
     if (ctrl.b >= 0) break;
@@ -482,7 +494,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       const int r = r0 + i * 128 + rw;
       const int rc = min(r, all_rows - 1), tok_q = rc / p.G;
-      const int head = run.kvh * p.G + (rc - tok_q * p.G);
+      const int head = run.kvh * p.G + (rc - tok_q * p.G);  // of the thread's row
       const int pos = p.causal ? run.len - run.rows + tok_q : run.len - 1;
       const int first = p.window > 0 ? pos - p.window + 1 : 0;  // first token the row reads
       float f_row;
@@ -608,7 +620,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (u > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
           warp_wait(smem_u32(&ctrl.o_done[i][buf ^ 1]), ((s_phase >> (buf ^ 1)) & 1) ^ 1u, abort, 67);
           tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t s[32];
             tmem_ld_32cols(to + 32 * c, s);
@@ -932,12 +944,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
       // ------------------------------------------------ the range's runs
       Walk walk;
       walk.b = ctrl.b;
-      load_span(a, p, walk.b, walk.w);
+      walk.w = ctrl.w;
       const int64_t per_head = head_units(p, walk.w);
       const int len = pair_units(p, walk.w);
-      walk.head = static_cast<int>(ctrl.off / per_head);
+      // (64-bit divisions are slow, and everyone waits for the first run)
+      walk.head = ctrl.off >> 32 || per_head >> 32
+                      ? static_cast<int>(ctrl.off / per_head)
+                      : static_cast<int>(static_cast<uint32_t>(ctrl.off) / static_cast<uint32_t>(per_head));
       const int64_t in_head = ctrl.off - walk.head * per_head;
-      walk.pair = static_cast<int>(min(in_head / len, static_cast<int64_t>(walk.w.groups / 2)));
+      const int64_t pair = in_head >> 32 ? in_head / len : static_cast<uint32_t>(in_head) / static_cast<uint32_t>(len);
+      walk.pair = static_cast<int>(min(pair, static_cast<int64_t>(walk.w.groups / 2)));
       walk.off = static_cast<int>(in_head - static_cast<int64_t>(walk.pair) * len);
       walk.at = u0;
       walk.left = u1 - u0;
@@ -970,6 +986,7 @@ template <int D>
 __global__ void __launch_bounds__(512)
     kv4_prompt_join_kernel(const Args a, const AttnParams p) {
   using C = PCfg<D>;
+  grid_launch_dependents();
   grid_dependency_wait();
   const int first = blockIdx.x >> 2, part = blockIdx.x & 3;  // 4 CTAs a group, 64 rows each
   const int4 rec = p.rec[first];
@@ -982,19 +999,19 @@ __global__ void __launch_bounds__(512)
   for (int x = threadIdx.x; x < 64 * kTpr; x += 512) {
     const int r = part * 64 + x / kTpr, d = (x % kTpr) * 8;
     if (r0 + r >= all_rows) continue;
+    auto slot = [&](int c) { return p.part + static_cast<int64_t>(2 * c + (c == first ? rec.w : 0)) * C::kSlot; };
     float mm = -INFINITY, ll = 0.f, v[8] = {};
+    for (int c = first; c <= rec.z; ++c) mm = fmaxf(mm, slot(c)[kGroup * D + r]);
+#pragma unroll 2
     for (int c = first; c <= rec.z; ++c) {
-      const float* s = p.part + static_cast<int64_t>(2 * c + (c == first ? rec.w : 0)) * C::kSlot;
+      const float* s = slot(c);
       const float pm = s[kGroup * D + r], pl = s[kGroup * D + kGroup + r];
       const float4 y = *reinterpret_cast<const float4*>(s + r * D + d);
       const float4 z = *reinterpret_cast<const float4*>(s + r * D + d + 4);
-      if (pl == 0.f) continue;  // nothing read there
-      const float mn = fmaxf(mm, pm);
-      const float f0 = mm == -INFINITY ? 0.f : ex2(mm - mn), f1 = ex2(pm - mn);
-      mm = mn;
-      ll = ll * f0 + pl * f1;
-      v[0] = v[0] * f0 + y.x * f1, v[1] = v[1] * f0 + y.y * f1, v[2] = v[2] * f0 + y.z * f1, v[3] = v[3] * f0 + y.w * f1;
-      v[4] = v[4] * f0 + z.x * f1, v[5] = v[5] * f0 + z.y * f1, v[6] = v[6] * f0 + z.z * f1, v[7] = v[7] * f0 + z.w * f1;
+      const float f = pl != 0.f ? ex2(pm - mm) : 0.f;  // 0: nothing read there
+      ll += pl * f;
+      v[0] += y.x * f, v[1] += y.y * f, v[2] += y.z * f, v[3] += y.w * f;
+      v[4] += z.x * f, v[5] += z.y * f, v[6] += z.z * f, v[7] += z.w * f;
     }
     store_row<D>(p, w.s, kvh, r0 + r, d, v, mm, ll);
   }
