@@ -69,8 +69,9 @@ struct Cfg {
   static constexpr int kSlot = kRows * (D + 2);  // floats of a partial: sums, maxima, weights
   static constexpr size_t kSmem = kWarps * 2 * kSideBytes + kWarps * kRows * kPitch * 4;
   static constexpr int kJoin = D * kTiles > 256 ? 2 : 4;  // thread groups that join pieces (static shared memory)
-  // registers: 4 CTAs an SM where the sums and queries leave 128 a thread
-  static constexpr int kMinCtas = D * kTiles <= 128 ? 4 : D * kTiles <= 256 ? 3 : 2;
+  // CTAs an SM, by what their registers leave: 2 with 255 registers a thread for 16 rows (3, with spills:
+  // 117 against 93 us at 32 x 4 rows, D = 128), 3 for up to 8 (4: 68 against 60 us at 8 rows, D = 128)
+  static constexpr int kMinCtas = NT == 2 ? 2 : 3;
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
