@@ -465,14 +465,14 @@ void trace_after(cudaStream_t s, const char* name) {
 }
 
 rnl_status read_device_errors(int* site) {
-  unsigned int words[13] = {};
+  unsigned int words[14] = {};
   if (read_clear_error_rowwise(&words[0]) != RNL_OK || read_clear_error_gemm(&words[1]) != RNL_OK ||
       read_clear_error_skinny(&words[2]) != RNL_OK || read_clear_error_pair(&words[3]) != RNL_OK ||
       read_clear_error_norm(&words[4]) != RNL_OK || read_clear_error_selftest(&words[5]) != RNL_OK ||
       read_clear_error_rope(&words[6]) != RNL_OK || read_clear_error_mx(&words[7]) != RNL_OK ||
       read_clear_error_quant(&words[8]) != RNL_OK || read_clear_error_decmma(&words[9]) != RNL_OK ||
       read_clear_error_kv4cache(&words[10]) != RNL_OK || read_clear_error_kv4attn(&words[11]) != RNL_OK ||
-      read_clear_error_kv4prompt(&words[12]) != RNL_OK)
+      read_clear_error_kv4prompt(&words[12]) != RNL_OK || read_clear_error_axes(&words[13]) != RNL_OK)
     return RNL_ERR_LAUNCH;
   for (unsigned int w : words) {
     if (w != 0) {

@@ -180,7 +180,7 @@ rnl_status launch_qkv_rope(const void* y, int64_t T, int64_t Hq, int64_t Hkv, in
                            const int32_t* positions, const float* cos_sin, int64_t max_pos,
                            void* q, void* k, void* v, cudaStream_t s);
 
-// The same with one position per axis (positions [axes, T]) and the host map
+// The same with one position per axis (ropeaxes.cu; positions [axes, T]) and the host map
 // axis_of_pair [D / 2]; null gammas: no head norm.
 rnl_status launch_qkv_rope_axes(const void* y, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
                                 const void* q_gamma, const void* k_gamma, float eps,
@@ -332,6 +332,7 @@ rnl_status read_clear_error_rope(unsigned int* word);
 rnl_status read_clear_error_mx(unsigned int* word);
 rnl_status read_clear_error_quant(unsigned int* word);
 rnl_status read_clear_error_decmma(unsigned int* word);
+rnl_status read_clear_error_axes(unsigned int* word);
 rnl_status read_clear_error_kv4cache(unsigned int* word);
 rnl_status read_clear_error_kv4attn(unsigned int* word);
 rnl_status read_clear_error_kv4prompt(unsigned int* word);

@@ -12,15 +12,7 @@
 //
 // One warp per (token, group of 8 heads); each head row is read once and
 // written once (HBM bound).
-//
-// Positions of several axes (rnl_qkv_rope_axes: time, height and width of a
-// video, row and column of an image): pair i reads its angle's column i from
-// the row of axis_of_pair[i]'s position, so a token gathers from up to four
-// table rows instead of one; the head norms are optional there.  The gather is
-// once per warp (8 heads).
 #include <cuda_bf16.h>
-
-#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -92,12 +84,6 @@ __device__ __forceinline__ void load_f32n(const float* p, float (&f)[N]) {
 // processed.
 constexpr int kHeadsPerWarp = 8;
 
-// Which axis' position turns each pair (i, i + D/2); kernel argument.
-struct OneAxis {};
-struct AxisMap {
-  uint8_t a[128];  // axis of pair i, i < D/2
-};
-
 // Lane l holds R = D/64 elements of each half of a head row: i in
 // [l R, l R + R) and their rotation partners i + D/2, so the rotation needs
 // no shuffle, and every load or store instruction of the warp covers a
@@ -106,18 +92,14 @@ struct AxisMap {
 // head's partial over 4 lanes, 2 more finish it), one rsqrt a lane, and
 // 8 shuffles hand every head its factor: 17 shuffles and 1 rsqrt for 8
 // heads instead of 40 and 8.
-//
-// Map = OneAxis: pos [T], both gammas given.  Map = AxisMap: pos [axes, T], a
-// null gamma leaves its heads without the norm.
-template <int D, class Map>
+template <int D>
 __global__ void __launch_bounds__(kRopeWarps * 32)
     qkv_rope_kernel(const __nv_bfloat16* __restrict__ y, int64_t T, int Hq, int Hkv, int groups,
                     const __nv_bfloat16* __restrict__ q_gamma,
                     const __nv_bfloat16* __restrict__ k_gamma, float eps,
                     const int* __restrict__ pos, const float* __restrict__ cs, int P,
                     __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ k,
-                    __nv_bfloat16* __restrict__ v, const __grid_constant__ Map map) {
-  constexpr bool kAxes = !std::is_same<Map, OneAxis>::value;
+                    __nv_bfloat16* __restrict__ v) {
   constexpr int R = D / 64;  // values of each half per lane
   constexpr int kHalf = D / 2;
   const int lane = threadIdx.x & 31;
@@ -141,41 +123,20 @@ __global__ void __launch_bounds__(kRopeWarps * 32)
   bool p_ok = true;
   float c[R], sn[R], gql[R], gqh[R], gkl[R], gkh[R];
   if (any_qk) {
-    if constexpr (kAxes) {
-      int p[R];
-      bool ok = true;
-#pragma unroll
-      for (int e = 0; e < R; ++e) {
-        p[e] = __ldg(pos + map.a[lane * R + e] * T + t);
-        ok = ok && p[e] >= 0 && p[e] < P;
-      }
-      p_ok = __all_sync(0xffffffffu, ok);
-      if (p_ok) {
-#pragma unroll
-        for (int e = 0; e < R; ++e) {
-          const float* col = cs + static_cast<int64_t>(p[e]) * D + lane * R + e;
-          c[e] = __ldg(col);
-          sn[e] = __ldg(col + kHalf);
-        }
-      } else if (lane == 0) {
-        atomicCAS(&g_err_rope, 0u, kErrArg | (41u << 8));
-      }
+    const int p = __ldg(pos + t);
+    p_ok = p >= 0 && p < P;
+    if (!p_ok) {  // nothing is read from the table; the caller gets RNL_ERR_ARG
+      if (lane == 0) atomicCAS(&g_err_rope, 0u, kErrArg | (40u << 8));
     } else {
-      const int p = __ldg(pos + t);
-      p_ok = p >= 0 && p < P;
-      if (!p_ok) {  // nothing is read from the table; the caller gets RNL_ERR_ARG
-        if (lane == 0) atomicCAS(&g_err_rope, 0u, kErrArg | (40u << 8));
-      } else {
-        const float* row = cs + static_cast<int64_t>(p) * D + lane * R;
-        load_f32n<R>(row, c);
-        load_f32n<R>(row + kHalf, sn);
-      }
+      const float* row = cs + static_cast<int64_t>(p) * D + lane * R;
+      load_f32n<R>(row, c);
+      load_f32n<R>(row + kHalf, sn);
     }
-    if (kAxes ? q_gamma != nullptr : Hq > 0) {
+    if (Hq > 0) {
       load_bf16n<R>(q_gamma + lane * R, gql);
       load_bf16n<R>(q_gamma + kHalf + lane * R, gqh);
     }
-    if (kAxes ? k_gamma != nullptr : Hkv > 0) {
+    if (Hkv > 0) {
       load_bf16n<R>(k_gamma + lane * R, gkl);
       load_bf16n<R>(k_gamma + kHalf + lane * R, gkh);
     }
@@ -230,11 +191,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32)
     float ol[R], oh[R];
 #pragma unroll
     for (int e = 0; e < R; ++e) {
-      float zl = lo[j][e], zh = hi[j][e];
-      if (!kAxes || (is_q ? q_gamma : k_gamma) != nullptr) {
-        zl = bf16_round(__fmul_rn(__fmul_rn(zl, r[j]), is_q ? gql[e] : gkl[e]));
-        zh = bf16_round(__fmul_rn(__fmul_rn(zh, r[j]), is_q ? gqh[e] : gkh[e]));
-      }
+      const float zl = bf16_round(__fmul_rn(__fmul_rn(lo[j][e], r[j]), is_q ? gql[e] : gkl[e]));
+      const float zh = bf16_round(__fmul_rn(__fmul_rn(hi[j][e], r[j]), is_q ? gqh[e] : gkh[e]));
       ol[e] = __fsub_rn(__fmul_rn(zl, c[e]), __fmul_rn(zh, sn[e]));
       oh[e] = __fadd_rn(__fmul_rn(zh, c[e]), __fmul_rn(zl, sn[e]));
     }
@@ -247,13 +205,10 @@ __global__ void __launch_bounds__(kRopeWarps * 32)
 
 bool qkv_rope_head_dim_ok(int64_t D) { return D == 64 || D == 128 || D == 256; }
 
-namespace {
-
-template <class Map>
-rnl_status launch_rope(const void* y, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
-                       const void* q_gamma, const void* k_gamma, float eps,
-                       const int32_t* positions, const float* cos_sin, int64_t max_pos, void* q,
-                       void* k, void* v, const Map& map, const char* name, cudaStream_t s) {
+rnl_status launch_qkv_rope(const void* y, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                           const void* q_gamma, const void* k_gamma, float eps,
+                           const int32_t* positions, const float* cos_sin, int64_t max_pos,
+                           void* q, void* k, void* v, cudaStream_t s) {
   const int64_t H = Hq + 2 * Hkv;
   if (T * H == 0) return RNL_OK;
   const int groups = static_cast<int>((H + kHeadsPerWarp - 1) / kHeadsPerWarp);
@@ -269,42 +224,21 @@ rnl_status launch_rope(const void* y, int64_t T, int64_t Hq, int64_t Hkv, int64_
   trace_before(s);
   switch (D) {
     case 64:
-      qkv_rope_kernel<64, Map><<<blocks, kRopeWarps * 32, 0, s>>>(yp, T, hq, hkv, groups, qg, kg, eps,
-                                                                  positions, cos_sin, P, qp, kp, vp, map);
+      qkv_rope_kernel<64><<<blocks, kRopeWarps * 32, 0, s>>>(yp, T, hq, hkv, groups, qg, kg, eps, positions,
+                                                             cos_sin, P, qp, kp, vp);
       break;
     case 128:
-      qkv_rope_kernel<128, Map><<<blocks, kRopeWarps * 32, 0, s>>>(yp, T, hq, hkv, groups, qg, kg, eps,
-                                                                   positions, cos_sin, P, qp, kp, vp, map);
+      qkv_rope_kernel<128><<<blocks, kRopeWarps * 32, 0, s>>>(yp, T, hq, hkv, groups, qg, kg, eps, positions,
+                                                              cos_sin, P, qp, kp, vp);
       break;
     default:
-      qkv_rope_kernel<256, Map><<<blocks, kRopeWarps * 32, 0, s>>>(yp, T, hq, hkv, groups, qg, kg, eps,
-                                                                   positions, cos_sin, P, qp, kp, vp, map);
+      qkv_rope_kernel<256><<<blocks, kRopeWarps * 32, 0, s>>>(yp, T, hq, hkv, groups, qg, kg, eps, positions,
+                                                              cos_sin, P, qp, kp, vp);
       break;
   }
   const rnl_status st = cudaGetLastError() == cudaSuccess ? RNL_OK : RNL_ERR_LAUNCH;
-  trace_after(s, name);
+  trace_after(s, "qkv_rope");
   return st;
-}
-
-}  // namespace
-
-rnl_status launch_qkv_rope(const void* y, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
-                           const void* q_gamma, const void* k_gamma, float eps,
-                           const int32_t* positions, const float* cos_sin, int64_t max_pos,
-                           void* q, void* k, void* v, cudaStream_t s) {
-  return launch_rope(y, T, Hq, Hkv, D, q_gamma, k_gamma, eps, positions, cos_sin, max_pos, q, k, v,
-                     OneAxis{}, "qkv_rope", s);
-}
-
-rnl_status launch_qkv_rope_axes(const void* y, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
-                                const void* q_gamma, const void* k_gamma, float eps,
-                                const int32_t* positions, const uint8_t* axis_of_pair,
-                                const float* cos_sin, int64_t max_pos, void* q, void* k, void* v,
-                                cudaStream_t s) {
-  AxisMap map = {};
-  for (int64_t i = 0; i < D / 2; ++i) map.a[i] = axis_of_pair[i];
-  return launch_rope(y, T, Hq, Hkv, D, q_gamma, k_gamma, eps, positions, cos_sin, max_pos, q, k, v,
-                     map, "qkv_rope_axes", s);
 }
 
 rnl_status read_clear_error_rope(unsigned int* word) {
