@@ -28,7 +28,7 @@ struct Side {
 struct Args {
   Side k, v;
   int n_pages, Hkv, page, page_shift;  // page = tokens a page, a power of two
-  int D, block_shift;                  // log2 of the elements a scale covers
+  int D, d_shift, block_shift;         // D = 1 << d_shift; log2 of the elements a scale covers
   const int* table;                    // [n_seqs, max_pages]
   const int* lens;                     // [n_seqs]
   const int* cu;                       // [n_seqs + 1] or null: one row a sequence
@@ -46,6 +46,7 @@ inline Args make_args(const rnl_kv4_cache& c, const rnl_kv4_seqs& q) {
   a.page_shift = 0;
   while ((1 << a.page_shift) < a.page) ++a.page_shift;
   a.D = static_cast<int>(c.head_dim);
+  a.d_shift = c.head_dim == 64 ? 6 : c.head_dim == 128 ? 7 : 8;
   a.block_shift = c.block == 64 ? 6 : 5;
   a.table = q.block_table;
   a.lens = q.seq_lens;

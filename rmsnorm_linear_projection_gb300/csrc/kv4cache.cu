@@ -11,10 +11,11 @@
 //   gather: the same positions read back, value(code) * 2^X, exact in bf16.
 //
 // Both are bound by their bf16 traffic (2 bytes an element against 0.53 for
-// codes and scales).  One warp takes a (row, k or v, chunk of 1024 elements):
-// the row's sequence and page are looked up once by the warp, every lane
-// moves 8 elements (16 bytes of bf16, 4 bytes of codes) an access, four in
-// flight.
+// codes and scales).  One warp takes a chunk of 1024 elements (k or v) of
+// two consecutive rows; every lane moves 8 elements (16 bytes of bf16,
+// 4 bytes of codes) an access, all of the warp's on their way at once.  The
+// sequence is looked up once and kept while the rows stay in it; the writer's
+// loads do not wait for it.
 #include "kv4.cuh"
 
 namespace rnl {
@@ -25,124 +26,163 @@ using namespace kv4;
 __device__ unsigned int g_err_kv4cache;
 
 constexpr int kCacheWarps = 4;
-constexpr int kVecs = 4;  // 8-element vectors a lane has in flight
+constexpr int kVecs = 4;  // 8-element vectors of a row that a lane takes
 
-// The (row, side, chunk) of this warp and the cache row of its head 0.
+// The (rows, side, chunk) of this warp.
 struct WarpJob {
-  int t, chunk;
+  int t0, n, chunk;  // first row, number of rows
   bool is_v;
-  int64_t row0;
 };
+template <int ROWS>
 __device__ __forceinline__ bool warp_job(const Args& a, int chunks, WarpJob& j) {
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kCacheWarps + (threadIdx.x >> 5);
-  if (w >= static_cast<int64_t>(a.n_rows) * 2 * chunks) return false;
-  j.t = static_cast<int>(w / (2 * chunks));
-  const int rest = static_cast<int>(w - static_cast<int64_t>(j.t) * 2 * chunks);
+  const int groups = (a.n_rows + ROWS - 1) / ROWS;
+  if (w >= static_cast<int64_t>(groups) * 2 * chunks) return false;
+  const int g = static_cast<int>(w / (2 * chunks));
+  const int rest = static_cast<int>(w - static_cast<int64_t>(g) * 2 * chunks);
   j.is_v = rest >= chunks;
   j.chunk = j.is_v ? rest - chunks : rest;
-  const int b = seq_of_row(a, j.t);
-  if (b < 0) return false;  // rows behind the last sequence are left alone
-  Seq s;
-  if (!load_seq(a, b, s, &g_err_kv4cache, 42)) return false;
-  if (j.t < s.row0) return false;  // cu_rows out of order
-  const int pos = s.len - s.rows + (j.t - s.row0);
-  if (pos < 0) {  // more rows than the length counts
-    atomicCAS(&g_err_kv4cache, 0u, kErrArg | (43u << 8));
-    return false;
-  }
-  j.row0 = token_row(a, b, pos, 0, &g_err_kv4cache, 44);
-  return j.row0 >= 0;
+  j.t0 = g * ROWS;
+  j.n = min(ROWS, a.n_rows - j.t0);
+  return true;
 }
 
+// The cache row of head 0 for row t, -1 where there is none; the sequence is
+// looked up when t has left it.
+struct Place {
+  int b = -2;
+  Seq s = {0, 0, 0};
+};
+__device__ __forceinline__ int64_t row_of(const Args& a, int t, Place& at) {
+  if (at.b < 0 || t < at.s.row0 || t >= at.s.row0 + at.s.rows) {
+    at.b = seq_of_row(a, t);
+    if (at.b < 0) return -1;  // rows behind the last sequence are left alone
+    if (!load_seq(a, at.b, at.s, &g_err_kv4cache, 42) || t < at.s.row0) {  // or cu_rows out of order
+      at.b = -2;
+      return -1;
+    }
+  }
+  const int pos = at.s.len - at.s.rows + (t - at.s.row0);
+  if (pos < 0) {  // more rows than the length counts
+    atomicCAS(&g_err_kv4cache, 0u, kErrArg | (43u << 8));
+    return -1;
+  }
+  return token_row(a, at.b, pos, 0, &g_err_kv4cache, 44);
+}
+
+constexpr int kAppendRows = 2;
 __global__ void __launch_bounds__(kCacheWarps * 32)
     kv4_append_kernel(const __nv_bfloat16* __restrict__ k, int64_t k_stride,
                       const __nv_bfloat16* __restrict__ v, int64_t v_stride, const Args a, int chunks) {
   WarpJob j;
-  if (!warp_job(a, chunks, j)) return;
+  if (!warp_job<kAppendRows>(a, chunks, j)) return;
   const int lane = threadIdx.x & 31;
-  const __nv_bfloat16* src = j.is_v ? v + j.t * v_stride : k + j.t * k_stride;
   const Side side = j.is_v ? a.v : a.k;
   const int n = a.Hkv * a.D;
   const int e0 = (j.chunk * kVecs * 32 + lane) * 8;
-  uint4 x[kVecs];
+  uint4 x[kAppendRows][kVecs];
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int e = e0 + i * 256;
-    x[i] = e < n ? __ldg(reinterpret_cast<const uint4*>(src + e)) : make_uint4(0, 0, 0, 0);
-  }
+  for (int r = 0; r < kAppendRows; ++r) {
+    const int t = j.t0 + min(r, j.n - 1);
+    const __nv_bfloat16* src = j.is_v ? v + t * v_stride : k + t * k_stride;
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int e = e0 + i * 256;
-    float f[8];
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    // the largest magnitude by its bits: a NaN or infinity gives exponent 255
-    uint32_t am = 0;
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      f[2 * p] = __uint_as_float(w[p] << 16);
-      f[2 * p + 1] = __uint_as_float(w[p] & 0xFFFF0000u);
-      am = max(am, max((w[p] << 16) & 0x7FFFFFFFu, w[p] & 0x7FFF0000u));
+    for (int i = 0; i < kVecs; ++i) {
+      const int e = e0 + i * 256;
+      x[r][i] = e < n ? __ldg(reinterpret_cast<const uint4*>(src + e)) : make_uint4(0, 0, 0, 0);
     }
-    am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
-    am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-    if (a.block_shift == 6) am = max(am, __shfl_xor_sync(0xffffffffu, am, 4));
-    const int eb = static_cast<int>(am >> 23);
-    const int byte = eb == 255 ? 255 : max(eb - 2, 0);
-    // 2^-X for X = byte - 127: exponent field 254 - byte, at least 1 (byte <= 252)
-    const float inv = __uint_as_float(static_cast<uint32_t>(max(254 - byte, 1)) << 23);
+  }
+  Place at;
+  int64_t row0[kAppendRows];
 #pragma unroll
-    for (int p = 0; p < 8; ++p) f[p] = __fmul_rn(f[p], inv);
-    if (e >= n) continue;
-    const int head = e / a.D, d = e - head * a.D;
-    const int64_t row = j.row0 + (static_cast<int64_t>(head) << a.page_shift);
-    *reinterpret_cast<uint32_t*>(side.codes + (row * a.D + d) / 2) = e2m1x8_code(f);
-    if ((d & ((1 << a.block_shift) - 1)) == 0)
-      side.scales[row * (a.D >> a.block_shift) + (d >> a.block_shift)] = static_cast<uint8_t>(byte);
+  for (int r = 0; r < kAppendRows; ++r) row0[r] = r < j.n ? row_of(a, j.t0 + r, at) : -1;
+#pragma unroll
+  for (int r = 0; r < kAppendRows; ++r) {
+    if (row0[r] < 0) continue;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int e = e0 + i * 256;
+      float f[8];
+      const uint32_t w[4] = {x[r][i].x, x[r][i].y, x[r][i].z, x[r][i].w};
+      // the largest magnitude by its bits: a NaN or infinity gives exponent 255
+      uint32_t am = 0;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        f[2 * p] = __uint_as_float(w[p] << 16);
+        f[2 * p + 1] = __uint_as_float(w[p] & 0xFFFF0000u);
+        am = max(am, max((w[p] << 16) & 0x7FFFFFFFu, w[p] & 0x7FFF0000u));
+      }
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+      if (a.block_shift == 6) am = max(am, __shfl_xor_sync(0xffffffffu, am, 4));
+      const int eb = static_cast<int>(am >> 23);
+      const int byte = eb == 255 ? 255 : max(eb - 2, 0);
+      // 2^-X for X = byte - 127: exponent field 254 - byte, at least 1 (byte <= 252)
+      const float inv = __uint_as_float(static_cast<uint32_t>(max(254 - byte, 1)) << 23);
+#pragma unroll
+      for (int p = 0; p < 8; ++p) f[p] = __fmul_rn(f[p], inv);
+      if (e >= n) continue;
+      const int head = e >> a.d_shift, d = e & (a.D - 1);
+      const int64_t row = row0[r] + (static_cast<int64_t>(head) << a.page_shift);
+      *reinterpret_cast<uint32_t*>(side.codes + ((row << a.d_shift) + d) / 2) = e2m1x8_code(f);
+      if ((d & ((1 << a.block_shift) - 1)) == 0)
+        side.scales[(row << (a.d_shift - a.block_shift)) + (d >> a.block_shift)] = static_cast<uint8_t>(byte);
+    }
   }
 }
 
+constexpr int kGatherRows = 2;
 __global__ void __launch_bounds__(kCacheWarps * 32)
     kv4_gather_kernel(const Args a, __nv_bfloat16* __restrict__ k, __nv_bfloat16* __restrict__ v, int chunks) {
   WarpJob j;
-  if (!warp_job(a, chunks, j)) return;
+  if (!warp_job<kGatherRows>(a, chunks, j)) return;
   const int lane = threadIdx.x & 31;
   const int n = a.Hkv * a.D;
-  __nv_bfloat16* dst = (j.is_v ? v : k) + static_cast<int64_t>(j.t) * n;
   const Side side = j.is_v ? a.v : a.k;
   const int e0 = (j.chunk * kVecs * 32 + lane) * 8;
-  uint32_t c[kVecs], s[kVecs];
+  Place at;
+  int64_t row0[kGatherRows];
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int e = e0 + i * 256;
-    if (e < n) {
-      const int head = e / a.D, d = e - head * a.D;
-      const int64_t row = j.row0 + (static_cast<int64_t>(head) << a.page_shift);
-      c[i] = __ldg(reinterpret_cast<const uint32_t*>(side.codes + (row * a.D + d) / 2));
-      s[i] = __ldg(side.scales + row * (a.D >> a.block_shift) + (d >> a.block_shift));
+  for (int r = 0; r < kGatherRows; ++r) row0[r] = r < j.n ? row_of(a, j.t0 + r, at) : -1;
+  uint32_t c[kGatherRows][kVecs], s[kGatherRows][kVecs];
+#pragma unroll
+  for (int r = 0; r < kGatherRows; ++r)
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int e = e0 + i * 256;
+      if (row0[r] >= 0 && e < n) {
+        const int head = e >> a.d_shift, d = e & (a.D - 1);
+        const int64_t row = row0[r] + (static_cast<int64_t>(head) << a.page_shift);
+        c[r][i] = __ldg(reinterpret_cast<const uint32_t*>(side.codes + ((row << a.d_shift) + d) / 2));
+        s[r][i] = __ldg(side.scales + (row << (a.d_shift - a.block_shift)) + (d >> a.block_shift));
+      }
     }
-  }
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int e = e0 + i * 256;
-    if (e >= n) break;
-    uint32_t h[4], o[4];
-    e2m1x8_to_half(c[i], h);
-    const float p = e8m0_value(s[i]);
+  for (int r = 0; r < kGatherRows; ++r) {
+    if (row0[r] < 0) continue;
+    __nv_bfloat16* dst = (j.is_v ? v : k) + static_cast<int64_t>(j.t0 + r) * n;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[q]));
-      const __nv_bfloat162 b = __floats2bfloat162_rn(__fmul_rn(f.x, p), __fmul_rn(f.y, p));
-      o[q] = *reinterpret_cast<const uint32_t*>(&b);
+    for (int i = 0; i < kVecs; ++i) {
+      const int e = e0 + i * 256;
+      if (e >= n) break;
+      uint32_t h[4], o[4];
+      e2m1x8_to_half(c[r][i], h);
+      const float p = e8m0_value(s[r][i]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[q]));
+        const __nv_bfloat162 b = __floats2bfloat162_rn(__fmul_rn(f.x, p), __fmul_rn(f.y, p));
+        o[q] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      *reinterpret_cast<uint4*>(dst + e) = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    *reinterpret_cast<uint4*>(dst + e) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
 inline int chunks_of(const rnl_kv4_cache& c) {
   return static_cast<int>((c.n_kv_heads * c.head_dim + kVecs * 256 - 1) / (kVecs * 256));
 }
-inline unsigned blocks_of(const rnl_kv4_seqs& q, int chunks) {
-  return static_cast<unsigned>((q.n_rows * 2 * chunks + kCacheWarps - 1) / kCacheWarps);
+inline unsigned blocks_of(const rnl_kv4_seqs& q, int rows, int chunks) {
+  return static_cast<unsigned>(((q.n_rows + rows - 1) / rows * 2 * chunks + kCacheWarps - 1) / kCacheWarps);
 }
 
 }  // namespace
@@ -151,7 +191,7 @@ rnl_status launch_kv4_append(const void* k, int64_t k_stride, const void* v, int
                              const rnl_kv4_cache& c, const rnl_kv4_seqs& q, cudaStream_t s) {
   const int chunks = chunks_of(c);
   trace_before(s);
-  kv4_append_kernel<<<blocks_of(q, chunks), kCacheWarps * 32, 0, s>>>(
+  kv4_append_kernel<<<blocks_of(q, kAppendRows, chunks), kCacheWarps * 32, 0, s>>>(
       static_cast<const __nv_bfloat16*>(k), k_stride, static_cast<const __nv_bfloat16*>(v), v_stride,
       make_args(c, q), chunks);
   const rnl_status st = cudaGetLastError() == cudaSuccess ? RNL_OK : RNL_ERR_LAUNCH;
@@ -163,7 +203,7 @@ rnl_status launch_kv4_gather(const rnl_kv4_cache& c, const rnl_kv4_seqs& q, void
                              cudaStream_t s) {
   const int chunks = chunks_of(c);
   trace_before(s);
-  kv4_gather_kernel<<<blocks_of(q, chunks), kCacheWarps * 32, 0, s>>>(
+  kv4_gather_kernel<<<blocks_of(q, kGatherRows, chunks), kCacheWarps * 32, 0, s>>>(
       make_args(c, q), static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out), chunks);
   const rnl_status st = cudaGetLastError() == cudaSuccess ? RNL_OK : RNL_ERR_LAUNCH;
   trace_after(s, "kv4_gather");
