@@ -11,11 +11,10 @@
 //   gather: the same positions read back, value(code) * 2^X, exact in bf16.
 //
 // Both are bound by their bf16 traffic (2 bytes an element against 0.53 for
-// codes and scales).  One warp takes a chunk of 1024 elements (k or v) of
-// two consecutive rows; every lane moves 8 elements (16 bytes of bf16,
-// 4 bytes of codes) an access, all of the warp's on their way at once.  The
-// sequence is looked up once and kept while the rows stay in it; the writer's
-// loads do not wait for it.
+// codes and scales).  One warp takes 1024 elements of one row, of k and of v:
+// every lane moves 8 elements (16 bytes of bf16, 4 bytes of codes) an access,
+// eight accesses on their way at once, and the sequence is looked up once for
+// both sides; the writer's loads do not wait for it.
 #include "kv4.cuh"
 
 namespace rnl {
@@ -28,76 +27,50 @@ __device__ unsigned int g_err_kv4cache;
 constexpr int kCacheWarps = 4;
 constexpr int kVecs = 4;  // 8-element vectors of a row that a lane takes
 
-// The (rows, side, chunk) of this warp.
-struct WarpJob {
-  int t0, n, chunk;  // first row, number of rows
-  bool is_v;
-};
-template <int ROWS>
-__device__ __forceinline__ bool warp_job(const Args& a, int chunks, WarpJob& j) {
+// The row and chunk of this warp.
+__device__ __forceinline__ bool warp_job(const Args& a, int chunks, int& t, int& chunk) {
   const int64_t w = static_cast<int64_t>(blockIdx.x) * kCacheWarps + (threadIdx.x >> 5);
-  const int groups = (a.n_rows + ROWS - 1) / ROWS;
-  if (w >= static_cast<int64_t>(groups) * 2 * chunks) return false;
-  const int g = static_cast<int>(w / (2 * chunks));
-  const int rest = static_cast<int>(w - static_cast<int64_t>(g) * 2 * chunks);
-  j.is_v = rest >= chunks;
-  j.chunk = j.is_v ? rest - chunks : rest;
-  j.t0 = g * ROWS;
-  j.n = min(ROWS, a.n_rows - j.t0);
+  if (w >= static_cast<int64_t>(a.n_rows) * chunks) return false;
+  t = static_cast<int>(w / chunks);
+  chunk = static_cast<int>(w - static_cast<int64_t>(t) * chunks);
   return true;
 }
 
-// The cache row of head 0 for row t, -1 where there is none; the sequence is
-// looked up when t has left it.
-struct Place {
-  int b = -2;
-  Seq s = {0, 0, 0};
-};
-__device__ __forceinline__ int64_t row_of(const Args& a, int t, Place& at) {
-  if (at.b < 0 || t < at.s.row0 || t >= at.s.row0 + at.s.rows) {
-    at.b = seq_of_row(a, t);
-    if (at.b < 0) return -1;  // rows behind the last sequence are left alone
-    if (!load_seq(a, at.b, at.s, &g_err_kv4cache, 42) || t < at.s.row0) {  // or cu_rows out of order
-      at.b = -2;
-      return -1;
-    }
-  }
-  const int pos = at.s.len - at.s.rows + (t - at.s.row0);
+// The cache row of head 0 for row t, -1 where there is none.
+__device__ __forceinline__ int64_t row_of(const Args& a, int t) {
+  const int b = seq_of_row(a, t);
+  if (b < 0) return -1;  // rows behind the last sequence are left alone
+  Seq s;
+  if (!load_seq(a, b, s, &g_err_kv4cache, 42) || t < s.row0) return -1;  // or cu_rows out of order
+  const int pos = s.len - s.rows + (t - s.row0);
   if (pos < 0) {  // more rows than the length counts
     atomicCAS(&g_err_kv4cache, 0u, kErrArg | (43u << 8));
     return -1;
   }
-  return token_row(a, at.b, pos, 0, &g_err_kv4cache, 44);
+  return token_row(a, b, pos, 0, &g_err_kv4cache, 44);
 }
 
-constexpr int kAppendRows = 2;
 __global__ void __launch_bounds__(kCacheWarps * 32)
     kv4_append_kernel(const __nv_bfloat16* __restrict__ k, int64_t k_stride,
                       const __nv_bfloat16* __restrict__ v, int64_t v_stride, const Args a, int chunks) {
-  WarpJob j;
-  if (!warp_job<kAppendRows>(a, chunks, j)) return;
-  const int lane = threadIdx.x & 31;
-  const Side side = j.is_v ? a.v : a.k;
+  int t, chunk;
+  if (!warp_job(a, chunks, t, chunk)) return;
   const int n = a.Hkv * a.D;
-  const int e0 = (j.chunk * kVecs * 32 + lane) * 8;
-  uint4 x[kAppendRows][kVecs];
+  const int e0 = (chunk * kVecs * 32 + (threadIdx.x & 31)) * 8;
+  const __nv_bfloat16* const src[2] = {k + t * k_stride, v + t * v_stride};
+  uint4 x[2][kVecs];
 #pragma unroll
-  for (int r = 0; r < kAppendRows; ++r) {
-    const int t = j.t0 + min(r, j.n - 1);
-    const __nv_bfloat16* src = j.is_v ? v + t * v_stride : k + t * k_stride;
+  for (int r = 0; r < 2; ++r)
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const int e = e0 + i * 256;
-      x[r][i] = e < n ? __ldg(reinterpret_cast<const uint4*>(src + e)) : make_uint4(0, 0, 0, 0);
+      x[r][i] = e < n ? __ldg(reinterpret_cast<const uint4*>(src[r] + e)) : make_uint4(0, 0, 0, 0);
     }
-  }
-  Place at;
-  int64_t row0[kAppendRows];
+  const int64_t row0 = row_of(a, t);
+  if (row0 < 0) return;
 #pragma unroll
-  for (int r = 0; r < kAppendRows; ++r) row0[r] = r < j.n ? row_of(a, j.t0 + r, at) : -1;
-#pragma unroll
-  for (int r = 0; r < kAppendRows; ++r) {
-    if (row0[r] < 0) continue;
+  for (int r = 0; r < 2; ++r) {
+    const Side& side = r == 0 ? a.k : a.v;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const int e = e0 + i * 256;
@@ -122,7 +95,7 @@ __global__ void __launch_bounds__(kCacheWarps * 32)
       for (int p = 0; p < 8; ++p) f[p] = __fmul_rn(f[p], inv);
       if (e >= n) continue;
       const int head = e >> a.d_shift, d = e & (a.D - 1);
-      const int64_t row = row0[r] + (static_cast<int64_t>(head) << a.page_shift);
+      const int64_t row = row0 + (static_cast<int64_t>(head) << a.page_shift);
       *reinterpret_cast<uint32_t*>(side.codes + ((row << a.d_shift) + d) / 2) = e2m1x8_code(f);
       if ((d & ((1 << a.block_shift) - 1)) == 0)
         side.scales[(row << (a.d_shift - a.block_shift)) + (d >> a.block_shift)] = static_cast<uint8_t>(byte);
@@ -130,36 +103,32 @@ __global__ void __launch_bounds__(kCacheWarps * 32)
   }
 }
 
-constexpr int kGatherRows = 2;
 __global__ void __launch_bounds__(kCacheWarps * 32)
     kv4_gather_kernel(const Args a, __nv_bfloat16* __restrict__ k, __nv_bfloat16* __restrict__ v, int chunks) {
-  WarpJob j;
-  if (!warp_job<kGatherRows>(a, chunks, j)) return;
-  const int lane = threadIdx.x & 31;
+  int t, chunk;
+  if (!warp_job(a, chunks, t, chunk)) return;
   const int n = a.Hkv * a.D;
-  const Side side = j.is_v ? a.v : a.k;
-  const int e0 = (j.chunk * kVecs * 32 + lane) * 8;
-  Place at;
-  int64_t row0[kGatherRows];
+  const int e0 = (chunk * kVecs * 32 + (threadIdx.x & 31)) * 8;
+  const int64_t row0 = row_of(a, t);
+  if (row0 < 0) return;
+  uint32_t c[2][kVecs], s[2][kVecs];
 #pragma unroll
-  for (int r = 0; r < kGatherRows; ++r) row0[r] = r < j.n ? row_of(a, j.t0 + r, at) : -1;
-  uint32_t c[kGatherRows][kVecs], s[kGatherRows][kVecs];
-#pragma unroll
-  for (int r = 0; r < kGatherRows; ++r)
+  for (int r = 0; r < 2; ++r) {
+    const Side& side = r == 0 ? a.k : a.v;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const int e = e0 + i * 256;
-      if (row0[r] >= 0 && e < n) {
+      if (e < n) {
         const int head = e >> a.d_shift, d = e & (a.D - 1);
-        const int64_t row = row0[r] + (static_cast<int64_t>(head) << a.page_shift);
+        const int64_t row = row0 + (static_cast<int64_t>(head) << a.page_shift);
         c[r][i] = __ldg(reinterpret_cast<const uint32_t*>(side.codes + ((row << a.d_shift) + d) / 2));
         s[r][i] = __ldg(side.scales + (row << (a.d_shift - a.block_shift)) + (d >> a.block_shift));
       }
     }
+  }
 #pragma unroll
-  for (int r = 0; r < kGatherRows; ++r) {
-    if (row0[r] < 0) continue;
-    __nv_bfloat16* dst = (j.is_v ? v : k) + static_cast<int64_t>(j.t0 + r) * n;
+  for (int r = 0; r < 2; ++r) {
+    __nv_bfloat16* dst = (r == 0 ? k : v) + static_cast<int64_t>(t) * n;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       const int e = e0 + i * 256;
@@ -181,8 +150,8 @@ __global__ void __launch_bounds__(kCacheWarps * 32)
 inline int chunks_of(const rnl_kv4_cache& c) {
   return static_cast<int>((c.n_kv_heads * c.head_dim + kVecs * 256 - 1) / (kVecs * 256));
 }
-inline unsigned blocks_of(const rnl_kv4_seqs& q, int rows, int chunks) {
-  return static_cast<unsigned>(((q.n_rows + rows - 1) / rows * 2 * chunks + kCacheWarps - 1) / kCacheWarps);
+inline unsigned blocks_of(const rnl_kv4_seqs& q, int chunks) {
+  return static_cast<unsigned>((q.n_rows * chunks + kCacheWarps - 1) / kCacheWarps);
 }
 
 }  // namespace
@@ -191,7 +160,7 @@ rnl_status launch_kv4_append(const void* k, int64_t k_stride, const void* v, int
                              const rnl_kv4_cache& c, const rnl_kv4_seqs& q, cudaStream_t s) {
   const int chunks = chunks_of(c);
   trace_before(s);
-  kv4_append_kernel<<<blocks_of(q, kAppendRows, chunks), kCacheWarps * 32, 0, s>>>(
+  kv4_append_kernel<<<blocks_of(q, chunks), kCacheWarps * 32, 0, s>>>(
       static_cast<const __nv_bfloat16*>(k), k_stride, static_cast<const __nv_bfloat16*>(v), v_stride,
       make_args(c, q), chunks);
   const rnl_status st = cudaGetLastError() == cudaSuccess ? RNL_OK : RNL_ERR_LAUNCH;
@@ -203,7 +172,7 @@ rnl_status launch_kv4_gather(const rnl_kv4_cache& c, const rnl_kv4_seqs& q, void
                              cudaStream_t s) {
   const int chunks = chunks_of(c);
   trace_before(s);
-  kv4_gather_kernel<<<blocks_of(q, kGatherRows, chunks), kCacheWarps * 32, 0, s>>>(
+  kv4_gather_kernel<<<blocks_of(q, chunks), kCacheWarps * 32, 0, s>>>(
       make_args(c, q), static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out), chunks);
   const rnl_status st = cudaGetLastError() == cudaSuccess ? RNL_OK : RNL_ERR_LAUNCH;
   trace_after(s, "kv4_gather");

@@ -27,7 +27,7 @@ namespace {
 
 __device__ unsigned int g_err_axes;  // kErrArg | site: a position outside [0, P)
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kGroups = 4;  // head groups a warp has in flight
 
 struct AxisMap {
@@ -55,7 +55,7 @@ __device__ __forceinline__ float bf16_round(float v) { return __bfloat162float(_
 
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32)
-    qkv_rope_axes_kernel(const __nv_bfloat16* __restrict__ y, int64_t T, int Hq, int Hkv, int parts,
+    qkv_rope_axes_kernel(const __nv_bfloat16* __restrict__ y, int64_t T, int Hq, int Hkv, int parts, int per,
                          const __nv_bfloat16* __restrict__ q_gamma, const __nv_bfloat16* __restrict__ k_gamma,
                          float eps, const int* __restrict__ pos, const float* __restrict__ cs, int P,
                          __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ k,
@@ -70,13 +70,14 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int64_t wid = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (wid >= T * parts) return;
   const int64_t t = wid / parts;
-  const int h0 = static_cast<int>(wid - t * parts) * kGroups * kHeads;
+  const int h0 = static_cast<int>(wid - t * parts) * per * kHeads;
+  const int h1 = min(h0 + per * kHeads, H);  // the warp's heads [h0, h1)
   const __nv_bfloat16* yt = y + t * H * D + sub * 8;
   uint4 lo[kGroups], hi[kGroups];
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
     const int h = h0 + g * kHeads + lane / kLanes;
-    if (h < H) {
+    if (h < h1) {
       lo[g] = __ldg(reinterpret_cast<const uint4*>(yt + static_cast<int64_t>(h) * D));
       hi[g] = __ldg(reinterpret_cast<const uint4*>(yt + static_cast<int64_t>(h) * D + kHalf));
     }
@@ -114,9 +115,9 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
-    if (h0 + g * kHeads >= H) break;  // the warp's last group
+    if (h0 + g * kHeads >= h1) break;
     const int h = h0 + g * kHeads + lane / kLanes;
-    const bool live = h < H, turned = live && h < nqk, is_q = h < Hq;
+    const bool live = h < h1, turned = live && h < nqk, is_q = h < Hq;
     const __nv_bfloat16* gamma = is_q ? q_gamma : k_gamma;
     float fl[8], fh[8];
     unpack8(lo[g], fl);
@@ -177,11 +178,13 @@ template <int D>
 void launch(const void* y, int64_t T, int64_t Hq, int64_t Hkv, const void* q_gamma, const void* k_gamma,
             float eps, const int32_t* positions, const float* cos_sin, int64_t max_pos, void* q, void* k,
             void* v, const AxisMap& map, cudaStream_t s) {
-  constexpr int kPer = kGroups * 512 / D;  // heads a warp
-  const int64_t parts = (Hq + 2 * Hkv + kPer - 1) / kPer;
+  constexpr int kHeads = 512 / D;  // heads a group
+  const int64_t groups = (Hq + 2 * Hkv + kHeads - 1) / kHeads;
+  const int64_t parts = (groups + kGroups - 1) / kGroups;  // warps a token, their groups spread evenly
+  const int64_t per = (groups + parts - 1) / parts;
   const unsigned blocks = static_cast<unsigned>((T * parts + kWarps - 1) / kWarps);
   qkv_rope_axes_kernel<D><<<blocks, kWarps * 32, 0, s>>>(
-      static_cast<const __nv_bfloat16*>(y), T, static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(parts),
+      static_cast<const __nv_bfloat16*>(y), T, static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(parts), static_cast<int>(per),
       static_cast<const __nv_bfloat16*>(q_gamma), static_cast<const __nv_bfloat16*>(k_gamma), eps, positions, cos_sin,
       static_cast<int>(max_pos), static_cast<__nv_bfloat16*>(q), static_cast<__nv_bfloat16*>(k),
       static_cast<__nv_bfloat16*>(v), map);
