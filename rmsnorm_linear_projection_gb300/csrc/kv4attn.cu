@@ -54,7 +54,7 @@ constexpr int kMaxCtas = 640;                              // partial-sum slots 
 
 // What an item costs a CTA beside its tiles (queries, joining the warps), in
 // tiles: counted when the tiles are dealt out.
-constexpr int kItemCost = 2;
+constexpr int kItemCost = 6;
 
 template <int D, int NT>
 struct Cfg {
