@@ -162,8 +162,8 @@ def _stream(device, stream):
     if device.index is not None and device.index != cur:
         raise ValueError(f"tensors are on {device} but the current CUDA device is cuda:{cur}; "
                          f"make the call under torch.cuda.device({device})")
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+    # (the handle itself: making a Stream object costs a small call 2 us)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(cur) if stream is None else stream.cuda_stream)
 
 
 def _check(status, what):
@@ -176,7 +176,7 @@ def _need(t, name, dtype, shape, device):
         raise ValueError(f"{name} is required")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -293,9 +293,9 @@ def rnl_qkv_rope_axes(y, n_q_heads, n_kv_heads, head_dim, q_gamma, k_gamma, posi
         _need(k_gamma, "k_gamma", torch.bfloat16, (D,), dev)
     A = positions.shape[0]
     _need(positions, "positions", torch.int32, (A, T), dev)
+    if len(axis_of_pair) != D // 2:
+        raise ValueError(f"axis_of_pair must hold {D // 2} values, got {len(axis_of_pair)}")
     axes = bytes(axis_of_pair)
-    if len(axes) != D // 2:
-        raise ValueError(f"axis_of_pair must hold {D // 2} values, got {len(axes)}")
     P = cos_sin.shape[0]
     _need(cos_sin, "cos_sin", torch.float32, (P, D), dev)
     q_out, k_out, v_out = _qkv_outputs(T, Hq, Hkv, D, dev, q_out, k_out, v_out)
@@ -337,27 +337,36 @@ class Kv4Cache:
 
 def _kv4_seqs(cache, block_table, seq_lens, cu_rows, n_rows):
     dev = cache.device
-    B = seq_lens.shape[0]
+    B, pages = seq_lens.shape[0], block_table.shape[-1]
     _need(seq_lens, "seq_lens", torch.int32, (B,), dev)
-    _need(block_table, "block_table", torch.int32, (B, block_table.shape[-1]), dev)
+    _need(block_table, "block_table", torch.int32, (B, pages), dev)
     if cu_rows is not None:
         _need(cu_rows, "cu_rows", torch.int32, (B + 1,), dev)
     return _Kv4SeqsC(block_table.data_ptr(), seq_lens.data_ptr(), None if cu_rows is None else cu_rows.data_ptr(),
-                     B, block_table.shape[-1], n_rows)
+                     B, pages, n_rows)
 
 
 def _need_rows(t, name, shape, device):
     """A bf16 [rows, heads, head_dim] tensor whose rows may be apart; the row stride."""
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     T, H, D = shape
-    if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D)):
+    row, head, one = t.stride()
+    if T and H and (one != 1 or (H > 1 and head != D)):
         raise ValueError(f"{name} must have contiguous rows of heads")
-    return t.stride(0) if T > 1 else H * D
+    return row if T > 1 else H * D
+
+
+def _out(t, name, dtype, shape, device):
+    """An output: the caller's, checked, or a new tensor."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, name, dtype, shape, device)
+    return t
 
 
 def rnl_kv4_append(k, v, cache, block_table, seq_lens, cu_rows=None, stream=None):
@@ -365,8 +374,9 @@ def rnl_kv4_append(k, v, cache, block_table, seq_lens, cu_rows=None, stream=None
     last positions of their sequences; seq_lens counts them already."""
     T = k.shape[0]
     dev = cache.device
-    ks = _need_rows(k, "k", (T, cache.n_kv_heads, cache.head_dim), dev)
-    vs = _need_rows(v, "v", (T, cache.n_kv_heads, cache.head_dim), dev)
+    shape = (T, cache.n_kv_heads, cache.head_dim)
+    ks = _need_rows(k, "k", shape, dev)
+    vs = _need_rows(v, "v", shape, dev)
     seqs = _kv4_seqs(cache, block_table, seq_lens, cu_rows, T)
     _check(load().rnl_kv4_append(_ptr(k), ks, _ptr(v), vs, cache._c(), seqs, _stream(dev, stream)),
            "rnl_kv4_append")
@@ -377,11 +387,9 @@ def rnl_kv4_gather(cache, block_table, seq_lens, n_rows, cu_rows=None, k_out=Non
     returns (k, v) [n_rows, Hkv, D]."""
     dev = cache.device
     shape = (n_rows, cache.n_kv_heads, cache.head_dim)
-    k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k_out is None else k_out
-    v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v_out is None else v_out
-    _need(k_out, "k_out", torch.bfloat16, shape, dev)
-    _need(v_out, "v_out", torch.bfloat16, shape, dev)
     seqs = _kv4_seqs(cache, block_table, seq_lens, cu_rows, n_rows)
+    k_out = _out(k_out, "k_out", torch.bfloat16, shape, dev)
+    v_out = _out(v_out, "v_out", torch.bfloat16, shape, dev)
     _check(load().rnl_kv4_gather(cache._c(), seqs, _ptr(k_out), _ptr(v_out), _stream(dev, stream)),
            "rnl_kv4_gather")
     return k_out, v_out
@@ -395,12 +403,10 @@ def rnl_kv4_attention(q, cache, block_table, seq_lens, cu_rows=None, scale=None,
     D = cache.head_dim
     dev = cache.device
     qs = _need_rows(q, "q", (T, Hq, D), dev)
-    if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-    _need(out, "out", torch.bfloat16, (T, Hq, D), dev)
+    seqs = _kv4_seqs(cache, block_table, seq_lens, cu_rows, T)
     if lse_out is not None:
         _need(lse_out, "lse_out", torch.float32, (T, Hq), dev)
-    seqs = _kv4_seqs(cache, block_table, seq_lens, cu_rows, T)
+    out = _out(out, "out", torch.bfloat16, (T, Hq, D), dev)
     ws = _workspace(workspace_size(OP_KV4_ATTENTION, T, D, Hq, cache.n_kv_heads), dev, workspace)
     _check(load().rnl_kv4_attention(_ptr(q), qs, Hq, cache._c(), seqs,
                                     float(D ** -0.5 if scale is None else scale), int(bool(causal)), int(window),
