@@ -384,7 +384,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
       const bool edge = tok0 < cur.w.lo || tok0 + TT > cur.w.hi;
       // largest scale byte of a side; at an edge of what the rows read, the
       // scale bytes of tokens that no row reads become 0 first, so that
-      // whatever stands there gives zero operands
+      // whatever stands there gives zero operands.  A block that is not finite
+      // (byte 255) becomes zeros too, and the rows that read its token get a
+      // normaliser that is not a number
       auto top_scale = [&](uint8_t* scales) {
         uint32_t* sc = reinterpret_cast<uint32_t*>(scales) + lane;
         uint32_t w[kSW];
@@ -407,19 +409,48 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
           fence_proxy_async_shared();  // the next copy into this buffer comes after these writes
           __syncwarp();
         }
-        uint32_t t = w[0];
-        if constexpr (kSW == 2) t = __vmaxu4(t, w[1]);
-        t = __vmaxu4(t, t >> 16);
-        return static_cast<int>(__reduce_max_sync(0xffffffffu, max(t & 0xFFu, (t >> 8) & 0xFFu)));
+        auto top = [&]() {
+          uint32_t t = w[0];
+          if constexpr (kSW == 2) t = __vmaxu4(t, w[1]);
+          t = __vmaxu4(t, t >> 16);
+          return static_cast<int>(__reduce_max_sync(0xffffffffu, max(t & 0xFFu, (t >> 8) & 0xFFu)));
+        };
+        const int all = top();
+        if (all != 255) return all;
+        uint64_t bad = 0;
+#pragma unroll
+        for (int y = 0; y < kSW; ++y) {
+          uint32_t keep = 0;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            if ((w[y] >> (8 * x) & 0xFFu) == 255u)
+              bad |= 1ull << ((y * 32 + lane) * 4 + x) / kSB;
+            else
+              keep |= 0xFFu << (8 * x);
+          }
+          w[y] &= keep;
+          if ((y * 32 + lane) * 4 < TT * kSB) sc[y * 32] = w[y];
+        }
+        bad = static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bad >> 32))) << 32 |
+              __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bad));
+        fence_proxy_async_shared();
+        __syncwarp();
+#pragma unroll
+        for (int t = 0; t < T8; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int lo = max(pos[t][h] - win + 1 - tok0, 0), hi = min(pos[t][h] - tok0, TT - 1);
+            if (hi >= lo && (bad & (~0ull << lo) & (~0ull >> (63 - hi))) != 0) l[t][h] = NAN;
+          }
+        return top();
       };
       quick_wait(bar_k, phase & 1, &sh_abort, &g_err_kv4attn, 47);
       float s[T8][MS][4];
       float f_tile = 0.f;
       if (any) {
-        const int top_k = top_scale(ks + kCodeBytes);
-        const int ref_k = max(top_k, 13);
+        const int ref_k = max(top_scale(ks + kCodeBytes), 13);
         const float fk = pow2i(140 - ref_k);
-        f_tile = top_k == 255 ? NAN : pow2w(ref_k - 140);
+        f_tile = pow2w(ref_k - 140);
         // ---- scores, transposed: 16 tokens x 8 rows
         // tokens of a group of 16: matrix row x is token x/2 (x even) or 4 + (x/2 ^ 1)
         // (x odd), plus 8 for x >= 8: reads of keys free of bank conflicts
@@ -475,8 +506,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
       if (any) {
         // ---- softmax over the tile
         const bool whole = tok0 + TT - 1 <= pos_min && tok0 > pos_max - win;
-        const int top_v = top_scale(vs + kCodeBytes);
-        const int new_v = max(ref_v, top_v);
+        const int new_v = max(ref_v, top_scale(vs + kCodeBytes));
         const float fv = ref_v == new_v ? 1.f : pow2i(ref_v - new_v);
         ref_v = new_v;
         uint32_t pb[T8][MS][2];
@@ -624,7 +654,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
         l[t][h] = x;
       }
     __syncthreads();
-    const float f_v = ref_v == 255 ? NAN : 1.f;
 #pragma unroll
     for (int t = 0; t < T8; ++t)
 #pragma unroll
@@ -634,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, ml[w][0][r]);
         // sums stand for value * 2^(ref_v - 127 - 13) * p 2^15
-        const float f = l[t][h] == 0.f ? 0.f : ex2(m[t][h] - mm) * f_v;
+        const float f = l[t][h] == 0.f ? 0.f : ex2(m[t][h] - mm);
         const float fa = pow2i((ref_v - 155) / 2), fb = pow2i(ref_v - 155 - (ref_v - 155) / 2);
         float* dst = merge + (warp * kRows + r) * kPitch + n * (D / 8);
         if constexpr (kTwin) {

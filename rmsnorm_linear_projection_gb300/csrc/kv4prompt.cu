@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       // sums stand for value * 2^(ref_v - 127 - 13), weights and sums both times 2^7
       const bool complete = run.n == run.all;
       const float inv = complete ? (l != 0.f ? 1.f / l : 0.f) : 1.f / 128.f;
-      const float fa = pow2i((ref_v - 140) / 2), fb = pow2i(ref_v - 140 - (ref_v - 140) / 2) * (ref_v == 255 ? NAN : 1.f);
+      const float fa = pow2i((ref_v - 140) / 2), fb = pow2i(ref_v - 140 - (ref_v - 140) / 2);
       const int64_t orow = static_cast<int64_t>(run.row0 + tok_q) * p.Hq + head;
       float* slot = p.part + static_cast<int64_t>(2 * cta + (nth > 0)) * C::kSlot;
       const int rg = i * 128 + rw;
@@ -709,6 +709,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
       for (int x = 0; x < kSB; ++x) t = max(t, (w >> (8 * x)) & 0xFFu);
       return t;
     };
+    // A token with a block that is not finite (scale byte 255), keys or values: its
+    // keys become NaN operands, so that exactly the rows that read it get a weight
+    // that is not a number; its values become zeros.
+    auto bad_bytes = [](uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & w & 0x80808080u; };
+    auto clean = [&](uint32_t w) { return w & ~((bad_bytes(w) >> 7) * 255u); };
     // Of the token's 16-byte runs of codes a warp's lanes take different ones at
     // a time (run c + tk/2), and their 8-dim chunks are permuted by the token's
     // number: reads and writes free of bank conflicts.
@@ -729,12 +734,18 @@ __global__ void __launch_bounds__(kPThreads, 1)
       auto scale_word = [&](uint32_t of) -> uint32_t {
         return live ? ld_shared<kSB>(of + tk * kSB) : 0u;  // else: whatever stands there gives zero operands
       };
-      const uint32_t word = scale_word(raw + C::kRawCodes);
+      uint32_t word = scale_word(raw + C::kRawCodes);
       // the tile's largest scales, over the four warps; the keys' warps look at
       // the values' too, for the softmax
-      const uint32_t own = __reduce_max_sync(0xffffffffu, top_of(word));
-      const uint32_t other =
-          values ? 0u : __reduce_max_sync(0xffffffffu, top_of(scale_word(raw + C::kRawCodes + C::kRawScales)));
+      const uint32_t own = __reduce_max_sync(0xffffffffu, top_of(clean(word)));
+      uint32_t other = 0;
+      if (values) {
+        word = clean(word);
+      } else {
+        const uint32_t word_v = scale_word(raw + C::kRawCodes + C::kRawScales);
+        other = __reduce_max_sync(0xffffffffu, top_of(clean(word_v)));
+        if ((bad_bytes(word) | bad_bytes(word_v)) != 0) word = 0xFFFFFFFFu;
+      }
       uint4 c[D / 32];
 #pragma unroll
       for (int x = 0; x < D / 32; ++x)
@@ -756,10 +767,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
       ref_v = max((info.w & 1) ? 13 : ref_v, top_v);
       const int ref = values ? ref_v : max(top, 13);
       if (tk == 0 && !values) {
-        ctrl.k_info[count & 3] = top == 255 ? NAN : pow2w(ref - 140);
+        ctrl.k_info[count & 3] = pow2w(ref - 140);
         ctrl.v_info[count & 3] = ref_v;
       }
-      const float fr = pow2i(140 - ref);
+      const float fr = word == 0xFFFFFFFFu ? NAN : pow2i(140 - ref);
       const uint32_t at = row_at + stage * kTileBytes;
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) {

@@ -434,3 +434,40 @@ def test_prompt_then_steps_through_the_projection():
         check_attention(q, c, t, lens, cu if step == 0 else None)
         rows = [1, 1]
         lens = [n + 1 for n in lens]
+
+
+@pytest.mark.parametrize("D,block", [(64, 64), (64, 32), (128, 32), (128, 64), (256, 32), (256, 64)])
+@pytest.mark.parametrize("rows,G", [(1, 4), (2, 4), (4, 4), (1, 1), (200, 2), (140, 8)])
+@pytest.mark.parametrize("window", [0, 90])
+def test_blocks_that_are_not_finite_reach_only_the_rows_that_read_them(D, block, rows, G, window):
+    """Keys and values that are not finite, in front of a window, among the rows'
+    own tokens (which earlier rows do not read) and in the history: a row that
+    reads one gets NaN and lse NaN, all others what they would get without it."""
+    g = gen(D + rows + window)
+    n, H = 450, 2
+    c, t = filled(g, [n, 70], H, 32, D, block)
+    lens, cu = [n, 70], [0, rows, rows + 1]
+    # (head, side, token); with a window also old tokens that no row, or only the first rows, read
+    marks = [(0, "k", n - 1), (0, "v", n - max(1, rows // 2)), (1, "v", n - 1)]
+    if window:
+        marks += [(0, "k", n - rows - window - 1), (0, "v", n - rows - window + 1), (1, "k", n - rows - window)]
+    elif rows == 200:
+        marks += [(1, "k", n - 130)]
+    clean = rnl.Kv4Cache(*(x.clone() for x in (c.k_codes, c.k_scales, c.v_codes, c.v_scales)))
+    pos = torch.arange(n - rows, n)
+    bad = torch.zeros(rows + 1, H, dtype=torch.bool)
+    for h, side, tok in marks:
+        page, off = int(t[0, tok // 32]), tok % 32
+        part = tok % (D // block)
+        getattr(c, side + "_scales")[page, h, off, part] = 255
+        getattr(clean, side + "_scales")[page, h, off, part] = 0
+        bad[:rows, h] |= (pos >= tok) & ((pos - tok < window) if window else True)
+    q = randn(g, rows + 1, G * H, D).bfloat16()
+    out, lse = torch.empty_like(q), torch.empty(rows + 1, G * H, device="cuda")
+    rnl.rnl_kv4_attention(q, c, t, i32(lens), i32(cu), out=out, lse_out=lse, window=window)
+    rnl.rnl_check_device_error()
+    o, z, tol, ltol = plain.attention(q, clean, t, i32(lens), i32(cu), window=window)
+    bad = bad.repeat_interleave(G, 1).cuda()
+    assert out[bad].isnan().all() and lse[bad].isnan().all()
+    assert ((out.double() - o).abs() <= tol)[~bad].all()
+    assert ((lse.double() - z).abs() <= ltol)[~bad].all()
