@@ -858,7 +858,7 @@ rnl_status launch_kv4_attention(const Kv4AttnArgs& x, const rnl_kv4_cache& c, co
   p.Hq = static_cast<int>(x.Hq);
   p.G = p.Hq / a.Hkv;
   p.causal = x.causal;
-  p.window = static_cast<int>(x.window);
+  p.window = x.window < (int64_t{1} << 30) ? static_cast<int>(x.window) : 0;  // lengths end at 2^30
   p.few = 0x7fffffff;
   bool after = false;
   if (q.cu_rows != nullptr && may_prompt(q.n_rows, p.G, a.D)) {

@@ -471,3 +471,40 @@ def test_blocks_that_are_not_finite_reach_only_the_rows_that_read_them(D, block,
     assert out[bad].isnan().all() and lse[bad].isnan().all()
     assert ((out.double() - o).abs() <= tol)[~bad].all()
     assert ((lse.double() - z).abs() <= ltol)[~bad].all()
+
+
+@pytest.mark.parametrize("rows", [1, 4, 150])
+def test_a_window_longer_than_any_sequence(rows):
+    g = gen(rows)
+    c, t = filled(g, [333], 2, 16, 128, 32)
+    q = randn(g, rows, 8, 128).bfloat16()
+    want = rnl.rnl_kv4_attention(q, c, t, i32([333]), i32([0, rows]))
+    for window in (333, 2 ** 30 - 1, 2 ** 30, 2 ** 31 - 1):
+        assert torch.equal(rnl.rnl_kv4_attention(q, c, t, i32([333]), i32([0, rows]), window=window), want)
+    # rows in front of the first token read nothing, whatever the window
+    out, _ = check_attention(q, c, t, [0], [0, rows], window=2 ** 31 - 1)
+    assert (out == 0).all()
+
+
+def test_calls_on_two_streams_at_once():
+    """Steps on one stream, a prompt on another, each with its own cache and
+    workspace: the bits of the calls alone."""
+    g = gen(77)
+    jobs = []
+    for lens, rows, D in (([5000] * 6, [1] * 6, 128), ([3000, 700], [900, 300], 128), ([2000] * 3, [4] * 3, 64)):
+        c, t = filled(g, lens, 2, 64, D, 32)
+        cu = [0]
+        for r in rows:
+            cu.append(cu[-1] + r)
+        args = (randn(g, cu[-1], 8, D).bfloat16(), c, t, i32(lens), i32(cu))
+        jobs.append((args, rnl.rnl_kv4_attention(*args), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for args, _, s in jobs:
+            with torch.cuda.stream(s):
+                got.append(rnl.rnl_kv4_attention(*args))
+    torch.cuda.synchronize()
+    rnl.rnl_check_device_error()
+    for i, out in enumerate(got):
+        assert torch.equal(out, jobs[i % len(jobs)][1])
