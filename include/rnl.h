@@ -263,7 +263,8 @@ typedef struct rnl_kv4_cache {
  * of r rows stands at position seq_lens[b] - r + i.  cu_rows = NULL: one row a
  * sequence (n_rows == n_seqs).  Rows from cu_rows[n_seqs] on belong to no
  * sequence: their outputs are left as they were (padded batches).
- *   block_table int32 [n_seqs, max_pages];  seq_lens int32 [n_seqs];
+ *   block_table int32 [n_seqs, max_pages] (max_pages * page_size and n_seqs at most
+ *   2^30, else RNL_ERR_SHAPE);  seq_lens int32 [n_seqs];
  *   cu_rows int32 [n_seqs + 1], not decreasing, from 0, or NULL
  * These are device arrays and are checked on the device: a sequence whose
  * rows or length are out of range (length above max_pages * page_size, rows
@@ -319,10 +320,11 @@ rnl_status rnl_kv4_gather(const rnl_kv4_cache *cache, const rnl_kv4_seqs *seqs, 
  * tokens that a row does not read, has no effect on it; a row that reads a
  * token with a scale byte of 255, in its keys or its values, gets NaN, and lse
  * NaN.  Softmax statistics and sums in FP32; products of binary16 operands that
- * hold the cache's values and q (scaled by powers of two) exactly down to 2^-37
- * of the largest near them (a scale byte of 0, 2^-127, counts as zero); the
- * softmax weights are rounded to binary16: 11 bits, for weights of at least
- * 2^-21 of the row's largest, fewer below.
+ * hold the cache's values and q, scaled by powers of two, exactly: values down
+ * to 2^-37 of the largest near them (a scale byte of 0, 2^-127, counts as zero),
+ * elements of q down to 2^-31 of the row's largest.  The softmax weights are
+ * rounded to binary16: 11 bits, for weights of at least 2^-21 of the row's
+ * largest, fewer below.
  * Workspace: rnl_workspace_size(RNL_OP_KV4_ATTENTION, n_rows, head_dim,
  * n_q_heads, n_kv_heads) bytes; results do not depend on its contents.  Calls
  * that may run at the same time (other streams, other graphs) need one each.

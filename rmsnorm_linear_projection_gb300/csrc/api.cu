@@ -251,7 +251,7 @@ S8Layout s8_layout(void* ws, int64_t M, int64_t K, int64_t N) {
 rnl_status check_kv4(const rnl_kv4_cache* c, const rnl_kv4_seqs* q) {
   if (!c || !q) return RNL_ERR_NULL;
   if (bad_dim(c->n_pages) || c->n_pages == 0 || bad_dim(c->n_kv_heads) || c->n_kv_heads == 0 ||
-      c->n_kv_heads > 65535 || bad_dim(q->n_seqs) || bad_dim(q->max_pages) || bad_dim(q->n_rows))
+      c->n_kv_heads > 65535 || bad_dim(q->n_seqs) || q->n_seqs > (int64_t{1} << 30) || bad_dim(q->max_pages) || bad_dim(q->n_rows))
     return RNL_ERR_SHAPE;
   if (!qkv_rope_head_dim_ok(c->head_dim)) return RNL_ERR_UNSUPPORTED;
   if (!mx_block_ok(c->block)) return RNL_ERR_ARG;

@@ -828,7 +828,16 @@ rnl_status launch_split(const AttnParams& p, const Args& a, const DeviceInfo& de
 }  // namespace
 
 namespace {
-constexpr int kFewRows = 32;  // rows of a sequence (times G) up to which this file's kernel takes it
+// Rows of a sequence (times G) up to which this file's kernel takes it.  It reads
+// the cache once per 16 rows, the prompt kernel once per 256, but that takes
+// 30 us longer to start: 8, 16 and 32 rows (G = 4) of 32 sequences of 2000 to
+// 9000 tokens 154, 281 and 531 us here, 168, 175 and 179 us there.
+constexpr int kFewRows = 32;
+// Rows times key heads times tokens (as many as the tables can hold) up to which
+// the prompt kernel is not launched at all: 16 rows of 2 sequences of up to 9000
+// tokens (9.2 million) 37 us here, 60 us there; 32 rows over 12000 (12.3 million)
+// 58 and 68; 32 rows of 2 sequences of 6000 (12.3 million) 64 and 56.
+constexpr int64_t kFewWork = 12000000;
 size_t few_workspace_bytes(int64_t D) {
   const size_t slot = static_cast<size_t>(16) * (static_cast<size_t>(D) + 2) * 4;  // NT = 2
   return (kMaxCtas * (sizeof(int4) + 2 * slot) + 255) / 256 * 256;
@@ -861,7 +870,8 @@ rnl_status launch_kv4_attention(const Kv4AttnArgs& x, const rnl_kv4_cache& c, co
   p.window = x.window < (int64_t{1} << 30) ? static_cast<int>(x.window) : 0;  // lengths end at 2^30
   p.few = 0x7fffffff;
   bool after = false;
-  if (q.cu_rows != nullptr && may_prompt(q.n_rows, p.G, a.D)) {
+  const int64_t tokens = c.n_kv_heads * (q.max_pages * c.page_size);  // below 2^46
+  if (q.cu_rows != nullptr && may_prompt(q.n_rows, p.G, a.D) && q.n_rows * p.G > kFewWork / std::max<int64_t>(tokens, 1)) {
     p.few = kFewRows;
     const rnl_status pst = launch_kv4_prompt(p, a, static_cast<int>(c.block),
                                              static_cast<char*>(x.ws) + few_workspace_bytes(a.D), dev, s);

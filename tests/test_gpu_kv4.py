@@ -75,13 +75,29 @@ def filled(g, lens, H, page, D, block, spread=0.0, chan=0.5):
     return c, t
 
 
+def wide(t, page):
+    """The tables with room for 2^19 tokens more: with many rows the call then expects
+    enough work for the prompt kernel, which small tables keep from it."""
+    more = torch.full((t.shape[0], 2 ** 19 // page), -9, dtype=torch.int32, device="cuda")
+    return torch.cat([t, more], 1)
+
+
 def check_attention(q, c, t, lens, cu=None, **kw):
+    """Both kernels where many rows allow both; the narrow tables' outputs."""
+    ref = plain.attention(q, c, t, i32(lens), None if cu is None else i32(cu), **kw)
+    many = cu is not None and q.shape[0] * q.shape[1] // c.n_kv_heads > 32 and c.head_dim < 256
+    if many:
+        check_outputs(ref, q, c, wide(t, c.page_size), lens, cu, **kw)
+    return check_outputs(ref, q, c, t, lens, cu, **kw)
+
+
+def check_outputs(ref, q, c, t, lens, cu, **kw):
     T, Hq, D = q.shape
     lse = torch.full((T, Hq), 123.0, device="cuda")
     out = torch.full((T, Hq, D), 320.0, dtype=torch.bfloat16, device="cuda")
     rnl.rnl_kv4_attention(q, c, t, i32(lens), None if cu is None else i32(cu), out=out, lse_out=lse, **kw)
     rnl.rnl_check_device_error()
-    o, z, tol, ltol = plain.attention(q, c, t, i32(lens), None if cu is None else i32(cu), **kw)
+    o, z, tol, ltol = ref
     own = ~torch.isnan(z)
     assert (out[~own] == 320.0).all() and (lse[~own] == 123.0).all(), "rows of no sequence were written"
     off = (out.double() - o).abs()[own]
@@ -463,20 +479,22 @@ def test_blocks_that_are_not_finite_reach_only_the_rows_that_read_them(D, block,
         getattr(clean, side + "_scales")[page, h, off, part] = 0
         bad[:rows, h] |= (pos >= tok) & ((pos - tok < window) if window else True)
     q = randn(g, rows + 1, G * H, D).bfloat16()
-    out, lse = torch.empty_like(q), torch.empty(rows + 1, G * H, device="cuda")
-    rnl.rnl_kv4_attention(q, c, t, i32(lens), i32(cu), out=out, lse_out=lse, window=window)
-    rnl.rnl_check_device_error()
     o, z, tol, ltol = plain.attention(q, clean, t, i32(lens), i32(cu), window=window)
     bad = bad.repeat_interleave(G, 1).cuda()
-    assert out[bad].isnan().all() and lse[bad].isnan().all()
-    assert ((out.double() - o).abs() <= tol)[~bad].all()
-    assert ((lse.double() - z).abs() <= ltol)[~bad].all()
+    for tt in (t, wide(t, 32)):
+        out, lse = torch.empty_like(q), torch.empty(rows + 1, G * H, device="cuda")
+        rnl.rnl_kv4_attention(q, c, tt, i32(lens), i32(cu), out=out, lse_out=lse, window=window)
+        rnl.rnl_check_device_error()
+        assert out[bad].isnan().all() and lse[bad].isnan().all()
+        assert ((out.double() - o).abs() <= tol)[~bad].all()
+        assert ((lse.double() - z).abs() <= ltol)[~bad].all()
 
 
 @pytest.mark.parametrize("rows", [1, 4, 150])
 def test_a_window_longer_than_any_sequence(rows):
     g = gen(rows)
     c, t = filled(g, [333], 2, 16, 128, 32)
+    t = wide(t, 16)
     q = randn(g, rows, 8, 128).bfloat16()
     want = rnl.rnl_kv4_attention(q, c, t, i32([333]), i32([0, rows]))
     for window in (333, 2 ** 30 - 1, 2 ** 30, 2 ** 31 - 1):
@@ -508,3 +526,67 @@ def test_calls_on_two_streams_at_once():
     rnl.rnl_check_device_error()
     for i, out in enumerate(got):
         assert torch.equal(out, jobs[i % len(jobs)][1])
+
+
+def test_bad_sequences_with_many_rows():
+    """Page ids outside the cache, lengths and rows out of range, in the prompt
+    kernel: reported, and the sequences beside them right."""
+    g = gen(6)
+    n, rows, page = 300, 90, 32
+    c, t = filled(g, [n, n], 2, page, 128, 32)
+    t = wide(t, page)
+    q = randn(g, 2 * rows, 8, 128).bfloat16()
+    bad_page, minus = t.clone(), t.clone()
+    bad_page[0, 3], minus[0, 9] = c.n_pages, -1
+    cu = i32([0, rows, 2 * rows])
+    want = rnl.rnl_kv4_attention(q, c, t, i32([n, n]), cu)
+    for tt, lens, rr in ((bad_page, i32([n, n]), cu), (minus, i32([n, n]), cu), (t, i32([-5, n]), cu),
+                         (t, i32([2 ** 31 - 1, n]), cu), (t, i32([n, n]), i32([rows + 7, rows, 2 * rows]))):
+        out = torch.full_like(q, 320.0)
+        rnl.rnl_kv4_attention(q, c, tt, lens, rr, out=out)
+        with pytest.raises(rnl.RnlError, match="RNL_ERR_ARG"):
+            rnl.rnl_check_device_error()
+        # (two bf16 roundings of sums whose weights differ by their own rounding)
+        assert ((out[rows:].double() - want[rows:].double()).abs() <= 2.0 ** -7 * want[rows:].double().abs() + 1e-3).all()
+        if tt is t:
+            assert (out[:rows] == 320.0).all()
+    rnl.rnl_check_device_error()
+
+
+def test_captured_prompts_follow_their_inputs():
+    """A captured call of many rows, replayed over other lengths, row counts and
+    queries in the same buffers, with a workspace full of what was there before."""
+    g = gen(14)
+    T, Hq, Hkv, D, page = 400, 8, 2, 128, 64
+    c, t = filled(g, [900, 640, 333], Hkv, page, D, 32)
+    t = wide(t, page)
+    q = randn(g, T, Hq, D).bfloat16()
+    lens, cu = i32([900, 640, 333]), i32([0, 200, 380, 400])
+    size = rnl.workspace_size(rnl.OP_KV4_ATTENTION, T, D, Hq, Hkv)
+    ws = torch.randint(0, 256, (size,), device="cuda").to(torch.uint8)
+    out, lse = torch.empty_like(q), torch.empty(T, Hq, device="cuda")
+
+    def call():
+        rnl.rnl_kv4_attention(q, c, t, lens, cu, out=out, lse_out=lse, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+        side.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=side):
+            call()
+    torch.cuda.synchronize()
+    for i, (now, rows) in enumerate((([900, 640, 333], [0, 200, 380, 400]), ([300, 2, 1], [0, 300, 301, 302]),
+                                     ([0, 640, 333], [0, 5, 10, 300]), ([900, 600, 330], [0, 0, 399, 400]))):
+        lens.copy_(i32(now))
+        cu.copy_(i32(rows))
+        q.copy_(randn(gen(200 + i), *q.shape).bfloat16())
+        out.fill_(320.0)
+        gr.replay()
+        torch.cuda.synchronize()
+        rnl.rnl_check_device_error()
+        n = rows[-1]
+        want, _ = check_outputs(plain.attention(q, c, t, lens, cu), q, c, t, now, rows)
+        assert torch.equal(out[:n], want[:n]) and (out[n:] == 320.0).all()

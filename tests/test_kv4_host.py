@@ -63,7 +63,7 @@ CHILD = textwrap.dedent("""
         no_pages=(dict(P=0), {{}}), neg_heads=(dict(H=-1), {{}}), many_heads=(dict(H=1 << 17), {{}}),
         head_dim_80=(dict(D=80), {{}}), block_16=(dict(block=16), {{}}), page_24=(dict(S=24), {{}}),
         page_8=(dict(S=8), {{}}), page_2048=(dict(S=2048), {{}}), long_table=({{}}, dict(M=1 << 27)),
-        neg_seqs=({{}}, dict(B=-1)), rows_are_not_sequences=({{}}, dict(cu=None)), huge_rows=({{}}, dict(T=1 << 40)),
+        neg_seqs=({{}}, dict(B=-1)), many_seqs=({{}}, dict(B=(1 << 30) + 1)), rows_are_not_sequences=({{}}, dict(cu=None)), huge_rows=({{}}, dict(T=1 << 40)),
         null_codes=(dict(vc=None), {{}}), null_scales=(dict(ks=None), {{}}), null_lens=({{}}, dict(n=None)),
         null_table=({{}}, dict(t=None)), misaligned_codes=(dict(kc=B), {{}}), misaligned_scales=(dict(vs=B), {{}}),
         misaligned_table=({{}}, dict(t=C)), misaligned_lens=({{}}, dict(n=C)), misaligned_rows=({{}}, dict(cu=C)))
@@ -150,7 +150,7 @@ for _call in ("append", "gather", "attention"):
     WANT.update({f"{_call}_{_k}": _v for _k, _v in {
         "no_device": DEVICE, "one_row_each": DEVICE, "no_rows": OK, "no_pages": SHAPE, "neg_heads": SHAPE,
         "many_heads": SHAPE, "head_dim_80": UNSUPPORTED, "block_16": ARG, "page_24": UNSUPPORTED,
-        "page_8": UNSUPPORTED, "page_2048": UNSUPPORTED, "long_table": SHAPE, "neg_seqs": SHAPE,
+        "page_8": UNSUPPORTED, "page_2048": UNSUPPORTED, "long_table": SHAPE, "neg_seqs": SHAPE, "many_seqs": SHAPE,
         "rows_are_not_sequences": SHAPE, "huge_rows": SHAPE, "null_codes": NULL, "null_scales": NULL,
         "null_lens": NULL, "null_table": NULL, "misaligned_codes": ALIGN, "misaligned_scales": ALIGN,
         "misaligned_table": ALIGN, "misaligned_lens": ALIGN, "misaligned_rows": ALIGN, "null_cache": NULL,
