@@ -14,7 +14,10 @@
 // codes and scales).  One warp takes 1024 elements of one row, of k and of v:
 // every lane moves 8 elements (16 bytes of bf16, 4 bytes of codes) an access,
 // eight accesses on their way at once, and the sequence is looked up once for
-// both sides; the writer's loads do not wait for it.
+// both sides; the writer's loads do not wait for it.  Measured at a captured
+// call, cold: prefixes of 9000 to 20000 tokens read back at 5.4 TB/s (10 of
+// them: 6.35), prompts written and read back at 3.7 TB/s (20 of them: 4.95);
+// 512 elements a warp were slower (50 against 43 us for either).
 #include "kv4.cuh"
 
 namespace rnl {

@@ -17,6 +17,9 @@
 // pairs share an axis, 16 loads otherwise.  The sums of squares are added in
 // the order of qkvrope.cu's kernel (its lane's R = D / 64 elements of either
 // half, then a tree over its 32 lanes), so that one axis gives the same bits.
+// Measured: 18433 tokens of 48 heads of 64 without norm 47 us (4.8 TB/s; 70000
+// tokens 5.6); 4096 tokens of 48 heads of 128 with norm 33 us, where the norm's
+// instructions count (32768 tokens: 4.5 TB/s, without norm 5.5).
 #include <cuda_bf16.h>
 
 #include "internal.h"
