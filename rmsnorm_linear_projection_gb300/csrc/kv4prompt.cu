@@ -64,8 +64,10 @@ constexpr int kPThreads = kPWarps * 32;
 // registers a thread after the roles part, within what the block is launched with
 constexpr int kLaunchRegs = 96, kSoftRegs = 136, kFillRegs = 64, kMmaRegs = 72;
 static_assert(8 * kSoftRegs + 8 * kFillRegs + 4 * kMmaRegs <= kPWarps * kLaunchRegs, "register file");
-// what a group costs beside its tiles (queries, output), in tiles
-constexpr int kGroupCost = 3;
+// What a group costs beside its tiles (queries, output), in tiles.  12 prompts of
+// 300 to 1500 rows: 330 us, with 3 tiles 338, 5 345, 7 359; 6 of 100 to 800 rows
+// over 1000 to 9000 tokens, D = 64: 125 us, with 3 tiles 136, 5 121.
+constexpr int kGroupCost = 4;
 constexpr int kMaxPromptCtas = 160;
 constexpr float kTop = 7.f;        // weights are scaled by 2^7: room for 2^9 above the maximum in use
 
