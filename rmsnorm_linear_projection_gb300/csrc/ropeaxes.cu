@@ -17,9 +17,9 @@
 // pairs share an axis, 16 loads otherwise.  The sums of squares are added in
 // the order of qkvrope.cu's kernel (its lane's R = D / 64 elements of either
 // half, then a tree over its 32 lanes), so that one axis gives the same bits.
-// Measured: 18433 tokens of 48 heads of 64 without norm 47 us (4.8 TB/s; 70000
-// tokens 5.6); 4096 tokens of 48 heads of 128 with norm 33 us, where the norm's
-// instructions count (32768 tokens: 4.5 TB/s, without norm 5.5).
+// Measured: 18433 tokens of 48 heads of 64 without norm 43 us (5.2 TB/s); 4096
+// tokens of 48 heads of 128 with norm 31 us, where loads wait for the norm's
+// arithmetic (32768 tokens: 4.5 TB/s, without norm 5.5).
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -31,6 +31,7 @@ namespace {
 __device__ unsigned int g_err_axes;  // kErrArg | site: a position outside [0, P)
 
 constexpr int kWarps = 4;
+constexpr int kMinCtas = 5;  // by registers (102); 4 for head_dim 64 without it, 47 against 43 us at 18433 tokens
 constexpr int kGroups = 4;  // head groups a warp has in flight
 
 struct AxisMap {
@@ -57,7 +58,7 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 __device__ __forceinline__ float bf16_round(float v) { return __bfloat162float(__float2bfloat16_rn(v)); }
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, kMinCtas)
     qkv_rope_axes_kernel(const __nv_bfloat16* __restrict__ y, int64_t T, int Hq, int Hkv, int parts, int per,
                          const __nv_bfloat16* __restrict__ q_gamma, const __nv_bfloat16* __restrict__ k_gamma,
                          float eps, const int* __restrict__ pos, const float* __restrict__ cs, int P,
