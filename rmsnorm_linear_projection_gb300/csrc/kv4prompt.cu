@@ -34,7 +34,7 @@
 // a dependent kernel.
 //
 // Measured (two prompts of 1000 to 2048 rows over 6000 to 10240 tokens, G = 4,
-// D = 128): 367 us, 1028 TFLOP/s, tensor pipe 48 % active; a tile takes 1.87 us
+// D = 128): 369 to 373 us, 1011 to 1022 TFLOP/s, tensor pipe 47 % active; a tile takes 1.87 us
 // where the products alone would take 1.1.  What bounds it is the softmax (a
 // thread a row: exponentials, conversions, TMEM reads) beside 8 to 10 us a run.
 #include <algorithm>
