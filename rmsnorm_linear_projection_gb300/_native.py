@@ -6,6 +6,10 @@ passes none, and the raw pointers plus the current CUDA stream are handed to
 the C entry point of the same name.  Every step of the computation runs in
 the library's CUDA kernels; there is no other code path.  If the library
 has not been built, every call raises.
+
+stream=s enqueues a call on s as if it were made under torch.cuda.stream(s):
+what it allocates belongs to s, and the caller orders s against the streams
+that write its inputs and read its outputs.
 """
 from __future__ import annotations
 
@@ -191,10 +195,28 @@ def workspace_size(op: int, T: int, K: int, N: int, N2: int = 0) -> int:
     return int(v)
 
 
-def _workspace(nbytes, device, given):
+def _new(shape, dtype, device, stream, returned=True):
+    """A tensor that a call on `stream` (None: the current one) writes.  It comes
+    from that stream's memory: a block of the current stream's pool would be
+    given out again when the call returns (a workspace), or may still be in
+    use by earlier work there (an output), with nothing that orders the kernels
+    on `stream` against either.  What is returned is also recorded on the
+    current stream, where the caller may go on with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned and t.is_cuda:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _workspace(nbytes, device, given, stream):
     if given is not None:
         return given
-    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    return _new((max(nbytes, 1),), torch.uint8, device, stream, returned=False)
 
 
 def rmsnorm_linear_bf16(x, gamma, W, eps=1e-6, norm_mode=NORM_RSQRT, out=None,
@@ -209,9 +231,9 @@ def rmsnorm_linear_bf16(x, gamma, W, eps=1e-6, norm_mode=NORM_RSQRT, out=None,
         _need(gamma, "gamma", torch.bfloat16, (K,), dev)
     odt = torch.bfloat16 if out_dtype == OUT_BF16 else torch.float32
     if out is None:
-        out = torch.empty((T, N), dtype=odt, device=dev)
+        out = _new((T, N), odt, dev, stream)
     _need(out, "out", odt, (T, N), dev)
-    ws = _workspace(workspace_size(OP_BF16, T, K, N, out_dtype), dev, workspace)
+    ws = _workspace(workspace_size(OP_BF16, T, K, N, out_dtype), dev, workspace, stream)
     _check(load().rmsnorm_linear_bf16(_ptr(x), _ptr(gamma), _ptr(W), T, K, N, float(eps),
                                       int(norm_mode), _ptr(out), int(out_dtype), _ptr(ws),
                                       ws.numel() * ws.element_size(), _stream(dev, stream)),
@@ -237,9 +259,9 @@ def rmsnorm_linear_bf16_ex(x, gamma, W, residual=None, x_sum_out=None, beta=None
     if rstd_out is not None:
         _need(rstd_out, "rstd_out", torch.float32, (T,), dev)
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+        out = _new((T, N), torch.bfloat16, dev, stream)
     _need(out, "out", torch.bfloat16, (T, N), dev)
-    ws = _workspace(workspace_size(OP_BF16, T, K, N, OUT_BF16), dev, workspace)
+    ws = _workspace(workspace_size(OP_BF16, T, K, N, OUT_BF16), dev, workspace, stream)
     _check(load().rmsnorm_linear_bf16_ex(_ptr(x), _ptr(residual), _ptr(x_sum_out), _ptr(gamma),
                                          _ptr(beta), _ptr(W), _ptr(bias), T, K, N, float(eps),
                                          int(norm_mode), _ptr(out), _ptr(rstd_out), _ptr(ws),
@@ -248,10 +270,10 @@ def rmsnorm_linear_bf16_ex(x, gamma, W, residual=None, x_sum_out=None, beta=None
     return out
 
 
-def _qkv_outputs(T, Hq, Hkv, D, dev, q_out, k_out, v_out):
-    q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev) if q_out is None else q_out
-    k_out = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=dev) if k_out is None else k_out
-    v_out = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=dev) if v_out is None else v_out
+def _qkv_outputs(T, Hq, Hkv, D, dev, q_out, k_out, v_out, stream):
+    q_out = _new((T, Hq, D), torch.bfloat16, dev, stream) if q_out is None else q_out
+    k_out = _new((T, Hkv, D), torch.bfloat16, dev, stream) if k_out is None else k_out
+    v_out = _new((T, Hkv, D), torch.bfloat16, dev, stream) if v_out is None else v_out
     _need(q_out, "q_out", torch.bfloat16, (T, Hq, D), dev)
     _need(k_out, "k_out", torch.bfloat16, (T, Hkv, D), dev)
     _need(v_out, "v_out", torch.bfloat16, (T, Hkv, D), dev)
@@ -271,7 +293,7 @@ def rnl_qkv_rope(y, n_q_heads, n_kv_heads, head_dim, q_gamma, k_gamma, positions
     _need(positions, "positions", torch.int32, (T,), dev)
     P = cos_sin.shape[0]
     _need(cos_sin, "cos_sin", torch.float32, (P, D), dev)
-    q_out, k_out, v_out = _qkv_outputs(T, Hq, Hkv, D, dev, q_out, k_out, v_out)
+    q_out, k_out, v_out = _qkv_outputs(T, Hq, Hkv, D, dev, q_out, k_out, v_out, stream)
     _check(load().rnl_qkv_rope(_ptr(y), T, Hq, Hkv, D, _ptr(q_gamma), _ptr(k_gamma), float(eps),
                                _ptr(positions), _ptr(cos_sin), P, _ptr(q_out), _ptr(k_out),
                                _ptr(v_out), _stream(dev, stream)), "rnl_qkv_rope")
@@ -298,7 +320,7 @@ def rnl_qkv_rope_axes(y, n_q_heads, n_kv_heads, head_dim, q_gamma, k_gamma, posi
     axes = bytes(axis_of_pair)
     P = cos_sin.shape[0]
     _need(cos_sin, "cos_sin", torch.float32, (P, D), dev)
-    q_out, k_out, v_out = _qkv_outputs(T, Hq, Hkv, D, dev, q_out, k_out, v_out)
+    q_out, k_out, v_out = _qkv_outputs(T, Hq, Hkv, D, dev, q_out, k_out, v_out, stream)
     _check(load().rnl_qkv_rope_axes(_ptr(y), T, Hq, Hkv, D, _ptr(q_gamma), _ptr(k_gamma), float(eps),
                                     _ptr(positions), A, axes, _ptr(cos_sin), P, _ptr(q_out), _ptr(k_out),
                                     _ptr(v_out), _stream(dev, stream)), "rnl_qkv_rope_axes")
@@ -361,10 +383,10 @@ def _need_rows(t, name, shape, device):
     return row if T > 1 else H * D
 
 
-def _out(t, name, dtype, shape, device):
+def _out(t, name, dtype, shape, device, stream):
     """An output: the caller's, checked, or a new tensor."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _new(shape, dtype, device, stream)
     _need(t, name, dtype, shape, device)
     return t
 
@@ -388,8 +410,8 @@ def rnl_kv4_gather(cache, block_table, seq_lens, n_rows, cu_rows=None, k_out=Non
     dev = cache.device
     shape = (n_rows, cache.n_kv_heads, cache.head_dim)
     seqs = _kv4_seqs(cache, block_table, seq_lens, cu_rows, n_rows)
-    k_out = _out(k_out, "k_out", torch.bfloat16, shape, dev)
-    v_out = _out(v_out, "v_out", torch.bfloat16, shape, dev)
+    k_out = _out(k_out, "k_out", torch.bfloat16, shape, dev, stream)
+    v_out = _out(v_out, "v_out", torch.bfloat16, shape, dev, stream)
     _check(load().rnl_kv4_gather(cache._c(), seqs, _ptr(k_out), _ptr(v_out), _stream(dev, stream)),
            "rnl_kv4_gather")
     return k_out, v_out
@@ -406,8 +428,8 @@ def rnl_kv4_attention(q, cache, block_table, seq_lens, cu_rows=None, scale=None,
     seqs = _kv4_seqs(cache, block_table, seq_lens, cu_rows, T)
     if lse_out is not None:
         _need(lse_out, "lse_out", torch.float32, (T, Hq), dev)
-    out = _out(out, "out", torch.bfloat16, (T, Hq, D), dev)
-    ws = _workspace(workspace_size(OP_KV4_ATTENTION, T, D, Hq, cache.n_kv_heads), dev, workspace)
+    out = _out(out, "out", torch.bfloat16, (T, Hq, D), dev, stream)
+    ws = _workspace(workspace_size(OP_KV4_ATTENTION, T, D, Hq, cache.n_kv_heads), dev, workspace, stream)
     _check(load().rnl_kv4_attention(_ptr(q), qs, Hq, cache._c(), seqs,
                                     float(D ** -0.5 if scale is None else scale), int(bool(causal)), int(window),
                                     _ptr(out), _ptr(lse_out), _ptr(ws), ws.numel() * ws.element_size(),
@@ -433,8 +455,8 @@ def rmsnorm_linear_qkv_rope(x, gamma, W, n_q_heads, n_kv_heads, head_dim, q_gamm
     _need(positions, "positions", torch.int32, (T,), dev)
     P = cos_sin.shape[0]
     _need(cos_sin, "cos_sin", torch.float32, (P, D), dev)
-    q_out, k_out, v_out = _qkv_outputs(T, Hq, Hkv, D, dev, q_out, k_out, v_out)
-    ws = _workspace(workspace_size(OP_QKV_ROPE, T, K, N), dev, workspace)
+    q_out, k_out, v_out = _qkv_outputs(T, Hq, Hkv, D, dev, q_out, k_out, v_out, stream)
+    ws = _workspace(workspace_size(OP_QKV_ROPE, T, K, N), dev, workspace, stream)
     _check(load().rmsnorm_linear_qkv_rope(_ptr(x), _ptr(gamma), _ptr(W), T, K, Hq, Hkv, D,
                                           float(eps), int(norm_mode), _ptr(q_gamma), _ptr(k_gamma),
                                           float(head_eps), _ptr(positions), _ptr(cos_sin), P,
@@ -456,9 +478,9 @@ def quant_matmul_reduce_sum(x1, x2, x1_scale, x2_scale, out=None, workspace=None
     _need(x1_scale, "x1_scale", torch.float32, (B, M), dev)
     _need(x2_scale, "x2_scale", torch.bfloat16, (N,), dev)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        out = _new((M, N), torch.bfloat16, dev, stream)
     _need(out, "out", torch.bfloat16, (M, N), dev)
-    ws = _workspace(workspace_size(OP_QMRS, M, K, N, B), dev, workspace)
+    ws = _workspace(workspace_size(OP_QMRS, M, K, N, B), dev, workspace, stream)
     _check(load().quant_matmul_reduce_sum(_ptr(x1), _ptr(x2), _ptr(x1_scale), _ptr(x2_scale), B, M, K, N,
                                           _ptr(out), _ptr(ws), ws.numel() * ws.element_size(),
                                           _stream(dev, stream)),
@@ -478,13 +500,13 @@ def rmsnorm_linear_w8a8(x, gamma, Wq, w_scale, eps=1e-6, norm_mode=NORM_RSQRT, o
     if gamma is not None:
         _need(gamma, "gamma", torch.bfloat16, (K,), dev)
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+        out = _new((T, N), torch.bfloat16, dev, stream)
     _need(out, "out", torch.bfloat16, (T, N), dev)
     if q_out is not None:
         _need(q_out, "q_out", torch.int8, (T, K), dev)
     if x_scale_out is not None:
         _need(x_scale_out, "x_scale_out", torch.float32, (T,), dev)
-    ws = _workspace(workspace_size(OP_W8A8, T, K, N), dev, workspace)
+    ws = _workspace(workspace_size(OP_W8A8, T, K, N), dev, workspace, stream)
     _check(load().rmsnorm_linear_w8a8(_ptr(x), _ptr(gamma), _ptr(Wq), _ptr(w_scale), T, K, N,
                                       float(eps), int(norm_mode), _ptr(out), _ptr(q_out),
                                       _ptr(x_scale_out), _ptr(ws), ws.numel() * ws.element_size(),
@@ -500,7 +522,7 @@ def rnl_w8a8_prepare_weight(Wq, out=None, stream=None):
     dev = Wq.device
     _need(Wq, "Wq", torch.int8, (N, K), dev)
     if out is None:
-        out = torch.empty((N, K), dtype=torch.bfloat16, device=dev)
+        out = _new((N, K), torch.bfloat16, dev, stream)
     _need(out, "Wb", torch.bfloat16, (N, K), dev)
     _check(load().rnl_w8a8_prepare_weight(_ptr(Wq), N, K, _ptr(out), _stream(dev, stream)),
            "rnl_w8a8_prepare_weight")
@@ -519,13 +541,13 @@ def rmsnorm_linear_w8a8_prepared(x, gamma, Wb, w_scale, eps=1e-6, norm_mode=NORM
     if gamma is not None:
         _need(gamma, "gamma", torch.bfloat16, (K,), dev)
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+        out = _new((T, N), torch.bfloat16, dev, stream)
     _need(out, "out", torch.bfloat16, (T, N), dev)
     if q_out is not None:
         _need(q_out, "q_out", torch.int8, (T, K), dev)
     if x_scale_out is not None:
         _need(x_scale_out, "x_scale_out", torch.float32, (T,), dev)
-    ws = _workspace(workspace_size(OP_W8A8_PREPARED, T, K, N), dev, workspace)
+    ws = _workspace(workspace_size(OP_W8A8_PREPARED, T, K, N), dev, workspace, stream)
     _check(load().rmsnorm_linear_w8a8_prepared(_ptr(x), _ptr(gamma), _ptr(Wb), _ptr(w_scale), T, K, N,
                                                float(eps), int(norm_mode), _ptr(out), _ptr(q_out),
                                                _ptr(x_scale_out), _ptr(ws), ws.numel() * ws.element_size(),
@@ -550,13 +572,13 @@ def rmsnorm_linear_mxfp8(x, gamma, w_codes, w_scale, eps=1e-6, norm_mode=NORM_RS
         _need(gamma, "gamma", torch.bfloat16, (K,), dev)
     odt = torch.bfloat16 if out_dtype == OUT_BF16 else torch.float32
     if out is None:
-        out = torch.empty((T, N), dtype=odt, device=dev)
+        out = _new((T, N), odt, dev, stream)
     _need(out, "out", odt, (T, N), dev)
     if x_codes_out is not None:
         _need(x_codes_out, "x_codes_out", torch.uint8, (T, K), dev)
     if x_scale_out is not None:
         _need(x_scale_out, "x_scale_out", torch.uint8, (T, nb), dev)
-    ws = _workspace(workspace_size(OP_MXFP8, T, K, N), dev, workspace)
+    ws = _workspace(workspace_size(OP_MXFP8, T, K, N), dev, workspace, stream)
     _check(load().rmsnorm_linear_mxfp8(_ptr(x), _ptr(gamma), _ptr(w_codes), _ptr(w_scale), T, K, N,
                                        float(eps), int(norm_mode), int(block), _ptr(out), int(out_dtype),
                                        _ptr(x_codes_out), _ptr(x_scale_out), _ptr(ws),
@@ -578,9 +600,9 @@ def mxfp8_scaled_mm(x_codes, x_scale, w_codes, w_scale, block=64, out=None, out_
     _need(w_scale, "w_scale", torch.uint8, (N, nb), dev)
     odt = torch.bfloat16 if out_dtype == OUT_BF16 else torch.float32
     if out is None:
-        out = torch.empty((T, N), dtype=odt, device=dev)
+        out = _new((T, N), odt, dev, stream)
     _need(out, "out", odt, (T, N), dev)
-    ws = _workspace(workspace_size(OP_MXFP8, T, K, N), dev, workspace)
+    ws = _workspace(workspace_size(OP_MXFP8, T, K, N), dev, workspace, stream)
     _check(load().mxfp8_scaled_mm(_ptr(x_codes), _ptr(x_scale), _ptr(w_codes), _ptr(w_scale), T, K, N,
                                   int(block), _ptr(out), int(out_dtype), _ptr(ws),
                                   ws.numel() * ws.element_size(), _stream(dev, stream)),
@@ -597,7 +619,7 @@ def rnl_head_rmsnorm(y, n_heads, head_dim, gamma=None, eps=1e-6, norm_mode=NORM_
     if gamma is not None:
         _need(gamma, "gamma", torch.bfloat16, (head_dim,), dev)
     if out is None:
-        out = torch.empty_like(y)
+        out = _new(y.shape, y.dtype, dev, stream)
     _need(out, "out", torch.bfloat16, (T, n_heads * head_dim), dev)
     _check(load().rnl_head_rmsnorm(_ptr(y), T, n_heads, head_dim, _ptr(gamma), float(eps), int(norm_mode),
                                    _ptr(out), _stream(dev, stream)),
@@ -619,11 +641,11 @@ def mla_q_chain_head_norm(x, W_qa, gamma_cq, W_qb, head_dim, head_gamma=None, ep
     if head_gamma is not None:
         _need(head_gamma, "head_gamma", torch.bfloat16, (head_dim,), dev)
     if out is None:
-        out = torch.empty((T, N2), dtype=torch.bfloat16, device=dev)
+        out = _new((T, N2), torch.bfloat16, dev, stream)
     _need(out, "out", torch.bfloat16, (T, N2), dev)
     if qa_out is not None:
         _need(qa_out, "qa_out", torch.bfloat16, (T, N1), dev)
-    ws = _workspace(workspace_size(OP_MLA, T, K, N1, N2), dev, workspace)
+    ws = _workspace(workspace_size(OP_MLA, T, K, N1, N2), dev, workspace, stream)
     _check(load().mla_q_chain_head_norm(_ptr(x), _ptr(W_qa), _ptr(gamma_cq), _ptr(W_qb), T, K, N1, N2,
                                         float(eps), int(norm_mode), int(head_dim), _ptr(head_gamma),
                                         float(head_eps), _ptr(out), _ptr(qa_out), _ptr(ws),
@@ -643,11 +665,11 @@ def mla_q_chain(x, W_qa, gamma_cq, W_qb, eps=1e-6, norm_mode=NORM_SQRT_DIV, out=
     _need(gamma_cq, "gamma_cq", torch.bfloat16, (N1,), dev)
     _need(W_qb, "W_qb", torch.bfloat16, (N2, N1), dev)
     if out is None:
-        out = torch.empty((T, N2), dtype=torch.bfloat16, device=dev)
+        out = _new((T, N2), torch.bfloat16, dev, stream)
     _need(out, "out", torch.bfloat16, (T, N2), dev)
     if qa_out is not None:
         _need(qa_out, "qa_out", torch.bfloat16, (T, N1), dev)
-    ws = _workspace(workspace_size(OP_MLA, T, K, N1, N2), dev, workspace)
+    ws = _workspace(workspace_size(OP_MLA, T, K, N1, N2), dev, workspace, stream)
     _check(load().mla_q_chain(_ptr(x), _ptr(W_qa), _ptr(gamma_cq), _ptr(W_qb), T, K, N1, N2,
                               float(eps), int(norm_mode), _ptr(out), _ptr(qa_out), _ptr(ws),
                               ws.numel() * ws.element_size(), _stream(dev, stream)),
@@ -665,7 +687,7 @@ def rmsnorm_linear_skinny_noalloc(x, W, eps=1e-6, norm_mode=NORM_RSQRT, out=None
     _need(x, "x", torch.bfloat16, (T, K), dev)
     _need(W, "W", torch.bfloat16, (N, K), dev)
     if out is None:
-        out = torch.empty((T, N), dtype=torch.float32, device=dev)
+        out = _new((T, N), torch.float32, dev, stream)
     _need(out, "out", torch.float32, (T, N), dev)
     _check(load().rmsnorm_linear_skinny_noalloc(_ptr(x), _ptr(W), T, K, N, float(eps),
                                                 int(norm_mode), _ptr(out), _stream(dev, stream)),
@@ -681,9 +703,9 @@ def rnl_gemm_s8s8s32(A, B, out=None, workspace=None, stream=None):
     _need(A, "A", torch.int8, (M, K), dev)
     _need(B, "B", torch.int8, (N, K), dev)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.int32, device=dev)
+        out = _new((M, N), torch.int32, dev, stream)
     _need(out, "C", torch.int32, (M, N), dev)
-    ws = _workspace(workspace_size(OP_GEMM_S8, M, K, N), dev, workspace)
+    ws = _workspace(workspace_size(OP_GEMM_S8, M, K, N), dev, workspace, stream)
     _check(load().rnl_gemm_s8s8s32(_ptr(A), _ptr(B), _ptr(out), M, N, K, _ptr(ws),
                                    ws.numel() * ws.element_size(), _stream(dev, stream)),
            "rnl_gemm_s8s8s32")
