@@ -322,6 +322,8 @@ rnl_status launch_skinny(const void* x, const void* W, int64_t T, int64_t K, int
                          cudaStream_t s);
 
 // ---- device error words (one per kernel module) ----
+// A read takes about 8 us, so the modules that a program need not use (the
+// last four) leave *word alone until one of their kernels has been launched.
 rnl_status read_clear_error_rowwise(unsigned int* word);
 rnl_status read_clear_error_gemm(unsigned int* word);
 rnl_status read_clear_error_skinny(unsigned int* word);

@@ -42,6 +42,7 @@
 // sums.  Query rows are scaled by a power of two of their own, weights by 2^15
 // (p <= 1, so that weights down to 2^-29 keep all 11 bits).
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "kv4.cuh"
@@ -52,6 +53,7 @@ namespace {
 using namespace kv4;
 
 __device__ unsigned int g_err_kv4attn;
+std::atomic<bool> g_launched{false};
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
@@ -858,6 +860,7 @@ size_t kv4_attn_workspace_bytes(int64_t T, int64_t D, int64_t G) {
 
 rnl_status launch_kv4_attention(const Kv4AttnArgs& x, const rnl_kv4_cache& c, const rnl_kv4_seqs& q,
                                 cudaStream_t s) {
+  g_launched.store(true, std::memory_order_relaxed);
   DeviceInfo dev;
   const rnl_status st = current_device(&dev);
   if (st != RNL_OK) return st;
@@ -904,6 +907,7 @@ rnl_status launch_kv4_attention(const Kv4AttnArgs& x, const rnl_kv4_cache& c, co
 }
 
 rnl_status read_clear_error_kv4attn(unsigned int* word) {
+  if (!g_launched.load(std::memory_order_relaxed)) return RNL_OK;
   unsigned int v = 0, zero = 0;
   if (cudaMemcpyFromSymbol(&v, g_err_kv4attn, sizeof v) != cudaSuccess) return RNL_ERR_LAUNCH;
   if (v != 0 && cudaMemcpyToSymbol(g_err_kv4attn, &zero, sizeof zero) != cudaSuccess)

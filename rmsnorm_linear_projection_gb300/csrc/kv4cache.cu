@@ -18,6 +18,8 @@
 // call, cold: prefixes of 9000 to 20000 tokens read back at 5.4 TB/s (10 of
 // them: 6.35), prompts written and read back at 3.7 TB/s (20 of them: 4.95);
 // 512 elements a warp were slower (50 against 43 us for either).
+#include <atomic>
+
 #include "kv4.cuh"
 
 namespace rnl {
@@ -26,6 +28,7 @@ namespace {
 using namespace kv4;
 
 __device__ unsigned int g_err_kv4cache;
+std::atomic<bool> g_launched{false};
 
 constexpr int kCacheWarps = 4;
 constexpr int kVecs = 4;  // 8-element vectors of a row that a lane takes
@@ -161,6 +164,7 @@ inline unsigned blocks_of(const rnl_kv4_seqs& q, int chunks) {
 
 rnl_status launch_kv4_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                              const rnl_kv4_cache& c, const rnl_kv4_seqs& q, cudaStream_t s) {
+  g_launched.store(true, std::memory_order_relaxed);
   const int chunks = chunks_of(c);
   trace_before(s);
   kv4_append_kernel<<<blocks_of(q, chunks), kCacheWarps * 32, 0, s>>>(
@@ -173,6 +177,7 @@ rnl_status launch_kv4_append(const void* k, int64_t k_stride, const void* v, int
 
 rnl_status launch_kv4_gather(const rnl_kv4_cache& c, const rnl_kv4_seqs& q, void* k_out, void* v_out,
                              cudaStream_t s) {
+  g_launched.store(true, std::memory_order_relaxed);
   const int chunks = chunks_of(c);
   trace_before(s);
   kv4_gather_kernel<<<blocks_of(q, chunks), kCacheWarps * 32, 0, s>>>(
@@ -183,6 +188,7 @@ rnl_status launch_kv4_gather(const rnl_kv4_cache& c, const rnl_kv4_seqs& q, void
 }
 
 rnl_status read_clear_error_kv4cache(unsigned int* word) {
+  if (!g_launched.load(std::memory_order_relaxed)) return RNL_OK;
   unsigned int v = 0, zero = 0;
   if (cudaMemcpyFromSymbol(&v, g_err_kv4cache, sizeof v) != cudaSuccess) return RNL_ERR_LAUNCH;
   if (v != 0 && cudaMemcpyToSymbol(g_err_kv4cache, &zero, sizeof zero) != cudaSuccess)

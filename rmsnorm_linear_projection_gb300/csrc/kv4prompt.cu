@@ -38,6 +38,7 @@
 // where the products alone would take 1.1.  What bounds it is the softmax (a
 // thread a row: exponentials, conversions, TMEM reads) beside 8 to 10 us a run.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "kv4.cuh"
@@ -48,6 +49,7 @@ namespace {
 using namespace kv4;
 
 __device__ unsigned int g_err_kv4prompt;
+std::atomic<bool> g_launched{false};
 
 constexpr int kT = 128;            // tokens a tile of operands
 constexpr int kU = 64;             // tokens a step of products and softmax
@@ -1084,6 +1086,7 @@ size_t kv4_prompt_workspace_bytes(int64_t D) {
 
 rnl_status launch_kv4_prompt(const AttnParams& p0, const Args& a, int block, void* ws, const DeviceInfo& dev,
                              cudaStream_t s) {
+  g_launched.store(true, std::memory_order_relaxed);
   AttnParams p = p0;
   p.rec = static_cast<int4*>(ws);
   p.part = reinterpret_cast<float*>(p.rec + kMaxPromptCtas);
@@ -1092,6 +1095,7 @@ rnl_status launch_kv4_prompt(const AttnParams& p0, const Args& a, int block, voi
 }
 
 rnl_status read_clear_error_kv4prompt(unsigned int* word) {
+  if (!g_launched.load(std::memory_order_relaxed)) return RNL_OK;
   unsigned int v = 0, zero = 0;
   if (cudaMemcpyFromSymbol(&v, g_err_kv4prompt, sizeof v) != cudaSuccess) return RNL_ERR_LAUNCH;
   if (v != 0 && cudaMemcpyToSymbol(g_err_kv4prompt, &zero, sizeof zero) != cudaSuccess)

@@ -22,6 +22,8 @@
 // arithmetic (32768 tokens: 4.5 TB/s, without norm 5.5).
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -29,6 +31,7 @@ namespace rnl {
 namespace {
 
 __device__ unsigned int g_err_axes;  // kErrArg | site: a position outside [0, P)
+std::atomic<bool> g_launched{false};
 
 constexpr int kWarps = 4;
 constexpr int kMinCtas = 5;  // by registers (102); 4 for head_dim 64 without it, 47 against 43 us at 18433 tokens
@@ -202,6 +205,7 @@ rnl_status launch_qkv_rope_axes(const void* y, int64_t T, int64_t Hq, int64_t Hk
                                 const float* cos_sin, int64_t max_pos, void* q, void* k, void* v,
                                 cudaStream_t s) {
   if (T * (Hq + 2 * Hkv) == 0) return RNL_OK;
+  g_launched.store(true, std::memory_order_relaxed);
   AxisMap map = {};
   for (int64_t i = 0; i < D / 2; ++i) map.a[i] = axis_of_pair[i];
   trace_before(s);
@@ -217,6 +221,7 @@ rnl_status launch_qkv_rope_axes(const void* y, int64_t T, int64_t Hq, int64_t Hk
 }
 
 rnl_status read_clear_error_axes(unsigned int* word) {
+  if (!g_launched.load(std::memory_order_relaxed)) return RNL_OK;
   unsigned int v = 0, zero = 0;
   if (cudaMemcpyFromSymbol(&v, g_err_axes, sizeof v) != cudaSuccess) return RNL_ERR_LAUNCH;
   if (v != 0 && cudaMemcpyToSymbol(g_err_axes, &zero, sizeof zero) != cudaSuccess) return RNL_ERR_LAUNCH;
