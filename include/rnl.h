@@ -271,7 +271,10 @@ typedef struct rnl_kv4_cache {
  * beyond n_rows, cu_rows decreasing) and a page id outside [0, n_pages) make
  * the next rnl_check_device_error() return RNL_ERR_ARG; the rows concerned are
  * left unwritten or, for a bad page that attention would read, unspecified.
- * Two sequences may share pages that the call only reads.
+ * Two sequences may share pages that the call only reads.  Entries of pages
+ * that a call has no token to read or write in are not looked at: behind a
+ * sequence's length, in front of the rows (append, gather), or wholly in front
+ * of the first row's window (attention).
  */
 typedef struct rnl_kv4_seqs {
   const int32_t *block_table, *seq_lens, *cu_rows;

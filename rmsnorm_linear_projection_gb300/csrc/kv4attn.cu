@@ -286,7 +286,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     const int tok = (ahead.w.t0 + ahead.tile) * TT + chunk_at;
     page_off = tok & (a.page - 1);
     page_head = ahead.head;
-    if (chunk_at < TT && tok < ahead.w.hi)
+    // (not what lies wholly in front of a window: that page may have been given back)
+    if (chunk_at < TT && tok < ahead.w.hi && tok + chunk_tokens > ahead.w.lo)
       page = __ldg(a.table + static_cast<int64_t>(ahead.b) * a.max_pages + (tok >> a.page_shift));
     else
       page = -2;
