@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import operator
 import os
 import threading
 
@@ -317,7 +318,8 @@ def rnl_qkv_rope_axes(y, n_q_heads, n_kv_heads, head_dim, q_gamma, k_gamma, posi
     _need(positions, "positions", torch.int32, (A, T), dev)
     if len(axis_of_pair) != D // 2:
         raise ValueError(f"axis_of_pair must hold {D // 2} values, got {len(axis_of_pair)}")
-    axes = bytes(axis_of_pair)
+    # (value by value: bytes() would take an integer array's memory instead)
+    axes = bytes([operator.index(a) for a in axis_of_pair])
     P = cos_sin.shape[0]
     _need(cos_sin, "cos_sin", torch.float32, (P, D), dev)
     q_out, k_out, v_out = _qkv_outputs(T, Hq, Hkv, D, dev, q_out, k_out, v_out, stream)
