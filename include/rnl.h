@@ -320,14 +320,17 @@ rnl_status rnl_kv4_gather(const rnl_kv4_cache *cache, const rnl_kv4_seqs *seqs, 
  *   lse_out fp32 [n_rows, n_q_heads] or NULL: log sum_j exp(scale * q . k[j])
  * A row that reads no token (length 0, or a position below 0) gets zeros and
  * lse -infinity.  What stands in the cache behind a sequence's length, or at
- * tokens that a row does not read, has no effect on it; a row that reads a
- * token with a scale byte of 255, in its keys or its values, gets NaN, and lse
- * NaN.  Softmax statistics and sums in FP32; products of binary16 operands that
- * hold the cache's values and q, scaled by powers of two, exactly: values down
- * to 2^-37 of the largest near them (a scale byte of 0, 2^-127, counts as zero),
- * elements of q down to 2^-31 of the row's largest.  The softmax weights are
- * rounded to binary16: 11 bits, for weights of at least 2^-21 of the row's
- * largest, fewer below.
+ * tokens that a row does not read, has no effect on it (but for the rounding of
+ * its weights, which can go another way); a row that reads a token with a scale
+ * byte of 255, in its keys or its values, gets NaN, and lse NaN.  Softmax
+ * statistics and sums in FP32; products of binary16 operands that hold the
+ * cache's values and q, scaled by powers of two, exactly: keys and values down
+ * to 2^-36 of the largest that the row reads in the same 128 tokens (keys) or up
+ * to there (values; a scale byte of 0, 2^-127, counts as zero), elements of q
+ * down to 2^-31 of the row's largest.  The softmax weights are rounded to
+ * binary16: 11 bits, for weights of at least 2^-21 of the row's largest, fewer
+ * below.  Where tokens that only some rows of a call read are 2^36 times others,
+ * those rows are computed one at a time in FP32, which takes much longer.
  * Workspace: rnl_workspace_size(RNL_OP_KV4_ATTENTION, n_rows, head_dim,
  * n_q_heads, n_kv_heads) bytes; results do not depend on its contents.  Calls
  * that may run at the same time (other streams, other graphs) need one each.

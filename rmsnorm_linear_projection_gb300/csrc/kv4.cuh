@@ -225,6 +225,130 @@ __device__ __forceinline__ void store_row(const AttnParams& p, const Seq& s, int
   if (d == 0 && p.lse != nullptr) p.lse[row] = ll != 0.f ? mm * kLn2 + logf(ll) : -INFINITY;
 }
 
+// Rows taken by themselves.  The rows of an item share their operands, and with
+// them the reference scale R: E2M1 * 2^(X - R + 13) is exact in binary16 for
+// X >= R - kSpread only.  Where a token that some of the rows do not read (later
+// in a causal prompt, older than their window) is so much larger than others,
+// R would be that token's and the rest would vanish for those rows too.  The
+// kernels see that from the scale bytes of the tiles that the mask cuts, and
+// such an item's rows are computed by one_row instead.
+constexpr int kSpread = 36;
+
+// A warp computes row r of key head kvh over the tokens of [lo, hi) that it
+// reads, in FP32 straight from the cache: a token a lane for the scores, D / 32
+// dims a lane for the sums v.  m is the maximum in log2 units, l the sum of the
+// weights 2^(x - m).
+template <int D>
+__device__ __forceinline__ void one_row(const Args& a, const AttnParams& p, const Seq& s, int b, int kvh, int r,
+                                        int lo, int hi, unsigned int* err, uint32_t site, float& m, float& l,
+                                        float (&v)[D / 32]) {
+  const int lane = threadIdx.x & 31;
+  const int tok_q = r / p.G;
+  const int pos = p.causal ? s.len - s.rows + tok_q : s.len - 1;
+  lo = max(max(lo, 0), p.window > 0 ? pos - p.window + 1 : 0);
+  hi = min(hi, pos + 1);
+  const __nv_bfloat16* q = p.q + (s.row0 + tok_q) * p.q_stride + static_cast<int64_t>(kvh * p.G + (r - tok_q * p.G)) * D;
+  uint32_t am = 0;
+  for (int i = lane; i < D / 2; i += 32) {
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(q) + i);
+    am = max(am, max((w << 16) & 0x7FFFFFFFu, w & 0x7FFF0000u));
+  }
+  // q is taken times 2^-e, below 2, and a block's scale times 2^-16, so that no sum overflows
+  const int e = max(static_cast<int>(__reduce_max_sync(0xffffffffu, am) >> 23), 1) - 127;
+  const float q1 = pow2i(-e / 2), q2 = pow2i(-e - (-e) / 2);
+  const float f1 = pow2i((e + 16) / 2), f2 = pow2i(e + 16 - (e + 16) / 2);
+  const int n_blocks = D >> a.block_shift, words = 1 << (a.block_shift - 3);
+  m = -INFINITY;
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) v[i] = 0.f;
+  for (int t0 = lo; t0 < hi; t0 += 32) {
+    const int64_t row = t0 + lane < hi ? token_row(a, b, t0 + lane, kvh, err, site) : -1;
+    float x = -INFINITY;
+    if (row >= 0) {
+      const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.k.codes + row * (D / 2));
+      float sum = 0.f;
+      bool finite = true;
+#pragma unroll 1
+      for (int c = 0; c < n_blocks; ++c) {
+        const uint32_t byte = __ldg(a.k.scales + row * n_blocks + c);
+        finite = finite && byte != 255u && __ldg(a.v.scales + row * n_blocks + c) != 255u;
+        float part = 0.f;
+#pragma unroll 1
+        for (int w = c * words; w < (c + 1) * words; ++w) {
+          const uint4 u = __ldg(reinterpret_cast<const uint4*>(q) + w);
+          const uint32_t qw[4] = {u.x, u.y, u.z, u.w};
+          uint32_t h[4];
+          e2m1x8_to_half(__ldg(codes + w), h);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float2 k2 = __half22float2(h2(h[y]));
+            part = fmaf(__uint_as_float(qw[y] << 16) * q1 * q2, k2.x, part);
+            part = fmaf(__uint_as_float(qw[y] & 0xFFFF0000u) * q1 * q2, k2.y, part);
+          }
+        }
+        sum = fmaf(part, byte_scale(byte) * (1.f / 65536.f), sum);
+      }
+      x = finite ? sum * p.scale_log2 * f1 * f2 : NAN;
+    }
+    float mx = x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn;
+    const float al = ex2(m - mu), w = ex2(x - mu);
+    m = mn;
+    float all = w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    l = fmaf(l, al, all);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) v[i] *= al;
+#pragma unroll 1
+    for (int j = 0; j < 32; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      const int64_t rj = __shfl_sync(0xffffffffu, row, j);
+      if (wj == 0.f) continue;
+      const uint8_t* c = a.v.codes + rj * (D / 2) + lane * (D / 64);
+      uint32_t code;
+      if constexpr (D == 64) code = __ldg(c);
+      else if constexpr (D == 128) code = __ldg(reinterpret_cast<const uint16_t*>(c));
+      else code = __ldg(reinterpret_cast<const uint32_t*>(c));
+      const float f = wj * byte_scale(__ldg(a.v.scales + rj * n_blocks + ((lane * (D / 32)) >> a.block_shift)));
+      uint32_t h[4];
+      e2m1x8_to_half(code, h);
+#pragma unroll
+      for (int i = 0; i < D / 32; i += 2) {
+        const float2 z = __half22float2(h2(h[i / 2]));
+        v[i] = fmaf(z.x, f, v[i]);
+        v[i + 1] = fmaf(z.y, f, v[i + 1]);
+      }
+    }
+  }
+}
+
+// one_row's result as an output row, or as row i of a partial of `rows` rows.
+template <int D>
+__device__ __forceinline__ void store_one_row(const AttnParams& p, const Seq& s, int kvh, int r, float m, float l,
+                                              const float (&v)[D / 32], float* partial, int i, int rows) {
+  const int lane = threadIdx.x & 31, d = lane * (D / 32);
+  if (partial != nullptr) {
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) partial[i * D + d + x] = v[x];
+    if (lane == 0) {
+      partial[rows * D + i] = m;
+      partial[rows * D + rows + i] = l;
+    }
+    return;
+  }
+  const int tok = r / p.G;
+  const int64_t row = static_cast<int64_t>(s.row0 + tok) * p.Hq + kvh * p.G + (r - tok * p.G);
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int x = 0; x < D / 32; x += 2)
+    *reinterpret_cast<__nv_bfloat162*>(p.out + row * D + d + x) = __floats2bfloat162_rn(v[x] * inv, v[x + 1] * inv);
+  if (lane == 0 && p.lse != nullptr) p.lse[row] = l != 0.f ? m * kLn2 + logf(l) : -INFINITY;
+}
+
 __device__ __forceinline__ int64_t range_start(int64_t units, int c, int n) { return units * c / n; }
 
 }  // namespace kv4

@@ -37,8 +37,8 @@
 //
 // Scales.  2^X of a block does not fit binary16's range, 2^(X - R) does, where
 // R is the largest X of the tile (keys) or of the tiles so far (values): an
-// operand is E2M1 * 2^(X - R + 13), exact unless it lies 2^37 below the
-// largest, and 2^(R - 13) goes into the FP32 factors of the scores and of the
+// operand is E2M1 * 2^(X - R + 13), exact down to 2^-36 of the largest (kv4.cuh,
+// kSpread), and 2^(R - 13) goes into the FP32 factors of the scores and of the
 // sums.  Query rows are scaled by a power of two of their own, weights by 2^15
 // (p <= 1, so that weights down to 2^-29 keep all 11 bits).
 #include <algorithm>
@@ -149,9 +149,60 @@ __device__ __forceinline__ void skip(const Args& a, const AttnParams& p, Cursor&
   }
 }
 
-template <int D, int NT, int BS>
+// The place of unit `off` of sequence b's items, u0 of the range [u0, u1); `at`:
+// where its first tile stands.
+template <int D, int NT>
+__device__ __forceinline__ Cursor cursor_at(int b, const Span& w, long long off, int64_t u0, int64_t u1, int64_t& at) {
+  Cursor c;
+  c.b = b;
+  c.w = w;
+  // (a 64-bit division is slow)
+  const int item = off >> 32 ? static_cast<int>(off / (c.w.tiles + kItemCost))
+                             : static_cast<int>(static_cast<uint32_t>(off) / (c.w.tiles + kItemCost));
+  c.head = item / c.w.groups;
+  c.group = item - c.head * c.w.groups;
+  c.tile = static_cast<int>(off - static_cast<long long>(item) * (c.w.tiles + kItemCost)) - kItemCost;
+  c.left = static_cast<int>(u1 - u0);
+  at = u0;
+  if (c.tile < 0) {
+    at -= c.tile;
+    c.left += c.tile;
+    c.tile = 0;
+  }
+  return c;
+}
+
+// The rows of the CTA's segments in `alone` (bit: number, up to 31) by
+// themselves, a warp a row.
+template <int D, int NT>
+__device__ __noinline__ void segments_by_rows(const Args& a, const AttnParams& p, int b, const Span& first, long long off,
+                                              int64_t u0, int64_t u1, uint32_t alone) {
+  using C = Cfg<D, NT>;
+  int64_t at;
+  Cursor cur = cursor_at<D, NT>(b, first, off, u0, u1, at);
+  for (int seg = 0; cur.left > 0; ++seg) {
+    const int n = min(cur.w.tiles - cur.tile, cur.left);
+    if (alone >> min(seg, 31) & 1) {
+      const Seq& s = cur.w.s;
+      const int from = (cur.w.t0 + cur.tile) * C::TT;
+      float* slot = p.part + static_cast<int64_t>(2 * blockIdx.x + (seg > 0)) * C::kSlot;
+      for (int i = threadIdx.x >> 5; i < C::kRows; i += kWarps) {
+        const int r = cur.group * C::kRows + i;
+        if (r >= s.rows * p.G) break;
+        float m, l, v[D / 32];
+        one_row<D>(a, p, s, cur.b, cur.head, r, from, min(from + n * C::TT, cur.w.hi), &g_err_kv4attn, 46, m, l, v);
+        store_one_row<D>(p, s, cur.head, r, m, l, v, n == cur.w.tiles ? nullptr : slot, i, C::kRows);
+      }
+    }
+    skip<D, NT>(a, p, cur, n);
+  }
+}
+
+// MIXED: the rows of a sequence may differ in what they read (several causal
+// rows).  Without it, 8 sequences of 131072 tokens take 235 us instead of 240.
+template <int D, int NT, int BS, bool MIXED>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
-    kv4_attn_kernel(const Args a, const AttnParams p) {
+    kv4_attn_kernel(const __grid_constant__ Args a, const __grid_constant__ AttnParams p) {
   using C = Cfg<D, NT>;
   constexpr int TT = C::TT, kRows = C::kRows, kPitch = C::kPitch, T8 = C::kTiles;
   constexpr bool kTwin = NT == 0;   // both parities in one product
@@ -169,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
   __shared__ float sh_ml[2][kWarps][2][kRows];
   __shared__ long long sh_sum[kWarps];
   __shared__ int sh_b, sh_abort;
+  __shared__ uint32_t sh_alone;  // segments whose rows are taken by themselves in the end
   __shared__ long long sh_off;
   __shared__ Span sh_w;
   float* merge = reinterpret_cast<float*>(smem + kWarps * 2 * kSideBytes);
@@ -180,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     for (int i = 0; i < kWarps * 2; ++i) mbar_init(smem_u32(&full[i]), 1);
     sh_abort = 0;
     sh_b = -1;
+    sh_alone = 0;
     fence_mbar_init();
   }
   // ---- this CTA's range of tiles
@@ -243,22 +296,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     grid_dependency_wait();
     return;
   }
-  Cursor cur;  // the CTA's place
-  cur.b = sh_b;
-  cur.w = sh_w;
-  // (a 64-bit division is slow)
-  const int item = sh_off >> 32 ? static_cast<int>(sh_off / (cur.w.tiles + kItemCost))
-                                : static_cast<int>(static_cast<uint32_t>(sh_off) / (cur.w.tiles + kItemCost));
-  cur.head = item / cur.w.groups;
-  cur.group = item - cur.head * cur.w.groups;
-  cur.tile = static_cast<int>(sh_off - static_cast<long long>(item) * (cur.w.tiles + kItemCost)) - kItemCost;
-  cur.left = static_cast<int>(u1 - u0);
-  int64_t at = u0;  // where the range's first tile stands
-  if (cur.tile < 0) {
-    at -= cur.tile;
-    cur.left += cur.tile;
-    cur.tile = 0;
-  }
+  int64_t at;  // where the range's first tile stands
+  Cursor cur = cursor_at<D, NT>(sh_b, sh_w, sh_off, u0, u1, at);  // the CTA's place
 
   // ---- the warp's buffers: a tile of keys and a tile of values, each fetched
   // again as soon as it has been read
@@ -384,19 +423,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
       m[t][0] = m[t][1] = -INFINITY;
       l[t][0] = l[t][1] = 0.f;
     }
-    int ref_v = 13;  // below 13 the factor 2^(140 - ref) would leave binary32
+    // tokens that some row of the group reads
+    const int seen_lo = max(cur.w.lo, pos_min - win + 1), seen_hi = min(cur.w.hi, pos_max + 1);
+    int ref_v = MIXED ? 0 : 13;  // 0: no tile yet; else at least 13 (below, the factor 2^(140 - ref) would leave binary32)
+    int common_v = 13;     // the same over the tiles that every row reads whole
+    bool alone = false;    // the rows have to be taken by themselves (one_row)
 
     for (int i = (warp - done % kWarps + kWarps) % kWarps; i < seg_tiles; i += kWarps) {
       const int tok0 = (cur.w.t0 + cur.tile + i) * TT;
       // a tile that no row of this group reads (causal, earlier rows): nothing
-      const bool any = tok0 <= pos_max && tok0 + TT > pos_min - win + 1 && cur.w.hi > 0;
-      const bool edge = tok0 < cur.w.lo || tok0 + TT > cur.w.hi;
+      const bool any = tok0 < seen_hi && tok0 + TT > seen_lo;
+      const bool whole = tok0 + TT - 1 <= pos_min && tok0 > pos_max - win;
+      const bool cut = MIXED && pos_min != pos_max && !whole;  // with tokens that only some of the rows read
+      const bool edge = tok0 < seen_lo || tok0 + TT > seen_hi || cut;
       // largest scale byte of a side; at an edge of what the rows read, the
       // scale bytes of tokens that no row reads become 0 first, so that
       // whatever stands there gives zero operands.  A block that is not finite
       // (byte 255) becomes zeros too, and the rows that read its token get a
       // normaliser that is not a number
-      auto top_scale = [&](uint8_t* scales) {
+      // `low`: the smallest byte that is not 0 where `edge` (MIXED), else 256
+      auto top_scale = [&](uint8_t* scales, bool edge, int& low) {
         uint32_t* sc = reinterpret_cast<uint32_t*>(scales) + lane;
         uint32_t w[kSW];
 #pragma unroll
@@ -408,13 +454,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const int tok = tok0 + ((y * 32 + lane) * 4 + x) / kSB;
-              if (tok >= cur.w.lo && tok < cur.w.hi) keep |= 0xFFu << (8 * x);
+              if (tok >= seen_lo && tok < seen_hi) keep |= 0xFFu << (8 * x);
             }
             w[y] &= keep;
             if (has) sc[y * 32] = w[y];
           }
         }
+        low = 256;
         if (edge) {
+          if constexpr (MIXED) {
+            uint32_t t = 0xFFFFFFFFu;
+#pragma unroll
+            for (int y = 0; y < kSW; ++y) t = __vminu4(t, __vsub4(w[y], 0x01010101u));  // 0 becomes 255
+            t = __vminu4(t, t >> 16 | 0xFFFF0000u);
+            low = static_cast<int>(__reduce_min_sync(0xffffffffu, min(t & 0xFFu, (t >> 8) & 0xFFu))) + 1;
+          }
           fence_proxy_async_shared();  // the next copy into this buffer comes after these writes
           __syncwarp();
         }
@@ -457,7 +511,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
       float s[T8][MS][4];
       float f_tile = 0.f;
       if (any) {
-        const int ref_k = max(top_scale(ks + kCodeBytes), 13);
+        int low;
+        const int ref_k = max(top_scale(ks + kCodeBytes, edge, low), 13);
+        alone |= cut && ref_k - low > kSpread;
         const float fk = pow2i(140 - ref_k);
         f_tile = pow2w(ref_k - 140);
         // ---- scores, transposed: 16 tokens x 8 rows
@@ -514,8 +570,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
       phase ^= 1u;
       if (any) {
         // ---- softmax over the tile
-        const bool whole = tok0 + TT - 1 <= pos_min && tok0 > pos_max - win;
-        const int new_v = max(ref_v, top_scale(vs + kCodeBytes));
+        int low;
+        const int top_v = top_scale(vs + kCodeBytes, edge || (MIXED && ref_v > common_v), low);
+        const int new_v = MIXED ? max(max(ref_v, top_v), 13) : max(ref_v, top_v);
+        if constexpr (MIXED) {
+          common_v = max(common_v, cut ? 13 : top_v);
+          // far above the sums so far, or this tile's values far below what only some rows read
+          alone |= (cut && ref_v != 0 && new_v - ref_v > kSpread) || (new_v > common_v && new_v - low > kSpread);
+        }
         const float fv = ref_v == new_v ? 1.f : pow2i(ref_v - new_v);
         ref_v = new_v;
         uint32_t pb[T8][MS][2];
@@ -662,6 +724,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
         }
         l[t][h] = x;
       }
+    if (MIXED && alone && lane == 0) atomicOr(&sh_alone, 1u << min(seg, 31));
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < T8; ++t)
@@ -695,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     constexpr int kTpr = D / 8;  // threads a row, 8 dims each
     for (int x = tid; x < kRows * kTpr; x += kThreads) {
       const int r = x / kTpr, d = (x - r * kTpr) * 8;
-      if (r0 + r >= all_rows) continue;
+      if (r0 + r >= all_rows || (MIXED && (sh_alone >> min(seg, 31) & 1))) continue;
       float mm = -INFINITY, ll = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[w][0][r]);
@@ -735,6 +798,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     at += seg_tiles + kItemCost;
     skip<D, NT>(a, p, cur, seg_tiles);
   }
+  if (MIXED) __syncthreads();
+  if (MIXED && sh_alone != 0)
+    segments_by_rows<D, NT>(a, p, sh_b, sh_w, sh_off, u0, u1, sh_alone);
   grid_dependency_wait();
 }
 
@@ -803,10 +869,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kJoin * 128)
   }
 }
 
-template <int D, int NT, int BS>
+template <int D, int NT, int BS, bool MIXED>
 rnl_status launch_split(const AttnParams& p, const Args& a, const DeviceInfo& dev, bool after_prompt, cudaStream_t s) {
   using C = Cfg<D, NT>;
-  const rnl_status st = ensure_smem_attr(reinterpret_cast<const void*>(kv4_attn_kernel<D, NT, BS>), dev.device, C::kSmem);
+  const rnl_status st = ensure_smem_attr(reinterpret_cast<const void*>(kv4_attn_kernel<D, NT, BS, MIXED>), dev.device, C::kSmem);
   if (st != RNL_OK) return st;
   const int ctas = std::min(dev.sm_count * C::kMinCtas, kMaxCtas);
   cudaLaunchAttribute at[1];
@@ -822,7 +888,7 @@ rnl_status launch_split(const AttnParams& p, const Args& a, const DeviceInfo& de
   // call in the stream may write what this kernel reads
   cfg.numAttrs = after_prompt ? 1 : 0;
   trace_before(s);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_attn_kernel<D, NT, BS>, a, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_attn_kernel<D, NT, BS, MIXED>, a, p);
   trace_after(s, "kv4_attn");
   if (e != cudaSuccess) return RNL_ERR_LAUNCH;
   cfg.blockDim = dim3(C::kJoin * 128);
@@ -892,19 +958,23 @@ rnl_status launch_kv4_attention(const Kv4AttnArgs& x, const rnl_kv4_cache& c, co
   // (with 8 rows an item 131072 tokens x 8 take 267 us instead of 242; with 16, 32
   // sequences of 2 rows 91 instead of 66)
   const int64_t rows = (q.n_rows + q.n_seqs - 1) / q.n_seqs * p.G;
-  auto go = [&](auto d) {
-    constexpr int D = decltype(d)::value;
-    if (c.block == 64)
-      return rows <= 4   ? launch_split<D, 0, 64>(p, a, dev, after, s)
-             : rows <= 8 ? launch_split<D, 1, 64>(p, a, dev, after, s)
-                         : launch_split<D, 2, 64>(p, a, dev, after, s);
-    return rows <= 4   ? launch_split<D, 0, 32>(p, a, dev, after, s)
-           : rows <= 8 ? launch_split<D, 1, 32>(p, a, dev, after, s)
-                       : launch_split<D, 2, 32>(p, a, dev, after, s);
+  const bool mixed = a.cu != nullptr && p.causal;
+  auto go = [&](auto d, auto bs) {
+    constexpr int D = decltype(d)::value, BS = decltype(bs)::value;
+    if (mixed)
+      return rows <= 4   ? launch_split<D, 0, BS, true>(p, a, dev, after, s)
+             : rows <= 8 ? launch_split<D, 1, BS, true>(p, a, dev, after, s)
+                         : launch_split<D, 2, BS, true>(p, a, dev, after, s);
+    return rows <= 4   ? launch_split<D, 0, BS, false>(p, a, dev, after, s)
+           : rows <= 8 ? launch_split<D, 1, BS, false>(p, a, dev, after, s)
+                       : launch_split<D, 2, BS, false>(p, a, dev, after, s);
   };
-  if (a.D == 64) return go(std::integral_constant<int, 64>{});
-  if (a.D == 128) return go(std::integral_constant<int, 128>{});
-  return go(std::integral_constant<int, 256>{});
+  auto by_block = [&](auto d) {
+    return c.block == 64 ? go(d, std::integral_constant<int, 64>{}) : go(d, std::integral_constant<int, 32>{});
+  };
+  if (a.D == 64) return by_block(std::integral_constant<int, 64>{});
+  if (a.D == 128) return by_block(std::integral_constant<int, 128>{});
+  return by_block(std::integral_constant<int, 256>{});
 }
 
 rnl_status read_clear_error_kv4attn(unsigned int* word) {

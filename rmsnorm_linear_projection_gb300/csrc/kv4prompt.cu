@@ -3,7 +3,7 @@
 // fifth-generation tensor cores.  The formulas, operands and scales are those
 // of kv4attn.cu: E2M1 values times 2^(X - R + 13) in binary16, where R is the
 // tile's largest scale (keys) or the largest so far (values), exact down to
-// 2^-37 of it; queries scaled by a power of two per row.
+// 2^-36 of it (kv4.cuh, kSpread); queries scaled by a power of two per row.
 //
 // A CTA works on 256 rows (token x query head of one key head), two tiles of
 // 128, against tiles of 128 tokens in steps of 64:
@@ -114,6 +114,16 @@ __device__ __forceinline__ void group_tokens(const AttnParams& p, const Seq& s, 
     if (p.window > 0) lo = max(0, s.len - s.rows + g * kGroup / p.G + 1 - p.window);
   }
 }
+// The tokens that every row of the group reads.
+__device__ __forceinline__ void common_tokens(const AttnParams& p, const Seq& s, int g, int& lo, int& hi) {
+  lo = 0;
+  hi = s.len;
+  if (p.causal) {
+    const int last = min((g + 1) * kGroup, s.rows * p.G) - 1;
+    hi = max(0, s.len - s.rows + g * kGroup / p.G + 1);
+    if (p.window > 0) lo = max(0, s.len - s.rows + last / p.G + 1 - p.window);
+  }
+}
 __device__ __forceinline__ int tiles_between(int lo, int hi) {
   return hi > lo ? (hi + kT - 1) / kT - lo / kT : 1;  // at least one: rows without a token still get zeros
 }
@@ -208,12 +218,34 @@ __device__ __forceinline__ bool next_run(const Args& a, const AttnParams& p, Wal
   return false;
 }
 
+// The walk from unit `off` of sequence b's items on.
+__device__ __forceinline__ Walk walk_from(const AttnParams& p, int b, const Span& w, int64_t off, int64_t at,
+                                          int64_t left) {
+  Walk c;
+  c.b = b;
+  c.w = w;
+  const int64_t per_head = head_units(p, w);
+  const int len = pair_units(p, w);
+  // (64-bit divisions are slow, and everyone waits for the first run)
+  c.head = off >> 32 || per_head >> 32
+               ? static_cast<int>(off / per_head)
+               : static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(per_head));
+  const int64_t in_head = off - c.head * per_head;
+  const int64_t pair = in_head >> 32 ? in_head / len : static_cast<uint32_t>(in_head) / static_cast<uint32_t>(len);
+  c.pair = static_cast<int>(min(pair, static_cast<int64_t>(w.groups / 2)));
+  c.off = static_cast<int>(in_head - static_cast<int64_t>(c.pair) * len);
+  c.at = at;
+  c.left = left;
+  return c;
+}
+
 // A run as the roles read it.
 struct Run {
   int row0, rows, len;         // the sequence
   int groups, group, seq, kvh;
   int lo, tile, n, all;        // tokens from lo on, in tiles: first, number, number of the whole group
   int hi, stop;
+  int common_lo, common_hi;    // the tokens that every row of the group reads
   int64_t unit;
 };
 constexpr int kRuns = 4;
@@ -224,7 +256,10 @@ struct __align__(16) PCtrl {
   uint64_t raw_full[kMaxRing], raw_empty[kMaxRing];
   uint64_t run_full[kRuns], run_empty[kRuns];
   Run run[kRuns];
-  int4 raw_info[kMaxRing];      // first token, the group's tokens, 1: a run's first tile, 2: no more tiles
+  // first token, the group's tokens, 1: a run's first tile, 2: no more tiles, 4: with
+  // tokens that only some of the rows read; the run's number (up to 31) from bit 8 on
+  int4 raw_info[kMaxRing];
+  uint32_t alone;               // runs whose rows have to be taken by themselves (one_row)
   float k_info[4];   // score factor of tile x at x % 4
   int v_info[4];     // the values' reference scale byte
   int top[2][2][kFillWarps], stop[2], done[2][2];
@@ -322,7 +357,7 @@ __device__ __forceinline__ void idle_wait(uint32_t bar, uint32_t parity, volatil
 // Named barriers.  A warp that polls takes issue slots from those that work:
 // of the warps that wait for the same thing one polls, the others stand at a
 // named barrier, which costs nothing.  1-2: a row tile's warps, 3-4: the warps
-// that fill keys, values.
+// that fill keys, values; 5: both row tiles' warps, once.
 template <int WARPS>
 __device__ __forceinline__ void meet(int bar) {
   asm volatile("barrier.cta.sync %0, %1;" ::"r"(bar), "n"(WARPS * 32) : "memory");
@@ -364,9 +399,30 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t x, uint32_t 
                : "memory");
 }
 
+// The rows of the CTA's runs in ctrl.alone by themselves, a softmax warp a row.
+// After all runs: this takes as long as it takes, and nothing waits for it.
+template <int D>
+__device__ __noinline__ void runs_by_rows(const Args& a, const AttnParams& p, const PCtrl& ctrl, int64_t u0, int64_t u1) {
+  using C = PCfg<D>;
+  Walk walk = walk_from(p, ctrl.b, ctrl.w, ctrl.off, u0, u1 - u0);
+  for (int nth = 0; next_run(a, p, walk); ++nth) {
+    if ((ctrl.alone >> min(nth, 31) & 1) == 0) continue;
+    const Seq& s = walk.w.s;
+    const int from = (walk.lo / kT + walk.tile) * kT;
+    float* slot = p.part + static_cast<int64_t>(2 * blockIdx.x + (nth > 0)) * C::kSlot;
+    for (int rg = threadIdx.x >> 5; rg < kGroup; rg += kSoftWarps) {
+      const int r = walk.group * kGroup + rg;
+      if (r >= s.rows * p.G) break;
+      float m, l, v[D / 32];
+      one_row<D>(a, p, s, walk.seq, walk.kvh, r, from, min(from + walk.n * kT, walk.hi), &g_err_kv4prompt, 51, m, l, v);
+      store_one_row<D>(p, s, walk.kvh, r, m, l, v, walk.n == walk.all ? nullptr : slot, rg, kGroup);
+    }
+  }
+}
+
 template <int D, int BS>
 __global__ void __launch_bounds__(kPThreads, 1)
-    kv4_prompt_kernel(const Args a, const AttnParams p) {
+    kv4_prompt_kernel(const __grid_constant__ Args a, const __grid_constant__ AttnParams p) {
   using C = PCfg<D>;
   constexpr int kSB = D / BS;
   constexpr uint32_t kTileBytes = C::kTileBytes;
@@ -402,6 +458,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       mbar_init(smem_u32(&ctrl.raw_empty[i]), kFillWarps);
     }
     ctrl.abort = 0;
+    ctrl.alone = 0;
     ctrl.b = -1;
     fence_mbar_init();
   }
@@ -649,6 +706,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
       for (int buf = 0; buf < 2; ++buf)
         warp_wait(smem_u32(&ctrl.o_done[i][buf]), ((s_phase >> buf) & 1) ^ 1u, abort, 50);
       tc_fence_after();
+      // rows that are taken by themselves later are stored there alone
+      const bool stored = r < all_rows && (*const_cast<volatile uint32_t*>(&ctrl.alone) >> min(nth, 31) & 1) == 0;
       // sums stand for value * 2^(ref_v - 127 - 13), weights and sums both times 2^7
       const bool complete = run.n == run.all;
       const float inv = complete ? (l != 0.f ? 1.f / l : 0.f) : 1.f / 128.f;
@@ -664,7 +723,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         float v[32];
 #pragma unroll
         for (int x = 0; x < 32; ++x) v[x] = __uint_as_float(s[x]) * inv * fa * fb;
-        if (r < all_rows) {
+        if (stored) {
           if (complete) {
             uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + 32 * c);
 #pragma unroll
@@ -685,7 +744,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
       }
       tc_fence_before();  // the next run's products overwrite these sums
-      if (r < all_rows) {
+      if (stored) {
         const float lt = l * (1.f / 128.f);
         if (complete) {
           if (p.lse != nullptr) p.lse[orow] = lt != 0.f ? m * kLn2 + logf(lt) : -INFINITY;
@@ -703,6 +762,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctrl.run_empty[nth % kRuns]));
     }
+    meet<kSoftWarps>(5);  // every tile has been filled: the upper rows' warps may be ahead of the others
+    if (*const_cast<volatile uint32_t*>(&ctrl.alone) != 0) runs_by_rows<D>(a, p, ctrl, u0, u1);
   } else if (warp < kMmaWarp) {
     // ---------------------------------------------- codes to binary16 tiles
     regs_dec<kFillRegs>();
@@ -718,6 +779,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
       for (int x = 0; x < kSB; ++x) t = max(t, (w >> (8 * x)) & 0xFFu);
       return t;
     };
+    // 255 less the smallest byte that is not 0, or 0
+    auto low_of = [](uint32_t w) {
+      uint32_t t = 0;
+#pragma unroll
+      for (int x = 0; x < kSB; ++x) t = max(t, (255u - ((w >> (8 * x)) & 0xFFu)) % 255u);
+      return t;
+    };
     // A token with a block that is not finite (scale byte 255), keys or values: its
     // keys become NaN operands, so that exactly the rows that read it get a weight
     // that is not a number; its values become zeros.
@@ -729,6 +797,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const uint32_t row_at = tiles + static_cast<uint32_t>(tk) * 128u;
     const uint32_t swz = static_cast<uint32_t>(tk & 7) << 4;
     int ref_v = 13;
+    int common_v = 13;  // the same over the tiles that every row reads whole
     for (int count = 0, rs = values ? 1 : 0, rp = 0;; ++count) {
       const int stage = count & 1;
       if (fw == 3) {  // polling warps on different schedulers
@@ -748,6 +817,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
       // the values' too, for the softmax
       const uint32_t own = __reduce_max_sync(0xffffffffu, top_of(clean(word)));
       uint32_t other = 0;
+      // whether what only some rows read may be too far above the rest (kv4.cuh, kSpread)
+      const bool spread = (info.w & 4) || (values && !(info.w & 1) && ref_v > common_v);
+      const uint32_t low = spread ? __reduce_max_sync(0xffffffffu, low_of(clean(word))) : 0u;
       if (values) {
         word = clean(word);
       } else {
@@ -761,19 +833,28 @@ __global__ void __launch_bounds__(kPThreads, 1)
         c[x] = ld_shared16(raw + tk * (D / 2) + (((x + (tk >> 1)) & (D / 32 - 1)) << 4));
       __syncwarp();  // the warp has read the stage
       if (lane == 0) {
-        ctrl.top[values][stage][fw] = static_cast<int>(own | (other << 8));
+        ctrl.top[values][stage][fw] = static_cast<int>(own | (other << 8) | (low << 16));
         mbar_arrive(smem_u32(&ctrl.raw_empty[rs]));
       }
       if (fw == 3) idle_wait(empty + 8 * stage, ((count >> 1) & 1) ^ 1u, abort, 52);
       meet<kFillWarps>(3 + values);
-      int top = 0, top_v = 0;
+      int top = 0, top_v = 0, bottom = 255;
 #pragma unroll
       for (int x = 0; x < kFillWarps; ++x) {
         const int t = ctrl.top[values][stage][x];
         top = max(top, t & 0xFF);
-        top_v = max(top_v, values ? t & 0xFF : t >> 8);
+        top_v = max(top_v, values ? t & 0xFF : (t >> 8) & 0xFF);
+        bottom = min(bottom, 255 - (t >> 16));
       }
+      const int before = ref_v;
       ref_v = max((info.w & 1) ? 13 : ref_v, top_v);
+      bool alone = spread && top - bottom > kSpread;
+      if (values) {
+        const bool first = info.w & 1, cut = info.w & 4;
+        common_v = max(first ? 13 : common_v, cut ? 13 : top_v);
+        alone = (cut && !first && ref_v - before > kSpread) || (spread && ref_v > common_v && ref_v - bottom > kSpread);
+      }
+      if (alone && tk == 0) atomicOr(&ctrl.alone, 1u << (info.w >> 8));
       const int ref = values ? ref_v : max(top, 13);
       if (tk == 0 && !values) {
         ctrl.k_info[count & 3] = pow2w(ref - 140);
@@ -918,6 +999,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const Run& run = ctrl.run[nth % kRuns];
         if (__any_sync(0xffffffffu, run.stop || *abort)) break;
         const int n_tiles = run.n, lo = run.lo, hi = run.hi, kvh = run.kvh;
+        const int common_lo = run.common_lo, common_hi = run.common_hi;
         const int* table = a.table + static_cast<int64_t>(run.seq) * a.max_pages;
         int tok0 = (lo / kT + run.tile) * kT;
         __syncwarp();
@@ -941,7 +1023,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             idle_wait(smem_u32(&ctrl.raw_empty[rs]), rp, abort, 61);
             const uint32_t bar = smem_u32(&ctrl.raw_full[rs]);
             if (lane == 0) {
-              ctrl.raw_info[rs] = make_int4(tok0, lo, hi, k == 0);
+              const bool cut = max(tok0, lo) < common_lo || min(tok0 + kT, hi) > common_hi;
+              ctrl.raw_info[rs] = make_int4(tok0, lo, hi, (k == 0) | cut << 2 | min(nth, 31) << 8);
               mbar_arrive_expect_tx(bar, total);
             }
             __syncwarp();
@@ -962,21 +1045,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
     } else if (warp == kWalkWarp && lane == 0) {
       // ------------------------------------------------ the range's runs
-      Walk walk;
-      walk.b = ctrl.b;
-      walk.w = ctrl.w;
-      const int64_t per_head = head_units(p, walk.w);
-      const int len = pair_units(p, walk.w);
-      // (64-bit divisions are slow, and everyone waits for the first run)
-      walk.head = ctrl.off >> 32 || per_head >> 32
-                      ? static_cast<int>(ctrl.off / per_head)
-                      : static_cast<int>(static_cast<uint32_t>(ctrl.off) / static_cast<uint32_t>(per_head));
-      const int64_t in_head = ctrl.off - walk.head * per_head;
-      const int64_t pair = in_head >> 32 ? in_head / len : static_cast<uint32_t>(in_head) / static_cast<uint32_t>(len);
-      walk.pair = static_cast<int>(min(pair, static_cast<int64_t>(walk.w.groups / 2)));
-      walk.off = static_cast<int>(in_head - static_cast<int64_t>(walk.pair) * len);
-      walk.at = u0;
-      walk.left = u1 - u0;
+      Walk walk = walk_from(p, ctrl.b, ctrl.w, ctrl.off, u0, u1 - u0);
       for (int nth = 0, more = 1; more; ++nth) {
         more = next_run(a, p, walk);
         mbar_wait(smem_u32(&ctrl.run_empty[nth % kRuns]), ((nth / kRuns) & 1) ^ 1, abort, &g_err_kv4prompt, 66);
@@ -987,6 +1056,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           run.groups = walk.w.groups, run.group = walk.group, run.seq = walk.seq, run.kvh = walk.kvh;
           run.lo = walk.lo, run.hi = walk.hi, run.tile = walk.tile, run.n = walk.n, run.all = walk.all;
           run.unit = walk.unit;
+          common_tokens(p, walk.w.s, walk.group, run.common_lo, run.common_hi);
         }
         mbar_arrive(smem_u32(&ctrl.run_full[nth % kRuns]));
       }

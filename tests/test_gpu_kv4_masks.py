@@ -1,8 +1,12 @@
 """Attention over the 4-bit cache (rnl_kv4_attention): what the mask leaves out.
-Pages in front of a window may have been freed."""
+Pages in front of a window may have been freed, and tokens that a row does not
+read, of whatever size, leave it alone."""
+import math
+
 import pytest
 import torch
 
+import kv4_plain as plain
 from test_gpu_kv4 import filled, gen, i32, randn, wide
 
 pytestmark = pytest.mark.gpu
@@ -42,3 +46,88 @@ def test_pages_in_front_of_a_window_may_be_gone(D, page, rows):
                 out = rnl.rnl_kv4_attention(q, c, freed, i32(lens), cu, window=window)
                 rnl.rnl_check_device_error()
                 assert torch.equal(out, want)
+
+
+def reference(q, c, t, lens, cu, window):
+    """(out, lse, their bounds) in 64 bits.  The bounds are kv4_plain's (2^-8 of the
+    output, 2^-11 + 2^-18 + 2 delta of sum p |v| / l, 2^-36 of the largest value),
+    with delta and the largest value over the tokens that the row reads."""
+    o, z, _, _ = plain.attention(q, c, t, i32(lens), i32(cu), window=window)
+    tol, ltol = torch.full_like(o, math.nan), torch.full_like(z, math.nan)
+    T, Hq, D = q.shape
+    G, scale = Hq // c.n_kv_heads, D ** -0.5
+    for b, n in enumerate(lens):
+        r = cu[b + 1] - cu[b]
+        rows = slice(cu[b], cu[b + 1])
+        pos = torch.arange(n - r, n, device=q.device)[:, None]
+        j = torch.arange(n, device=q.device)[None]
+        see = (j <= pos) & ((j > pos - window) if window else True)
+        for h in range(Hq):
+            k, v = plain.sequence(c, t[b], n, h // G)
+            k, v = k.nan_to_num(0, 0, 0), v.nan_to_num(0, 0, 0)  # (rows that read those are looked at apart)
+            qd = q[rows, h].double()
+            p = torch.softmax((qd @ k.t() * scale).masked_fill(~see, -math.inf), -1)
+            delta = (D * 2.0 ** -23 * scale * (qd.abs() @ k.abs().t())).masked_fill(~see, 0).amax(-1, keepdim=True)
+            top = torch.where(see, v.abs().amax(-1)[None], 0.0).amax(-1, keepdim=True)
+            tol[rows, h] = (2.0 ** -8 * o[rows, h].abs() + (2.0 ** -11 + 2.0 ** -18 + 2 * delta) * (p @ v.abs()) +
+                            2.0 ** -36 * top)
+            ltol[rows, h] = delta[:, 0] + 2.0 ** -20 * z[rows, h].abs().clamp_min(1)
+    return o, z, tol, ltol
+
+
+def check(q, c, t, lens, cu, window, ref, skip=None):
+    o, z, tol, ltol = ref
+    for tt in (t, wide(t, c.page_size)):  # both kernels where there are many rows
+        out, lse = torch.full_like(q, 320.0), torch.full(q.shape[:2], 123.0, device="cuda")
+        rnl.rnl_kv4_attention(q, c, tt, i32(lens), i32(cu), out=out, lse_out=lse, window=window)
+        rnl.rnl_check_device_error()
+        ok = ((out.double() - o).abs() <= tol).all(-1) & ((lse.double() - z).abs() <= ltol)
+        if skip is not None:
+            assert out[skip].isnan().all() and lse[skip].isnan().all()
+            ok = ok | skip
+        assert ok.all(), f"{int((~ok).sum())} of {ok.numel()} rows, first {(~ok).nonzero()[0].tolist()}"
+
+
+def louder(c, t, head, side, tok, up):
+    """That token's keys or values times 2^up."""
+    getattr(c, side + "_scales")[int(t[0, tok // c.page_size]), head, tok % c.page_size] += up
+
+
+@pytest.mark.parametrize("D,block", [(64, 32), (128, 32), (128, 64), (256, 64)])
+@pytest.mark.parametrize("rows,G", [(2, 1), (3, 4), (4, 4), (8, 2), (60, 1), (130, 2), (300, 1), (140, 8)])
+@pytest.mark.parametrize("window", [0, 90])
+@pytest.mark.parametrize("up", [60, 120])
+def test_large_tokens_reach_only_the_rows_that_read_them(D, block, rows, G, window, up):
+    """Keys and values 2^60 and 2^120 times the others, among the rows' own tokens
+    and at the front of a window: a row that does not read one gets what it would
+    get without it, to the bound of its own tokens."""
+    g = gen(D + rows + window + up)
+    n, H = 450, 2
+    lens, cu = [n, 333], [0, rows, rows + 2]
+    c, t = filled(g, lens, H, 32, D, block)
+    marks = [(0, "k", n - 1), (0, "v", n - max(1, rows // 2)), (1, "v", n - 1)]
+    if window:
+        marks += [(0, "k", n - rows - window + 1), (1, "v", n - rows - window + 1), (1, "k", n - rows - window)]
+    for h, side, tok in marks:
+        louder(c, t, h, side, tok, up)
+    q = randn(g, rows + 2, G * H, D).bfloat16()
+    check(q, c, t, lens, cu, window, reference(q, c, t, lens, cu, window))
+
+
+@pytest.mark.parametrize("D,rows,G", [(64, 5, 2), (128, 5, 4), (256, 5, 1), (128, 200, 4), (64, 200, 1)])
+def test_large_and_not_finite_tokens_together(D, rows, G):
+    """A token that is far larger than the others and one that is not finite: rows
+    that read the second get NaN, the others are right."""
+    g = gen(D + rows)
+    n = 400
+    for side in ("k", "v"):
+        c, t = filled(g, [n], 1, 16, D, 32)
+        louder(c, t, 0, "k", n - 1, 70)
+        louder(c, t, 0, "v", n - 2, 70)
+        tok = n - 3
+        bad = torch.zeros(rows, G, dtype=torch.bool, device="cuda")
+        bad[rows - 3:] = True
+        q = randn(g, rows, G, D).bfloat16()
+        ref = reference(q, c, t, [n], [0, rows], 0)  # without the second
+        getattr(c, side + "_scales")[int(t[0, tok // 16]), 0, tok % 16, 1] = 255
+        check(q, c, t, [n], [0, rows], 0, ref, skip=bad)
