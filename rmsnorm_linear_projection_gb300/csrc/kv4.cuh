@@ -234,6 +234,12 @@ __device__ __forceinline__ void store_row(const AttnParams& p, const Seq& s, int
 // such an item's rows are computed by one_row instead.
 constexpr int kSpread = 36;
 
+// So are rows with scores this large (in log2 units): the exponents of their
+// weights come from one FMA, score times factor less the rounded maximum, which
+// is half a step of the maximum off, from here on enough to take the largest
+// weight out of binary16 or to nothing.
+constexpr float kTopScore = 4194304.f;
+
 // A warp computes row r of key head kvh over the tokens of [lo, hi) that it
 // reads, in FP32 straight from the cache: a token a lane for the scores, D / 32
 // dims a lane for the sums v.  m is the maximum in log2 units, l the sum of the

@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     constexpr int kTpr = D / 8;  // threads a row, 8 dims each
     for (int x = tid; x < kRows * kTpr; x += kThreads) {
       const int r = x / kTpr, d = (x - r * kTpr) * 8;
-      if (r0 + r >= all_rows || (MIXED && (sh_alone >> min(seg, 31) & 1))) continue;
+      if (r0 + r >= all_rows || (sh_alone >> min(seg, 31) & 1)) continue;
       float mm = -INFINITY, ll = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[w][0][r]);
@@ -774,6 +774,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
         v[0] += y.x, v[1] += y.y, v[2] += y.z, v[3] += y.w;
         v[4] += z.x, v[5] += z.y, v[6] += z.z, v[7] += z.w;
       }
+      // scores that the steps of 15 - maximum are too coarse for: a weight may have
+      // left binary16 (the sums are not finite then) or vanished
+      if (d == 0 && (!(fabsf(v[0]) < INFINITY) || (fabsf(mm) >= kTopScore && mm != -INFINITY)))
+        atomicOr(&sh_alone, 1u << min(seg, 31));
       if (complete) {
         store_row<D>(p, cur.w.s, kvh, r0 + r, d, v, mm, ll);
       } else {
@@ -798,8 +802,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     at += seg_tiles + kItemCost;
     skip<D, NT>(a, p, cur, seg_tiles);
   }
-  if (MIXED) __syncthreads();
-  if (MIXED && sh_alone != 0)
+  __syncthreads();
+  if (sh_alone != 0)
     segments_by_rows<D, NT>(a, p, sh_b, sh_w, sh_off, u0, u1, sh_alone);
   grid_dependency_wait();
 }

@@ -595,6 +595,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (lane == 0) mbar_arrive(smem_u32(&ctrl.q_full[i]));
 
       float m = -INFINITY, l = 0.f;
+      bool large = false;
       int ref_v = 13;
       int tok0 = (run.lo / kT + run.tile) * kT;
       for (int u = 0; u < 2 * n_tiles; ++u, tok0 += kU) {
@@ -638,6 +639,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 alpha = ex2(m - top);
                 m = top;
                 l *= alpha;
+                large |= fabsf(top) >= kTopScore;
               }
             }
             const float bias = kTop - (m == -INFINITY ? 0.f : m);
@@ -706,6 +708,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       for (int buf = 0; buf < 2; ++buf)
         warp_wait(smem_u32(&ctrl.o_done[i][buf]), ((s_phase >> buf) & 1) ^ 1u, abort, 50);
       tc_fence_after();
+      if (large && r < all_rows) atomicOr(&ctrl.alone, 1u << min(nth, 31));
       // rows that are taken by themselves later are stored there alone
       const bool stored = r < all_rows && (*const_cast<volatile uint32_t*>(&ctrl.alone) >> min(nth, 31) & 1) == 0;
       // sums stand for value * 2^(ref_v - 127 - 13), weights and sums both times 2^7

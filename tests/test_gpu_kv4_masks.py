@@ -114,6 +114,21 @@ def test_large_tokens_reach_only_the_rows_that_read_them(D, block, rows, G, wind
     check(q, c, t, lens, cu, window, reference(q, c, t, lens, cu, window))
 
 
+@pytest.mark.parametrize("D,rows,G,n", [(128, 4, 4, 9000), (64, 7, 1, 5000), (256, 30, 2, 3000), (128, 400, 4, 5000),
+                                        (64, 90, 8, 7000)])
+@pytest.mark.parametrize("window", [0, 1500])
+@pytest.mark.parametrize("side", ["k", "v"])
+def test_large_tokens_of_items_that_are_cut(D, rows, G, n, window, side):
+    """One long sequence whose items several CTAs share: only some of the pieces
+    hold a tile with such a token, and the pieces still join."""
+    g = gen(n + rows + window)
+    c, t = filled(g, [n], 1, 64, D, 32)
+    louder(c, t, 0, side, n - 1, 80)
+    louder(c, t, 0, side, n - rows - (window or rows) + 1, 50)
+    q = randn(g, rows, G, D).bfloat16()
+    check(q, c, t, [n], [0, rows], window, reference(q, c, t, [n], [0, rows], window))
+
+
 @pytest.mark.parametrize("D,rows,G", [(64, 5, 2), (128, 5, 4), (256, 5, 1), (128, 200, 4), (64, 200, 1)])
 def test_large_and_not_finite_tokens_together(D, rows, G):
     """A token that is far larger than the others and one that is not finite: rows
@@ -131,3 +146,79 @@ def test_large_and_not_finite_tokens_together(D, rows, G):
         ref = reference(q, c, t, [n], [0, rows], 0)  # without the second
         getattr(c, side + "_scales")[int(t[0, tok // 16]), 0, tok % 16, 1] = 255
         check(q, c, t, [n], [0, rows], 0, ref, skip=bad)
+
+
+@pytest.mark.parametrize("rows", [6, 150])
+def test_small_early_values_under_large_later_ones(rows):
+    """Values and keys that grow by 2^140 along the rows' own tokens: every row to
+    the bound of what it reads."""
+    g = gen(rows)
+    n, D = 600, 128
+    c, t = filled(g, [n], 1, 32, D, 32)
+    for tok in range(n):
+        up = 0 if tok < n - rows else 140 * (tok - (n - rows)) // rows
+        for side in ("k", "v"):
+            s = getattr(c, side + "_scales")
+            at = (int(t[0, tok // 32]), 0, tok % 32)
+            s[at] = (s[at].int() - 30 + up).clamp(1, 250).to(torch.uint8)
+    q = (randn(g, rows, 4, D) * 2.0 ** -20).bfloat16()
+    check(q, c, t, [n], [0, rows], 0, reference(q, c, t, [n], [0, rows], 0))
+
+
+@pytest.mark.parametrize("D,Hkv,G", [(64, 1, 4), (128, 2, 4), (128, 1, 16), (256, 1, 2)])
+@pytest.mark.parametrize("rows", [1, 4, 150])
+@pytest.mark.parametrize("scale", [1e5, -1e8, 1e14, 1e30])
+def test_large_scores(D, Hkv, G, rows, scale):
+    """Scores of 10^6 to 10^31: finite, and where one token's score is ahead of all
+    others by more than the scores' own error (D 2^-23 scale sum |q k| each) and
+    another 100, the output is that token's values and lse its score."""
+    g = gen(D + rows)
+    lens, cu = [700, 45], [0, rows, rows + 1]
+    c, t = filled(g, lens, Hkv, 32, D, 32)
+    q = randn(g, rows + 1, Hkv * G, D).bfloat16()
+    for causal, tt in ((True, t), (False, t), (True, wide(t, 32)), (False, wide(t, 32))):
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+        rnl.rnl_kv4_attention(q, c, tt, i32(lens), i32(cu), scale=scale, causal=causal, out=out, lse_out=lse)
+        rnl.rnl_check_device_error()
+        assert out.isfinite().all() and lse.isfinite().all()
+        clear = 0
+        for b, n in enumerate(lens):
+            r = cu[b + 1] - cu[b]
+            pos = torch.arange(n - r, n, device="cuda")[:, None]
+            see = (torch.arange(n, device="cuda")[None] <= pos) if causal else torch.ones(r, n, dtype=torch.bool, device="cuda")
+            for h in range(Hkv * G):
+                k, v = plain.sequence(c, t[b], n, h // G)
+                qd = q[cu[b]:cu[b + 1], h].double()
+                s = (qd @ k.t() * scale).masked_fill(~see, -math.inf)
+                delta = (D * 2.0 ** -23 * abs(scale) * (qd.abs() @ k.abs().t())).amax(-1)
+                top = s.topk(2, -1)
+                ok = top.values[:, 0] - top.values[:, 1] > 2 * delta + 100
+                clear += int(ok.sum())
+                want = v[top.indices[:, 0]]
+                assert ((out[cu[b]:cu[b + 1], h].double() - want).abs() <= 2.0 ** -8 * want.abs())[ok].all()
+                off = (lse[cu[b]:cu[b + 1], h].double() - top.values[:, 0]).abs()
+                assert (off <= delta + 2.0 ** -20 * top.values[:, 0].abs())[ok].all()
+        assert clear > (rows + 1) * Hkv * G // 2
+
+
+@pytest.mark.parametrize("rows,n", [(1, 300), (1, 9000), (4, 9000), (200, 3000)])
+@pytest.mark.parametrize("scale", [1.0, 1e12, -1e25])
+def test_equal_scores_of_any_size(rows, n, scale):
+    """Equal keys: every token the same weight, the mean of the values, whatever the
+    score is (the same sum for every token, in the same order)."""
+    g = gen(rows + n)
+    D = 128
+    c, t = filled(g, [n], 1, 64, D, 32)
+    for x in (c.k_codes, c.k_scales):
+        x[:] = x[0, 0, 0].clone()
+    c.k_scales.clamp_(100, 130)
+    q = randn(g, rows, 4, D).bfloat16()
+    v = plain.sequence(c, t[0], n, 0)[1]
+    for tt in (t, wide(t, 64)):
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+        rnl.rnl_kv4_attention(q, c, tt, i32([n]), i32([0, rows]), scale=scale, causal=False, out=out, lse_out=lse)
+        rnl.rnl_check_device_error()
+        want, size = v.mean(0), v.abs().mean(0)
+        # 2^-8 for the output, 2^-11 of sum p |v| for the weights, 2^-18 for the sums
+        assert ((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2.0 ** -18) * size).all()
+        assert lse.isfinite().all()
