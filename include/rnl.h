@@ -330,8 +330,8 @@ rnl_status rnl_kv4_gather(const rnl_kv4_cache *cache, const rnl_kv4_seqs *seqs, 
  * down to 2^-31 of the row's largest.  The softmax weights are rounded to
  * binary16: 11 bits, for weights of at least 2^-21 of the row's largest, fewer
  * below.  Where tokens that only some rows of a call read are 2^36 times others,
- * or scores (times log2 e) reach 2^22 in size,
- * the rows concerned are computed one at a time in FP32, which takes much longer.
+ * or scores (times log2 e) reach 2^22 in size, the rows concerned are computed
+ * one at a time in FP32, which takes much longer.
  * Workspace: rnl_workspace_size(RNL_OP_KV4_ATTENTION, n_rows, head_dim,
  * n_q_heads, n_kv_heads) bytes; results do not depend on its contents.  Calls
  * that may run at the same time (other streams, other graphs) need one each.

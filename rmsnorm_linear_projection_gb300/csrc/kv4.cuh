@@ -182,6 +182,14 @@ __device__ __forceinline__ bool quick_wait(uint32_t bar, uint32_t parity, volati
   return ok != 0 || mbar_wait(bar, parity, abort, err, site);
 }
 
+// After a wait has given up: what the CTA still has in flight is waited for all
+// the same (with a limit of its own), before its shared memory or TMEM goes back.
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+  const unsigned long long t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > kWaitLimitNs) return;
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));

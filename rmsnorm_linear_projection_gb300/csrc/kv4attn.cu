@@ -359,6 +359,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     locate();
   }
 
+  bool gave_up = false;  // a wait of this warp ran out: it fetches no more and runs to its end, phase as it was
   int done = 0;      // tiles of the range before the current segment
   int seg = 0;
   while (cur.left > 0) {
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
           }
         return top();
       };
-      quick_wait(bar_k, phase & 1, &sh_abort, &g_err_kv4attn, 47);
+      gave_up |= !quick_wait(bar_k, phase & 1, &sh_abort, &g_err_kv4attn, 47);
       float s[T8][MS][4];
       float f_tile = 0.f;
       if (any) {
@@ -564,10 +565,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
         }
       }
       __syncwarp();  // every lane has read the keys
-      const bool more = ahead.left > 0;
+      bool more = __all_sync(0xffffffffu, ahead.left > 0 && !gave_up);
       if (more) fetch_keys();
-      quick_wait(bar_v, phase & 1, &sh_abort, &g_err_kv4attn, 47);
-      phase ^= 1u;
+      gave_up |= !quick_wait(bar_v, phase & 1, &sh_abort, &g_err_kv4attn, 47);
+      more = __all_sync(0xffffffffu, more && !gave_up);
+      phase ^= gave_up ? 0u : 1u;
       if (any) {
         // ---- softmax over the tile
         int low;
@@ -801,6 +803,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     ++seg;
     at += seg_tiles + kItemCost;
     skip<D, NT>(a, p, cur, seg_tiles);
+  }
+  if (gave_up) {  // keys and values of that tile, and the next one's keys if they were asked for
+    drain_wait(bar_k, phase & 1);
+    drain_wait(bar_v, phase & 1);
+    drain_wait(bar_k, (phase & 1) ^ 1u);
   }
   __syncthreads();
   if (sh_alone != 0)

@@ -255,6 +255,7 @@ struct __align__(16) PCtrl {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t raw_full[kMaxRing], raw_empty[kMaxRing];
   uint64_t run_full[kRuns], run_empty[kRuns];
+  uint64_t drained[2];          // a row tile's products, after a wait has given up
   Run run[kRuns];
   // first token, the group's tokens, 1: a run's first tile, 2: no more tiles, 4: with
   // tokens that only some of the rows read; the run's number (up to 31) from bit 8 on
@@ -340,18 +341,17 @@ __device__ __forceinline__ void tmem_st_32cols(uint32_t taddr, const uint32_t (&
       : "memory");
 }
 
-__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t site) {
-  quick_wait(bar, parity, abort, &g_err_kv4prompt, site);
-  __syncwarp();
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t site) {
+  return __all_sync(0xffffffffu, quick_wait(bar, parity, abort, &g_err_kv4prompt, site));
 }
 
 // The same for waits with slack: the warp sleeps between polls.
-__device__ __forceinline__ void idle_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t site) {
+__device__ __forceinline__ bool idle_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t site) {
   for (int n = 0; n < 64; ++n) {
     if (mbar_try_wait(bar, parity)) break;
     __nanosleep(64);
   }
-  warp_wait(bar, parity, abort, site);
+  return warp_wait(bar, parity, abort, site);
 }
 
 // Named barriers.  A warp that polls takes issue slots from those that work:
@@ -448,6 +448,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       mbar_init(smem_u32(&ctrl.k_empty[i]), 2);
       mbar_init(smem_u32(&ctrl.v_full[i]), kFillWarps);
       mbar_init(smem_u32(&ctrl.v_empty[i]), 2);
+      mbar_init(smem_u32(&ctrl.drained[i]), 1);
     }
     for (int i = 0; i < kRuns; ++i) {
       mbar_init(smem_u32(&ctrl.run_full[i]), 1);
@@ -978,7 +979,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
         count += n_tiles;
       }
       // the last arrival on this CTA's barriers
-      if (count > 0) wait(&ctrl.v_empty[(count - 1) & 1], ((count - 1) >> 1) & 1, 59);
+      if (ok && count > 0) wait(&ctrl.v_empty[(count - 1) & 1], ((count - 1) >> 1) & 1, 59);
+      if (!ok) {  // whatever has been issued
+        if (elect_one()) umma_commit(smem_u32(&ctrl.drained[i]));
+        __syncwarp();
+        drain_wait(smem_u32(&ctrl.drained[i]), 0);
+      }
     } else if (warp == kLoadWarp) {
       // ------------------------------------------------ codes from the pages
       // A bulk copy a lane: of a page's codes, scales or (with the keys) the
@@ -997,10 +1003,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
           rp ^= 1u;
         }
       };
-      for (int nth = 0;; ++nth) {
-        idle_wait(smem_u32(&ctrl.run_full[nth % kRuns]), (nth / kRuns) & 1, abort, 65);
+      bool ok = true;
+      for (int nth = 0; ok; ++nth) {
+        ok = idle_wait(smem_u32(&ctrl.run_full[nth % kRuns]), (nth / kRuns) & 1, abort, 65);
         const Run& run = ctrl.run[nth % kRuns];
-        if (__any_sync(0xffffffffu, run.stop || *abort)) break;
+        if (!ok || run.stop) break;
         const int n_tiles = run.n, lo = run.lo, hi = run.hi, kvh = run.kvh;
         const int common_lo = run.common_lo, common_hi = run.common_hi;
         const int* table = a.table + static_cast<int64_t>(run.seq) * a.max_pages;
@@ -1012,18 +1019,19 @@ __global__ void __launch_bounds__(kPThreads, 1)
           return chunk_at < kT && tok < hi && tok + chunk_tokens > lo ? __ldg(table + (tok >> a.page_shift)) : -2;
         };
         int page = page_of(tok0);
-        for (int k = 0; k < n_tiles; ++k, tok0 += kT) {
+        for (int k = 0; k < n_tiles && ok; ++k, tok0 += kT) {
           const int next = k + 1 < n_tiles ? page_of(tok0 + kT) : -2;  // a tile early
-          const bool ok = page >= 0 && page < a.n_pages;
-          if (!ok && page != -2) atomicCAS(&g_err_kv4prompt, 0u, kErrArg | (51u << 8));
+          const bool there = page >= 0 && page < a.n_pages;
+          if (!there && page != -2) atomicCAS(&g_err_kv4prompt, 0u, kErrArg | (51u << 8));
           const int64_t row = ((static_cast<int64_t>(page) * a.Hkv + kvh) << a.page_shift) +
                               ((tok0 + chunk_at) & (a.page - 1));
 #pragma unroll
           for (int v = 0; v < 2; ++v) {  // keys, values
-            const bool mine = ok && what < (v ? 2 : 3);
+            const bool mine = there && what < (v ? 2 : 3);
             const uint8_t* src = what == 0 ? (v ? a.v.codes : a.k.codes) : (v || what == 2 ? a.v.scales : a.k.scales);
             const uint32_t total = __reduce_add_sync(0xffffffffu, mine ? bytes : 0u);
-            idle_wait(smem_u32(&ctrl.raw_empty[rs]), rp, abort, 61);
+            ok = idle_wait(smem_u32(&ctrl.raw_empty[rs]), rp, abort, 61);
+            if (!ok) break;
             const uint32_t bar = smem_u32(&ctrl.raw_full[rs]);
             if (lane == 0) {
               const bool cut = max(tok0, lo) < common_lo || min(tok0 + kT, hi) > common_hi;
@@ -1038,20 +1046,25 @@ __global__ void __launch_bounds__(kPThreads, 1)
           page = next;
         }
       }
-      for (int v = 0; v < 2; ++v) {
-        idle_wait(smem_u32(&ctrl.raw_empty[rs]), rp, abort, 61);
+      for (int v = 0; v < 2 && ok; ++v) {
+        ok = idle_wait(smem_u32(&ctrl.raw_empty[rs]), rp, abort, 61);
+        if (!ok) break;
         if (lane == 0) {
           ctrl.raw_info[rs] = make_int4(0, 0, 0, 2);
           mbar_arrive(smem_u32(&ctrl.raw_full[rs]));
         }
         stage_up();
       }
+      if (!ok)  // the last copies of every place, of this round or the one before
+        for (int x = 0; x < kRing; ++x) drain_wait(smem_u32(&ctrl.raw_full[x]), x < rs ? rp ^ 1u : rp);
     } else if (warp == kWalkWarp && lane == 0) {
       // ------------------------------------------------ the range's runs
       Walk walk = walk_from(p, ctrl.b, ctrl.w, ctrl.off, u0, u1 - u0);
       for (int nth = 0, more = 1; more; ++nth) {
         more = next_run(a, p, walk);
-        mbar_wait(smem_u32(&ctrl.run_empty[nth % kRuns]), ((nth / kRuns) & 1) ^ 1, abort, &g_err_kv4prompt, 66);
+        // (a run that is still read must not change: the others end by `abort`)
+        if (!mbar_wait(smem_u32(&ctrl.run_empty[nth % kRuns]), ((nth / kRuns) & 1) ^ 1, abort, &g_err_kv4prompt, 66))
+          break;
         Run& run = ctrl.run[nth % kRuns];
         run.stop = !more;
         if (more) {
