@@ -800,6 +800,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // number: reads and writes free of bank conflicts.
     const uint32_t row_at = tiles + static_cast<uint32_t>(tk) * 128u;
     const uint32_t swz = static_cast<uint32_t>(tk & 7) << 4;
+    const uint32_t zero = static_cast<uint32_t>(p.causal) >> 1;
     int ref_v = 13;
     int common_v = 13;  // the same over the tiles that every row reads whole
     for (int count = 0, rs = values ? 1 : 0, rp = 0;; ++count) {
@@ -835,8 +836,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
       for (int x = 0; x < D / 32; ++x)
         c[x] = ld_shared16(raw + tk * (D / 2) + (((x + (tk >> 1)) & (D / 32 - 1)) << 4));
-      __syncwarp();  // the warp has read the stage
-      if (lane == 0) {
+      // The warp has read the place once the codes are in registers.  Program order
+      // alone does not see to that: the loads may be moved to where the codes are
+      // used, past the arrival, and then read what the next copy brings.  So the
+      // arrival depends on them (`zero` is 0, which the compiler does not know).
+      uint32_t read = info.w;
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) read |= c[x].x | c[x].y | c[x].z | c[x].w;
+      const bool done = __all_sync(0xffffffffu, (read & zero) == 0);
+      if (lane == 0 && done) {
         ctrl.top[values][stage][fw] = static_cast<int>(own | (other << 8) | (low << 16));
         mbar_arrive(smem_u32(&ctrl.raw_empty[rs]));
       }
