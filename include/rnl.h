@@ -112,8 +112,8 @@ int rnl_version(void);
  * 1 for a debug build (compiled with RNL_DEBUG), 0 otherwise.  A debug build
  * computes the same results and additionally checks, on the device, every
  * shared-memory stage offset, TMEM column range, workspace record or flag
- * index and output index of its GEMM, norm-pass and skinny kernels before
- * use; a failed check skips that access, and rnl_check_device_error() then
+ * index and output index of its GEMM, norm-pass and skinny kernels, and of the
+ * multi-axis rotary, 4-bit cache and attention kernels, before use; a failed check skips that access, and rnl_check_device_error() then
  * returns RNL_ERR_BOUNDS with the check's site.  No kernel traps.
  */
 int rnl_debug_build(void);

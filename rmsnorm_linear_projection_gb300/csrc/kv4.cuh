@@ -111,6 +111,11 @@ __device__ __forceinline__ int64_t token_row(const Args& a, int b, int pos, int 
   return ((static_cast<int64_t>(p) * a.Hkv + head) << a.page_shift) + (pos & (a.page - 1));
 }
 
+// Whether n tokens from cache row `row` on lie in the cache (for the debug build's checks).
+__device__ __forceinline__ bool in_cache(const Args& a, int64_t row, int n) {
+  return row >= 0 && row + n <= (static_cast<int64_t>(a.n_pages) * a.Hkv << a.page_shift);
+}
+
 // 8 codes -> 4 half2 of consecutive elements (exact).
 __device__ __forceinline__ void e2m1x8_to_half(uint32_t w, uint32_t (&h)[4]) {
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"

@@ -334,8 +334,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
   int64_t fetch_at = 0;      // byte offset of this lane's copy
   uint32_t fetch_lanes = 0;  // the lanes that have one
   auto fetch_keys = [&]() {  // and settle the place that the values' copies use too
-    const bool ok = page >= 0 && page < a.n_pages;
-    if (!ok && page != -2) atomicCAS(&g_err_kv4attn, 0u, kErrArg | (46u << 8));  // a page id outside the cache
+    const bool ok = page >= 0 && page < a.n_pages &&
+                    RNL_DCHECK(&g_err_kv4attn,
+                               chunk_at + chunk_tokens <= TT &&
+                                   in_cache(a, ((static_cast<int64_t>(page) * a.Hkv + page_head) << a.page_shift) + page_off,
+                                            chunk_tokens),
+                               104);
+    if (!ok && page != -2 && (page < 0 || page >= a.n_pages)) atomicCAS(&g_err_kv4attn, 0u, kErrArg | (46u << 8));  // a page id outside the cache
     fetch_lanes = __ballot_sync(0xffffffffu, ok);
     fetch_at = (((static_cast<int64_t>(page) * a.Hkv + page_head) << a.page_shift) + page_off) * row_bytes;
     if (lane == 0)
@@ -760,6 +765,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     constexpr int kTpr = D / 8;  // threads a row, 8 dims each
     for (int x = tid; x < kRows * kTpr; x += kThreads) {
       const int r = x / kTpr, d = (x - r * kTpr) * 8;
+      if (!RNL_DCHECK(&g_err_kv4attn,
+                      cta < kMaxCtas && cur.w.s.row0 + (all_rows - 1) / p.G < a.n_rows && (kvh + 1) * p.G <= p.Hq, 105))
+        continue;
       if (r0 + r >= all_rows || (sh_alone >> min(seg, 31) & 1)) continue;
       float mm = -INFINITY, ll = 0.f;
 #pragma unroll
@@ -834,6 +842,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kJoin * 128)
   load_span<D, NT>(a, p, rec.y, w);
   const int kvh = rec.x / w.groups, group = rec.x - kvh * w.groups;
   const int all_rows = w.s.rows * p.G, r0 = group * kRows;
+  if (!RNL_DCHECK(&g_err_kv4attn, rec.z >= first && rec.z < kMaxCtas && r0 < all_rows && kvh < a.Hkv, 106)) return;
   const int tid = threadIdx.x, g = tid >> 7;
   const float* base = p.part + static_cast<int64_t>(2) * first * C::kSlot;
   auto slot = [&](int c) { return base + static_cast<int64_t>(2 * (c - first) + (c == first ? rec.w : 0)) * C::kSlot; };

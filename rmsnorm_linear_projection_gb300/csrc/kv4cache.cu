@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kCacheWarps * 32)
       if (e >= n) continue;
       const int head = e >> a.d_shift, d = e & (a.D - 1);
       const int64_t row = row0 + (static_cast<int64_t>(head) << a.page_shift);
+      if (!RNL_DCHECK(&g_err_kv4cache, in_cache(a, row, 1) && head < a.Hkv && d + 8 <= a.D, 100)) continue;
       *reinterpret_cast<uint32_t*>(side.codes + ((row << a.d_shift) + d) / 2) = e2m1x8_code(f);
       if ((d & ((1 << a.block_shift) - 1)) == 0)
         side.scales[(row << (a.d_shift - a.block_shift)) + (d >> a.block_shift)] = static_cast<uint8_t>(byte);
@@ -127,6 +128,7 @@ __global__ void __launch_bounds__(kCacheWarps * 32)
       if (e < n) {
         const int head = e >> a.d_shift, d = e & (a.D - 1);
         const int64_t row = row0 + (static_cast<int64_t>(head) << a.page_shift);
+        if (!RNL_DCHECK(&g_err_kv4cache, in_cache(a, row, 1) && head < a.Hkv && d + 8 <= a.D, 101)) return;
         c[r][i] = __ldg(reinterpret_cast<const uint32_t*>(side.codes + ((row << a.d_shift) + d) / 2));
         s[r][i] = __ldg(side.scales + (row << (a.d_shift - a.block_shift)) + (d >> a.block_shift));
       }

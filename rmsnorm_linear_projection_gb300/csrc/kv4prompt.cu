@@ -711,7 +711,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
       tc_fence_after();
       if (large && r < all_rows) atomicOr(&ctrl.alone, 1u << min(nth, 31));
       // rows that are taken by themselves later are stored there alone
-      const bool stored = r < all_rows && (*const_cast<volatile uint32_t*>(&ctrl.alone) >> min(nth, 31) & 1) == 0;
+      const bool stored = RNL_DCHECK(&g_err_kv4prompt,
+                                     cta < kMaxPromptCtas && run.row0 + (all_rows - 1) / p.G < a.n_rows && head < p.Hq, 110) &&
+                          r < all_rows && (*const_cast<volatile uint32_t*>(&ctrl.alone) >> min(nth, 31) & 1) == 0;
       // sums stand for value * 2^(ref_v - 127 - 13), weights and sums both times 2^7
       const bool complete = run.n == run.all;
       const float inv = complete ? (l != 0.f ? 1.f / l : 0.f) : 1.f / 128.f;
@@ -919,6 +921,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const uint32_t ts = tmem + i * 128, to = tmem + 256 + i * D;
       constexpr uint32_t kStep = kU * 128 >> 4;  // a step's rows of an operand
       auto scores = [&](int stage, int half) {
+        if (!RNL_DCHECK(&g_err_kv4prompt, stage < 2 && half < 2 && i * 128 + (half + 1) * kU <= 256, 108)) return;
         const uint32_t kd = k_lo + stage * (kTileBytes >> 4) + half * kStep;
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
@@ -928,6 +931,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         umma_commit(smem_u32(&ctrl.s_full[i][half]));
       };
       auto sums = [&](int stage, int half, bool fresh) {
+        if (!RNL_DCHECK(&g_err_kv4prompt, stage < 2 && half < 2 && 256 + (i + 1) * D <= 512, 109)) return;
         const uint32_t vd = v_lo + stage * (kTileBytes >> 4) + half * kStep;
 #pragma unroll
         for (int x = 0; x < kU / 16; ++x)
@@ -1035,11 +1039,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
                               ((tok0 + chunk_at) & (a.page - 1));
 #pragma unroll
           for (int v = 0; v < 2; ++v) {  // keys, values
-            const bool mine = there && what < (v ? 2 : 3);
+            bool mine = there && what < (v ? 2 : 3);
             const uint8_t* src = what == 0 ? (v ? a.v.codes : a.k.codes) : (v || what == 2 ? a.v.scales : a.k.scales);
-            const uint32_t total = __reduce_add_sync(0xffffffffu, mine ? bytes : 0u);
             ok = idle_wait(smem_u32(&ctrl.raw_empty[rs]), rp, abort, 61);
             if (!ok) break;
+            if (!RNL_DCHECK(&g_err_kv4prompt,
+                            rs >= 0 && rs < kRing && (!there || (chunk_at + chunk_tokens <= kT && in_cache(a, row, chunk_tokens))),
+                            107))
+              mine = false;
+            const uint32_t total = __reduce_add_sync(0xffffffffu, mine ? bytes : 0u);
             const uint32_t bar = smem_u32(&ctrl.raw_full[rs]);
             if (lane == 0) {
               const bool cut = max(tok0, lo) < common_lo || min(tok0 + kT, hi) > common_hi;
@@ -1109,6 +1117,7 @@ __global__ void __launch_bounds__(512)
   load_span(a, p, rec.y, w);
   const int kvh = rec.x / w.groups, group = rec.x - kvh * w.groups;
   const int all_rows = w.s.rows * p.G, r0 = group * kGroup;
+  if (!RNL_DCHECK(&g_err_kv4prompt, rec.z >= first && rec.z < kMaxPromptCtas && r0 < all_rows && kvh < a.Hkv, 111)) return;
   constexpr int kTpr = D / 8;
   for (int x = threadIdx.x; x < 64 * kTpr; x += 512) {
     const int r = part * 64 + x / kTpr, d = (x % kTpr) * 8;

@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
     const int h = h0 + g * kHeads + lane / kLanes;
-    if (h < h1) {
+    if (h < h1 && RNL_DCHECK(&g_err_axes, t < T && h >= 0 && h < H, 102)) {
       lo[g] = __ldg(reinterpret_cast<const uint4*>(yt + static_cast<int64_t>(h) * D));
       hi[g] = __ldg(reinterpret_cast<const uint4*>(yt + static_cast<int64_t>(h) * D + kHalf));
     }
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas)
         }
       }
     }
-    if (!live) continue;
+    if (!live || !RNL_DCHECK(&g_err_axes, h < H && sub * 8 + 8 <= kHalf, 103)) continue;
     if (!turned) {  // a v head: copied
       __nv_bfloat16* dst = v + (t * Hkv + (h - nqk)) * D + sub * 8;
       *reinterpret_cast<uint4*>(dst) = lo[g];
