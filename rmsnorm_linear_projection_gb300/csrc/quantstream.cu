@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(kThreadsQS, 1)
     for (int i = 1; i <= kConsumerWarps; ++i) gm = max(gm, ctrl->gmax[i]);
     *gmax_out = __uint_as_float(gm);
   }
+  const uint32_t zero = static_cast<uint32_t>(nvec) >> 30;
   for (int64_t j = pair; j < rows; j += kPairs) {
     const uint32_t s = static_cast<uint32_t>(j % slots);
     const uint32_t use = static_cast<uint32_t>(j / slots);
@@ -343,9 +344,14 @@ __global__ void __launch_bounds__(kThreadsQS, 1)
     uint4 xv[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) xv[i] = rp[lane + 64 * i];
-    // this half of the row is in registers: the warp's share of the slot goes back
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&ctrl->empty[s]));
+    // this half of the row is in registers: the warp's share of the slot goes
+    // back.  (The arrival depends on the loads, which might otherwise be carried
+    // out after it; `zero` is 0, which the compiler does not know.)
+    uint32_t read = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) read |= xv[i].x | xv[i].y | xv[i].z | xv[i].w;
+    const bool done = __all_sync(0xFFFFFFFFu, (read & zero) == 0);
+    if (lane == 0 && done) mbar_arrive(smem_u32(&ctrl->empty[s]));
     float whi, wlo;
     pass_sum<MODE, VPL>(xv, inv_d, whi, wlo);
     if (lane == 0) {
