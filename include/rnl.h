@@ -332,6 +332,12 @@ rnl_status rnl_kv4_gather(const rnl_kv4_cache *cache, const rnl_kv4_seqs *seqs, 
  * below.  Where tokens that only some rows of a call read are 2^36 times others,
  * or scores (times log2 e) reach 2^22 in size, the rows concerned are computed
  * one at a time in FP32, which takes much longer.
+ * Two kernels: one for sequences of up to 32 rows x G, one on the tensor cores
+ * for more, with head_dim 64 and 128.  head_dim 256 is right in every form but
+ * has no kernel for many rows (a 2048-row chunk takes milliseconds).  Which one
+ * takes a sequence goes by its rows, head_dim and the tables' room
+ * (max_pages * page_size), so that other tables can change the output's last
+ * bits; the same call gives the same bits every time.
  * Workspace: rnl_workspace_size(RNL_OP_KV4_ATTENTION, n_rows, head_dim,
  * n_q_heads, n_kv_heads) bytes; results do not depend on its contents.  Calls
  * that may run at the same time (other streams, other graphs) need one each.

@@ -31,9 +31,13 @@
 // shared memory as binary16 first, 8 times the bytes the codes have.
 //
 // Measured (G = 4, D = 128, cold caches): 8 sequences of 131072 tokens 242 us,
-// 4.7 TB/s of cache, bound by issue slots (59 %) and the code conversions; 32
-// sequences of 4 rows over 2000 to 9000 tokens 92 us, bound by mma.sync and its
-// latency with two warps a scheduler (16 rows take 255 registers).
+// 4.7 TB/s of cache: latency, 59 % of the issue slots with three warps a
+// scheduler that wait for their own chains (tensor pipe 25 %, conversions); 32
+// sequences of 4 rows over 2000 to 9000 tokens 95 us, the same with two warps a
+// scheduler (16 rows take 255 registers; tensor pipe 35 %).  head_dim 256: 64
+// sequences of 1 to 16384 tokens 261 us against 174 of bytes; prompts come here too
+// (kv4prompt.cu has no form for them) and read the cache once per 16 rows: 2048 and
+// 1500 rows over 10240 and 8000 tokens, G = 2, 5.0 ms.
 //
 // Scales.  2^X of a block does not fit binary16's range, 2^(X - R) does, where
 // R is the largest X of the tile (keys) or of the tiles so far (values): an
@@ -60,8 +64,8 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCtas = 640;                              // partial-sum slots in the workspace
 
 // What an item costs a CTA beside its tiles (queries, joining the warps), in
-// tiles: counted when the tiles are dealt out.  64 sequences of 1 to 16384 tokens:
-// 58 us, with 2 tiles 88, 4 68, 9 60, 14 64.
+// tiles: counted when the tiles are dealt out.  64 sequences of 1 to 16384 tokens
+// (60 us now): 58 us, with 2 tiles 88, 4 68, 9 60, 14 64.
 constexpr int kItemCost = 6;
 
 template <int D, int NT>
@@ -199,7 +203,8 @@ __device__ __noinline__ void segments_by_rows(const Args& a, const AttnParams& p
 }
 
 // MIXED: the rows of a sequence may differ in what they read (several causal
-// rows).  Without it, 8 sequences of 131072 tokens take 235 us instead of 240.
+// rows).  64 sequences of 1 to 16384 tokens, Hkv = 8, a row each: 149 us with it
+// (given with cu_rows), 142 without.
 template <int D, int NT, int BS, bool MIXED>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kMinCtas)
     kv4_attn_kernel(const __grid_constant__ Args a, const __grid_constant__ AttnParams p) {
@@ -931,13 +936,16 @@ constexpr int kFewRows = 32;
 // Rows times key heads times tokens (as many as the tables can hold) up to which
 // the prompt kernel is not launched at all: 16 rows of 2 sequences of up to 9000
 // tokens (9.2 million) 37 us here, 60 us there; 32 rows over 12000 (12.3 million)
-// 58 and 68; 32 rows of 2 sequences of 6000 (12.3 million) 64 and 56.
+// 58 and 68; 32 rows of 2 sequences of 6000 (12.3 million) 64 and 56.  Lengths are on
+// the device, so tables with room for a longer context count as longer sequences: 8
+// rows (G = 4) of 2 sequences of 6000 tokens 32 us with tables of 6016 tokens, 38 with
+// 131072, and the output's last bits then come from the other kernel.
 constexpr int64_t kFewWork = 12000000;
 size_t few_workspace_bytes(int64_t D) {
   const size_t slot = static_cast<size_t>(16) * (static_cast<size_t>(D) + 2) * 4;  // NT = 2
   return (kMaxCtas * (sizeof(int4) + 2 * slot) + 255) / 256 * 256;
 }
-// Whether some sequence may have more than kFewRows rows.
+// Whether some sequence may have more than kFewRows rows, and a prompt kernel (not for head_dim 256).
 bool may_prompt(int64_t T, int64_t G, int64_t D) { return T * G > kFewRows && kv4_prompt_fits(D); }
 }  // namespace
 
@@ -976,7 +984,9 @@ rnl_status launch_kv4_attention(const Kv4AttnArgs& x, const rnl_kv4_cache& c, co
   }
   // 4, 8 or 16 rows an item: the fewest that hold the rows a sequence has on average
   // (with 8 rows an item 131072 tokens x 8 take 267 us instead of 242; with 16, 32
-  // sequences of 2 rows 91 instead of 66)
+  // sequences of 2 rows 91 instead of 66).  The rows of prompts count in that average, though the other
+  // kernel takes them: 64 single tokens beside a prompt of 2048 rows get items of 16 rows (380 us, the
+  // two alone 149 and 157)
   const int64_t rows = (q.n_rows + q.n_seqs - 1) / q.n_seqs * p.G;
   const bool mixed = a.cu != nullptr && p.causal;
   auto go = [&](auto d, auto bs) {

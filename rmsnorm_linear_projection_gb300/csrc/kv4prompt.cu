@@ -34,9 +34,11 @@
 // a dependent kernel.
 //
 // Measured (two prompts of 1000 to 2048 rows over 6000 to 10240 tokens, G = 4,
-// D = 128): 369 to 373 us, 1011 to 1022 TFLOP/s, tensor pipe 47 % active; a tile takes 1.87 us
-// where the products alone would take 1.1.  What bounds it is the softmax (a
-// thread a row: exponentials, conversions, TMEM reads) beside 8 to 10 us a run.
+// D = 128): 375 to 379 us, 995 to 1006 TFLOP/s, tensor pipe 46 % active; a tile takes
+// 1.9 us where the products alone would take 1.1.  What it waits for is the softmax (a
+// thread a row: exponentials, conversions, TMEM reads) beside 8 to 10 us a run, in
+// which a run's queries and first scores wait for the output of the run before.  With
+// a window of 4096 tokens (2048 and 1500 rows over 10240 and 8000): 300 us against 127.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
