@@ -222,3 +222,42 @@ def test_equal_scores_of_any_size(rows, n, scale):
         # 2^-8 for the output, 2^-11 of sum p |v| for the weights, 2^-18 for the sums
         assert ((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2.0 ** -18) * size).all()
         assert lse.isfinite().all()
+
+
+@pytest.mark.parametrize("rows,G,D,copies", [(3, 2, 64, 800), (2, 4, 128, 800), (40, 1, 64, 300), (36, 2, 128, 300)])
+def test_large_tokens_in_many_short_sequences(rows, G, D, copies):
+    """A large token in every sequence of a batch, so that a CTA has more such items
+    than it keeps apart (31): some twenty sequences, each many times over."""
+    g = gen(rows + D)
+    B = 23
+    lens = [rows + (b * 7) % 40 for b in range(B)]
+    c, t = filled(g, lens, 1, 16, D, 32)
+    for side, up in (("k", 60), ("v", 90)):
+        s = getattr(c, side + "_scales")
+        last = torch.tensor([n - 1 - (side == "v") for n in lens], device="cuda")
+        s[t[torch.arange(B, device="cuda"), last // 16].long(), :, last % 16] += up
+    cu = [rows * b for b in range(B + 1)]
+    q = randn(g, rows * B, G, D).bfloat16()
+    o, z, tol, ltol = reference(q, c, t, lens, cu, 0)
+    many = q.repeat(copies, 1, 1)
+    out, lse = torch.empty_like(many), torch.empty(many.shape[:2], device="cuda")
+    rnl.rnl_kv4_attention(many, c, t.repeat(copies, 1), i32(lens).repeat(copies),
+                          i32([rows * b for b in range(B * copies + 1)]), out=out, lse_out=lse)
+    rnl.rnl_check_device_error()
+    assert ((out.view(copies, *q.shape).double() - o).abs() <= tol).all()
+    assert ((lse.view(copies, *z.shape).double() - z).abs() <= ltol).all()
+
+
+@pytest.mark.parametrize("D,rows,G", [(64, 1, 4), (128, 4, 4), (256, 3, 2), (128, 150, 2), (64, 300, 1)])
+def test_queries_that_are_not_numbers_stay_to_themselves(D, rows, G):
+    g = gen(D + rows)
+    n = 500
+    c, t = filled(g, [n, 77], 2, 32, D, 32)
+    lens, cu = [n, 77], [0, rows, rows + 1]
+    q = randn(g, rows + 1, 2 * G, D).bfloat16()
+    ref = reference(q, c, t, lens, cu, 0)
+    bad = torch.zeros(rows + 1, 2 * G, dtype=torch.bool, device="cuda")
+    bad[rows // 2, 1] = bad[0, 0] = True
+    q[rows // 2, 1, 5] = math.nan
+    q[0, 0] = math.nan
+    check(q, c, t, lens, cu, 0, ref, skip=bad)

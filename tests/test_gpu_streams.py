@@ -120,3 +120,24 @@ def test_a_handle_of_another_library_is_a_stream_too():
     out = rnl.rnl_kv4_attention(*job, stream=Handle(s))
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_captured_calls_on_given_streams():
+    """Calls on the capturing stream and on one forked from it, inside one graph."""
+    jobs = attention_jobs(torch.Generator(device="cuda").manual_seed(8))
+    want = [rnl.rnl_kv4_attention(*j) for j in jobs]
+    torch.cuda.synchronize()
+    side, fork = torch.cuda.Stream(), torch.cuda.Stream()
+    graph, outs = torch.cuda.CUDAGraph(), []
+    with torch.cuda.graph(graph, stream=side):
+        fork.wait_stream(side)
+        for i, j in enumerate(jobs):
+            outs.append(rnl.rnl_kv4_attention(*j, stream=side if i % 2 else fork))
+        side.wait_stream(fork)
+    for _ in range(3):
+        for o in outs:
+            o.fill_(320.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        rnl.rnl_check_device_error()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
