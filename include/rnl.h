@@ -102,7 +102,9 @@ enum {
   RNL_OP_QMRS = 5,
   RNL_OP_MXFP8 = 6,
   RNL_OP_W8A8_PREPARED = 7,
-  RNL_OP_KV4_ATTENTION = 8
+  RNL_OP_KV4_ATTENTION = 8,
+  RNL_OP_GROUPED = 9,
+  RNL_OP_MOE_ROUTE = 10
 };
 
 /* Library version (major * 10000 + minor * 100 + patch). */
@@ -132,6 +134,8 @@ const char *rnl_status_string(rnl_status s);
  *   RNL_OP_MXFP8:   T, K, N; N2 ignored (rmsnorm_linear_mxfp8 and mxfp8_scaled_mm)
  *   RNL_OP_W8A8_PREPARED: T, K, N; N2 ignored (rmsnorm_linear_w8a8_prepared)
  *   RNL_OP_KV4_ATTENTION: T = rows, K = head_dim, N = n_q_heads, N2 = n_kv_heads
+ *   RNL_OP_GROUPED: T = M, K, N, N2 = n_experts (rnl_grouped_linear_bf16)
+ *   RNL_OP_MOE_ROUTE: T, K = top_k, N = n_experts; N2 ignored
  * Returns (size_t)-1 for invalid sizes.  Host-only; needs no GPU.
  */
 size_t rnl_workspace_size(int op, int64_t T, int64_t K, int64_t N, int64_t N2);
@@ -502,6 +506,102 @@ rnl_status mxfp8_scaled_mm(const uint8_t *x_codes, const uint8_t *x_scale, const
                            const uint8_t *w_scale, int64_t T, int64_t K, int64_t N, int64_t block,
                            void *out, int out_dtype, void *workspace, size_t workspace_bytes,
                            rnl_stream_t stream);
+
+/*
+ * Rows into MXFP8 without a product behind them: the operand of
+ * mxfp8_scaled_mm and of rnl_grouped_linear_mxfp8.
+ *   x         bf16 [T, K]
+ *   residual, x_sum_out, gamma  as in rmsnorm_linear_bf16_ex: s = bf16(x +
+ *             residual), written to x_sum_out (NULL, x, residual, or disjoint
+ *             from both); the norm is s's
+ *   codes     E4M3FN bytes [T, K];  scale  E8M0 bytes [T, K / block]
+ * The codes and scales of rmsnorm_linear_mxfp8 for the same (finite) rows, to the
+ * bit.  A row whose sum of squares is infinite has rstd 0.  A block of y that holds an infinity or NaN gets scale byte 255 (NaN) and codes
+ * 0.  block 32 or 64 (else RNL_ERR_ARG), K % block == 0 (else RNL_ERR_SHAPE),
+ * K at most 65536 (else RNL_ERR_UNSUPPORTED).  16-byte aligned tensors (scale:
+ * any).  No workspace.
+ * rnl_quant_mxfp8: the same blocks of x itself, no add and no norm.
+ */
+rnl_status rnl_add_rmsnorm_mxfp8(const void *x, const void *residual, void *x_sum_out, const void *gamma,
+                                 int64_t T, int64_t K, float eps, int norm_mode, int64_t block,
+                                 uint8_t *codes, uint8_t *scale, rnl_stream_t stream);
+rnl_status rnl_quant_mxfp8(const void *x, int64_t T, int64_t K, int64_t block, uint8_t *codes,
+                           uint8_t *scale, rnl_stream_t stream);
+
+/*
+ * A layer of experts behind the projection (no counterpart on the pages):
+ *   logits = rmsnorm_linear_bf16(x, router weight), FP32 out
+ *   rnl_moe_route          each token's experts, their weights, the rows grouped
+ *   rnl_grouped_linear_*   the products, a weight for each group of rows
+ *   rnl_moe_combine        each token's rows weighted and added up
+ *
+ * rnl_moe_route: for each token the top_k experts of the largest logits, in
+ * falling order (equal ones: the lower expert first), and their softmax weights.
+ *   logits  fp32 [T, n_experts].  -infinity and NaN: the expert is not chosen
+ *           and has no share in the softmax; +infinity: the token's infinite
+ *           ones share it evenly, the finite ones get 0
+ *   renormalize  1: the weights of the chosen ones add up to 1; 0: their share
+ *           in the softmax over all experts
+ *   ids     int32 [T, top_k], weights fp32 [T, top_k]: -1 and 0 in the places of
+ *           a token that has fewer than top_k experts to choose from
+ *   offsets int32 [n_experts + 1]: rows offsets[e] .. offsets[e + 1] - 1 of the
+ *           grouped order are expert e's
+ *   rows    int32 [T * top_k]: the token of each grouped row, in the order of
+ *           (token, place) within an expert; -1 from offsets[n_experts] on
+ *   slots   int32 [T, top_k]: the grouped row of each choice, -1 where none
+ * n_experts up to 1024, top_k up to 32 (else RNL_ERR_UNSUPPORTED) and n_experts
+ * (else RNL_ERR_SHAPE).  4-byte aligned tensors.  Workspace:
+ * rnl_workspace_size(RNL_OP_MOE_ROUTE, T, top_k, n_experts, 0) bytes (0 for a
+ * few tokens).  T == 0 writes the offsets.
+ */
+#define RNL_MOE_MAX_EXPERTS 1024
+#define RNL_MOE_MAX_TOP_K 32
+rnl_status rnl_moe_route(const float *logits, int64_t T, int64_t n_experts, int64_t top_k,
+                         int renormalize, int32_t *ids, float *weights, int32_t *offsets,
+                         int32_t *rows, int32_t *slots, void *workspace, size_t workspace_bytes,
+                         rnl_stream_t stream);
+
+/*
+ * Products grouped by expert, groups of any size:
+ *   out[i] = bf16(sum_k x[rows[i], k] * W[e, n, k])      offsets[e] <= i < offsets[e + 1]
+ *   x       bf16 [n_x_rows, K];  W bf16 [n_experts, N, K]
+ *   offsets int32 [n_experts + 1] on the device, not decreasing, within [0, M];
+ *           otherwise nothing is computed and the next rnl_check_device_error()
+ *           returns RNL_ERR_ARG
+ *   rows    int32 [M] or NULL (row i reads x[i]; n_x_rows == M): several rows may
+ *           read one of x.  A value outside [0, n_x_rows) is reported as
+ *           RNL_ERR_ARG and that row's output is unspecified
+ *   swiglu  0: out bf16 [M, N]
+ *           1: W[e] holds N / 2 gate rows, then N / 2 up rows:
+ *              out bf16 [M, N / 2] = bf16(silu(g) * u) of the FP32 sums; N % 32
+ *              == 0 (else RNL_ERR_UNSUPPORTED)
+ * Rows of out outside every group (before offsets[0], from offsets[n_experts]
+ * on) are left as they were.  FP32 accumulation; the order of the sums depends
+ * on the sizes of all groups, so that a row's last bit may differ between calls
+ * whose groups differ; the same call gives the same bits every time.  K % 8 ==
+ * 0, 16-byte aligned x, W and out.  Workspace:
+ * rnl_workspace_size(RNL_OP_GROUPED, M, K, N, n_experts) bytes; results do not
+ * depend on its contents, and calls that may run at the same time need one
+ * each.
+ */
+rnl_status rnl_grouped_linear_bf16(const void *x, int64_t n_x_rows, const void *W, int64_t n_experts,
+                                   int64_t N, int64_t K, const int32_t *offsets, const int32_t *rows,
+                                   int64_t M, int swiglu, void *out, void *workspace,
+                                   size_t workspace_bytes, rnl_stream_t stream);
+
+/*
+ * The weighted sum of every token's grouped rows:
+ *   out[t] = bf16(residual[t] + sum_j weights[t, j] * y[slots[t, j]])
+ *   y bf16 [M, N], N % 8 == 0;  slots int32 [T, top_k], weights fp32 [T, top_k]
+ *   residual bf16 [T, N] or NULL;  out bf16 [T, N], may be residual itself
+ * FP32 sums in the order of j, the residual last, rounded once.  Slots of -1 are
+ * left out (their weights are not read as numbers); others outside [0, M) too,
+ * and are reported as RNL_ERR_ARG.  out must not overlap y.  16-byte aligned y,
+ * residual and out.  No workspace.
+ */
+rnl_status rnl_moe_combine(const void *y, int64_t M, int64_t N, const int32_t *slots,
+                           const float *weights, int64_t T, int64_t top_k, const void *residual,
+                           void *out, rnl_stream_t stream);
 
 /*
  * MLA two-stage q chain.

@@ -25,6 +25,14 @@ arguments; the computation runs in the library's CUDA kernels.
                           the 4-bit paged KV cache: quantise k and v into it, read them back
     rnl_kv4_attention     attention over that cache: single tokens, drafts, prompts,
                           cross attention
+    rnl_add_rmsnorm_mxfp8, rnl_quant_mxfp8
+                          rows into MXFP8 operands, with the residual add and
+                          the norm or as they are
+    rnl_moe_route, rnl_moe_combine
+                          tokens to experts (top-k, weights, rows grouped) and
+                          the weighted sum back
+    rnl_grouped_linear_bf16
+                          products grouped by expert with ragged sizes
     rnl_pipeline_*        host-buffer pipeline: calls fed from and answering into
                           pinned host memory, copies overlapped with the kernels
     debug_library()       route calls through librnl_debug.so, the build whose
@@ -36,8 +44,10 @@ from ._native import (  # noqa: F401
     NORM_SQRT_DIV,
     OP_BF16,
     OP_GEMM_S8,
+    OP_GROUPED,
     OP_KV4_ATTENTION,
     OP_MLA,
+    OP_MOE_ROUTE,
     OP_MXFP8,
     OP_QKV_ROPE,
     OP_QMRS,
@@ -46,6 +56,7 @@ from ._native import (  # noqa: F401
     OUT_BF16,
     OUT_FP32,
     Kv4Cache,
+    MoeRoute,
     PipelineHandle,
     RnlError,
     debug_library,
@@ -61,13 +72,17 @@ from ._native import (  # noqa: F401
     rmsnorm_linear_skinny_noalloc,
     rmsnorm_linear_w8a8,
     rmsnorm_linear_w8a8_prepared,
+    rnl_add_rmsnorm_mxfp8,
     rnl_check_device_error,
     rnl_debug_build,
     rnl_gemm_s8s8s32,
+    rnl_grouped_linear_bf16,
     rnl_head_rmsnorm,
     rnl_kv4_append,
     rnl_kv4_attention,
     rnl_kv4_gather,
+    rnl_moe_combine,
+    rnl_moe_route,
     rnl_pipeline_create,
     rnl_pipeline_destroy,
     rnl_pipeline_submit_bf16,
@@ -76,6 +91,7 @@ from ._native import (  # noqa: F401
     rnl_pipeline_wait,
     rnl_qkv_rope,
     rnl_qkv_rope_axes,
+    rnl_quant_mxfp8,
     rnl_selftest_bounds_check,
     rnl_selftest_wait_timeout,
     rnl_trace_enable,

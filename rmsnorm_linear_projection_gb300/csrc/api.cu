@@ -425,6 +425,24 @@ rnl_status make_map_2d_plain(CUtensorMap* map, CUtensorMapDataType dtype, const 
                    CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+rnl_status make_map_5d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, const uint64_t (&dims)[5],
+                       const uint64_t (&strides)[4], const uint32_t (&box)[5], bool swizzle) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return RNL_ERR_DEVICE;
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5];
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  for (int i = 0; i < 5; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    if (i < 4) st[i] = strides[i];
+  }
+  const CUresult r = enc(map, dtype, 5, const_cast<void*>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? RNL_OK : RNL_ERR_ARG;
+}
+
 namespace {
 std::mutex g_attr_mu;
 std::map<std::pair<const void*, int>, size_t> g_attr_done;  // the dynamic shared memory each kernel may use
@@ -465,14 +483,15 @@ void trace_after(cudaStream_t s, const char* name) {
 }
 
 rnl_status read_device_errors(int* site) {
-  unsigned int words[14] = {};
+  unsigned int words[16] = {};
   if (read_clear_error_rowwise(&words[0]) != RNL_OK || read_clear_error_gemm(&words[1]) != RNL_OK ||
       read_clear_error_skinny(&words[2]) != RNL_OK || read_clear_error_pair(&words[3]) != RNL_OK ||
       read_clear_error_norm(&words[4]) != RNL_OK || read_clear_error_selftest(&words[5]) != RNL_OK ||
       read_clear_error_rope(&words[6]) != RNL_OK || read_clear_error_mx(&words[7]) != RNL_OK ||
       read_clear_error_quant(&words[8]) != RNL_OK || read_clear_error_decmma(&words[9]) != RNL_OK ||
       read_clear_error_kv4cache(&words[10]) != RNL_OK || read_clear_error_kv4attn(&words[11]) != RNL_OK ||
-      read_clear_error_kv4prompt(&words[12]) != RNL_OK || read_clear_error_axes(&words[13]) != RNL_OK)
+      read_clear_error_kv4prompt(&words[12]) != RNL_OK || read_clear_error_axes(&words[13]) != RNL_OK ||
+      read_clear_error_moe(&words[14]) != RNL_OK || read_clear_error_grouped(&words[15]) != RNL_OK)
     return RNL_ERR_LAUNCH;
   for (unsigned int w : words) {
     if (w != 0) {
@@ -537,6 +556,10 @@ size_t rnl_workspace_size(int op, int64_t T, int64_t K, int64_t N, int64_t N2) {
     case RNL_OP_KV4_ATTENTION:
       if (!qkv_rope_head_dim_ok(K) || N == 0 || N2 == 0 || N % N2 != 0) return static_cast<size_t>(-1);
       return round_up(kv4_attn_workspace_bytes(T, K, N / N2));
+    case RNL_OP_GROUPED:
+      return kGemmPartialBytes;
+    case RNL_OP_MOE_ROUTE:
+      return round_up(moe_route_workspace_bytes(T, N));
     case RNL_OP_QKV_ROPE:
       return bf16_layout(nullptr, T, K, N, RNL_OUT_BF16).bytes + round_up(static_cast<size_t>(T) * N * 2);
   }
@@ -1159,6 +1182,131 @@ rnl_status rnl_gemm_s8s8s32(const int8_t* A, const int8_t* B, int32_t* C, int64_
   g.chunk_ws = l.chunk;
   g.chunk_ws_bytes = kGemmPartialBytes;
   return launch_gemm(g, s);
+}
+
+// x_sum is one of the inputs (in place) or disjoint from both
+static bool sum_overlaps(const void* x_sum, const void* x, const void* residual, int64_t n_bytes) {
+  if (!x_sum || x_sum == x || x_sum == residual) return false;
+  const uintptr_t o = reinterpret_cast<uintptr_t>(x_sum), n = static_cast<uintptr_t>(n_bytes);
+  for (const void* in : {x, residual}) {
+    const uintptr_t i = reinterpret_cast<uintptr_t>(in);
+    if (in && o < i + n && i < o + n) return true;
+  }
+  return false;
+}
+
+rnl_status rnl_add_rmsnorm_mxfp8(const void* x, const void* residual, void* x_sum_out, const void* gamma,
+                                 int64_t T, int64_t K, float eps, int norm_mode, int64_t block,
+                                 uint8_t* codes, uint8_t* scale, rnl_stream_t stream) {
+  if (bad_dim(T) || bad_dim(K) || K == 0) return RNL_ERR_SHAPE;
+  if (bad_mode(norm_mode) || bad_eps(eps) || !mx_block_ok(block)) return RNL_ERR_ARG;
+  if (K % block != 0) return RNL_ERR_SHAPE;
+  if (K > 65536) return RNL_ERR_UNSUPPORTED;
+  if (x_sum_out && !residual) return RNL_ERR_ARG;  // nothing to write back
+  if (sum_overlaps(x_sum_out, x, residual, T * K * 2)) return RNL_ERR_ARG;
+  if (T == 0) return RNL_OK;
+  if (!x || !codes || !scale) return RNL_ERR_NULL;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(x_sum_out) || !aligned16(gamma) || !aligned16(codes))
+    return RNL_ERR_ALIGN;
+  return launch_quant_mxfp8(x, residual, x_sum_out, gamma, T, K, true, eps, norm_mode, block, codes, scale,
+                            cs(stream));
+}
+
+rnl_status rnl_quant_mxfp8(const void* x, int64_t T, int64_t K, int64_t block, uint8_t* codes, uint8_t* scale,
+                           rnl_stream_t stream) {
+  if (bad_dim(T) || bad_dim(K) || K == 0) return RNL_ERR_SHAPE;
+  if (!mx_block_ok(block)) return RNL_ERR_ARG;
+  if (K % block != 0) return RNL_ERR_SHAPE;
+  if (K > 65536) return RNL_ERR_UNSUPPORTED;
+  if (T == 0) return RNL_OK;
+  if (!x || !codes || !scale) return RNL_ERR_NULL;
+  if (!aligned16(x) || !aligned16(codes)) return RNL_ERR_ALIGN;
+  return launch_quant_mxfp8(x, nullptr, nullptr, nullptr, T, K, false, 0.f, 0, block, codes, scale, cs(stream));
+}
+
+static bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+rnl_status rnl_moe_route(const float* logits, int64_t T, int64_t n_experts, int64_t top_k, int renormalize,
+                         int32_t* ids, float* weights, int32_t* offsets, int32_t* rows, int32_t* slots,
+                         void* workspace, size_t workspace_bytes, rnl_stream_t stream) {
+  if (bad_dim(T) || bad_dim(n_experts) || bad_dim(top_k) || n_experts == 0 || top_k == 0 || top_k > n_experts ||
+      bad_dim(T * top_k))
+    return RNL_ERR_SHAPE;
+  if (n_experts > RNL_MOE_MAX_EXPERTS || top_k > RNL_MOE_MAX_TOP_K) return RNL_ERR_UNSUPPORTED;
+  if (renormalize != 0 && renormalize != 1) return RNL_ERR_ARG;
+  if (!offsets || (T > 0 && (!logits || !ids || !weights || !rows || !slots))) return RNL_ERR_NULL;
+  if (misaligned4(logits) || misaligned4(ids) || misaligned4(weights) || misaligned4(offsets) ||
+      misaligned4(rows) || misaligned4(slots) || !aligned16(workspace))
+    return RNL_ERR_ALIGN;
+  const size_t need = moe_route_workspace_bytes(T, n_experts);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return RNL_ERR_WORKSPACE;
+  DeviceInfo dev;
+  const rnl_status st = current_device(&dev);
+  if (st != RNL_OK) return st;
+  return launch_moe_route(logits, T, n_experts, top_k, renormalize, ids, weights, offsets, rows, slots, workspace,
+                          cs(stream));
+}
+
+rnl_status rnl_moe_combine(const void* y, int64_t M, int64_t N, const int32_t* slots, const float* weights,
+                           int64_t T, int64_t top_k, const void* residual, void* out, rnl_stream_t stream) {
+  if (bad_dim(M) || bad_dim(N) || N == 0 || bad_dim(T) || bad_dim(top_k) || bad_dim(T * top_k) ||
+      bad_dim(T * (N / 8) / 256 + 1))
+    return RNL_ERR_SHAPE;
+  if (T == 0) return RNL_OK;
+  if (!out || (M > 0 && !y) || (top_k > 0 && (!slots || !weights))) return RNL_ERR_NULL;
+  if (N % 8 != 0 || !aligned16(y) || !aligned16(residual) || !aligned16(out) || misaligned4(slots) ||
+      misaligned4(weights))
+    return RNL_ERR_ALIGN;
+  const uintptr_t ob = reinterpret_cast<uintptr_t>(out), on = static_cast<uintptr_t>(T) * N * 2;
+  const uintptr_t rb = reinterpret_cast<uintptr_t>(residual), yb = reinterpret_cast<uintptr_t>(y);
+  if (residual && rb != ob && rb < ob + on && ob < rb + on) return RNL_ERR_ARG;  // partial overlap
+  if (y && yb < ob + on && ob < yb + static_cast<uintptr_t>(M) * N * 2) return RNL_ERR_ARG;
+  DeviceInfo dev;
+  const rnl_status st = current_device(&dev);
+  if (st != RNL_OK) return st;
+  return launch_moe_combine(y, M, N, slots, weights, T, top_k, residual, out, cs(stream));
+}
+
+// What the two grouped products check alike; *go: there is something to do.
+static rnl_status check_grouped(const GroupedArgs& g, size_t workspace_bytes, bool* go) {
+  *go = false;
+  if (bad_dim(g.R) || bad_dim(g.E) || bad_dim(g.N) || bad_dim(g.K) || bad_dim(g.M) || g.E == 0 || g.N == 0 ||
+      g.K == 0 || bad_dim(g.E * g.N) || (!g.rows && g.R != g.M))
+    return RNL_ERR_SHAPE;
+  if (g.E > RNL_MOE_MAX_EXPERTS || (g.swiglu && g.N % 32 != 0)) return RNL_ERR_UNSUPPORTED;
+  if (g.M == 0) return RNL_OK;
+  if (g.R == 0) return RNL_ERR_SHAPE;  // rows of nothing
+  if (!g.x || !g.w || !g.offsets || !g.out) return RNL_ERR_NULL;
+  if (!aligned16(g.x) || !aligned16(g.w) || !aligned16(g.out) || misaligned4(g.offsets) || misaligned4(g.rows) ||
+      !aligned16(g.ws))
+    return RNL_ERR_ALIGN;
+  if (!g.ws || workspace_bytes < kGemmPartialBytes) return RNL_ERR_WORKSPACE;
+  *go = true;
+  return RNL_OK;
+}
+
+rnl_status rnl_grouped_linear_bf16(const void* x, int64_t n_x_rows, const void* W, int64_t n_experts, int64_t N,
+                                   int64_t K, const int32_t* offsets, const int32_t* rows, int64_t M, int swiglu,
+                                   void* out, void* workspace, size_t workspace_bytes, rnl_stream_t stream) {
+  if (swiglu != 0 && swiglu != 1) return RNL_ERR_ARG;
+  GroupedArgs g;
+  g.x = x;
+  g.R = n_x_rows;
+  g.w = W;
+  g.E = n_experts;
+  g.N = N;
+  g.K = K;
+  g.offsets = offsets;
+  g.rows = rows;
+  g.M = M;
+  g.swiglu = swiglu == 1;
+  g.out = out;
+  g.ws = workspace;
+  bool go;
+  const rnl_status st = check_grouped(g, workspace_bytes, &go);
+  if (st != RNL_OK) return st;
+  if (K % 8 != 0) return RNL_ERR_ALIGN;
+  return go ? launch_grouped_bf16(g, cs(stream)) : RNL_OK;
 }
 
 rnl_status rnl_check_device_error(rnl_stream_t stream, int* site) {

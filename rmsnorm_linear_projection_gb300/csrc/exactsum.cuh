@@ -127,8 +127,8 @@ __device__ __forceinline__ void ffx2_add_squares8(const uint4& u, float inv_d, u
     ffx2_two_sum(hs[k], ls[k], t);
   }
 }
-// the binary32 rounding of the warp's total of all lanes' chains
-__device__ __forceinline__ float ffx2_warp_total(uint64_t (&hs)[4], uint64_t (&ls)[4]) {
+// the warp's total of all lanes' chains, left as a pair (the same on every lane)
+__device__ __forceinline__ void ffx2_warp_hilo(uint64_t (&hs)[4], uint64_t (&ls)[4], float& hi, float& lo) {
   ffx2_two_sum(hs[0], ls[0], hs[1]);
   ls[0] = ffx2_add(ls[0], ls[1]);
   ffx2_two_sum(hs[2], ls[2], hs[3]);
@@ -138,10 +138,15 @@ __device__ __forceinline__ float ffx2_warp_total(uint64_t (&hs)[4], uint64_t (&l
   float h0, h1, l0, l1;
   ffx2_unpack(hs[0], h0, h1);
   ffx2_unpack(ls[0], l0, l1);
-  float hi, e;
+  float e;
   two_sum(h0, h1, hi, e);
-  float lo = __fadd_rn(__fadd_rn(l0, l1), e);
+  lo = __fadd_rn(__fadd_rn(l0, l1), e);
   ff_warp_merge(hi, lo);
+}
+// the binary32 rounding of that total
+__device__ __forceinline__ float ffx2_warp_total(uint64_t (&hs)[4], uint64_t (&ls)[4]) {
+  float hi, lo;
+  ffx2_warp_hilo(hs, ls, hi, lo);
   return __fadd_rn(hi, lo);
 }
 

@@ -1,0 +1,396 @@
+// grouped.cu -- products grouped by expert with ragged sizes, bf16:
+//
+//   out[i] = bf16(sum_k x[rows[i], k] W[e, :, k])        rows i of expert e
+//   out[i] = bf16(silu(g) u),  g = the first half of W[e]'s rows, u the second    (swiglu)
+//
+// on CTA pairs (tcgen05.mma.cta_group::2): a unit is 256 weight rows (128 a
+// CTA, the M side) against a tile of up to 256 rows of the group (the N side,
+// half of them staged by each CTA), see grouped.cuh.  The group's rows are
+// fetched by TMA gathers of four rows, so that no sorted copy of x is written;
+// for swiglu the weight box interleaves 16 gate rows with the 16 up rows of the
+// same features, which puts both sums of a feature into one warp's lanes.
+//
+// Roles per CTA (320 threads): warp 0 producer (lane 0 the weight box, every
+// lane a gather of four rows), warp 1 MMA issue (even CTA), warps 2-9 epilogue.
+// Every wait is bounded (ptx.cuh).
+#include <cuda_bf16.h>
+
+#include <atomic>
+
+#include "grouped.cuh"
+#include "internal.h"
+
+namespace rnl {
+namespace {
+
+using namespace gemm;
+using namespace grouped;
+
+__device__ unsigned int g_err_grouped;
+std::atomic<bool> g_launched{false};
+
+constexpr int kTile = 256;                        // rows of a group a tile, at most
+constexpr int kStep = 32;                         // the pair's products take N in steps of 32
+constexpr uint32_t kStageBytes = 2 * kABytes;     // 128 weight rows and up to 128 group rows of 64 bf16
+constexpr int64_t kSlotWords = 2 * 128 * kTile;   // partial sums of one pair: [CTA][column][lane]
+constexpr int kMaxPairs = kMaxPartialSlots - 1;   // the last slot holds the flags
+
+struct __align__(8) Ctrl {
+  uint64_t full[kMaxStages];   // even CTA: both CTAs' loads of a stage
+  uint64_t empty[kMaxStages];  // each CTA: its stage read by the pair's MMAs
+  uint64_t tmem_full[2];       // each CTA: accumulator ready
+  uint64_t tmem_empty[2];      // even CTA: both CTAs' epilogues have read it
+  uint32_t tmem_base;
+  int abort;
+};
+
+__host__ __device__ constexpr size_t table_bytes(int E) { return (static_cast<size_t>(E) + 1) * 8; }
+
+struct Args {
+  const int32_t* offsets;
+  const int32_t* rows;  // may be null
+  int R;                // rows of x
+  int M;                // rows of out
+  int E, N, K;          // N weight rows an expert
+  int stages;
+  __nv_bfloat16* out;
+  float* partial;
+  uint64_t* flags;
+  uint64_t epoch;
+};
+
+template <bool SWIGLU>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_bf16_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                        const Args a) {
+  constexpr int kFeatCta = SWIGLU ? 64 : 128;  // output features a CTA
+  constexpr uint32_t kTmemCols = 512;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t base = (raw_addr + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw_addr);
+  Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + a.stages * kStageBytes);
+  int* off = reinterpret_cast<int*>(ctrl + 1);
+  int* pre = off + a.E + 1;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1;
+  const int num_pairs = gridDim.x >> 1;
+  const int N_out = SWIGLU ? a.N / 2 : a.N;
+  const int num_f = (N_out + 2 * kFeatCta - 1) / (2 * kFeatCta);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      mbar_init(smem_u32(&ctrl->full[s]), 1);
+      mbar_init(smem_u32(&ctrl->empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&ctrl->tmem_full[b]), 1);
+      mbar_init(smem_u32(&ctrl->tmem_empty[b]), 2 * kEpiWarps);
+    }
+    ctrl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&ctrl->tmem_base), kTmemCols);
+    tmem_relinquish_pair();
+  }
+  grid_launch_dependents();
+  grid_dependency_wait();
+  build_groups(a.offsets, a.E, a.M, num_f, kTile, off, pre, &g_err_grouped, 110);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = ctrl->tmem_base;
+  volatile int* abort = &ctrl->abort;
+  const Groups groups{off, pre, a.E, num_f};
+  const int num_kb = (a.K + BK - 1) / BK;
+  const Sched sc(pre[a.E], num_pairs, num_kb);
+  const Walk walk(sc, pair);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      tma_prefetch_map(&map_w);
+      tma_prefetch_map(&map_x);
+    }
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (int it = 0; it < walk.n && ok; ++it) {
+      const Item w = walk.at(sc, it);
+      const Tile t = tile_at<kTile, kStep>(groups, w.tile);
+      const int half = t.n / 2;
+      // this lane's four rows of the CTA's half; rows behind the tile's last one
+      // repeat it (their columns are not stored)
+      const bool has = 4 * lane < half;
+      int4 r = make_int4(0, 0, 0, 0);
+      if (has) {
+        int v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = t.row0 + min(static_cast<int>(rank) * half + 4 * lane + i, t.valid - 1);
+          v[i] = a.rows != nullptr ? a.rows[at] : at;
+          if (v[i] < 0 || v[i] >= a.R) {
+            atomicCAS(&g_err_grouped, 0u, kErrArg | (111u << 8));
+            v[i] = 0;
+          }
+        }
+        r = make_int4(v[0], v[1], v[2], v[3]);
+      }
+      const uint32_t bytes = 2 * kABytes + static_cast<uint32_t>(t.n) * BK * 2;  // of both CTAs
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        bool got = true;
+        if (lane == 0)
+          got = mbar_wait_cluster(smem_u32(&ctrl->empty[stage]), phase ^ 1u, abort, &g_err_grouped, 112);
+        got = __shfl_sync(0xffffffffu, got, 0);
+        if (!got || !RNL_DCHECK(&g_err_grouped, stage < static_cast<uint32_t>(a.stages) && half <= 128, 113)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sa = base + stage * kStageBytes;
+        const uint32_t full_local = smem_u32(&ctrl->full[stage]);
+        const uint32_t full_even = mapa_shared(full_local, 0);
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive_expect_tx(full_local, bytes);
+          const int f0 = (t.f * 2 + static_cast<int>(rank)) * kFeatCta;
+          if constexpr (SWIGLU)
+            tma_load_5d_pair(sa, &map_w, full_even, kb * BK, 0, 0, f0 / 16, t.e);
+          else
+            tma_load_2d_pair(sa, &map_w, full_even, kb * BK, t.e * a.N + f0);
+        }
+        __syncwarp();
+        if (has) tma_gather4_pair(sa + kABytes + lane * 512, &map_x, full_even, kb * BK, r);
+        if (++stage == static_cast<uint32_t>(a.stages)) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issue
+    if (rank == 0 && lane == 0) {
+      uint32_t stage = 0, phase = 0;
+      bool ok = true;
+      for (int it = 0; it < walk.n && ok; ++it) {
+        const Item w = walk.at(sc, it);
+        const Tile t = tile_at<kTile, kStep>(groups, w.tile);
+        const uint32_t buf = it & 1;
+        if (!mbar_wait_cluster(smem_u32(&ctrl->tmem_empty[buf]), ((it >> 1) & 1) ^ 1u, abort, &g_err_grouped, 114))
+          break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + buf * kAccStride;
+        const uint32_t idesc = idesc_bf16(256, t.n);
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (!mbar_wait_cluster(smem_u32(&ctrl->full[stage]), phase, abort, &g_err_grouped, 115)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = base + stage * kStageBytes;
+          const uint64_t adesc = desc_kmajor_sw128(sa);
+          const uint64_t bdesc = desc_kmajor_sw128(sa + kABytes);
+#pragma unroll
+          for (int k = 0; k < BK / 16; ++k)
+            umma_bf16_pair(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, (kb > w.kb0 || k > 0) ? 1u : 0u);
+          umma_commit_pair(smem_u32(&ctrl->empty[stage]), 0x3);
+          if (++stage == static_cast<uint32_t>(a.stages)) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit_pair(smem_u32(&ctrl->tmem_full[buf]), 0x3);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int ew = warp - 2;
+    const int quarter = warp & 3;  // TMEM lanes this warp may access
+    const int half = ew >> 2;      // takes every other 32-column group
+    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t empty_even[2] = {mapa_shared(smem_u32(&ctrl->tmem_empty[0]), 0),
+                                    mapa_shared(smem_u32(&ctrl->tmem_empty[1]), 0)};
+    const int64_t lane_off = static_cast<int64_t>(rank) * 128 * kTile + quarter * 32 + lane;
+    for (int it = 0; it < walk.n; ++it) {
+      const Item w = walk.at(sc, it);
+      const Tile t = tile_at<kTile, kStep>(groups, w.tile);
+      const uint32_t buf = it & 1;
+      bool got = mbar_wait_cluster(smem_u32(&ctrl->tmem_full[buf]), (it >> 1) & 1, abort, &g_err_grouped, 116);
+      if (w.kind == kFinish && got && lane == 0)
+        for (int q = w.first; q < pair && got; ++q)
+          got = flag_wait(a.flags + (static_cast<int64_t>(q) * 2 + rank) * kEpiWarps + ew, a.epoch, abort,
+                          &g_err_grouped, 117);
+      if (!__all_sync(0xffffffffu, got)) break;
+      __syncwarp();  // what lane 0 acquired is every lane's
+      tc_fence_after();
+      const int f0 = (t.f * 2 + static_cast<int>(rank)) * kFeatCta;
+      const int feat = SWIGLU ? f0 + quarter * 16 + (lane & 15) : f0 + quarter * 32 + lane;
+      for (int c = half * 32; c < t.n; c += 64) {
+        uint32_t r[32];
+        tmem_ld_32cols(tmem_base + lane_addr + buf * kAccStride + c, r);
+        tmem_ld_wait();
+        if (!RNL_DCHECK(&g_err_grouped, c + 32 <= kTile && t.row0 + t.valid <= a.M && pair < kMaxPairs, 118)) continue;
+        if (w.kind == kPartial) {
+          float* dst = a.partial + pair * kSlotWords + lane_off + static_cast<int64_t>(c) * 128;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) dst[j * 128] = __uint_as_float(r[j]);
+          continue;
+        }
+        for (int q = w.first; q < pair; ++q) {  // the lower workers' parts, in their order
+          const float* src = a.partial + q * kSlotWords + lane_off + static_cast<int64_t>(c) * 128;
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __ldcg(src + j * 128);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + v[j]);
+        }
+        if constexpr (SWIGLU)
+          store_cols_swiglu(a.out, N_out, t.row0, t.valid, c, feat, lane, r);
+        else
+          store_cols(a.out, N_out, t.row0, t.valid, c, feat, lane, r);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0)
+          mbar_arrive(smem_u32(&ctrl->tmem_empty[buf]));
+        else
+          mbar_arrive_cluster(empty_even[buf]);
+        // a flag is consumed by one warp, which sets it back, so that a replayed
+        // graph waits for its own
+        for (int q = w.first; q < pair; ++q) a.flags[(static_cast<int64_t>(q) * 2 + rank) * kEpiWarps + ew] = 0;
+      }
+      if (w.kind == kPartial) {
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) flag_release(a.flags + (static_cast<int64_t>(pair) * 2 + rank) * kEpiWarps + ew, a.epoch);
+      }
+    }
+  }
+
+  // a CTA that gave up on a wait lets the copies and products in flight end
+  if (*abort) {
+    const unsigned long long t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 100000ull) __nanosleep(1000);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+// CTA pairs that are resident at once (all of the grid is).
+template <bool SWIGLU>
+int resident_pairs(const DeviceInfo& dev, size_t smem) {
+  static std::atomic<int> cached[64];
+  const int c = cached[dev.device].load(std::memory_order_relaxed);
+  if (c > 0) return c;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (dev.sm_count / 2), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, grouped_bf16_kernel<SWIGLU>, &cfg) != cudaSuccess) n = 0;
+  cudaGetLastError();
+  if (n <= 0 || n > dev.sm_count / 2) n = dev.sm_count / 2;
+  if (n > kMaxPairs) n = kMaxPairs;
+  cached[dev.device].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+template <bool SWIGLU>
+rnl_status launch(const GroupedArgs& g, const DeviceInfo& dev, cudaStream_t s) {
+  auto kern = grouped_bf16_kernel<SWIGLU>;
+  const size_t fixed = 1024 + sizeof(Ctrl) + table_bytes(static_cast<int>(g.E));
+  const size_t fit = (kSmemLimit - fixed) / kStageBytes;
+  const int stages = static_cast<int>(fit < static_cast<size_t>(kMaxStages) ? fit : kMaxStages);
+  const size_t smem = fixed + stages * kStageBytes;
+  if (ensure_smem_attr(reinterpret_cast<const void*>(kern), dev.device, kSmemLimit) != RNL_OK) return RNL_ERR_LAUNCH;
+  CUtensorMap mw, mx;
+  const uint64_t N = g.N, K = g.K;
+  rnl_status st;
+  if (SWIGLU) {
+    // [expert][16 features][gate / up][feature][k]: 64 features' gate and up rows in groups of 16
+    const uint64_t dims[5] = {K, 16, 2, N / 32, static_cast<uint64_t>(g.E)};
+    const uint64_t strides[4] = {2 * K, N * K, 32 * K, 2 * N * K};
+    const uint32_t box[5] = {BK, 16, 2, 4, 1};
+    st = make_map_5d(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.w, dims, strides, box, true);
+  } else {
+    st = make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.w, K, g.E * N, 2 * K, BK, 128);
+  }
+  if (st != RNL_OK) return st;
+  st = make_map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.x, K, g.R, 2 * K, BK, 1);
+  if (st != RNL_OK) return st;
+  Args a;
+  a.offsets = g.offsets;
+  a.rows = g.rows;
+  a.R = static_cast<int>(g.R);
+  a.M = static_cast<int>(g.M);
+  a.E = static_cast<int>(g.E);
+  a.N = static_cast<int>(g.N);
+  a.K = static_cast<int>(g.K);
+  a.stages = stages;
+  a.out = static_cast<__nv_bfloat16*>(g.out);
+  a.partial = static_cast<float*>(g.ws);
+  a.flags = reinterpret_cast<uint64_t*>(a.partial + kMaxPairs * kSlotWords);
+  a.epoch = next_flag_epoch();
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(resident_pairs<SWIGLU>(dev, smem)), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  trace_before(s);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mw, mx, a);
+  trace_after(s, SWIGLU ? "grouped_bf16_swiglu" : "grouped_bf16");
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return RNL_ERR_LAUNCH;
+  }
+  return RNL_OK;
+}
+
+}  // namespace
+
+rnl_status launch_grouped_bf16(const GroupedArgs& g, cudaStream_t s) {
+  if (g.M == 0) return RNL_OK;
+  DeviceInfo dev;
+  const rnl_status st = current_device(&dev);
+  if (st != RNL_OK) return st;
+  g_launched.store(true, std::memory_order_relaxed);
+  return g.swiglu ? launch<true>(g, dev, s) : launch<false>(g, dev, s);
+}
+
+rnl_status read_clear_error_grouped(unsigned int* word) {
+  if (!g_launched.load(std::memory_order_relaxed)) return RNL_OK;
+  unsigned int v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_err_grouped, sizeof v) != cudaSuccess) return RNL_ERR_LAUNCH;
+  if (v != 0 && cudaMemcpyToSymbol(g_err_grouped, &zero, sizeof zero) != cudaSuccess) return RNL_ERR_LAUNCH;
+  *word = v;
+  return RNL_OK;
+}
+
+}  // namespace rnl

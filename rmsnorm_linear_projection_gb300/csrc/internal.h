@@ -34,6 +34,11 @@ rnl_status make_map_2d_plain(CUtensorMap* map, CUtensorMapDataType dtype, const 
                              uint64_t inner, uint64_t outer, uint64_t row_bytes,
                              uint32_t box_inner, uint32_t box_outer);
 
+// 5-D map (dims and box innermost first, strides of dimensions 1 .. 4 in bytes),
+// with the 128-byte swizzle or none.
+rnl_status make_map_5d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, const uint64_t (&dims)[5],
+                       const uint64_t (&strides)[4], const uint32_t (&box)[5], bool swizzle);
+
 // Raises a kernel's dynamic shared-memory limit on `device` (the current one)
 // to at least `bytes`: set on a (kernel, device)'s first call and again only
 // when a call needs more than was set; thread-safe.  The cache outlives a
@@ -212,6 +217,38 @@ size_t kv4_attn_workspace_bytes(int64_t T, int64_t D, int64_t G);
 rnl_status launch_kv4_attention(const Kv4AttnArgs& a, const rnl_kv4_cache& c, const rnl_kv4_seqs& q,
                                 cudaStream_t s);
 
+// ---- rows into MXFP8 (mxquant.cu) ----
+// norm false: x's rows as they are (residual, x_sum, gamma null).  K a multiple
+// of block, at most 65536; x_sum may be x or residual.
+rnl_status launch_quant_mxfp8(const void* x, const void* residual, void* x_sum, const void* gamma, int64_t T,
+                              int64_t K, bool norm, float eps, int mode, int64_t block, uint8_t* codes,
+                              uint8_t* scale, cudaStream_t s);
+
+// ---- tokens to experts and back (moe.cu) ----
+size_t moe_route_workspace_bytes(int64_t T, int64_t E);
+rnl_status launch_moe_route(const float* logits, int64_t T, int64_t E, int64_t k, int renorm, int32_t* ids,
+                            float* weights, int32_t* offsets, int32_t* rows, int32_t* slots, void* ws,
+                            cudaStream_t s);
+rnl_status launch_moe_combine(const void* y, int64_t M, int64_t N, const int32_t* slots, const float* weights,
+                              int64_t T, int64_t k, const void* residual, void* out, cudaStream_t s);
+
+// ---- products grouped by expert (grouped.cu, groupedmx.cu) ----
+struct GroupedArgs {
+  const void* x = nullptr;  // bf16 or E4M3 [R, K]
+  const uint8_t* x_scale = nullptr;
+  int64_t R = 0;
+  const void* w = nullptr;  // bf16 or E4M3 [E, N, K]
+  const uint8_t* w_scale = nullptr;
+  int64_t E = 0, N = 0, K = 0, block = 0;
+  const int32_t* offsets = nullptr;
+  const int32_t* rows = nullptr;  // may be null
+  int64_t M = 0;
+  bool swiglu = false;
+  void* out = nullptr;  // bf16 [M, N] ([M, N / 2] with swiglu)
+  void* ws = nullptr;
+};
+rnl_status launch_grouped_bf16(const GroupedArgs& g, cudaStream_t s);
+
 // ---- tcgen05 GEMM (gemm_tc.cu) ----
 enum class Epi : int {
   kBf16 = 0,         // out bf16 = acc
@@ -323,7 +360,7 @@ rnl_status launch_skinny(const void* x, const void* W, int64_t T, int64_t K, int
 
 // ---- device error words (one per kernel module) ----
 // A read takes about 8 us, so the modules that a program need not use (the
-// last four) leave *word alone until one of their kernels has been launched.
+// last six) leave *word alone until one of their kernels has been launched.
 rnl_status read_clear_error_rowwise(unsigned int* word);
 rnl_status read_clear_error_gemm(unsigned int* word);
 rnl_status read_clear_error_skinny(unsigned int* word);
@@ -338,6 +375,8 @@ rnl_status read_clear_error_axes(unsigned int* word);
 rnl_status read_clear_error_kv4cache(unsigned int* word);
 rnl_status read_clear_error_kv4attn(unsigned int* word);
 rnl_status read_clear_error_kv4prompt(unsigned int* word);
+rnl_status read_clear_error_moe(unsigned int* word);
+rnl_status read_clear_error_grouped(unsigned int* word);
 // Reads and clears all of them without synchronising (api.cu): RNL_OK, or
 // RNL_ERR_TIMEOUT / RNL_ERR_ARG with the first recorded site in *site
 // (optional).
