@@ -1273,6 +1273,7 @@ static rnl_status check_grouped(const GroupedArgs& g, size_t workspace_bytes, bo
   if (bad_dim(g.R) || bad_dim(g.E) || bad_dim(g.N) || bad_dim(g.K) || bad_dim(g.M) || g.E == 0 || g.N == 0 ||
       g.K == 0 || bad_dim(g.E * g.N) || (!g.rows && g.R != g.M))
     return RNL_ERR_SHAPE;
+  if (g.K > RNL_GROUPED_MAX_K) return RNL_ERR_SHAPE;
   if (g.E > RNL_MOE_MAX_EXPERTS || (g.swiglu && g.N % 32 != 0)) return RNL_ERR_UNSUPPORTED;
   if (g.M == 0) return RNL_OK;
   if (g.R == 0) return RNL_ERR_SHAPE;  // rows of nothing

@@ -5,13 +5,17 @@
 //
 // on CTA pairs (tcgen05.mma.cta_group::2): a unit is 256 weight rows (128 a
 // CTA, the M side) against a tile of up to 256 rows of the group (the N side,
-// half of them staged by each CTA), see grouped.cuh.  The group's rows are
-// fetched by TMA gathers of four rows, so that no sorted copy of x is written;
-// for swiglu the weight box interleaves 16 gate rows with the 16 up rows of the
+// half of them staged by each CTA), see grouped.cuh.  The rows named by `rows` are
+// gathered while they are staged (16-byte asynchronous copies by four warps),
+// so that no sorted copy of x is written.  Measured against it: TMA gathers of
+// four rows take 54 cycles each, and a stage that the tensor cores read in 512
+// cycles needs 32 of them (32768 x 2048 -> 2816 over 32 experts: 541 against 277
+// us); rows that stand in order anyway by TMA boxes, 4096 x 4096 -> 4864: 115
+// against 103 us.  For swiglu the weight box interleaves 16 gate rows with the 16 up rows of the
 // same features, which puts both sums of a feature into one warp's lanes.
 //
-// Roles per CTA (320 threads): warp 0 producer (lane 0 the weight box, every
-// lane a gather of four rows), warp 1 MMA issue (even CTA), warps 2-9 epilogue.
+// Roles per CTA (480 threads): warp 0 weight boxes (TMA), warp 1 MMA issue (even CTA),
+// warps 2-9 epilogue, warps 10-13 gathers, warp 14 their hand-over.
 // Every wait is bounded (ptx.cuh).
 #include <cuda_bf16.h>
 
@@ -35,9 +39,14 @@ constexpr uint32_t kStageBytes = 2 * kABytes;     // 128 weight rows and up to 1
 constexpr int64_t kSlotWords = 2 * 128 * kTile;   // partial sums of one pair: [CTA][column][lane]
 constexpr int kMaxPairs = kMaxPartialSlots - 1;   // the last slot holds the flags
 
+constexpr int kGatherWarps = 4;                   // 32 of the CTA's rows each
+constexpr int kRelayWarp = 2 + kEpiWarps + kGatherWarps;
+constexpr int kThreadsG = (kRelayWarp + 1) * 32;
+
 struct __align__(8) Ctrl {
   uint64_t full[kMaxStages];   // even CTA: both CTAs' loads of a stage
   uint64_t empty[kMaxStages];  // each CTA: its stage read by the pair's MMAs
+  uint64_t landed[kMaxStages];  // each CTA: its gathered rows of a stage
   uint64_t tmem_full[2];       // each CTA: accumulator ready
   uint64_t tmem_empty[2];      // even CTA: both CTAs' epilogues have read it
   uint32_t tmem_base;
@@ -47,6 +56,7 @@ struct __align__(8) Ctrl {
 __host__ __device__ constexpr size_t table_bytes(int E) { return (static_cast<size_t>(E) + 1) * 8; }
 
 struct Args {
+  const __nv_bfloat16* x;
   const int32_t* offsets;
   const int32_t* rows;  // may be null
   int R;                // rows of x
@@ -60,9 +70,8 @@ struct Args {
 };
 
 template <bool SWIGLU>
-__global__ void __launch_bounds__(kThreads, 1)
-    grouped_bf16_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-                        const Args a) {
+__global__ void __launch_bounds__(kThreadsG, 1)
+    grouped_bf16_kernel(const __grid_constant__ CUtensorMap map_w, const Args a) {
   constexpr int kFeatCta = SWIGLU ? 64 : 128;  // output features a CTA
   constexpr uint32_t kTmemCols = 512;
   extern __shared__ uint8_t smem_raw[];
@@ -80,10 +89,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int num_pairs = gridDim.x >> 1;
   const int N_out = SWIGLU ? a.N / 2 : a.N;
   const int num_f = (N_out + 2 * kFeatCta - 1) / (2 * kFeatCta);
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(smem_u32(&ctrl->full[s]), 1);
+      mbar_init(smem_u32(&ctrl->full[s]), 3);  // the weight's bytes, and each CTA's rows
+      mbar_init(smem_u32(&ctrl->landed[s]), kGatherWarps * 32);
       mbar_init(smem_u32(&ctrl->empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -109,104 +118,149 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Groups groups{off, pre, a.E, num_f};
   const int num_kb = (a.K + BK - 1) / BK;
   const Sched sc(pre[a.E], num_pairs, num_kb);
-  const Walk walk(sc, pair);
+  Walk<kTile, kStep> walk(sc, groups, pair, lane);
 
   if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      tma_prefetch_map(&map_w);
-      tma_prefetch_map(&map_x);
-    }
+    // ------------------------------------------------------- weight producer
+    if (lane == 0) tma_prefetch_map(&map_w);
     uint32_t stage = 0, phase = 0;
     bool ok = true;
     for (int it = 0; it < walk.n && ok; ++it) {
-      const Item w = walk.at(sc, it);
-      const Tile t = tile_at<kTile, kStep>(groups, w.tile);
-      const int half = t.n / 2;
-      // this lane's four rows of the CTA's half; rows behind the tile's last one
-      // repeat it (their columns are not stored)
-      const bool has = 4 * lane < half;
-      int4 r = make_int4(0, 0, 0, 0);
-      if (has) {
-        int v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int at = t.row0 + min(static_cast<int>(rank) * half + 4 * lane + i, t.valid - 1);
-          v[i] = a.rows != nullptr ? a.rows[at] : at;
-          if (v[i] < 0 || v[i] >= a.R) {
-            atomicCAS(&g_err_grouped, 0u, kErrArg | (111u << 8));
-            v[i] = 0;
+      const Item w = walk.at(it);
+      if (lane == 0) {
+        const int f0 = (w.t.f * 2 + static_cast<int>(rank)) * kFeatCta;
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (!mbar_wait_cluster(smem_u32(&ctrl->empty[stage]), phase ^ 1u, abort, &g_err_grouped, 112) ||
+              !RNL_DCHECK(&g_err_grouped, stage < static_cast<uint32_t>(a.stages), 113)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sa = base + stage * kStageBytes;
+          const uint32_t full_local = smem_u32(&ctrl->full[stage]);
+          const uint32_t full_even = mapa_shared(full_local, 0);
+          if (rank == 0) mbar_arrive_expect_tx(full_local, 2 * kABytes);  // both CTAs' boxes
+          if constexpr (SWIGLU)
+            tma_load_5d_pair(sa, &map_w, full_even, kb * BK, 0, 0, f0 / 16, w.t.e);
+          else
+            tma_load_2d_pair(sa, &map_w, full_even, kb * BK, w.t.e * a.N + f0);
+          if (++stage == static_cast<uint32_t>(a.stages)) {
+            stage = 0;
+            phase ^= 1u;
           }
         }
-        r = make_int4(v[0], v[1], v[2], v[3]);
       }
-      const uint32_t bytes = 2 * kABytes + static_cast<uint32_t>(t.n) * BK * 2;  // of both CTAs
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+  } else if (warp == kRelayWarp) {
+    // --------------------------------------------------------------- relay
+    // hands a stage's rows to the tensor cores.  Not by the warps that copy:
+    // their fence would wait for every copy that they have in flight
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (int it = 0; it < walk.n && ok; ++it) {
+      const Item w = walk.at(it);
+      if (lane == 0) {
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (!mbar_wait(smem_u32(&ctrl->landed[stage]), phase, abort, &g_err_grouped, 108)) {
+            ok = false;
+            break;
+          }
+          fence_proxy_async_shared();
+          const uint32_t full_local = smem_u32(&ctrl->full[stage]);
+          if (rank == 0)
+            mbar_arrive(full_local);
+          else
+            mbar_arrive_remote(mapa_shared(full_local, 0));
+          if (++stage == static_cast<uint32_t>(a.stages)) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+  } else if (warp >= 2 + kEpiWarps) {
+    // ------------------------------------------------------------- gathers
+    // each warp brings 32 of the CTA's rows, 16 bytes a lane and copy, to where a
+    // TMA load with the 128-byte swizzle would put them
+    const int gw = warp - (2 + kEpiWarps);
+    const int sub = lane >> 3, chunk = lane & 7;
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (int it = 0; it < walk.n && ok; ++it) {
+      const Item w = walk.at(it);
+      const int half = w.t.n / 2;
+      const int first = static_cast<int>(rank) * half + gw * 32 + sub;
+      const __nv_bfloat16* src[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // rows behind the tile's last one repeat it (their columns are not stored)
+        int v = w.t.row0 + min(first + 4 * i, w.t.valid - 1);
+        if (a.rows != nullptr) v = a.rows[v];
+        if (v < 0 || v >= a.R) {
+          atomicCAS(&g_err_grouped, 0u, kErrArg | (111u << 8));
+          v = 0;
+        }
+        src[i] = a.x + static_cast<int64_t>(v) * a.K + chunk * 8;
+      }
       for (int kb = w.kb0; kb < w.kb1; ++kb) {
-        bool got = true;
-        if (lane == 0)
-          got = mbar_wait_cluster(smem_u32(&ctrl->empty[stage]), phase ^ 1u, abort, &g_err_grouped, 112);
-        got = __shfl_sync(0xffffffffu, got, 0);
-        if (!got || !RNL_DCHECK(&g_err_grouped, stage < static_cast<uint32_t>(a.stages) && half <= 128, 113)) {
+        const bool got = mbar_wait_cluster(smem_u32(&ctrl->empty[stage]), phase ^ 1u, abort, &g_err_grouped, 119);
+        if (!__all_sync(0xffffffffu, got && RNL_DCHECK(&g_err_grouped, half <= 128, 109))) {
           ok = false;
           break;
         }
-        const uint32_t sa = base + stage * kStageBytes;
-        const uint32_t full_local = smem_u32(&ctrl->full[stage]);
-        const uint32_t full_even = mapa_shared(full_local, 0);
-        if (lane == 0) {
-          if (rank == 0) mbar_arrive_expect_tx(full_local, bytes);
-          const int f0 = (t.f * 2 + static_cast<int>(rank)) * kFeatCta;
-          if constexpr (SWIGLU)
-            tma_load_5d_pair(sa, &map_w, full_even, kb * BK, 0, 0, f0 / 16, t.e);
-          else
-            tma_load_2d_pair(sa, &map_w, full_even, kb * BK, t.e * a.N + f0);
-        }
-        __syncwarp();
-        if (has) tma_gather4_pair(sa + kABytes + lane * 512, &map_x, full_even, kb * BK, r);
+        const uint32_t dst = base + stage * kStageBytes + kABytes + (gw * 32 + sub) * 128;
+        const int k0 = kb * BK;
+        const uint32_t bytes = k0 + chunk * 8 < a.K ? 16u : 0u;
+        const int from = bytes ? k0 : -chunk * 8;  // an address inside the row where nothing is read
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (gw * 32 + 4 * i < half)  // (row & 7) = sub + 4 (i & 1)
+            cp_async_16(dst + i * 512 + ((chunk ^ (sub + 4 * (i & 1))) << 4), src[i] + from, bytes);
+        cp_async_arrive(smem_u32(&ctrl->landed[stage]));
         if (++stage == static_cast<uint32_t>(a.stages)) {
           stage = 0;
           phase ^= 1u;
         }
       }
     }
-    __syncwarp();
+    cp_async_wait_all();  // nothing in flight when the warp leaves
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issue
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       uint32_t stage = 0, phase = 0;
       bool ok = true;
       for (int it = 0; it < walk.n && ok; ++it) {
-        const Item w = walk.at(sc, it);
-        const Tile t = tile_at<kTile, kStep>(groups, w.tile);
-        const uint32_t buf = it & 1;
-        if (!mbar_wait_cluster(smem_u32(&ctrl->tmem_empty[buf]), ((it >> 1) & 1) ^ 1u, abort, &g_err_grouped, 114))
-          break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + buf * kAccStride;
-        const uint32_t idesc = idesc_bf16(256, t.n);
-        for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (!mbar_wait_cluster(smem_u32(&ctrl->full[stage]), phase, abort, &g_err_grouped, 115)) {
-            ok = false;
-            break;
-          }
+        const Item w = walk.at(it);
+        if (lane == 0) {
+          const uint32_t buf = it & 1;
+          ok = mbar_wait_cluster(smem_u32(&ctrl->tmem_empty[buf]), ((it >> 1) & 1) ^ 1u, abort, &g_err_grouped, 114);
           tc_fence_after();
-          const uint32_t sa = base + stage * kStageBytes;
-          const uint64_t adesc = desc_kmajor_sw128(sa);
-          const uint64_t bdesc = desc_kmajor_sw128(sa + kABytes);
+          const uint32_t d_tmem = tmem_base + buf * kAccStride;
+          const uint32_t idesc = idesc_bf16(256, w.t.n);
+          for (int kb = w.kb0; kb < w.kb1 && ok; ++kb) {
+            if (!mbar_wait_cluster(smem_u32(&ctrl->full[stage]), phase, abort, &g_err_grouped, 115)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = base + stage * kStageBytes;
+            const uint64_t adesc = desc_kmajor_sw128(sa);
+            const uint64_t bdesc = desc_kmajor_sw128(sa + kABytes);
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k)
-            umma_bf16_pair(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, (kb > w.kb0 || k > 0) ? 1u : 0u);
-          umma_commit_pair(smem_u32(&ctrl->empty[stage]), 0x3);
-          if (++stage == static_cast<uint32_t>(a.stages)) {
-            stage = 0;
-            phase ^= 1u;
+            for (int k = 0; k < BK / 16; ++k)
+              umma_bf16_pair(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, (kb > w.kb0 || k > 0) ? 1u : 0u);
+            umma_commit_pair(smem_u32(&ctrl->empty[stage]), 0x3);
+            if (++stage == static_cast<uint32_t>(a.stages)) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
+          if (ok) umma_commit_pair(smem_u32(&ctrl->tmem_full[buf]), 0x3);
         }
-        if (!ok) break;
-        umma_commit_pair(smem_u32(&ctrl->tmem_full[buf]), 0x3);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
       }
     }
-    __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
     const int ew = warp - 2;
@@ -217,8 +271,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     mapa_shared(smem_u32(&ctrl->tmem_empty[1]), 0)};
     const int64_t lane_off = static_cast<int64_t>(rank) * 128 * kTile + quarter * 32 + lane;
     for (int it = 0; it < walk.n; ++it) {
-      const Item w = walk.at(sc, it);
-      const Tile t = tile_at<kTile, kStep>(groups, w.tile);
+      const Item w = walk.at(it);
+      const Tile& t = w.t;
       const uint32_t buf = it & 1;
       bool got = mbar_wait_cluster(smem_u32(&ctrl->tmem_full[buf]), (it >> 1) & 1, abort, &g_err_grouped, 116);
       if (w.kind == kFinish && got && lane == 0)
@@ -260,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (rank == 0)
           mbar_arrive(smem_u32(&ctrl->tmem_empty[buf]));
         else
-          mbar_arrive_cluster(empty_even[buf]);
+          mbar_arrive_remote(empty_even[buf]);  // (what it orders are reads of TMEM)
         // a flag is consumed by one warp, which sets it back, so that a replayed
         // graph waits for its own
         for (int q = w.first; q < pair; ++q) a.flags[(static_cast<int64_t>(q) * 2 + rank) * kEpiWarps + ew] = 0;
@@ -300,7 +354,7 @@ int resident_pairs(const DeviceInfo& dev, size_t smem) {
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (dev.sm_count / 2), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(kThreadsG, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -321,7 +375,7 @@ rnl_status launch(const GroupedArgs& g, const DeviceInfo& dev, cudaStream_t s) {
   const int stages = static_cast<int>(fit < static_cast<size_t>(kMaxStages) ? fit : kMaxStages);
   const size_t smem = fixed + stages * kStageBytes;
   if (ensure_smem_attr(reinterpret_cast<const void*>(kern), dev.device, kSmemLimit) != RNL_OK) return RNL_ERR_LAUNCH;
-  CUtensorMap mw, mx;
+  CUtensorMap mw;
   const uint64_t N = g.N, K = g.K;
   rnl_status st;
   if (SWIGLU) {
@@ -334,9 +388,8 @@ rnl_status launch(const GroupedArgs& g, const DeviceInfo& dev, cudaStream_t s) {
     st = make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.w, K, g.E * N, 2 * K, BK, 128);
   }
   if (st != RNL_OK) return st;
-  st = make_map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.x, K, g.R, 2 * K, BK, 1);
-  if (st != RNL_OK) return st;
   Args a;
+  a.x = static_cast<const __nv_bfloat16*>(g.x);
   a.offsets = g.offsets;
   a.rows = g.rows;
   a.R = static_cast<int>(g.R);
@@ -358,13 +411,13 @@ rnl_status launch(const GroupedArgs& g, const DeviceInfo& dev, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * static_cast<unsigned>(resident_pairs<SWIGLU>(dev, smem)), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(kThreadsG, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   trace_before(s);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mw, mx, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mw, a);
   trace_after(s, SWIGLU ? "grouped_bf16_swiglu" : "grouped_bf16");
   if (e != cudaSuccess) {
     cudaGetLastError();

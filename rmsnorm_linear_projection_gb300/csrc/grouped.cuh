@@ -119,7 +119,8 @@ struct Sched {
   int units;
   int dp;      // tiles that go whole
   int sk;      // tiles whose k-blocks are cut into ranges
-  int sk_units;  // workers that get a range
+  int sk_units;  // workers that get a range: share k-blocks, the first `more` of them one more
+  int share, more;
   int num_kb;
   __device__ __forceinline__ Sched(int tiles, int workers, int kbs) {
     units = workers;
@@ -127,29 +128,35 @@ struct Sched {
     dp = tiles >= 2 * workers ? (tiles / workers - 1) * workers : 0;
     sk = tiles - dp;
     // a range of fewer than 4 k-blocks is not worth its joining
-    const int64_t most = static_cast<int64_t>(sk) * kbs / 4;
-    sk_units = most < 1 ? 1 : (most < workers ? static_cast<int>(most) : workers);
+    const int total = sk * kbs;  // below 2^31: sk < 2 * 128, K at most RNL_GROUPED_MAX_K
+    sk_units = max(1, min(total / 4, workers));
+    share = total / sk_units;
+    more = total - share * sk_units;
   }
-  __device__ __forceinline__ int64_t start(int u) const {
-    return static_cast<int64_t>(u) * sk * num_kb / sk_units;
-  }
+  // first k-block (of the flattened sk tiles) of worker u's range
+  __device__ __forceinline__ int start(int u) const { return u * share + min(u, more); }
 };
 
 enum : int { kWhole = 0, kFinish = 1, kPartial = 2 };
 
+// What a worker does to one tile: k-blocks [kb0, kb1) of it.
 struct Item {
-  int tile, kb0, kb1, kind;
-  int first;  // kFinish: the lowest worker that holds a part of the tile
+  Tile t;
+  int kb0, kb1, kind;
+  int first;  // kFinish: the lowest worker that holds a part of the tile (else the worker itself)
 };
 
-// The items of one worker, in order.
+// The items of one worker, in order.  A warp works out 32 items at once, one a
+// lane, and hands them round: one by one they cost each role about 0.8 us a tile.
+template <int kTile, int kStep>
 struct Walk {
+  const Sched& s;
+  const Groups& g;
   int n;
-  int unit, n_sk, n_dp, tile_lo;
-  int64_t u0, u1;
+  int unit, n_sk, n_dp, tile_lo, u0, u1, lane;
   bool fin_last;
-  __device__ __forceinline__ Walk(const Sched& s, int u) {
-    unit = u;
+  Item mine;
+  __device__ __forceinline__ Walk(const Sched& sc, const Groups& gr, int u, int ln) : s(sc), g(gr), unit(u), lane(ln) {
     n_dp = u < s.dp ? (s.dp - u + s.units - 1) / s.units : 0;
     n_sk = 0;
     u0 = u1 = 0;
@@ -159,15 +166,14 @@ struct Walk {
       u0 = s.start(u);
       u1 = s.start(u + 1);
       if (u1 > u0) {
-        tile_lo = static_cast<int>(u0 / s.num_kb);
-        n_sk = static_cast<int>((u1 - 1) / s.num_kb) - tile_lo + 1;
-        fin_last = u0 > static_cast<int64_t>(tile_lo) * s.num_kb &&
-                   u1 >= static_cast<int64_t>(tile_lo + 1) * s.num_kb;
+        tile_lo = u0 / s.num_kb;
+        n_sk = (u1 - 1) / s.num_kb - tile_lo + 1;
+        fin_last = u0 > tile_lo * s.num_kb && u1 >= (tile_lo + 1) * s.num_kb;
       }
     }
     n = n_sk + n_dp;
   }
-  __device__ __forceinline__ Item at(const Sched& s, int it) const {
+  __device__ __forceinline__ Item make(int it) const {
     Item w;
     w.first = unit;
     int j;  // index among the range's tiles, highest first
@@ -175,7 +181,7 @@ struct Walk {
     if (it < early) {
       j = it;
     } else if (it < early + n_dp) {
-      w.tile = unit + (it - early) * s.units;
+      w.t = tile_at<kTile, kStep>(g, unit + (it - early) * s.units);
       w.kb0 = 0;
       w.kb1 = s.num_kb;
       w.kind = kWhole;
@@ -184,10 +190,10 @@ struct Walk {
       j = n_sk - 1;
     }
     const int t = tile_lo + (n_sk - 1 - j);
-    const int64_t ts = static_cast<int64_t>(t) * s.num_kb;
-    w.tile = s.dp + t;
-    w.kb0 = static_cast<int>(u0 > ts ? u0 - ts : 0);
-    w.kb1 = static_cast<int>(u1 < ts + s.num_kb ? u1 - ts : s.num_kb);
+    const int ts = t * s.num_kb;
+    w.t = tile_at<kTile, kStep>(g, s.dp + t);
+    w.kb0 = max(u0 - ts, 0);
+    w.kb1 = min(u1 - ts, s.num_kb);
     w.kind = w.kb1 < s.num_kb ? kPartial : (w.kb0 > 0 ? kFinish : kWhole);
     if (w.kind == kFinish) {
       int q = unit - 1;
@@ -196,30 +202,68 @@ struct Walk {
     }
     return w;
   }
+  // Item `it`, the same on every lane; called by the whole warp, for it = 0, 1, ...
+  __device__ __forceinline__ Item at(int it) {
+    if ((it & 31) == 0 && it + lane < n) mine = make(it + lane);
+    Item w;
+    const int from = it & 31;
+    w.t.e = __shfl_sync(0xffffffffu, mine.t.e, from);
+    w.t.f = __shfl_sync(0xffffffffu, mine.t.f, from);
+    w.t.row0 = __shfl_sync(0xffffffffu, mine.t.row0, from);
+    w.t.valid = __shfl_sync(0xffffffffu, mine.t.valid, from);
+    w.t.n = (w.t.valid + kStep - 1) / kStep * kStep;
+    w.kb0 = __shfl_sync(0xffffffffu, mine.kb0, from);
+    w.kb1 = __shfl_sync(0xffffffffu, mine.kb1, from);
+    w.kind = __shfl_sync(0xffffffffu, mine.kind, from);
+    w.first = __shfl_sync(0xffffffffu, mine.first, from);
+    return w;
+  }
 };
 
-// x * sigmoid(x) * u; the exponential is good to a few units of FP32's last
-// place times |g|, far inside the bf16 rounding that follows.
-__device__ __forceinline__ float swiglu_of(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+// g * sigmoid(g) * u.  The exponential is good to a few units of FP32's last place
+// times |g|, the reciprocal to one, both far inside the bf16 rounding that
+// follows; a correctly rounded division here has a branch, which kept the
+// columns of a thread from overlapping.  Where sigmoid(g) is below 2^-126 (g < -87)
+// the product is 0.
+__device__ __forceinline__ float swiglu_of(float g, float u) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-g)));
+  return g * r * u;
+}
+
+// Stores words w[i] at dst + i * step, i < n, of the lanes that are on; whole: of
+// all lanes, n = COUNT (no predicates, so that the stores go out back to back).
+template <int COUNT>
+__device__ __forceinline__ void store_words(__nv_bfloat16* dst, int64_t step, const uint32_t (&w)[COUNT], bool on,
+                                            int n) {
+  if (__all_sync(0xffffffffu, on && n >= COUNT)) {
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) *reinterpret_cast<uint32_t*>(dst + i * step) = w[i];
+  } else if (on) {
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i)
+      if (i < n) *reinterpret_cast<uint32_t*>(dst + i * step) = w[i];
+  }
+}
 
 // Writes 32 columns (rows row0 + col .. of the output) of a warp's 32 TMEM
 // lanes (32 weight rows; feat: the lane's feature) as bf16.  Neighbouring lanes
-// exchange a value each, so that every store takes two features of one row.
+// exchange a value each, so that every store takes two features of one row; all
+// exchanges come before the stores (one by one in turn they took 130 cycles
+// each).
 __device__ __forceinline__ void store_cols(__nv_bfloat16* __restrict__ out, int N, int64_t row0, int valid, int col,
                                            int feat, int lane, const uint32_t (&r)[32]) {
   if ((N & 1) == 0) {
-    const bool odd = lane & 1;
-    // the column pair's first row for even lanes, its second one for odd ones
-    __nv_bfloat16* dst = out + (row0 + col + (odd ? 1 : 0)) * N + (feat & ~1);
-    const bool f_ok = (feat | 1) < N;
+    const int odd = lane & 1;  // takes the column pair's second row
+    uint32_t w[16];
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? r[j] : r[j + 1], 1);
-      const uint32_t word = odd ? gemm::bf16x2_bits(__uint_as_float(got), __uint_as_float(r[j + 1]))
-                                : gemm::bf16x2_bits(__uint_as_float(r[j]), __uint_as_float(got));
-      if (f_ok && col + j + (odd ? 1 : 0) < valid)
-        *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(j) * N) = word;
+    for (int j = 0; j < 16; ++j) {
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? r[2 * j] : r[2 * j + 1], 1);
+      w[j] = odd ? gemm::bf16x2_bits(__uint_as_float(got), __uint_as_float(r[2 * j + 1]))
+                 : gemm::bf16x2_bits(__uint_as_float(r[2 * j]), __uint_as_float(got));
     }
+    store_words<16>(out + (row0 + col + odd) * N + (feat & ~1), 2 * static_cast<int64_t>(N), w, (feat | 1) < N,
+                    (valid - col - odd + 1) >> 1);
   } else {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
@@ -235,21 +279,20 @@ __device__ __forceinline__ void store_cols_swiglu(__nv_bfloat16* __restrict__ ou
                                                   int col, int feat, int lane, const uint32_t (&r)[32]) {
   const bool hi = lane & 16, odd = lane & 1;
   const int sub = (hi ? 1 : 0) + (odd ? 2 : 0);  // the row of four that this lane stores
-  __nv_bfloat16* dst = out + (row0 + col + sub) * F + (feat & ~1);
-  const bool f_ok = feat < F;
+  float v[16];
 #pragma unroll
-  for (int j = 0; j < 32; j += 4) {
-    float v[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {  // lanes 0-15 take column j + 2h, lanes 16-31 the next one
-      const uint32_t a = r[j + 2 * h], b = r[j + 2 * h + 1];
-      const float got = __uint_as_float(__shfl_xor_sync(0xffffffffu, hi ? a : b, 16));
-      v[h] = hi ? swiglu_of(got, __uint_as_float(b)) : swiglu_of(__uint_as_float(a), got);
-    }
-    const float got = __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[1], 1);
-    const uint32_t word = odd ? gemm::bf16x2_bits(got, v[1]) : gemm::bf16x2_bits(v[0], got);
-    if (f_ok && col + j + sub < valid) *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(j) * F) = word;
+  for (int j = 0; j < 16; ++j) {  // lanes 0-15 take column 2j, lanes 16-31 the next one
+    const float got = __uint_as_float(__shfl_xor_sync(0xffffffffu, hi ? r[2 * j] : r[2 * j + 1], 16));
+    v[j] = hi ? swiglu_of(got, __uint_as_float(r[2 * j + 1])) : swiglu_of(__uint_as_float(r[2 * j]), got);
   }
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float got = __shfl_xor_sync(0xffffffffu, odd ? v[2 * j] : v[2 * j + 1], 1);
+    w[j] = odd ? gemm::bf16x2_bits(got, v[2 * j + 1]) : gemm::bf16x2_bits(v[2 * j], got);
+  }
+  store_words<8>(out + (row0 + col + sub) * F + (feat & ~1), 4 * static_cast<int64_t>(F), w, feat < F,
+                 (valid - col - sub + 3) >> 2);
 }
 
 }  // namespace grouped
