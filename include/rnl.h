@@ -134,7 +134,7 @@ const char *rnl_status_string(rnl_status s);
  *   RNL_OP_MXFP8:   T, K, N; N2 ignored (rmsnorm_linear_mxfp8 and mxfp8_scaled_mm)
  *   RNL_OP_W8A8_PREPARED: T, K, N; N2 ignored (rmsnorm_linear_w8a8_prepared)
  *   RNL_OP_KV4_ATTENTION: T = rows, K = head_dim, N = n_q_heads, N2 = n_kv_heads
- *   RNL_OP_GROUPED: T = M, K, N, N2 = n_experts (rnl_grouped_linear_bf16)
+ *   RNL_OP_GROUPED: T = M, K, N, N2 = n_experts (rnl_grouped_linear_bf16 and _mxfp8)
  *   RNL_OP_MOE_ROUTE: T, K = top_k, N = n_experts; N2 ignored
  * Returns (size_t)-1 for invalid sizes.  Host-only; needs no GPU.
  */
@@ -589,6 +589,23 @@ rnl_status rnl_grouped_linear_bf16(const void *x, int64_t n_x_rows, const void *
                                    int64_t N, int64_t K, const int32_t *offsets, const int32_t *rows,
                                    int64_t M, int swiglu, void *out, void *workspace,
                                    size_t workspace_bytes, rnl_stream_t stream);
+
+/*
+ * The same on MXFP8 operands (rnl_add_rmsnorm_mxfp8, rnl_quant_mxfp8):
+ *   x_codes E4M3FN bytes [n_x_rows, K];  x_scale E8M0 bytes [n_x_rows, K / block]
+ *   w_codes E4M3FN bytes [n_experts, N, K];  w_scale E8M0 bytes [n_experts, N, K / block]
+ *   block   32 or 64 (else RNL_ERR_ARG), K % block == 0 (else RNL_ERR_SHAPE)
+ * out[i, n] = sum_k value(x code) 2^(x byte - 127) value(w code) 2^(w byte - 127),
+ * accumulated in FP32 on the block-scaled tensor cores.  A scale byte of 255 or a
+ * NaN code makes the outputs that read it NaN.  Everything else as
+ * rnl_grouped_linear_bf16; the scales need no alignment (rows whose K / block is a
+ * multiple of 16 at block 32, of 8 at block 64, are loaded in the fewest pieces).
+ */
+rnl_status rnl_grouped_linear_mxfp8(const uint8_t *x_codes, const uint8_t *x_scale, int64_t n_x_rows,
+                                    const uint8_t *w_codes, const uint8_t *w_scale, int64_t n_experts,
+                                    int64_t N, int64_t K, int64_t block, const int32_t *offsets,
+                                    const int32_t *rows, int64_t M, int swiglu, void *out, void *workspace,
+                                    size_t workspace_bytes, rnl_stream_t stream);
 
 /*
  * The weighted sum of every token's grouped rows:

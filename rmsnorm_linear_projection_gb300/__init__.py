@@ -31,7 +31,7 @@ arguments; the computation runs in the library's CUDA kernels.
     rnl_moe_route, rnl_moe_combine
                           tokens to experts (top-k, weights, rows grouped) and
                           the weighted sum back
-    rnl_grouped_linear_bf16
+    rnl_grouped_linear_bf16, rnl_grouped_linear_mxfp8
                           products grouped by expert with ragged sizes
     rnl_pipeline_*        host-buffer pipeline: calls fed from and answering into
                           pinned host memory, copies overlapped with the kernels
@@ -77,6 +77,7 @@ from ._native import (  # noqa: F401
     rnl_debug_build,
     rnl_gemm_s8s8s32,
     rnl_grouped_linear_bf16,
+    rnl_grouped_linear_mxfp8,
     rnl_head_rmsnorm,
     rnl_kv4_append,
     rnl_kv4_attention,

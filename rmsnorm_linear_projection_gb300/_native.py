@@ -47,7 +47,7 @@ EXPORTS = ("rnl_version", "rnl_debug_build", "rnl_selftest_bounds_check", "rnl_s
            "mxfp8_scaled_mm", "rnl_head_rmsnorm", "mla_q_chain_head_norm", "rnl_w8a8_prepare_weight",
            "rmsnorm_linear_w8a8_prepared", "rnl_qkv_rope_axes", "rnl_kv4_append", "rnl_kv4_gather",
            "rnl_kv4_attention", "rnl_add_rmsnorm_mxfp8", "rnl_quant_mxfp8", "rnl_moe_route",
-           "rnl_grouped_linear_bf16", "rnl_moe_combine")
+           "rnl_grouped_linear_bf16", "rnl_grouped_linear_mxfp8", "rnl_moe_combine")
 
 
 class RnlError(RuntimeError):
@@ -115,6 +115,7 @@ def _declare(lib):
         "rnl_quant_mxfp8": (I, [P, I64, I64, I64, P, P, P]),
         "rnl_moe_route": (I, [P, I64, I64, I64, I, P, P, P, P, P, P, SZ, P]),
         "rnl_grouped_linear_bf16": (I, [P, I64, P, I64, I64, I64, P, P, I64, I, P, P, SZ, P]),
+        "rnl_grouped_linear_mxfp8": (I, [P, P, I64, P, P, I64, I64, I64, I64, P, P, I64, I, P, P, SZ, P]),
         "rnl_moe_combine": (I, [P, I64, I64, P, P, I64, I64, P, P, P]),
     })
     for name, (res, args) in sig.items():
@@ -702,6 +703,25 @@ def rnl_grouped_linear_bf16(x, W, offsets, rows=None, swiglu=False, out=None, wo
     _check(load().rnl_grouped_linear_bf16(_ptr(x), x.shape[0], _ptr(W), E, N, K, _ptr(offsets), _ptr(rows), M,
                                           int(bool(swiglu)), _ptr(out), _ptr(ws), ws.numel() * ws.element_size(),
                                           _stream(dev, stream)), "rnl_grouped_linear_bf16")
+    return out
+
+
+def rnl_grouped_linear_mxfp8(x_codes, x_scale, w_codes, w_scale, offsets, rows=None, swiglu=False, block=64, out=None,
+                             workspace=None, stream=None):
+    """rnl_grouped_linear_bf16 on MXFP8 operands: codes uint8 [R, K] and [E, N, K],
+    scale bytes uint8 [R, K / block] and [E, N, K / block]; bf16 out."""
+    dev = x_codes.device
+    M, E, N, K, out = _grouped_sizes(x_codes, w_codes, offsets, rows, swiglu, out, dev, stream)
+    R, nb = x_codes.shape[0], K // block if block else 0
+    _need(x_codes, "x_codes", torch.uint8, (R, K), dev)
+    _need(x_scale, "x_scale", torch.uint8, (R, nb), dev)
+    _need(w_codes, "w_codes", torch.uint8, (E, N, K), dev)
+    _need(w_scale, "w_scale", torch.uint8, (E, N, nb), dev)
+    ws = _workspace(workspace_size(OP_GROUPED, M, K, N, E), dev, workspace, stream)
+    _check(load().rnl_grouped_linear_mxfp8(_ptr(x_codes), _ptr(x_scale), R, _ptr(w_codes), _ptr(w_scale), E, N, K,
+                                           int(block), _ptr(offsets), _ptr(rows), M, int(bool(swiglu)), _ptr(out),
+                                           _ptr(ws), ws.numel() * ws.element_size(), _stream(dev, stream)),
+           "rnl_grouped_linear_mxfp8")
     return out
 
 

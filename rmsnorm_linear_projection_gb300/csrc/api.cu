@@ -1307,7 +1307,37 @@ rnl_status rnl_grouped_linear_bf16(const void* x, int64_t n_x_rows, const void* 
   const rnl_status st = check_grouped(g, workspace_bytes, &go);
   if (st != RNL_OK) return st;
   if (K % 8 != 0) return RNL_ERR_ALIGN;
-  return go ? launch_grouped_bf16(g, cs(stream)) : RNL_OK;
+  return go ? launch_grouped(g, cs(stream)) : RNL_OK;
+}
+
+rnl_status rnl_grouped_linear_mxfp8(const uint8_t* x_codes, const uint8_t* x_scale, int64_t n_x_rows,
+                                    const uint8_t* w_codes, const uint8_t* w_scale, int64_t n_experts, int64_t N,
+                                    int64_t K, int64_t block, const int32_t* offsets, const int32_t* rows, int64_t M,
+                                    int swiglu, void* out, void* workspace, size_t workspace_bytes,
+                                    rnl_stream_t stream) {
+  if ((swiglu != 0 && swiglu != 1) || !mx_block_ok(block)) return RNL_ERR_ARG;
+  if (K % block != 0) return RNL_ERR_SHAPE;
+  GroupedArgs g;
+  g.x = x_codes;
+  g.x_scale = x_scale;
+  g.R = n_x_rows;
+  g.w = w_codes;
+  g.w_scale = w_scale;
+  g.E = n_experts;
+  g.N = N;
+  g.K = K;
+  g.block = block;
+  g.offsets = offsets;
+  g.rows = rows;
+  g.M = M;
+  g.swiglu = swiglu == 1;
+  g.out = out;
+  g.ws = workspace;
+  bool go;
+  const rnl_status st = check_grouped(g, workspace_bytes, &go);
+  if (st != RNL_OK || !go) return st;
+  if (!x_scale || !w_scale) return RNL_ERR_NULL;
+  return launch_grouped(g, cs(stream));
 }
 
 rnl_status rnl_check_device_error(rnl_stream_t stream, int* site) {

@@ -1,4 +1,5 @@
-// grouped.cu -- products grouped by expert with ragged sizes, bf16:
+// grouped.cu -- products grouped by expert with ragged sizes, of bf16 or of
+// MXFP8 operands (E4M3 codes with an E8M0 scale per 32 or 64 elements):
 //
 //   out[i] = bf16(sum_k x[rows[i], k] W[e, :, k])        rows i of expert e
 //   out[i] = bf16(silu(g) u),  g = the first half of W[e]'s rows, u the second    (swiglu)
@@ -15,7 +16,8 @@
 // same features, which puts both sums of a feature into one warp's lanes.
 //
 // Roles per CTA (480 threads): warp 0 weight boxes (TMA), warp 1 MMA issue (even CTA),
-// warps 2-9 epilogue, warps 10-13 gathers, warp 14 their hand-over.
+// warps 2-9 epilogue, warps 10-13 gathers, warp 14 their hand-over; MXFP8 (608
+// threads) warps 15-18 the scales into tensor memory.
 // Every wait is bounded (ptx.cuh).
 #include <cuda_bf16.h>
 
@@ -33,15 +35,32 @@ using namespace grouped;
 __device__ unsigned int g_err_grouped;
 std::atomic<bool> g_launched{false};
 
-constexpr int kTile = 256;                        // rows of a group a tile, at most
+constexpr int kRowBytes = 128;                    // of a k-block: 64 bf16 or 128 codes
 constexpr int kStep = 32;                         // the pair's products take N in steps of 32
-constexpr uint32_t kStageBytes = 2 * kABytes;     // 128 weight rows and up to 128 group rows of 64 bf16
-constexpr int64_t kSlotWords = 2 * 128 * kTile;   // partial sums of one pair: [CTA][column][lane]
-constexpr int kMaxPairs = kMaxPartialSlots - 1;   // the last slot holds the flags
-
 constexpr int kGatherWarps = 4;                   // 32 of the CTA's rows each
 constexpr int kRelayWarp = 2 + kEpiWarps + kGatherWarps;
-constexpr int kThreadsG = (kRelayWarp + 1) * 32;
+constexpr int kScaleWarps = 4;                    // one a TMEM lane quarter
+constexpr int64_t kSlotWords = 2 * 128 * 256;     // partial sums of one pair: [CTA][column][lane]
+constexpr int kMaxPairs = kMaxPartialSlots - 1;   // the last slot holds the flags
+
+// Scales of four k-blocks in shared memory: [k-block][32 rows][lane] words, a word
+// the four E8M0 bytes of a row's k-block; 4 x 32 weight rows, then 7 x 32 rows of x.
+constexpr int kSfBatch = 4;
+constexpr int kSfWords = 11 * 32;
+
+// MX: two accumulators of 224 columns leave 64 columns of TMEM for the scales of
+// four k-blocks (weight rows' at +0, the group's at +8 of 16).
+template <bool MX>
+struct Form {
+  static constexpr int kTile = MX ? 224 : 256;  // rows of a group a tile, at most
+  static constexpr int kThreads = (kRelayWarp + 1 + (MX ? kScaleWarps : 0)) * 32;
+  static constexpr uint32_t kStageBytes = kABytes + kTile / 2 * kRowBytes;
+  static constexpr size_t kSfBytes = MX ? 2 * kSfBatch * kSfWords * 4 : 0;
+  static constexpr uint32_t kSfBase = 2 * kTile;
+  static constexpr int kSfSlots = 4;
+  static_assert(kStageBytes % 1024 == 0, "swizzle atoms");
+  static_assert(!MX || kSfBase + kSfSlots * 16 <= 512, "TMEM columns");
+};
 
 struct __align__(8) Ctrl {
   uint64_t full[kMaxStages];   // even CTA: both CTAs' loads of a stage
@@ -49,6 +68,8 @@ struct __align__(8) Ctrl {
   uint64_t landed[kMaxStages];  // each CTA: its gathered rows of a stage
   uint64_t tmem_full[2];       // each CTA: accumulator ready
   uint64_t tmem_empty[2];      // even CTA: both CTAs' epilogues have read it
+  uint64_t sf_full[4];         // even CTA: both CTAs' scales of a slot are in TMEM
+  uint64_t sf_empty[4];        // each CTA: the slot's k-block has been multiplied
   uint32_t tmem_base;
   int abort;
 };
@@ -56,12 +77,18 @@ struct __align__(8) Ctrl {
 __host__ __device__ constexpr size_t table_bytes(int E) { return (static_cast<size_t>(E) + 1) * 8; }
 
 struct Args {
-  const __nv_bfloat16* x;
+  const uint8_t* x;
+  int64_t row_bytes;    // of x and W
+  const uint8_t* x_scale;
+  const uint8_t* w_scale;
+  int nb;               // scale bytes a row
+  int sf_vec;           // bytes a load of scales: what the rows' alignment allows (16 / 8 at most, 4 / 2 or 1)
   const int32_t* offsets;
   const int32_t* rows;  // may be null
   int R;                // rows of x
   int M;                // rows of out
-  int E, N, K;          // N weight rows an expert
+  int E, N;             // N weight rows an expert
+  int num_kb;
   int stages;
   __nv_bfloat16* out;
   float* partial;
@@ -69,9 +96,64 @@ struct Args {
   uint64_t epoch;
 };
 
-template <bool SWIGLU>
-__global__ void __launch_bounds__(kThreadsG, 1)
-    grouped_bf16_kernel(const __grid_constant__ CUtensorMap map_w, const Args a) {
+// The row of x behind row i of the grouped order (0 where it is none: reported)
+__device__ __forceinline__ int source_row(const Args& a, int i) {
+  int v = i;
+  if (a.rows != nullptr) v = a.rows[i];
+  if (v < 0 || v >= a.R) {
+    atomicCAS(&g_err_grouped, 0u, kErrArg | (111u << 8));
+    v = 0;
+  }
+  return v;
+}
+
+// The scale words of four k-blocks from kb on of the row at p (bytes of K / BLK a
+// row, nb of them; 127 behind the last).  A 64-element scale is given to the
+// hardware's 32-element blocks twice.
+template <int BLK>
+__device__ __forceinline__ void load_scales(const uint8_t* p, int kb, int nb, int vec, uint32_t (&w)[kSfBatch]) {
+  constexpr int kPer = 128 / BLK;  // bytes a k-block: 4 or 2
+  const int b0 = kb * kPer;
+  if (vec == 4 * kPer && b0 + 4 * kPer <= nb) {
+    if constexpr (BLK == 32) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(p + b0));
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    } else {
+      const uint2 u = __ldg(reinterpret_cast<const uint2*>(p + b0));
+      w[0] = __byte_perm(u.x, 0, 0x1100), w[1] = __byte_perm(u.x, 0, 0x3322);
+      w[2] = __byte_perm(u.y, 0, 0x1100), w[3] = __byte_perm(u.y, 0, 0x3322);
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < kSfBatch; ++k) {
+    const int b = b0 + k * kPer;
+    if (vec >= kPer && b + kPer <= nb) {
+      if constexpr (BLK == 32)
+        w[k] = __ldg(reinterpret_cast<const uint32_t*>(p + b));
+      else
+        w[k] = __byte_perm(__ldg(reinterpret_cast<const uint16_t*>(p + b)), 0, 0x1100);
+    } else {
+      uint32_t v = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int at = b + j * kPer / 4;
+        v |= static_cast<uint32_t>(at < nb ? __ldg(p + at) : 127) << (8 * j);
+      }
+      w[k] = v;
+    }
+  }
+}
+
+// BLK: 0 for bf16, 32 or 64 for MXFP8 operands with that many elements a scale.
+template <bool SWIGLU, int BLK>
+__global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap map_w, const Args a) {
+  constexpr bool MX = BLK != 0;
+  using F = Form<MX>;
+  constexpr int kTile = F::kTile;
+  constexpr uint32_t kStageBytes = F::kStageBytes;
+  constexpr int kBKElems = MX ? kRowBytes : kRowBytes / 2;
   constexpr int kFeatCta = SWIGLU ? 64 : 128;  // output features a CTA
   constexpr uint32_t kTmemCols = 512;
   extern __shared__ uint8_t smem_raw[];
@@ -79,7 +161,8 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   const uint32_t base = (raw_addr + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw_addr);
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + a.stages * kStageBytes);
-  int* off = reinterpret_cast<int*>(ctrl + 1);
+  uint32_t* sf_smem = reinterpret_cast<uint32_t*>(ctrl + 1);  // 2 x [kSfBatch][kSfWords]
+  int* off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(sf_smem) + F::kSfBytes);
   int* pre = off + a.E + 1;
 
   const int warp = threadIdx.x >> 5;
@@ -99,6 +182,10 @@ __global__ void __launch_bounds__(kThreadsG, 1)
       mbar_init(smem_u32(&ctrl->tmem_full[b]), 1);
       mbar_init(smem_u32(&ctrl->tmem_empty[b]), 2 * kEpiWarps);
     }
+    for (int b = 0; b < F::kSfSlots; ++b) {
+      mbar_init(smem_u32(&ctrl->sf_full[b]), 2 * kScaleWarps);
+      mbar_init(smem_u32(&ctrl->sf_empty[b]), 1);
+    }
     ctrl->abort = 0;
     fence_mbar_init();
   }
@@ -116,8 +203,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   const uint32_t tmem_base = ctrl->tmem_base;
   volatile int* abort = &ctrl->abort;
   const Groups groups{off, pre, a.E, num_f};
-  const int num_kb = (a.K + BK - 1) / BK;
-  const Sched sc(pre[a.E], num_pairs, num_kb);
+  const Sched sc(pre[a.E], num_pairs, a.num_kb);
   Walk<kTile, kStep> walk(sc, groups, pair, lane);
 
   if (warp == 0) {
@@ -140,9 +226,9 @@ __global__ void __launch_bounds__(kThreadsG, 1)
           const uint32_t full_even = mapa_shared(full_local, 0);
           if (rank == 0) mbar_arrive_expect_tx(full_local, 2 * kABytes);  // both CTAs' boxes
           if constexpr (SWIGLU)
-            tma_load_5d_pair(sa, &map_w, full_even, kb * BK, 0, 0, f0 / 16, w.t.e);
+            tma_load_5d_pair(sa, &map_w, full_even, kb * kBKElems, 0, 0, f0 / 16, w.t.e);
           else
-            tma_load_2d_pair(sa, &map_w, full_even, kb * BK, w.t.e * a.N + f0);
+            tma_load_2d_pair(sa, &map_w, full_even, kb * kBKElems, w.t.e * a.N + f0);
           if (++stage == static_cast<uint32_t>(a.stages)) {
             stage = 0;
             phase ^= 1u;
@@ -179,6 +265,88 @@ __global__ void __launch_bounds__(kThreadsG, 1)
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
+  } else if (MX && warp > kRelayWarp) {
+    // ------------------------------------------------------- scale writers
+    // four k-blocks at a time: the 128 threads load the scales of the CTA's weight
+    // rows and of all the tile's rows (three rows a thread), turn them into words in
+    // shared memory, and each warp copies a k-block's words into its lane quarter of
+    // a TMEM slot once the slot's last k-block has been multiplied
+    if constexpr (MX) {
+      const int quarter = warp & 3;
+      const int me = (warp - kRelayWarp - 1) * 32 + lane;
+      const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+      uint32_t slot = 0, phase = 0, buf = 0;
+      bool ok = true;
+      // (a warp that gives up on a slot still takes part in the barriers below)
+      for (int it = 0; it < walk.n; ++it) {
+        const Item w = walk.at(it);
+        // rows me (weight), me and me + 128 (group)
+        const int f0 = (w.t.f * 2 + static_cast<int>(rank)) * kFeatCta;
+        const uint8_t* p[3] = {nullptr, nullptr, nullptr};
+        {
+          int n;
+          if (SWIGLU) {  // TMEM lane 32 q + 16 h + i: feature 16 q + i, gate (h = 0) or up
+            const int f = f0 + (me >> 5) * 16 + (me & 15);
+            n = f < N_out ? f + ((me & 16) ? N_out : 0) : -1;
+          } else {
+            n = f0 + me < a.N ? f0 + me : -1;
+          }
+          if (n >= 0) p[0] = a.w_scale + (static_cast<int64_t>(w.t.e) * a.N + n) * a.nb;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (me + 128 * h < w.t.valid)
+              p[1 + h] = a.x_scale + static_cast<int64_t>(source_row(a, w.t.row0 + me + 128 * h)) * a.nb;
+        }
+        for (int kb = w.kb0 & ~(kSfBatch - 1); kb < w.kb1; kb += kSfBatch) {
+          uint32_t v[3][kSfBatch];
+#pragma unroll
+          for (int h = 0; h < 3; ++h) {
+#pragma unroll
+            for (int k = 0; k < kSfBatch; ++k) v[h][k] = 0x7F7F7F7Fu;
+            if (p[h] != nullptr) load_scales<BLK>(p[h], kb, a.nb, a.sf_vec, v[h]);
+          }
+          uint32_t* sf = sf_smem + buf * (kSfBatch * kSfWords);
+#pragma unroll
+          for (int k = 0; k < kSfBatch; ++k) {
+            sf[k * kSfWords + me] = v[0][k];
+            sf[k * kSfWords + 128 + me] = v[1][k];
+            if (me < 96) sf[k * kSfWords + 256 + me] = v[2][k];
+          }
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          for (int k = kb < w.kb0 ? w.kb0 - kb : 0; ok && k < kSfBatch && kb + k < w.kb1; ++k) {
+            const uint32_t* s = sf + k * kSfWords + lane;
+            uint4 wa = make_uint4(s[0], s[32], s[64], s[96]);
+            uint4 wb0 = make_uint4(s[128], s[160], s[192], s[224]);
+            uint4 wb1 = make_uint4(s[256], s[288], s[320], 0u);
+            const bool got = mbar_wait_cluster(smem_u32(&ctrl->sf_empty[slot]), phase ^ 1u, abort, &g_err_grouped, 106);
+            if (!__all_sync(0xffffffffu, got)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t col = tmem_base + lane_addr + F::kSfBase + slot * 16;
+            tmem_st_4cols(col, wa);
+            tmem_st_4cols(col + 8, wb0);
+            tmem_st_4cols(col + 12, wb1);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              const uint32_t bar = smem_u32(&ctrl->sf_full[slot]);
+              if (rank == 0)
+                mbar_arrive(bar);
+              else
+                mbar_arrive_remote(mapa_shared(bar, 0));
+            }
+            if (++slot == F::kSfSlots) {
+              slot = 0;
+              phase ^= 1u;
+            }
+          }
+          buf ^= 1u;
+        }
+      }
+    }
   } else if (warp >= 2 + kEpiWarps) {
     // ------------------------------------------------------------- gathers
     // each warp brings 32 of the CTA's rows, 16 bytes a lane and copy, to where a
@@ -191,28 +359,20 @@ __global__ void __launch_bounds__(kThreadsG, 1)
       const Item w = walk.at(it);
       const int half = w.t.n / 2;
       const int first = static_cast<int>(rank) * half + gw * 32 + sub;
-      const __nv_bfloat16* src[8];
+      const uint8_t* src[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        // rows behind the tile's last one repeat it (their columns are not stored)
-        int v = w.t.row0 + min(first + 4 * i, w.t.valid - 1);
-        if (a.rows != nullptr) v = a.rows[v];
-        if (v < 0 || v >= a.R) {
-          atomicCAS(&g_err_grouped, 0u, kErrArg | (111u << 8));
-          v = 0;
-        }
-        src[i] = a.x + static_cast<int64_t>(v) * a.K + chunk * 8;
-      }
+      for (int i = 0; i < 8; ++i)  // rows behind the tile's last one repeat it (their columns are not stored)
+        src[i] = a.x + source_row(a, w.t.row0 + min(first + 4 * i, w.t.valid - 1)) * a.row_bytes + chunk * 16;
       for (int kb = w.kb0; kb < w.kb1; ++kb) {
         const bool got = mbar_wait_cluster(smem_u32(&ctrl->empty[stage]), phase ^ 1u, abort, &g_err_grouped, 119);
-        if (!__all_sync(0xffffffffu, got && RNL_DCHECK(&g_err_grouped, half <= 128, 109))) {
+        if (!__all_sync(0xffffffffu, got && RNL_DCHECK(&g_err_grouped, half <= kTile / 2, 109))) {
           ok = false;
           break;
         }
         const uint32_t dst = base + stage * kStageBytes + kABytes + (gw * 32 + sub) * 128;
-        const int k0 = kb * BK;
-        const uint32_t bytes = k0 + chunk * 8 < a.K ? 16u : 0u;
-        const int from = bytes ? k0 : -chunk * 8;  // an address inside the row where nothing is read
+        const int k0 = kb * kRowBytes;
+        const uint32_t bytes = k0 + chunk * 16 < a.row_bytes ? 16u : 0u;
+        const int from = bytes ? k0 : -chunk * 16;  // an address inside the row where nothing is read
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (gw * 32 + 4 * i < half)  // (row & 7) = sub + 4 (i & 1)
@@ -228,7 +388,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issue
     if (rank == 0) {
-      uint32_t stage = 0, phase = 0;
+      uint32_t stage = 0, phase = 0, slot = 0, sf_phase = 0;
       bool ok = true;
       for (int it = 0; it < walk.n && ok; ++it) {
         const Item w = walk.at(it);
@@ -236,10 +396,11 @@ __global__ void __launch_bounds__(kThreadsG, 1)
           const uint32_t buf = it & 1;
           ok = mbar_wait_cluster(smem_u32(&ctrl->tmem_empty[buf]), ((it >> 1) & 1) ^ 1u, abort, &g_err_grouped, 114);
           tc_fence_after();
-          const uint32_t d_tmem = tmem_base + buf * kAccStride;
-          const uint32_t idesc = idesc_bf16(256, w.t.n);
+          const uint32_t d_tmem = tmem_base + buf * kTile;
+          const uint32_t idesc = MX ? idesc_mxf8(256, w.t.n) : idesc_bf16(256, w.t.n);
           for (int kb = w.kb0; kb < w.kb1 && ok; ++kb) {
-            if (!mbar_wait_cluster(smem_u32(&ctrl->full[stage]), phase, abort, &g_err_grouped, 115)) {
+            if (!mbar_wait_cluster(smem_u32(&ctrl->full[stage]), phase, abort, &g_err_grouped, 115) ||
+                (MX && !mbar_wait_cluster(smem_u32(&ctrl->sf_full[slot]), sf_phase, abort, &g_err_grouped, 107))) {
               ok = false;
               break;
             }
@@ -247,10 +408,23 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             const uint32_t sa = base + stage * kStageBytes;
             const uint64_t adesc = desc_kmajor_sw128(sa);
             const uint64_t bdesc = desc_kmajor_sw128(sa + kABytes);
+            const uint32_t sf = tmem_base + F::kSfBase + slot * 16;
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k)
-              umma_bf16_pair(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, (kb > w.kb0 || k > 0) ? 1u : 0u);
+            for (int k = 0; k < 4; ++k) {  // 32 bytes of a row each
+              const uint32_t add = (kb > w.kb0 || k > 0) ? 1u : 0u;
+              if constexpr (MX)
+                umma_mxf8_pair(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc_mxf8_id(idesc, k), sf, sf + 8, add);
+              else
+                umma_bf16_pair(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, add);
+            }
             umma_commit_pair(smem_u32(&ctrl->empty[stage]), 0x3);
+            if constexpr (MX) {
+              umma_commit_pair(smem_u32(&ctrl->sf_empty[slot]), 0x3);
+              if (++slot == F::kSfSlots) {
+                slot = 0;
+                sf_phase ^= 1u;
+              }
+            }
             if (++stage == static_cast<uint32_t>(a.stages)) {
               stage = 0;
               phase ^= 1u;
@@ -269,7 +443,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t empty_even[2] = {mapa_shared(smem_u32(&ctrl->tmem_empty[0]), 0),
                                     mapa_shared(smem_u32(&ctrl->tmem_empty[1]), 0)};
-    const int64_t lane_off = static_cast<int64_t>(rank) * 128 * kTile + quarter * 32 + lane;
+    const int64_t lane_off = static_cast<int64_t>(rank) * 128 * 256 + quarter * 32 + lane;
     for (int it = 0; it < walk.n; ++it) {
       const Item w = walk.at(it);
       const Tile& t = w.t;
@@ -286,7 +460,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
       const int feat = SWIGLU ? f0 + quarter * 16 + (lane & 15) : f0 + quarter * 32 + lane;
       for (int c = half * 32; c < t.n; c += 64) {
         uint32_t r[32];
-        tmem_ld_32cols(tmem_base + lane_addr + buf * kAccStride + c, r);
+        tmem_ld_32cols(tmem_base + lane_addr + buf * kTile + c, r);
         tmem_ld_wait();
         if (!RNL_DCHECK(&g_err_grouped, c + 32 <= kTile && t.row0 + t.valid <= a.M && pair < kMaxPairs, 118)) continue;
         if (w.kind == kPartial) {
@@ -342,7 +516,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
 }
 
 // CTA pairs that are resident at once (all of the grid is).
-template <bool SWIGLU>
+template <bool SWIGLU, int BLK>
 int resident_pairs(const DeviceInfo& dev, size_t smem) {
   static std::atomic<int> cached[64];
   const int c = cached[dev.device].load(std::memory_order_relaxed);
@@ -354,12 +528,12 @@ int resident_pairs(const DeviceInfo& dev, size_t smem) {
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (dev.sm_count / 2), 1, 1);
-  cfg.blockDim = dim3(kThreadsG, 1, 1);
+  cfg.blockDim = dim3(Form<BLK != 0>::kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, grouped_bf16_kernel<SWIGLU>, &cfg) != cudaSuccess) n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, grouped_kernel<SWIGLU, BLK>, &cfg) != cudaSuccess) n = 0;
   cudaGetLastError();
   if (n <= 0 || n > dev.sm_count / 2) n = dev.sm_count / 2;
   if (n > kMaxPairs) n = kMaxPairs;
@@ -367,36 +541,51 @@ int resident_pairs(const DeviceInfo& dev, size_t smem) {
   return n;
 }
 
-template <bool SWIGLU>
+template <bool SWIGLU, int BLK>
 rnl_status launch(const GroupedArgs& g, const DeviceInfo& dev, cudaStream_t s) {
-  auto kern = grouped_bf16_kernel<SWIGLU>;
-  const size_t fixed = 1024 + sizeof(Ctrl) + table_bytes(static_cast<int>(g.E));
-  const size_t fit = (kSmemLimit - fixed) / kStageBytes;
+  constexpr bool MX = BLK != 0;
+  using F = Form<MX>;
+  auto kern = grouped_kernel<SWIGLU, BLK>;
+  const size_t fixed = 1024 + sizeof(Ctrl) + F::kSfBytes + table_bytes(static_cast<int>(g.E));
+  const size_t fit = (kSmemLimit - fixed) / F::kStageBytes;
   const int stages = static_cast<int>(fit < static_cast<size_t>(kMaxStages) ? fit : kMaxStages);
-  const size_t smem = fixed + stages * kStageBytes;
+  const size_t smem = fixed + stages * F::kStageBytes;
   if (ensure_smem_attr(reinterpret_cast<const void*>(kern), dev.device, kSmemLimit) != RNL_OK) return RNL_ERR_LAUNCH;
   CUtensorMap mw;
-  const uint64_t N = g.N, K = g.K;
+  const uint64_t N = g.N, K = g.K, row = MX ? K : 2 * K;
+  constexpr uint32_t kBox = MX ? kRowBytes : kRowBytes / 2;
+  const CUtensorMapDataType dt = MX ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   rnl_status st;
   if (SWIGLU) {
     // [expert][16 features][gate / up][feature][k]: 64 features' gate and up rows in groups of 16
     const uint64_t dims[5] = {K, 16, 2, N / 32, static_cast<uint64_t>(g.E)};
-    const uint64_t strides[4] = {2 * K, N * K, 32 * K, 2 * N * K};
-    const uint32_t box[5] = {BK, 16, 2, 4, 1};
-    st = make_map_5d(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.w, dims, strides, box, true);
+    const uint64_t strides[4] = {row, N / 2 * row, 16 * row, N * row};
+    const uint32_t box[5] = {kBox, 16, 2, 4, 1};
+    st = make_map_5d(&mw, dt, g.w, dims, strides, box, true);
   } else {
-    st = make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.w, K, g.E * N, 2 * K, BK, 128);
+    st = make_map_2d(&mw, dt, g.w, K, g.E * N, row, kBox, 128);
   }
   if (st != RNL_OK) return st;
   Args a;
-  a.x = static_cast<const __nv_bfloat16*>(g.x);
+  a.x = static_cast<const uint8_t*>(g.x);
+  a.row_bytes = static_cast<int64_t>(row);
+  a.x_scale = g.x_scale;
+  a.w_scale = g.w_scale;
+  a.nb = MX ? static_cast<int>(g.K / g.block) : 0;
+  a.sf_vec = 1;
+  if constexpr (MX) {
+    constexpr int kPer = 128 / BLK;
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(g.x_scale) | reinterpret_cast<uintptr_t>(g.w_scale) |
+                           static_cast<uintptr_t>(a.nb);
+    a.sf_vec = bits % (4 * kPer) == 0 ? 4 * kPer : (bits % kPer == 0 ? kPer : 1);
+  }
   a.offsets = g.offsets;
   a.rows = g.rows;
   a.R = static_cast<int>(g.R);
   a.M = static_cast<int>(g.M);
   a.E = static_cast<int>(g.E);
   a.N = static_cast<int>(g.N);
-  a.K = static_cast<int>(g.K);
+  a.num_kb = static_cast<int>((row + kRowBytes - 1) / kRowBytes);
   a.stages = stages;
   a.out = static_cast<__nv_bfloat16*>(g.out);
   a.partial = static_cast<float*>(g.ws);
@@ -410,15 +599,16 @@ rnl_status launch(const GroupedArgs& g, const DeviceInfo& dev, cudaStream_t s) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(resident_pairs<SWIGLU>(dev, smem)), 1, 1);
-  cfg.blockDim = dim3(kThreadsG, 1, 1);
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(resident_pairs<SWIGLU, BLK>(dev, smem)), 1, 1);
+  cfg.blockDim = dim3(F::kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   trace_before(s);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mw, a);
-  trace_after(s, SWIGLU ? "grouped_bf16_swiglu" : "grouped_bf16");
+  trace_after(s, MX ? (SWIGLU ? "grouped_mxfp8_swiglu" : "grouped_mxfp8")
+                    : (SWIGLU ? "grouped_bf16_swiglu" : "grouped_bf16"));
   if (e != cudaSuccess) {
     cudaGetLastError();
     return RNL_ERR_LAUNCH;
@@ -428,13 +618,15 @@ rnl_status launch(const GroupedArgs& g, const DeviceInfo& dev, cudaStream_t s) {
 
 }  // namespace
 
-rnl_status launch_grouped_bf16(const GroupedArgs& g, cudaStream_t s) {
+rnl_status launch_grouped(const GroupedArgs& g, cudaStream_t s) {
   if (g.M == 0) return RNL_OK;
   DeviceInfo dev;
   const rnl_status st = current_device(&dev);
   if (st != RNL_OK) return st;
   g_launched.store(true, std::memory_order_relaxed);
-  return g.swiglu ? launch<true>(g, dev, s) : launch<false>(g, dev, s);
+  if (g.block == 0) return g.swiglu ? launch<true, 0>(g, dev, s) : launch<false, 0>(g, dev, s);
+  if (g.block == 32) return g.swiglu ? launch<true, 32>(g, dev, s) : launch<false, 32>(g, dev, s);
+  return g.swiglu ? launch<true, 64>(g, dev, s) : launch<false, 64>(g, dev, s);
 }
 
 rnl_status read_clear_error_grouped(unsigned int* word) {

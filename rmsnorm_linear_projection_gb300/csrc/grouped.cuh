@@ -1,5 +1,4 @@
-// grouped.cuh -- what the grouped products (grouped.cu, groupedmx.cu) share:
-// the tiles of ragged groups, the work list over them and the epilogue stores.
+// grouped.cuh -- pieces of the grouped products (grouped.cu): the tiles of ragged groups, the work list over them and the epilogue stores.
 //
 //   out[i] = x[rows[i]] W[e]^T   for the rows i of expert e, offsets[e] <= i < offsets[e + 1]
 //

@@ -232,7 +232,7 @@ rnl_status launch_moe_route(const float* logits, int64_t T, int64_t E, int64_t k
 rnl_status launch_moe_combine(const void* y, int64_t M, int64_t N, const int32_t* slots, const float* weights,
                               int64_t T, int64_t k, const void* residual, void* out, cudaStream_t s);
 
-// ---- products grouped by expert (grouped.cu, groupedmx.cu) ----
+// ---- products grouped by expert (grouped.cu) ----
 struct GroupedArgs {
   const void* x = nullptr;  // bf16 or E4M3 [R, K]
   const uint8_t* x_scale = nullptr;
@@ -247,7 +247,7 @@ struct GroupedArgs {
   void* out = nullptr;  // bf16 [M, N] ([M, N / 2] with swiglu)
   void* ws = nullptr;
 };
-rnl_status launch_grouped_bf16(const GroupedArgs& g, cudaStream_t s);
+rnl_status launch_grouped(const GroupedArgs& g, cudaStream_t s);  // block 0: bf16
 
 // ---- tcgen05 GEMM (gemm_tc.cu) ----
 enum class Epi : int {

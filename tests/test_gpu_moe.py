@@ -234,3 +234,94 @@ def test_grouped(counts, K, N, gather):
 @pytest.mark.parametrize("gather", [False, True])
 def test_grouped_swiglu(counts, K, N, gather):
     check_grouped(counts, K, N, True, gather, tail=3)
+
+
+# ------------------------------------------------- products by expert, MXFP8
+def mx_values(codes, scales, block):
+    v = codes.view(torch.float8_e4m3fn).double()
+    return v * torch.exp2(scales.double() - 127).repeat_interleave(block, dim=-1)
+
+
+def mx_codes(g, *shape):
+    c = torch.randint(0, 252, shape, generator=g, device="cuda", dtype=torch.uint8)
+    return torch.where(c < 126, c, c + 2)  # every value but NaN
+
+
+def mx_case(counts, K, N, block, gather, seed, tail=0):
+    g = gen(seed)
+    E, M = len(counts), sum(counts) + tail
+    offsets = [0]
+    for c in counts:
+        offsets.append(offsets[-1] + c)
+    R = max(M // 3, 1) if gather else M
+    x, w = mx_codes(g, R, K), mx_codes(g, E, N, K)
+    xs = torch.randint(110, 130, (R, K // block), generator=g, device="cuda", dtype=torch.uint8)
+    ws = torch.randint(105, 118, (E, N, K // block), generator=g, device="cuda", dtype=torch.uint8)
+    rows = torch.randint(0, R, (M,), generator=g, device="cuda", dtype=torch.int32) if gather else None
+    return x, xs, w, ws, offsets, rows, M
+
+
+def check_mx(counts, K, N, block, swiglu, gather, seed=0, tail=0):
+    x, xs, w, ws, offsets, rows, M = mx_case(counts, K, N, block, gather, seed, tail)
+    if swiglu:
+        ws = ws - 4  # gates of ordinary size
+    out = torch.full((M, N // 2 if swiglu else N), 7.0, dtype=torch.bfloat16, device="cuda")
+    rnl.rnl_grouped_linear_mxfp8(x, xs, w, ws, i32(offsets), rows=rows, swiglu=swiglu, block=block, out=out)
+    rnl.rnl_check_device_error()
+    n = offsets[-1]
+    ref, bound = plain_grouped(mx_values(x, xs, block), mx_values(w, ws, block), offsets, rows, swiglu)
+    err = (out[:n].double() - ref).abs()
+    assert (err <= bound).all(), f"{(err > bound).sum()} of {err.numel()}, worst {(err / bound).max():.2f}"
+    assert (out[n:] == 7).all()
+
+
+MX_SHAPES = [
+    ([1], 64, 1), ([1], 128, 128), ([3, 0, 0, 5], 192, 40), ([0, 16, 17, 1], 128, 256), ([223, 224, 225], 320, 130),
+    ([300, 0, 31, 1, 600], 512, 513), ([1, 2, 3, 4, 5, 6, 7, 8], 1088, 520), ([4097], 64, 96),
+    ([700, 20, 5000, 1], 256, 768), ([2] * 64, 2048, 256), ([128] * 8, 1024, 1024), ([500, 3], 4096, 640),
+]
+
+
+@pytest.mark.parametrize("counts,K,N", MX_SHAPES)
+@pytest.mark.parametrize("block", [32, 64])
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped_mx(counts, K, N, block, gather):
+    check_mx(counts, K, N, block, False, gather, tail=2)
+
+
+@pytest.mark.parametrize("counts,K,N", [(c, K, max(32, N // 32 * 32)) for c, K, N in MX_SHAPES])
+@pytest.mark.parametrize("block", [32, 64])
+def test_grouped_mx_swiglu(counts, K, N, block):
+    check_mx(counts, K, N, block, True, True)
+
+
+@pytest.mark.parametrize("K", [32, 96, 160, 2080])
+def test_grouped_mx_odd_blocks(K):
+    """K / 32 odd: scale rows without any alignment."""
+    check_mx([5, 40, 300], K, 200, 32, False, True)
+
+
+def test_grouped_mx_agrees_with_scaled_mm():
+    x, xs, w, ws, _, _, _ = mx_case([300], 1024, 384, 64, False, 4)
+    a = rnl.rnl_grouped_linear_mxfp8(x, xs, w, ws, i32([0, 300]))
+    b = rnl.mxfp8_scaled_mm(x, xs, w[0], ws[0])
+    # each is within the bound of the exact value (the two add up in other orders, so
+    # where terms cancel they are more than a bf16 step of the value apart):
+    # |a - b| <= |a - ref| + |b - ref| <= 2 bound
+    _, bound = plain_grouped(mx_values(x, xs, 64), mx_values(w, ws, 64), [0, 300], None, False)
+    far = (a.double() - b.double()).abs() > 2 * bound
+    assert not far.any(), int(far.sum())
+
+
+def test_grouped_mx_nan_scales_stay_in_their_rows():
+    x, xs, w, ws, offsets, _, _ = mx_case([40, 60], 512, 256, 32, False, 5)
+    good = rnl.rnl_grouped_linear_mxfp8(x, xs, w, ws, i32(offsets), block=32)
+    xs2, ws2 = xs.clone(), ws.clone()
+    xs2[7, 3] = 255
+    ws2[1, 100, 15] = 255
+    out = rnl.rnl_grouped_linear_mxfp8(x, xs2, w, ws2, i32(offsets), block=32)
+    bad = torch.zeros_like(out, dtype=torch.bool)
+    bad[7] = True
+    bad[40:, 100] = True
+    assert torch.equal(torch.isnan(out), bad)
+    assert torch.equal(out[~bad], good[~bad])
