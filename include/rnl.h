@@ -103,8 +103,8 @@ enum {
   RNL_OP_MXFP8 = 6,
   RNL_OP_W8A8_PREPARED = 7,
   RNL_OP_KV4_ATTENTION = 8,
-  RNL_OP_GROUPED = 9,
-  RNL_OP_MOE_ROUTE = 10
+  RNL_OP_GROUPED = 10, /* 9 is no operation */
+  RNL_OP_MOE_ROUTE = 11
 };
 
 /* Library version (major * 10000 + minor * 100 + patch). */

@@ -38,6 +38,15 @@ arguments; the computation runs in the library's CUDA kernels.
     debug_library()       route calls through librnl_debug.so, the build whose
                           kernels check their indices on the device
 """
+from ._experts import (  # noqa: F401
+    MoeRoute,
+    rnl_add_rmsnorm_mxfp8,
+    rnl_grouped_linear_bf16,
+    rnl_grouped_linear_mxfp8,
+    rnl_moe_combine,
+    rnl_moe_route,
+    rnl_quant_mxfp8,
+)
 from ._native import (  # noqa: F401
     EXPORTS,
     NORM_RSQRT,
@@ -56,7 +65,6 @@ from ._native import (  # noqa: F401
     OUT_BF16,
     OUT_FP32,
     Kv4Cache,
-    MoeRoute,
     PipelineHandle,
     RnlError,
     debug_library,
@@ -72,18 +80,13 @@ from ._native import (  # noqa: F401
     rmsnorm_linear_skinny_noalloc,
     rmsnorm_linear_w8a8,
     rmsnorm_linear_w8a8_prepared,
-    rnl_add_rmsnorm_mxfp8,
     rnl_check_device_error,
     rnl_debug_build,
     rnl_gemm_s8s8s32,
-    rnl_grouped_linear_bf16,
-    rnl_grouped_linear_mxfp8,
     rnl_head_rmsnorm,
     rnl_kv4_append,
     rnl_kv4_attention,
     rnl_kv4_gather,
-    rnl_moe_combine,
-    rnl_moe_route,
     rnl_pipeline_create,
     rnl_pipeline_destroy,
     rnl_pipeline_submit_bf16,
@@ -92,7 +95,6 @@ from ._native import (  # noqa: F401
     rnl_pipeline_wait,
     rnl_qkv_rope,
     rnl_qkv_rope_axes,
-    rnl_quant_mxfp8,
     rnl_selftest_bounds_check,
     rnl_selftest_wait_timeout,
     rnl_trace_enable,

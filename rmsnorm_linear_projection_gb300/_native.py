@@ -13,7 +13,6 @@ that write its inputs and read its outputs.
 """
 from __future__ import annotations
 
-import collections
 import contextlib
 import ctypes
 import operator
@@ -28,8 +27,8 @@ DEBUG_LIB_PATH = os.path.join(PKG, "librnl_debug.so")
 
 NORM_RSQRT, NORM_SQRT_DIV = 0, 1
 OUT_BF16, OUT_FP32 = 0, 1
-OP_BF16, OP_W8A8, OP_MLA, OP_GEMM_S8, OP_QKV_ROPE, OP_QMRS, OP_MXFP8, OP_W8A8_PREPARED, OP_KV4_ATTENTION, \
-    OP_GROUPED, OP_MOE_ROUTE = range(11)
+OP_BF16, OP_W8A8, OP_MLA, OP_GEMM_S8, OP_QKV_ROPE, OP_QMRS, OP_MXFP8, OP_W8A8_PREPARED, OP_KV4_ATTENTION = range(9)
+OP_GROUPED, OP_MOE_ROUTE = 10, 11
 
 STATUS = {
     0: "RNL_OK", 1: "RNL_ERR_NULL", 2: "RNL_ERR_SHAPE", 3: "RNL_ERR_ALIGN", 4: "RNL_ERR_ARG",
@@ -618,127 +617,6 @@ def mxfp8_scaled_mm(x_codes, x_scale, w_codes, w_scale, block=64, out=None, out_
                                   int(block), _ptr(out), int(out_dtype), _ptr(ws),
                                   ws.numel() * ws.element_size(), _stream(dev, stream)),
            "mxfp8_scaled_mm")
-    return out
-
-
-def rnl_add_rmsnorm_mxfp8(x, gamma=None, residual=None, x_sum_out=None, eps=1e-6, norm_mode=NORM_RSQRT, block=64,
-                          codes_out=None, scale_out=None, stream=None):
-    """Residual add (optional), RMSNorm and MX quantisation of the rows of x [T, K]
-    (bf16): returns (E4M3 codes uint8 [T, K], E8M0 scale bytes uint8
-    [T, K / block]), the operand of mxfp8_scaled_mm and rnl_grouped_linear_mxfp8.
-    x_sum_out may be x or residual (in-place add)."""
-    T, K = x.shape
-    dev = x.device
-    _need(x, "x", torch.bfloat16, (T, K), dev)
-    for t, name, shape in ((residual, "residual", (T, K)), (x_sum_out, "x_sum_out", (T, K)), (gamma, "gamma", (K,))):
-        if t is not None:
-            _need(t, name, torch.bfloat16, shape, dev)
-    codes_out = _out(codes_out, "codes_out", torch.uint8, (T, K), dev, stream)
-    scale_out = _out(scale_out, "scale_out", torch.uint8, (T, K // block if block else 0), dev, stream)
-    _check(load().rnl_add_rmsnorm_mxfp8(_ptr(x), _ptr(residual), _ptr(x_sum_out), _ptr(gamma), T, K, float(eps),
-                                        int(norm_mode), int(block), _ptr(codes_out), _ptr(scale_out),
-                                        _stream(dev, stream)), "rnl_add_rmsnorm_mxfp8")
-    return codes_out, scale_out
-
-
-def rnl_quant_mxfp8(x, block=64, codes_out=None, scale_out=None, stream=None):
-    """MX quantisation of the rows of x [T, K] (bf16) as they are; returns (codes, scale bytes)."""
-    T, K = x.shape
-    dev = x.device
-    _need(x, "x", torch.bfloat16, (T, K), dev)
-    codes_out = _out(codes_out, "codes_out", torch.uint8, (T, K), dev, stream)
-    scale_out = _out(scale_out, "scale_out", torch.uint8, (T, K // block if block else 0), dev, stream)
-    _check(load().rnl_quant_mxfp8(_ptr(x), T, K, int(block), _ptr(codes_out), _ptr(scale_out), _stream(dev, stream)),
-           "rnl_quant_mxfp8")
-    return codes_out, scale_out
-
-
-MoeRoute = collections.namedtuple("MoeRoute", "ids weights offsets rows slots")
-
-
-def rnl_moe_route(logits, top_k, renormalize=True, ids_out=None, weights_out=None, offsets_out=None, rows_out=None,
-                  slots_out=None, workspace=None, stream=None):
-    """The top_k experts of every token (logits fp32 [T, E]), their softmax weights,
-    and the tokens' rows grouped by expert: MoeRoute(ids [T, k], weights [T, k],
-    offsets [E + 1], rows [T * k], slots [T, k])."""
-    T, E = logits.shape
-    k = int(top_k)
-    dev = logits.device
-    _need(logits, "logits", torch.float32, (T, E), dev)
-    n = max(k, 0)
-    r = MoeRoute(_out(ids_out, "ids_out", torch.int32, (T, n), dev, stream),
-                 _out(weights_out, "weights_out", torch.float32, (T, n), dev, stream),
-                 _out(offsets_out, "offsets_out", torch.int32, (E + 1,), dev, stream),
-                 _out(rows_out, "rows_out", torch.int32, (T * n,), dev, stream),
-                 _out(slots_out, "slots_out", torch.int32, (T, n), dev, stream))
-    ws = _workspace(workspace_size(OP_MOE_ROUTE, T, n, E), dev, workspace, stream)
-    _check(load().rnl_moe_route(_ptr(logits), T, E, k, int(bool(renormalize)), _ptr(r.ids), _ptr(r.weights),
-                                _ptr(r.offsets), _ptr(r.rows), _ptr(r.slots), _ptr(ws),
-                                ws.numel() * ws.element_size(), _stream(dev, stream)), "rnl_moe_route")
-    return r
-
-
-def _grouped_sizes(x, W, offsets, rows, swiglu, out, dev, stream):
-    """What both grouped products check; returns (M, E, N, K, out)."""
-    R, K = x.shape
-    E, N = W.shape[0], W.shape[1]
-    _need(offsets, "offsets", torch.int32, (E + 1,), dev)
-    M = R
-    if rows is not None:
-        M = rows.shape[0]
-        _need(rows, "rows", torch.int32, (M,), dev)
-    out = _out(out, "out", torch.bfloat16, (M, N // 2 if swiglu else N), dev, stream)
-    return M, E, N, K, out
-
-
-def rnl_grouped_linear_bf16(x, W, offsets, rows=None, swiglu=False, out=None, workspace=None, stream=None):
-    """out[i] = x[rows[i]] @ W[e]^T for the rows i of expert e (offsets[e] <= i <
-    offsets[e + 1]; rows None: x[i]); with swiglu W[e] holds gate rows, then up
-    rows, and out = silu(gate) * up.  x [R, K], W [E, N, K], out [M, N or N / 2]."""
-    dev = x.device
-    M, E, N, K, out = _grouped_sizes(x, W, offsets, rows, swiglu, out, dev, stream)
-    _need(x, "x", torch.bfloat16, (x.shape[0], K), dev)
-    _need(W, "W", torch.bfloat16, (E, N, K), dev)
-    ws = _workspace(workspace_size(OP_GROUPED, M, K, N, E), dev, workspace, stream)
-    _check(load().rnl_grouped_linear_bf16(_ptr(x), x.shape[0], _ptr(W), E, N, K, _ptr(offsets), _ptr(rows), M,
-                                          int(bool(swiglu)), _ptr(out), _ptr(ws), ws.numel() * ws.element_size(),
-                                          _stream(dev, stream)), "rnl_grouped_linear_bf16")
-    return out
-
-
-def rnl_grouped_linear_mxfp8(x_codes, x_scale, w_codes, w_scale, offsets, rows=None, swiglu=False, block=64, out=None,
-                             workspace=None, stream=None):
-    """rnl_grouped_linear_bf16 on MXFP8 operands: codes uint8 [R, K] and [E, N, K],
-    scale bytes uint8 [R, K / block] and [E, N, K / block]; bf16 out."""
-    dev = x_codes.device
-    M, E, N, K, out = _grouped_sizes(x_codes, w_codes, offsets, rows, swiglu, out, dev, stream)
-    R, nb = x_codes.shape[0], K // block if block else 0
-    _need(x_codes, "x_codes", torch.uint8, (R, K), dev)
-    _need(x_scale, "x_scale", torch.uint8, (R, nb), dev)
-    _need(w_codes, "w_codes", torch.uint8, (E, N, K), dev)
-    _need(w_scale, "w_scale", torch.uint8, (E, N, nb), dev)
-    ws = _workspace(workspace_size(OP_GROUPED, M, K, N, E), dev, workspace, stream)
-    _check(load().rnl_grouped_linear_mxfp8(_ptr(x_codes), _ptr(x_scale), R, _ptr(w_codes), _ptr(w_scale), E, N, K,
-                                           int(block), _ptr(offsets), _ptr(rows), M, int(bool(swiglu)), _ptr(out),
-                                           _ptr(ws), ws.numel() * ws.element_size(), _stream(dev, stream)),
-           "rnl_grouped_linear_mxfp8")
-    return out
-
-
-def rnl_moe_combine(y, slots, weights, residual=None, out=None, stream=None):
-    """out[t] = residual[t] + sum_j weights[t, j] * y[slots[t, j]] (slots -1 left
-    out); y [M, N] bf16, slots and weights [T, k]; out may be residual."""
-    M, N = y.shape
-    T, k = slots.shape
-    dev = y.device
-    _need(y, "y", torch.bfloat16, (M, N), dev)
-    _need(slots, "slots", torch.int32, (T, k), dev)
-    _need(weights, "weights", torch.float32, (T, k), dev)
-    if residual is not None:
-        _need(residual, "residual", torch.bfloat16, (T, N), dev)
-    out = _out(out, "out", torch.bfloat16, (T, N), dev, stream)
-    _check(load().rnl_moe_combine(_ptr(y), M, N, _ptr(slots), _ptr(weights), T, k, _ptr(residual), _ptr(out),
-                                  _stream(dev, stream)), "rnl_moe_combine")
     return out
 
 

@@ -101,7 +101,7 @@ __device__ __forceinline__ int source_row(const Args& a, int i) {
   int v = i;
   if (a.rows != nullptr) v = a.rows[i];
   if (v < 0 || v >= a.R) {
-    atomicCAS(&g_err_grouped, 0u, kErrArg | (111u << 8));
+    atomicCAS(&g_err_grouped, 0u, kErrArg | (204u << 8));
     v = 0;
   }
   return v;
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
   }
   grid_launch_dependents();
   grid_dependency_wait();
-  build_groups(a.offsets, a.E, a.M, num_f, kTile, off, pre, &g_err_grouped, 110);
+  build_groups(a.offsets, a.E, a.M, num_f, kTile, off, pre, &g_err_grouped, 213);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
@@ -216,8 +216,8 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
       if (lane == 0) {
         const int f0 = (w.t.f * 2 + static_cast<int>(rank)) * kFeatCta;
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (!mbar_wait_cluster(smem_u32(&ctrl->empty[stage]), phase ^ 1u, abort, &g_err_grouped, 112) ||
-              !RNL_DCHECK(&g_err_grouped, stage < static_cast<uint32_t>(a.stages), 113)) {
+          if (!mbar_wait_cluster(smem_u32(&ctrl->empty[stage]), phase ^ 1u, abort, &g_err_grouped, 205) ||
+              !RNL_DCHECK(&g_err_grouped, stage < static_cast<uint32_t>(a.stages), 206)) {
             ok = false;
             break;
           }
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
       const Item w = walk.at(it);
       if (lane == 0) {
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (!mbar_wait(smem_u32(&ctrl->landed[stage]), phase, abort, &g_err_grouped, 108)) {
+          if (!mbar_wait(smem_u32(&ctrl->landed[stage]), phase, abort, &g_err_grouped, 202)) {
             ok = false;
             break;
           }
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
             uint4 wa = make_uint4(s[0], s[32], s[64], s[96]);
             uint4 wb0 = make_uint4(s[128], s[160], s[192], s[224]);
             uint4 wb1 = make_uint4(s[256], s[288], s[320], 0u);
-            const bool got = mbar_wait_cluster(smem_u32(&ctrl->sf_empty[slot]), phase ^ 1u, abort, &g_err_grouped, 106);
+            const bool got = mbar_wait_cluster(smem_u32(&ctrl->sf_empty[slot]), phase ^ 1u, abort, &g_err_grouped, 200);
             if (!__all_sync(0xffffffffu, got)) {
               ok = false;
               break;
@@ -364,8 +364,8 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
       for (int i = 0; i < 8; ++i)  // rows behind the tile's last one repeat it (their columns are not stored)
         src[i] = a.x + source_row(a, w.t.row0 + min(first + 4 * i, w.t.valid - 1)) * a.row_bytes + chunk * 16;
       for (int kb = w.kb0; kb < w.kb1; ++kb) {
-        const bool got = mbar_wait_cluster(smem_u32(&ctrl->empty[stage]), phase ^ 1u, abort, &g_err_grouped, 119);
-        if (!__all_sync(0xffffffffu, got && RNL_DCHECK(&g_err_grouped, half <= kTile / 2, 109))) {
+        const bool got = mbar_wait_cluster(smem_u32(&ctrl->empty[stage]), phase ^ 1u, abort, &g_err_grouped, 212);
+        if (!__all_sync(0xffffffffu, got && RNL_DCHECK(&g_err_grouped, half <= kTile / 2, 203))) {
           ok = false;
           break;
         }
@@ -394,13 +394,13 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
         const Item w = walk.at(it);
         if (lane == 0) {
           const uint32_t buf = it & 1;
-          ok = mbar_wait_cluster(smem_u32(&ctrl->tmem_empty[buf]), ((it >> 1) & 1) ^ 1u, abort, &g_err_grouped, 114);
+          ok = mbar_wait_cluster(smem_u32(&ctrl->tmem_empty[buf]), ((it >> 1) & 1) ^ 1u, abort, &g_err_grouped, 207);
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + buf * kTile;
           const uint32_t idesc = MX ? idesc_mxf8(256, w.t.n) : idesc_bf16(256, w.t.n);
           for (int kb = w.kb0; kb < w.kb1 && ok; ++kb) {
-            if (!mbar_wait_cluster(smem_u32(&ctrl->full[stage]), phase, abort, &g_err_grouped, 115) ||
-                (MX && !mbar_wait_cluster(smem_u32(&ctrl->sf_full[slot]), sf_phase, abort, &g_err_grouped, 107))) {
+            if (!mbar_wait_cluster(smem_u32(&ctrl->full[stage]), phase, abort, &g_err_grouped, 208) ||
+                (MX && !mbar_wait_cluster(smem_u32(&ctrl->sf_full[slot]), sf_phase, abort, &g_err_grouped, 201))) {
               ok = false;
               break;
             }
@@ -448,11 +448,11 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
       const Item w = walk.at(it);
       const Tile& t = w.t;
       const uint32_t buf = it & 1;
-      bool got = mbar_wait_cluster(smem_u32(&ctrl->tmem_full[buf]), (it >> 1) & 1, abort, &g_err_grouped, 116);
+      bool got = mbar_wait_cluster(smem_u32(&ctrl->tmem_full[buf]), (it >> 1) & 1, abort, &g_err_grouped, 209);
       if (w.kind == kFinish && got && lane == 0)
         for (int q = w.first; q < pair && got; ++q)
           got = flag_wait(a.flags + (static_cast<int64_t>(q) * 2 + rank) * kEpiWarps + ew, a.epoch, abort,
-                          &g_err_grouped, 117);
+                          &g_err_grouped, 210);
       if (!__all_sync(0xffffffffu, got)) break;
       __syncwarp();  // what lane 0 acquired is every lane's
       tc_fence_after();
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
         uint32_t r[32];
         tmem_ld_32cols(tmem_base + lane_addr + buf * kTile + c, r);
         tmem_ld_wait();
-        if (!RNL_DCHECK(&g_err_grouped, c + 32 <= kTile && t.row0 + t.valid <= a.M && pair < kMaxPairs, 118)) continue;
+        if (!RNL_DCHECK(&g_err_grouped, c + 32 <= kTile && t.row0 + t.valid <= a.M && pair < kMaxPairs, 211)) continue;
         if (w.kind == kPartial) {
           float* dst = a.partial + pair * kSlotWords + lane_off + static_cast<int64_t>(c) * 128;
 #pragma unroll

@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(256)
         const int s = __ldg(slots + t * k + j0 + j);
         w[j] = __ldg(weights + t * k + j0 + j);
         on[j] = s >= 0 && s < M;
-        if (!on[j] && s != -1) atomicCAS(&g_err_moe, 0u, kErrArg | (120u << 8));
+        if (!on[j] && s != -1) atomicCAS(&g_err_moe, 0u, kErrArg | (214u << 8));
         if (on[j]) u[j] = __ldg(y + static_cast<int64_t>(s) * nvec + v);
       }
     }
