@@ -49,7 +49,8 @@ constexpr int kSfBatch = 4;
 constexpr int kSfWords = 11 * 32;
 
 // MX: two accumulators of 224 columns leave 64 columns of TMEM for the scales of
-// four k-blocks (weight rows' at +0, the group's at +8 of 16).
+// four k-blocks, two slots of an even and an odd one (of 16 columns each: weight
+// rows' at +0, the group's at +8).
 template <bool MX>
 struct Form {
   static constexpr int kTile = MX ? 224 : 256;  // rows of a group a tile, at most
@@ -57,9 +58,9 @@ struct Form {
   static constexpr uint32_t kStageBytes = kABytes + kTile / 2 * kRowBytes;
   static constexpr size_t kSfBytes = MX ? 2 * kSfBatch * kSfWords * 4 : 0;
   static constexpr uint32_t kSfBase = 2 * kTile;
-  static constexpr int kSfSlots = 4;
+  static constexpr int kSfSlots = 2;
   static_assert(kStageBytes % 1024 == 0, "swizzle atoms");
-  static_assert(!MX || kSfBase + kSfSlots * 16 <= 512, "TMEM columns");
+  static_assert(!MX || kSfBase + kSfSlots * 32 <= 512, "TMEM columns");
 };
 
 struct __align__(8) Ctrl {
@@ -68,8 +69,8 @@ struct __align__(8) Ctrl {
   uint64_t landed[kMaxStages];  // each CTA: its gathered rows of a stage
   uint64_t tmem_full[2];       // each CTA: accumulator ready
   uint64_t tmem_empty[2];      // even CTA: both CTAs' epilogues have read it
-  uint64_t sf_full[4];         // even CTA: both CTAs' scales of a slot are in TMEM
-  uint64_t sf_empty[4];        // each CTA: the slot's k-block has been multiplied
+  uint64_t sf_full[2];         // even CTA: both CTAs' scales of a slot are in TMEM
+  uint64_t sf_empty[2];        // each CTA: the slot's k-blocks have been multiplied
   uint32_t tmem_base;
   int abort;
 };
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
   int* off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(sf_smem) + F::kSfBytes);
   int* pre = off + a.E + 1;
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1;
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
       if (lane == 0) {
         const int f0 = (w.t.f * 2 + static_cast<int>(rank)) * kFeatCta;
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (!mbar_wait_cluster(smem_u32(&ctrl->empty[stage]), phase ^ 1u, abort, &g_err_grouped, 205) ||
+          if (!mbar_wait(smem_u32(&ctrl->empty[stage]), phase ^ 1u, abort, &g_err_grouped, 205) ||
               !RNL_DCHECK(&g_err_grouped, stage < static_cast<uint32_t>(a.stages), 206)) {
             ok = false;
             break;
@@ -297,14 +298,18 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
             if (me + 128 * h < w.t.valid)
               p[1 + h] = a.x_scale + static_cast<int64_t>(source_row(a, w.t.row0 + me + 128 * h)) * a.nb;
         }
-        for (int kb = w.kb0 & ~(kSfBatch - 1); kb < w.kb1; kb += kSfBatch) {
-          uint32_t v[3][kSfBatch];
+        uint32_t v[3][kSfBatch];
+        auto load = [&](int kb) {
 #pragma unroll
           for (int h = 0; h < 3; ++h) {
 #pragma unroll
             for (int k = 0; k < kSfBatch; ++k) v[h][k] = 0x7F7F7F7Fu;
             if (p[h] != nullptr) load_scales<BLK>(p[h], kb, a.nb, a.sf_vec, v[h]);
           }
+        };
+        const int kb_first = w.kb0 & ~(kSfBatch - 1);
+        load(kb_first);
+        for (int kb = kb_first; kb < w.kb1; kb += kSfBatch) {
           uint32_t* sf = sf_smem + buf * (kSfBatch * kSfWords);
 #pragma unroll
           for (int k = 0; k < kSfBatch; ++k) {
@@ -313,21 +318,31 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
             if (me < 96) sf[k * kSfWords + 256 + me] = v[2][k];
           }
           asm volatile("bar.sync 1, 128;" ::: "memory");
-          for (int k = kb < w.kb0 ? w.kb0 - kb : 0; ok && k < kSfBatch && kb + k < w.kb1; ++k) {
-            const uint32_t* s = sf + k * kSfWords + lane;
-            uint4 wa = make_uint4(s[0], s[32], s[64], s[96]);
-            uint4 wb0 = make_uint4(s[128], s[160], s[192], s[224]);
-            uint4 wb1 = make_uint4(s[256], s[288], s[320], 0u);
-            const bool got = mbar_wait_cluster(smem_u32(&ctrl->sf_empty[slot]), phase ^ 1u, abort, &g_err_grouped, 200);
+          if (kb + kSfBatch < w.kb1) load(kb + kSfBatch);  // lands while this batch is written
+#pragma unroll
+          for (int k = 0; k < kSfBatch; k += 2) {  // a slot: two k-blocks
+            if (!ok || kb + k + 2 <= w.kb0 || kb + k >= w.kb1) continue;
+            uint4 wa[2], wb0[2], wb1[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t* s = sf + (k + h) * kSfWords + lane;
+              wa[h] = make_uint4(s[0], s[32], s[64], s[96]);
+              wb0[h] = make_uint4(s[128], s[160], s[192], s[224]);
+              wb1[h] = make_uint4(s[256], s[288], s[320], 0u);
+            }
+            const bool got = mbar_wait(smem_u32(&ctrl->sf_empty[slot]), phase ^ 1u, abort, &g_err_grouped, 200);
             if (!__all_sync(0xffffffffu, got)) {
               ok = false;
-              break;
+              continue;
             }
             tc_fence_after();
-            const uint32_t col = tmem_base + lane_addr + F::kSfBase + slot * 16;
-            tmem_st_4cols(col, wa);
-            tmem_st_4cols(col + 8, wb0);
-            tmem_st_4cols(col + 12, wb1);
+            const uint32_t col = tmem_base + lane_addr + F::kSfBase + slot * 32;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              tmem_st_4cols(col + 16 * h, wa[h]);
+              tmem_st_4cols(col + 16 * h + 8, wb0[h]);
+              tmem_st_4cols(col + 16 * h + 12, wb1[h]);
+            }
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -364,7 +379,7 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
       for (int i = 0; i < 8; ++i)  // rows behind the tile's last one repeat it (their columns are not stored)
         src[i] = a.x + source_row(a, w.t.row0 + min(first + 4 * i, w.t.valid - 1)) * a.row_bytes + chunk * 16;
       for (int kb = w.kb0; kb < w.kb1; ++kb) {
-        const bool got = mbar_wait_cluster(smem_u32(&ctrl->empty[stage]), phase ^ 1u, abort, &g_err_grouped, 212);
+        const bool got = mbar_wait(smem_u32(&ctrl->empty[stage]), phase ^ 1u, abort, &g_err_grouped, 212);
         if (!__all_sync(0xffffffffu, got && RNL_DCHECK(&g_err_grouped, half <= kTile / 2, 203))) {
           ok = false;
           break;
@@ -392,23 +407,25 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
       bool ok = true;
       for (int it = 0; it < walk.n && ok; ++it) {
         const Item w = walk.at(it);
-        if (lane == 0) {
-          const uint32_t buf = it & 1;
-          ok = mbar_wait_cluster(smem_u32(&ctrl->tmem_empty[buf]), ((it >> 1) & 1) ^ 1u, abort, &g_err_grouped, 207);
+        const uint32_t buf = it & 1;
+        ok = mbar_wait(smem_u32(&ctrl->tmem_empty[buf]), ((it >> 1) & 1) ^ 1u, abort, &g_err_grouped, 207);
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + buf * kTile;
+        const uint32_t idesc = MX ? idesc_mxf8(256, w.t.n) : idesc_bf16(256, w.t.n);
+        for (int kb = w.kb0; kb < w.kb1 && ok; ++kb) {
+          // (MX: a slot of scales holds an even and the next odd k-block)
+          const bool sf_new = MX && ((kb & 1) == 0 || kb == w.kb0);
+          ok = mbar_wait(smem_u32(&ctrl->full[stage]), phase, abort, &g_err_grouped, 208) &&
+               (!sf_new || mbar_wait(smem_u32(&ctrl->sf_full[slot]), sf_phase, abort, &g_err_grouped, 201));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t d_tmem = tmem_base + buf * kTile;
-          const uint32_t idesc = MX ? idesc_mxf8(256, w.t.n) : idesc_bf16(256, w.t.n);
-          for (int kb = w.kb0; kb < w.kb1 && ok; ++kb) {
-            if (!mbar_wait_cluster(smem_u32(&ctrl->full[stage]), phase, abort, &g_err_grouped, 208) ||
-                (MX && !mbar_wait_cluster(smem_u32(&ctrl->sf_full[slot]), sf_phase, abort, &g_err_grouped, 201))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t sa = base + stage * kStageBytes;
-            const uint64_t adesc = desc_kmajor_sw128(sa);
-            const uint64_t bdesc = desc_kmajor_sw128(sa + kABytes);
-            const uint32_t sf = tmem_base + F::kSfBase + slot * 16;
+          const uint32_t sa = base + stage * kStageBytes;
+          const uint64_t adesc = desc_kmajor_sw128(sa);
+          const uint64_t bdesc = desc_kmajor_sw128(sa + kABytes);
+          const uint32_t sf = tmem_base + F::kSfBase + slot * 32 + (kb & 1) * 16;
+          const bool sf_done = MX && ((kb & 1) != 0 || kb + 1 == w.kb1);
+          if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {  // 32 bytes of a row each
               const uint32_t add = (kb > w.kb0 || k > 0) ? 1u : 0u;
@@ -418,21 +435,19 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
                 umma_bf16_pair(d_tmem, adesc + 2 * k, bdesc + 2 * k, idesc, add);
             }
             umma_commit_pair(smem_u32(&ctrl->empty[stage]), 0x3);
-            if constexpr (MX) {
-              umma_commit_pair(smem_u32(&ctrl->sf_empty[slot]), 0x3);
-              if (++slot == F::kSfSlots) {
-                slot = 0;
-                sf_phase ^= 1u;
-              }
-            }
-            if (++stage == static_cast<uint32_t>(a.stages)) {
-              stage = 0;
-              phase ^= 1u;
-            }
+            if (sf_done) umma_commit_pair(smem_u32(&ctrl->sf_empty[slot]), 0x3);
+            if (kb + 1 == w.kb1) umma_commit_pair(smem_u32(&ctrl->tmem_full[buf]), 0x3);
           }
-          if (ok) umma_commit_pair(smem_u32(&ctrl->tmem_full[buf]), 0x3);
+          __syncwarp();
+          if (sf_done && ++slot == F::kSfSlots) {
+            slot = 0;
+            sf_phase ^= 1u;
+          }
+          if (++stage == static_cast<uint32_t>(a.stages)) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
       }
     }
   } else {
@@ -448,7 +463,7 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
       const Item w = walk.at(it);
       const Tile& t = w.t;
       const uint32_t buf = it & 1;
-      bool got = mbar_wait_cluster(smem_u32(&ctrl->tmem_full[buf]), (it >> 1) & 1, abort, &g_err_grouped, 209);
+      bool got = mbar_wait(smem_u32(&ctrl->tmem_full[buf]), (it >> 1) & 1, abort, &g_err_grouped, 209);
       if (w.kind == kFinish && got && lane == 0)
         for (int q = w.first; q < pair && got; ++q)
           got = flag_wait(a.flags + (static_cast<int64_t>(q) * 2 + rank) * kEpiWarps + ew, a.epoch, abort,

@@ -281,8 +281,8 @@ __device__ __forceinline__ void store_cols_swiglu(__nv_bfloat16* __restrict__ ou
   float v[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {  // lanes 0-15 take column 2j, lanes 16-31 the next one
-    const float got = __uint_as_float(__shfl_xor_sync(0xffffffffu, hi ? r[2 * j] : r[2 * j + 1], 16));
-    v[j] = hi ? swiglu_of(got, __uint_as_float(r[2 * j + 1])) : swiglu_of(__uint_as_float(r[2 * j]), got);
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? r[2 * j] : r[2 * j + 1], 16);
+    v[j] = swiglu_of(__uint_as_float(hi ? got : r[2 * j]), __uint_as_float(hi ? r[2 * j + 1] : got));
   }
   uint32_t w[8];
 #pragma unroll
