@@ -31,18 +31,6 @@ def _output(t, name, dtype, shape, dev, stream):
     return t
 
 
-def _mx_outputs(codes, scale, T, K, block, dev, stream):
-    """Codes and scale bytes: the caller's, or parts of one new tensor (an allocation
-    costs a small call 3.5 us, a view of one 0.7)."""
-    nb = K // block if block else 0
-    if codes is None and scale is None:
-        n = T * K
-        buf = _output(None, "", _U8, (n + T * nb,), dev, stream)
-        return buf.as_strided((T, K), (K, 1), 0), buf.as_strided((T, nb), (nb, 1), n)
-    return (_output(codes, "codes_out", _U8, (T, K), dev, stream),
-            _output(scale, "scale_out", _U8, (T, nb), dev, stream))
-
-
 def _space(nbytes, dev, given, stream):
     """(address, bytes) of the workspace and what keeps it alive; none where none is needed."""
     if given is None:
@@ -66,7 +54,8 @@ def rnl_add_rmsnorm_mxfp8(x, gamma=None, residual=None, x_sum_out=None, eps=1e-6
     pr = None if residual is None else _check(residual, "residual", _BF16, shape, dev)
     ps = None if x_sum_out is None else _check(x_sum_out, "x_sum_out", _BF16, shape, dev)
     pg = None if gamma is None else _check(gamma, "gamma", _BF16, (K,), dev)
-    codes_out, scale_out = _mx_outputs(codes_out, scale_out, T, K, block, dev, stream)
+    codes_out = _output(codes_out, "codes_out", _U8, shape, dev, stream)
+    scale_out = _output(scale_out, "scale_out", _U8, (T, K // block if block else 0), dev, stream)
     status = nat.load().rnl_add_rmsnorm_mxfp8(px, pr, ps, pg, T, K, eps, norm_mode, block, codes_out.data_ptr(),
                                               scale_out.data_ptr(), nat._stream(dev, stream))
     if status:
@@ -79,7 +68,8 @@ def rnl_quant_mxfp8(x, block=64, codes_out=None, scale_out=None, stream=None):
     shape = T, K = x.shape
     dev = x.device
     px = _check(x, "x", _BF16, shape, dev)
-    codes_out, scale_out = _mx_outputs(codes_out, scale_out, T, K, block, dev, stream)
+    codes_out = _output(codes_out, "codes_out", _U8, shape, dev, stream)
+    scale_out = _output(scale_out, "scale_out", _U8, (T, K // block if block else 0), dev, stream)
     status = nat.load().rnl_quant_mxfp8(px, T, K, block, codes_out.data_ptr(), scale_out.data_ptr(),
                                         nat._stream(dev, stream))
     if status:
@@ -99,19 +89,11 @@ def rnl_moe_route(logits, top_k, renormalize=True, ids_out=None, weights_out=Non
     dev = logits.device
     pl = _check(logits, "logits", _F32, (T, E), dev)
     k = max(top_k, 0)
-    if ids_out is None and weights_out is None and offsets_out is None and rows_out is None and slots_out is None:
-        n = T * k  # parts of one tensor, as _mx_outputs
-        buf = _output(None, "", _I32, (4 * n + E + 1,), dev, stream)
-        at = buf.as_strided
-        two, step = (T, k), (k, 1)
-        ids, slots, rows, offsets = at(two, step, 0), at(two, step, n), at((n,), (1,), 2 * n), at((E + 1,), (1,), 4 * n)
-        weights = buf.view(_F32).as_strided(two, step, 3 * n)
-    else:
-        ids = _output(ids_out, "ids_out", _I32, (T, k), dev, stream)
-        weights = _output(weights_out, "weights_out", _F32, (T, k), dev, stream)
-        offsets = _output(offsets_out, "offsets_out", _I32, (E + 1,), dev, stream)
-        rows = _output(rows_out, "rows_out", _I32, (T * k,), dev, stream)
-        slots = _output(slots_out, "slots_out", _I32, (T, k), dev, stream)
+    ids = _output(ids_out, "ids_out", _I32, (T, k), dev, stream)
+    weights = _output(weights_out, "weights_out", _F32, (T, k), dev, stream)
+    offsets = _output(offsets_out, "offsets_out", _I32, (E + 1,), dev, stream)
+    rows = _output(rows_out, "rows_out", _I32, (T * k,), dev, stream)
+    slots = _output(slots_out, "slots_out", _I32, (T, k), dev, stream)
     pw, nw, _keep = _space(nat.workspace_size(nat.OP_MOE_ROUTE, T, k, E), dev, workspace, stream)
     status = nat.load().rnl_moe_route(pl, T, E, top_k, 1 if renormalize else 0, ids.data_ptr(), weights.data_ptr(),
                                       offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(), pw, nw,

@@ -97,52 +97,61 @@ struct Args {
   uint64_t epoch;
 };
 
-// The row of x behind row i of the grouped order (0 where it is none: reported)
-__device__ __forceinline__ int source_row(const Args& a, int i) {
-  int v = i;
-  if (a.rows != nullptr) v = a.rows[i];
-  if (v < 0 || v >= a.R) {
-    atomicCAS(&g_err_grouped, 0u, kErrArg | (204u << 8));
-    v = 0;
-  }
-  return v;
+// The scale bytes of four k-blocks from kb on of one row, as they are loaded:
+// nothing is done with them before put_scales, so that a load's latency is not
+// waited for.  form: 2 one load, 1 one a k-block (both by the rows' alignment), 0
+// byte by byte, put together at once.
+template <int BLK>
+__device__ __forceinline__ int scale_form(int kb, int nb, int vec) {
+  constexpr int kPer = 128 / BLK;  // bytes a k-block: 4 or 2
+  const bool whole = (kb + kSfBatch) * kPer <= nb;
+  return whole && vec == 4 * kPer ? 2 : (whole && vec >= kPer ? 1 : 0);
 }
 
-// The scale words of four k-blocks from kb on of the row at p (bytes of K / BLK a
-// row, nb of them; 127 behind the last).  A 64-element scale is given to the
-// hardware's 32-element blocks twice.
 template <int BLK>
-__device__ __forceinline__ void load_scales(const uint8_t* p, int kb, int nb, int vec, uint32_t (&w)[kSfBatch]) {
-  constexpr int kPer = 128 / BLK;  // bytes a k-block: 4 or 2
-  const int b0 = kb * kPer;
-  if (vec == 4 * kPer && b0 + 4 * kPer <= nb) {
+__device__ __forceinline__ void load_scales(const uint8_t* p, int kb, int nb, int form, uint32_t (&w)[kSfBatch]) {
+  constexpr int kPer = 128 / BLK;
+  const uint8_t* q = p + kb * kPer;
+  if (form == 2) {
     if constexpr (BLK == 32) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(p + b0));
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(q));
       w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
     } else {
-      const uint2 u = __ldg(reinterpret_cast<const uint2*>(p + b0));
-      w[0] = __byte_perm(u.x, 0, 0x1100), w[1] = __byte_perm(u.x, 0, 0x3322);
-      w[2] = __byte_perm(u.y, 0, 0x1100), w[3] = __byte_perm(u.y, 0, 0x3322);
+      const uint2 u = __ldg(reinterpret_cast<const uint2*>(q));
+      w[0] = u.x, w[1] = u.y;
     }
-    return;
-  }
+  } else if (form == 1) {
 #pragma unroll
-  for (int k = 0; k < kSfBatch; ++k) {
-    const int b = b0 + k * kPer;
-    if (vec >= kPer && b + kPer <= nb) {
+    for (int k = 0; k < kSfBatch; ++k) {
       if constexpr (BLK == 32)
-        w[k] = __ldg(reinterpret_cast<const uint32_t*>(p + b));
+        w[k] = __ldg(reinterpret_cast<const uint32_t*>(q) + k);
       else
-        w[k] = __byte_perm(__ldg(reinterpret_cast<const uint16_t*>(p + b)), 0, 0x1100);
-    } else {
+        w[k] = __ldg(reinterpret_cast<const uint16_t*>(q) + k);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kSfBatch; ++k) {
       uint32_t v = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int at = b + j * kPer / 4;
+        const int at = kb * kPer + k * kPer + j * kPer / 4;
         v |= static_cast<uint32_t>(at < nb ? __ldg(p + at) : 127) << (8 * j);
       }
       w[k] = v;
     }
+  }
+}
+
+// The words of what load_scales has loaded, k-blocks kSfWords words apart.  A
+// 64-element scale is given to the hardware's 32-element blocks twice.
+template <int BLK>
+__device__ __forceinline__ void put_scales(uint32_t* dst, const uint32_t (&w)[kSfBatch], int form) {
+#pragma unroll
+  for (int k = 0; k < kSfBatch; ++k) {
+    uint32_t v = w[k];
+    if (BLK == 64 && form == 2) v = __byte_perm(w[k >> 1], 0, (k & 1) ? 0x3322 : 0x1100);
+    if (BLK == 64 && form == 1) v = __byte_perm(v, 0, 0x1100);
+    dst[k * kSfWords] = v;
   }
 }
 
@@ -278,47 +287,65 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
       const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
       uint32_t slot = 0, phase = 0, buf = 0;
       bool ok = true;
+      // rows me (weight), me and me + 128 (group) of the item in hand, and the next
+      // one's group rows, which are looked up an item ahead; scales are loaded a
+      // batch ahead, the next item's first ones during the last batch
+      const uint8_t* p[3];
+      uint32_t v[3][kSfBatch];
+      int form, next_row[2];
+      auto look_up = [&](const Item& w) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = w.t.row0 + min(me + 128 * h, w.t.valid - 1);
+          next_row[h] = a.rows != nullptr ? a.rows[i] : i;
+        }
+      };
+      auto point = [&](const Item& w) {
+        const int f0 = (w.t.f * 2 + static_cast<int>(rank)) * kFeatCta;
+        // rows that are none take another's scale, their products are not stored
+        int n;
+        if (SWIGLU)  // TMEM lane 32 q + 16 h + i: feature 16 q + i, gate (h = 0) or up
+          n = min(f0 + (me >> 5) * 16 + (me & 15), N_out - 1) + ((me & 16) ? N_out : 0);
+        else
+          n = min(f0 + me, a.N - 1);
+        p[0] = a.w_scale + (static_cast<int64_t>(w.t.e) * a.N + n) * a.nb;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = next_row[h];  // (the gathers report one that is out of range)
+          p[1 + h] = a.x_scale + static_cast<int64_t>(r >= 0 && r < a.R ? r : 0) * a.nb;
+        }
+      };
+      auto load = [&](int kb) {
+        form = scale_form<BLK>(kb, a.nb, a.sf_vec);
+#pragma unroll
+        for (int h = 0; h < 3; ++h) load_scales<BLK>(p[h], kb, a.nb, form, v[h]);
+      };
+      Item w, next;
+      if (walk.n > 0) {
+        next = walk.at(0);
+        look_up(next);
+        point(next);
+        load(next.kb0 & ~(kSfBatch - 1));
+      }
       // (a warp that gives up on a slot still takes part in the barriers below)
       for (int it = 0; it < walk.n; ++it) {
-        const Item w = walk.at(it);
-        // rows me (weight), me and me + 128 (group)
-        const int f0 = (w.t.f * 2 + static_cast<int>(rank)) * kFeatCta;
-        const uint8_t* p[3] = {nullptr, nullptr, nullptr};
-        {
-          int n;
-          if (SWIGLU) {  // TMEM lane 32 q + 16 h + i: feature 16 q + i, gate (h = 0) or up
-            const int f = f0 + (me >> 5) * 16 + (me & 15);
-            n = f < N_out ? f + ((me & 16) ? N_out : 0) : -1;
-          } else {
-            n = f0 + me < a.N ? f0 + me : -1;
-          }
-          if (n >= 0) p[0] = a.w_scale + (static_cast<int64_t>(w.t.e) * a.N + n) * a.nb;
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (me + 128 * h < w.t.valid)
-              p[1 + h] = a.x_scale + static_cast<int64_t>(source_row(a, w.t.row0 + me + 128 * h)) * a.nb;
-        }
-        uint32_t v[3][kSfBatch];
-        auto load = [&](int kb) {
-#pragma unroll
-          for (int h = 0; h < 3; ++h) {
-#pragma unroll
-            for (int k = 0; k < kSfBatch; ++k) v[h][k] = 0x7F7F7F7Fu;
-            if (p[h] != nullptr) load_scales<BLK>(p[h], kb, a.nb, a.sf_vec, v[h]);
-          }
-        };
-        const int kb_first = w.kb0 & ~(kSfBatch - 1);
-        load(kb_first);
-        for (int kb = kb_first; kb < w.kb1; kb += kSfBatch) {
+        w = next;
+        for (int kb = w.kb0 & ~(kSfBatch - 1); kb < w.kb1; kb += kSfBatch) {
           uint32_t* sf = sf_smem + buf * (kSfBatch * kSfWords);
-#pragma unroll
-          for (int k = 0; k < kSfBatch; ++k) {
-            sf[k * kSfWords + me] = v[0][k];
-            sf[k * kSfWords + 128 + me] = v[1][k];
-            if (me < 96) sf[k * kSfWords + 256 + me] = v[2][k];
-          }
+          put_scales<BLK>(sf + me, v[0], form);
+          put_scales<BLK>(sf + 128 + me, v[1], form);
+          if (me < 96) put_scales<BLK>(sf + 256 + me, v[2], form);
           asm volatile("bar.sync 1, 128;" ::: "memory");
-          if (kb + kSfBatch < w.kb1) load(kb + kSfBatch);  // lands while this batch is written
+          if (kb <= w.kb0 && it + 1 < walk.n) {  // the item's first batch
+            next = walk.at(it + 1);
+            look_up(next);
+          }
+          if (kb + kSfBatch < w.kb1) {
+            load(kb + kSfBatch);
+          } else if (it + 1 < walk.n) {
+            point(next);
+            load(next.kb0 & ~(kSfBatch - 1));
+          }
 #pragma unroll
           for (int k = 0; k < kSfBatch; k += 2) {  // a slot: two k-blocks
             if (!ok || kb + k + 2 <= w.kb0 || kb + k >= w.kb1) continue;
@@ -370,14 +397,36 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
     const int sub = lane >> 3, chunk = lane & 7;
     uint32_t stage = 0, phase = 0;
     bool ok = true;
+    Item w, next;
+    int row[8];  // of the next item
+    auto look_up = [&](const Item& i) {
+      const int first = static_cast<int>(rank) * (i.t.n / 2) + gw * 32 + sub;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {  // rows behind the tile's last one repeat it (their columns are not stored)
+        row[j] = i.t.row0 + min(first + 4 * j, i.t.valid - 1);
+        if (a.rows != nullptr) row[j] = a.rows[row[j]];
+      }
+    };
+    if (walk.n > 0) {
+      next = walk.at(0);
+      look_up(next);
+    }
     for (int it = 0; it < walk.n && ok; ++it) {
-      const Item w = walk.at(it);
+      w = next;
       const int half = w.t.n / 2;
-      const int first = static_cast<int>(rank) * half + gw * 32 + sub;
       const uint8_t* src[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)  // rows behind the tile's last one repeat it (their columns are not stored)
-        src[i] = a.x + source_row(a, w.t.row0 + min(first + 4 * i, w.t.valid - 1)) * a.row_bytes + chunk * 16;
+      for (int i = 0; i < 8; ++i) {
+        if (row[i] < 0 || row[i] >= a.R) {
+          atomicCAS(&g_err_grouped, 0u, kErrArg | (204u << 8));
+          row[i] = 0;
+        }
+        src[i] = a.x + row[i] * a.row_bytes + chunk * 16;
+      }
+      if (it + 1 < walk.n) {
+        next = walk.at(it + 1);
+        look_up(next);
+      }
       for (int kb = w.kb0; kb < w.kb1; ++kb) {
         const bool got = mbar_wait(smem_u32(&ctrl->empty[stage]), phase ^ 1u, abort, &g_err_grouped, 212);
         if (!__all_sync(0xffffffffu, got && RNL_DCHECK(&g_err_grouped, half <= kTile / 2, 203))) {

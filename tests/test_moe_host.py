@@ -278,7 +278,7 @@ def test_every_wrapper_is_covered_and_public():
     assert wrappers <= set(rnl.EXPORTS)
 
 
-def test_outputs_that_share_a_tensor_do_not_overlap(monkeypatch):
+def test_outputs_of_small_calls(monkeypatch):
     monkeypatch.setattr(nat, "load", lambda path=None: FakeLib())
     monkeypatch.setattr(nat, "_stream", lambda dev, stream: None)
     r = ex.rnl_moe_route(z(5, 7, dtype=F32), 3)
