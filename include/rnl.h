@@ -582,7 +582,9 @@ rnl_status rnl_moe_route(const float *logits, int64_t T, int64_t n_experts, int6
  * 0, 16-byte aligned x, W and out.  Workspace:
  * rnl_workspace_size(RNL_OP_GROUPED, M, K, N, n_experts) bytes; results do not
  * depend on its contents, and calls that may run at the same time need one
- * each.  K at most RNL_GROUPED_MAX_K, n_experts up to RNL_MOE_MAX_EXPERTS.
+ * each.  n_experts up to RNL_MOE_MAX_EXPERTS (else RNL_ERR_UNSUPPORTED); K at most
+ * RNL_GROUPED_MAX_K, M, n_experts * N and (M / 224 + n_experts) * (N / 128 + 1) at
+ * most 2^30 (else RNL_ERR_SHAPE).
  */
 #define RNL_GROUPED_MAX_K (1 << 24)
 rnl_status rnl_grouped_linear_bf16(const void *x, int64_t n_x_rows, const void *W, int64_t n_experts,

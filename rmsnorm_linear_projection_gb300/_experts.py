@@ -8,6 +8,7 @@ and the messages of _native._need where it fails.
 from __future__ import annotations
 
 import collections
+import functools
 
 import torch
 
@@ -29,6 +30,10 @@ def _output(t, name, dtype, shape, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev) if stream is None else nat._new(shape, dtype, dev, stream)
     _check(t, name, dtype, shape, dev)
     return t
+
+
+# a function of the sizes alone; the call itself is 1 us of a small call's 10
+_workspace_size = functools.lru_cache(maxsize=256)(nat.workspace_size)
 
 
 def _space(nbytes, dev, given, stream):
@@ -94,7 +99,7 @@ def rnl_moe_route(logits, top_k, renormalize=True, ids_out=None, weights_out=Non
     offsets = _output(offsets_out, "offsets_out", _I32, (E + 1,), dev, stream)
     rows = _output(rows_out, "rows_out", _I32, (T * k,), dev, stream)
     slots = _output(slots_out, "slots_out", _I32, (T, k), dev, stream)
-    pw, nw, _keep = _space(nat.workspace_size(nat.OP_MOE_ROUTE, T, k, E), dev, workspace, stream)
+    pw, nw, _keep = _space(_workspace_size(nat.OP_MOE_ROUTE, T, k, E), dev, workspace, stream)
     status = nat.load().rnl_moe_route(pl, T, E, top_k, 1 if renormalize else 0, ids.data_ptr(), weights.data_ptr(),
                                       offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(), pw, nw,
                                       nat._stream(dev, stream))
@@ -122,7 +127,7 @@ def rnl_grouped_linear_bf16(x, W, offsets, rows=None, swiglu=False, out=None, wo
     dev = x.device
     px, pW = _check(x, "x", _BF16, (R, K), dev), _check(W, "W", _BF16, (E, N, K), dev)
     M, po, pr, out = _rows_and_output(R, E, N, offsets, rows, swiglu, out, dev, stream)
-    pw, nw, _keep = _space(nat.workspace_size(nat.OP_GROUPED, M, K, N, E), dev, workspace, stream)
+    pw, nw, _keep = _space(_workspace_size(nat.OP_GROUPED, M, K, N, E), dev, workspace, stream)
     status = nat.load().rnl_grouped_linear_bf16(px, R, pW, E, N, K, po, pr, M, 1 if swiglu else 0, out.data_ptr(), pw,
                                                 nw, nat._stream(dev, stream))
     if status:
@@ -141,7 +146,7 @@ def rnl_grouped_linear_mxfp8(x_codes, x_scale, w_codes, w_scale, offsets, rows=N
     px, pxs = _check(x_codes, "x_codes", _U8, (R, K), dev), _check(x_scale, "x_scale", _U8, (R, nb), dev)
     pW, pWs = _check(w_codes, "w_codes", _U8, (E, N, K), dev), _check(w_scale, "w_scale", _U8, (E, N, nb), dev)
     M, po, pr, out = _rows_and_output(R, E, N, offsets, rows, swiglu, out, dev, stream)
-    pw, nw, _keep = _space(nat.workspace_size(nat.OP_GROUPED, M, K, N, E), dev, workspace, stream)
+    pw, nw, _keep = _space(_workspace_size(nat.OP_GROUPED, M, K, N, E), dev, workspace, stream)
     status = nat.load().rnl_grouped_linear_mxfp8(px, pxs, R, pW, pWs, E, N, K, block, po, pr, M, 1 if swiglu else 0,
                                                  out.data_ptr(), pw, nw, nat._stream(dev, stream))
     if status:

@@ -1271,9 +1271,14 @@ rnl_status rnl_moe_combine(const void* y, int64_t M, int64_t N, const int32_t* s
 static rnl_status check_grouped(const GroupedArgs& g, size_t workspace_bytes, bool* go) {
   *go = false;
   if (bad_dim(g.R) || bad_dim(g.E) || bad_dim(g.N) || bad_dim(g.K) || bad_dim(g.M) || g.E == 0 || g.N == 0 ||
-      g.K == 0 || bad_dim(g.E * g.N) || (!g.rows && g.R != g.M))
+      g.K == 0 || (!g.rows && g.R != g.M))
     return RNL_ERR_SHAPE;
-  if (g.K > RNL_GROUPED_MAX_K) return RNL_ERR_SHAPE;
+  // rows, weight rows and tiles (of 128 outputs x 224 rows at least, one more an
+  // expert) stay inside 32-bit kernel indices
+  constexpr int64_t kMost = int64_t{1} << 30;
+  if (g.K > RNL_GROUPED_MAX_K || g.M > kMost || g.E > kMost / g.N ||
+      (g.M / 224 + g.E) * (g.N / 128 + 1) > kMost)
+    return RNL_ERR_SHAPE;
   if (g.E > RNL_MOE_MAX_EXPERTS || (g.swiglu && g.N % 32 != 0)) return RNL_ERR_UNSUPPORTED;
   if (g.M == 0) return RNL_OK;
   if (g.R == 0) return RNL_ERR_SHAPE;  // rows of nothing

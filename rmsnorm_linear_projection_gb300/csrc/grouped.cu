@@ -43,10 +43,11 @@ constexpr int kScaleWarps = 4;                    // one a TMEM lane quarter
 constexpr int64_t kSlotWords = 2 * 128 * 256;     // partial sums of one pair: [CTA][column][lane]
 constexpr int kMaxPairs = kMaxPartialSlots - 1;   // the last slot holds the flags
 
-// Scales of four k-blocks in shared memory: [k-block][32 rows][lane] words, a word
-// the four E8M0 bytes of a row's k-block; 4 x 32 weight rows, then 7 x 32 rows of x.
+// Scales go through shared memory four k-blocks at a time, a row's bytes of them
+// (16, or 8 with 64 elements a scale) after the other: 128 weight rows, then 224
+// rows of x.
 constexpr int kSfBatch = 4;
-constexpr int kSfWords = 11 * 32;
+constexpr int kSfRows = 11 * 32;
 
 // MX: two accumulators of 224 columns leave 64 columns of TMEM for the scales of
 // four k-blocks, two slots of an even and an odd one (of 16 columns each: weight
@@ -56,14 +57,14 @@ struct Form {
   static constexpr int kTile = MX ? 224 : 256;  // rows of a group a tile, at most
   static constexpr int kThreads = (kRelayWarp + 1 + (MX ? kScaleWarps : 0)) * 32;
   static constexpr uint32_t kStageBytes = kABytes + kTile / 2 * kRowBytes;
-  static constexpr size_t kSfBytes = MX ? 2 * kSfBatch * kSfWords * 4 : 0;
+  static constexpr size_t kSfBytes = MX ? 2 * kSfRows * 16 : 0;
   static constexpr uint32_t kSfBase = 2 * kTile;
   static constexpr int kSfSlots = 2;
   static_assert(kStageBytes % 1024 == 0, "swizzle atoms");
   static_assert(!MX || kSfBase + kSfSlots * 32 <= 512, "TMEM columns");
 };
 
-struct __align__(8) Ctrl {
+struct __align__(16) Ctrl {
   uint64_t full[kMaxStages];   // even CTA: both CTAs' loads of a stage
   uint64_t empty[kMaxStages];  // each CTA: its stage read by the pair's MMAs
   uint64_t landed[kMaxStages];  // each CTA: its gathered rows of a stage
@@ -133,8 +134,8 @@ __device__ __forceinline__ void load_scales(const uint8_t* p, int kb, int nb, in
     for (int k = 0; k < kSfBatch; ++k) {
       uint32_t v = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int at = kb * kPer + k * kPer + j * kPer / 4;
+      for (int j = 0; j < kPer; ++j) {
+        const int at = (kb + k) * kPer + j;
         v |= static_cast<uint32_t>(at < nb ? __ldg(p + at) : 127) << (8 * j);
       }
       w[k] = v;
@@ -142,16 +143,29 @@ __device__ __forceinline__ void load_scales(const uint8_t* p, int kb, int nb, in
   }
 }
 
-// The words of what load_scales has loaded, k-blocks kSfWords words apart.  A
-// 64-element scale is given to the hardware's 32-element blocks twice.
+// What load_scales has loaded of a row, its bytes one after the other.
 template <int BLK>
-__device__ __forceinline__ void put_scales(uint32_t* dst, const uint32_t (&w)[kSfBatch], int form) {
-#pragma unroll
-  for (int k = 0; k < kSfBatch; ++k) {
-    uint32_t v = w[k];
-    if (BLK == 64 && form == 2) v = __byte_perm(w[k >> 1], 0, (k & 1) ? 0x3322 : 0x1100);
-    if (BLK == 64 && form == 1) v = __byte_perm(v, 0, 0x1100);
-    dst[k * kSfWords] = v;
+__device__ __forceinline__ void put_scales(uint8_t* dst, const uint32_t (&w)[kSfBatch], int form) {
+  if constexpr (BLK == 32)
+    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+  else
+    *reinterpret_cast<uint2*>(dst) =
+        form == 2 ? make_uint2(w[0], w[1])
+                  : make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
+}
+
+// The scale words of two k-blocks of a row (its bytes in shared memory at p): a byte
+// for each 32-element block of the hardware, a 64-element scale given to it twice.
+template <int BLK>
+__device__ __forceinline__ void take_scales(const uint8_t* p, uint32_t& even, uint32_t& odd) {
+  if constexpr (BLK == 32) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    even = u.x;
+    odd = u.y;
+  } else {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+    even = __byte_perm(u, 0, 0x1100);
+    odd = __byte_perm(u, 0, 0x3322);
   }
 }
 
@@ -171,7 +185,7 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
   const uint32_t base = (raw_addr + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw_addr);
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + a.stages * kStageBytes);
-  uint32_t* sf_smem = reinterpret_cast<uint32_t*>(ctrl + 1);  // 2 x [kSfBatch][kSfWords]
+  uint32_t* sf_smem = reinterpret_cast<uint32_t*>(ctrl + 1);  // two batches of scales
   int* off = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(sf_smem) + F::kSfBytes);
   int* pre = off + a.E + 1;
 
@@ -285,22 +299,26 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
       const int quarter = warp & 3;
       const int me = (warp - kRelayWarp - 1) * 32 + lane;
       const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-      uint32_t slot = 0, phase = 0, buf = 0;
+      uint32_t slot = 0, phase = 0;
       bool ok = true;
-      // rows me (weight), me and me + 128 (group) of the item in hand, and the next
-      // one's group rows, which are looked up an item ahead; scales are loaded a
-      // batch ahead, the next item's first ones during the last batch
+      // Scales are loaded two batches ahead, across items (one batch ahead, a batch
+      // took as long as its loads, 1.1 us), and the rows of the group are looked up an
+      // item ahead.  What is being loaded: batch `kb` of item `it`, rows me (weight),
+      // me and me + 128 (group).
+      int it = 0, kb = 0, next_row[2];
       const uint8_t* p[3];
-      uint32_t v[3][kSfBatch];
-      int form, next_row[2];
-      auto look_up = [&](const Item& w) {
+      Item w, next;
+      auto look_up = [&]() {  // the next item and its rows
+        next = walk.at(it + 1 < walk.n ? it + 1 : it);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int i = w.t.row0 + min(me + 128 * h, w.t.valid - 1);
+          const int i = next.t.row0 + min(me + 128 * h, next.t.valid - 1);
           next_row[h] = a.rows != nullptr ? a.rows[i] : i;
         }
       };
-      auto point = [&](const Item& w) {
+      auto enter = [&]() {  // makes the next item the one in hand
+        w = next;
+        kb = w.kb0 & ~(kSfBatch - 1);
         const int f0 = (w.t.f * 2 + static_cast<int>(rank)) * kFeatCta;
         // rows that are none take another's scale, their products are not stored
         int n;
@@ -314,78 +332,82 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
           const int r = next_row[h];  // (the gathers report one that is out of range)
           p[1 + h] = a.x_scale + static_cast<int64_t>(r >= 0 && r < a.R ? r : 0) * a.nb;
         }
+        look_up();
       };
-      auto load = [&](int kb) {
-        form = scale_form<BLK>(kb, a.nb, a.sf_vec);
+      // a batch: its scales, its first k-block and the range of them that is multiplied
+      struct Batch {
+        uint32_t v[3][kSfBatch];
+        int form, kb, lo, hi;  // hi 0: none
+      };
+      auto load = [&](Batch& b) {
+        b.hi = 0;
+        if (it >= walk.n) return;
+        b.form = scale_form<BLK>(kb, a.nb, a.sf_vec);
 #pragma unroll
-        for (int h = 0; h < 3; ++h) load_scales<BLK>(p[h], kb, a.nb, form, v[h]);
+        for (int h = 0; h < 3; ++h) load_scales<BLK>(p[h], kb, a.nb, b.form, b.v[h]);
+        b.kb = kb;
+        b.lo = w.kb0;
+        b.hi = w.kb1;
+        kb += kSfBatch;
+        if (kb >= w.kb1 && ++it < walk.n) enter();
       };
-      Item w, next;
+      constexpr int kRowScale = BLK == 32 ? 16 : 8;  // bytes of a row and batch
+      auto write = [&](Batch& b, uint8_t* sf) {
+        put_scales<BLK>(sf + me * kRowScale, b.v[0], b.form);
+        put_scales<BLK>(sf + (128 + me) * kRowScale, b.v[1], b.form);
+        if (me < 96) put_scales<BLK>(sf + (256 + me) * kRowScale, b.v[2], b.form);
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const int first = b.kb, lo = b.lo, hi = b.hi;
+        load(b);
+#pragma unroll
+        for (int k = 0; k < kSfBatch; k += 2) {  // a slot: two k-blocks
+          // (a warp that gives up on a slot still takes part in the barriers)
+          if (!ok || first + k + 2 <= lo || first + k >= hi) continue;
+          uint32_t even[16], odd[16];  // columns: weight rows' words at 0, the group's at 8
+          const uint8_t* q = sf + lane * kRowScale + k * (kRowScale / kSfBatch);
+#pragma unroll
+          for (int j = 0; j < 11; ++j)
+            take_scales<BLK>(q + j * 32 * kRowScale, even[j < 4 ? j : j + 4], odd[j < 4 ? j : j + 4]);
+#pragma unroll
+          for (int j = 4; j < 8; ++j) even[j] = odd[j] = 0u;
+          even[15] = odd[15] = 0u;
+          const bool got = mbar_wait(smem_u32(&ctrl->sf_empty[slot]), phase ^ 1u, abort, &g_err_grouped, 200);
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            continue;
+          }
+          tc_fence_after();
+          const uint32_t col = tmem_base + lane_addr + F::kSfBase + slot * 32;
+          tmem_st_16cols(col, even);
+          tmem_st_16cols(col + 16, odd);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            const uint32_t bar = smem_u32(&ctrl->sf_full[slot]);
+            if (rank == 0)
+              mbar_arrive(bar);
+            else
+              mbar_arrive_remote(mapa_shared(bar, 0));
+          }
+          if (++slot == F::kSfSlots) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      };
       if (walk.n > 0) {
-        next = walk.at(0);
-        look_up(next);
-        point(next);
-        load(next.kb0 & ~(kSfBatch - 1));
-      }
-      // (a warp that gives up on a slot still takes part in the barriers below)
-      for (int it = 0; it < walk.n; ++it) {
-        w = next;
-        for (int kb = w.kb0 & ~(kSfBatch - 1); kb < w.kb1; kb += kSfBatch) {
-          uint32_t* sf = sf_smem + buf * (kSfBatch * kSfWords);
-          put_scales<BLK>(sf + me, v[0], form);
-          put_scales<BLK>(sf + 128 + me, v[1], form);
-          if (me < 96) put_scales<BLK>(sf + 256 + me, v[2], form);
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-          if (kb <= w.kb0 && it + 1 < walk.n) {  // the item's first batch
-            next = walk.at(it + 1);
-            look_up(next);
-          }
-          if (kb + kSfBatch < w.kb1) {
-            load(kb + kSfBatch);
-          } else if (it + 1 < walk.n) {
-            point(next);
-            load(next.kb0 & ~(kSfBatch - 1));
-          }
-#pragma unroll
-          for (int k = 0; k < kSfBatch; k += 2) {  // a slot: two k-blocks
-            if (!ok || kb + k + 2 <= w.kb0 || kb + k >= w.kb1) continue;
-            uint4 wa[2], wb0[2], wb1[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t* s = sf + (k + h) * kSfWords + lane;
-              wa[h] = make_uint4(s[0], s[32], s[64], s[96]);
-              wb0[h] = make_uint4(s[128], s[160], s[192], s[224]);
-              wb1[h] = make_uint4(s[256], s[288], s[320], 0u);
-            }
-            const bool got = mbar_wait(smem_u32(&ctrl->sf_empty[slot]), phase ^ 1u, abort, &g_err_grouped, 200);
-            if (!__all_sync(0xffffffffu, got)) {
-              ok = false;
-              continue;
-            }
-            tc_fence_after();
-            const uint32_t col = tmem_base + lane_addr + F::kSfBase + slot * 32;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              tmem_st_4cols(col + 16 * h, wa[h]);
-              tmem_st_4cols(col + 16 * h + 8, wb0[h]);
-              tmem_st_4cols(col + 16 * h + 12, wb1[h]);
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              const uint32_t bar = smem_u32(&ctrl->sf_full[slot]);
-              if (rank == 0)
-                mbar_arrive(bar);
-              else
-                mbar_arrive_remote(mapa_shared(bar, 0));
-            }
-            if (++slot == F::kSfSlots) {
-              slot = 0;
-              phase ^= 1u;
-            }
-          }
-          buf ^= 1u;
+        it = -1;
+        look_up();
+        it = 0;
+        enter();
+        Batch b0, b1;
+        load(b0);
+        load(b1);
+        while (b0.hi > 0) {
+          write(b0, reinterpret_cast<uint8_t*>(sf_smem));
+          if (b1.hi == 0) break;
+          write(b1, reinterpret_cast<uint8_t*>(sf_smem) + kSfRows * 16);
         }
       }
     }
@@ -454,8 +476,9 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
     if (rank == 0) {
       uint32_t stage = 0, phase = 0, slot = 0, sf_phase = 0;
       bool ok = true;
+      Item next = walk.at(0);
       for (int it = 0; it < walk.n && ok; ++it) {
-        const Item w = walk.at(it);
+        const Item w = next;
         const uint32_t buf = it & 1;
         ok = mbar_wait(smem_u32(&ctrl->tmem_empty[buf]), ((it >> 1) & 1) ^ 1u, abort, &g_err_grouped, 207);
         tc_fence_after();
@@ -488,6 +511,7 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
             if (kb + 1 == w.kb1) umma_commit_pair(smem_u32(&ctrl->tmem_full[buf]), 0x3);
           }
           __syncwarp();
+          if (kb == w.kb0 && it + 1 < walk.n) next = walk.at(it + 1);  // while the products run
           if (sf_done && ++slot == F::kSfSlots) {
             slot = 0;
             sf_phase ^= 1u;

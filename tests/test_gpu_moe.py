@@ -325,3 +325,185 @@ def test_grouped_mx_nan_scales_stay_in_their_rows():
     bad[40:, 100] = True
     assert torch.equal(torch.isnan(out), bad)
     assert torch.equal(out[~bad], good[~bad])
+
+
+# ------------------------------------------------------- how calls are made
+def test_bad_offsets_and_rows_are_reported():
+    g = gen(3)
+    x, W = randn(g, 8, 64).bfloat16(), randn(g, 3, 32, 64).bfloat16()
+    for off in ([0, 5, 3, 8], [0, 2, 4, 9], [-1, 2, 4, 8]):
+        out = torch.full((8, 32), 7.0, dtype=torch.bfloat16, device="cuda")
+        rnl.rnl_grouped_linear_bf16(x, W, i32(off), out=out)
+        with pytest.raises(rnl.RnlError) as e:
+            rnl.rnl_check_device_error()
+        assert e.value.status == 4 and (out == 7).all()
+    rows = i32([0, 1, 8, 3, -1, 5, 6, 7])
+    good = i32([0, 1, 2, 3, 4, 5, 6, 7])
+    off = i32([0, 3, 5, 8])
+    out = rnl.rnl_grouped_linear_bf16(x, W, off, rows=rows)
+    with pytest.raises(rnl.RnlError) as e:
+        rnl.rnl_check_device_error()
+    assert e.value.status == 4
+    want = rnl.rnl_grouped_linear_bf16(x, W, off, rows=good)
+    fine = [0, 1, 3, 5, 6, 7]
+    assert torch.equal(out[fine], want[fine])
+
+
+def test_rows_in_front_of_the_first_group_stay():
+    g = gen(4)
+    x, W = randn(g, 100, 128).bfloat16(), randn(g, 2, 64, 128).bfloat16()
+    out = torch.full((100, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    rnl.rnl_grouped_linear_bf16(x, W, i32([30, 60, 90]), out=out)
+    want = rnl.rnl_grouped_linear_bf16(x[30:90].contiguous(), W, i32([0, 30, 60]))
+    assert (out[:30] == 7).all() and (out[90:] == 7).all() and torch.equal(out[30:90], want)
+
+
+def layer(g, T, E, k, K, F):
+    """A layer of experts: its weights, bf16 and MXFP8."""
+    w1 = (randn(g, E, 2 * F, K) / math.sqrt(K)).bfloat16()
+    w2 = (randn(g, E, K, F) / math.sqrt(F)).bfloat16()
+    q1, s1 = rnl.rnl_quant_mxfp8(w1.view(-1, K), block=32)
+    q2, s2 = rnl.rnl_quant_mxfp8(w2.view(-1, F), block=32)
+    return dict(wr=(randn(g, E, K) / math.sqrt(K)).bfloat16(), gamma=(1 + 0.1 * randn(g, K)).bfloat16(), w1=w1, w2=w2,
+                q1=q1.view(E, 2 * F, K), s1=s1.view(E, 2 * F, -1), q2=q2.view(E, K, F), s2=s2.view(E, K, -1))
+
+
+def run_layer(p, x, res, k, mx, stream=None):
+    """The calls as they are used: residual add and norm, router, experts, sum back."""
+    st = dict(stream=stream)
+    s = torch.empty_like(x)
+    codes, scale = rnl.rnl_add_rmsnorm_mxfp8(x, p["gamma"], residual=res, x_sum_out=s, block=32, **st)
+    logits = rnl.rmsnorm_linear_bf16(s, None, p["wr"], out_dtype=rnl.OUT_FP32, **st)
+    r = rnl.rnl_moe_route(logits, k, **st)
+    if mx:
+        h = rnl.rnl_grouped_linear_mxfp8(codes, scale, p["q1"], p["s1"], r.offsets, rows=r.rows, swiglu=True, block=32, **st)
+        hq, hs = rnl.rnl_quant_mxfp8(h, block=32, **st)
+        y = rnl.rnl_grouped_linear_mxfp8(hq, hs, p["q2"], p["s2"], r.offsets, block=32, **st)
+    else:
+        h = rnl.rnl_grouped_linear_bf16(s, p["w1"], r.offsets, rows=r.rows, swiglu=True, **st)
+        y = rnl.rnl_grouped_linear_bf16(h, p["w2"], r.offsets, **st)
+    return rnl.rnl_moe_combine(y, r.slots, r.weights, residual=s, **st), s, logits, r, codes, scale, h
+
+
+@pytest.mark.parametrize("T,E,k,K,F", [(1, 8, 2, 512, 256), (70, 16, 4, 512, 352), (600, 32, 4, 768, 384)])
+@pytest.mark.parametrize("mx", [False, True])
+def test_layer_of_experts(T, E, k, K, F, mx):
+    """A run of the calls together, against 64 bits from the same routing.  The
+    intermediate rows are the calls' own bf16 rows (their error is tested above);
+    the last step is held to the sum of its rows' bounds."""
+    g = gen(T + K)
+    p = layer(g, T, E, k, K, F)
+    x, res = randn(g, T, K).bfloat16(), randn(g, T, K).bfloat16()
+    out, s, logits, r, codes, scale, h = run_layer(p, x, res, k, mx)
+    rnl.rnl_check_device_error()
+    assert torch.equal(s, (x.float() + res.float()).bfloat16())
+    ids, weights, offsets, rows, slots = plain_route(logits, k, True)
+    assert r.ids.tolist() == ids and r.rows.tolist() == rows
+    if mx:
+        a1, b1 = mx_values(codes, scale, 32), mx_values(p["q1"], p["s1"], 32)
+        hq, hs = rnl.rnl_quant_mxfp8(h, block=32)
+        a2, b2 = mx_values(hq, hs, 32), mx_values(p["q2"], p["s2"], 32)
+    else:
+        a1, b1, a2, b2 = s.double(), p["w1"].double(), h.double(), p["w2"].double()
+    ref, bound = plain_grouped(a1, b1, offsets, r.rows, True)
+    assert ((h.double() - ref).abs() <= bound).all()
+    y, yb = plain_grouped(a2, b2, offsets, None, False)
+    w = r.weights.double()[..., None]
+    at = r.slots.long()
+    want = s.double() + (w * y[at]).sum(1)
+    tol = (w * yb[at]).sum(1) + 2.0 ** -8 * want.abs() + (k + 1) * 2.0 ** -24 * (s.double().abs() + (w * y[at].abs()).sum(1))
+    assert ((out.double() - want).abs() <= tol * (1 + 2.0 ** -7)).all()  # (the sum rounds its bounds' rows too)
+
+
+def test_layer_on_given_streams():
+    """Layers in flight at once on streams of their own give the bits of the calls alone."""
+    g = gen(8)
+    jobs = []
+    for T, E, k, K, F in ((200, 16, 4, 512, 256), (3, 16, 4, 512, 256), (1000, 8, 2, 768, 384)):
+        p = layer(g, T, E, k, K, F)
+        for mx in (False, True):
+            jobs.append((p, randn(g, T, K).bfloat16(), randn(g, T, K).bfloat16(), k, mx))
+    want = [run_layer(*j)[0] for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(3):
+        got = [run_layer(*j, stream=s)[0] for j, s in zip(jobs, streams)]
+        torch.full((1 << 20,), 0xA5, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_layer_captured_and_replayed():
+    """A captured layer, replayed with other inputs and other routings in the same
+    buffers, gives the bits of the calls made one by one."""
+    g = gen(9)
+    T, E, k, K, F = 300, 16, 4, 512, 256
+    p = layer(g, T, E, k, K, F)
+    x, res = randn(g, T, K).bfloat16(), randn(g, T, K).bfloat16()
+    for mx in (False, True):
+        run_layer(p, x, res, k, mx)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = run_layer(p, x, res, k, mx)[0]
+        for i in range(6):
+            x.copy_(randn(g, T, K))
+            if i % 2:
+                p["wr"].copy_(randn(g, E, K) * (4 if i == 3 else 0.05))
+            graph.replay()
+            got = out.clone()
+            assert torch.equal(got, run_layer(p, x, res, k, mx)[0]), i
+        graph.replay()
+        graph.replay()
+        assert torch.equal(out, got)
+    rnl.rnl_check_device_error()
+
+
+def test_same_call_same_bits_whatever_the_workspace_holds():
+    g = gen(10)
+    x, W = randn(g, 900, 2048).bfloat16(), randn(g, 8, 640, 2048).bfloat16()
+    off = i32([0, 100, 103, 103, 400, 401, 700, 800, 900])
+    want = rnl.rnl_grouped_linear_bf16(x, W, off)
+    n = rnl.workspace_size(rnl.OP_GROUPED, 900, 2048, 640, 8)
+    for fill in (0, 255, 1):
+        ws = torch.full((n,), fill, dtype=torch.uint8, device="cuda")
+        for _ in range(5):
+            assert torch.equal(rnl.rnl_grouped_linear_bf16(x, W, off, workspace=ws), want)
+    rnl.rnl_check_device_error()
+
+
+def test_strided_and_wrong_device_arguments_are_refused():
+    x, W, off = torch.zeros(8, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, 8, 64, dtype=torch.bfloat16, device="cuda"), i32([0, 4, 8])
+    with pytest.raises(ValueError):
+        rnl.rnl_grouped_linear_bf16(x[:, :64], W, off)
+    with pytest.raises(ValueError):
+        rnl.rnl_grouped_linear_bf16(x[:, :64].contiguous(), W, off.cpu())
+    with pytest.raises(ValueError):
+        rnl.rnl_grouped_linear_bf16(x[:, :64].contiguous(), W, off, workspace=torch.empty(1 << 26, dtype=torch.uint8))
+    with pytest.raises(rnl.RnlError):
+        rnl.rnl_grouped_linear_bf16(x[:, :64].contiguous(), W, off, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+
+
+def test_offsets_past_32_bits():
+    """Weights and outputs of more than 2^32 bytes (and elements, for the codes)."""
+    free = torch.cuda.mem_get_info()[0]
+    if free < 40 << 30:
+        pytest.skip("not enough memory")
+    E, N, K = 9, 8192, 65536   # 4.8e9 codes
+    w = torch.zeros(E, N, K, dtype=torch.uint8, device="cuda")
+    g = gen(11)
+    w[0], w[8] = mx_codes(g, N, K), mx_codes(g, N, K)
+    ws = torch.full((E, N, K // 64), 108, dtype=torch.uint8, device="cuda")
+    x, xs = mx_codes(g, 9, K), torch.full((9, K // 64), 110, dtype=torch.uint8, device="cuda")
+    out = rnl.rnl_grouped_linear_mxfp8(x, xs, w, ws, i32([0, 4] + [4] * 7 + [9]))
+    for rows, e in ((slice(0, 4), 0), (slice(4, 9), 8)):
+        ref, bound = plain_grouped(mx_values(x[rows], xs[rows], 64), mx_values(w[e:e + 1, ::64], ws[e:e + 1, ::64], 64),
+                                   [0, rows.stop - rows.start], None, False)
+        assert ((out[rows, ::64].double() - ref).abs() <= bound).all()
+    del w
+    # 2.2e9 outputs
+    M, N, K = 270000, 8192, 64
+    x, W = randn(g, M, K).bfloat16(), randn(g, 2, N, K).bfloat16()
+    out = rnl.rnl_grouped_linear_bf16(x, W, i32([0, 5, M]))
+    for rows in (slice(0, 5), slice(M - 300, M)):
+        ref, bound = plain_grouped(x[rows], W[:1] if rows.start == 0 else W[1:], [0, rows.stop - rows.start], None, False)
+        assert ((out[rows].double() - ref).abs() <= bound).all()

@@ -117,6 +117,8 @@ CHILD = textwrap.dedent("""
     g("no_K", K=0)
     g("huge_EN", E=1024, N=1 << 22)
     g("huge_K", K=(1 << 24) + 32)
+    g("huge_M", R=(1 << 30) + 1, M=(1 << 30) + 1)
+    g("huge_tiles", R=1 << 29, M=1 << 29, N=1 << 18)
     g("N_48_swiglu", N=48, sw=1)
     g("swiglu", sw=1)
     g("bad_flag", sw=2)
@@ -159,7 +161,7 @@ REFUSALS = {
                     null_y=NULL, null_slots=NULL, null_out=NULL, in_place=DEVICE, overlaps_residual=ARG,
                     overlaps_y=ARG, misaligned_out=ALIGN, misaligned_weights=ALIGN, huge=SHAPE),
     "g": dict(no_device=DEVICE, gathered=DEVICE, no_rows=OK, rows_of_nothing=SHAPE, M_is_not_R=SHAPE, neg_R=SHAPE,
-              no_experts=SHAPE, E_1025=UNSUPPORTED, no_N=SHAPE, no_K=SHAPE, huge_EN=SHAPE, huge_K=SHAPE,
+              no_experts=SHAPE, E_1025=UNSUPPORTED, no_N=SHAPE, no_K=SHAPE, huge_EN=SHAPE, huge_K=SHAPE, huge_M=SHAPE, huge_tiles=SHAPE,
               N_48_swiglu=UNSUPPORTED, swiglu=DEVICE, bad_flag=ARG, null_x=NULL, null_W=NULL, null_offsets=NULL,
               null_out=NULL, null_workspace=WORKSPACE, small_workspace=WORKSPACE, misaligned_x=ALIGN,
               misaligned_W=ALIGN, misaligned_out=ALIGN, misaligned_offsets=ALIGN, misaligned_rows=ALIGN,
@@ -246,6 +248,7 @@ def seen(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "current")
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
     monkeypatch.setattr(nat, "load", lambda path=None: FakeLib())
+    monkeypatch.setattr(ex, "_workspace_size", nat.workspace_size)  # not remembered
     monkeypatch.setattr(nat, "_stream", lambda dev, stream: launched.append(stream))
 
     def call(f, stream):
@@ -280,6 +283,7 @@ def test_every_wrapper_is_covered_and_public():
 
 def test_outputs_of_small_calls(monkeypatch):
     monkeypatch.setattr(nat, "load", lambda path=None: FakeLib())
+    monkeypatch.setattr(ex, "_workspace_size", nat.workspace_size)
     monkeypatch.setattr(nat, "_stream", lambda dev, stream: None)
     r = ex.rnl_moe_route(z(5, 7, dtype=F32), 3)
     for i, t in enumerate(r):
