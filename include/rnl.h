@@ -600,8 +600,8 @@ rnl_status rnl_grouped_linear_bf16(const void *x, int64_t n_x_rows, const void *
  * out[i, n] = sum_k value(x code) 2^(x byte - 127) value(w code) 2^(w byte - 127),
  * accumulated in FP32 on the block-scaled tensor cores.  A scale byte of 255 or a
  * NaN code makes the outputs that read it NaN.  Everything else as
- * rnl_grouped_linear_bf16; the scales need no alignment (rows whose K / block is a
- * multiple of 16 at block 32, of 8 at block 64, are loaded in the fewest pieces).
+ * rnl_grouped_linear_bf16; the scales need no alignment (but rows with K / block a
+ * multiple of 4 are loaded in far fewer pieces).
  */
 rnl_status rnl_grouped_linear_mxfp8(const uint8_t *x_codes, const uint8_t *x_scale, int64_t n_x_rows,
                                     const uint8_t *w_codes, const uint8_t *w_scale, int64_t n_experts,

@@ -84,7 +84,7 @@ struct Args {
   const uint8_t* x_scale;
   const uint8_t* w_scale;
   int nb;               // scale bytes a row
-  int sf_vec;           // bytes a load of scales: what the rows' alignment allows (16 / 8 at most, 4 / 2 or 1)
+  int sf_vec;           // bytes a load of scales: what the rows' alignment allows (a batch's 16 or 8, 4 or 1)
   const int32_t* offsets;
   const int32_t* rows;  // may be null
   int R;                // rows of x
@@ -98,60 +98,52 @@ struct Args {
   uint64_t epoch;
 };
 
-// The scale bytes of four k-blocks from kb on of one row, as they are loaded:
-// nothing is done with them before put_scales, so that a load's latency is not
-// waited for.  form: 2 one load, 1 one a k-block (both by the rows' alignment), 0
-// byte by byte, put together at once.
+// The scale bytes of four k-blocks from kb on of one row (127 behind its last),
+// Sf::kRowWords words.  vec: bytes a load, what the rows' alignment allows: the whole
+// batch (where the row has it), words, or single bytes put together.
 template <int BLK>
-__device__ __forceinline__ int scale_form(int kb, int nb, int vec) {
-  constexpr int kPer = 128 / BLK;  // bytes a k-block: 4 or 2
-  const bool whole = (kb + kSfBatch) * kPer <= nb;
-  return whole && vec == 4 * kPer ? 2 : (whole && vec >= kPer ? 1 : 0);
-}
+struct Sf {
+  static constexpr int kRowBytes = kSfBatch * 128 / BLK;  // of a row and batch: 16 or 8
+  static constexpr int kRowWords = kRowBytes / 4;
+};
 
 template <int BLK>
-__device__ __forceinline__ void load_scales(const uint8_t* p, int kb, int nb, int form, uint32_t (&w)[kSfBatch]) {
-  constexpr int kPer = 128 / BLK;
-  const uint8_t* q = p + kb * kPer;
-  if (form == 2) {
-    if constexpr (BLK == 32) {
+__device__ __forceinline__ void load_scales(const uint8_t* p, int kb, int nb, int vec,
+                                            uint32_t (&w)[Sf<BLK>::kRowWords]) {
+  constexpr int kBytes = Sf<BLK>::kRowBytes, kWords = Sf<BLK>::kRowWords;
+  const int b0 = kb / kSfBatch * kBytes;
+  const uint8_t* q = p + b0;
+  if (vec == kBytes && b0 + kBytes <= nb) {
+    if constexpr (kWords == 4) {
       const uint4 u = __ldg(reinterpret_cast<const uint4*>(q));
       w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
     } else {
       const uint2 u = __ldg(reinterpret_cast<const uint2*>(q));
       w[0] = u.x, w[1] = u.y;
     }
-  } else if (form == 1) {
+  } else if (vec >= 4) {
 #pragma unroll
-    for (int k = 0; k < kSfBatch; ++k) {
-      if constexpr (BLK == 32)
-        w[k] = __ldg(reinterpret_cast<const uint32_t*>(q) + k);
-      else
-        w[k] = __ldg(reinterpret_cast<const uint16_t*>(q) + k);
-    }
+    for (int i = 0; i < kWords; ++i)
+      w[i] = b0 + 4 * i < nb ? __ldg(reinterpret_cast<const uint32_t*>(q) + i) : 0x7F7F7F7Fu;
   } else {
 #pragma unroll
-    for (int k = 0; k < kSfBatch; ++k) {
+    for (int i = 0; i < kWords; ++i) {
       uint32_t v = 0;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int at = (kb + k) * kPer + j;
-        v |= static_cast<uint32_t>(at < nb ? __ldg(p + at) : 127) << (8 * j);
-      }
-      w[k] = v;
+      for (int j = 0; j < 4; ++j)
+        v |= static_cast<uint32_t>(b0 + 4 * i + j < nb ? __ldg(q + 4 * i + j) : 127) << (8 * j);
+      w[i] = v;
     }
   }
 }
 
-// What load_scales has loaded of a row, its bytes one after the other.
+// What load_scales has loaded of a row, into shared memory.
 template <int BLK>
-__device__ __forceinline__ void put_scales(uint8_t* dst, const uint32_t (&w)[kSfBatch], int form) {
+__device__ __forceinline__ void put_scales(uint8_t* dst, const uint32_t (&w)[Sf<BLK>::kRowWords]) {
   if constexpr (BLK == 32)
     *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
   else
-    *reinterpret_cast<uint2*>(dst) =
-        form == 2 ? make_uint2(w[0], w[1])
-                  : make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
+    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
 }
 
 // The scale words of two k-blocks of a row (its bytes in shared memory at p): a byte
@@ -336,26 +328,25 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
       };
       // a batch: its scales, its first k-block and the range of them that is multiplied
       struct Batch {
-        uint32_t v[3][kSfBatch];
-        int form, kb, lo, hi;  // hi 0: none
+        uint32_t v[3][Sf<BLK>::kRowWords];
+        int kb, lo, hi;  // hi 0: none
       };
       auto load = [&](Batch& b) {
         b.hi = 0;
         if (it >= walk.n) return;
-        b.form = scale_form<BLK>(kb, a.nb, a.sf_vec);
 #pragma unroll
-        for (int h = 0; h < 3; ++h) load_scales<BLK>(p[h], kb, a.nb, b.form, b.v[h]);
+        for (int h = 0; h < 3; ++h) load_scales<BLK>(p[h], kb, a.nb, a.sf_vec, b.v[h]);
         b.kb = kb;
         b.lo = w.kb0;
         b.hi = w.kb1;
         kb += kSfBatch;
         if (kb >= w.kb1 && ++it < walk.n) enter();
       };
-      constexpr int kRowScale = BLK == 32 ? 16 : 8;  // bytes of a row and batch
+      constexpr int kRowScale = Sf<BLK>::kRowBytes;
       auto write = [&](Batch& b, uint8_t* sf) {
-        put_scales<BLK>(sf + me * kRowScale, b.v[0], b.form);
-        put_scales<BLK>(sf + (128 + me) * kRowScale, b.v[1], b.form);
-        if (me < 96) put_scales<BLK>(sf + (256 + me) * kRowScale, b.v[2], b.form);
+        put_scales<BLK>(sf + me * kRowScale, b.v[0]);
+        put_scales<BLK>(sf + (128 + me) * kRowScale, b.v[1]);
+        if (me < 96) put_scales<BLK>(sf + (256 + me) * kRowScale, b.v[2]);
         asm volatile("bar.sync 1, 128;" ::: "memory");
         const int first = b.kb, lo = b.lo, hi = b.hi;
         load(b);
@@ -662,10 +653,9 @@ rnl_status launch(const GroupedArgs& g, const DeviceInfo& dev, cudaStream_t s) {
   a.nb = MX ? static_cast<int>(g.K / g.block) : 0;
   a.sf_vec = 1;
   if constexpr (MX) {
-    constexpr int kPer = 128 / BLK;
     const uintptr_t bits = reinterpret_cast<uintptr_t>(g.x_scale) | reinterpret_cast<uintptr_t>(g.w_scale) |
                            static_cast<uintptr_t>(a.nb);
-    a.sf_vec = bits % (4 * kPer) == 0 ? 4 * kPer : (bits % kPer == 0 ? kPer : 1);
+    a.sf_vec = bits % Sf<BLK>::kRowBytes == 0 ? Sf<BLK>::kRowBytes : (bits % 4 == 0 ? 4 : 1);
   }
   a.offsets = g.offsets;
   a.rows = g.rows;
