@@ -5,7 +5,7 @@
 // Weight rows stand on the tensor core's M side (128 TMEM lanes a CTA), the
 // group's rows on its N side, because N may be any multiple of 16 (of 32 on a CTA
 // pair): a group of 5 rows costs a 16-wide product instead of a 128-row one, and a large group is
-// cut into equal tiles of at most kTile rows.  How many rows an expert has is
+// cut into near-equal tiles of at most kTile rows.  How many rows an expert has is
 // known on the device only: every CTA reads the offsets and builds the table
 // of the groups' first tiles itself.
 #pragma once
@@ -93,15 +93,19 @@ __device__ __forceinline__ Tile tile_at(const Groups& g, int t) {
   r.e = lo;
   const int loc = t - g.pre[lo];
   const int cnt = g.off[lo + 1] - g.off[lo];
+  // the group's steps are dealt out to its tiles as evenly as whole steps allow:
+  // 900 rows in steps of 32 are 256 + 3 x 224, not 4 x 256
   const int nt = token_tiles(cnt, kTile);
-  const int ns = ((cnt + nt - 1) / nt + kStep - 1) / kStep * kStep;  // (nt - 1) ns < cnt, as ns <= kTile
+  const int steps = (cnt + kStep - 1) / kStep;
+  const int each = steps / nt, more = steps - each * nt;
   const int super = loc / (kSuper * g.num_f);
   const int gm = min(nt - super * kSuper, kSuper);
   const int in = loc - super * kSuper * g.num_f;
   const int tt = super * kSuper + in % gm;
   r.f = in / gm;
-  r.row0 = g.off[lo] + tt * ns;
-  r.valid = min(ns, cnt - tt * ns);
+  const int first = (tt * each + min(tt, more)) * kStep;
+  r.row0 = g.off[lo] + first;
+  r.valid = min((each + (tt < more ? 1 : 0)) * kStep, cnt - first);
   r.n = (r.valid + kStep - 1) / kStep * kStep;
   return r;
 }
