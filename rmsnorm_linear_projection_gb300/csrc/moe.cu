@@ -2,7 +2,10 @@
 // the router's logits, softmax weights, the rows grouped by expert) and the
 // weighted sum of a token's expert rows back.
 //
-// Routing.  One warp a token: a lane holds every 32nd logit as an
+// Routing (bound by latency: a few MB are read).  32 warps a CTA and 64 tokens, so
+// that a warp has two tokens to choose for; with 8 warps of 8 tokens each, and
+// the counts added up by as few threads, the two launches took 19.3 and 14.9 us
+// for 8192 tokens over 128 experts, now 9.6 each (17.8 us a call in a graph).  One warp a token: a lane holds every 32nd logit as an
 // order-preserving integer, and k rounds of two warp reductions take the
 // largest key and, among equals, the lowest expert.  The rows are grouped by a
 // stable counting sort, (token, place) order within an expert: each CTA counts
@@ -23,7 +26,7 @@ namespace {
 __device__ unsigned int g_err_moe;
 std::atomic<bool> g_launched{false};
 
-constexpr int kThreadsR = 256;
+constexpr int kThreadsR = 1024;
 constexpr int kWarpsR = kThreadsR / 32;
 constexpr int kMinTokens = 64;  // tokens a CTA; more when there would be over kMaxBlocks CTAs
 constexpr int kMaxBlocks = 256;
@@ -55,24 +58,24 @@ struct RouteArgs {
 // exp(v - m) with infinities of the same sign at distance 0
 __device__ __forceinline__ float soft(float v, float m) { return v == m ? 1.0f : expf(v - m); }
 
-// One token's choices; lane j < k gets the j-th one's key and expert (key 0:
-// none).  VPL: logits a lane.
 template <int VPL>
-__device__ __forceinline__ void choose(const RouteArgs& p, int64_t t, int lane, uint32_t& my_key, int& my_id,
-                                       float& my_w) {
-  uint32_t key[VPL];
+__device__ __forceinline__ void load_keys(const RouteArgs& p, int64_t t, int lane, uint32_t (&key)[VPL]) {
   const float* l = p.logits + t * p.E;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = lane + 32 * i;
     key[i] = e < p.E ? key_of(l[e]) : 0u;
   }
-  uint32_t all[VPL];
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) all[i] = key[i];
+}
+
+// One token's choices from its keys (which are used up); lane j < k gets the j-th
+// one's key, expert and weight (key 0: none).  VPL: logits a lane.
+template <int VPL>
+__device__ __forceinline__ void choose(const RouteArgs& p, int lane, uint32_t (&key)[VPL], uint32_t& my_key,
+                                       int& my_id, float& my_w) {
   my_key = 0u;
   my_id = -1;
-  uint32_t top = 0u;
+  float mx = 0.f, sum = 0.f;
   for (int j = 0; j < p.k; ++j) {
     uint32_t best = 0u;
     int at = 0;
@@ -85,27 +88,29 @@ __device__ __forceinline__ void choose(const RouteArgs& p, int64_t t, int lane, 
     const uint32_t m = __reduce_max_sync(0xffffffffu, best);
     if (m == 0u) break;  // the same on every lane
     const uint32_t e = __reduce_min_sync(0xffffffffu, best == m ? static_cast<uint32_t>(lane + 32 * at) : 0xffffffffu);
-    if (j == 0) top = m;
+    if (j == 0) {
+      mx = logit_of(m);
+      if (!p.renorm) {  // the softmax' sum over all experts
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+          if (key[i] != 0u) sum += soft(logit_of(key[i]), mx);
+      }
+    }
     if (lane == j) {
       my_key = m;
       my_id = static_cast<int>(e);
     }
-    if ((e & 31u) == static_cast<uint32_t>(lane)) {
+    // (a select for each, not a store to key[e / 32]: the keys stay in registers)
+    const uint32_t gone = (e & 31u) == static_cast<uint32_t>(lane) ? e >> 5 : 0xffffffffu;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (i == static_cast<int>(e >> 5)) key[i] = 0u;
+    for (int i = 0; i < VPL; ++i) {
+      uint32_t k = key[i];
+      asm("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %1, %2;\n\tselp.u32 %0, 0, %0, p;\n\t}" : "+r"(k) : "r"(gone), "r"(i));
+      key[i] = k;
     }
   }
-  const float mx = logit_of(top);
   const float mine = my_key != 0u ? soft(logit_of(my_key), mx) : 0.f;
-  float sum = 0.f;
-  if (p.renorm) {
-    sum = mine;
-  } else {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (all[i] != 0u) sum += soft(logit_of(all[i]), mx);
-  }
+  if (p.renorm) sum = mine;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   my_w = my_key != 0u ? mine / sum : 0.f;
@@ -117,19 +122,35 @@ __device__ void choose_all(const RouteArgs& p, int64_t t0, int64_t t1, int* cnt)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int e = threadIdx.x; e < p.E; e += kThreadsR) cnt[e] = 0;
   __syncthreads();
-  for (int64_t t = t0 + warp; t < t1; t += kWarpsR) {
-    uint32_t key;
+  constexpr bool kAhead = VPL <= 8;  // the next token's logits while this one's are looked through
+  uint32_t key[VPL], next[kAhead ? VPL : 1];
+  int64_t t = t0 + warp;
+  if (kAhead && t < t1) load_keys<VPL>(p, t, lane, key);
+  for (; t < t1; t += kWarpsR) {
+    if constexpr (kAhead) {
+      if (t + kWarpsR < t1) load_keys<VPL>(p, t + kWarpsR, lane, next);
+    } else {
+      load_keys<VPL>(p, t, lane, key);
+    }
+    uint32_t my_key;
     int id;
     float w;
-    choose<VPL>(p, t, lane, key, id, w);
+    choose<VPL>(p, lane, key, my_key, id, w);
     if (lane < p.k) {
       p.ids[t * p.k + lane] = id;
       p.weights[t * p.k + lane] = w;
       if (id >= 0) atomicAdd(cnt + id, 1);
     }
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = next[i];
+    }
   }
   __syncthreads();
 }
+
+// Warps that rank a CTA's choices: their counts, E values each, stay in 48 KB.
+__host__ __device__ inline int rank_warps(int E) { return E <= 256 ? kWarpsR : 8; }
 
 // before[e]: rows of expert e of the CTAs before this one; then the first row of
 // expert e of this CTA.  Shared: before [E], total [E], wcnt [warps][E].
@@ -166,15 +187,16 @@ __device__ void place_all(const RouteArgs& p, int64_t t0, int64_t t1, int* befor
   for (int64_t i = carry + static_cast<int64_t>(blockIdx.x) * kThreadsR + threadIdx.x; i < p.T * p.k;
        i += static_cast<int64_t>(gridDim.x) * kThreadsR)
     p.rows[i] = -1;
-  // each warp takes an equal run of the CTA's choices
-  const int64_t n = (t1 - t0) * p.k;
-  const int64_t run = ((n + kWarpsR - 1) / kWarpsR + 31) / 32 * 32;
+  // each ranking warp takes an equal run of the CTA's choices
+  const int rw = rank_warps(p.E);
+  const int64_t n = warp < rw ? (t1 - t0) * p.k : 0;
+  const int64_t run = ((n + rw - 1) / rw + 31) / 32 * 32;
   const int64_t i0 = t0 * p.k + warp * run;
   const int64_t end = t1 * p.k;
-  const int64_t i1 = i0 + run < end ? i0 + run : end;
-  for (int i = threadIdx.x; i < kWarpsR * p.E; i += kThreadsR) wcnt[i] = 0;
+  const int64_t i1 = i0 + run < end ? i0 + run : end;  // (run 0 for the other warps: nothing)
+  for (int i = threadIdx.x; i < rw * p.E; i += kThreadsR) wcnt[i] = 0;
   __syncthreads();
-  int* mine = wcnt + warp * p.E;
+  int* mine = wcnt + (warp < rw ? warp : 0) * p.E;
   for (int64_t i = i0 + lane; i < i1; i += 32) {
     const int id = p.ids[i];
     if (id >= 0) atomicAdd(mine + id, 1);
@@ -182,7 +204,7 @@ __device__ void place_all(const RouteArgs& p, int64_t t0, int64_t t1, int* befor
   __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += kThreadsR) {
     int at = before[e];
-    for (int w = 0; w < kWarpsR; ++w) {
+    for (int w = 0; w < rw; ++w) {
       const int c = wcnt[w * p.E + e];
       wcnt[w * p.E + e] = at;
       at += c;
@@ -245,6 +267,7 @@ __global__ void __launch_bounds__(kThreadsR) route_place_kernel(RouteArgs p) {
   if (part < parts)
     for (int e = threadIdx.x % lanes; e < p.E; e += lanes) {
       int all = 0, bef = 0;
+#pragma unroll 8
       for (int b = part; b < B; b += parts) {
         const int c = p.hist[static_cast<int64_t>(b) * p.E + e];
         all += c;
@@ -355,7 +378,7 @@ rnl_status launch_moe_route(const float* logits, int64_t T, int64_t E, int64_t k
   p.hist = static_cast<int32_t*>(ws);
   const int blocks = route_blocks(T > 0 ? T : 1, &p.per);
   g_launched.store(true, std::memory_order_relaxed);
-  const size_t smem = static_cast<size_t>(E) * 4 * (2 + kWarpsR);  // at most 40 KB
+  const size_t smem = static_cast<size_t>(E) * 4 * (2 + rank_warps(static_cast<int>(E)));  // at most 40 KB
   trace_before(s);
   cudaError_t e;
   if (E <= 32)

@@ -236,6 +236,17 @@ def test_grouped_swiglu(counts, K, N, gather):
     check_grouped(counts, K, N, True, gather, tail=3)
 
 
+def test_grouped_many_experts():
+    """As many experts as the library takes, most without a row."""
+    counts = [0] * 1024
+    for e, c in ((0, 3), (1, 40), (500, 300), (501, 1), (1022, 7), (1023, 260)):
+        counts[e] = c
+    check_grouped(counts, 136, 96, False, True)
+    check_grouped([1] * 1024, 64, 64, True, False)
+    check_mx(counts, 192, 96, 32, False, True)
+    check_mx([2] * 1024, 64, 64, 64, True, False)
+
+
 # ------------------------------------------------- products by expert, MXFP8
 def mx_values(codes, scales, block):
     v = codes.view(torch.float8_e4m3fn).double()
