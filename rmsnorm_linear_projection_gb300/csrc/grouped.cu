@@ -11,8 +11,7 @@
 // so that no sorted copy of x is written.  Measured against it: TMA gathers of
 // four rows take 54 cycles each, and a stage that the tensor cores read in 512
 // cycles needs 32 of them (32768 x 2048 -> 2816 over 32 experts: 541 against 277
-// us); rows that stand in order anyway by TMA boxes, 4096 x 4096 -> 4864: 115
-// against 103 us.  For swiglu the weight box interleaves 16 gate rows with the 16 up rows of the
+// us).  For swiglu the weight box interleaves 16 gate rows with the 16 up rows of the
 // same features, which puts both sums of a feature into one warp's lanes.
 //
 // Roles per CTA (480 threads): warp 0 weight boxes (TMA), warp 1 MMA issue (even CTA),
@@ -62,6 +61,11 @@ struct Form {
   static constexpr int kSfSlots = 2;
   static_assert(kStageBytes % 1024 == 0, "swizzle atoms");
   static_assert(!MX || kSfBase + kSfSlots * 32 <= 512, "TMEM columns");
+};
+
+// x as boxes of 128, 64, 32 and 16 rows (rows that stand in order)
+struct XMaps {
+  CUtensorMap m[4];
 };
 
 struct __align__(16) Ctrl {
@@ -164,7 +168,7 @@ __device__ __forceinline__ void take_scales(const uint8_t* p, uint32_t& even, ui
 // BLK: 0 for bf16, 32 or 64 for MXFP8 operands with that many elements a scale.
 template <bool SWIGLU, int BLK>
 __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
-    grouped_kernel(const __grid_constant__ CUtensorMap map_w, const Args a) {
+    grouped_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ XMaps maps_x, const Args a) {
   constexpr bool MX = BLK != 0;
   using F = Form<MX>;
   constexpr int kTile = F::kTile;
@@ -188,9 +192,13 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
   const int num_pairs = gridDim.x >> 1;
   const int N_out = SWIGLU ? a.N / 2 : a.N;
   const int num_f = (N_out + 2 * kFeatCta - 1) / (2 * kFeatCta);
+  // MXFP8 rows that stand in order come as TMA boxes (24008 x 768 -> 4096 130 against
+  // 146 us: their copies by 16 bytes fill the load pipe), all others by the gathering
+  // warps (bf16 28004 x 1408 -> 2048 in order: 128 against 140 us by boxes)
+  const bool gather = !MX || a.rows != nullptr;
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(smem_u32(&ctrl->full[s]), 3);  // the weight's bytes, and each CTA's rows
+      mbar_init(smem_u32(&ctrl->full[s]), gather ? 3 : 1);  // the boxes' bytes, and each CTA's gathered rows
       mbar_init(smem_u32(&ctrl->landed[s]), kGatherWarps * 32);
       mbar_init(smem_u32(&ctrl->empty[s]), 1);
     }
@@ -224,13 +232,20 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------- weight producer
-    if (lane == 0) tma_prefetch_map(&map_w);
+    // and, where they come so, the group's rows: as boxes of 128 to 16 rows
+    if (lane == 0) {
+      tma_prefetch_map(&map_w);
+      if (!gather) tma_prefetch_map(&maps_x.m[0]);
+    }
     uint32_t stage = 0, phase = 0;
     bool ok = true;
     for (int it = 0; it < walk.n && ok; ++it) {
       const Item w = walk.at(it);
       if (lane == 0) {
         const int f0 = (w.t.f * 2 + static_cast<int>(rank)) * kFeatCta;
+        const int half = w.t.n / 2;
+        const int x_row = w.t.row0 + static_cast<int>(rank) * half;
+        const uint32_t bytes = 2 * kABytes + (gather ? 0u : static_cast<uint32_t>(w.t.n) * kRowBytes);  // of both CTAs
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (!mbar_wait(smem_u32(&ctrl->empty[stage]), phase ^ 1u, abort, &g_err_grouped, 205) ||
               !RNL_DCHECK(&g_err_grouped, stage < static_cast<uint32_t>(a.stages), 206)) {
@@ -240,11 +255,20 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
           const uint32_t sa = base + stage * kStageBytes;
           const uint32_t full_local = smem_u32(&ctrl->full[stage]);
           const uint32_t full_even = mapa_shared(full_local, 0);
-          if (rank == 0) mbar_arrive_expect_tx(full_local, 2 * kABytes);  // both CTAs' boxes
+          if (rank == 0) mbar_arrive_expect_tx(full_local, bytes);
           if constexpr (SWIGLU)
             tma_load_5d_pair(sa, &map_w, full_even, kb * kBKElems, 0, 0, f0 / 16, w.t.e);
           else
             tma_load_2d_pair(sa, &map_w, full_even, kb * kBKElems, w.t.e * a.N + f0);
+          if (!gather) {
+            int at = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+              if (half & (128 >> b)) {
+                tma_load_2d_pair(sa + kABytes + at * kRowBytes, &maps_x.m[b], full_even, kb * kBKElems, x_row + at);
+                at += 128 >> b;
+              }
+          }
           if (++stage == static_cast<uint32_t>(a.stages)) {
             stage = 0;
             phase ^= 1u;
@@ -258,7 +282,7 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
     // hands a stage's rows to the tensor cores.  Not by the warps that copy:
     // their fence would wait for every copy that they have in flight
     uint32_t stage = 0, phase = 0;
-    bool ok = true;
+    bool ok = gather;
     for (int it = 0; it < walk.n && ok; ++it) {
       const Item w = walk.at(it);
       if (lane == 0) {
@@ -409,7 +433,7 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
     const int gw = warp - (2 + kEpiWarps);
     const int sub = lane >> 3, chunk = lane & 7;
     uint32_t stage = 0, phase = 0;
-    bool ok = true;
+    bool ok = gather;
     Item w, next;
     int row[8];  // of the next item
     auto look_up = [&](const Item& i) {
@@ -420,7 +444,7 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
         if (a.rows != nullptr) row[j] = a.rows[row[j]];
       }
     };
-    if (walk.n > 0) {
+    if (ok && walk.n > 0) {
       next = walk.at(0);
       look_up(next);
     }
@@ -645,6 +669,11 @@ rnl_status launch(const GroupedArgs& g, const DeviceInfo& dev, cudaStream_t s) {
     st = make_map_2d(&mw, dt, g.w, K, g.E * N, row, kBox, 128);
   }
   if (st != RNL_OK) return st;
+  XMaps mx;
+  for (int b = 0; b < 4; ++b) {
+    st = make_map_2d(&mx.m[b], dt, g.x, K, g.R, row, kBox, 128 >> b);
+    if (st != RNL_OK) return st;
+  }
   Args a;
   a.x = static_cast<const uint8_t*>(g.x);
   a.row_bytes = static_cast<int64_t>(row);
@@ -684,7 +713,7 @@ rnl_status launch(const GroupedArgs& g, const DeviceInfo& dev, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   trace_before(s);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mw, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mw, mx, a);
   trace_after(s, MX ? (SWIGLU ? "grouped_mxfp8_swiglu" : "grouped_mxfp8")
                     : (SWIGLU ? "grouped_bf16_swiglu" : "grouped_bf16"));
   if (e != cudaSuccess) {
