@@ -552,12 +552,12 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
       const Tile& t = w.t;
       const uint32_t buf = it & 1;
       bool got = mbar_wait(smem_u32(&ctrl->tmem_full[buf]), (it >> 1) & 1, abort, &g_err_grouped, 209);
-      if (w.kind == kFinish && got && lane == 0)
-        for (int q = w.first; q < pair && got; ++q)
+      if (w.kind == kFinish)  // a flag a lane
+        for (int q = w.first + lane; q < pair && got; q += 32)
           got = flag_wait(a.flags + (static_cast<int64_t>(q) * 2 + rank) * kEpiWarps + ew, a.epoch, abort,
                           &g_err_grouped, 210);
       if (!__all_sync(0xffffffffu, got)) break;
-      __syncwarp();  // what lane 0 acquired is every lane's
+      __syncwarp();  // what a lane acquired is every lane's
       tc_fence_after();
       const int f0 = (t.f * 2 + static_cast<int>(rank)) * kFeatCta;
       const int feat = SWIGLU ? f0 + quarter * 16 + (lane & 15) : f0 + quarter * 32 + lane;
@@ -572,13 +572,23 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
           for (int j = 0; j < 32; ++j) dst[j * 128] = __uint_as_float(r[j]);
           continue;
         }
-        for (int q = w.first; q < pair; ++q) {  // the lower workers' parts, in their order
-          const float* src = a.partial + q * kSlotWords + lane_off + static_cast<int64_t>(c) * 128;
-          float v[32];
+        if (w.first < pair) {  // the lower workers' parts, in their order; half a part's loads ahead
+          const float* src = a.partial + w.first * kSlotWords + lane_off + static_cast<int64_t>(c) * 128;
+          float lo[16], hi[16];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __ldcg(src + j * 128);
+          for (int j = 0; j < 16; ++j) lo[j] = __ldcg(src + j * 128);
+          for (int q = w.first; q < pair; ++q, src += kSlotWords) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + v[j]);
+            for (int j = 0; j < 16; ++j) hi[j] = __ldcg(src + (16 + j) * 128);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + lo[j]);
+            if (q + 1 < pair) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) lo[j] = __ldcg(src + kSlotWords + j * 128);
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) r[16 + j] = __float_as_uint(__uint_as_float(r[16 + j]) + hi[j]);
+          }
         }
         if constexpr (SWIGLU)
           store_cols_swiglu(a.out, N_out, t.row0, t.valid, c, feat, lane, r);
@@ -592,10 +602,10 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
           mbar_arrive(smem_u32(&ctrl->tmem_empty[buf]));
         else
           mbar_arrive_remote(empty_even[buf]);  // (what it orders are reads of TMEM)
-        // a flag is consumed by one warp, which sets it back, so that a replayed
-        // graph waits for its own
-        for (int q = w.first; q < pair; ++q) a.flags[(static_cast<int64_t>(q) * 2 + rank) * kEpiWarps + ew] = 0;
       }
+      // a flag is consumed by one warp, which sets it back, so that a replayed
+      // graph waits for its own
+      for (int q = w.first + lane; q < pair; q += 32) a.flags[(static_cast<int64_t>(q) * 2 + rank) * kEpiWarps + ew] = 0;
       if (w.kind == kPartial) {
         __threadfence();
         __syncwarp();
