@@ -78,6 +78,7 @@ struct __align__(16) Ctrl {
   uint64_t sf_empty[2];        // each CTA: the slot's k-blocks have been multiplied
   uint32_t tmem_base;
   int abort;
+  Plan plan;
 };
 
 __host__ __device__ constexpr size_t table_bytes(int E) { return (static_cast<size_t>(E) + 1) * 8; }
@@ -220,15 +221,15 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
   grid_launch_dependents();
   grid_dependency_wait();
   build_groups(a.offsets, a.E, a.M, num_f, kTile, off, pre, &g_err_grouped, 213);
+  const Groups groups{off, pre, a.E, num_f};
+  if (warp == 0) make_plan<kTile, kStep>(ctrl->plan, groups, num_pairs, a.num_kb, pair, lane);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = ctrl->tmem_base;
   volatile int* abort = &ctrl->abort;
-  const Groups groups{off, pre, a.E, num_f};
-  const Sched sc(pre[a.E], num_pairs, a.num_kb);
-  Walk<kTile, kStep> walk(sc, groups, pair, lane);
+  Walk<kTile, kStep> walk(ctrl->plan, groups, lane);
 
   if (warp == 0) {
     // ------------------------------------------------------- weight producer

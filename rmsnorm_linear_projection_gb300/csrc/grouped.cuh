@@ -44,7 +44,8 @@ struct Tile {
 __device__ __forceinline__ int token_tiles(int cnt, int tile) { return (cnt + tile - 1) / tile; }
 
 // Fills off and pre (shared memory, E + 1 values each) from the offsets; called
-// by every thread of the block, which must synchronise afterwards.  Offsets
+// by every thread of the block, which must synchronise afterwards (warp 0, which
+// writes pre, need not).  Offsets
 // that decrease or leave [0, M] are reported, and no tile is made.
 __device__ __forceinline__ void build_groups(const int32_t* __restrict__ offsets, int E, int M, int num_f,
                                              int tile, int* off, int* pre, unsigned int* err, uint32_t site) {
@@ -75,6 +76,7 @@ __device__ __forceinline__ void build_groups(const int32_t* __restrict__ offsets
     } else if (lane == 0) {
       pre[E] = static_cast<int>(base);
     }
+    __syncwarp();
   }
 }
 
@@ -125,7 +127,7 @@ struct Sched {
   int sk_units;  // workers that get a range: share k-blocks, the first `more` of them one more
   int share, more;
   int num_kb;
-  __device__ __forceinline__ Sched(int tiles, int workers, int kbs) {
+  __device__ __forceinline__ void set(int tiles, int workers, int kbs) {
     units = workers;
     num_kb = kbs;
     dp = tiles >= 2 * workers ? (tiles / workers - 1) * workers : 0;
@@ -149,22 +151,24 @@ struct Item {
   int first;  // kFinish: the lowest worker that holds a part of the tile (else the worker itself)
 };
 
-// The items of one worker, in order.  A warp works out 32 items at once, one a
-// lane, and hands them round: one by one they cost each role about 0.8 us a tile.
-template <int kTile, int kStep>
-struct Walk {
-  const Sched& s;
-  const Groups& g;
+// The items of one worker, in order: what they are made from (in shared memory,
+// filled by one thread), and the first kTable of them.
+constexpr int kTable = 16;  // (with 32 the table costs a stage of the pipeline from 86 experts on, with 16 from 150)
+struct Plan {
+  Sched s;
   int n;
-  int unit, n_sk, n_dp, tile_lo, u0, u1, lane;
-  bool fin_last;
-  Item mine;
-  __device__ __forceinline__ Walk(const Sched& sc, const Groups& gr, int u, int ln) : s(sc), g(gr), unit(u), lane(ln) {
+  int unit, n_sk, n_dp, tile_lo, u0, u1;
+  int fin_last;
+  int4 table[kTable][2];
+
+  __device__ __forceinline__ void set(int tiles, int workers, int kbs, int u) {
+    s.set(tiles, workers, kbs);
+    unit = u;
     n_dp = u < s.dp ? (s.dp - u + s.units - 1) / s.units : 0;
     n_sk = 0;
     u0 = u1 = 0;
     tile_lo = 0;
-    fin_last = false;
+    fin_last = 0;
     if (u < s.sk_units && s.sk > 0) {
       u0 = s.start(u);
       u1 = s.start(u + 1);
@@ -176,49 +180,83 @@ struct Walk {
     }
     n = n_sk + n_dp;
   }
-  __device__ __forceinline__ Item make(int it) const {
-    Item w;
-    w.first = unit;
-    int j;  // index among the range's tiles, highest first
-    const int early = fin_last ? n_sk - 1 : n_sk;
-    if (it < early) {
-      j = it;
-    } else if (it < early + n_dp) {
-      w.t = tile_at<kTile, kStep>(g, unit + (it - early) * s.units);
-      w.kb0 = 0;
-      w.kb1 = s.num_kb;
-      w.kind = kWhole;
-      return w;
-    } else {
-      j = n_sk - 1;
-    }
-    const int t = tile_lo + (n_sk - 1 - j);
-    const int ts = t * s.num_kb;
-    w.t = tile_at<kTile, kStep>(g, s.dp + t);
-    w.kb0 = max(u0 - ts, 0);
-    w.kb1 = min(u1 - ts, s.num_kb);
-    w.kind = w.kb1 < s.num_kb ? kPartial : (w.kb0 > 0 ? kFinish : kWhole);
-    if (w.kind == kFinish) {
-      int q = unit - 1;
-      while (s.start(q) > ts) --q;
-      w.first = q;
-    }
+};
+
+template <int kTile, int kStep>
+__device__ __forceinline__ Item make_item(const Plan& p, const Groups& g, int it) {
+  const Sched& s = p.s;
+  Item w;
+  w.first = p.unit;
+  int j;  // index among the range's tiles, highest first
+  const int early = p.fin_last ? p.n_sk - 1 : p.n_sk;
+  if (it < early) {
+    j = it;
+  } else if (it < early + p.n_dp) {
+    w.t = tile_at<kTile, kStep>(g, p.unit + (it - early) * s.units);
+    w.kb0 = 0;
+    w.kb1 = s.num_kb;
+    w.kind = kWhole;
     return w;
+  } else {
+    j = p.n_sk - 1;
   }
+  const int t = p.tile_lo + (p.n_sk - 1 - j);
+  const int ts = t * s.num_kb;
+  w.t = tile_at<kTile, kStep>(g, s.dp + t);
+  w.kb0 = max(p.u0 - ts, 0);
+  w.kb1 = min(p.u1 - ts, s.num_kb);
+  w.kind = w.kb1 < s.num_kb ? kPartial : (w.kb0 > 0 ? kFinish : kWhole);
+  if (w.kind == kFinish) {
+    int q = p.unit - 1;
+    while (s.start(q) > ts) --q;
+    w.first = q;
+  }
+  return w;
+}
+
+// Fills the plan and its table: by one warp, after build_groups' (the same warp's)
+// part.  Every warp for itself, it took 1.3 to 2.3 us of a launch.
+template <int kTile, int kStep>
+__device__ __forceinline__ void make_plan(Plan& p, const Groups& g, int workers, int kbs, int unit, int lane) {
+  if (lane == 0) p.set(g.pre[g.E], workers, kbs, unit);
+  __syncwarp();
+  if (lane < p.n && lane < kTable) {
+    const Item w = make_item<kTile, kStep>(p, g, lane);
+    p.table[lane][0] = make_int4(w.t.e, w.t.f, w.t.row0, w.t.valid);
+    p.table[lane][1] = make_int4(w.kb0, w.kb1, w.kind, w.first);
+  }
+}
+
+// The items one after the other: the first ones from the plan's table; behind them
+// a warp works out 32 at once, one a lane, and hands them round (one by one they
+// cost each role about 0.8 us a tile).
+template <int kTile, int kStep>
+struct Walk {
+  const Plan& p;
+  const Groups& g;
+  int n, lane;
+  Item mine;
+  __device__ __forceinline__ Walk(const Plan& plan, const Groups& gr, int ln) : p(plan), g(gr), n(plan.n), lane(ln) {}
   // Item `it`, the same on every lane; called by the whole warp, for it = 0, 1, ...
   __device__ __forceinline__ Item at(int it) {
-    if ((it & 31) == 0 && it + lane < n) mine = make(it + lane);
     Item w;
-    const int from = it & 31;
-    w.t.e = __shfl_sync(0xffffffffu, mine.t.e, from);
-    w.t.f = __shfl_sync(0xffffffffu, mine.t.f, from);
-    w.t.row0 = __shfl_sync(0xffffffffu, mine.t.row0, from);
-    w.t.valid = __shfl_sync(0xffffffffu, mine.t.valid, from);
+    if (it < kTable) {
+      const int4 a = p.table[it][0], b = p.table[it][1];
+      w.t.e = a.x, w.t.f = a.y, w.t.row0 = a.z, w.t.valid = a.w;
+      w.kb0 = b.x, w.kb1 = b.y, w.kind = b.z, w.first = b.w;
+    } else {
+      const int from = (it - kTable) & 31;
+      if (from == 0 && it + lane < n) mine = make_item<kTile, kStep>(p, g, it + lane);
+      w.t.e = __shfl_sync(0xffffffffu, mine.t.e, from);
+      w.t.f = __shfl_sync(0xffffffffu, mine.t.f, from);
+      w.t.row0 = __shfl_sync(0xffffffffu, mine.t.row0, from);
+      w.t.valid = __shfl_sync(0xffffffffu, mine.t.valid, from);
+      w.kb0 = __shfl_sync(0xffffffffu, mine.kb0, from);
+      w.kb1 = __shfl_sync(0xffffffffu, mine.kb1, from);
+      w.kind = __shfl_sync(0xffffffffu, mine.kind, from);
+      w.first = __shfl_sync(0xffffffffu, mine.first, from);
+    }
     w.t.n = (w.t.valid + kStep - 1) / kStep * kStep;
-    w.kb0 = __shfl_sync(0xffffffffu, mine.kb0, from);
-    w.kb1 = __shfl_sync(0xffffffffu, mine.kb1, from);
-    w.kind = __shfl_sync(0xffffffffu, mine.kind, from);
-    w.first = __shfl_sync(0xffffffffu, mine.first, from);
     return w;
   }
 };

@@ -247,6 +247,16 @@ def test_grouped_many_experts():
     check_mx([2] * 1024, 64, 64, 64, True, False)
 
 
+def test_grouped_many_tiles_a_worker():
+    """More tiles a CTA pair than are worked out at the start, whole and cut ones."""
+    g = gen(12)
+    counts = torch.randint(1, 230, (100,), generator=g, device="cuda").tolist()
+    check_grouped(counts, 72, 8200, False, False)
+    check_grouped(counts, 64, 8192, True, True)
+    check_mx(counts, 64, 8200, 32, False, False)
+    check_mx(counts, 192, 8192, 64, True, True)
+
+
 # ------------------------------------------------- products by expert, MXFP8
 def mx_values(codes, scales, block):
     v = codes.view(torch.float8_e4m3fn).double()
