@@ -32,6 +32,14 @@ def _output(t, name, dtype, shape, dev, stream):
     return t
 
 
+def _stream(dev, stream):
+    """The raw stream of a call on dev (nat._stream for everything but the current
+    stream of the current device, refusals among it)."""
+    if stream is None and dev.type == "cuda" and dev.index == torch._C._cuda_getDevice():
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    return nat._stream(dev, stream)
+
+
 # a function of the sizes alone; the call itself is 1 us of a small call's 10
 _workspace_size = functools.lru_cache(maxsize=256)(nat.workspace_size)
 
@@ -61,8 +69,8 @@ def rnl_add_rmsnorm_mxfp8(x, gamma=None, residual=None, x_sum_out=None, eps=1e-6
     pg = None if gamma is None else _check(gamma, "gamma", _BF16, (K,), dev)
     codes_out = _output(codes_out, "codes_out", _U8, shape, dev, stream)
     scale_out = _output(scale_out, "scale_out", _U8, (T, K // block if block else 0), dev, stream)
-    status = nat.load().rnl_add_rmsnorm_mxfp8(px, pr, ps, pg, T, K, eps, norm_mode, block, codes_out.data_ptr(),
-                                              scale_out.data_ptr(), nat._stream(dev, stream))
+    status = (nat._lib or nat.load()).rnl_add_rmsnorm_mxfp8(px, pr, ps, pg, T, K, eps, norm_mode, block, codes_out.data_ptr(),
+                                              scale_out.data_ptr(), _stream(dev, stream))
     if status:
         raise nat.RnlError(status, "rnl_add_rmsnorm_mxfp8")
     return codes_out, scale_out
@@ -75,8 +83,8 @@ def rnl_quant_mxfp8(x, block=64, codes_out=None, scale_out=None, stream=None):
     px = _check(x, "x", _BF16, shape, dev)
     codes_out = _output(codes_out, "codes_out", _U8, shape, dev, stream)
     scale_out = _output(scale_out, "scale_out", _U8, (T, K // block if block else 0), dev, stream)
-    status = nat.load().rnl_quant_mxfp8(px, T, K, block, codes_out.data_ptr(), scale_out.data_ptr(),
-                                        nat._stream(dev, stream))
+    status = (nat._lib or nat.load()).rnl_quant_mxfp8(px, T, K, block, codes_out.data_ptr(), scale_out.data_ptr(),
+                                        _stream(dev, stream))
     if status:
         raise nat.RnlError(status, "rnl_quant_mxfp8")
     return codes_out, scale_out
@@ -100,9 +108,9 @@ def rnl_moe_route(logits, top_k, renormalize=True, ids_out=None, weights_out=Non
     rows = _output(rows_out, "rows_out", _I32, (T * k,), dev, stream)
     slots = _output(slots_out, "slots_out", _I32, (T, k), dev, stream)
     pw, nw, _keep = _space(_workspace_size(nat.OP_MOE_ROUTE, T, k, E), dev, workspace, stream)
-    status = nat.load().rnl_moe_route(pl, T, E, top_k, 1 if renormalize else 0, ids.data_ptr(), weights.data_ptr(),
+    status = (nat._lib or nat.load()).rnl_moe_route(pl, T, E, top_k, 1 if renormalize else 0, ids.data_ptr(), weights.data_ptr(),
                                       offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(), pw, nw,
-                                      nat._stream(dev, stream))
+                                      _stream(dev, stream))
     if status:
         raise nat.RnlError(status, "rnl_moe_route")
     return MoeRoute(ids, weights, offsets, rows, slots)
@@ -128,8 +136,8 @@ def rnl_grouped_linear_bf16(x, W, offsets, rows=None, swiglu=False, out=None, wo
     px, pW = _check(x, "x", _BF16, (R, K), dev), _check(W, "W", _BF16, (E, N, K), dev)
     M, po, pr, out = _rows_and_output(R, E, N, offsets, rows, swiglu, out, dev, stream)
     pw, nw, _keep = _space(_workspace_size(nat.OP_GROUPED, M, K, N, E), dev, workspace, stream)
-    status = nat.load().rnl_grouped_linear_bf16(px, R, pW, E, N, K, po, pr, M, 1 if swiglu else 0, out.data_ptr(), pw,
-                                                nw, nat._stream(dev, stream))
+    status = (nat._lib or nat.load()).rnl_grouped_linear_bf16(px, R, pW, E, N, K, po, pr, M, 1 if swiglu else 0, out.data_ptr(), pw,
+                                                nw, _stream(dev, stream))
     if status:
         raise nat.RnlError(status, "rnl_grouped_linear_bf16")
     return out
@@ -147,8 +155,8 @@ def rnl_grouped_linear_mxfp8(x_codes, x_scale, w_codes, w_scale, offsets, rows=N
     pW, pWs = _check(w_codes, "w_codes", _U8, (E, N, K), dev), _check(w_scale, "w_scale", _U8, (E, N, nb), dev)
     M, po, pr, out = _rows_and_output(R, E, N, offsets, rows, swiglu, out, dev, stream)
     pw, nw, _keep = _space(_workspace_size(nat.OP_GROUPED, M, K, N, E), dev, workspace, stream)
-    status = nat.load().rnl_grouped_linear_mxfp8(px, pxs, R, pW, pWs, E, N, K, block, po, pr, M, 1 if swiglu else 0,
-                                                 out.data_ptr(), pw, nw, nat._stream(dev, stream))
+    status = (nat._lib or nat.load()).rnl_grouped_linear_mxfp8(px, pxs, R, pW, pWs, E, N, K, block, po, pr, M, 1 if swiglu else 0,
+                                                 out.data_ptr(), pw, nw, _stream(dev, stream))
     if status:
         raise nat.RnlError(status, "rnl_grouped_linear_mxfp8")
     return out
@@ -164,7 +172,7 @@ def rnl_moe_combine(y, slots, weights, residual=None, out=None, stream=None):
     ps, pw = _check(slots, "slots", _I32, (T, k), dev), _check(weights, "weights", _F32, (T, k), dev)
     pr = None if residual is None else _check(residual, "residual", _BF16, (T, N), dev)
     out = _output(out, "out", _BF16, (T, N), dev, stream)
-    status = nat.load().rnl_moe_combine(py, M, N, ps, pw, T, k, pr, out.data_ptr(), nat._stream(dev, stream))
+    status = (nat._lib or nat.load()).rnl_moe_combine(py, M, N, ps, pw, T, k, pr, out.data_ptr(), _stream(dev, stream))
     if status:
         raise nat.RnlError(status, "rnl_moe_combine")
     return out

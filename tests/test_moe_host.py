@@ -248,6 +248,7 @@ def seen(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "current")
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
     monkeypatch.setattr(nat, "load", lambda path=None: FakeLib())
+    monkeypatch.setattr(nat, "_lib", None)
     monkeypatch.setattr(ex, "_workspace_size", nat.workspace_size)  # not remembered
     monkeypatch.setattr(nat, "_stream", lambda dev, stream: launched.append(stream))
 
@@ -283,6 +284,7 @@ def test_every_wrapper_is_covered_and_public():
 
 def test_outputs_of_small_calls(monkeypatch):
     monkeypatch.setattr(nat, "load", lambda path=None: FakeLib())
+    monkeypatch.setattr(nat, "_lib", None)
     monkeypatch.setattr(ex, "_workspace_size", nat.workspace_size)
     monkeypatch.setattr(nat, "_stream", lambda dev, stream: None)
     r = ex.rnl_moe_route(z(5, 7, dtype=F32), 3)
