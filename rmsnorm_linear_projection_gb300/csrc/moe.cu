@@ -187,9 +187,10 @@ __device__ void place_all(const RouteArgs& p, int64_t t0, int64_t t1, int* befor
   for (int64_t i = carry + static_cast<int64_t>(blockIdx.x) * kThreadsR + threadIdx.x; i < p.T * p.k;
        i += static_cast<int64_t>(gridDim.x) * kThreadsR)
     p.rows[i] = -1;
-  // each ranking warp takes an equal run of the CTA's choices
-  const int rw = rank_warps(p.E);
-  const int64_t n = warp < rw ? (t1 - t0) * p.k : 0;
+  // each ranking warp takes an equal run of the CTA's choices, 32 at least
+  const int64_t all_n = (t1 - t0) * p.k;
+  const int rw = static_cast<int>(min(static_cast<int64_t>(rank_warps(p.E)), max(int64_t{1}, (all_n + 31) / 32)));
+  const int64_t n = warp < rw ? all_n : 0;
   const int64_t run = ((n + rw - 1) / rw + 31) / 32 * 32;
   const int64_t i0 = t0 * p.k + warp * run;
   const int64_t end = t1 * p.k;
