@@ -176,6 +176,29 @@ __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Launches a kernel that begins with grid_dependency_wait as a programmatic dependent
+// of the one before it in the stream.  Small kernels let the next one start behind
+// their own wait: with the trigger in front of it, kernels pile up behind a long
+// one and hold its SMs' places (16 tokens through a layer of experts in MXFP8: 147
+// against 140 us, 141 without a trigger).
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                                    A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(block, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
 // ------------------------------------------------------------------- TMA
 // Non-binding hint: bring the 128-byte line holding p into L2.
 __device__ __forceinline__ void prefetch_l2(const void* p) {
