@@ -45,9 +45,10 @@ __device__ __forceinline__ int token_tiles(int cnt, int tile) { return (cnt + ti
 
 // Fills off and pre (shared memory, E + 1 values each) from the offsets; called
 // by every thread of the block, which must synchronise afterwards (warp 0, which
-// writes pre, need not).  Offsets
+// writes pre, need not).  (offsets without __restrict__: read-only loads need not stay
+// behind the wait for the kernel before.)  Offsets
 // that decrease or leave [0, M] are reported, and no tile is made.
-__device__ __forceinline__ void build_groups(const int32_t* __restrict__ offsets, int E, int M, int num_f,
+__device__ __forceinline__ void build_groups(const int32_t* offsets, int E, int M, int num_f,
                                              int tile, int* off, int* pre, unsigned int* err, uint32_t site) {
   for (int i = threadIdx.x; i <= E; i += blockDim.x) off[i] = offsets[i];
   __syncthreads();

@@ -300,8 +300,9 @@ int route_blocks(int64_t T, int* per) {
 // loaded four at a time and added in FP32 in the order of the places.  Bound by
 // HBM: 8192 tokens x 8 rows of 4096 in 104 us, 6.4 TB/s.
 __global__ void __launch_bounds__(256)
-    combine_kernel(const uint4* __restrict__ y, int64_t M, int nvec, const int32_t* __restrict__ slots,
-                   const float* __restrict__ weights, int64_t total, int k, const uint4* residual, uint4* out) {
+    combine_kernel(const uint4* y, int64_t M, int nvec, const int32_t* slots, const float* weights, int64_t total,
+                   int k, const uint4* residual, uint4* out) {
+  // (plain loads: read-only ones need not stay behind the wait)
   grid_dependency_wait();
   grid_launch_dependents();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -319,11 +320,11 @@ __global__ void __launch_bounds__(256)
     for (int j = 0; j < 4; ++j) {
       on[j] = false;
       if (j0 + j < k) {
-        const int s = __ldg(slots + t * k + j0 + j);
-        w[j] = __ldg(weights + t * k + j0 + j);
+        const int s = slots[t * k + j0 + j];
+        w[j] = weights[t * k + j0 + j];
         on[j] = s >= 0 && s < M;
         if (!on[j] && s != -1) atomicCAS(&g_err_moe, 0u, kErrArg | (214u << 8));
-        if (on[j]) u[j] = __ldg(y + static_cast<int64_t>(s) * nvec + v);
+        if (on[j]) u[j] = y[static_cast<int64_t>(s) * nvec + v];
       }
     }
 #pragma unroll

@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(1024) quant_kernel(QuantArgs p) {
       for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], rstd);
       if (p.gamma != nullptr && live) {
         float g[8];
-        unpack8(__ldg(p.gamma + v), g);
+        unpack8(p.gamma[v], g);  // (a plain load: a read-only one need not stay behind the wait)
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], g[j]);
       }
