@@ -198,10 +198,10 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
   const int num_pairs = gridDim.x >> 1;
   const int N_out = SWIGLU ? a.N / 2 : a.N;
   const int num_f = (N_out + 2 * kFeatCta - 1) / (2 * kFeatCta);
-  // MXFP8 rows that stand in order come as TMA boxes (24008 x 768 -> 4096 130 against
-  // 146 us: their copies by 16 bytes fill the load pipe), all others by the gathering
-  // warps (bf16 28004 x 1408 -> 2048 in order: 128 against 140 us by boxes)
-  const bool gather = !MX || a.rows != nullptr;
+  // rows that stand in order come as TMA boxes (900 rows x 32 experts, 1408 -> 2048 in
+  // bf16: 111 against 117 us by the gathering warps; MXFP8 4032 x 8192 -> 4864 94
+  // against 106)
+  const bool gather = a.rows != nullptr;
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(smem_u32(&ctrl->full[s]), gather ? 3 : 1);  // the boxes' bytes, and each CTA's gathered rows
@@ -238,57 +238,75 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------- weight producer
-    // and, where they come so, the group's rows: as boxes of 128 to 16 rows
-    if (lane == 0) {
-      tma_prefetch_map(&map_w);
-      if (!gather) tma_prefetch_map(&maps_x.m[0]);
-    }
+    if (lane == 0) tma_prefetch_map(&map_w);
     uint32_t stage = 0, phase = 0;
     bool ok = true;
     for (int it = 0; it < walk.n && ok; ++it) {
       const Item w = walk.at(it);
-      if (lane == 0) {
-        const int f0 = (w.t.f * 2 + static_cast<int>(rank)) * kFeatCta;
-        const int half = w.t.n / 2;
-        const int x_row = w.t.row0 + static_cast<int>(rank) * half;
-        const uint32_t bytes = 2 * kABytes + (gather ? 0u : static_cast<uint32_t>(w.t.n) * kRowBytes);  // of both CTAs
-        for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (!mbar_wait(smem_u32(&ctrl->empty[stage]), phase ^ 1u, abort, &g_err_grouped, 205) ||
-              !RNL_DCHECK(&g_err_grouped, stage < static_cast<uint32_t>(a.stages), 206)) {
-            ok = false;
-            break;
-          }
-          const uint32_t sa = base + stage * kStageBytes;
-          const uint32_t full_local = smem_u32(&ctrl->full[stage]);
-          const uint32_t full_even = mapa_shared(full_local, 0);
+      const int f0 = (w.t.f * 2 + static_cast<int>(rank)) * kFeatCta;
+      const uint32_t bytes = 2 * kABytes + (gather ? 0u : static_cast<uint32_t>(w.t.n) * kRowBytes);  // of both CTAs
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        ok = mbar_wait(smem_u32(&ctrl->empty[stage]), phase ^ 1u, abort, &g_err_grouped, 205) &&
+             RNL_DCHECK(&g_err_grouped, stage < static_cast<uint32_t>(a.stages), 206);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t sa = base + stage * kStageBytes;
+        const uint32_t full_local = smem_u32(&ctrl->full[stage]);
+        const uint32_t full_even = mapa_shared(full_local, 0);
+        if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(full_local, bytes);
           if constexpr (SWIGLU)
             tma_load_5d_pair(sa, &map_w, full_even, kb * kBKElems, 0, 0, f0 / 16, w.t.e);
           else
             tma_load_2d_pair(sa, &map_w, full_even, kb * kBKElems, w.t.e * a.N + f0);
-          if (!gather) {
-            int at = 0;
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-              if (half & (128 >> b)) {
-                tma_load_2d_pair(sa + kABytes + at * kRowBytes, &maps_x.m[b], full_even, kb * kBKElems, x_row + at);
-                at += 128 >> b;
-              }
-          }
-          if (++stage == static_cast<uint32_t>(a.stages)) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        if (++stage == static_cast<uint32_t>(a.stages)) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+  } else if (warp == kRelayWarp && !gather) {
+    // -------------------------------------------------------- row producer
+    // rows that stand in order: as boxes of 128 to 16 rows.  (A warp of its own, and an
+    // elected lane of it: from lane 0 of the weight's warp MXFP8 4032 x 8192 -> 4864 took
+    // 122 us, from lane 0 of this one 109)
+    if (lane == 0) tma_prefetch_map(&maps_x.m[0]);
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (int it = 0; it < walk.n && ok; ++it) {
+      const Item w = walk.at(it);
+      const int half = w.t.n / 2;
+      const int x_row = w.t.row0 + static_cast<int>(rank) * half;
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait(smem_u32(&ctrl->empty[stage]), phase ^ 1u, abort, &g_err_grouped, 215));
+        if (!ok) break;
+        const uint32_t dst = base + stage * kStageBytes + kABytes;
+        const uint32_t full_even = mapa_shared(smem_u32(&ctrl->full[stage]), 0);
+        if (elect_one()) {
+          int at = 0;
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            if (half & (128 >> b)) {
+              tma_load_2d_pair(dst + at * kRowBytes, &maps_x.m[b], full_even, kb * kBKElems, x_row + at);
+              at += 128 >> b;
+            }
+        }
+        __syncwarp();
+        if (++stage == static_cast<uint32_t>(a.stages)) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
     }
   } else if (warp == kRelayWarp) {
     // --------------------------------------------------------------- relay
     // hands a stage's rows to the tensor cores.  Not by the warps that copy:
     // their fence would wait for every copy that they have in flight
     uint32_t stage = 0, phase = 0;
-    bool ok = gather;
+    bool ok = true;
     for (int it = 0; it < walk.n && ok; ++it) {
       const Item w = walk.at(it);
       if (lane == 0) {
@@ -448,8 +466,7 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
       const int first = static_cast<int>(rank) * (i.t.n / 2) + gw * 32 + sub;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {  // rows behind the tile's last one repeat it (their columns are not stored)
-        row[j] = i.t.row0 + min(first + 4 * j, i.t.valid - 1);
-        if (a.rows != nullptr) row[j] = a.rows[row[j]];
+        row[j] = a.rows[i.t.row0 + min(first + 4 * j, i.t.valid - 1)];
       }
     };
     if (ok && walk.n > 0) {
