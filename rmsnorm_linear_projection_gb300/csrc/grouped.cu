@@ -8,20 +8,24 @@
 // CTA, the M side) against a tile of up to 256 rows of the group (the N side,
 // half of them staged by each CTA), see grouped.cuh.  The rows named by `rows` are
 // gathered while they are staged (16-byte asynchronous copies by four warps),
-// so that no sorted copy of x is written.  Measured against it: TMA gathers of
-// four rows take 54 cycles each, and a stage that the tensor cores read in 512
-// cycles needs 32 of them (32768 x 2048 -> 2816 over 32 experts: 541 against 277
-// us).  For swiglu the weight box interleaves 16 gate rows with the 16 up rows of the
-// same features, which puts both sums of a feature into one warp's lanes.
+// so that no sorted copy of x is written; rows that stand in order come as TMA boxes.
+// Measured against the copies: TMA gathers of four rows, issued by elected lanes of
+// the four warps: MXFP8 32000 x 4096 -> 2 x 768 over 64 experts 162-165 against 168-170
+// us, bf16 32768 x 2048 -> 2 x 1408 over 32 experts 228-234 against 219-227.  (Each warp
+// must then have rows in every stage: one without any can fall a phase of `empty`
+// behind.)  For swiglu the weight box interleaves 16 gate rows with the 16 up rows of
+// the same features, which puts both sums of a feature into one warp's lanes.
 //
-// Measured: 4096 x 4096 -> 4864 with one expert 87-90 us, 1.81-1.87 PFLOP/s (bound by
-// the tensor pipe), MXFP8 4032 x 8192 -> 4864 104 us, 3.08 PFLOP/s (by L2 -> SM copies:
-// 30 KB a k-block); 32768 x 2048 -> 2 x 1408 over 32 experts 233 us, 255-270 once the
-// power limit holds; 64 rows over 34 experts of the same size 63 us (HBM, 6.2 TB/s).
+// Measured: 4096 x 4096 -> 4864 with one expert 84-85 us, 1.92 PFLOP/s (bound by
+// the tensor pipe), gathered 86-89; MXFP8 4032 x 8192 -> 4864 94 us, 3.41 PFLOP/s,
+// gathered 106 (by L2 -> SM copies: 30 KB a k-block); 32768 x 2048 -> 2 x 1408 over 32
+// experts 219-233 us, 255-270 once the power limit holds; 64 rows over 34 experts of
+// the same size 63 us (HBM, 6.2 TB/s).
 //
 // Roles per CTA (480 threads): warp 0 weight boxes (TMA), warp 1 MMA issue (even CTA),
-// warps 2-9 epilogue, warps 10-13 gathers, warp 14 their hand-over; MXFP8 (608
-// threads) warps 15-18 the scales into tensor memory.
+// warps 2-9 epilogue, warps 10-13 gathers, warp 14 their hand-over, or the boxes of
+// rows that stand in order; MXFP8 (608 threads) warps 15-18 the scales into tensor
+// memory.
 // Every wait is bounded (ptx.cuh).
 #include <cuda_bf16.h>
 
