@@ -524,7 +524,8 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
       for (int it = 0; it < walk.n && ok; ++it) {
         const Item w = next;
         const uint32_t buf = it & 1;
-        ok = mbar_wait(smem_u32(&ctrl->tmem_empty[buf]), ((it >> 1) & 1) ^ 1u, abort, &g_err_grouped, 207);
+        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&ctrl->tmem_empty[buf]), ((it >> 1) & 1) ^ 1u, abort,
+                                               &g_err_grouped, 207));
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + buf * kTile;
         const uint32_t idesc = MX ? idesc_mxf8(256, w.t.n) : idesc_bf16(256, w.t.n);
