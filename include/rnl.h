@@ -59,7 +59,9 @@
  *     stream-K hand-off, QuantMatMulReduceSum's batch sum) are set back to 0
  *     by the launch that consumes them, so every replay waits for its own.
  *     After rnl_check_device_error() has reported RNL_ERR_TIMEOUT, set the
- *     failed call's workspace to zero before a graph that uses it replays.
+ *     failed call's workspace to zero before a graph that uses it replays, or
+ *     capture the graph again.  (The grouped products need neither: they set their
+ *     flags back to 0 in a launch that gave up, too.)
  */
 #ifndef RNL_H
 #define RNL_H

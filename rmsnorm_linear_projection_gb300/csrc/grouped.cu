@@ -586,7 +586,18 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
         for (int q = w.first + lane; q < pair && got; q += 32)
           got = flag_wait(a.flags + (static_cast<int64_t>(q) * 2 + rank) * kEpiWarps + ew, a.epoch, abort,
                           &g_err_grouped, 210);
-      if (!__all_sync(0xffffffffu, got)) break;
+      if (!__all_sync(0xffffffffu, got)) {
+        // the flags that this warp has not visited: of its own partial sums, which
+        // are the first item, and of the parts that its last item joins
+        if (w.kind == kPartial && lane == 0)
+          join_visit(a.flags + (static_cast<int64_t>(pair) * 2 + rank) * kEpiWarps + ew, join_gave_up(a.epoch), a.epoch);
+        if (ctrl->plan.fin_last) {
+          const Item last = make_item<kTile, kStep>(ctrl->plan, groups, walk.n - 1);
+          for (int q = last.first + lane; q < pair; q += 32)
+            join_visit(a.flags + (static_cast<int64_t>(q) * 2 + rank) * kEpiWarps + ew, join_gave_up(a.epoch), a.epoch);
+        }
+        break;
+      }
       __syncwarp();  // what a lane acquired is every lane's
       tc_fence_after();
       const int f0 = (t.f * 2 + static_cast<int>(rank)) * kFeatCta;
@@ -639,7 +650,8 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
       if (w.kind == kPartial) {
         __threadfence();
         __syncwarp();
-        if (lane == 0) flag_release(a.flags + (static_cast<int64_t>(pair) * 2 + rank) * kEpiWarps + ew, a.epoch);
+        if (lane == 0)
+          join_visit(a.flags + (static_cast<int64_t>(pair) * 2 + rank) * kEpiWarps + ew, a.epoch, a.epoch);
       }
     }
   }

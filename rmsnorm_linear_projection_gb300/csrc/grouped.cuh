@@ -15,6 +15,7 @@
 #include <cstdint>
 
 #include "gemm_common.cuh"
+#include "joinflag.h"
 #include "ptx.cuh"
 
 namespace rnl {
@@ -151,6 +152,15 @@ struct Item {
   int kb0, kb1, kind;
   int first;  // kFinish: the lowest worker that holds a part of the tile (else the worker itself)
 };
+
+// One side's visit of a join's flag (joinflag.h): leaves v there (the epoch: partial
+// sums are handed over, what this thread has seen written stands before it; or
+// join_gave_up), or 0 where the other side has been.
+__device__ __forceinline__ void join_visit(uint64_t* f, uint64_t v, uint64_t epoch) {
+  uint64_t found;
+  asm volatile("atom.acq_rel.gpu.global.exch.b64 %0, [%1], %2;" : "=l"(found) : "l"(f), "l"(v) : "memory");
+  if (join_is_second(found, epoch)) *reinterpret_cast<volatile uint64_t*>(f) = 0;
+}
 
 // The items of one worker, in order: what they are made from (in shared memory,
 // filled by one thread), and the first kTable of them.
