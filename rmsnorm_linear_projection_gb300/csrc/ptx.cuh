@@ -177,7 +177,11 @@ __device__ __forceinline__ void grid_launch_dependents() {
 }
 
 // Launches a kernel that begins with grid_dependency_wait as a programmatic dependent
-// of the one before it in the stream.  Small kernels let the next one start behind
+// of the one before it in the stream.  What the kernel before may have written
+// is read by plain loads (or ld.cg) behind that wait: the read-only path (__ldg,
+// ld.global.nc) is for data that nobody writes while the kernel is there, which a
+// dependent is before its predecessor has ended, and such a load need not stay
+// behind the wait.  Small kernels let the next one start behind
 // their own wait: with the trigger in front of it, kernels pile up behind a long
 // one and hold its SMs' places (16 tokens through a layer of experts in MXFP8: 147
 // against 140 us, 141 without a trigger).
