@@ -578,7 +578,8 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
     const uint32_t empty_even[2] = {mapa_shared(smem_u32(&ctrl->tmem_empty[0]), 0),
                                     mapa_shared(smem_u32(&ctrl->tmem_empty[1]), 0)};
     const int64_t lane_off = static_cast<int64_t>(rank) * 128 * 256 + quarter * 32 + lane;
-    for (int it = 0; it < walk.n; ++it) {
+    int it = 0;
+    for (; it < walk.n; ++it) {
       const Item w = walk.at(it);
       const Tile& t = w.t;
       const uint32_t buf = it & 1;
@@ -587,18 +588,7 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
         for (int q = w.first + lane; q < pair && got; q += 32)
           got = flag_wait(a.flags + (static_cast<int64_t>(q) * 2 + rank) * kEpiWarps + ew, a.epoch, abort,
                           &g_err_grouped, 210);
-      if (!__all_sync(0xffffffffu, got)) {
-        // the flags that this warp has not visited: of its own partial sums, which
-        // are the first item, and of the parts that its last item joins
-        if (w.kind == kPartial && lane == 0)
-          join_visit(a.flags + (static_cast<int64_t>(pair) * 2 + rank) * kEpiWarps + ew, join_gave_up(a.epoch), a.epoch);
-        if (ctrl->plan.fin_last) {
-          const Item last = make_item<kTile, kStep>(ctrl->plan, groups, walk.n - 1);
-          for (int q = last.first + lane; q < pair; q += 32)
-            join_visit(a.flags + (static_cast<int64_t>(q) * 2 + rank) * kEpiWarps + ew, join_gave_up(a.epoch), a.epoch);
-        }
-        break;
-      }
+      if (!__all_sync(0xffffffffu, got)) break;
       __syncwarp();  // what a lane acquired is every lane's
       tc_fence_after();
       const int f0 = (t.f * 2 + static_cast<int>(rank)) * kFeatCta;
@@ -655,6 +645,8 @@ __global__ void __launch_bounds__(Form<BLK != 0>::kThreads, 1)
           join_visit(a.flags + (static_cast<int64_t>(pair) * 2 + rank) * kEpiWarps + ew, a.epoch, a.epoch);
       }
     }
+    if (it < walk.n)  // a wait has run out
+      give_up_joins<kTile, kStep>(ctrl->plan, groups, it, lane, a.flags + rank * kEpiWarps + ew, 2 * kEpiWarps, a.epoch);
   }
 
   // a CTA that gave up on a wait lets the copies and products in flight end

@@ -225,6 +225,20 @@ __device__ __forceinline__ Item make_item(const Plan& p, const Groups& g, int it
   return w;
 }
 
+// The flags that a warp has not visited when it leaves its worker's items at item
+// `it`: of the worker's own partial sums, which are its first item, and of the parts
+// that its last item joins.  (Not inline: the registers are the items' own.)
+template <int kTile, int kStep>
+__device__ __noinline__ void give_up_joins(const Plan& p, const Groups& g, int it, int lane, uint64_t* flags, int step,
+                                           uint64_t epoch) {
+  if (it == 0 && lane == 0 && make_item<kTile, kStep>(p, g, 0).kind == kPartial)
+    join_visit(flags + static_cast<int64_t>(p.unit) * step, join_gave_up(epoch), epoch);
+  if (!p.fin_last) return;
+  const Item last = make_item<kTile, kStep>(p, g, p.n - 1);
+  for (int q = last.first + lane; q < p.unit; q += 32)
+    join_visit(flags + static_cast<int64_t>(q) * step, join_gave_up(epoch), epoch);
+}
+
 // Fills the plan and its table: by one warp, after build_groups' (the same warp's)
 // part.  Every warp for itself, it took 1.3 to 2.3 us of a launch.
 template <int kTile, int kStep>

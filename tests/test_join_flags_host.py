@@ -86,9 +86,15 @@ def test_every_way_out_of_the_epilogue_visits_the_flags():
     text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, "grouped.cu")).read())
     epilogue = text[text.index("const int ew = warp - 2"):]
     epilogue = epilogue[:epilogue.index("if (*abort)")]
+    # the one way out of the items in front of their end, and what stands behind the loop for it
     breaks = [m.start() for m in re.finditer(r"\bbreak;", epilogue)]
     assert len(breaks) == 1 and "return" not in epilogue
-    block = epilogue[epilogue.index("if (!__all_sync(0xffffffffu, got))"):breaks[0]]
-    # the flag of the warp's own partial sums, and those of the parts that it joins
-    assert block.count("join_visit(") == 2 and block.count("join_gave_up(a.epoch)") == 2
-    assert "flag_release" not in epilogue and epilogue.count("join_visit(") == 3
+    behind = epilogue[breaks[0]:]
+    assert re.search(r"if \(it < walk\.n\)\s+give_up_joins<", behind) and epilogue.count("give_up_joins<") == 1
+    # partial sums are handed over by a visit, too
+    assert "flag_release" not in epilogue and epilogue.count("join_visit(") == 1
+    helper = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, "grouped.cuh")).read())
+    helper = helper[helper.index("void give_up_joins("):]
+    helper = helper[:helper.index("\n}\n")]
+    # the flag of the worker's own partial sums, and those of the parts that it joins
+    assert helper.count("join_visit(") == 2 and helper.count("join_gave_up(epoch)") == 2
