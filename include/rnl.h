@@ -484,7 +484,8 @@ rnl_status mla_q_chain_head_norm(const void *x, const void *W_qa, const void *ga
  * X = floor(log2 max|y|) - 8 (at least -127; an all-zero block gets -127),
  * scale byte X + 127, codes E4M3(y * 2^-X) rounded to nearest even and
  * saturated to +-448.  Codes and scales are exact functions of x, gamma and
- * eps (the FP32 sum of squares is the rounding of the exact sum).  The
+ * eps (the FP32 sum of squares is the rounding of the exact sum: past FP32's
+ * largest value it is infinite, rstd is 0 and the row's codes are zeros).  The
  * product is accumulated in FP32 on the tensor cores from the exactly
  * dequantised operands.  K % block == 0, T * K and N * K below 2^36
  * (else RNL_ERR_SHAPE); x, gamma, w_codes, out 16-byte aligned.  Workspace: rnl_workspace_size(RNL_OP_MXFP8, T, K, N, 0) bytes.
@@ -518,8 +519,9 @@ rnl_status mxfp8_scaled_mm(const uint8_t *x_codes, const uint8_t *x_scale, const
  *             from both); the norm is s's
  *   codes     E4M3FN bytes [T, K];  scale  E8M0 bytes [T, K / block]
  * The codes and scales of rmsnorm_linear_mxfp8 for the same (finite) rows, to the
- * bit.  A row whose sum of squares is infinite has rstd 0.  A block of y that holds an infinity or NaN gets scale byte 255 (NaN) and codes
- * 0.  block 32 or 64 (else RNL_ERR_ARG), K % block == 0 (else RNL_ERR_SHAPE),
+ * bit.  A row whose sum of squares is past FP32's largest value has rstd 0.  A block
+ * of y that holds an infinity or NaN gets scale byte 255 (NaN) and codes 0.
+ * block 32 or 64 (else RNL_ERR_ARG), K % block == 0 (else RNL_ERR_SHAPE),
  * K at most 65536 (else RNL_ERR_UNSUPPORTED).  16-byte aligned tensors (scale:
  * any).  No workspace.
  * rnl_quant_mxfp8: the same blocks of x itself, no add and no norm.

@@ -66,11 +66,15 @@ __device__ __forceinline__ void ff_warp_hilo(const float (&hs)[8], const float (
   lo_out = lo;
 }
 
+// The binary32 rounding of a pair.  A sum past the largest value is infinite, and has
+// no rounding error to add (TwoSum's error terms are NaN there).
+__device__ __forceinline__ float ff_round(float hi, float lo) { return isinf(hi) ? hi : __fadd_rn(hi, lo); }
+
 // The binary32 rounding of the warp's total (the same value on every lane).
 __device__ __forceinline__ float ff_warp_total(const float (&hs)[8], const float (&ls)[8]) {
   float hi, lo;
   ff_warp_hilo(hs, ls, hi, lo);
-  return __fadd_rn(hi, lo);
+  return ff_round(hi, lo);
 }
 
 // ---- The same float-float sum on packed f32x2 arithmetic: two chains per
@@ -147,7 +151,7 @@ __device__ __forceinline__ void ffx2_warp_hilo(uint64_t (&hs)[4], uint64_t (&ls)
 __device__ __forceinline__ float ffx2_warp_total(uint64_t (&hs)[4], uint64_t (&ls)[4]) {
   float hi, lo;
   ffx2_warp_hilo(hs, ls, hi, lo);
-  return __fadd_rn(hi, lo);
+  return ff_round(hi, lo);
 }
 
 // rstd from the binary32 sum, one correctly rounded operation per step:

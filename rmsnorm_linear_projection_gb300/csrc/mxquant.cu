@@ -115,8 +115,7 @@ __global__ void __launch_bounds__(1024) quant_kernel(QuantArgs p) {
       lo = q.y;
       ff_warp_merge(hi, lo);
     }
-    // an infinite sum has no rounding error to add (the error terms are NaN)
-    rstd = rstd_of_sum<kMode>(isinf(hi) ? hi : __fadd_rn(hi, lo), p.inv_d, p.eps);
+    rstd = rstd_of_sum<kMode>(ff_round(hi, lo), p.inv_d, p.eps);
   }
   constexpr int kGroup = BLK / 8;  // lanes a block
   uint8_t* srow = p.scale + static_cast<int64_t>(blockIdx.x) * (p.nvec / kGroup);

@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreadsQS, 1)
     float tot, e;
     two_sum(ctrl->hi[pair][0], ctrl->hi[pair][1], tot, e);
     const float rest = __fadd_rn(__fadd_rn(ctrl->lo[pair][0], ctrl->lo[pair][1]), e);
-    const float rstd = rstd_of_sum<MODE>(__fadd_rn(tot, rest), inv_d, eps);
+    const float rstd = rstd_of_sum<MODE>(ff_round(tot, rest), inv_d, eps);
     const float wmax = pass_amax<GAMMA, VPL>(xv, ga_s + 32 * sub, gb_s + 32 * sub, lane, rstd);
     if (lane == 0) ctrl->amax[pair][sub] = __float_as_uint(wmax);
     asm volatile("bar.sync %0, 64;" ::"r"(pbar) : "memory");
