@@ -16,7 +16,7 @@
 
 #include "gemm_common.cuh"
 #include "joinflag.h"
-#include "ptx.cuh"
+#include "ptx_more.cuh"
 
 namespace rnl {
 namespace grouped {

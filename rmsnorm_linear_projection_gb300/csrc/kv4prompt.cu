@@ -44,6 +44,7 @@
 #include <type_traits>
 
 #include "kv4.cuh"
+#include "ptx_more.cuh"
 
 namespace rnl {
 namespace {
@@ -283,16 +284,6 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead) {
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
-}
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok));
-  return ok != 0;
 }
 // The products of one 16-wide step; descriptors as their low words (address
 // and leading offset) with constant high words, so that a step costs a 32-bit

@@ -18,7 +18,7 @@
 #include <atomic>
 
 #include "internal.h"
-#include "ptx.cuh"
+#include "ptx_more.cuh"
 
 namespace rnl {
 namespace {

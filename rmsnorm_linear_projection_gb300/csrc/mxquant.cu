@@ -22,7 +22,7 @@
 
 #include "exactsum.cuh"
 #include "internal.h"
-#include "ptx.cuh"
+#include "ptx_more.cuh"
 
 namespace rnl {
 namespace {
