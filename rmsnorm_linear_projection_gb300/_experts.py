@@ -55,6 +55,11 @@ def _space(nbytes, dev, given, stream):
     return given.data_ptr(), given.numel() * given.element_size(), given
 
 
+def _blocks(K, block):
+    """Blocks of a row; sizes that the call refuses have none."""
+    return K // block if block > 0 else 0
+
+
 def rnl_add_rmsnorm_mxfp8(x, gamma=None, residual=None, x_sum_out=None, eps=1e-6, norm_mode=nat.NORM_RSQRT, block=64,
                           codes_out=None, scale_out=None, stream=None):
     """Residual add (optional), RMSNorm and MX quantisation of the rows of x [T, K]
@@ -68,7 +73,7 @@ def rnl_add_rmsnorm_mxfp8(x, gamma=None, residual=None, x_sum_out=None, eps=1e-6
     ps = None if x_sum_out is None else _check(x_sum_out, "x_sum_out", _BF16, shape, dev)
     pg = None if gamma is None else _check(gamma, "gamma", _BF16, (K,), dev)
     codes_out = _output(codes_out, "codes_out", _U8, shape, dev, stream)
-    scale_out = _output(scale_out, "scale_out", _U8, (T, K // block if block else 0), dev, stream)
+    scale_out = _output(scale_out, "scale_out", _U8, (T, _blocks(K, block)), dev, stream)
     status = (nat._lib or nat.load()).rnl_add_rmsnorm_mxfp8(px, pr, ps, pg, T, K, eps, norm_mode, block, codes_out.data_ptr(),
                                               scale_out.data_ptr(), _stream(dev, stream))
     if status:
@@ -82,7 +87,7 @@ def rnl_quant_mxfp8(x, block=64, codes_out=None, scale_out=None, stream=None):
     dev = x.device
     px = _check(x, "x", _BF16, shape, dev)
     codes_out = _output(codes_out, "codes_out", _U8, shape, dev, stream)
-    scale_out = _output(scale_out, "scale_out", _U8, (T, K // block if block else 0), dev, stream)
+    scale_out = _output(scale_out, "scale_out", _U8, (T, _blocks(K, block)), dev, stream)
     status = (nat._lib or nat.load()).rnl_quant_mxfp8(px, T, K, block, codes_out.data_ptr(), scale_out.data_ptr(),
                                         _stream(dev, stream))
     if status:
@@ -101,7 +106,7 @@ def rnl_moe_route(logits, top_k, renormalize=True, ids_out=None, weights_out=Non
     T, E = logits.shape
     dev = logits.device
     pl = _check(logits, "logits", _F32, (T, E), dev)
-    k = max(top_k, 0)
+    k = min(max(top_k, 0), E)  # (the call refuses what is outside)
     ids = _output(ids_out, "ids_out", _I32, (T, k), dev, stream)
     weights = _output(weights_out, "weights_out", _F32, (T, k), dev, stream)
     offsets = _output(offsets_out, "offsets_out", _I32, (E + 1,), dev, stream)
@@ -150,7 +155,7 @@ def rnl_grouped_linear_mxfp8(x_codes, x_scale, w_codes, w_scale, offsets, rows=N
     R, K = x_codes.shape
     E, N = w_codes.shape[0], w_codes.shape[1]
     dev = x_codes.device
-    nb = K // block if block else 0
+    nb = _blocks(K, block)
     px, pxs = _check(x_codes, "x_codes", _U8, (R, K), dev), _check(x_scale, "x_scale", _U8, (R, nb), dev)
     pW, pWs = _check(w_codes, "w_codes", _U8, (E, N, K), dev), _check(w_scale, "w_scale", _U8, (E, N, nb), dev)
     M, po, pr, out = _rows_and_output(R, E, N, offsets, rows, swiglu, out, dev, stream)
