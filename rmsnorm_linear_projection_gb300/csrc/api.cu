@@ -426,7 +426,7 @@ rnl_status make_map_2d_plain(CUtensorMap* map, CUtensorMapDataType dtype, const 
 }
 
 rnl_status make_map_5d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, const uint64_t (&dims)[5],
-                       const uint64_t (&strides)[4], const uint32_t (&box)[5], bool swizzle) {
+                       const uint64_t (&strides)[4], const uint32_t (&box)[5]) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return RNL_ERR_DEVICE;
   cuuint64_t d[5], st[4];
@@ -438,8 +438,8 @@ rnl_status make_map_5d(CUtensorMap* map, CUtensorMapDataType dtype, const void* 
     if (i < 4) st[i] = strides[i];
   }
   const CUresult r = enc(map, dtype, 5, const_cast<void*>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? RNL_OK : RNL_ERR_ARG;
 }
 

@@ -711,13 +711,13 @@ rnl_status launch(const GroupedArgs& g, const DeviceInfo& dev, cudaStream_t s) {
     const uint64_t dims[5] = {K, 16, 2, N / 32, static_cast<uint64_t>(g.E)};
     const uint64_t strides[4] = {row, N / 2 * row, 16 * row, N * row};
     const uint32_t box[5] = {kBox, 16, 2, 4, 1};
-    st = make_map_5d(&mw, dt, g.w, dims, strides, box, true);
+    st = make_map_5d(&mw, dt, g.w, dims, strides, box);
   } else {
     st = make_map_2d(&mw, dt, g.w, K, g.E * N, row, kBox, 128);
   }
   if (st != RNL_OK) return st;
-  XMaps mx;
-  for (int b = 0; b < 4; ++b) {
+  XMaps mx = {};  // (gathered rows take no boxes)
+  for (int b = 0; b < 4 && g.rows == nullptr; ++b) {
     st = make_map_2d(&mx.m[b], dt, g.x, K, g.R, row, kBox, 128 >> b);
     if (st != RNL_OK) return st;
   }

@@ -1,10 +1,11 @@
-// grouped.cuh -- pieces of the grouped products (grouped.cu): the tiles of ragged groups, the work list over them and the epilogue stores.
+// grouped.cuh -- pieces of the grouped products (grouped.cu): the tiles of ragged groups,
+// the work list over them and the epilogue stores.
 //
 //   out[i] = x[rows[i]] W[e]^T   for the rows i of expert e, offsets[e] <= i < offsets[e + 1]
 //
-// Weight rows stand on the tensor core's M side (128 TMEM lanes a CTA), the
-// group's rows on its N side, because N may be any multiple of 16 (of 32 on a CTA
-// pair): a group of 5 rows costs a 16-wide product instead of a 128-row one, and a large group is
+// Weight rows stand on the tensor core's M side (256 of a CTA pair, 128 TMEM lanes
+// each), the group's rows on its N side, because N may be any multiple of 32: a group
+// of 5 rows costs a 32-wide product instead of a 256-row one, and a large group is
 // cut into near-equal tiles of at most kTile rows.  How many rows an expert has is
 // known on the device only: every CTA reads the offsets and builds the table
 // of the groups' first tiles itself.
@@ -21,7 +22,6 @@
 namespace rnl {
 namespace grouped {
 
-constexpr int kMaxExperts = 1024;
 constexpr int kEpiWarps = 8;
 // token tiles of a group walked before the next weight rows: their operand
 // (16 x 256 rows of 4096 bf16: 34 MB) stays in L2 while the weight passes
@@ -37,7 +37,7 @@ struct Groups {
 
 // One output tile: rows [row0, row0 + valid) of the grouped order against the
 // weight rows of feature tile f of expert e; n: valid rounded up to the step of
-// the product's N side (16 on one CTA, 32 on a pair).
+// the product's N side (32).
 struct Tile {
   int e, f, row0, valid, n;
 };
@@ -162,8 +162,8 @@ __device__ __forceinline__ void join_visit(uint64_t* f, uint64_t v, uint64_t epo
   if (join_is_second(found, epoch)) *reinterpret_cast<volatile uint64_t*>(f) = 0;
 }
 
-// The items of one worker, in order: what they are made from (in shared memory,
-// filled by one thread), and the first kTable of them.
+// The items of one worker, in order: what they are made from, and the first kTable of
+// them (in shared memory, filled by one warp).
 constexpr int kTable = 16;  // (with 32 the table costs a stage of the pipeline from 86 experts on, with 16 from 150)
 struct Plan {
   Sched s;

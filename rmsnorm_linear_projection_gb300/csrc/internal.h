@@ -35,9 +35,9 @@ rnl_status make_map_2d_plain(CUtensorMap* map, CUtensorMapDataType dtype, const 
                              uint32_t box_inner, uint32_t box_outer);
 
 // 5-D map (dims and box innermost first, strides of dimensions 1 .. 4 in bytes),
-// with the 128-byte swizzle or none.
+// with the 128-byte swizzle.
 rnl_status make_map_5d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, const uint64_t (&dims)[5],
-                       const uint64_t (&strides)[4], const uint32_t (&box)[5], bool swizzle);
+                       const uint64_t (&strides)[4], const uint32_t (&box)[5]);
 
 // Raises a kernel's dynamic shared-memory limit on `device` (the current one)
 // to at least `bytes`: set on a (kernel, device)'s first call and again only

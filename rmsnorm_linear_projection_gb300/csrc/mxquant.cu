@@ -17,9 +17,9 @@
 // and its sum.  Bound by HBM: 16384 x 4096 in 69.6 us, 6.76 TB/s; 8192 x 4096 38.4 us,
 // 6.1 TB/s, with two vectors a thread 42, one 52, eight 48, with a persistent CTA
 // that loads the next row while it works on one 47 and more.
-#include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include "bf16x8.cuh"
 #include "exactsum.cuh"
 #include "internal.h"
 #include "ptx_more.cuh"
@@ -37,30 +37,6 @@ struct QuantArgs {
   uint2* codes;
   uint8_t* scale;
 };
-
-__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-
-// bf16(a + b), one rounding of the exact sum for every pair of bf16 values
-__device__ __forceinline__ uint4 add_bf16x8(const uint4& a, const uint4& b) {
-  float fa[8], fb[8];
-  unpack8(a, fa);
-  unpack8(b, fb);
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h =
-        __floats2bfloat162_rn(__fadd_rn(fa[2 * i], fb[2 * i]), __fadd_rn(fa[2 * i + 1], fb[2 * i + 1]));
-    o[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
 
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
