@@ -117,7 +117,8 @@ int rnl_version(void);
  * computes the same results and additionally checks, on the device, every
  * shared-memory stage offset, TMEM column range, workspace record or flag
  * index and output index of its GEMM, norm-pass and skinny kernels, and of the
- * multi-axis rotary, 4-bit cache, attention and grouped kernels, before use; a failed check skips that access, and rnl_check_device_error() then
+ * multi-axis rotary, 4-bit cache, attention, routing and grouped kernels, before
+ * use; a failed check skips that access, and rnl_check_device_error() then
  * returns RNL_ERR_BOUNDS with the check's site.  No kernel traps.
  */
 int rnl_debug_build(void);

@@ -214,7 +214,8 @@ __device__ void place_all(const RouteArgs& p, int64_t t0, int64_t t1, int* befor
   __syncthreads();
   for (int64_t b = i0; b < i1; b += 32) {
     const int64_t i = b + lane;
-    const int id = i < i1 ? p.ids[i] : -1;
+    int id = i < i1 ? p.ids[i] : -1;
+    if (!RNL_DCHECK(&g_err_moe, id >= -1 && id < p.E, 216)) id = -1;
     const uint32_t same = __match_any_sync(0xffffffffu, id);
     const int rank = __popc(same & ((1u << lane) - 1u));
     int pos = -1;
@@ -224,7 +225,7 @@ __device__ void place_all(const RouteArgs& p, int64_t t0, int64_t t1, int* befor
     __syncwarp();
     if (i < i1) {
       p.slots[i] = pos;
-      if (pos >= 0) p.rows[pos] = static_cast<int32_t>(i / p.k);
+      if (pos >= 0 && RNL_DCHECK(&g_err_moe, pos < p.T * p.k, 217)) p.rows[pos] = static_cast<int32_t>(i / p.k);
     }
   }
 }
