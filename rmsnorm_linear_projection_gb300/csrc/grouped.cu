@@ -16,11 +16,11 @@
 // behind.)  For swiglu the weight box interleaves 16 gate rows with the 16 up rows of
 // the same features, which puts both sums of a feature into one warp's lanes.
 //
-// Measured: 4096 x 4096 -> 4864 with one expert 84-85 us, 1.92 PFLOP/s (bound by
-// the tensor pipe), gathered 86-89; MXFP8 4032 x 8192 -> 4864 94 us, 3.41 PFLOP/s,
+// Measured: 4096 x 4096 -> 4864 with one expert 83-85 us, 1.92 PFLOP/s (bound by
+// the tensor pipe), gathered 87-89; MXFP8 4032 x 8192 -> 4864 94 us, 3.41 PFLOP/s,
 // gathered 106 (by L2 -> SM copies: 30 KB a k-block); 32768 x 2048 -> 2 x 1408 over 32
-// experts 219-233 us, 255-270 once the power limit holds; 64 rows over 34 experts of
-// the same size 63 us (HBM, 6.2 TB/s).
+// experts 219-233 us, 259-274 once the power limit holds; 64 rows over 34 experts of
+// the same size 62-64 us (HBM, 6.2 TB/s).
 //
 // Roles per CTA (480 threads): warp 0 weight boxes (TMA), warp 1 MMA issue (even CTA),
 // warps 2-9 epilogue, warps 10-13 gathers, warp 14 their hand-over, or the boxes of

@@ -98,7 +98,9 @@ __device__ __forceinline__ Tile tile_at(const Groups& g, int t) {
   const int loc = t - g.pre[lo];
   const int cnt = g.off[lo + 1] - g.off[lo];
   // the group's steps are dealt out to its tiles as evenly as whole steps allow:
-  // 900 rows in steps of 32 are 256 + 3 x 224, not 4 x 256
+  // 900 rows in steps of 32 are 256 + 3 x 224, not 3 x 256 + 132 (32 experts of them
+  // 113.6 -> 111.3 us, of 520 rows 76.7 -> 74.0; MXFP8 65536 rows over 128 experts
+  // 347 -> 340)
   const int nt = token_tiles(cnt, kTile);
   const int steps = (cnt + kStep - 1) / kStep;
   const int each = steps / nt, more = steps - each * nt;

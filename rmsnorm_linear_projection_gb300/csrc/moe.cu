@@ -5,9 +5,10 @@
 // Routing (bound by latency: a few MB are read).  32 warps a CTA and 64 tokens, so
 // that a warp has two tokens to choose for; with 8 warps of 8 tokens each, and
 // the counts added up by as few threads, the two launches took 19.3 and 14.9 us
-// for 8192 tokens over 128 experts, now 9.6 each (17.8 us a call in a graph).  One warp a token: a lane holds every 32nd logit as an
-// order-preserving integer, and k rounds of two warp reductions take the
-// largest key and, among equals, the lowest expert.  The rows are grouped by a
+// for 8192 tokens over 128 experts, now 9.6 to 11 each (17.7 us a call in a graph).
+// One warp a token: a lane holds every 32nd logit as an order-preserving integer, and
+// k rounds of two warp reductions take the largest key and, among equals, the lowest
+// expert.  The rows are grouped by a
 // stable counting sort, (token, place) order within an expert: each CTA counts
 // its tokens' choices, then adds up the counts of the CTAs before it and ranks
 // its own choices warp by warp (match_any).  Nothing depends on the order of
